@@ -7,19 +7,23 @@ contiguous group of ``group_size`` columns,
   mamba2: out = cast(w[col] * cast(y*silu(gate) * rsqrt(mean((y*silu(gate))^2) + eps)))
   onnx:   out = cast(x * rsqrt(mean(x^2) + eps) * scale[j] * silu(gate))
 
-computed by hand-written CUDA kernels behind a C ABI (``include/ggrn.h``,
-``libggrn.so``).  This package is the thin Python binding.
+and the two operators that come before it in the Mamba-2 mixer, for prompts
+and for single tokens: the short causal convolution (``causal_conv``,
+``causal_conv_step``) and the selective state space scan (``ssm_scan``,
+``ssm_scan_step``).  All computed by hand-written CUDA kernels behind a C ABI
+(``include/ggrn.h``, ``libggrn.so``).  This package is the thin Python binding.
 """
 from .binding import (BF16, DTYPE_CODE, F16, F32, MAMBA2, ONNX, PATH_AUTO, PATH_NAMES,
                       PATH_SCALAR, PATH_STRADDLE, PATH_STREAM, PATH_TEAM, PATH_WIDE,
                       PATH_WIDE_CLUSTER, DecodeGraph,
-                      GgrnError, fault_status, forward, forward_host, forward_inproj,
+                      GgrnError, causal_conv, causal_conv_step, fault_status, forward, forward_host, forward_inproj,
                       ggrn_forward, ggrn_forward_host, ggrn_forward_inproj,
                       ggrn_forward_inproj_host, ggrn_forward_noalloc, ggrn_forward_path,
                       ggrn_norm_outproj, norm_outproj, ggrn_plan, host_workspace, library_path, load, plan,
-                      status_string)
+                      scan_workspace_bytes, ssm_scan, ssm_scan_step, status_string)
 
-__all__ = ["forward", "forward_host", "forward_inproj", "plan", "DecodeGraph", "GgrnError",
+__all__ = ["causal_conv", "causal_conv_step", "ssm_scan", "ssm_scan_step", "scan_workspace_bytes",
+           "forward", "forward_host", "forward_inproj", "plan", "DecodeGraph", "GgrnError",
            "ggrn_forward", "ggrn_forward_host", "ggrn_forward_inproj", "ggrn_forward_inproj_host",
            "ggrn_forward_noalloc", "ggrn_norm_outproj", "norm_outproj",
            "ggrn_forward_path", "ggrn_plan", "host_workspace", "load",

@@ -35,7 +35,11 @@ EXPORTS = ("ggrn_forward", "ggrn_forward_path", "ggrn_plan", "ggrn_graph_create"
            "ggrn_fault_status", "ggrn_last_cuda_error", "ggrn_forward_noalloc",
            "ggrn_forward_inproj", "ggrn_forward_host", "ggrn_forward_inproj_host",
            "ggrn_host_workspace_bytes", "ggrn_selftest_wait_timeout", "ggrn_norm_outproj",
-           "ggrn_norm_outproj_workspace_bytes")
+           "ggrn_norm_outproj_workspace_bytes", "ggrn_conv", "ggrn_conv_step", "ggrn_scan",
+           "ggrn_scan_step", "ggrn_scan_workspace_bytes", "ggrn_graph_create_steps")
+# ggrn_activation / ggrn_step_kind
+ACT_CODE = {None: 0, "silu": 1}
+STEP_FORWARD, STEP_CONV, STEP_SCAN = 0, 1, 2
 
 
 class GgrnError(RuntimeError):
@@ -65,6 +69,36 @@ class Call(ctypes.Structure):
                 ("group_size", ctypes.c_int64), ("y_row_stride", ctypes.c_int64),
                 ("gate_row_stride", ctypes.c_int64), ("out_row_stride", ctypes.c_int64),
                 ("eps", ctypes.c_float), ("dtype", ctypes.c_int32), ("mode", ctypes.c_int32)]
+
+
+class ConvCall(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("x", "w", "bias", "out", "state", "slots",
+                                                "resume", "cu_seqlens")] +
+                [(n, ctypes.c_int64) for n in ("rows", "seqs", "width", "x_row_stride",
+                                               "out_row_stride", "state_slots",
+                                               "state_slot_stride")] +
+                [(n, ctypes.c_int32) for n in ("taps", "activation", "dtype")])
+
+
+class ScanCall(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("x", "dt", "b", "c", "a", "d", "dt_bias", "out",
+                                                "state", "slots", "resume", "cu_seqlens",
+                                                "workspace")] +
+                [(n, ctypes.c_int64) for n in ("workspace_bytes", "rows", "seqs", "heads",
+                                               "head_dim", "groups", "state_size", "x_row_stride",
+                                               "dt_row_stride", "b_row_stride", "c_row_stride",
+                                               "out_row_stride", "state_slots",
+                                               "state_slot_stride")] +
+                [("dt_min", ctypes.c_float), ("dt_max", ctypes.c_float),
+                 ("dt_softplus", ctypes.c_int32), ("dtype", ctypes.c_int32)])
+
+
+class _StepUnion(ctypes.Union):
+    _fields_ = [("forward", Call), ("conv", ConvCall), ("scan", ScanCall)]
+
+
+class Step(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("u", _StepUnion)]
 
 
 _lock = threading.Lock()
@@ -132,6 +166,16 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         L.ggrn_fault_status.restype = ci
         L.ggrn_last_cuda_error.argtypes = []
         L.ggrn_last_cuda_error.restype = ctypes.c_char_p
+        for name, call in (("ggrn_conv", ConvCall), ("ggrn_conv_step", ConvCall),
+                           ("ggrn_scan", ScanCall), ("ggrn_scan_step", ScanCall)):
+            fn = getattr(L, name)
+            fn.argtypes = [ctypes.POINTER(call), vp]
+            fn.restype = ci
+        L.ggrn_scan_workspace_bytes.argtypes = [ctypes.POINTER(ScanCall)]
+        L.ggrn_scan_workspace_bytes.restype = i64
+        L.ggrn_graph_create_steps.argtypes = [ctypes.POINTER(Step), ctypes.c_int32,
+                                              ctypes.POINTER(ctypes.c_void_p)]
+        L.ggrn_graph_create_steps.restype = ci
         _lib = L
         return L
 
@@ -461,34 +505,342 @@ def _packed_pair(y, gate, rows, width, ys, gts):
     return base, ycol, gcol
 
 
+# ---------------------------------------------------------------------------
+# The mixer around the norm: causal convolution and state space scan.
+# ---------------------------------------------------------------------------
+def _rows_of(t: torch.Tensor, width: int, name: str) -> tuple[int, int]:
+    """(rows, row_stride) of a tensor viewed as [rows, width]; an axis of one
+    element may have any stride."""
+    shape, strides = t.shape, t.stride()
+    if len(shape) == 0 or shape[-1] != width:
+        raise ValueError(f"{name} must have {width} columns")
+    if width != 1 and strides[-1] != 1:
+        raise ValueError(f"{name} needs unit stride on its last dimension")
+    if len(shape) == 2:
+        return shape[0], (strides[0] if shape[0] > 1 else width)
+    if t.numel() == 0:
+        return 0, width
+    rows, stride = 1, width
+    for size, step in zip(reversed(shape[:-1]), reversed(strides[:-1])):
+        if size == 1:
+            continue
+        if rows == 1:
+            stride = step
+        elif step != stride * rows:
+            raise ValueError(f"{name}: leading axes do not fold into one row axis")
+        rows *= size
+    return rows, stride
+
+
+def _vector(t, n: int, dtype, device, name: str):
+    """Pointer of an optional contiguous vector of n elements."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.numel() != n or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} elements on {device}")
+    return t.data_ptr()
+
+
+def _fill_seqs(k, x, device, cu_seqlens, state, slots, resume, held: tuple, dtype, step: bool):
+    """Sequences and pool of a call: the fields both operators share."""
+    if step:
+        n = k.rows
+        k.seqs = n
+    elif cu_seqlens is not None:
+        n = cu_seqlens.numel() - 1
+        if n < 0:
+            raise ValueError("cu_seqlens holds one offset more than there are sequences")
+        k.cu_seqlens = _vector(cu_seqlens, n + 1, torch.int32, device, "cu_seqlens")
+        k.seqs = n
+    else:
+        n = 1
+        for size in x.shape[:-2]:
+            n *= size
+        k.seqs = n
+    if state is None:
+        if slots is not None or resume is not None:
+            raise ValueError("slots and resume name entries of a state: pass one")
+        return
+    if state.dtype != dtype or state.device != device:
+        raise ValueError(f"state must be a {dtype} tensor on {device}")
+    if state.shape[1:] != held:
+        raise ValueError(f"state must be [slots, {', '.join(map(str, held))}]")
+    expect = 1
+    for size, stride in zip(reversed(state.shape[1:]), reversed(state.stride()[1:])):
+        if size != 1 and stride != expect:
+            raise ValueError("the entries of state must be contiguous")
+        expect *= size
+    if slots is None and state.shape[0] < n:
+        raise ValueError(f"state has {state.shape[0]} entries for {n} sequences")
+    k.state = state.data_ptr()
+    k.state_slots = state.shape[0]
+    k.state_slot_stride = state.stride(0) if state.shape[0] > 1 else expect
+    k.slots = _vector(slots, n, torch.int32, device, "slots")
+    if resume is not None:
+        if resume.dtype not in (torch.bool, torch.uint8):
+            raise ValueError("resume must be a bool or uint8 tensor")
+        k.resume = _vector(resume, n, resume.dtype, device, "resume")
+
+
+def _conv_call(x, weight, bias, activation, cu_seqlens, state, slots, resume, out, step: bool):
+    """(ConvCall, out) of a convolution's arguments."""
+    if not x.is_cuda:
+        raise ValueError("the convolution runs on CUDA tensors only (no CPU path)")
+    dtype, device = x.dtype, x.device
+    if dtype not in DTYPE_CODE:
+        raise ValueError(f"unsupported dtype {dtype}")
+    if activation not in ACT_CODE:
+        raise ValueError(f"unknown activation {activation!r}")
+    if x.dim() < 2:
+        raise ValueError("x must be [rows, width] or [batch, length, width]")
+    if weight.dim() != 2:
+        raise ValueError("weight must be [width, taps]")
+    width = x.shape[-1]
+    taps = weight.shape[1]
+    k = ConvCall()
+    k.rows, k.x_row_stride = _rows_of(x, width, "x")
+    k.x = x.data_ptr()
+    k.width, k.taps, k.activation, k.dtype = width, taps, ACT_CODE[activation], DTYPE_CODE[dtype]
+    k.w = _vector(weight, width * taps, torch.float32, device, "weight")
+    k.bias = _vector(bias, width, torch.float32, device, "bias")
+    if out is None:
+        out = torch.empty(x.shape, dtype=dtype, device=device)
+    elif out.shape != x.shape or out.dtype != dtype or out.device != device:
+        raise ValueError("out must have the shape, dtype and device of x")
+    k.out = out.data_ptr()
+    k.out_row_stride = _rows_of(out, width, "out")[1]
+    _fill_seqs(k, x, device, cu_seqlens, state, slots, resume, (taps - 1, width), dtype, step)
+    return k, out
+
+
+def _launch(fn, k, device, what: str) -> None:
+    """A call on its tensors' device and that device's current stream."""
+    if torch.cuda.current_device() == device.index:
+        st = fn(ctypes.byref(k), torch.cuda.current_stream().cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            st = fn(ctypes.byref(k), torch.cuda.current_stream().cuda_stream)
+    if st != OK:
+        raise GgrnError(st, what)
+
+
+def causal_conv(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None, *,
+                activation: str | None = "silu", cu_seqlens: torch.Tensor | None = None,
+                state: torch.Tensor | None = None, slots: torch.Tensor | None = None,
+                resume: torch.Tensor | None = None,
+                out: torch.Tensor | None = None) -> torch.Tensor:
+    """The mixer's depthwise causal convolution over prompts (``ggrn_conv``):
+    ``out[t, c] = silu(bias[c] + sum_k weight[c, k] * x[t - (taps-1) + k, c])``.
+
+    ``x``: [rows, width] (one sequence, or those of ``cu_seqlens``) or [batch,
+    length, width], f32, f16 or bf16, row-strided views allowed (the x B C
+    columns of a packed in-proj are read in place).  ``weight``: f32 [width,
+    taps], 2 to 4 taps.  ``bias``: f32 [width].  ``activation``: "silu" or None.
+    ``cu_seqlens``: int32 [sequences + 1] row offsets of packed sequences; rows
+    behind the last one are left alone.  ``state``: [slots, taps - 1, width] of
+    x's dtype, receives each sequence's last inputs in its entry (``slots``,
+    int32; entry i without it), whose old contents the sequences with
+    ``resume`` continue.  Entries of one call are distinct.
+    """
+    k, out = _conv_call(x, weight, bias, activation, cu_seqlens, state, slots, resume, out, False)
+    _launch(load().ggrn_conv, k, x.device, "ggrn_conv")
+    return out
+
+
+def causal_conv_step(x: torch.Tensor, state: torch.Tensor, weight: torch.Tensor,
+                     bias: torch.Tensor | None = None, *, activation: str | None = "silu",
+                     slots: torch.Tensor | None = None,
+                     out: torch.Tensor | None = None) -> torch.Tensor:
+    """``causal_conv`` for one new row of each sequence (``ggrn_conv_step``):
+    ``x`` [batch, width]; row i continues entry ``slots[i]`` (i without slots)
+    of ``state`` and updates it in place.  A row whose slot is outside the pool
+    is skipped: its output row is left as it was.
+    """
+    k, out = _conv_call(x, weight, bias, activation, None, state, slots, None, out, True)
+    _launch(load().ggrn_conv_step, k, x.device, "ggrn_conv_step")
+    return out
+
+
+def _scan_call(x, dt, a, b, c, head_dim, state_size, d, dt_bias, dt_softplus, dt_limits,
+               cu_seqlens, state, slots, resume, out, step: bool):
+    """(ScanCall, out) of a scan's arguments."""
+    if not x.is_cuda:
+        raise ValueError("the scan runs on CUDA tensors only (no CPU path)")
+    dtype, device = x.dtype, x.device
+    if dtype not in DTYPE_CODE:
+        raise ValueError(f"unsupported dtype {dtype}")
+    if x.dim() < 2:
+        raise ValueError("x must be [rows, width] or [batch, length, width]")
+    width, heads, gn = x.shape[-1], a.numel(), b.shape[-1]
+    if heads == 0 or head_dim * heads != width:
+        raise ValueError(f"x has {width} columns, not {heads} heads of {head_dim}")
+    if state_size <= 0 or gn % state_size or gn == 0:
+        raise ValueError(f"b has {gn} columns, not a multiple of state_size {state_size}")
+    lead = x.shape[:-1]
+    for t, n, name in ((dt, heads, "dt"), (b, gn, "b"), (c, gn, "c")):
+        if t.dtype != dtype or t.device != device:
+            raise ValueError(f"{name} must have the dtype and device of x")
+        if t.shape[:-1] != lead or t.shape[-1] != n:
+            raise ValueError(f"{name} must have the leading shape of x and {n} columns")
+    k = ScanCall()
+    k.rows, k.x_row_stride = _rows_of(x, width, "x")
+    k.dt_row_stride = _rows_of(dt, heads, "dt")[1]
+    k.b_row_stride = _rows_of(b, gn, "b")[1]
+    k.c_row_stride = _rows_of(c, gn, "c")[1]
+    k.x, k.dt, k.b, k.c = x.data_ptr(), dt.data_ptr(), b.data_ptr(), c.data_ptr()
+    k.heads, k.head_dim, k.groups, k.state_size = heads, head_dim, gn // state_size, state_size
+    k.a = _vector(a, heads, torch.float32, device, "a")
+    k.d = _vector(d, heads, torch.float32, device, "d")
+    k.dt_bias = _vector(dt_bias, heads, torch.float32, device, "dt_bias")
+    k.dt_min, k.dt_max = dt_limits
+    k.dt_softplus, k.dtype = (1 if dt_softplus else 0), DTYPE_CODE[dtype]
+    if out is None:
+        out = torch.empty(x.shape, dtype=dtype, device=device)
+    elif out.shape != x.shape or out.dtype != dtype or out.device != device:
+        raise ValueError("out must have the shape, dtype and device of x")
+    k.out = out.data_ptr()
+    k.out_row_stride = _rows_of(out, width, "out")[1]
+    _fill_seqs(k, x, device, cu_seqlens, state, slots, resume, (heads, head_dim, state_size),
+               torch.float32, step)
+    return k, out
+
+
+def ssm_scan(x: torch.Tensor, dt: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
+             c: torch.Tensor, *, head_dim: int, state_size: int, d: torch.Tensor | None = None,
+             dt_bias: torch.Tensor | None = None, dt_softplus: bool = True,
+             dt_limits: tuple[float, float] = (0.0, float("inf")),
+             cu_seqlens: torch.Tensor | None = None, state: torch.Tensor | None = None,
+             slots: torch.Tensor | None = None, resume: torch.Tensor | None = None,
+             out: torch.Tensor | None = None,
+             workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """The selective state space scan of the Mamba-2 mixer over prompts
+    (``ggrn_scan``).  Per head h of ``head_dim`` columns and its group g:
+
+        dt_t = clamp(softplus(dt[t, h] + dt_bias[h]), *dt_limits)
+        S_t  = exp(dt_t * a[h]) * S_{t-1} + dt_t * outer(x[t, h], b[t, g])
+        out[t, h] = S_t @ c[t, g] + d[h] * x[t, h]
+
+    ``x``: [rows, heads * head_dim] or [batch, length, ...]; ``dt``: [..,
+    heads]; ``b``, ``c``: [.., groups * state_size]; all of one dtype (f32, f16,
+    bf16), row-strided views allowed.  ``a``, ``d``, ``dt_bias``: f32 [heads].
+    ``dt_softplus=False`` takes ``dt + dt_bias`` as it is.  ``state``: f32
+    [slots, heads, head_dim, state_size]; ``cu_seqlens``, ``slots`` and
+    ``resume`` as in ``causal_conv``.  ``workspace``: optional uint8 device
+    tensor of ``scan_workspace_bytes`` (allocated when omitted and needed).
+    """
+    k, out = _scan_call(x, dt, a, b, c, head_dim, state_size, d, dt_bias, dt_softplus, dt_limits,
+                        cu_seqlens, state, slots, resume, out, False)
+    lib = load()
+    if workspace is None:
+        n = lib.ggrn_scan_workspace_bytes(ctypes.byref(k))
+        if n > 0:
+            workspace = torch.empty(n, dtype=torch.uint8, device=x.device)
+    elif workspace.device != x.device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the device of x")
+    if workspace is not None:
+        k.workspace = workspace.data_ptr()
+        k.workspace_bytes = workspace.numel() * workspace.element_size()
+    _launch(lib.ggrn_scan, k, x.device, "ggrn_scan")
+    return out
+
+
+def ssm_scan_step(x: torch.Tensor, dt: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
+                  c: torch.Tensor, state: torch.Tensor, *, d: torch.Tensor | None = None,
+                  dt_bias: torch.Tensor | None = None, dt_softplus: bool = True,
+                  dt_limits: tuple[float, float] = (0.0, float("inf")),
+                  slots: torch.Tensor | None = None,
+                  out: torch.Tensor | None = None) -> torch.Tensor:
+    """``ssm_scan`` for one new row of each sequence (``ggrn_scan_step``): row i
+    of ``x`` [batch, heads * head_dim] advances entry ``slots[i]`` (i without
+    slots) of ``state`` [slots, heads, head_dim, state_size] in place.  A row
+    whose slot is outside the pool is skipped: its output row is left as it
+    was.
+    """
+    if state.dim() != 4:
+        raise ValueError("state must be [slots, heads, head_dim, state_size]")
+    k, out = _scan_call(x, dt, a, b, c, state.shape[2], state.shape[3], d, dt_bias, dt_softplus,
+                        dt_limits, None, state, slots, None, out, True)
+    _launch(load().ggrn_scan_step, k, x.device, "ggrn_scan_step")
+    return out
+
+
+def scan_workspace_bytes(x, dt, a, b, c, *, head_dim: int, state_size: int,
+                         cu_seqlens: torch.Tensor | None = None) -> int:
+    """Workspace bytes of ``ssm_scan`` on these tensors (0: none needed)."""
+    k, _ = _scan_call(x, dt, a, b, c, head_dim, state_size, None, None, True, (0.0, 0.0),
+                      cu_seqlens, None, None, None, None, False)
+    return load().ggrn_scan_workspace_bytes(ctypes.byref(k))
+
+
+def _given(c: dict, name: str):
+    """An argument that a graph's call has to bring."""
+    if c.get(name) is None:
+        raise ValueError(f"a call of a graph needs {name}")
+    return c.pop(name)
+
+
 class DecodeGraph:
     """A chain of calls captured once into a CUDA graph and replayed with one launch.
 
     ``calls``: list of dicts with the tensors and arguments of ``forward``
-    (``y``, ``gate``, ``w``, ``out``, ``group_size``, ``eps``, ``mode``).  The
-    tensors are baked into the graph: keep them alive and refill them in
-    place between replays.  A chain of one call is launched directly on each
-    replay (a graph of one small kernel costs more to launch than the kernel).
+    (``y``, ``gate``, ``w``, ``out``, ``group_size``, ``eps``, ``mode``), or, with
+    ``op`` set to "causal_conv_step" or "ssm_scan_step", those of that function
+    (``out`` included), in the order they run: a decode step of the mixer is
+    its convolution, scan and norm.  Each replay advances the states.  The
+    tensors are baked into the graph: keep them alive and refill them in place
+    between replays.  A chain of one call is launched directly on each replay
+    (a graph of one small kernel costs more to launch than the kernel).
     """
 
     def __init__(self, calls: list[dict]):
-        arr = (Call * len(calls))()
+        arr = (Step * len(calls))()
         self._keep = []
-        for i, c in enumerate(calls):
-            y, gate, w, out = c["y"], c["gate"], c["w"], c["out"]
-            width = y.shape[-1]
-            rows, ys = _as_rows(y, width, "y")
-            _, gts = _as_rows(gate, width, "gate")
-            _, os_ = _as_rows(out, width, "out")
-            arr[i] = Call(y.data_ptr(), gate.data_ptr(), w.data_ptr(), out.data_ptr(), rows, width,
-                          c["group_size"], ys, gts, os_, float(c["eps"]), DTYPE_CODE[y.dtype],
-                          MODE_CODE[c.get("mode", "mamba2")])
-            self._keep.extend([y, gate, w, out])
+        device = None
+        for i, call in enumerate(calls):
+            c = dict(call)
+            op = c.pop("op", "forward")
+            self._keep.extend(v for v in c.values() if isinstance(v, torch.Tensor))
+            if op == "forward":
+                y, gate, w, out = c["y"], c["gate"], c["w"], c["out"]
+                width = y.shape[-1]
+                rows, ys = _as_rows(y, width, "y")
+                _, gts = _as_rows(gate, width, "gate")
+                _, os_ = _as_rows(out, width, "out")
+                arr[i].kind = STEP_FORWARD
+                arr[i].u.forward = Call(y.data_ptr(), gate.data_ptr(), w.data_ptr(),
+                                        out.data_ptr(), rows, width, c["group_size"], ys, gts, os_,
+                                        float(c["eps"]), DTYPE_CODE[y.dtype],
+                                        MODE_CODE[c.get("mode", "mamba2")])
+                here = y.device
+            elif op == "causal_conv_step":
+                arr[i].kind = STEP_CONV
+                arr[i].u.conv = _conv_call(c.pop("x"), c.pop("weight"), c.pop("bias", None),
+                                           c.pop("activation", "silu"), None, c.pop("state"),
+                                           c.pop("slots", None), None, _given(c, "out"), True)[0]
+                here = call["x"].device
+            elif op == "ssm_scan_step":
+                st = c.pop("state")
+                if st.dim() != 4:
+                    raise ValueError("state must be [slots, heads, head_dim, state_size]")
+                arr[i].kind = STEP_SCAN
+                arr[i].u.scan = _scan_call(c.pop("x"), c.pop("dt"), c.pop("a"), c.pop("b"),
+                                           c.pop("c"), st.shape[2], st.shape[3], c.pop("d", None),
+                                           c.pop("dt_bias", None), c.pop("dt_softplus", True),
+                                           c.pop("dt_limits", (0.0, float("inf"))), None, st,
+                                           c.pop("slots", None), None, _given(c, "out"), True)[0]
+                here = call["x"].device
+            else:
+                raise ValueError(f"unknown op {op!r}")
+            if op != "forward" and c:
+                raise ValueError(f"{op} takes no {', '.join(sorted(c))}")
+            if device is not None and here != device:
+                raise ValueError("the calls of a graph run on one device")
+            device = here
+        self.device = device
         self._handle = ctypes.c_void_p()
-        st = load().ggrn_graph_create(arr, len(calls), ctypes.byref(self._handle))
+        st = load().ggrn_graph_create_steps(arr, len(calls), ctypes.byref(self._handle))
         if st != OK:
-            raise GgrnError(st, "ggrn_graph_create")
-        self.device = calls[0]["y"].device
+            raise GgrnError(st, "ggrn_graph_create_steps")
 
     def replay(self, stream: torch.cuda.Stream | None = None) -> None:
         s = stream.cuda_stream if stream is not None else torch.cuda.current_stream(self.device).cuda_stream

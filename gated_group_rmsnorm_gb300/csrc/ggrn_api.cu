@@ -17,9 +17,11 @@
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
+#include <new>
 
 #include "../../include/ggrn.h"
 #include "ggrn_internal.h"
+#include "ggrn_mixer.cuh"
 #include "ggrn_slots.h"
 
 // Device status word of the library (one per device): kernels whose bounded
@@ -838,9 +840,77 @@ int forward_impl(const Args& a, int path, cudaStream_t s) {
 
 struct DecodeGraph {
   cudaGraphExec_t exec = nullptr;  // the captured chain (two or more calls)
-  bool direct = false;             // one call: launched as ggrn_forward would
-  Args call;
+  bool direct = false;             // one call: launched as the call itself would
+  ggrn_step step;
 };
+
+Args args_of(const ggrn_call& c) {
+  return make_args(c.y, c.gate, c.w, c.out, c.rows, c.width, c.group_size, c.y_row_stride,
+                   c.gate_row_stride, c.out_row_stride, c.eps, c.dtype, c.mode);
+}
+
+// One call of a decode chain: its argument checks alone, and the call.
+int check_step(const ggrn_step& t) {
+  if (t.kind == GGRN_STEP_CONV) return check_conv(t.u.conv, true);
+  if (t.kind == GGRN_STEP_SCAN) return check_scan(t.u.scan, true);
+  if (t.kind != GGRN_STEP_FORWARD) return GGRN_ERR_ARG;
+  const Args a = args_of(t.u.forward);
+  const int st = validate(a);
+  Plan p;
+  return st != GGRN_OK || a.rows == 0 ? st : make_plan(a, kAuto, &p);
+}
+int enqueue_step(const ggrn_step& t, cudaStream_t s) {
+  if (t.kind == GGRN_STEP_CONV) return ggrn_conv_step(&t.u.conv, s);
+  if (t.kind == GGRN_STEP_SCAN) return ggrn_scan_step(&t.u.scan, s);
+  return forward_impl(args_of(t.u.forward), kAuto, s);
+}
+
+// The handle of a chain whose calls `at(i)` gives.
+template <typename At>
+int create_graph(At at, int32_t n, void** graph) {
+  // Validate and plan every call before capturing anything.
+  for (int32_t i = 0; i < n; ++i) {
+    const int st = check_step(at(i));
+    if (st != GGRN_OK) return st;
+  }
+  // symbol lookups before the capture starts
+  if (!fault_word() || !sched_words()) return GGRN_ERR_CUDA;
+  if (n == 1) {
+    // A graph of one small kernel costs more to launch than the kernel
+    // itself (decode: 4.1 against 3.4-3.7 us per call): a one-call chain is
+    // launched directly on each replay, with the same buffers.
+    DecodeGraph* dg = new (std::nothrow) DecodeGraph();
+    if (!dg) return GGRN_ERR_CUDA;
+    dg->direct = true;
+    dg->step = at(0);
+    *graph = dg;
+    return GGRN_OK;
+  }
+  cudaStream_t s = nullptr;
+  if (cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking) != cudaSuccess) return GGRN_ERR_CUDA;
+  int status = GGRN_OK;
+  cudaGraph_t g = nullptr;
+  if (cudaStreamBeginCapture(s, cudaStreamCaptureModeThreadLocal) != cudaSuccess) {
+    cudaStreamDestroy(s);
+    return GGRN_ERR_CUDA;
+  }
+  for (int32_t i = 0; i < n && status == GGRN_OK; ++i) status = enqueue_step(at(i), s);
+  cudaError_t e = cudaStreamEndCapture(s, &g);
+  if (status == GGRN_OK && e != cudaSuccess) status = GGRN_ERR_CUDA;
+  DecodeGraph* dg = nullptr;
+  if (status == GGRN_OK) {
+    dg = new (std::nothrow) DecodeGraph();
+    if (!dg || cudaGraphInstantiate(&dg->exec, g, 0) != cudaSuccess) {
+      status = GGRN_ERR_CUDA;
+      delete dg;
+      dg = nullptr;
+    }
+  }
+  if (g) cudaGraphDestroy(g);
+  cudaStreamDestroy(s);
+  if (status == GGRN_OK) *graph = dg;
+  return status;
+}
 
 }  // namespace
 
@@ -872,6 +942,8 @@ int plan_family(const Args& a, int path, int vpl, Plan* p) {
 }
 
 int launch_plan(const Args& a, const Plan& p, cudaStream_t s) { return launch(a, p, s); }
+
+int device_sms() { return sm_count(); }
 
 void record_cuda_error(cudaError_t e) { tl_last_cuda_error = e; }
 
@@ -999,68 +1071,26 @@ extern "C" int ggrn_plan(const void* y, const void* gate, const void* w, const v
 extern "C" int ggrn_graph_create(const ggrn_call* calls, int32_t n, void** graph) {
   if (!graph || n <= 0 || !calls) return GGRN_ERR_ARG;
   *graph = nullptr;
-  // Validate and plan every call before capturing anything.
-  for (int32_t i = 0; i < n; ++i) {
-    const ggrn_call& c = calls[i];
-    const Args a = make_args(c.y, c.gate, c.w, c.out, c.rows, c.width, c.group_size,
-                             c.y_row_stride, c.gate_row_stride, c.out_row_stride, c.eps, c.dtype,
-                             c.mode);
-    int st = validate(a);
-    if (st != GGRN_OK) return st;
-    Plan p;
-    if (a.rows > 0 && (st = make_plan(a, kAuto, &p)) != GGRN_OK) return st;
-  }
-  // symbol lookups before the capture starts
-  if (!fault_word() || !sched_words()) return GGRN_ERR_CUDA;
-  if (n == 1) {
-    // A graph of one small kernel costs more to launch than the kernel
-    // itself (decode: 4.1 against 3.4-3.7 us per call): a one-call chain is
-    // launched directly on each replay, with the same buffers.
-    DecodeGraph* dg = new DecodeGraph();
-    dg->direct = true;
-    const ggrn_call& c = calls[0];
-    dg->call = make_args(c.y, c.gate, c.w, c.out, c.rows, c.width, c.group_size,
-                         c.y_row_stride, c.gate_row_stride, c.out_row_stride, c.eps, c.dtype,
-                         c.mode);
-    *graph = dg;
-    return GGRN_OK;
-  }
-  cudaStream_t s = nullptr;
-  if (cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking) != cudaSuccess) return GGRN_ERR_CUDA;
-  int status = GGRN_OK;
-  cudaGraph_t g = nullptr;
-  if (cudaStreamBeginCapture(s, cudaStreamCaptureModeThreadLocal) != cudaSuccess) {
-    cudaStreamDestroy(s);
-    return GGRN_ERR_CUDA;
-  }
-  for (int32_t i = 0; i < n && status == GGRN_OK; ++i) {
-    const ggrn_call& c = calls[i];
-    const Args a = make_args(c.y, c.gate, c.w, c.out, c.rows, c.width, c.group_size,
-                             c.y_row_stride, c.gate_row_stride, c.out_row_stride, c.eps, c.dtype,
-                             c.mode);
-    status = forward_impl(a, kAuto, s);
-  }
-  cudaError_t e = cudaStreamEndCapture(s, &g);
-  if (status == GGRN_OK && e != cudaSuccess) status = GGRN_ERR_CUDA;
-  DecodeGraph* dg = nullptr;
-  if (status == GGRN_OK) {
-    dg = new DecodeGraph();
-    if (cudaGraphInstantiate(&dg->exec, g, 0) != cudaSuccess) {
-      status = GGRN_ERR_CUDA;
-      delete dg;
-      dg = nullptr;
-    }
-  }
-  if (g) cudaGraphDestroy(g);
-  cudaStreamDestroy(s);
-  if (status == GGRN_OK) *graph = dg;
-  return status;
+  return create_graph(
+      [calls](int32_t i) {
+        ggrn_step t = {};
+        t.kind = GGRN_STEP_FORWARD;
+        t.u.forward = calls[i];
+        return t;
+      },
+      n, graph);
+}
+
+extern "C" int ggrn_graph_create_steps(const ggrn_step* steps, int32_t n, void** graph) {
+  if (!graph || n <= 0 || !steps) return GGRN_ERR_ARG;
+  *graph = nullptr;
+  return create_graph([steps](int32_t i) -> const ggrn_step& { return steps[i]; }, n, graph);
 }
 
 extern "C" int ggrn_graph_launch(void* graph, void* cuda_stream) {
   if (!graph) return GGRN_ERR_ARG;
   DecodeGraph* dg = static_cast<DecodeGraph*>(graph);
-  if (dg->direct) return forward_impl(dg->call, kAuto, static_cast<cudaStream_t>(cuda_stream));
+  if (dg->direct) return enqueue_step(dg->step, static_cast<cudaStream_t>(cuda_stream));
   return cudaGraphLaunch(dg->exec, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess
              ? GGRN_OK
              : GGRN_ERR_CUDA;

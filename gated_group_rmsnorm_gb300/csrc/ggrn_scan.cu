@@ -1,0 +1,552 @@
+// ggrn_scan.cu -- the selective state space scan of the Mamba-2 mixer (one
+// decay per head) for prompts and for single tokens.
+//
+//   dt[t] = clamp(softplus(dt_raw + dt_bias)),  e[t] = exp(dt[t] a)
+//   S[t]  = e[t] S[t-1] + dt[t] x[t] (x) B[t],  y[t] = S[t] C[t] + d x[t]
+//
+// with S [head_dim, state_size] per head and B, C shared by the heads of a
+// group.
+//
+// k_scan is the recurrence as it stands, for every type and size: the state
+// lives in registers in f32 (4 rows of S x 16 columns per thread, a team of
+// lanes across the columns), tokens come in blocks of 16 through shared
+// memory, three f32x2 instructions per pair of state entries and token.
+//
+// A sequence longer than a part (see find_part) is cut: a first launch runs
+// every part but the last of its sequence from a zero state, for its final
+// state and its decay alone; k_scan_join turns those into the states at the
+// parts' starts; the main launch then runs all parts at once.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "ggrn_scan.cuh"
+
+namespace ggrn {
+namespace scan {
+
+// ---------------------------------------------------------------------------
+// k_scan: the recurrence, token by token.
+// ---------------------------------------------------------------------------
+constexpr int kBlock = 16;   // tokens staged in shared memory at a time
+constexpr int kCols = 16;    // state columns of a thread: 4 runs of 4, team-interleaved
+constexpr int kMaxThreads = 256;
+constexpr int kMinPart = 64;  // rows of the shortest part worth its join
+
+template <typename T>
+__device__ __forceinline__ float ld1(const T* p) {
+  return Elem<T>::load1(p, 0);
+}
+
+// RP: rows of S per thread.  `STATE_ONLY`: the first launch of a cut scan.
+template <typename T, int RP, bool STATE_ONLY>
+__global__ void __launch_bounds__(kMaxThreads) k_scan(const Params p, const int tl, const int prows) {
+  extern __shared__ float smem[];
+  const int P = p.P, N = p.N;
+  const int NP = tl * kCols;                 // state columns padded to the teams' span
+  float* sB = smem;                          // [kBlock][NP]
+  float* sC = sB + kBlock * NP;              // [kBlock][NP]
+  float* sX = sC + kBlock * NP;              // [kBlock][prows]
+  float* sY = sX + kBlock * prows;           // [kBlock][prows]
+  float* sDt = sY + kBlock * prows;          // [kBlock] dt, [kBlock] decay
+  pdl_wait();
+  pdl_launch_dependents();
+  const Part part = find_part(p.q, p.part, blockIdx.x);
+  if (part.seq < 0 || (STATE_ONLY && part.index == part.count - 1)) return;
+  // (offsets that do not ascend may count more places than there are)
+  if (part.count > 1 && part.place + (STATE_ONLY ? 1 : 0) >= p.places) return;
+  const int h = blockIdx.y, g = h / p.hpg;
+  const int row0 = blockIdx.z * prows;
+  const int rows_here = min(prows, P - row0);
+  const int tid = threadIdx.x, nthr = blockDim.x;
+  const int l = tid & (tl - 1);
+  const int r0 = tid / tl * RP;              // this thread's first row of the tile
+  const float a = __ldg(p.a + h), dbias = p.dt_bias ? __ldg(p.dt_bias + h) : 0.0f;
+  const float dskip = p.d ? __ldg(p.d + h) : 0.0f;
+  const int64_t slot = seq_slot(p.q, part.seq);
+
+  float s[RP][kCols];
+  // the state this part starts from: the workspace's for a cut sequence,
+  // else the pool's or zeros
+  const float* from = nullptr;
+  if (!STATE_ONLY) {
+    if (part.count > 1) {
+      from = p.ws + (part.place * p.H + h) * P * N;
+    } else if (slot >= 0 && seq_resumes(p.q, part.seq)) {
+      from = p.state + slot * p.slot_stride + static_cast<int64_t>(h) * P * N;
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < RP; ++r)
+#pragma unroll
+    for (int j = 0; j < kCols; ++j) {
+      const int n = (j / 4 * tl + l) * 4 + j % 4, row = row0 + r0 + r;
+      s[r][j] = from && n < N && r0 + r < rows_here ? from[static_cast<int64_t>(row) * N + n] : 0.0f;
+    }
+
+  const T* x = static_cast<const T*>(p.x) + static_cast<int64_t>(h) * P + row0;
+  const T* b = static_cast<const T*>(p.b) + static_cast<int64_t>(g) * N;
+  const T* c = static_cast<const T*>(p.c) + static_cast<int64_t>(g) * N;
+  const T* dtp = static_cast<const T*>(p.dt) + h;
+  T* out = static_cast<T*>(p.out) + static_cast<int64_t>(h) * P + row0;
+  float log_decay = 0.0f;  // STATE_ONLY, thread 0
+
+  for (int64_t t0 = part.begin; t0 < part.end; t0 += kBlock) {
+    const int nt = static_cast<int>(min(static_cast<int64_t>(kBlock), part.end - t0));
+    __syncthreads();
+    for (int i = tid; i < nt * NP; i += nthr) {
+      const int t = i / NP, n = i - t * NP;
+      sB[i] = n < N ? ld1(b + (t0 + t) * p.bs + n) : 0.0f;
+      if (!STATE_ONLY) sC[i] = n < N ? ld1(c + (t0 + t) * p.cs + n) : 0.0f;
+    }
+    for (int i = tid; i < nt * prows; i += nthr) {
+      const int t = i / prows, r = i - t * prows;
+      sX[i] = r < rows_here ? ld1(x + (t0 + t) * p.xs + r) : 0.0f;
+    }
+    if (tid < nt) {
+      const float dt = dt_of(ld1(dtp + (t0 + tid) * p.dts), dbias, p);
+      sDt[tid] = dt;
+      sDt[kBlock + tid] = expf(dt * a);
+    }
+    __syncthreads();
+    if (STATE_ONLY && tid == 0)
+      for (int t = 0; t < nt; ++t) log_decay = fmaf(sDt[t], a, log_decay);
+    for (int t = 0; t < nt; ++t) {
+      const float dt = sDt[t], e = sDt[kBlock + t];
+      float xv[RP], y0[RP], y1[RP];
+#pragma unroll
+      for (int r = 0; r < RP; ++r) {
+        xv[r] = dt * sX[t * prows + r0 + r];
+        y0[r] = y1[r] = 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < kCols; j += 4) {
+        const float4 bv = *reinterpret_cast<const float4*>(sB + t * NP + (j / 4 * tl + l) * 4);
+        float4 cv = make_float4(0, 0, 0, 0);
+        if (!STATE_ONLY)
+          cv = *reinterpret_cast<const float4*>(sC + t * NP + (j / 4 * tl + l) * 4);
+#pragma unroll
+        for (int r = 0; r < RP; ++r) {
+          float u0, u1, u2, u3;
+          mul2(u0, u1, bv.x, bv.y, xv[r], xv[r]);
+          mul2(u2, u3, bv.z, bv.w, xv[r], xv[r]);
+          fma2(s[r][j], s[r][j + 1], s[r][j], s[r][j + 1], e, e, u0, u1);
+          fma2(s[r][j + 2], s[r][j + 3], s[r][j + 2], s[r][j + 3], e, e, u2, u3);
+          if (!STATE_ONLY) {
+            fma2(y0[r], y1[r], s[r][j], s[r][j + 1], cv.x, cv.y, y0[r], y1[r]);
+            fma2(y0[r], y1[r], s[r][j + 2], s[r][j + 3], cv.z, cv.w, y0[r], y1[r]);
+          }
+        }
+      }
+      if (!STATE_ONLY) {
+#pragma unroll
+        for (int r = 0; r < RP; ++r) {
+          float y = y0[r] + y1[r];
+          for (int o = tl >> 1; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+          if (l == 0) sY[t * prows + r0 + r] = y;
+        }
+      }
+    }
+    if (!STATE_ONLY) {
+      __syncthreads();
+      for (int i = tid; i < nt * prows; i += nthr) {
+        const int t = i / prows, r = i - t * prows;
+        if (r < rows_here)
+          Elem<T>::store1(out + (t0 + t) * p.os + r, 0, fmaf(dskip, sX[i], sY[i]));
+      }
+    }
+  }
+
+  // where the state goes: the next part's place in the workspace, or the pool
+  float* to = nullptr;
+  if (STATE_ONLY) {
+    to = p.ws + ((part.place + 1) * p.H + h) * P * N;
+    if (tid == 0 && blockIdx.z == 0)
+      p.ws_decay[part.place * p.H + h] = expf(log_decay);
+  } else if (part.index == part.count - 1 && slot >= 0) {
+    to = p.state + slot * p.slot_stride + static_cast<int64_t>(h) * P * N;
+  }
+  if (!to) return;
+#pragma unroll
+  for (int r = 0; r < RP; ++r)
+#pragma unroll
+    for (int j = 0; j < kCols; ++j) {
+      const int n = (j / 4 * tl + l) * 4 + j % 4, row = row0 + r0 + r;
+      if (n < N && r0 + r < rows_here) to[static_cast<int64_t>(row) * N + n] = s[r][j];
+    }
+}
+
+// ---------------------------------------------------------------------------
+// k_scan_join: the states at the starts of a cut sequence's parts.  The place
+// of part i > 0 holds what part i - 1 adds to the state from a zero start; a
+// thread takes one state entry through the parts of its sequence.  grid:
+// (blocks of entries, heads, sequences).
+// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(256) k_scan_join(const Params p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t seq = blockIdx.z;
+  const int h = blockIdx.y;
+  int64_t begin, end;
+  seq_range(p.q, seq, begin, end);
+  const int64_t count = parts_of(end - begin, p.part);
+  if (count == 1) return;
+  // place of the sequence's first part
+  int64_t first = 0;
+  if (!p.q.cu) {
+    first = seq * count;
+  } else {
+    const int lane = threadIdx.x & 31;
+    for (int64_t i = lane; i < seq; i += 32) {
+      int64_t b, e;
+      seq_range(p.q, i, b, e);
+      first += static_cast<int64_t>(part_counts(e - b, p.part) >> 32);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) first += __shfl_xor_sync(0xffffffffu, first, o);
+  }
+  if (first + count > p.places) return;  // offsets that do not ascend: no places for these
+  const int64_t PN = static_cast<int64_t>(p.P) * p.N;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  if (i >= PN) return;
+  const int64_t slot = seq_slot(p.q, seq);
+  float s = slot >= 0 && seq_resumes(p.q, seq)
+                ? p.state[slot * p.slot_stride + static_cast<int64_t>(h) * PN + i]
+                : 0.0f;
+  float* w = p.ws + (first * p.H + h) * PN + i;
+  const float* decay = p.ws_decay + first * p.H + h;
+  w[0] = s;
+  const int64_t stride = static_cast<int64_t>(p.H) * PN;
+  for (int64_t k = 0; k + 1 < count; ++k) {
+    w += stride;
+    s = fmaf(s, decay[k * p.H], *w);
+    *w = s;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// k_scan_step: one token.  Bound by the state's bytes (8 per entry, read and
+// written once).  A warp takes kStepRows rows of one head's S at a time, all
+// their loads in flight before the first is used; the lanes hold B and C of
+// their columns.  VEC: lanes take 4 columns (16 bytes), state_size a multiple
+// of 4 and the pool 16-byte aligned; else one column each.
+// ---------------------------------------------------------------------------
+constexpr int kStepRows = 4;
+constexpr int kStepThreads = 128;
+
+template <typename T, int CH, bool VEC>
+__global__ void __launch_bounds__(kStepThreads) k_scan_step(const Params p, const int tl,
+                                                            const int tile) {
+  constexpr int E = VEC ? 4 : 1;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t i = blockIdx.x;
+  const int h = blockIdx.y, g = h / p.hpg, P = p.P, N = p.N;
+  const int64_t slot = seq_slot(p.q, i);
+  if (slot < 0) return;
+  const int l = threadIdx.x & (tl - 1);          // lane of the team of a row
+  const int team = threadIdx.x / tl, teams = kStepThreads / tl;
+  const int p0 = blockIdx.z * tile;
+  const int p1 = min(P, p0 + tile);
+  const T* x = static_cast<const T*>(p.x) + i * p.xs + static_cast<int64_t>(h) * P;
+  T* out = static_cast<T*>(p.out) + i * p.os + static_cast<int64_t>(h) * P;
+  float* st = p.state + slot * p.slot_stride + static_cast<int64_t>(h) * P * N;
+
+  // the first rows' states are in flight before anything else is waited for
+  float s[kStepRows][CH * E];
+  auto fetch = [&](int r0) {
+#pragma unroll
+    for (int r = 0; r < kStepRows; ++r) {
+      const int row = r0 + r * teams;
+#pragma unroll
+      for (int k = 0; k < CH; ++k) {
+        const int n = (k * tl + l) * E;
+        if (row < p1 && n < N) {
+          if constexpr (VEC) {
+            const float4 v = __ldcs(reinterpret_cast<const float4*>(st + static_cast<int64_t>(row) * N + n));
+            s[r][k * 4] = v.x, s[r][k * 4 + 1] = v.y, s[r][k * 4 + 2] = v.z, s[r][k * 4 + 3] = v.w;
+          } else {
+            s[r][k] = st[static_cast<int64_t>(row) * N + n];
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < E; ++e) s[r][k * E + e] = 0.0f;
+        }
+      }
+    }
+  };
+  fetch(p0 + team);
+  float bv[CH * E], cv[CH * E];
+  const T* b = static_cast<const T*>(p.b) + i * p.bs + static_cast<int64_t>(g) * N;
+  const T* c = static_cast<const T*>(p.c) + i * p.cs + static_cast<int64_t>(g) * N;
+#pragma unroll
+  for (int k = 0; k < CH; ++k)
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int n = (k * tl + l) * E + e;
+      bv[k * E + e] = n < N ? ld1(b + n) : 0.0f;
+      cv[k * E + e] = n < N ? ld1(c + n) : 0.0f;
+    }
+  const float dt = dt_of(ld1(static_cast<const T*>(p.dt) + i * p.dts + h),
+                         p.dt_bias ? __ldg(p.dt_bias + h) : 0.0f, p);
+  const float e = expf(dt * __ldg(p.a + h));
+  const float dskip = p.d ? __ldg(p.d + h) : 0.0f;
+  // every team of a warp makes the same number of rounds (the shuffles)
+  for (int r0 = p0; r0 < p1; r0 += kStepRows * teams) {
+    if (r0 > p0) fetch(r0 + team);
+#pragma unroll
+    for (int r = 0; r < kStepRows; ++r) {
+      const int row = r0 + team + r * teams;
+      const float xv = row < p1 ? ld1(x + row) : 0.0f;
+      const float xd = dt * xv;
+      float y = 0.0f;
+#pragma unroll
+      for (int k = 0; k < CH * E; ++k) {
+        s[r][k] = fmaf(s[r][k], e, xd * bv[k]);
+        y = fmaf(s[r][k], cv[k], y);
+      }
+#pragma unroll
+      for (int k = 0; k < CH; ++k) {
+        const int n = (k * tl + l) * E;
+        if (row < p1 && n < N) {
+          if constexpr (VEC)
+            __stcs(reinterpret_cast<float4*>(st + static_cast<int64_t>(row) * N + n),
+                   make_float4(s[r][k * 4], s[r][k * 4 + 1], s[r][k * 4 + 2], s[r][k * 4 + 3]));
+          else
+            st[static_cast<int64_t>(row) * N + n] = s[r][k];
+        }
+      }
+      for (int o = tl >> 1; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+      if (l == 0 && row < p1) Elem<T>::store1(out + row, 0, fmaf(dskip, xv, y));
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side.
+// ---------------------------------------------------------------------------
+int pow2_at_least(int v) {
+  int p = 1;
+  while (p < v) p <<= 1;
+  return p;
+}
+
+// Rows of S per CTA and threads of k_scan.
+struct Shape {
+  int tl, threads, prows, ptiles;
+  size_t smem;
+};
+constexpr int kRowsPerThread = 4;
+Shape shape_of(int P, int N) {
+  Shape s;
+  s.tl = pow2_at_least((N + kCols - 1) / kCols);
+  const int most = kMaxThreads / s.tl * kRowsPerThread;  // rows of the largest CTA
+  s.ptiles = (P + most - 1) / most;
+  const int teams = ((P + s.ptiles - 1) / s.ptiles + kRowsPerThread - 1) / kRowsPerThread;
+  s.threads = (teams * s.tl + 31) / 32 * 32;
+  s.prows = s.threads / s.tl * kRowsPerThread;
+  s.ptiles = (P + s.prows - 1) / s.prows;
+  s.smem = (2 * static_cast<size_t>(kBlock) * s.tl * kCols + 2 * kBlock * s.prows + 2 * kBlock) * 4;
+  return s;
+}
+
+// Rows of a part of k_scan: long sequences are cut until the launch holds
+// about three CTAs for each SM.
+int64_t part_rows(int64_t rows, int64_t ctas_per_part) {
+  const int64_t want = 3 * static_cast<int64_t>(device_sms());
+  const int64_t parts = std::max<int64_t>(1, want / std::max<int64_t>(1, ctas_per_part));
+  const int64_t part = (rows + parts - 1) / parts;
+  return std::max<int64_t>(kMinPart, (part + kBlock - 1) / kBlock * kBlock);
+}
+
+// The most rows a sequence can have.
+int64_t longest(const ggrn_scan_call& c) {
+  return c.cu_seqlens || c.seqs <= 0 ? c.rows : c.rows / c.seqs;
+}
+
+struct Layout {
+  int64_t part, parts;      // rows of a part; the most parts there can be
+  int64_t places;           // the most of them that are of cut sequences
+  bool cut;                 // whether a sequence may have more than one
+  int64_t state_bytes, bytes;
+};
+Layout layout_of(const ggrn_scan_call& c) {
+  Layout l;
+  const Shape s = shape_of(static_cast<int>(c.head_dim), static_cast<int>(c.state_size));
+  l.part = part_rows(c.rows, c.heads * s.ptiles);
+  l.cut = longest(c) > l.part;
+  if (!l.cut) l.part = std::max<int64_t>(1, longest(c));
+  l.parts = c.rows / l.part + c.seqs;
+  if (!c.cu_seqlens && c.seqs > 0)
+    l.parts = c.seqs * std::max<int64_t>(1, (c.rows / c.seqs + l.part - 1) / l.part);
+  l.places = l.state_bytes = l.bytes = 0;
+  if (l.cut) {
+    l.places = c.cu_seqlens ? std::min(l.parts, 2 * (c.rows / l.part)) : l.parts;
+    l.state_bytes = (l.places * c.heads * c.head_dim * c.state_size * 4 + 15) / 16 * 16;
+    l.bytes = l.state_bytes + (l.places * c.heads * 4 + 15) / 16 * 16;
+  }
+  return l;
+}
+
+// Sizes alone (what ggrn_scan_workspace_bytes looks at).
+int check_sizes(const ggrn_scan_call& c) {
+  if (c.dtype != kF32 && c.dtype != kF16 && c.dtype != kBF16) return GGRN_ERR_DTYPE;
+  if (c.rows < 0 || c.heads <= 0 || c.head_dim <= 0 || c.groups <= 0 || c.state_size <= 0 ||
+      c.heads % c.groups != 0)
+    return GGRN_ERR_SHAPE;
+  if (c.state_size > 256 || c.heads > 65535 || c.head_dim > 65535) return GGRN_ERR_UNSUPPORTED;
+  return GGRN_OK;
+}
+
+int check(const ggrn_scan_call& c, bool step, Params* p) {
+  int st = check_sizes(c);
+  if (st != GGRN_OK) return st;
+  if (!(c.dt_min >= 0.0f) || !(c.dt_max >= c.dt_min)) return GGRN_ERR_ARG;
+  const int es = mixer::elem_bytes(c.dtype);
+  const int64_t width = c.heads * c.head_dim, gn = c.groups * c.state_size;
+  const int64_t held = width * c.state_size;
+  st = mixer::check_seqs(c.rows, c.seqs, c.cu_seqlens, c.state, c.slots, c.resume, c.state_slots,
+                         held, c.state_slot_stride, step, &p->q);
+  if (st != GGRN_OK) return st;
+  mixer::Buffer x, dt, b, cc, out, state;
+  if (!mixer::extent(c.x, c.rows, width, c.x_row_stride, es, &x) ||
+      !mixer::extent(c.dt, c.rows, c.heads, c.dt_row_stride, es, &dt) ||
+      !mixer::extent(c.b, c.rows, gn, c.b_row_stride, es, &b) ||
+      !mixer::extent(c.c, c.rows, gn, c.c_row_stride, es, &cc) ||
+      !mixer::extent(c.out, c.rows, width, c.out_row_stride, es, &out) ||
+      !mixer::extent(c.state, c.state ? c.state_slots : 0, held, c.state_slot_stride, 4, &state))
+    return GGRN_ERR_SHAPE;
+  if (c.rows == 0 && (!c.state || p->q.seqs == 0)) return GGRN_OK;
+  if (!c.a || (c.rows > 0 && (!c.x || !c.dt || !c.b || !c.c || !c.out))) return GGRN_ERR_NULL;
+  for (const void* q : {c.x, c.dt, c.b, c.c, static_cast<const void*>(c.out)})
+    if (!mixer::aligned_to(q, es)) return GGRN_ERR_ALIGN;
+  for (const float* q : {c.a, c.d, c.dt_bias, static_cast<const float*>(c.state)})
+    if (!mixer::aligned_to(q, 4)) return GGRN_ERR_ALIGN;
+  const int64_t n = p->q.seqs;
+  const mixer::Buffer ins[] = {x,
+                               dt,
+                               b,
+                               cc,
+                               {c.a, c.heads * 4},
+                               {c.d, c.heads * 4},
+                               {c.dt_bias, c.heads * 4},
+                               {p->q.cu, (n + 1) * 4},
+                               {p->q.slots, n * 4},
+                               {p->q.resume, n}};
+  const mixer::Buffer ws = {step ? nullptr : c.workspace, c.workspace_bytes};
+  for (const mixer::Buffer& o : {out, state, ws})
+    for (const mixer::Buffer& i : ins)
+      if (mixer::overlap(o, i)) return GGRN_ERR_OVERLAP;
+  if (mixer::overlap(out, state) || mixer::overlap(out, ws) || mixer::overlap(state, ws))
+    return GGRN_ERR_OVERLAP;
+  p->x = c.x, p->dt = c.dt, p->b = c.b, p->c = c.c;
+  p->a = c.a, p->d = c.d, p->dt_bias = c.dt_bias;
+  p->out = c.out;
+  p->state = c.state;
+  const bool many = c.rows > 1;
+  p->xs = many ? c.x_row_stride : 0, p->dts = many ? c.dt_row_stride : 0;
+  p->bs = many ? c.b_row_stride : 0, p->cs = many ? c.c_row_stride : 0;
+  p->os = many ? c.out_row_stride : 0;
+  p->slot_stride = c.state_slots > 1 ? c.state_slot_stride : 0;
+  p->H = static_cast<int>(c.heads), p->P = static_cast<int>(c.head_dim);
+  p->N = static_cast<int>(c.state_size);
+  p->hpg = static_cast<int>(c.heads / c.groups);
+  p->dt_min = c.dt_min, p->dt_max = c.dt_max;
+  p->softplus = c.dt_softplus;
+  return GGRN_OK;
+}
+
+template <typename T>
+int run_typed(const ggrn_scan_call& c, Params& p, const Layout& l, cudaStream_t s) {
+  const Shape sh = shape_of(p.P, p.N);
+  if (l.parts > INT32_MAX || sh.ptiles > 65535 || (l.cut && p.q.seqs > 65535))
+    return GGRN_ERR_UNSUPPORTED;
+  const dim3 grid(static_cast<unsigned>(l.parts), static_cast<unsigned>(p.H),
+                  static_cast<unsigned>(sh.ptiles));
+  if (l.cut) {
+    int st = mixer::launch(k_scan<T, kRowsPerThread, true>, grid, sh.threads, sh.smem, s, p, sh.tl,
+                           sh.prows);
+    if (st != GGRN_OK) return st;
+    st = launch_join(p, s);
+    if (st != GGRN_OK) return st;
+  }
+  return mixer::launch(k_scan<T, kRowsPerThread, false>, grid, sh.threads, sh.smem, s, p, sh.tl,
+                       sh.prows);
+}
+
+template <typename T>
+int step_typed(const Params& p, cudaStream_t s) {
+  const bool vec = p.N % 4 == 0 && mixer::aligned_to(p.state, 16) && p.slot_stride % 4 == 0;
+  const int lanes = (p.N + (vec ? 3 : 0)) / (vec ? 4 : 1);
+  const int tl = std::min(32, pow2_at_least(lanes));
+  const int ch = (lanes + tl - 1) / tl;  // 1, 2 (vectors) or 1..8 (single columns)
+  // one round of rows per CTA while the launch is small, else two
+  const int round = kStepRows * (kStepThreads / tl);
+  const int64_t rounds = p.q.rows * p.H * ((p.P + round - 1) / round);
+  const int tile = rounds > 16 * device_sms() ? 2 * round : round;
+  const int64_t tiles = (p.P + tile - 1) / tile;
+  if (p.q.rows > INT32_MAX || tiles > 65535) return GGRN_ERR_UNSUPPORTED;
+  const dim3 grid(static_cast<unsigned>(p.q.rows), static_cast<unsigned>(p.H),
+                  static_cast<unsigned>(tiles));
+  if (vec)
+    return ch == 1 ? mixer::launch(k_scan_step<T, 1, true>, grid, kStepThreads, 0, s, p, tl, tile)
+                   : mixer::launch(k_scan_step<T, 2, true>, grid, kStepThreads, 0, s, p, tl, tile);
+  if (ch <= 2) return mixer::launch(k_scan_step<T, 2, false>, grid, kStepThreads, 0, s, p, tl, tile);
+  return mixer::launch(k_scan_step<T, 8, false>, grid, kStepThreads, 0, s, p, tl, tile);
+}
+
+int run(const ggrn_scan_call* call, bool step, void* stream) {
+  if (!call) return GGRN_ERR_ARG;
+  const ggrn_scan_call& c = *call;
+  Params p = {};
+  const int st = check(c, step, &p);
+  if (st != GGRN_OK || (c.rows == 0 && (!c.state || p.q.seqs == 0))) return st;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (step) {
+    if (c.dtype == kF32) return step_typed<float>(p, s);
+    if (c.dtype == kF16) return step_typed<__half>(p, s);
+    return step_typed<__nv_bfloat16>(p, s);
+  }
+  const Layout l = layout_of(c);
+  if (l.bytes > 0) {
+    if (!c.workspace) return GGRN_ERR_NULL;
+    if (!mixer::aligned_to(c.workspace, 16)) return GGRN_ERR_ALIGN;
+    if (c.workspace_bytes < l.bytes) return GGRN_ERR_ARG;
+    p.ws = static_cast<float*>(c.workspace);
+    p.ws_decay = p.ws + l.state_bytes / 4;
+  }
+  p.part = l.part;
+  p.parts = l.parts;
+  p.places = l.places;
+  if (c.dtype == kF32) return run_typed<float>(c, p, l, s);
+  if (c.dtype == kF16) return run_typed<__half>(c, p, l, s);
+  return run_typed<__nv_bfloat16>(c, p, l, s);
+}
+
+int launch_join(const Params& p, cudaStream_t s) {
+  const int64_t pn = static_cast<int64_t>(p.P) * p.N;
+  const dim3 grid(static_cast<unsigned>((pn + 255) / 256), static_cast<unsigned>(p.H),
+                  static_cast<unsigned>(p.q.seqs));
+  return mixer::launch(k_scan_join, grid, 256, 0, s, p);
+}
+
+}  // namespace scan
+
+int check_scan(const ggrn_scan_call& c, bool step) {
+  scan::Params p = {};
+  return scan::check(c, step, &p);
+}
+
+}  // namespace ggrn
+
+extern "C" int ggrn_scan(const ggrn_scan_call* call, void* cuda_stream) {
+  return ggrn::scan::run(call, false, cuda_stream);
+}
+extern "C" int ggrn_scan_step(const ggrn_scan_call* call, void* cuda_stream) {
+  return ggrn::scan::run(call, true, cuda_stream);
+}
+extern "C" int64_t ggrn_scan_workspace_bytes(const ggrn_scan_call* call) {
+  if (!call || ggrn::scan::check_sizes(*call) != GGRN_OK || call->seqs < 0) return 0;
+  return ggrn::scan::layout_of(*call).bytes;
+}

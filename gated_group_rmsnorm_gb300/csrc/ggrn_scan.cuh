@@ -1,0 +1,42 @@
+// ggrn_scan.cuh -- parameters and helpers shared by the scan's kernels.
+#pragma once
+
+#include "ggrn_mixer.cuh"
+
+namespace ggrn {
+namespace scan {
+
+struct Params {
+  const void* x;
+  const void* dt;
+  const void* b;
+  const void* c;
+  const float* a;
+  const float* d;
+  const float* dt_bias;
+  void* out;
+  float* state;
+  float* ws;        // by place: states at the starts of parts, [places][H][P][N]
+  float* ws_decay;  // decays over parts, [places][H]
+  Seqs q;
+  int64_t xs, dts, bs, cs, os, slot_stride;
+  int64_t part, parts, places;
+  int H, P, N, hpg;  // hpg: heads per group
+  float dt_min, dt_max;
+  int softplus;
+};
+
+// dt of one token and head: softplus as log1p(exp(v)), v itself from 20 on
+// (the difference is below 2^-28 of it); a NaN stays one.
+__device__ __forceinline__ float dt_of(float raw, float bias, const Params& p) {
+  float v = raw + bias;
+  if (p.softplus) v = v > 20.0f ? v : log1pf(expf(v));
+  v = v < p.dt_min ? p.dt_min : v;
+  return v > p.dt_max ? p.dt_max : v;
+}
+
+// Enqueue k_scan_join (the states at the parts' starts).
+int launch_join(const Params& p, cudaStream_t s);
+
+}  // namespace scan
+}  // namespace ggrn

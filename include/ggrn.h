@@ -399,6 +399,144 @@ int ggrn_forward_noalloc(const void* y, const void* gate, const void* w, void* o
                          int64_t gate_row_stride, int64_t out_row_stride, float eps, int dtype,
                          int mode, void* cuda_stream);
 
+/* --------------------------------------------------------------------------
+ * The Mamba-2 mixer around the norm: the short causal convolution and the
+ * selective state space scan whose output is the norm's y.  One in-proj row
+ * per token is packed as [z | x B C | dt]; z is the norm's gate, the
+ * convolution runs over the x B C columns, the scan over its output and the
+ * dt columns:
+ *   conv: u = x B C columns of the in-proj
+ *     v[t,c]  = bias[c] + sum_{k < taps} w[c,k] * u[t - (taps-1) + k, c]
+ *     out     = cast_T(silu(v))   (or v itself, GGRN_ACT_NONE)
+ *   scan, per head h of head_dim columns, group g = h / (heads / groups):
+ *     dt[t]   = clamp(softplus(dt_raw[t,h] + dt_bias[h]), dt_min, dt_max)
+ *     S[t]    = exp(dt[t] * a[h]) * S[t-1] + dt[t] * x[t,h,:] (x) B[t,g,:]
+ *     out     = cast_T(S[t] C[t,g,:] + d[h] * x[t,h,:])
+ * All arithmetic in f32 or better; T in {f32, f16, bf16}.
+ *
+ * Sequences.  The rows of a call are `seqs` sequences one behind the other:
+ * with cu_seqlens (DEVICE int32 [seqs + 1], ascending, cu_seqlens[0] >= 0)
+ * sequence i is rows [cu_seqlens[i], cu_seqlens[i+1]); without it (NULL)
+ * every sequence has rows / seqs rows.  Rows of no sequence (behind the last
+ * one, say) have no part in any result and their output rows are left as
+ * they were.  Offsets outside [0, rows] are
+ * clamped into it; a sequence may be empty.
+ *
+ * States.  What a sequence leaves for its next token lives in a pool of
+ * `state_slots` entries of the caller's, state_slot_stride elements apart:
+ *   conv: T   [taps - 1, width]              the last taps - 1 inputs, oldest first
+ *   scan: f32 [heads, head_dim, state_size]  S
+ * slots (DEVICE int32 [seqs], NULL = entry i is sequence i's) names each
+ * sequence's entry; entries of one call are distinct (two sequences with one
+ * entry leave either's values in it); a sequence whose slot is outside
+ * [0, state_slots) has no entry.  resume (DEVICE uint8 [seqs], NULL = all
+ * zero): nonzero starts the sequence from its entry, zero from zeros.
+ * Either way the entry receives the state after the sequence's last row (of
+ * an empty sequence: the one it started from).  state == NULL: no pool,
+ * every sequence starts from zeros and nothing is kept (slots and resume
+ * must be NULL too).
+ *
+ * The _step forms take one row for each of `rows` sequences and always
+ * resume (cu_seqlens, resume and seqs are ignored, state is required); a row
+ * whose slot is outside the pool (padding of a decode batch) is skipped: its
+ * output row is left as it was.
+ *
+ * Memory, streams and errors are those of ggrn_forward: caller-owned device
+ * pointers, row strides in elements (ignored for a single row), nothing
+ * allocated, everything enqueued on `cuda_stream` and capturable in a graph,
+ * argument errors returned before anything is enqueued.  out and state may
+ * overlap no other buffer.  Results are deterministic.
+ * -------------------------------------------------------------------------- */
+typedef enum { GGRN_ACT_NONE = 0, GGRN_ACT_SILU = 1 } ggrn_activation;
+
+typedef struct {
+  const void* x;              /* T [rows, width], row stride x_row_stride */
+  const float* w;             /* [width, taps] contiguous */
+  const float* bias;          /* [width], or NULL */
+  void* out;                  /* T [rows, width], row stride out_row_stride */
+  void* state;                /* T, or NULL (not in the step form) */
+  const int32_t* slots;       /* [seqs] (step: [rows]), or NULL */
+  const uint8_t* resume;      /* [seqs], or NULL */
+  const int32_t* cu_seqlens;  /* [seqs + 1], or NULL */
+  int64_t rows, seqs, width;
+  int64_t x_row_stride, out_row_stride;
+  int64_t state_slots, state_slot_stride;
+  int32_t taps;               /* 2, 3 or 4 */
+  int32_t activation;         /* ggrn_activation */
+  int32_t dtype;              /* ggrn_dtype of x, out and state */
+} ggrn_conv_call;
+
+typedef struct {
+  const void* x;              /* T [rows, heads * head_dim] */
+  const void* dt;             /* T [rows, heads] */
+  const void* b;              /* T [rows, groups * state_size] */
+  const void* c;              /* T [rows, groups * state_size] */
+  const float* a;             /* [heads], finite (negative for a decay) */
+  const float* d;             /* [heads], or NULL (0) */
+  const float* dt_bias;       /* [heads], or NULL (0) */
+  void* out;                  /* T [rows, heads * head_dim] */
+  float* state;               /* f32, or NULL (not in the step form) */
+  const int32_t* slots;
+  const uint8_t* resume;
+  const int32_t* cu_seqlens;
+  void* workspace;            /* ggrn_scan only: DEVICE, 16-byte aligned */
+  int64_t workspace_bytes;
+  int64_t rows, seqs, heads, head_dim, groups, state_size;
+  int64_t x_row_stride, dt_row_stride, b_row_stride, c_row_stride, out_row_stride;
+  int64_t state_slots, state_slot_stride;
+  float dt_min, dt_max;       /* 0 <= dt_min <= dt_max (0 and +inf: no limits) */
+  int32_t dt_softplus;        /* 0: dt = clamp(dt_raw + dt_bias, dt_min, dt_max) */
+  int32_t dtype;              /* ggrn_dtype of x, dt, b, c and out */
+} ggrn_scan_call;
+
+/*
+ * ggrn_conv / ggrn_conv_step -- the causal convolution over prompts / over
+ * one row of each sequence.  Return GGRN_ERR_SHAPE for negative or
+ * inconsistent sizes (rows not a multiple of seqs without cu_seqlens, a
+ * stride below its row's width, too few slots, overflow),
+ * GGRN_ERR_UNSUPPORTED for taps outside 2..4, GGRN_ERR_DTYPE for an unknown
+ * dtype, GGRN_ERR_ARG for an unknown activation, a NULL call, or slots or
+ * resume without state, GGRN_ERR_NULL, GGRN_ERR_ALIGN (a pointer not aligned
+ * to its element), GGRN_ERR_OVERLAP, GGRN_ERR_CUDA.
+ */
+int ggrn_conv(const ggrn_conv_call* call, void* cuda_stream);
+int ggrn_conv_step(const ggrn_conv_call* call, void* cuda_stream);
+
+/*
+ * ggrn_scan / ggrn_scan_step -- the selective state space scan over prompts /
+ * over one row of each sequence.  state_size is 1..256 and head_dim any
+ * positive number.  Statuses as above; GGRN_ERR_SHAPE also when heads is not
+ * a multiple of groups, GGRN_ERR_UNSUPPORTED for state_size > 256,
+ * GGRN_ERR_ARG for limits out of order or not numbers and for a workspace
+ * too small.
+ */
+int ggrn_scan(const ggrn_scan_call* call, void* cuda_stream);
+int ggrn_scan_step(const ggrn_scan_call* call, void* cuda_stream);
+
+/* Workspace bytes of ggrn_scan for this call (only its sizes and dtype, the
+ * alignment of its pointers and whether cu_seqlens is NULL are looked at):
+ * 0 where none is needed or the call is invalid. */
+int64_t ggrn_scan_workspace_bytes(const ggrn_scan_call* call);
+
+/* One call of a decode chain that is not only norms. */
+typedef enum { GGRN_STEP_FORWARD = 0, GGRN_STEP_CONV = 1, GGRN_STEP_SCAN = 2 } ggrn_step_kind;
+typedef struct {
+  int32_t kind;              /* ggrn_step_kind: which member of `u` */
+  union {
+    ggrn_call forward;       /* ggrn_forward */
+    ggrn_conv_call conv;     /* ggrn_conv_step */
+    ggrn_scan_call scan;     /* ggrn_scan_step */
+  } u;
+} ggrn_step;
+
+/*
+ * ggrn_graph_create_steps -- ggrn_graph_create for a chain that mixes the
+ * norm with the step forms above (a decode step of the mixer: convolution,
+ * scan, norm).  Launched and destroyed like any decode graph; each replay
+ * advances the states.  GGRN_ERR_ARG for an unknown kind.
+ */
+int ggrn_graph_create_steps(const ggrn_step* steps, int32_t n, void** graph);
+
 #ifdef __cplusplus
 }
 #endif
