@@ -366,6 +366,7 @@ int64_t longest(const ggrn_scan_call& c) {
 }
 
 struct Layout {
+  bool tc;                  // on the tensor cores
   int64_t part, parts;      // rows of a part; the most parts there can be
   int64_t places;           // the most of them that are of cut sequences
   bool cut;                 // whether a sequence may have more than one
@@ -374,7 +375,8 @@ struct Layout {
 Layout layout_of(const ggrn_scan_call& c) {
   Layout l;
   const Shape s = shape_of(static_cast<int>(c.head_dim), static_cast<int>(c.state_size));
-  l.part = part_rows(c.rows, c.heads * s.ptiles);
+  l.tc = tc_covers(c);
+  l.part = l.tc ? tc_part_rows(c, longest(c)) : part_rows(c.rows, c.heads * s.ptiles);
   l.cut = longest(c) > l.part;
   if (!l.cut) l.part = std::max<int64_t>(1, longest(c));
   l.parts = c.rows / l.part + c.seqs;
@@ -519,6 +521,10 @@ int run(const ggrn_scan_call* call, bool step, void* stream) {
   p.part = l.part;
   p.parts = l.parts;
   p.places = l.places;
+  if (l.tc) {
+    if (l.parts > INT32_MAX || (l.cut && p.q.seqs > 65535)) return GGRN_ERR_UNSUPPORTED;
+    return tc_run(c, p, l.cut, s);
+  }
   if (c.dtype == kF32) return run_typed<float>(c, p, l, s);
   if (c.dtype == kF16) return run_typed<__half>(c, p, l, s);
   return run_typed<__nv_bfloat16>(c, p, l, s);

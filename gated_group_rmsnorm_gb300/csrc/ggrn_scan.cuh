@@ -38,5 +38,11 @@ __device__ __forceinline__ float dt_of(float raw, float bias, const Params& p) {
 // Enqueue k_scan_join (the states at the parts' starts).
 int launch_join(const Params& p, cudaStream_t s);
 
+// The tensor-core kernels (ggrn_scan_tc.cu): whether they cover a call, the
+// rows of their parts, and their launches.
+bool tc_covers(const ggrn_scan_call& c);
+int64_t tc_part_rows(const ggrn_scan_call& c, int64_t longest);
+int tc_run(const ggrn_scan_call& c, const Params& p, bool cut, cudaStream_t s);
+
 }  // namespace scan
 }  // namespace ggrn
