@@ -22,19 +22,24 @@
 // smaller one underflows in any case, and the prefix sums stay exact enough
 // beside it.
 //
-// One CTA per part of a sequence and head (or tile of a head's columns):
-// 16 warps share the elementwise work (X and its pieces into shared memory, G
-// to M, S and Y out of tensor memory; a warp reads the 32 tensor-memory lanes
-// that its number allows), one thread issues the products, one warp makes the
-// decays a chunk ahead.  B and C come by asynchronous copies into the
-// 128-byte swizzled layout, which serves B both as rows of the state columns
-// (G) and as its transpose (dS); X, its pieces and S lie in the 32-byte
-// swizzled layout, whose 16-column atoms fit any head size.
+// One CTA per part of a sequence and head (or tile of a head's columns), its
+// warps specialised so that all stages of neighbouring chunks overlap:
+//   X    4 warps  X from global memory, w X in pieces, both into shared memory
+//   M    4 warps  G out of tensor memory, decays applied, M back into it
+//   SY   8 warps  S in registers (dS out of tensor memory, S into shared
+//                 memory as the next chunk's operand), Y out of tensor memory
+//   and one warp each that issues the products, copies B and C (tensor-map
+//   copies, 128-byte swizzle: one layout serves B as rows of state columns in G
+//   and as its transpose in dS), and makes the decays.
+// X, its pieces and S lie in the 32-byte swizzled layout, whose 16-column
+// atoms fit any head size.  Products are issued in the order C S, dS, M X, G of
+// the next chunk, which leaves every other stage the time of two products.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cstdint>
+#include <cstring>
 #include <mutex>
 
 #include "ggrn_scan.cuh"
@@ -55,13 +60,15 @@ constexpr float kMinLog = -256.0f;
 constexpr uint32_t kRowsBytes = kQ * 128 * 2;      // B or C: 32 KB
 constexpr uint32_t kAtomBytes = kQ * 16 * 2;       // one 16-column atom of X: 4 KB
 constexpr uint32_t kDecayFloats = 5 * kQ + 8;      // pre, col, dt, w, row + block sums, decay
-// tensor memory columns (full kernel; the state-only one has dS at 0)
+constexpr int kDecays = 3;                         // chunks of decays kept
+// tensor memory columns (k_scan_tc; k_scan_tc_state has dS at 0)
 constexpr uint32_t kColG = 0, kColM = 128, kColDs = 192;
 
 struct TcParams {
   Params p;
   unsigned int* fault;
   int tile;        // columns of a head per CTA, a multiple of 16 up to 96
+  int cbufs;       // buffers of C: 1 or 2
   int xvec, ovec;  // 16-byte rows of x / out (else 8-byte)
 };
 
@@ -143,13 +150,129 @@ __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_al
 
 using Bf = Elem<__nv_bfloat16>;
 
-// WQ: warps on each quarter of the tensor-memory lanes.
-template <int WQ, bool STATE_ONLY>
-__global__ void __launch_bounds__((4 * WQ + 2) * 32, STATE_ONLY ? 2 : 1)
-    k_scan_tc(const TcParams tp) {
-  constexpr int NT = WQ * 128;                          // threads of the elementwise warps
-  constexpr int AW = (kMaxAtoms + WQ - 1) / WQ;         // atoms of a warp
-  constexpr int XI = (kMaxAtoms * 256 + NT - 1) / NT;   // 16-byte chunks of X of a thread
+// The decays of one chunk into shared memory: `raw` holds the raw dt of tokens
+// 32 b + lane, `left` the rows from the chunk's first on.  Returns the sum of
+// the chunk's l.
+__device__ __forceinline__ float make_decays(const float (&raw)[4], int64_t left, float bias,
+                                             float a2, const Params& p, float (&pre)[4],
+                                             float (&suf)[4], float (&dt)[4], float (&tot)[4]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const bool valid = 32 * b + lane < left;
+    dt[b] = valid ? dt_of(raw[b], bias, p) : 0.0f;
+    float l = valid ? dt[b] * a2 : 0.0f;
+    l = l < kMinLog ? kMinLog : l;
+    pre[b] = l;
+    suf[b] = __shfl_down_sync(0xffffffffu, l, 1);
+    if (lane == 31) suf[b] = 0.0f;
+  }
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const float u = __shfl_up_sync(0xffffffffu, pre[b], o);
+      const float d = __shfl_down_sync(0xffffffffu, suf[b], o);
+      if (lane >= o) pre[b] += u;
+      if (lane + o < 32) suf[b] += d;
+    }
+#pragma unroll
+  for (int b = 0; b < 4; ++b) tot[b] = __shfl_sync(0xffffffffu, pre[b], 31);
+  return tot[0] + tot[1] + tot[2] + tot[3];
+}
+
+// The three bf16 pieces of eight products w x, each piece what the ones before
+// leave, cut off (not rounded: 8 bits each of 24).
+__device__ __forceinline__ void pieces_of(const uint4& x, float w, uint4 (&u)[3]) {
+  float v[8];
+  uint32_t out[3][4];
+  Bf::unpack(x, v);
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    float a, b;
+    mul2(a, b, v[e], v[e + 1], w, w);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const uint32_t ha = __float_as_uint(a), hb = __float_as_uint(b);
+      out[k][e / 2] = __byte_perm(ha, hb, 0x7632);
+      if (k < 2)
+        fma2(a, b, __uint_as_float(ha & 0xffff0000u), __uint_as_float(hb & 0xffff0000u), -1.0f,
+             -1.0f, a, b);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 3; ++k) u[k] = make_uint4(out[k][0], out[k][1], out[k][2], out[k][3]);
+}
+
+// X of one chunk: 16-byte pieces `id` of a thread, columns in pairs of an
+// atom, so that a warp reads whole 32-byte sectors and writes without
+// conflicts.
+__device__ __forceinline__ uint4 load_x(const __nv_bfloat16* src, int col, int pw, bool vec) {
+  if (vec) return ld_stream(src);
+  uint4 v = make_uint4(0, 0, 0, 0);
+  const uint2 lo = __ldg(reinterpret_cast<const uint2*>(src));
+  v.x = lo.x, v.y = lo.y;
+  if (col + 4 < pw) {
+    const uint2 hi = __ldg(reinterpret_cast<const uint2*>(src + 4));
+    v.z = hi.x, v.w = hi.y;
+  }
+  return v;
+}
+
+// Bounded waits of a CTA: on a timeout the CTA's flag and the library's status
+// word are set and every role leaves its loop.
+struct Waits {
+  volatile uint32_t* flag;
+  unsigned int* fault;
+  __device__ __forceinline__ bool one(uint32_t bar, uint32_t parity) const {
+    parity &= 1u;
+    if (mbar_try_wait(bar, parity)) return true;
+    for (uint32_t i = 0; i < kWaitLimit; ++i) {
+      if (mbar_try_wait(bar, parity)) return true;
+      if (*flag) return false;
+    }
+    *flag = 1;
+    atomicOr(fault, kFaultScanWait);
+    return false;
+  }
+  // for a whole warp, which stays together
+  __device__ __forceinline__ bool warp(uint32_t bar, uint32_t parity) const {
+    return __all_sync(0xffffffffu, one(bar, parity)) != 0;
+  }
+};
+
+// ---------------------------------------------------------------------------
+// k_scan_tc
+// ---------------------------------------------------------------------------
+constexpr int kWarpM = 4, kWarpSY = 8, kWarpMma = 16, kWarpCopy = 17, kWarpDt = 18;
+constexpr int kMainThreads = 19 * 32;
+constexpr int kXThreads = 128, kMThreads = 128, kSYThreads = 256;
+constexpr int kSYAtoms = kMaxAtoms / 2;                   // atoms of a warp of SY
+constexpr int kXPieces = kMaxAtoms * 256 / kXThreads;     // 16-byte pieces of X of a thread
+// barriers, 8 bytes each
+enum Bar {
+  kBFull = 0,    // [2] B landed
+  kBFree = 2,    // [2] B read by G and dS
+  kCFull = 4,    // [2] C landed
+  kCFree = 6,    // [2] C read by G and C S
+  kDtFull = 8,   // [3] decays made
+  kDtFree = 11,  // [3] and read
+  kTail = 14,    // B of a part's last, partial chunk landed
+  kWFull = 15,   // w X written
+  kXFull = 16,   // X written
+  kGDone = 17,   // G computed
+  kMFull = 18,   // M written, G read
+  kDsDone = 19,  // dS computed, w X read
+  kY1Done = 20,  // C S computed, S read
+  kSFull = 21,   // S written, dS read
+  kYDone = 22,   // Y computed, M read
+  kYRead = 23,   // Y and X read
+  kBars = 24
+};
+
+__global__ void __launch_bounds__(kMainThreads, 1)
+    k_scan_tc(const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ CUtensorMap tm_c,
+              const TcParams tp) {
   const Params& p = tp.p;
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw_u = smem_u32(smem_raw);
@@ -157,91 +280,102 @@ __global__ void __launch_bounds__((4 * WQ + 2) * 32, STATE_ONLY ? 2 : 1)
   unsigned char* base = smem_raw + (base_u - raw_u);
   const int atoms = tp.tile / 16;
   const uint32_t x_bytes = atoms * kAtomBytes;
-  const uint32_t sB = base_u, sC = sB + kRowsBytes;
-  const uint32_t sW = sC + (STATE_ONLY ? 0 : kRowsBytes);  // three pieces of w X
+  const uint32_t sB = base_u, sC = sB + 2 * kRowsBytes;
+  const uint32_t sW = sC + tp.cbufs * kRowsBytes;        // three pieces of w X
   const uint32_t sX = sW + 3 * x_bytes, sS = sX + x_bytes;
-  const uint32_t decay_off = (STATE_ONLY ? sX : sS + x_bytes) - base_u;
-  float* s_decay = reinterpret_cast<float*>(base + decay_off);  // [2][kDecayFloats]
-  const uint32_t bars = base_u + decay_off + 2 * kDecayFloats * 4;
-  // a phase of each per chunk: B and C landed; X written (and everything of
-  // the chunk before read); S written; M written; decays made; the products
-  // done: G, dS with C S^T, all; and Y stored
-  const uint32_t b_bc = bars, b_x = bars + 8, b_s = bars + 16, b_m = bars + 24, b_dt = bars + 32,
-                 b_g = bars + 40, b_ds = bars + 48, b_y = bars + 56, b_e = bars + 64;
-  volatile uint32_t* s_misc = reinterpret_cast<uint32_t*>(base + decay_off + 2 * kDecayFloats * 4 + 72);
+  const uint32_t decay_off = sS + x_bytes - base_u;
+  float* s_decay = reinterpret_cast<float*>(base + decay_off);
+  const uint32_t bars_off = decay_off + kDecays * kDecayFloats * 4;
+  volatile uint32_t* s_misc = reinterpret_cast<uint32_t*>(base + bars_off + 8 * kBars);
+  auto bar = [&](int i) { return base_u + bars_off + 8u * i; };
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
-    mbar_init(b_bc, NT);
-    mbar_init(b_x, NT);
-    mbar_init(b_s, NT);
-    mbar_init(b_m, NT);
-    mbar_init(b_dt, 32);
-    mbar_init(b_g, 1);
-    mbar_init(b_ds, 1);
-    mbar_init(b_y, 1);
-    mbar_init(b_e, NT);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(kBFull + i), 1);
+      mbar_init(bar(kBFree + i), 1);
+      mbar_init(bar(kCFull + i), 1);
+      mbar_init(bar(kCFree + i), 1);
+    }
+    for (int i = 0; i < kDecays; ++i) {
+      mbar_init(bar(kDtFull + i), 32);
+      mbar_init(bar(kDtFree + i), kSYThreads);
+    }
+    mbar_init(bar(kTail), 1);
+    mbar_init(bar(kWFull), kXThreads);
+    mbar_init(bar(kXFull), kXThreads);
+    mbar_init(bar(kGDone), 1);
+    mbar_init(bar(kMFull), kMThreads);
+    mbar_init(bar(kDsDone), 1);
+    mbar_init(bar(kY1Done), 1);
+    mbar_init(bar(kSFull), kSYThreads);
+    mbar_init(bar(kYDone), 1);
+    mbar_init(bar(kYRead), kSYThreads);
     s_misc[1] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  constexpr uint32_t kTmemCols = STATE_ONLY ? 128 : 512;
-  if (warp == 4 * WQ) tmem_alloc(smem_u32(const_cast<uint32_t*>(s_misc)), kTmemCols);
+  if (warp == kWarpMma) tmem_alloc(smem_u32(const_cast<uint32_t*>(s_misc)), 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_misc[0];
-  const uint32_t t_ds = tmem + (STATE_ONLY ? 0 : kColDs);
-  const uint32_t t_y1 = t_ds + tp.tile, t_y2 = t_y1 + tp.tile;
+  const uint32_t t_ds = tmem + kColDs, t_y1 = t_ds + tp.tile, t_y2 = t_y1 + tp.tile;
   pdl_wait();
   pdl_launch_dependents();
 
   const Part part = find_part(p.q, p.part, blockIdx.x);
   const int P = p.P, N = p.N;
-  const int h = blockIdx.y;
+  const int h = blockIdx.y, g = h / p.hpg;
   const int col0 = blockIdx.z * tp.tile;         // first column of the head here
-  bool run = part.seq >= 0 && !(STATE_ONLY && part.index == part.count - 1) &&
-             !(part.count > 1 && part.place + (STATE_ONLY ? 1 : 0) >= p.places);
+  const int pw = min(tp.tile, P - col0);         // and how many
+  const int64_t hcol = static_cast<int64_t>(h) * P + col0;
+  const bool run = part.seq >= 0 && !(part.count > 1 && part.place >= p.places);
   const int64_t rows = run ? part.end - part.begin : 0;
   const int chunks = static_cast<int>((rows + kQ - 1) / kQ);
-  auto fail = [&]() {
-    s_misc[1] = 1;
-    atomicOr(tp.fault, kFaultScanWait);
-  };
-  auto wait = [&](uint32_t bar, uint32_t parity) {
-    if (!s_misc[1] && mbar_wait(bar, parity & 1u)) return true;
-    if (!s_misc[1]) fail();
-    return false;
-  };
-
-  auto warp_wait = [&](uint32_t bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, wait(bar, parity)) != 0;
-  };
+  const Waits wait = {s_misc + 1, tp.fault};
+  // Each phase of a barrier is waited for in turn: a parity tells a phase from
+  // its neighbours only.
 
   if (!run) {
     // nothing: fall through to the end
-  } else if (warp == 4 * WQ) {
+  } else if (warp == kWarpMma) {
     // ---- the products ----
     if (lane == 0) {
       const uint32_t id_g = idesc_bf16(128, 128);
       const uint32_t id_ds = idesc_bf16(128, tp.tile) | kTransA | kTransB;
       const uint32_t id_y = idesc_bf16(128, tp.tile) | kTransB;
-      const uint64_t d_b = desc_sw128(sB), d_c = desc_sw128(sC);
-      const uint64_t d_bt = desc_t128(sB, kRowsBytes / 2);
       const uint64_t d_x = desc_t32(sX), d_s = desc_t32(sS);
       const int ksteps = (N + 15) / 16;
       // step k of 16 along the columns of a 128-byte swizzled tile
-      auto kk = [](int k) { return static_cast<uint64_t>((k >> 2) * (kRowsBytes / 2) + (k & 3) * 32) >> 4; };
-      int c = 0;
-      for (; c < chunks; ++c) {
-        if (!wait(b_bc, c)) break;
+      auto kk = [](int k) {
+        return static_cast<uint64_t>((k >> 2) * (kRowsBytes / 2) + (k & 3) * 32) >> 4;
+      };
+      auto cslot = [&](int c) { return tp.cbufs == 2 ? c & 1 : 0; };
+      auto cuse = [&](int c) { return tp.cbufs == 2 ? c >> 1 : c; };
+      auto issue_g = [&](int c) {
+        if (!wait.one(bar(kBFull + (c & 1)), c >> 1) || !wait.one(bar(kCFull + cslot(c)), cuse(c)))
+          return false;
         tc_fence_after();
-        if (!STATE_ONLY) {
-          for (int k = 0; k < ksteps; ++k)
-            mma_bf16(tmem + kColG, d_c + kk(k), d_b + kk(k), id_g, k > 0);
-          mma_commit(b_g);
-        }
-        if (!wait(b_x, c)) break;
+        const uint64_t d_b = desc_sw128(sB + (c & 1) * kRowsBytes);
+        const uint64_t d_c = desc_sw128(sC + cslot(c) * kRowsBytes);
+        for (int k = 0; k < ksteps; ++k) mma_bf16(tmem + kColG, d_c + kk(k), d_b + kk(k), id_g, k > 0);
+        mma_commit(bar(kGDone));
+        return true;
+      };
+      bool ok = chunks == 0 || issue_g(0);
+      for (int c = 0; ok && c < chunks; ++c) {
+        // C S (S of the chunk before, Y and dS read)
+        if (!(ok = wait.one(bar(kSFull), c) && (c == 0 || wait.one(bar(kYRead), c - 1)))) break;
         tc_fence_after();
+        const uint64_t d_c = desc_sw128(sC + cslot(c) * kRowsBytes);
+        for (int k = 0; k < ksteps; ++k)
+          mma_bf16(t_y1, d_c + kk(k), d_s + k * (512 >> 4), id_y, k > 0);
+        mma_commit(bar(kY1Done));
+        mma_commit(bar(kCFree + cslot(c)));
+        // dS
+        if (!(ok = wait.one(bar(kWFull), c))) break;
+        tc_fence_after();
+        const uint64_t d_bt = desc_t128(sB + (c & 1) * kRowsBytes, kRowsBytes / 2);
 #pragma unroll
         for (int piece = 2; piece >= 0; --piece) {
           const uint64_t d_w = desc_t32(sW + piece * x_bytes);
@@ -250,31 +384,72 @@ __global__ void __launch_bounds__((4 * WQ + 2) * 32, STATE_ONLY ? 2 : 1)
             mma_bf16(t_ds, d_bt + k * (2048 >> 4), d_w + k * (512 >> 4), id_ds,
                      piece < 2 || k > 0);
         }
-        if (!STATE_ONLY) {
-          if (!wait(b_s, c)) break;
-          tc_fence_after();
-          for (int k = 0; k < ksteps; ++k)
-            mma_bf16(t_y1, d_c + kk(k), d_s + k * (512 >> 4), id_y, k > 0);
-        }
-        mma_commit(b_ds);
-        if (!STATE_ONLY) {
-          if (!wait(b_m, c)) break;
-          tc_fence_after();
+        mma_commit(bar(kDsDone));
+        mma_commit(bar(kBFree + (c & 1)));
+        // M X
+        if (!(ok = wait.one(bar(kMFull), c) && wait.one(bar(kXFull), c))) break;
+        tc_fence_after();
 #pragma unroll
-          for (int k = 0; k < kQ / 16; ++k)
-            mma_bf16_ts(t_y2, tmem + kColM + 8 * k, d_x + k * (512 >> 4), id_y, k > 0);
-          mma_commit(b_y);
-        }
+        for (int k = 0; k < kQ / 16; ++k)
+          mma_bf16_ts(t_y2, tmem + kColM + 8 * k, d_x + k * (512 >> 4), id_y, k > 0);
+        mma_commit(bar(kYDone));
+        if (c + 1 < chunks) ok = issue_g(c + 1);
       }
-      // no product may still run when the tensor memory is freed
-      if (c < chunks) {
-        mma_commit(b_y);
-        for (uint32_t i = 0; i < kWaitLimit && !mbar_try_wait(b_y, c & 1u); ++i) {
-        }
+      // no product may still run when the tensor memory is freed: after a
+      // timeout, wait on a barrier nothing else completes any more
+      if (!ok) {
+        mbar_init(bar(kTail), 1);
+        mma_commit(bar(kTail));
+        mbar_wait(bar(kTail), 0);
       }
     }
-  } else if (warp == 4 * WQ + 1) {
-    // ---- the decays, a chunk ahead ----
+  } else if (warp == kWarpCopy) {
+    // ---- B and C ----
+    const int boxes = N > 64 ? 2 : 1;
+    const uint32_t bytes = boxes * (kRowsBytes / 2);
+    int c = 0;
+    for (; c < chunks; ++c) {
+      const int row = static_cast<int>(part.begin) + c * kQ;
+      const int left = static_cast<int>(rows - static_cast<int64_t>(c) * kQ);
+      const int bs = c & 1, cs = tp.cbufs == 2 ? c & 1 : 0, cu = tp.cbufs == 2 ? c >> 1 : c;
+      const bool tail = left < kQ;
+      const uint32_t b_at = sB + bs * kRowsBytes, c_at = sC + cs * kRowsBytes;
+      if (c >= 2 && !wait.warp(bar(kBFree + bs), (c >> 1) - 1)) break;
+      if (lane == 0) {
+        const uint32_t to = bar(tail ? static_cast<int>(kTail) : kBFull + bs);
+        mbar_expect_tx(to, bytes);
+        for (int i = 0; i < boxes; ++i)
+          tma_load_3d(b_at + i * (kRowsBytes / 2), &tm_b, 64 * i, g, row, to);
+      }
+      const bool c_free = cu == 0 || wait.warp(bar(kCFree + cs), cu - 1);
+      if (c_free && lane == 0) {
+        mbar_expect_tx(bar(kCFull + cs), bytes);
+        for (int i = 0; i < boxes; ++i)
+          tma_load_3d(c_at + i * (kRowsBytes / 2), &tm_c, 64 * i, g, row, bar(kCFull + cs));
+      }
+      if (tail) {
+        // rows of other sequences, or of none, count for nothing, whatever
+        // they hold
+        const bool landed = wait.warp(bar(kTail), 0);
+        if (!landed) break;
+        for (int i = lane; i < (kQ - left) * 8; i += 32)
+          for (int j = 0; j < boxes; ++j)
+            sts16(b_at + j * (kRowsBytes / 2) + left * 128 + i * 16, make_uint4(0, 0, 0, 0));
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBFull + bs));
+      }
+      if (!c_free) break;
+    }
+    // after a timeout, copies may still be on their way: give them the time of
+    // another wait (they target this CTA's shared memory)
+    if (c < chunks)
+      for (int i = 0; i < 2; ++i) {
+        mbar_wait(bar(kBFull + i), ((c + 1 - i) >> 1) & 1u ^ 1u);
+        mbar_wait(bar(kCFull + i), ((c + 1 - i) >> 1) & 1u ^ 1u);
+      }
+  } else if (warp == kWarpDt) {
+    // ---- the decays, chunks ahead ----
     const float a2 = __ldg(p.a + h) * kLog2e;
     const float bias = p.dt_bias ? __ldg(p.dt_bias + h) : 0.0f;
     const __nv_bfloat16* dtp = static_cast<const __nv_bfloat16*>(p.dt) + part.begin * p.dts + h;
@@ -286,35 +461,14 @@ __global__ void __launch_bounds__((4 * WQ + 2) * 32, STATE_ONLY ? 2 : 1)
         raw[b] = t < rows ? Bf::load1(dtp + t * p.dts, 0) : 0.0f;
       }
     };
-    fetch(0);
-    float log_total = 0.0f;
+    if (chunks > 0) fetch(0);
+    int slot = 0, use = 0;
     for (int c = 0; c < chunks; ++c) {
       float pre[4], suf[4], tot[4], dt[4];
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const bool valid = static_cast<int64_t>(c) * kQ + 32 * b + lane < rows;
-        dt[b] = valid ? dt_of(raw[b], bias, p) : 0.0f;
-        float l = valid ? dt[b] * a2 : 0.0f;
-        l = l < kMinLog ? kMinLog : l;
-        pre[b] = l;
-        suf[b] = __shfl_down_sync(0xffffffffu, l, 1);
-        if (lane == 31) suf[b] = 0.0f;
-      }
+      make_decays(raw, rows - static_cast<int64_t>(c) * kQ, bias, a2, p, pre, suf, dt, tot);
       if (c + 1 < chunks) fetch(c + 1);
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1)
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const float u = __shfl_up_sync(0xffffffffu, pre[b], o);
-          const float d = __shfl_down_sync(0xffffffffu, suf[b], o);
-          if (lane >= o) pre[b] += u;
-          if (lane + o < 32) suf[b] += d;
-        }
-#pragma unroll
-      for (int b = 0; b < 4; ++b) tot[b] = __shfl_sync(0xffffffffu, pre[b], 31);
-      // this half of the decays was last read for chunk c - 2
-      if (c >= 2 && !warp_wait(b_x, c - 1)) break;
-      float* s = s_decay + (c & 1) * kDecayFloats;
+      if (use > 0 && !wait.warp(bar(kDtFree + slot), use - 1)) break;
+      float* s = s_decay + slot * kDecayFloats;
       float before = 0.0f;
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
@@ -331,154 +485,95 @@ __global__ void __launch_bounds__((4 * WQ + 2) * 32, STATE_ONLY ? 2 : 1)
         if (lane == 0) s[5 * kQ + b] = tot[b];
       }
       if (lane == 0) s[5 * kQ + 4] = ex2_approx(before);
-      log_total += before;
-      mbar_arrive(b_dt);
+      mbar_arrive(bar(kDtFull + slot));
+      if (++slot == kDecays) slot = 0, ++use;
     }
-    if (STATE_ONLY && lane == 0 && blockIdx.z == 0)
-      p.ws_decay[part.place * p.H + h] = ex2_approx(log_total);
-  } else {
-    // ---- the elementwise warps ----
-    const int q = warp & 3, hf = warp >> 2;  // lanes 32 q.. of tensor memory; share of the columns
-    const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
-    const int g = h / p.hpg;
-    const int64_t hcol = static_cast<int64_t>(h) * P + col0;
-    const int pw = min(tp.tile, P - col0);   // columns here
+  } else if (warp < kWarpM) {
+    // ---- X and the pieces of w X ----
     const __nv_bfloat16* xg = static_cast<const __nv_bfloat16*>(p.x) + part.begin * p.xs + hcol;
-    const __nv_bfloat16* bg =
-        static_cast<const __nv_bfloat16*>(p.b) + part.begin * p.bs + static_cast<int64_t>(g) * N;
-    const __nv_bfloat16* cg =
-        static_cast<const __nv_bfloat16*>(p.c) + part.begin * p.cs + static_cast<int64_t>(g) * N;
-    __nv_bfloat16* og = static_cast<__nv_bfloat16*>(p.out) + part.begin * p.os + hcol;
-    const float dskip = p.d ? __ldg(p.d + h) : 0.0f;
-    const int64_t slot = seq_slot(p.q, part.seq);
-
-    auto load_bc = [&](int c) {
+    const int r0 = tid >> 1, col8 = (tid & 1) * 8;  // row 64 (i & 1) + r0 of atom i / 2
+    uint4 xr[kXPieces];
+    auto fetch = [&](int c) {
 #pragma unroll
-      for (int it = 0; it < 2048 / NT; ++it) {
-        const int id = it * NT + tid, r = id >> 4, ch = id & 15;
-        const int64_t t = static_cast<int64_t>(c) * kQ + r;
-        const bool valid = t < rows && ch * 8 < N;
-        const uint32_t at = (ch >> 3) * (kRowsBytes / 2) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
-        cp_async16(sB + at, valid ? bg + t * p.bs + ch * 8 : bg, valid);
-        if (!STATE_ONLY) cp_async16(sC + at, valid ? cg + t * p.cs + ch * 8 : cg, valid);
+      for (int i = 0; i < kXPieces; ++i) {
+        const int64_t t = static_cast<int64_t>(c) * kQ + (i & 1) * 64 + r0;
+        const int col = (i >> 1) * 16 + col8;
+        xr[i] = t < rows && col < pw ? load_x(xg + t * p.xs + col, col, pw, tp.xvec)
+                                     : make_uint4(0, 0, 0, 0);
       }
     };
-    uint4 xr[XI];
-    auto fetch_x = [&](int c) {
-#pragma unroll
-      for (int it = 0; it < XI; ++it) {
-        const int id = it * NT + tid;
-        const int r = (id & 255) >> 1, col = (id >> 8) * 16 + (id & 1) * 8;
-        const int64_t t = static_cast<int64_t>(c) * kQ + r;
-        xr[it] = make_uint4(0, 0, 0, 0);
-        if (t < rows && col < pw) {
-          const __nv_bfloat16* src = xg + t * p.xs + col;
-          if (tp.xvec) {
-            xr[it] = ld_stream(src);
-          } else {
-            const uint2 lo = __ldg(reinterpret_cast<const uint2*>(src));
-            xr[it].x = lo.x, xr[it].y = lo.y;
-            if (col + 4 < pw) {
-              const uint2 hi = __ldg(reinterpret_cast<const uint2*>(src + 4));
-              xr[it].z = hi.x, xr[it].w = hi.y;
-            }
-          }
-        }
-      }
-    };
-    if (chunks > 0) {
-      load_bc(0);
-      fetch_x(0);
-    }
-    // the state: lane n = 32 q + lane of S^T, columns 16 (hf + WQ k) + j
-    float s[AW][16];
-    const int n = 32 * q + lane;
-    const int64_t PN = static_cast<int64_t>(P) * N;
-    const float* from = nullptr;
-    if (!STATE_ONLY) {
-      if (part.count > 1) from = p.ws + (part.place * p.H + h) * PN;
-      else if (slot >= 0 && seq_resumes(p.q, part.seq)) from = p.state + slot * p.slot_stride + h * PN;
-    }
-    auto put_state = [&](int k) {  // its atom k as the bf16 operand
-      float v[8];
-#pragma unroll
-      for (int ck = 0; ck < 2; ++ck) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = s[k][8 * ck + j];
-        sts16(sS + (hf + WQ * k) * kAtomBytes + atom_at(n, ck), Bf::pack(v));
-      }
-    };
-#pragma unroll
-    for (int k = 0; k < AW; ++k) {
-      const int a = hf + WQ * k;
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const int col = a * 16 + j;
-        s[k][j] = from && n < N && a < atoms && col < pw
-                      ? from[static_cast<int64_t>(col0 + col) * N + n] : 0.0f;
-      }
-      if (!STATE_ONLY && a < atoms) put_state(k);
-    }
-    if (!STATE_ONLY) {
-      fence_async_smem();
-      mbar_arrive(b_s);
-    }
-
+    if (chunks > 0) fetch(0);
+    int slot = 0, use = 0;
     for (int c = 0; c < chunks; ++c) {
-      const float* sd = s_decay + (c & 1) * kDecayFloats;
-      cp_async_wait();
-      fence_async_smem();
-      mbar_arrive(b_bc);
-      // X and the pieces of w X
-      if (!warp_wait(b_dt, c)) break;
-      // (other warps may still read X of the chunk before)
-      if (!STATE_ONLY && c > 0 && !warp_wait(b_e, c - 1)) break;
+      if (!wait.warp(bar(kDtFull + slot), use)) break;
+      const float* sw = s_decay + slot * kDecayFloats + 3 * kQ;
+      const float w0 = sw[r0], w1 = sw[64 + r0];
+      if (c > 0 && !wait.warp(bar(kDsDone), c - 1)) break;
+      const uint32_t at0 = atom_at(r0, tid & 1);  // row 64 + r0: 8 groups further
 #pragma unroll
-      for (int it = 0; it < XI; ++it) {
-        const int id = it * NT + tid;
-        if (id < atoms * 256) {
-          const int r = (id & 255) >> 1;
-          const uint32_t at = (id >> 8) * kAtomBytes + atom_at(r, id & 1);
-          const float w = sd[3 * kQ + r];
-          float v[8], hi[8];
-          Bf::unpack(xr[it], v);
+      for (int i = 0; i < kXPieces; ++i) {
+        if (i < 2 * atoms) {
+          uint4 u[3];
+          pieces_of(xr[i], i & 1 ? w1 : w0, u);
+          const uint32_t at = sW + (i >> 1) * kAtomBytes + (i & 1) * 2048 + at0;
 #pragma unroll
-          for (int e = 0; e < 8; e += 2) mul2(v[e], v[e + 1], v[e], v[e + 1], w, w);
-          if (!STATE_ONLY) sts16(sX + at, xr[it]);
-#pragma unroll
-          for (int piece = 0; piece < 3; ++piece) {
-            const uint4 u = Bf::pack(v);
-            sts16(sW + piece * x_bytes + at, u);
-            if (piece < 2) {
-              Bf::unpack(u, hi);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) v[e] -= hi[e];
-            }
-          }
+          for (int k = 0; k < 3; ++k) sts16(at + k * x_bytes, u[k]);
         }
       }
       fence_async_smem();
-      tc_fence_before();
-      mbar_arrive(b_x);
-      if (c + 1 < chunks) fetch_x(c + 1);
-
-      if constexpr (!STATE_ONLY) {
-        // M of rows 32 q.. and columns 32 hf.. (WQ == 4)
+      mbar_arrive(bar(kWFull));
+      if (c > 0 && !wait.warp(bar(kYRead), c - 1)) break;
+#pragma unroll
+      for (int i = 0; i < kXPieces; ++i)
+        if (i < 2 * atoms) sts16(sX + (i >> 1) * kAtomBytes + (i & 1) * 2048 + at0, xr[i]);
+      fence_async_smem();
+      mbar_arrive(bar(kXFull));
+      if (c + 1 < chunks) fetch(c + 1);
+      if (++slot == kDecays) slot = 0, ++use;
+    }
+  } else if (warp < kWarpSY) {
+    // ---- M of rows 32 q + lane ----
+    const int q = warp & 3;
+    const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
+    int slot = 0, use = 0;
+    for (int c = 0; c < chunks; ++c) {
+      if (!wait.warp(bar(kDtFull + slot), use)) break;
+      const float* sd = s_decay + slot * kDecayFloats;
+      const float pre = sd[32 * q + lane];
+      if (!wait.warp(bar(kGDone), c)) break;
+      // the M before is read (by the same commit as Y's)
+      if (c > 0 && !wait.warp(bar(kYDone), c - 1)) break;
+      tc_fence_after();
+      float between = pre;  // row prefix + the blocks between
+#pragma unroll
+      for (int blk = 3; blk >= 0; --blk) {
         uint32_t m[16];
-        if (hf <= q) {
-          if (!warp_wait(b_g, c)) break;
-          tc_fence_after();
+        if (blk > q) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) m[j] = 0;
+        } else {
           uint32_t gr[32];
-          tmem_ld32_nowait(tmem + lanes + kColG + 32 * hf, gr);
-          const float pre = sd[32 * q + lane];
-          if (hf < q) {
-            float between = pre;
-            for (int b = hf + 1; b < q; ++b) between += sd[5 * kQ + b];
-            const float f = ex2_approx(between);
+          tmem_ld32_nowait(tmem + lanes + kColG + 32 * blk, gr);
+          if (blk == q) {
             tmem_ld_wait();
 #pragma unroll
             for (int j = 0; j < 32; j += 4) {
-              const float4 cf = *reinterpret_cast<const float4*>(sd + kQ + 32 * hf + j);
+              const float4 pj = *reinterpret_cast<const float4*>(sd + 32 * blk + j);
+              const float4 dj = *reinterpret_cast<const float4*>(sd + 2 * kQ + 32 * blk + j);
+              const float v0 = __uint_as_float(gr[j]) * (dj.x * ex2_approx(pre - pj.x));
+              const float v1 = __uint_as_float(gr[j + 1]) * (dj.y * ex2_approx(pre - pj.y));
+              const float v2 = __uint_as_float(gr[j + 2]) * (dj.z * ex2_approx(pre - pj.z));
+              const float v3 = __uint_as_float(gr[j + 3]) * (dj.w * ex2_approx(pre - pj.w));
+              m[j / 2] = Bf::pack2(j <= lane ? v0 : 0.0f, j + 1 <= lane ? v1 : 0.0f);
+              m[j / 2 + 1] = Bf::pack2(j + 2 <= lane ? v2 : 0.0f, j + 3 <= lane ? v3 : 0.0f);
+            }
+          } else {
+            const float f = ex2_approx(between);
+            between += sd[5 * kQ + blk];
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+              const float4 cf = *reinterpret_cast<const float4*>(sd + kQ + 32 * blk + j);
               float v0, v1, v2, v3;
               mul2(v0, v1, cf.x, cf.y, f, f);
               mul2(v2, v3, cf.z, cf.w, f, f);
@@ -487,37 +582,63 @@ __global__ void __launch_bounds__((4 * WQ + 2) * 32, STATE_ONLY ? 2 : 1)
               m[j / 2] = Bf::pack2(v0, v1);
               m[j / 2 + 1] = Bf::pack2(v2, v3);
             }
-          } else {
-            tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-              const float4 pj = *reinterpret_cast<const float4*>(sd + 32 * hf + j);
-              const float4 dj = *reinterpret_cast<const float4*>(sd + 2 * kQ + 32 * hf + j);
-              const float v0 = __uint_as_float(gr[j]) * (dj.x * ex2_approx(pre - pj.x));
-              const float v1 = __uint_as_float(gr[j + 1]) * (dj.y * ex2_approx(pre - pj.y));
-              const float v2 = __uint_as_float(gr[j + 2]) * (dj.z * ex2_approx(pre - pj.z));
-              const float v3 = __uint_as_float(gr[j + 3]) * (dj.w * ex2_approx(pre - pj.w));
-              m[j / 2] = Bf::pack2(j <= lane ? v0 : 0.0f, j + 1 <= lane ? v1 : 0.0f);
-              m[j / 2 + 1] = Bf::pack2(j + 2 <= lane ? v2 : 0.0f, j + 3 <= lane ? v3 : 0.0f);
-            }
           }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) m[j] = 0;
         }
-        tmem_st16(tmem + lanes + kColM + 16 * hf, m);
-        tc_fence_before();
-        mbar_arrive(b_m);
+        tmem_st16(tmem + lanes + kColM + 16 * blk, m);
       }
-
-      // S: B and C are read, the next ones may come
-      if (!warp_wait(b_ds, c)) break;
-      tc_fence_after();
-      if (c + 1 < chunks) load_bc(c + 1);
-      const float decay = sd[5 * kQ + 4];
+      tc_fence_before();
+      mbar_arrive(bar(kMFull));
+      if (++slot == kDecays) slot = 0, ++use;
+    }
+  } else {
+    // ---- S and Y: lanes 32 q.., atoms hf, hf + 2, .. ----
+    const int q = warp & 3, hf = (warp >> 2) & 1, n = 32 * q + lane;
+    const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
+    const float dskip = p.d ? __ldg(p.d + h) : 0.0f;
+    const int64_t slot_at = seq_slot(p.q, part.seq);
+    const int64_t PN = static_cast<int64_t>(P) * N;
+    float s[kSYAtoms][16];  // S^T: row n, columns 16 (hf + 2 k) + j
+    const float* from = nullptr;
+    if (part.count > 1) from = p.ws + (part.place * p.H + h) * PN;
+    else if (slot_at >= 0 && seq_resumes(p.q, part.seq))
+      from = p.state + slot_at * p.slot_stride + h * PN;
+    auto put = [&](int k) {  // atom k as the bf16 operand
+      float v[8];
 #pragma unroll
-      for (int k = 0; k < AW; ++k) {
-        const int a = hf + WQ * k;
+      for (int ck = 0; ck < 2; ++ck) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = s[k][8 * ck + j];
+        sts16(sS + (hf + 2 * k) * kAtomBytes + atom_at(n, ck), Bf::pack(v));
+      }
+    };
+#pragma unroll
+    for (int k = 0; k < kSYAtoms; ++k) {
+      const int a = hf + 2 * k;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const int col = a * 16 + j;
+        s[k][j] = from && n < N && a < atoms && col < pw
+                      ? from[static_cast<int64_t>(col0 + col) * N + n] : 0.0f;
+      }
+      if (a < atoms) put(k);
+    }
+    fence_async_smem();
+    mbar_arrive(bar(kSFull));
+    const int i = n;  // the row of Y
+    __nv_bfloat16* orow =
+        static_cast<__nv_bfloat16*>(p.out) + (part.begin + i) * p.os + hcol;
+    const int64_t ostep = static_cast<int64_t>(kQ) * p.os;
+    int slot = 0, use = 0;
+    for (int c = 0; c < chunks; ++c, orow += ostep) {
+      if (!wait.warp(bar(kDtFull + slot), use)) break;
+      const float* sd = s_decay + slot * kDecayFloats;
+      if (!wait.warp(bar(kDsDone), c)) break;
+      if (!wait.warp(bar(kY1Done), c)) break;
+      tc_fence_after();
+      const float decay = sd[5 * kQ + 4], e = sd[4 * kQ + i];
+#pragma unroll
+      for (int k = 0; k < kSYAtoms; ++k) {
+        const int a = hf + 2 * k;
         if (a < atoms) {
           uint32_t r[16];
           tmem_ld16(t_ds + lanes + a * 16, r);
@@ -525,104 +646,321 @@ __global__ void __launch_bounds__((4 * WQ + 2) * 32, STATE_ONLY ? 2 : 1)
           for (int j = 0; j < 16; j += 2)
             fma2(s[k][j], s[k][j + 1], s[k][j], s[k][j + 1], decay, decay, __uint_as_float(r[j]),
                  __uint_as_float(r[j + 1]));
-          if (!STATE_ONLY) put_state(k);
+          put(k);
         }
       }
+      fence_async_smem();
       tc_fence_before();
-      if constexpr (!STATE_ONLY) {
-        fence_async_smem();
-        mbar_arrive(b_s);
-        // Y
-        if (!warp_wait(b_y, c)) break;
-        tc_fence_after();
-        const int i = 32 * q + lane;
-        const int64_t t = static_cast<int64_t>(c) * kQ + i;
-        const float e = sd[4 * kQ + i];
+      mbar_arrive(bar(kSFull));
+      if (!wait.warp(bar(kYDone), c)) break;
+      tc_fence_after();
+      const bool valid = i < rows - static_cast<int64_t>(c) * kQ;
 #pragma unroll
-        for (int k = 0; k < AW; ++k) {
-          const int a = hf + WQ * k;
-          if (a >= atoms) continue;
-          uint32_t y1[16], y2[16];
-          tmem_ld16(t_y1 + lanes + a * 16, y1);
-          tmem_ld16(t_y2 + lanes + a * 16, y2);
+      for (int k = 0; k < kSYAtoms; ++k) {
+        const int a = hf + 2 * k;
+        if (a >= atoms) continue;
+        uint32_t y1[16], y2[16];
+        tmem_ld16(t_y1 + lanes + a * 16, y1);
+        tmem_ld16(t_y2 + lanes + a * 16, y2);
 #pragma unroll
-          for (int ck = 0; ck < 2; ++ck) {
-            float xv[8], y[8];
-            Bf::unpack(lds16(sX + a * kAtomBytes + atom_at(i, ck)), xv);
+        for (int ck = 0; ck < 2; ++ck) {
+          float xv[8], y[8];
+          Bf::unpack(lds16(sX + a * kAtomBytes + atom_at(i, ck)), xv);
 #pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-              fma2(y[j], y[j + 1], __uint_as_float(y1[8 * ck + j]),
-                   __uint_as_float(y1[8 * ck + j + 1]), e, e, __uint_as_float(y2[8 * ck + j]),
-                   __uint_as_float(y2[8 * ck + j + 1]));
-              fma2(y[j], y[j + 1], xv[j], xv[j + 1], dskip, dskip, y[j], y[j + 1]);
-            }
-            const int col = a * 16 + ck * 8;
-            if (t < rows && col < pw) {
-              const uint4 v = Bf::pack(y);
-              __nv_bfloat16* o = og + t * p.os + col;
-              if (tp.ovec) {
-                *reinterpret_cast<uint4*>(o) = v;
-              } else {
-                *reinterpret_cast<uint2*>(o) = make_uint2(v.x, v.y);
-                if (col + 4 < pw) *reinterpret_cast<uint2*>(o + 4) = make_uint2(v.z, v.w);
-              }
+          for (int j = 0; j < 8; j += 2) {
+            fma2(y[j], y[j + 1], __uint_as_float(y1[8 * ck + j]),
+                 __uint_as_float(y1[8 * ck + j + 1]), e, e, __uint_as_float(y2[8 * ck + j]),
+                 __uint_as_float(y2[8 * ck + j + 1]));
+            fma2(y[j], y[j + 1], xv[j], xv[j + 1], dskip, dskip, y[j], y[j + 1]);
+          }
+          const int col = a * 16 + ck * 8;
+          if (valid && col < pw) {
+            const uint4 v = Bf::pack(y);
+            if (tp.ovec) {
+              *reinterpret_cast<uint4*>(orow + col) = v;
+            } else {
+              *reinterpret_cast<uint2*>(orow + col) = make_uint2(v.x, v.y);
+              if (col + 4 < pw) *reinterpret_cast<uint2*>(orow + col + 4) = make_uint2(v.z, v.w);
             }
           }
         }
-        tc_fence_before();
-        mbar_arrive(b_e);
       }
+      tc_fence_before();
+      mbar_arrive(bar(kYRead));
+      mbar_arrive(bar(kDtFree + slot));
+      if (++slot == kDecays) slot = 0, ++use;
     }
-    cp_async_wait();
-
     // the state after the part's last row
-    float* to = nullptr;
-    if (STATE_ONLY) to = p.ws + ((part.place + 1) * p.H + h) * PN;
-    else if (part.index == part.count - 1 && slot >= 0) to = p.state + slot * p.slot_stride + h * PN;
-    if (to && n < N) {
+    if (part.index == part.count - 1 && slot_at >= 0 && n < N) {
+      float* to = p.state + slot_at * p.slot_stride + h * PN;
 #pragma unroll
-      for (int k = 0; k < AW; ++k)
+      for (int k = 0; k < kSYAtoms; ++k)
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          const int col = (hf + WQ * k) * 16 + j;
-          if (hf + WQ * k < atoms && col < pw) to[static_cast<int64_t>(col0 + col) * N + n] = s[k][j];
+          const int col = (hf + 2 * k) * 16 + j;
+          if (hf + 2 * k < atoms && col < pw) to[static_cast<int64_t>(col0 + col) * N + n] = s[k][j];
         }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 4 * WQ) {
+  if (warp == kWarpMma) {
     tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
+    tmem_dealloc(tmem, 512);
   }
 }
 
-uint32_t smem_bytes(int tile, bool state_only) {
-  const uint32_t x = tile / 16 * kAtomBytes;
-  return 1024 + (state_only ? kRowsBytes + 3 * x : 2 * kRowsBytes + 5 * x) +
-         2 * kDecayFloats * 4 + 72 + 8;
+// ---------------------------------------------------------------------------
+// k_scan_tc_state: the state a part adds from a zero start, and its decay (a
+// cut sequence's parts but the last).  Two CTAs per SM, whose stages overlap:
+// 8 warps write the pieces of w X and B, one thread issues dS, the 8 warps add
+// it to S in registers.
+// ---------------------------------------------------------------------------
+constexpr int kStateThreads = 10 * 32;
+
+__global__ void __launch_bounds__(kStateThreads, 2) k_scan_tc_state(const TcParams tp) {
+  constexpr int NT = 256;                       // threads of the elementwise warps
+  constexpr int AW = kMaxAtoms / 2;             // atoms of a warp
+  constexpr int XI = kMaxAtoms * 256 / NT;      // 16-byte pieces of X of a thread
+  const Params& p = tp.p;
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw_u = smem_u32(smem_raw);
+  const uint32_t base_u = (raw_u + 1023u) & ~1023u;
+  unsigned char* base = smem_raw + (base_u - raw_u);
+  const int atoms = tp.tile / 16;
+  const uint32_t x_bytes = atoms * kAtomBytes;
+  const uint32_t sB = base_u, sW = sB + kRowsBytes;
+  const uint32_t decay_off = kRowsBytes + 3 * x_bytes;
+  float* s_decay = reinterpret_cast<float*>(base + decay_off);  // [2][kQ] w, [2] decay
+  const uint32_t bars_off = decay_off + 2 * (kQ + 4) * 4;
+  volatile uint32_t* s_misc = reinterpret_cast<uint32_t*>(base + bars_off + 32);
+  // per chunk: B landed; w X written (and w read); decays made; dS computed
+  const uint32_t b_b = base_u + bars_off, b_x = b_b + 8, b_dt = b_b + 16, b_ds = b_b + 24;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    mbar_init(b_b, NT);
+    mbar_init(b_x, NT);
+    mbar_init(b_dt, 32);
+    mbar_init(b_ds, 1);
+    s_misc[1] = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 8) tmem_alloc(smem_u32(const_cast<uint32_t*>(s_misc)), 128);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_misc[0];
+  pdl_wait();
+  pdl_launch_dependents();
+
+  const Part part = find_part(p.q, p.part, blockIdx.x);
+  const int P = p.P, N = p.N;
+  const int h = blockIdx.y;
+  const int col0 = blockIdx.z * tp.tile;
+  // (offsets that do not ascend may count more places than there are)
+  const bool run = part.seq >= 0 && part.index < part.count - 1 && part.place + 1 < p.places;
+  const int64_t rows = run ? part.end - part.begin : 0;
+  const int chunks = static_cast<int>((rows + kQ - 1) / kQ);
+  const Waits wait = {s_misc + 1, tp.fault};
+
+  if (!run) {
+    // nothing: fall through to the end
+  } else if (warp == 8) {
+    if (lane == 0) {
+      const uint32_t id_ds = idesc_bf16(128, tp.tile) | kTransA | kTransB;
+      const uint64_t d_bt = desc_t128(sB, kRowsBytes / 2);
+      for (int c = 0; c < chunks; ++c) {
+        if (!wait.one(b_b, c) || !wait.one(b_x, c)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int piece = 2; piece >= 0; --piece) {
+          const uint64_t d_w = desc_t32(sW + piece * x_bytes);
+#pragma unroll
+          for (int k = 0; k < kQ / 16; ++k)
+            mma_bf16(tmem, d_bt + k * (2048 >> 4), d_w + k * (512 >> 4), id_ds,
+                     piece < 2 || k > 0);
+        }
+        mma_commit(b_ds);
+        // (waited for here too, so that none runs when the memory is freed)
+        if (!wait.one(b_ds, c)) break;
+      }
+    }
+  } else if (warp == 9) {
+    const float a2 = __ldg(p.a + h) * kLog2e;
+    const float bias = p.dt_bias ? __ldg(p.dt_bias + h) : 0.0f;
+    const __nv_bfloat16* dtp = static_cast<const __nv_bfloat16*>(p.dt) + part.begin * p.dts + h;
+    float raw[4];
+    auto fetch = [&](int c) {
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const int64_t t = static_cast<int64_t>(c) * kQ + 32 * b + lane;
+        raw[b] = t < rows ? Bf::load1(dtp + t * p.dts, 0) : 0.0f;
+      }
+    };
+    fetch(0);
+    float log_total = 0.0f;
+    for (int c = 0; c < chunks; ++c) {
+      float pre[4], suf[4], tot[4], dt[4];
+      const float total =
+          make_decays(raw, rows - static_cast<int64_t>(c) * kQ, bias, a2, p, pre, suf, dt, tot);
+      if (c + 1 < chunks) fetch(c + 1);
+      // this half was last read for chunk c - 2 (each phase waited for in turn)
+      if (c >= 1 && !wait.warp(b_x, c - 1)) break;
+      float* s = s_decay + (c & 1) * (kQ + 4);
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        float after = 0.0f;
+#pragma unroll
+        for (int k = 3; k > b; --k) after += tot[k];
+        s[32 * b + lane] = dt[b] * ex2_approx(suf[b] + after);
+      }
+      if (lane == 0) s[kQ] = ex2_approx(total);
+      log_total += total;
+      mbar_arrive(b_dt);
+    }
+    if (lane == 0 && blockIdx.z == 0) p.ws_decay[part.place * p.H + h] = ex2_approx(log_total);
+  } else {
+    const int q = warp & 3, hf = warp >> 2, n = 32 * q + lane;
+    const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
+    const int g = h / p.hpg, pw = min(tp.tile, P - col0);
+    const __nv_bfloat16* xg = static_cast<const __nv_bfloat16*>(p.x) + part.begin * p.xs +
+                              static_cast<int64_t>(h) * P + col0;
+    const __nv_bfloat16* bg =
+        static_cast<const __nv_bfloat16*>(p.b) + part.begin * p.bs + static_cast<int64_t>(g) * N;
+    auto load_b = [&](int c) {
+#pragma unroll
+      for (int it = 0; it < 2048 / NT; ++it) {
+        const int id = it * NT + tid, r = id >> 4, ch = id & 15;
+        const int64_t t = static_cast<int64_t>(c) * kQ + r;
+        const bool valid = t < rows && ch * 8 < N;
+        cp_async16(sB + (ch >> 3) * (kRowsBytes / 2) + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
+                   valid ? bg + t * p.bs + ch * 8 : bg, valid);
+      }
+    };
+    uint4 xr[XI];
+    auto fetch = [&](int c) {
+#pragma unroll
+      for (int it = 0; it < XI; ++it) {
+        const int id = it * NT + tid;
+        const int64_t t = static_cast<int64_t>(c) * kQ + ((id & 255) >> 1);
+        const int col = (id >> 8) * 16 + (id & 1) * 8;
+        xr[it] = t < rows && col < pw ? load_x(xg + t * p.xs + col, col, pw, tp.xvec)
+                                      : make_uint4(0, 0, 0, 0);
+      }
+    };
+    float s[AW][16];
+#pragma unroll
+    for (int k = 0; k < AW; ++k)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) s[k][j] = 0.0f;
+    load_b(0);
+    fetch(0);
+    for (int c = 0; c < chunks; ++c) {
+      const float* sd = s_decay + (c & 1) * (kQ + 4);
+      if (!wait.warp(b_dt, c)) break;
+      const float w = sd[(tid & 255) >> 1], decay = sd[kQ];
+      const uint32_t at0 = atom_at((tid & 255) >> 1, tid & 1);
+#pragma unroll
+      for (int it = 0; it < XI; ++it) {
+        if (it < atoms) {
+          uint4 u[3];
+          pieces_of(xr[it], w, u);
+#pragma unroll
+          for (int k = 0; k < 3; ++k) sts16(sW + k * x_bytes + it * kAtomBytes + at0, u[k]);
+        }
+      }
+      cp_async_wait();
+      fence_async_smem();
+      tc_fence_before();
+      mbar_arrive(b_b);
+      mbar_arrive(b_x);
+      if (c + 1 < chunks) fetch(c + 1);
+      if (!wait.warp(b_ds, c)) break;
+      tc_fence_after();
+      if (c + 1 < chunks) load_b(c + 1);
+#pragma unroll
+      for (int k = 0; k < AW; ++k) {
+        const int a = hf + 2 * k;
+        if (a < atoms) {
+          uint32_t r[16];
+          tmem_ld16(tmem + lanes + a * 16, r);
+#pragma unroll
+          for (int j = 0; j < 16; j += 2)
+            fma2(s[k][j], s[k][j + 1], s[k][j], s[k][j + 1], decay, decay, __uint_as_float(r[j]),
+                 __uint_as_float(r[j + 1]));
+        }
+      }
+      tc_fence_before();
+    }
+    cp_async_wait();
+    float* to = p.ws + ((part.place + 1) * p.H + h) * static_cast<int64_t>(P) * N;
+    if (n < N) {
+#pragma unroll
+      for (int k = 0; k < AW; ++k)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const int col = (hf + 2 * k) * 16 + j;
+          if (hf + 2 * k < atoms && col < pw) to[static_cast<int64_t>(col0 + col) * N + n] = s[k][j];
+        }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 128);
+  }
 }
+
+// ---------------------------------------------------------------------------
+// Host side.
+// ---------------------------------------------------------------------------
+constexpr uint32_t kSmemMost = 227 * 1024;
+uint32_t main_smem(int tile, int cbufs) {
+  return 1024 + (2 + cbufs) * kRowsBytes + 5 * (tile / 16 * kAtomBytes) +
+         kDecays * kDecayFloats * 4 + 8 * kBars + 8;
+}
+uint32_t state_smem(int tile) {
+  return 1024 + kRowsBytes + 3 * (tile / 16 * kAtomBytes) + 2 * (kQ + 4) * 4 + 32 + 8;
+}
+// C twice where it fits (tiles of up to 64 columns).
+int cbufs_of(int tile) { return main_smem(tile, 2) <= kSmemMost ? 2 : 1; }
 
 int tile_of(int64_t P) {
   const int64_t tiles = (P + 16 * kMaxAtoms - 1) / (16 * kMaxAtoms);
   return static_cast<int>(((P + tiles - 1) / tiles + 15) / 16 * 16);
 }
 
-constexpr int kMainWq = 4, kStateWq = 2;
-
 cudaError_t allow_smem() {
   static std::once_flag once;
   static cudaError_t err = cudaSuccess;
   std::call_once(once, [] {
-    err = cudaFuncSetAttribute(k_scan_tc<kMainWq, false>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               static_cast<int>(smem_bytes(16 * kMaxAtoms, false)));
+    err = cudaFuncSetAttribute(k_scan_tc, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               static_cast<int>(kSmemMost));
     if (err == cudaSuccess)
-      err = cudaFuncSetAttribute(k_scan_tc<kStateWq, true>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(smem_bytes(16 * kMaxAtoms, true)));
+      err = cudaFuncSetAttribute(k_scan_tc_state, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(state_smem(16 * kMaxAtoms)));
   });
   return err;
+}
+
+// [rows][groups][N] in boxes of 128 rows and 64 columns: columns behind N and
+// rows behind the buffer read as zeros.
+bool make_map(CUtensorMap* m, const void* ptr, int64_t N, int64_t groups, int64_t rows,
+              int64_t stride) {
+  EncodeTiled enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(groups),
+                              static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(N) * 2,
+                                 static_cast<cuuint64_t>(rows > 1 ? stride : groups * N) * 2};
+  const cuuint32_t box[3] = {64, 1, kQ};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
 }
 
 }  // namespace
@@ -630,6 +968,9 @@ cudaError_t allow_smem() {
 // bf16, state columns in whole 16-byte vectors and at most one tile, head
 // columns in whole 8-byte ones, and rows aligned to those.
 bool tc_covers(const ggrn_scan_call& c) {
+  if (c.rows > INT32_MAX / 2 || c.b_row_stride >= int64_t{1} << 38 ||
+      c.c_row_stride >= int64_t{1} << 38)
+    return false;  // (what a tensor map holds)
   if (c.dtype != kBF16 || c.state_size % 8 != 0 || c.state_size > 128 || c.head_dim % 4 != 0)
     return false;
   const bool many = c.rows > 1;
@@ -642,34 +983,33 @@ bool tc_covers(const ggrn_scan_call& c) {
 }
 
 // Rows of a part.  The launch's time goes by its waves of one CTA per SM, each
-// as long as a part's chunks; a cut costs the state-only launch over the same
-// chunks (about half of a chunk's time, two CTAs per SM) and the join.  The
-// lengths behind cu_seqlens are not known here: rows and sequences stand for
-// the number of parts.
+// as long as a part's chunks (and about one more to start and end); a cut
+// costs the state-only launch over the same chunks (about half of a chunk's
+// time, two CTAs per SM) and the join.  The lengths behind cu_seqlens are not
+// known here: sequences are taken for equally long, and where those stay
+// whole a part is twice their length, so that only longer ones are cut.
 int64_t tc_part_rows(const ggrn_scan_call& c, int64_t longest) {
   const int64_t tiles = (c.head_dim + tile_of(c.head_dim) - 1) / tile_of(c.head_dim);
   const int64_t heads = c.heads * tiles, sms = device_sms();
-  const int64_t all = std::max<int64_t>(1, (longest + kQ - 1) / kQ);
   const int64_t seqs = std::max<int64_t>(1, c.seqs);
+  const int64_t most = std::max<int64_t>(1, (longest + kQ - 1) / kQ);
+  const int64_t all =
+      std::min(most, std::max<int64_t>(1, ((c.rows + seqs - 1) / seqs + kQ - 1) / kQ));
   auto waves = [&](int64_t ctas) { return (ctas + sms - 1) / sms; };
   int64_t best = all;
   double best_cost = 0.0;
-  // parts of a whole number of chunks, as many as make a difference
   for (int64_t cuts = 1; cuts <= std::min<int64_t>(all, 64); ++cuts) {
     const int64_t k = (all + cuts - 1) / cuts;
-    const int64_t parts = c.cu_seqlens ? (c.rows + k * kQ - 1) / (k * kQ) + (seqs - 1)
-                                       : seqs * ((all + k - 1) / k);
-    double cost = static_cast<double>(waves(parts * heads)) * (k + 1.0);
-    if (k < all) {
-      const int64_t inner = std::max<int64_t>(1, parts - seqs);
-      cost += 0.5 * static_cast<double>(waves((inner * heads + 1) / 2)) * (k + 1.0) + 2.0;
-    }
+    const int64_t parts = (all + k - 1) / k;
+    double cost = static_cast<double>(waves(seqs * parts * heads)) * (k + 1.0);
+    if (parts > 1)
+      cost += 0.5 * static_cast<double>(waves((seqs * (parts - 1) * heads + 1) / 2)) * (k + 1.0) + 2.0;
     if (cuts == 1 || cost < best_cost) {
       best = k;
       best_cost = cost;
     }
   }
-  return best * kQ;
+  return (best == all ? std::min(most, 2 * all) : best) * kQ;
 }
 
 int tc_run(const ggrn_scan_call& c, const Params& p, bool cut, cudaStream_t s) {
@@ -680,22 +1020,28 @@ int tc_run(const ggrn_scan_call& c, const Params& p, bool cut, cudaStream_t s) {
   tp.tile = tile_of(p.P);
   tp.xvec = p.P % 8 == 0 && mixer::aligned_to(p.x, 16) && p.xs % 8 == 0;
   tp.ovec = p.P % 8 == 0 && mixer::aligned_to(p.out, 16) && p.os % 8 == 0;
+  tp.cbufs = cbufs_of(tp.tile);
   const cudaError_t e = allow_smem();
   if (e != cudaSuccess) {
     record_cuda_error(e);
     return GGRN_ERR_CUDA;
   }
+  CUtensorMap tm_b, tm_c;
+  std::memset(&tm_b, 0, sizeof(tm_b));
+  std::memset(&tm_c, 0, sizeof(tm_c));
+  if (c.rows > 0 && (!make_map(&tm_b, c.b, c.state_size, c.groups, c.rows, c.b_row_stride) ||
+                     !make_map(&tm_c, c.c, c.state_size, c.groups, c.rows, c.c_row_stride)))
+    return GGRN_ERR_UNSUPPORTED;
   const dim3 grid(static_cast<unsigned>(p.parts), static_cast<unsigned>(p.H),
                   static_cast<unsigned>((p.P + tp.tile - 1) / tp.tile));
   if (cut) {
-    int st = mixer::launch(k_scan_tc<kStateWq, true>, grid, (4 * kStateWq + 2) * 32,
-                           smem_bytes(tp.tile, true), s, tp);
+    int st = mixer::launch(k_scan_tc_state, grid, kStateThreads, state_smem(tp.tile), s, tp);
     if (st != GGRN_OK) return st;
     st = launch_join(p, s);
     if (st != GGRN_OK) return st;
   }
-  return mixer::launch(k_scan_tc<kMainWq, false>, grid, (4 * kMainWq + 2) * 32,
-                       smem_bytes(tp.tile, false), s, tp);
+  return mixer::launch(k_scan_tc, grid, kMainThreads, main_smem(tp.tile, tp.cbufs), s, tm_b, tm_c,
+                       tp);
 }
 
 }  // namespace scan

@@ -138,6 +138,22 @@ def test_a_long_sequence_is_cut(dtype, shape):
     check_state(st, new, nb, ns)
 
 
+@pytest.mark.parametrize("dtype,heads", [(torch.bfloat16, 160), (torch.float32, 500)])
+def test_a_long_sequence_in_one_part(dtype, heads):
+    """Enough heads to fill the GPU: many chunks one after the other."""
+    rows = 1200 if heads == 160 else 200
+    k = Case(rows, heads, 16, 1, 40, dtype, slots=1, seed=9)
+    v, w = k.on()
+    assert g.scan_workspace_bytes(v["x"], v["dt"], w["a"], v["b"], v["c"], head_dim=16,
+                                  state_size=40) == 0
+    st = k.state.cuda()
+    got = k.run(state=st, resume=torch.ones(1, dtype=torch.bool).cuda())
+    want, bound, size, new, nb, ns = k.want(spans=[(0, rows)], resume=[True])
+    check(got, want, bound, size, dtype)
+    check_state(st, new, nb, ns)
+    assert g.fault_status() == 0
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("a,dt_shift,limits", [
     (-0.0, 0.0, (0.0, math.inf)),       # no decay: long sums
