@@ -24,16 +24,20 @@
 //
 // One CTA per part of a sequence and head (or tile of a head's columns), its
 // warps specialised so that all stages of neighbouring chunks overlap:
-//   X    4 warps  X from global memory, w X in pieces, both into shared memory
-//   M    4 warps  G out of tensor memory, decays applied, M back into it
-//   SY   8 warps  S in registers (dS out of tensor memory, S into shared
-//                 memory as the next chunk's operand), Y out of tensor memory
-//   and one warp each that issues the products, copies B and C (tensor-map
-//   copies, 128-byte swizzle: one layout serves B as rows of state columns in G
-//   and as its transpose in dS), and makes the decays.
-// X, its pieces and S lie in the 32-byte swizzled layout, whose 16-column
-// atoms fit any head size.  Products are issued in the order C S, dS, M X, G of
-// the next chunk, which leaves every other stage the time of two products.
+//   X    4 warps   the pieces of w X
+//   M    8 warps   G out of tensor memory, decays applied, M back into it
+//   SY   16 warps  S in registers (dS out of tensor memory, S into shared
+//                  memory as the next chunk's operand), Y out of tensor memory
+// and one warp each that issues the products, copies (B, C, X in and Y out by
+// tensor-map copies) and makes the decays.  B and C lie in the 128-byte
+// swizzled layout, which serves B as rows of state columns in G and as its
+// transpose in dS; X, its pieces, S and Y in the 32-byte swizzled one, whose
+// 16-column atoms fit any head size (the layout of an operand does not change a
+// product's time).  Products are issued in the order C S, dS, M X, G of the
+// next chunk, which leaves every other stage the time of two products.  The
+// stages' loops are kept small: unrolled, the eight of them ran out of the
+// instruction cache (10 of 24 stall cycles an instruction) at a quarter of the
+// speed.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -51,7 +55,7 @@ namespace scan {
 namespace {
 
 constexpr int kQ = 128;            // tokens of a chunk (the products' M)
-constexpr int kMaxAtoms = 6;       // 16-column atoms of a tile of a head: 96 columns
+constexpr int kMaxAtoms = 5;       // 16-column atoms of a tile of a head: 80 columns
 constexpr uint32_t kFaultScanWait = 64u;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMinLog = -256.0f;
@@ -67,9 +71,8 @@ constexpr uint32_t kColG = 0, kColM = 128, kColDs = 192;
 struct TcParams {
   Params p;
   unsigned int* fault;
-  int tile;        // columns of a head per CTA, a multiple of 16 up to 96
-  int cbufs;       // buffers of C: 1 or 2
-  int xvec, ovec;  // 16-byte rows of x / out (else 8-byte)
+  int tile;        // columns of a head per CTA, a multiple of 16 up to 80
+  int xtma, otma;  // x / out by tensor-map copies (else 8 bytes at a time)
 };
 
 // D (+)= A B with A [128, K] in tensor memory.
@@ -102,30 +105,25 @@ __device__ __forceinline__ uint32_t atom_at(int r, int ck) {
   return (r >> 3) * 256 + (r & 7) * 32 + ((ck ^ ((r >> 2) & 1)) << 4);
 }
 
-__device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
-      "%30, %31}, [%32];"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
-        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        "=r"(r[7])
       : "r"(taddr));
 }
 __device__ __forceinline__ void tmem_ld_wait() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, "
-      "%10, %11, %12, %13, %14, %15};"
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};"
       :
       : "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-        "r"(r[15]), "r"(taddr)
+        "r"(taddr)
       : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void sts16(uint32_t addr, const uint4& v) {
@@ -140,14 +138,6 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
                : "r"(addr));
   return v;
 }
-// 16 bytes to shared memory, zeros where !valid (nothing is read then).
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(valid ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
 using Bf = Elem<__nv_bfloat16>;
 
 // The decays of one chunk into shared memory: `raw` holds the raw dt of tokens
@@ -167,7 +157,7 @@ __device__ __forceinline__ float make_decays(const float (&raw)[4], int64_t left
     suf[b] = __shfl_down_sync(0xffffffffu, l, 1);
     if (lane == 31) suf[b] = 0.0f;
   }
-#pragma unroll
+#pragma unroll 1
   for (int o = 1; o < 32; o <<= 1)
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
@@ -204,19 +194,31 @@ __device__ __forceinline__ void pieces_of(const uint4& x, float w, uint4 (&u)[3]
   for (int k = 0; k < 3; ++k) u[k] = make_uint4(out[k][0], out[k][1], out[k][2], out[k][3]);
 }
 
-// X of one chunk: 16-byte pieces `id` of a thread, columns in pairs of an
-// atom, so that a warp reads whole 32-byte sectors and writes without
-// conflicts.
-__device__ __forceinline__ uint4 load_x(const __nv_bfloat16* src, int col, int pw, bool vec) {
-  if (vec) return ld_stream(src);
+// Columns [col, col + 8) of a row of X whose rows are only 8-byte aligned.
+__device__ __forceinline__ uint4 load_x(const __nv_bfloat16* src, int col, int pw) {
   uint4 v = make_uint4(0, 0, 0, 0);
-  const uint2 lo = __ldg(reinterpret_cast<const uint2*>(src));
-  v.x = lo.x, v.y = lo.y;
+  if (col < pw) {
+    const uint2 lo = __ldg(reinterpret_cast<const uint2*>(src));
+    v.x = lo.x, v.y = lo.y;
+  }
   if (col + 4 < pw) {
     const uint2 hi = __ldg(reinterpret_cast<const uint2*>(src + 4));
     v.z = hi.x, v.w = hi.y;
   }
   return v;
+}
+
+// dS (+)= B^T [w X in pieces], smallest piece first; each step's B^T is kept
+// for its three pieces.
+__device__ __forceinline__ void issue_ds(uint32_t t_ds, uint64_t d_bt, uint64_t d_w, uint32_t piece,
+                                         uint32_t idesc) {
+#pragma unroll 2
+  for (int k = 0; k < kQ / 16; ++k) {
+    const uint64_t a = d_bt + k * (2048 >> 4), w = d_w + k * (512 >> 4);
+    mma_bf16_keep<Keep::kFill>(t_ds, a, w + 2 * piece, idesc, k > 0);
+    mma_bf16_keep<Keep::kUse>(t_ds, a, w + piece, idesc, true);
+    mma_bf16_keep<Keep::kLast>(t_ds, a, w, idesc, true);
+  }
 }
 
 // Bounded waits of a CTA: on a timeout the CTA's flag and the library's status
@@ -241,37 +243,46 @@ struct Waits {
   }
 };
 
+// Arrive for a whole warp (each lane's earlier work included).
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
 // ---------------------------------------------------------------------------
 // k_scan_tc
 // ---------------------------------------------------------------------------
-constexpr int kWarpM = 4, kWarpSY = 8, kWarpMma = 16, kWarpCopy = 17, kWarpDt = 18;
-constexpr int kMainThreads = 19 * 32;
-constexpr int kXThreads = 128, kMThreads = 128, kSYThreads = 256;
-constexpr int kSYAtoms = kMaxAtoms / 2;                   // atoms of a warp of SY
-constexpr int kXPieces = kMaxAtoms * 256 / kXThreads;     // 16-byte pieces of X of a thread
-// barriers, 8 bytes each
+constexpr int kXWarps = 4, kMWarps = 8, kSYWarps = 16;
+constexpr int kWarpM = kXWarps, kWarpSY = kWarpM + kMWarps, kWarpMma = kWarpSY + kSYWarps,
+              kWarpCopy = kWarpMma + 1, kWarpDt = kWarpMma + 2;
+constexpr int kMainThreads = (kWarpMma + 3) * 32;
+constexpr int kSYShare = kSYWarps / 4;                    // warps on a quarter of the lanes
+constexpr int kSYAtoms = (kMaxAtoms + kSYShare - 1) / kSYShare;
+// barriers, 8 bytes each; [2] and [3] by buffer
 enum Bar {
   kBFull = 0,    // [2] B landed
   kBFree = 2,    // [2] B read by G and dS
   kCFull = 4,    // [2] C landed
   kCFree = 6,    // [2] C read by G and C S
-  kDtFull = 8,   // [3] decays made
-  kDtFree = 11,  // [3] and read
-  kTail = 14,    // B of a part's last, partial chunk landed
-  kWFull = 15,   // w X written
-  kXFull = 16,   // X written
-  kGDone = 17,   // G computed
-  kMFull = 18,   // M written, G read
-  kDsDone = 19,  // dS computed, w X read
-  kY1Done = 20,  // C S computed, S read
-  kSFull = 21,   // S written, dS read
-  kYDone = 22,   // Y computed, M read
-  kYRead = 23,   // Y and X read
-  kBars = 24
+  kXLand = 8,    // [2] X landed
+  kYPut = 10,    // [2] Y in X's place (or stored)
+  kDtFull = 12,  // [3] decays made
+  kDtFree = 15,  // [3] and read
+  kTail = 18,    // B of a part's last, partial chunk landed
+  kWFull = 19,   // w X written
+  kGDone = 20,   // G computed
+  kMFull = 21,   // M written, G read
+  kDsDone = 22,  // dS computed, w X read
+  kY1Done = 23,  // C S computed, S read
+  kSFull = 24,   // S written, dS read
+  kYDone = 25,   // Y computed, M read
+  kYRead = 26,   // Y read
+  kBars = 27
 };
 
 __global__ void __launch_bounds__(kMainThreads, 1)
     k_scan_tc(const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ CUtensorMap tm_c,
+              const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_o,
               const TcParams tp) {
   const Params& p = tp.p;
   extern __shared__ unsigned char smem_raw[];
@@ -281,39 +292,27 @@ __global__ void __launch_bounds__(kMainThreads, 1)
   const int atoms = tp.tile / 16;
   const uint32_t x_bytes = atoms * kAtomBytes;
   const uint32_t sB = base_u, sC = sB + 2 * kRowsBytes;
-  const uint32_t sW = sC + tp.cbufs * kRowsBytes;        // three pieces of w X
-  const uint32_t sX = sW + 3 * x_bytes, sS = sX + x_bytes;
+  const uint32_t sW = sC + kRowsBytes;                   // three pieces of w X
+  const uint32_t sX = sW + 3 * x_bytes;                  // [2]
+  const uint32_t sS = sX + 2 * x_bytes;
   const uint32_t decay_off = sS + x_bytes - base_u;
   float* s_decay = reinterpret_cast<float*>(base + decay_off);
   const uint32_t bars_off = decay_off + kDecays * kDecayFloats * 4;
-  volatile uint32_t* s_misc = reinterpret_cast<uint32_t*>(base + bars_off + 8 * kBars);
+  volatile uint32_t* s_misc = reinterpret_cast<uint32_t*>(base + bars_off + 8 * kBars + 8);
   auto bar = [&](int i) { return base_u + bars_off + 8u * i; };
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(kBFull + i), 1);
-      mbar_init(bar(kBFree + i), 1);
-      mbar_init(bar(kCFull + i), 1);
-      mbar_init(bar(kCFree + i), 1);
-    }
-    for (int i = 0; i < kDecays; ++i) {
-      mbar_init(bar(kDtFull + i), 32);
-      mbar_init(bar(kDtFree + i), kSYThreads);
-    }
-    mbar_init(bar(kTail), 1);
-    mbar_init(bar(kWFull), kXThreads);
-    mbar_init(bar(kXFull), kXThreads);
-    mbar_init(bar(kGDone), 1);
-    mbar_init(bar(kMFull), kMThreads);
-    mbar_init(bar(kDsDone), 1);
-    mbar_init(bar(kY1Done), 1);
-    mbar_init(bar(kSFull), kSYThreads);
-    mbar_init(bar(kYDone), 1);
-    mbar_init(bar(kYRead), kSYThreads);
-    s_misc[1] = 0;
+  if (tid < kBars) {
+    const int i = tid;
+    mbar_init(bar(i), i == kWFull                                  ? kXWarps
+                      : i == kMFull                                ? kMWarps
+                      : (i >= kYPut && i < kYPut + 2) || i == kSFull || i == kYRead ||
+                              (i >= kDtFree && i < kDtFree + kDecays)
+                          ? kSYWarps
+                          : 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (tid == 0) s_misc[1] = 0;
   if (warp == kWarpMma) tmem_alloc(smem_u32(const_cast<uint32_t*>(s_misc)), 512);
   tc_fence_before();
   __syncthreads();
@@ -330,124 +329,155 @@ __global__ void __launch_bounds__(kMainThreads, 1)
   const int pw = min(tp.tile, P - col0);         // and how many
   const int64_t hcol = static_cast<int64_t>(h) * P + col0;
   const bool run = part.seq >= 0 && !(part.count > 1 && part.place >= p.places);
-  const int64_t rows = run ? part.end - part.begin : 0;
-  const int chunks = static_cast<int>((rows + kQ - 1) / kQ);
+  const int rows = run ? static_cast<int>(part.end - part.begin) : 0;
+  const int chunks = (rows + kQ - 1) / kQ;
   const Waits wait = {s_misc + 1, tp.fault};
   // Each phase of a barrier is waited for in turn: a parity tells a phase from
-  // its neighbours only.
+  // its neighbours only.  What may run ahead of a waiter by more is by buffer.
 
   if (!run) {
     // nothing: fall through to the end
   } else if (warp == kWarpMma) {
-    // ---- the products ----
-    if (lane == 0) {
-      const uint32_t id_g = idesc_bf16(128, 128);
-      const uint32_t id_ds = idesc_bf16(128, tp.tile) | kTransA | kTransB;
-      const uint32_t id_y = idesc_bf16(128, tp.tile) | kTransB;
-      const uint64_t d_x = desc_t32(sX), d_s = desc_t32(sS);
-      const int ksteps = (N + 15) / 16;
-      // step k of 16 along the columns of a 128-byte swizzled tile
-      auto kk = [](int k) {
-        return static_cast<uint64_t>((k >> 2) * (kRowsBytes / 2) + (k & 3) * 32) >> 4;
-      };
-      auto cslot = [&](int c) { return tp.cbufs == 2 ? c & 1 : 0; };
-      auto cuse = [&](int c) { return tp.cbufs == 2 ? c >> 1 : c; };
-      auto issue_g = [&](int c) {
-        if (!wait.one(bar(kBFull + (c & 1)), c >> 1) || !wait.one(bar(kCFull + cslot(c)), cuse(c)))
-          return false;
-        tc_fence_after();
+    // ---- the products (the whole warp waits, one lane issues) ----
+    const uint32_t id_g = idesc_bf16(128, 128);
+    const uint32_t id_ds = idesc_bf16(128, tp.tile) | kTransA | kTransB;
+    const uint32_t id_y = idesc_bf16(128, tp.tile) | kTransB;
+    const uint64_t d_s = desc_t32(sS), d_w = desc_t32(sW), d_c = desc_sw128(sC);
+    const uint32_t piece = x_bytes >> 4;
+    const int ksteps = (N + 15) / 16;
+    // step k of 16 along the columns of a 128-byte swizzled tile
+    auto kk = [](int k) {
+      return static_cast<uint64_t>((k >> 2) * (kRowsBytes / 2) + (k & 3) * 32) >> 4;
+    };
+    auto issue_g = [&](int c) {
+      if (!wait.warp(bar(kBFull + (c & 1)), c >> 1) || !wait.warp(bar(kCFull), c)) return false;
+      tc_fence_after();
+      if (elect_one()) {
         const uint64_t d_b = desc_sw128(sB + (c & 1) * kRowsBytes);
-        const uint64_t d_c = desc_sw128(sC + cslot(c) * kRowsBytes);
-        for (int k = 0; k < ksteps; ++k) mma_bf16(tmem + kColG, d_c + kk(k), d_b + kk(k), id_g, k > 0);
+#pragma unroll 2
+        for (int k = 0; k < ksteps; ++k)
+          mma_bf16(tmem + kColG, d_c + kk(k), d_b + kk(k), id_g, k > 0);
         mma_commit(bar(kGDone));
-        return true;
-      };
-      bool ok = chunks == 0 || issue_g(0);
-      for (int c = 0; ok && c < chunks; ++c) {
-        // C S (S of the chunk before, Y and dS read)
-        if (!(ok = wait.one(bar(kSFull), c) && (c == 0 || wait.one(bar(kYRead), c - 1)))) break;
-        tc_fence_after();
-        const uint64_t d_c = desc_sw128(sC + cslot(c) * kRowsBytes);
+      }
+      __syncwarp();
+      return true;
+    };
+    bool ok = chunks == 0 || issue_g(0);
+#pragma unroll 1
+    for (int c = 0; ok && c < chunks; ++c) {
+      // C S (S of the chunk before, Y and dS read)
+      if (!(ok = wait.warp(bar(kSFull), c) && (c == 0 || wait.warp(bar(kYRead), c - 1)))) break;
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll 2
         for (int k = 0; k < ksteps; ++k)
           mma_bf16(t_y1, d_c + kk(k), d_s + k * (512 >> 4), id_y, k > 0);
         mma_commit(bar(kY1Done));
-        mma_commit(bar(kCFree + cslot(c)));
-        // dS
-        if (!(ok = wait.one(bar(kWFull), c))) break;
-        tc_fence_after();
-        const uint64_t d_bt = desc_t128(sB + (c & 1) * kRowsBytes, kRowsBytes / 2);
-#pragma unroll
-        for (int piece = 2; piece >= 0; --piece) {
-          const uint64_t d_w = desc_t32(sW + piece * x_bytes);
-#pragma unroll
-          for (int k = 0; k < kQ / 16; ++k)
-            mma_bf16(t_ds, d_bt + k * (2048 >> 4), d_w + k * (512 >> 4), id_ds,
-                     piece < 2 || k > 0);
-        }
+        mma_commit(bar(kCFree));
+      }
+      __syncwarp();
+      // dS
+      if (!(ok = wait.warp(bar(kWFull), c))) break;
+      tc_fence_after();
+      if (elect_one()) {
+        issue_ds(t_ds, desc_t128(sB + (c & 1) * kRowsBytes, kRowsBytes / 2), d_w, piece, id_ds);
         mma_commit(bar(kDsDone));
         mma_commit(bar(kBFree + (c & 1)));
-        // M X
-        if (!(ok = wait.one(bar(kMFull), c) && wait.one(bar(kXFull), c))) break;
-        tc_fence_after();
-#pragma unroll
+      }
+      __syncwarp();
+      // M X
+      if (!(ok = wait.warp(bar(kMFull), c))) break;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t d_x = desc_t32(sX + (c & 1) * x_bytes);
+#pragma unroll 2
         for (int k = 0; k < kQ / 16; ++k)
           mma_bf16_ts(t_y2, tmem + kColM + 8 * k, d_x + k * (512 >> 4), id_y, k > 0);
         mma_commit(bar(kYDone));
-        if (c + 1 < chunks) ok = issue_g(c + 1);
       }
-      // no product may still run when the tensor memory is freed: after a
-      // timeout, wait on a barrier nothing else completes any more
-      if (!ok) {
-        mbar_init(bar(kTail), 1);
-        mma_commit(bar(kTail));
-        mbar_wait(bar(kTail), 0);
+      __syncwarp();
+      if (c + 1 < chunks) ok = issue_g(c + 1);
+    }
+    // no product may still run when the tensor memory is freed: after a
+    // timeout, wait on a barrier of their own
+    if (!ok) {
+      if (elect_one()) {
+        mbar_init(bar(kBars), 1);
+        mma_commit(bar(kBars));
       }
+      __syncwarp();
+      mbar_wait(bar(kBars), 0);
     }
   } else if (warp == kWarpCopy) {
-    // ---- B and C ----
+    // ---- B, C, X in and Y out ----
     const int boxes = N > 64 ? 2 : 1;
     const uint32_t bytes = boxes * (kRowsBytes / 2);
-    int c = 0;
-    for (; c < chunks; ++c) {
-      const int row = static_cast<int>(part.begin) + c * kQ;
-      const int left = static_cast<int>(rows - static_cast<int64_t>(c) * kQ);
-      const int bs = c & 1, cs = tp.cbufs == 2 ? c & 1 : 0, cu = tp.cbufs == 2 ? c >> 1 : c;
+    bool ok = true;
+    auto put_y = [&](int c) {  // chunk c's Y; full chunks only
+      if (tp.otma && rows - c * kQ >= kQ) {
+        if (lane == 0) {
+          for (int i = 0; i < atoms && 16 * i < pw; ++i)
+            tma_store_3d(&tm_o, sX + (c & 1) * x_bytes + i * kAtomBytes, col0 + 16 * i, h,
+                         static_cast<int>(part.begin) + c * kQ);
+          bulk_commit();
+          bulk_wait_read();
+        }
+        __syncwarp();
+      }
+    };
+#pragma unroll 1
+    for (int c = 0; c < chunks; ++c) {
+      const int row = static_cast<int>(part.begin) + c * kQ, left = rows - c * kQ;
+      const int slot = c & 1;
       const bool tail = left < kQ;
-      const uint32_t b_at = sB + bs * kRowsBytes, c_at = sC + cs * kRowsBytes;
-      if (c >= 2 && !wait.warp(bar(kBFree + bs), (c >> 1) - 1)) break;
+      const uint32_t b_at = sB + slot * kRowsBytes;
+      if (c >= 2 && !(ok = wait.warp(bar(kBFree + slot), (c >> 1) - 1))) break;
       if (lane == 0) {
-        const uint32_t to = bar(tail ? static_cast<int>(kTail) : kBFull + bs);
+        const uint32_t to = bar(tail ? static_cast<int>(kTail) : kBFull + slot);
         mbar_expect_tx(to, bytes);
         for (int i = 0; i < boxes; ++i)
           tma_load_3d(b_at + i * (kRowsBytes / 2), &tm_b, 64 * i, g, row, to);
       }
-      const bool c_free = cu == 0 || wait.warp(bar(kCFree + cs), cu - 1);
-      if (c_free && lane == 0) {
-        mbar_expect_tx(bar(kCFull + cs), bytes);
+      if (c >= 2) {
+        if (!(ok = wait.warp(bar(kYPut + slot), (c >> 1) - 1))) break;
+        put_y(c - 2);
+      }
+      if (lane == 0) {
+        if (tp.xtma) {
+          mbar_expect_tx(bar(kXLand + slot), x_bytes);
+          for (int i = 0; i < atoms; ++i)
+            tma_load_3d(sX + slot * x_bytes + i * kAtomBytes, &tm_x, col0 + 16 * i, h, row,
+                        bar(kXLand + slot));
+        } else {
+          mbar_arrive(bar(kXLand + slot));  // the place is free: the X warps load it
+        }
+      }
+      if (c >= 1 && !(ok = wait.warp(bar(kCFree), c - 1))) break;
+      if (lane == 0) {
+        mbar_expect_tx(bar(kCFull), bytes);
         for (int i = 0; i < boxes; ++i)
-          tma_load_3d(c_at + i * (kRowsBytes / 2), &tm_c, 64 * i, g, row, bar(kCFull + cs));
+          tma_load_3d(sC + i * (kRowsBytes / 2), &tm_c, 64 * i, g, row, bar(kCFull));
       }
       if (tail) {
         // rows of other sequences, or of none, count for nothing, whatever
         // they hold
-        const bool landed = wait.warp(bar(kTail), 0);
-        if (!landed) break;
+        if (!(ok = wait.warp(bar(kTail), 0))) break;
         for (int i = lane; i < (kQ - left) * 8; i += 32)
           for (int j = 0; j < boxes; ++j)
             sts16(b_at + j * (kRowsBytes / 2) + left * 128 + i * 16, make_uint4(0, 0, 0, 0));
         fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBFull + bs));
+        warp_arrive(bar(kBFull + slot));
       }
-      if (!c_free) break;
     }
-    // after a timeout, copies may still be on their way: give them the time of
-    // another wait (they target this CTA's shared memory)
-    if (c < chunks)
-      for (int i = 0; i < 2; ++i) {
-        mbar_wait(bar(kBFull + i), ((c + 1 - i) >> 1) & 1u ^ 1u);
-        mbar_wait(bar(kCFull + i), ((c + 1 - i) >> 1) & 1u ^ 1u);
-      }
+    for (int c = chunks > 2 ? chunks - 2 : 0; ok && c < chunks; ++c)
+      if ((ok = wait.warp(bar(kYPut + (c & 1)), c >> 1))) put_y(c);
+    if (!ok) {
+      // copies may still be on their way into this CTA's shared memory: the
+      // time of a bounded wait (on a barrier that nothing completes) is theirs
+      if (lane == 0) mbar_init(bar(kTail), 1);
+      __syncwarp();
+      mbar_wait(bar(kTail), 0);
+    }
   } else if (warp == kWarpDt) {
     // ---- the decays, chunks ahead ----
     const float a2 = __ldg(p.a + h) * kLog2e;
@@ -457,15 +487,16 @@ __global__ void __launch_bounds__(kMainThreads, 1)
     auto fetch = [&](int c) {
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        const int64_t t = static_cast<int64_t>(c) * kQ + 32 * b + lane;
+        const int t = c * kQ + 32 * b + lane;
         raw[b] = t < rows ? Bf::load1(dtp + t * p.dts, 0) : 0.0f;
       }
     };
-    if (chunks > 0) fetch(0);
+    fetch(0);
     int slot = 0, use = 0;
+#pragma unroll 1
     for (int c = 0; c < chunks; ++c) {
       float pre[4], suf[4], tot[4], dt[4];
-      make_decays(raw, rows - static_cast<int64_t>(c) * kQ, bias, a2, p, pre, suf, dt, tot);
+      make_decays(raw, rows - c * kQ, bias, a2, p, pre, suf, dt, tot);
       if (c + 1 < chunks) fetch(c + 1);
       if (use > 0 && !wait.warp(bar(kDtFree + slot), use - 1)) break;
       float* s = s_decay + slot * kDecayFloats;
@@ -485,57 +516,59 @@ __global__ void __launch_bounds__(kMainThreads, 1)
         if (lane == 0) s[5 * kQ + b] = tot[b];
       }
       if (lane == 0) s[5 * kQ + 4] = ex2_approx(before);
-      mbar_arrive(bar(kDtFull + slot));
+      warp_arrive(bar(kDtFull + slot));
       if (++slot == kDecays) slot = 0, ++use;
     }
   } else if (warp < kWarpM) {
-    // ---- X and the pieces of w X ----
+    // ---- the pieces of w X: row 64 (i & 1) + r0 of atom i / 2 ----
+    const int r0 = tid >> 1, col8 = (tid & 1) * 8;
+    const uint32_t at0 = atom_at(r0, tid & 1);
     const __nv_bfloat16* xg = static_cast<const __nv_bfloat16*>(p.x) + part.begin * p.xs + hcol;
-    const int r0 = tid >> 1, col8 = (tid & 1) * 8;  // row 64 (i & 1) + r0 of atom i / 2
-    uint4 xr[kXPieces];
-    auto fetch = [&](int c) {
-#pragma unroll
-      for (int i = 0; i < kXPieces; ++i) {
-        const int64_t t = static_cast<int64_t>(c) * kQ + (i & 1) * 64 + r0;
-        const int col = (i >> 1) * 16 + col8;
-        xr[i] = t < rows && col < pw ? load_x(xg + t * p.xs + col, col, pw, tp.xvec)
-                                     : make_uint4(0, 0, 0, 0);
-      }
-    };
-    if (chunks > 0) fetch(0);
     int slot = 0, use = 0;
+#pragma unroll 1
     for (int c = 0; c < chunks; ++c) {
-      if (!wait.warp(bar(kDtFull + slot), use)) break;
-      const float* sw = s_decay + slot * kDecayFloats + 3 * kQ;
-      const float w0 = sw[r0], w1 = sw[64 + r0];
-      if (c > 0 && !wait.warp(bar(kDsDone), c - 1)) break;
-      const uint32_t at0 = atom_at(r0, tid & 1);  // row 64 + r0: 8 groups further
-#pragma unroll
-      for (int i = 0; i < kXPieces; ++i) {
-        if (i < 2 * atoms) {
-          uint4 u[3];
-          pieces_of(xr[i], i & 1 ? w1 : w0, u);
-          const uint32_t at = sW + (i >> 1) * kAtomBytes + (i & 1) * 2048 + at0;
-#pragma unroll
-          for (int k = 0; k < 3; ++k) sts16(at + k * x_bytes, u[k]);
+      const uint32_t x_at = sX + (c & 1) * x_bytes + at0;
+      const int left = rows - c * kQ;
+      if (!wait.warp(bar(kXLand + (c & 1)), c >> 1)) break;
+      if (!tp.xtma || left < kQ) {
+        // (re)load what the copies do not give: rows behind the sequence count
+        // for nothing, whatever they hold
+#pragma unroll 1
+        for (int i = 0; i < 2 * atoms; ++i) {
+          const int r = (i & 1) * 64 + r0, col = (i >> 1) * 16 + col8;
+          if (r >= left) sts16(x_at + i * 2048, make_uint4(0, 0, 0, 0));
+          else if (!tp.xtma)
+            sts16(x_at + i * 2048,
+                  load_x(xg + static_cast<int64_t>(c * kQ + r) * p.xs + col, col, pw));
         }
       }
-      fence_async_smem();
-      mbar_arrive(bar(kWFull));
-      if (c > 0 && !wait.warp(bar(kYRead), c - 1)) break;
+      if (!wait.warp(bar(kDtFull + slot), use)) break;
+      const float* sw = s_decay + slot * kDecayFloats + 3 * kQ + r0;
+      const float w0 = sw[0], w1 = sw[64];
+      if (c > 0 && !wait.warp(bar(kDsDone), c - 1)) break;
+      uint32_t at = at0;
+#pragma unroll 1
+      for (int i = 0; i < atoms; ++i, at += kAtomBytes) {
+        const uint4 xa = lds16(sX + (c & 1) * x_bytes + at);
+        const uint4 xb = lds16(sX + (c & 1) * x_bytes + at + 2048);
+        uint4 u[3];
+        pieces_of(xa, w0, u);
 #pragma unroll
-      for (int i = 0; i < kXPieces; ++i)
-        if (i < 2 * atoms) sts16(sX + (i >> 1) * kAtomBytes + (i & 1) * 2048 + at0, xr[i]);
+        for (int k = 0; k < 3; ++k) sts16(sW + at + k * x_bytes, u[k]);
+        pieces_of(xb, w1, u);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) sts16(sW + at + 2048 + k * x_bytes, u[k]);
+      }
       fence_async_smem();
-      mbar_arrive(bar(kXFull));
-      if (c + 1 < chunks) fetch(c + 1);
+      warp_arrive(bar(kWFull));
       if (++slot == kDecays) slot = 0, ++use;
     }
   } else if (warp < kWarpSY) {
-    // ---- M of rows 32 q + lane ----
-    const int q = warp & 3;
+    // ---- M of rows 32 q + lane, column blocks hf and hf + 2 ----
+    const int q = warp & 3, hf = (warp >> 2) & 1;
     const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
     int slot = 0, use = 0;
+#pragma unroll 1
     for (int c = 0; c < chunks; ++c) {
       if (!wait.warp(bar(kDtFull + slot), use)) break;
       const float* sd = s_decay + slot * kDecayFloats;
@@ -544,60 +577,71 @@ __global__ void __launch_bounds__(kMainThreads, 1)
       // the M before is read (by the same commit as Y's)
       if (c > 0 && !wait.warp(bar(kYDone), c - 1)) break;
       tc_fence_after();
-      float between = pre;  // row prefix + the blocks between
+#pragma unroll 1
+      for (int blk = hf; blk < 4; blk += 2) {
+        const float* sj = sd + 32 * blk;
+        const uint32_t t_g = tmem + lanes + kColG + 32 * blk, t_m = tmem + lanes + kColM + 16 * blk;
+        uint32_t m[8];
+        if (blk < q) {
+          float between = pre;  // row prefix + the blocks between
+          for (int b = blk + 1; b < q; ++b) between += sd[5 * kQ + b];
+          const float f = ex2_approx(between);
+#pragma unroll 1
+          for (int j = 0; j < 32; j += 16) {
+            uint32_t gr[16];
+            tmem_ld16(t_g + j, gr);
 #pragma unroll
-      for (int blk = 3; blk >= 0; --blk) {
-        uint32_t m[16];
-        if (blk > q) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) m[j] = 0;
-        } else {
-          uint32_t gr[32];
-          tmem_ld32_nowait(tmem + lanes + kColG + 32 * blk, gr);
-          if (blk == q) {
-            tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-              const float4 pj = *reinterpret_cast<const float4*>(sd + 32 * blk + j);
-              const float4 dj = *reinterpret_cast<const float4*>(sd + 2 * kQ + 32 * blk + j);
-              const float v0 = __uint_as_float(gr[j]) * (dj.x * ex2_approx(pre - pj.x));
-              const float v1 = __uint_as_float(gr[j + 1]) * (dj.y * ex2_approx(pre - pj.y));
-              const float v2 = __uint_as_float(gr[j + 2]) * (dj.z * ex2_approx(pre - pj.z));
-              const float v3 = __uint_as_float(gr[j + 3]) * (dj.w * ex2_approx(pre - pj.w));
-              m[j / 2] = Bf::pack2(j <= lane ? v0 : 0.0f, j + 1 <= lane ? v1 : 0.0f);
-              m[j / 2 + 1] = Bf::pack2(j + 2 <= lane ? v2 : 0.0f, j + 3 <= lane ? v3 : 0.0f);
-            }
-          } else {
-            const float f = ex2_approx(between);
-            between += sd[5 * kQ + blk];
-            tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-              const float4 cf = *reinterpret_cast<const float4*>(sd + kQ + 32 * blk + j);
+            for (int e = 0; e < 16; e += 4) {
+              const float4 cf = *reinterpret_cast<const float4*>(sj + kQ + j + e);
               float v0, v1, v2, v3;
               mul2(v0, v1, cf.x, cf.y, f, f);
               mul2(v2, v3, cf.z, cf.w, f, f);
-              mul2(v0, v1, v0, v1, __uint_as_float(gr[j]), __uint_as_float(gr[j + 1]));
-              mul2(v2, v3, v2, v3, __uint_as_float(gr[j + 2]), __uint_as_float(gr[j + 3]));
-              m[j / 2] = Bf::pack2(v0, v1);
-              m[j / 2 + 1] = Bf::pack2(v2, v3);
+              mul2(v0, v1, v0, v1, __uint_as_float(gr[e]), __uint_as_float(gr[e + 1]));
+              mul2(v2, v3, v2, v3, __uint_as_float(gr[e + 2]), __uint_as_float(gr[e + 3]));
+              m[e / 2] = Bf::pack2(v0, v1);
+              m[e / 2 + 1] = Bf::pack2(v2, v3);
             }
+            tmem_st8(t_m + j / 2, m);
           }
+        } else if (blk == q) {
+#pragma unroll 1
+          for (int j = 0; j < 32; j += 16) {
+            uint32_t gr[16];
+            tmem_ld16(t_g + j, gr);
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+              const float4 pj = *reinterpret_cast<const float4*>(sj + j + e);
+              const float4 dj = *reinterpret_cast<const float4*>(sj + 2 * kQ + j + e);
+              const int k = lane - j - e;  // columns up to the row's own
+              const float v0 = __uint_as_float(gr[e]) * (dj.x * ex2_approx(pre - pj.x));
+              const float v1 = __uint_as_float(gr[e + 1]) * (dj.y * ex2_approx(pre - pj.y));
+              const float v2 = __uint_as_float(gr[e + 2]) * (dj.z * ex2_approx(pre - pj.z));
+              const float v3 = __uint_as_float(gr[e + 3]) * (dj.w * ex2_approx(pre - pj.w));
+              m[e / 2] = Bf::pack2(k >= 0 ? v0 : 0.0f, k >= 1 ? v1 : 0.0f);
+              m[e / 2 + 1] = Bf::pack2(k >= 2 ? v2 : 0.0f, k >= 3 ? v3 : 0.0f);
+            }
+            tmem_st8(t_m + j / 2, m);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) m[j] = 0;
+          tmem_st8(t_m, m);
+          tmem_st8(t_m + 8, m);
         }
-        tmem_st16(tmem + lanes + kColM + 16 * blk, m);
       }
+      tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(bar(kMFull));
+      warp_arrive(bar(kMFull));
       if (++slot == kDecays) slot = 0, ++use;
     }
   } else {
-    // ---- S and Y: lanes 32 q.., atoms hf, hf + 2, .. ----
-    const int q = warp & 3, hf = (warp >> 2) & 1, n = 32 * q + lane;
+    // ---- S and Y: lanes 32 q.., atoms hf, hf + 4 ----
+    const int q = warp & 3, hf = ((warp - kWarpSY) >> 2), n = 32 * q + lane;
     const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
     const float dskip = p.d ? __ldg(p.d + h) : 0.0f;
     const int64_t slot_at = seq_slot(p.q, part.seq);
     const int64_t PN = static_cast<int64_t>(P) * N;
-    float s[kSYAtoms][16];  // S^T: row n, columns 16 (hf + 2 k) + j
+    float s[kSYAtoms][16];  // S^T: row n, columns 16 (hf + 4 k) + j
     const float* from = nullptr;
     if (part.count > 1) from = p.ws + (part.place * p.H + h) * PN;
     else if (slot_at >= 0 && seq_resumes(p.q, part.seq))
@@ -608,12 +652,12 @@ __global__ void __launch_bounds__(kMainThreads, 1)
       for (int ck = 0; ck < 2; ++ck) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = s[k][8 * ck + j];
-        sts16(sS + (hf + 2 * k) * kAtomBytes + atom_at(n, ck), Bf::pack(v));
+        sts16(sS + (hf + kSYShare * k) * kAtomBytes + atom_at(n, ck), Bf::pack(v));
       }
     };
 #pragma unroll
     for (int k = 0; k < kSYAtoms; ++k) {
-      const int a = hf + 2 * k;
+      const int a = hf + kSYShare * k;
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
         const int col = a * 16 + j;
@@ -623,22 +667,19 @@ __global__ void __launch_bounds__(kMainThreads, 1)
       if (a < atoms) put(k);
     }
     fence_async_smem();
-    mbar_arrive(bar(kSFull));
+    warp_arrive(bar(kSFull));
     const int i = n;  // the row of Y
-    __nv_bfloat16* orow =
-        static_cast<__nv_bfloat16*>(p.out) + (part.begin + i) * p.os + hcol;
-    const int64_t ostep = static_cast<int64_t>(kQ) * p.os;
     int slot = 0, use = 0;
-    for (int c = 0; c < chunks; ++c, orow += ostep) {
+#pragma unroll 1
+    for (int c = 0; c < chunks; ++c) {
       if (!wait.warp(bar(kDtFull + slot), use)) break;
       const float* sd = s_decay + slot * kDecayFloats;
-      if (!wait.warp(bar(kDsDone), c)) break;
-      if (!wait.warp(bar(kY1Done), c)) break;
-      tc_fence_after();
       const float decay = sd[5 * kQ + 4], e = sd[4 * kQ + i];
+      if (!wait.warp(bar(kDsDone), c) || !wait.warp(bar(kY1Done), c)) break;
+      tc_fence_after();
 #pragma unroll
       for (int k = 0; k < kSYAtoms; ++k) {
-        const int a = hf + 2 * k;
+        const int a = hf + kSYShare * k;
         if (a < atoms) {
           uint32_t r[16];
           tmem_ld16(t_ds + lanes + a * 16, r);
@@ -651,43 +692,45 @@ __global__ void __launch_bounds__(kMainThreads, 1)
       }
       fence_async_smem();
       tc_fence_before();
-      mbar_arrive(bar(kSFull));
+      warp_arrive(bar(kSFull));
       if (!wait.warp(bar(kYDone), c)) break;
       tc_fence_after();
-      const bool valid = i < rows - static_cast<int64_t>(c) * kQ;
+      const int left = rows - c * kQ;
+      const bool stage = tp.otma && left >= kQ;  // Y into X's place, stored from there
+      __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.out) +
+                            (part.begin + c * kQ + i) * p.os + hcol;
+#pragma unroll 1
+      for (int a2 = 2 * hf; a2 < 2 * atoms; a2 += a2 & 1 ? 2 * kSYShare - 1 : 1) {
+        const uint32_t at = sX + (c & 1) * x_bytes + (a2 >> 1) * kAtomBytes + atom_at(i, a2 & 1);
+        uint32_t y1[8], y2[8];
+        tmem_ld8(t_y1 + lanes + a2 * 8, y1);
+        tmem_ld8(t_y2 + lanes + a2 * 8, y2);
+        float xv[8], y[8];
+        Bf::unpack(lds16(at), xv);
+        tmem_ld_wait();
 #pragma unroll
-      for (int k = 0; k < kSYAtoms; ++k) {
-        const int a = hf + 2 * k;
-        if (a >= atoms) continue;
-        uint32_t y1[16], y2[16];
-        tmem_ld16(t_y1 + lanes + a * 16, y1);
-        tmem_ld16(t_y2 + lanes + a * 16, y2);
-#pragma unroll
-        for (int ck = 0; ck < 2; ++ck) {
-          float xv[8], y[8];
-          Bf::unpack(lds16(sX + a * kAtomBytes + atom_at(i, ck)), xv);
-#pragma unroll
-          for (int j = 0; j < 8; j += 2) {
-            fma2(y[j], y[j + 1], __uint_as_float(y1[8 * ck + j]),
-                 __uint_as_float(y1[8 * ck + j + 1]), e, e, __uint_as_float(y2[8 * ck + j]),
-                 __uint_as_float(y2[8 * ck + j + 1]));
-            fma2(y[j], y[j + 1], xv[j], xv[j + 1], dskip, dskip, y[j], y[j + 1]);
-          }
-          const int col = a * 16 + ck * 8;
-          if (valid && col < pw) {
-            const uint4 v = Bf::pack(y);
-            if (tp.ovec) {
-              *reinterpret_cast<uint4*>(orow + col) = v;
-            } else {
-              *reinterpret_cast<uint2*>(orow + col) = make_uint2(v.x, v.y);
-              if (col + 4 < pw) *reinterpret_cast<uint2*>(orow + col + 4) = make_uint2(v.z, v.w);
-            }
-          }
+        for (int j = 0; j < 8; j += 2) {
+          fma2(y[j], y[j + 1], __uint_as_float(y1[j]), __uint_as_float(y1[j + 1]), e, e,
+               __uint_as_float(y2[j]), __uint_as_float(y2[j + 1]));
+          fma2(y[j], y[j + 1], xv[j], xv[j + 1], dskip, dskip, y[j], y[j + 1]);
+        }
+        const uint4 v = Bf::pack(y);
+        const int col = a2 * 8;
+        if (stage) {
+          sts16(at, v);
+        } else if (i < left && col < pw) {
+          *reinterpret_cast<uint2*>(orow + col) = make_uint2(v.x, v.y);
+          if (col + 4 < pw) *reinterpret_cast<uint2*>(orow + col + 4) = make_uint2(v.z, v.w);
         }
       }
+      fence_async_smem();
       tc_fence_before();
-      mbar_arrive(bar(kYRead));
-      mbar_arrive(bar(kDtFree + slot));
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar(kYRead));
+        mbar_arrive(bar(kYPut + (c & 1)));
+        mbar_arrive(bar(kDtFree + slot));
+      }
       if (++slot == kDecays) slot = 0, ++use;
     }
     // the state after the part's last row
@@ -697,8 +740,9 @@ __global__ void __launch_bounds__(kMainThreads, 1)
       for (int k = 0; k < kSYAtoms; ++k)
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          const int col = (hf + 2 * k) * 16 + j;
-          if (hf + 2 * k < atoms && col < pw) to[static_cast<int64_t>(col0 + col) * N + n] = s[k][j];
+          const int col = (hf + kSYShare * k) * 16 + j;
+          if (hf + kSYShare * k < atoms && col < pw)
+            to[static_cast<int64_t>(col0 + col) * N + n] = s[k][j];
         }
     }
   }
@@ -712,16 +756,17 @@ __global__ void __launch_bounds__(kMainThreads, 1)
 
 // ---------------------------------------------------------------------------
 // k_scan_tc_state: the state a part adds from a zero start, and its decay (a
-// cut sequence's parts but the last).  Two CTAs per SM, whose stages overlap:
-// 8 warps write the pieces of w X and B, one thread issues dS, the 8 warps add
-// it to S in registers.
+// cut sequence's parts but the last; all their chunks are full).  Two CTAs per
+// SM, whose stages overlap: one warp copies B and X (into the place of the
+// largest piece of w X), 8 warps write the pieces, one warp issues dS, the 8
+// warps add it to S in registers.
 // ---------------------------------------------------------------------------
-constexpr int kStateThreads = 10 * 32;
+constexpr int kStateThreads = 11 * 32;
 
-__global__ void __launch_bounds__(kStateThreads, 2) k_scan_tc_state(const TcParams tp) {
-  constexpr int NT = 256;                       // threads of the elementwise warps
-  constexpr int AW = kMaxAtoms / 2;             // atoms of a warp
-  constexpr int XI = kMaxAtoms * 256 / NT;      // 16-byte pieces of X of a thread
+__global__ void __launch_bounds__(kStateThreads, 2)
+    k_scan_tc_state(const __grid_constant__ CUtensorMap tm_b,
+                    const __grid_constant__ CUtensorMap tm_x, const TcParams tp) {
+  constexpr int AW = (kMaxAtoms + 1) / 2;       // atoms of a warp
   const Params& p = tp.p;
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw_u = smem_u32(smem_raw);
@@ -731,17 +776,19 @@ __global__ void __launch_bounds__(kStateThreads, 2) k_scan_tc_state(const TcPara
   const uint32_t x_bytes = atoms * kAtomBytes;
   const uint32_t sB = base_u, sW = sB + kRowsBytes;
   const uint32_t decay_off = kRowsBytes + 3 * x_bytes;
-  float* s_decay = reinterpret_cast<float*>(base + decay_off);  // [2][kQ] w, [2] decay
+  float* s_decay = reinterpret_cast<float*>(base + decay_off);  // [2][kQ + 4]: w, decay
   const uint32_t bars_off = decay_off + 2 * (kQ + 4) * 4;
-  volatile uint32_t* s_misc = reinterpret_cast<uint32_t*>(base + bars_off + 32);
-  // per chunk: B landed; w X written (and w read); decays made; dS computed
-  const uint32_t b_b = base_u + bars_off, b_x = b_b + 8, b_dt = b_b + 16, b_ds = b_b + 24;
+  volatile uint32_t* s_misc = reinterpret_cast<uint32_t*>(base + bars_off + 40);
+  // per chunk: B landed; X landed; w X written; decays made; dS computed
+  const uint32_t b_b = base_u + bars_off, b_x = b_b + 8, b_w = b_b + 16, b_dt = b_b + 24,
+                 b_ds = b_b + 32;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
-    mbar_init(b_b, NT);
-    mbar_init(b_x, NT);
-    mbar_init(b_dt, 32);
+    mbar_init(b_b, 1);
+    mbar_init(b_x, 1);
+    mbar_init(b_w, 8);
+    mbar_init(b_dt, 1);
     mbar_init(b_ds, 1);
     s_misc[1] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -757,34 +804,28 @@ __global__ void __launch_bounds__(kStateThreads, 2) k_scan_tc_state(const TcPara
   const Part part = find_part(p.q, p.part, blockIdx.x);
   const int P = p.P, N = p.N;
   const int h = blockIdx.y;
-  const int col0 = blockIdx.z * tp.tile;
+  const int col0 = blockIdx.z * tp.tile, pw = min(tp.tile, P - col0);
   // (offsets that do not ascend may count more places than there are)
   const bool run = part.seq >= 0 && part.index < part.count - 1 && part.place + 1 < p.places;
-  const int64_t rows = run ? part.end - part.begin : 0;
-  const int chunks = static_cast<int>((rows + kQ - 1) / kQ);
+  const int rows = run ? static_cast<int>(part.end - part.begin) : 0;
+  const int chunks = rows / kQ;
   const Waits wait = {s_misc + 1, tp.fault};
 
   if (!run) {
     // nothing: fall through to the end
   } else if (warp == 8) {
-    if (lane == 0) {
-      const uint32_t id_ds = idesc_bf16(128, tp.tile) | kTransA | kTransB;
-      const uint64_t d_bt = desc_t128(sB, kRowsBytes / 2);
-      for (int c = 0; c < chunks; ++c) {
-        if (!wait.one(b_b, c) || !wait.one(b_x, c)) break;
-        tc_fence_after();
-#pragma unroll
-        for (int piece = 2; piece >= 0; --piece) {
-          const uint64_t d_w = desc_t32(sW + piece * x_bytes);
-#pragma unroll
-          for (int k = 0; k < kQ / 16; ++k)
-            mma_bf16(tmem, d_bt + k * (2048 >> 4), d_w + k * (512 >> 4), id_ds,
-                     piece < 2 || k > 0);
-        }
+    const uint32_t id_ds = idesc_bf16(128, tp.tile) | kTransA | kTransB;
+#pragma unroll 1
+    for (int c = 0; c < chunks; ++c) {
+      if (!wait.warp(b_b, c) || !wait.warp(b_w, c)) break;
+      tc_fence_after();
+      if (elect_one()) {
+        issue_ds(tmem, desc_t128(sB, kRowsBytes / 2), desc_t32(sW), x_bytes >> 4, id_ds);
         mma_commit(b_ds);
-        // (waited for here too, so that none runs when the memory is freed)
-        if (!wait.one(b_ds, c)) break;
       }
+      __syncwarp();
+      // (waited for here too, so that none runs when the memory is freed)
+      if (!wait.warp(b_ds, c)) break;
     }
   } else if (warp == 9) {
     const float a2 = __ldg(p.a + h) * kLog2e;
@@ -793,20 +834,18 @@ __global__ void __launch_bounds__(kStateThreads, 2) k_scan_tc_state(const TcPara
     float raw[4];
     auto fetch = [&](int c) {
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const int64_t t = static_cast<int64_t>(c) * kQ + 32 * b + lane;
-        raw[b] = t < rows ? Bf::load1(dtp + t * p.dts, 0) : 0.0f;
-      }
+      for (int b = 0; b < 4; ++b)
+        raw[b] = Bf::load1(dtp + static_cast<int64_t>(c * kQ + 32 * b + lane) * p.dts, 0);
     };
     fetch(0);
     float log_total = 0.0f;
+#pragma unroll 1
     for (int c = 0; c < chunks; ++c) {
       float pre[4], suf[4], tot[4], dt[4];
-      const float total =
-          make_decays(raw, rows - static_cast<int64_t>(c) * kQ, bias, a2, p, pre, suf, dt, tot);
+      const float total = make_decays(raw, kQ, bias, a2, p, pre, suf, dt, tot);
       if (c + 1 < chunks) fetch(c + 1);
       // this half was last read for chunk c - 2 (each phase waited for in turn)
-      if (c >= 1 && !wait.warp(b_x, c - 1)) break;
+      if (c >= 1 && !wait.warp(b_w, c - 1)) break;
       float* s = s_decay + (c & 1) * (kQ + 4);
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
@@ -817,83 +856,80 @@ __global__ void __launch_bounds__(kStateThreads, 2) k_scan_tc_state(const TcPara
       }
       if (lane == 0) s[kQ] = ex2_approx(total);
       log_total += total;
-      mbar_arrive(b_dt);
+      warp_arrive(b_dt);
     }
     if (lane == 0 && blockIdx.z == 0) p.ws_decay[part.place * p.H + h] = ex2_approx(log_total);
+  } else if (warp == 10) {
+    const int boxes = N > 64 ? 2 : 1, g = h / p.hpg;
+    const uint32_t bytes = boxes * (kRowsBytes / 2);
+    bool ok = true;
+#pragma unroll 1
+    for (int c = 0; c < chunks; ++c) {
+      const int row = static_cast<int>(part.begin) + c * kQ;
+      if (c > 0 && !(ok = wait.warp(b_ds, c - 1))) break;
+      if (lane == 0) {
+        if (tp.xtma) {
+          mbar_expect_tx(b_x, x_bytes);
+          for (int i = 0; i < atoms; ++i)
+            tma_load_3d(sW + i * kAtomBytes, &tm_x, col0 + 16 * i, h, row, b_x);
+        } else {
+          mbar_arrive(b_x);
+        }
+        mbar_expect_tx(b_b, bytes);
+        for (int i = 0; i < boxes; ++i)
+          tma_load_3d(sB + i * (kRowsBytes / 2), &tm_b, 64 * i, g, row, b_b);
+      }
+    }
+    // every copy has landed before the CTA leaves
+    if (ok) wait.warp(b_b, chunks - 1);
   } else {
     const int q = warp & 3, hf = warp >> 2, n = 32 * q + lane;
     const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
-    const int g = h / p.hpg, pw = min(tp.tile, P - col0);
-    const __nv_bfloat16* xg = static_cast<const __nv_bfloat16*>(p.x) + part.begin * p.xs +
-                              static_cast<int64_t>(h) * P + col0;
-    const __nv_bfloat16* bg =
-        static_cast<const __nv_bfloat16*>(p.b) + part.begin * p.bs + static_cast<int64_t>(g) * N;
-    auto load_b = [&](int c) {
-#pragma unroll
-      for (int it = 0; it < 2048 / NT; ++it) {
-        const int id = it * NT + tid, r = id >> 4, ch = id & 15;
-        const int64_t t = static_cast<int64_t>(c) * kQ + r;
-        const bool valid = t < rows && ch * 8 < N;
-        cp_async16(sB + (ch >> 3) * (kRowsBytes / 2) + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
-                   valid ? bg + t * p.bs + ch * 8 : bg, valid);
-      }
-    };
-    uint4 xr[XI];
-    auto fetch = [&](int c) {
-#pragma unroll
-      for (int it = 0; it < XI; ++it) {
-        const int id = it * NT + tid;
-        const int64_t t = static_cast<int64_t>(c) * kQ + ((id & 255) >> 1);
-        const int col = (id >> 8) * 16 + (id & 1) * 8;
-        xr[it] = t < rows && col < pw ? load_x(xg + t * p.xs + col, col, pw, tp.xvec)
-                                      : make_uint4(0, 0, 0, 0);
-      }
-    };
+    const int r = tid >> 1, col8 = (tid & 1) * 8;  // row r of each atom
+    const uint32_t at0 = sW + atom_at(r, tid & 1);
+    const __nv_bfloat16* xg = static_cast<const __nv_bfloat16*>(p.x) + (part.begin + r) * p.xs +
+                              static_cast<int64_t>(h) * P + col0 + col8;
     float s[AW][16];
 #pragma unroll
     for (int k = 0; k < AW; ++k)
 #pragma unroll
       for (int j = 0; j < 16; ++j) s[k][j] = 0.0f;
-    load_b(0);
-    fetch(0);
+#pragma unroll 1
     for (int c = 0; c < chunks; ++c) {
       const float* sd = s_decay + (c & 1) * (kQ + 4);
       if (!wait.warp(b_dt, c)) break;
-      const float w = sd[(tid & 255) >> 1], decay = sd[kQ];
-      const uint32_t at0 = atom_at((tid & 255) >> 1, tid & 1);
+      const float w = sd[r], decay = sd[kQ];
+      if (!wait.warp(b_x, c)) break;
+#pragma unroll 1
+      for (int i = 0; i < atoms; ++i) {
+        const uint32_t at = at0 + i * kAtomBytes;
+        uint4 u[3];
+        pieces_of(tp.xtma ? lds16(at)
+                          : load_x(xg + static_cast<int64_t>(c * kQ) * p.xs + 16 * i,
+                                   16 * i + col8, pw),
+                  w, u);
 #pragma unroll
-      for (int it = 0; it < XI; ++it) {
-        if (it < atoms) {
-          uint4 u[3];
-          pieces_of(xr[it], w, u);
-#pragma unroll
-          for (int k = 0; k < 3; ++k) sts16(sW + k * x_bytes + it * kAtomBytes + at0, u[k]);
-        }
+        for (int k = 0; k < 3; ++k) sts16(at + k * x_bytes, u[k]);
       }
-      cp_async_wait();
       fence_async_smem();
       tc_fence_before();
-      mbar_arrive(b_b);
-      mbar_arrive(b_x);
-      if (c + 1 < chunks) fetch(c + 1);
+      warp_arrive(b_w);
       if (!wait.warp(b_ds, c)) break;
       tc_fence_after();
-      if (c + 1 < chunks) load_b(c + 1);
 #pragma unroll
       for (int k = 0; k < AW; ++k) {
         const int a = hf + 2 * k;
         if (a < atoms) {
-          uint32_t r[16];
-          tmem_ld16(tmem + lanes + a * 16, r);
+          uint32_t v[16];
+          tmem_ld16(tmem + lanes + a * 16, v);
 #pragma unroll
           for (int j = 0; j < 16; j += 2)
-            fma2(s[k][j], s[k][j + 1], s[k][j], s[k][j + 1], decay, decay, __uint_as_float(r[j]),
-                 __uint_as_float(r[j + 1]));
+            fma2(s[k][j], s[k][j + 1], s[k][j], s[k][j + 1], decay, decay, __uint_as_float(v[j]),
+                 __uint_as_float(v[j + 1]));
         }
       }
       tc_fence_before();
     }
-    cp_async_wait();
     float* to = p.ws + ((part.place + 1) * p.H + h) * static_cast<int64_t>(P) * N;
     if (n < N) {
 #pragma unroll
@@ -916,16 +952,13 @@ __global__ void __launch_bounds__(kStateThreads, 2) k_scan_tc_state(const TcPara
 // ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
-constexpr uint32_t kSmemMost = 227 * 1024;
-uint32_t main_smem(int tile, int cbufs) {
-  return 1024 + (2 + cbufs) * kRowsBytes + 5 * (tile / 16 * kAtomBytes) +
-         kDecays * kDecayFloats * 4 + 8 * kBars + 8;
+uint32_t main_smem(int tile) {
+  return 1024 + 3 * kRowsBytes + 6 * (tile / 16 * kAtomBytes) + kDecays * kDecayFloats * 4 +
+         8 * kBars + 16;
 }
 uint32_t state_smem(int tile) {
-  return 1024 + kRowsBytes + 3 * (tile / 16 * kAtomBytes) + 2 * (kQ + 4) * 4 + 32 + 8;
+  return 1024 + kRowsBytes + 3 * (tile / 16 * kAtomBytes) + 2 * (kQ + 4) * 4 + 40 + 8;
 }
-// C twice where it fits (tiles of up to 64 columns).
-int cbufs_of(int tile) { return main_smem(tile, 2) <= kSmemMost ? 2 : 1; }
 
 int tile_of(int64_t P) {
   const int64_t tiles = (P + 16 * kMaxAtoms - 1) / (16 * kMaxAtoms);
@@ -937,7 +970,7 @@ cudaError_t allow_smem() {
   static cudaError_t err = cudaSuccess;
   std::call_once(once, [] {
     err = cudaFuncSetAttribute(k_scan_tc, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               static_cast<int>(kSmemMost));
+                               static_cast<int>(main_smem(16 * kMaxAtoms)));
     if (err == cudaSuccess)
       err = cudaFuncSetAttribute(k_scan_tc_state, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  static_cast<int>(state_smem(16 * kMaxAtoms)));
@@ -945,22 +978,21 @@ cudaError_t allow_smem() {
   return err;
 }
 
-// [rows][groups][N] in boxes of 128 rows and 64 columns: columns behind N and
-// rows behind the buffer read as zeros.
-bool make_map(CUtensorMap* m, const void* ptr, int64_t N, int64_t groups, int64_t rows,
-              int64_t stride) {
+// [rows][blocks][cols] in boxes of 128 rows and `box` columns: columns behind a
+// block's end and rows behind the buffer read as zeros and are not written.
+bool make_map(CUtensorMap* m, const void* ptr, int64_t cols, int64_t blocks, int64_t rows,
+              int64_t stride, uint32_t box, CUtensorMapSwizzle swizzle) {
   EncodeTiled enc = encode_fn();
   if (!enc) return false;
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(groups),
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(blocks),
                               static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(N) * 2,
-                                 static_cast<cuuint64_t>(rows > 1 ? stride : groups * N) * 2};
-  const cuuint32_t box[3] = {64, 1, kQ};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols) * 2,
+                                 static_cast<cuuint64_t>(rows > 1 ? stride : blocks * cols) * 2};
+  const cuuint32_t boxes[3] = {box, 1, kQ};
   const cuuint32_t estr[3] = {1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box,
-             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
-         CUDA_SUCCESS;
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, boxes,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
@@ -969,7 +1001,8 @@ bool make_map(CUtensorMap* m, const void* ptr, int64_t N, int64_t groups, int64_
 // columns in whole 8-byte ones, and rows aligned to those.
 bool tc_covers(const ggrn_scan_call& c) {
   if (c.rows > INT32_MAX / 2 || c.b_row_stride >= int64_t{1} << 38 ||
-      c.c_row_stride >= int64_t{1} << 38)
+      c.c_row_stride >= int64_t{1} << 38 || c.x_row_stride >= int64_t{1} << 38 ||
+      c.out_row_stride >= int64_t{1} << 38)
     return false;  // (what a tensor map holds)
   if (c.dtype != kBF16 || c.state_size % 8 != 0 || c.state_size > 128 || c.head_dim % 4 != 0)
     return false;
@@ -1018,30 +1051,33 @@ int tc_run(const ggrn_scan_call& c, const Params& p, bool cut, cudaStream_t s) {
   tp.fault = device_fault_word();
   if (!tp.fault) return GGRN_ERR_CUDA;
   tp.tile = tile_of(p.P);
-  tp.xvec = p.P % 8 == 0 && mixer::aligned_to(p.x, 16) && p.xs % 8 == 0;
-  tp.ovec = p.P % 8 == 0 && mixer::aligned_to(p.out, 16) && p.os % 8 == 0;
-  tp.cbufs = cbufs_of(tp.tile);
+  tp.xtma = p.P % 8 == 0 && mixer::aligned_to(p.x, 16) && p.xs % 8 == 0;
+  tp.otma = p.P % 8 == 0 && mixer::aligned_to(p.out, 16) && p.os % 8 == 0;
   const cudaError_t e = allow_smem();
   if (e != cudaSuccess) {
     record_cuda_error(e);
     return GGRN_ERR_CUDA;
   }
-  CUtensorMap tm_b, tm_c;
-  std::memset(&tm_b, 0, sizeof(tm_b));
-  std::memset(&tm_c, 0, sizeof(tm_c));
-  if (c.rows > 0 && (!make_map(&tm_b, c.b, c.state_size, c.groups, c.rows, c.b_row_stride) ||
-                     !make_map(&tm_c, c.c, c.state_size, c.groups, c.rows, c.c_row_stride)))
+  CUtensorMap tm[4];
+  std::memset(tm, 0, sizeof(tm));
+  constexpr CUtensorMapSwizzle k128 = CU_TENSOR_MAP_SWIZZLE_128B, k32 = CU_TENSOR_MAP_SWIZZLE_32B;
+  if (c.rows > 0 &&
+      (!make_map(tm, c.b, c.state_size, c.groups, c.rows, c.b_row_stride, 64, k128) ||
+       !make_map(tm + 1, c.c, c.state_size, c.groups, c.rows, c.c_row_stride, 64, k128) ||
+       (tp.xtma && !make_map(tm + 2, c.x, p.P, p.H, c.rows, c.x_row_stride, 16, k32)) ||
+       (tp.otma && !make_map(tm + 3, c.out, p.P, p.H, c.rows, c.out_row_stride, 16, k32))))
     return GGRN_ERR_UNSUPPORTED;
   const dim3 grid(static_cast<unsigned>(p.parts), static_cast<unsigned>(p.H),
                   static_cast<unsigned>((p.P + tp.tile - 1) / tp.tile));
   if (cut) {
-    int st = mixer::launch(k_scan_tc_state, grid, kStateThreads, state_smem(tp.tile), s, tp);
+    int st = mixer::launch(k_scan_tc_state, grid, kStateThreads, state_smem(tp.tile), s, tm[0],
+                           tm[2], tp);
     if (st != GGRN_OK) return st;
     st = launch_join(p, s);
     if (st != GGRN_OK) return st;
   }
-  return mixer::launch(k_scan_tc, grid, kMainThreads, main_smem(tp.tile, tp.cbufs), s, tm_b, tm_c,
-                       tp);
+  return mixer::launch(k_scan_tc, grid, kMainThreads, main_smem(tp.tile), s, tm[0], tm[1], tm[2],
+                       tm[3], tp);
 }
 
 }  // namespace scan

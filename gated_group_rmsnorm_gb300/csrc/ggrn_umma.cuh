@@ -29,6 +29,21 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
+// A box from shared memory to global memory; committed as a group, whose reads
+// of shared memory bulk_wait_read waits for.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int x, int y,
+                                             int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(src), "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
 __device__ __forceinline__ void tmem_alloc(uint32_t slot_smem, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot_smem),
                "r"(ncols)
@@ -53,6 +68,36 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint6
       " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
       : "memory");
+}
+// One lane of a converged warp.  Issue loops run on the whole warp with the
+// instructions under this: the compiler then keeps descriptors in uniform
+// registers (52 to 76 clocks an MMA of M = 128, K = 16, N = 16 to 64 from a loop
+// under it, against 96 under a test of the thread's number).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}"
+               : "=r"(p));
+  return p != 0;
+}
+// The A operand kept by the tensor core from one MMA (FILL) to the next ones
+// of the same A (USE, the last of them LAST): 11 + N / 2 clocks instead of
+// 44 + N / 2 at M = 128, K = 16.
+enum class Keep { kNone, kFill, kUse, kLast };
+template <Keep K>
+__device__ __forceinline__ void mma_bf16_keep(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                              uint32_t idesc, bool accumulate) {
+#define GGRN_MMA_KEEP(USAGE)                                                             \
+  asm volatile(                                                                          \
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"                                      \
+      " tcgen05.mma.cta_group::1.kind::f16.collector::a::" USAGE " [%0], %1, %2, %3, p;\n}" ::"r"( \
+          d_tmem),                                                                       \
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)                    \
+      : "memory")
+  if constexpr (K == Keep::kFill) GGRN_MMA_KEEP("fill");
+  else if constexpr (K == Keep::kUse) GGRN_MMA_KEEP("use");
+  else if constexpr (K == Keep::kLast) GGRN_MMA_KEEP("lastuse");
+  else GGRN_MMA_KEEP("discard");
+#undef GGRN_MMA_KEEP
 }
 // Arrive once on `bar` when every MMA this thread issued so far has completed.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
