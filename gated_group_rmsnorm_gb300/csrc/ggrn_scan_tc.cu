@@ -140,35 +140,66 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
 }
 using Bf = Elem<__nv_bfloat16>;
 
-// The decays of one chunk into shared memory: `raw` holds the raw dt of tokens
-// 32 b + lane, `left` the rows from the chunk's first on.  Returns the sum of
-// the chunk's l.
-__device__ __forceinline__ float make_decays(const float (&raw)[4], int64_t left, float bias,
-                                             float a2, const Params& p, float (&pre)[4],
-                                             float (&suf)[4], float (&dt)[4], float (&tot)[4]) {
+// The decays of one chunk, by one warp: dt of token 32 b + lane comes from
+// `raw[b]` (tokens from `left` on count for nothing), goes through `s_dt`, and
+// lane k takes tokens 4 k .. 4 k + 3, so that the blocks of 32 tokens are
+// runs of 8 lanes.  pre: sums of l from the block's start, suf: to its end;
+// before / after: sums of the blocks before and behind.  Returns the chunk's.
+struct Decays {
+  float dt[4], pre[4], suf[4];
+  float block, before, after;
+};
+__device__ __forceinline__ float make_decays(const float (&raw)[4], int left, float bias, float a2,
+                                             const Params& p, float* s_dt, Decays& d) {
   const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int b = 0; b < 4; ++b) {
-    const bool valid = 32 * b + lane < left;
-    dt[b] = valid ? dt_of(raw[b], bias, p) : 0.0f;
-    float l = valid ? dt[b] * a2 : 0.0f;
-    l = l < kMinLog ? kMinLog : l;
-    pre[b] = l;
-    suf[b] = __shfl_down_sync(0xffffffffu, l, 1);
-    if (lane == 31) suf[b] = 0.0f;
-  }
+  float r = raw[0];
 #pragma unroll 1
-  for (int o = 1; o < 32; o <<= 1)
+  for (int b = 0; b < 4; ++b) {
+    s_dt[32 * b + lane] = 32 * b + lane < left ? dt_of(r, bias, p) : 0.0f;
+    r = b == 0 ? raw[1] : b == 1 ? raw[2] : raw[3];
+  }
+  __syncwarp();
+  const float4 v = *reinterpret_cast<const float4*>(s_dt + 4 * lane);
+  d.dt[0] = v.x, d.dt[1] = v.y, d.dt[2] = v.z, d.dt[3] = v.w;
+  float l[4];
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const float u = __shfl_up_sync(0xffffffffu, pre[b], o);
-      const float d = __shfl_down_sync(0xffffffffu, suf[b], o);
-      if (lane >= o) pre[b] += u;
-      if (lane + o < 32) suf[b] += d;
-    }
+  for (int k = 0; k < 4; ++k) {
+    l[k] = 4 * lane + k < left ? d.dt[k] * a2 : 0.0f;  // (not 0 times infinity)
+    l[k] = l[k] < kMinLog ? kMinLog : l[k];
+  }
+  d.pre[0] = l[0];
+  d.suf[3] = 0.0f;
 #pragma unroll
-  for (int b = 0; b < 4; ++b) tot[b] = __shfl_sync(0xffffffffu, pre[b], 31);
-  return tot[0] + tot[1] + tot[2] + tot[3];
+  for (int k = 1; k < 4; ++k) d.pre[k] = d.pre[k - 1] + l[k];
+#pragma unroll
+  for (int k = 2; k >= 0; --k) d.suf[k] = d.suf[k + 1] + l[k + 1];
+  // the lanes before and behind this one in its block
+  float up = d.pre[3], down = d.pre[3];
+  const int at = lane & 7;
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) {
+    const float u = __shfl_up_sync(0xffffffffu, up, o, 8);
+    const float w = __shfl_down_sync(0xffffffffu, down, o, 8);
+    if (at >= o) up += u;
+    if (at + o < 8) down += w;
+  }
+  d.block = __shfl_sync(0xffffffffu, up, 7, 8);
+  up = __shfl_up_sync(0xffffffffu, up, 1, 8);
+  down = __shfl_down_sync(0xffffffffu, down, 1, 8);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (at > 0) d.pre[k] += up;
+    if (at < 7) d.suf[k] += down;
+  }
+  const float t0 = __shfl_sync(0xffffffffu, d.block, 0), t1 = __shfl_sync(0xffffffffu, d.block, 8),
+              t2 = __shfl_sync(0xffffffffu, d.block, 16), t3 = __shfl_sync(0xffffffffu, d.block, 24);
+  const int b = lane >> 3;
+  d.before = b == 0 ? 0.0f : b == 1 ? t0 : b == 2 ? t0 + t1 : t0 + t1 + t2;
+  d.after = b == 3 ? 0.0f : b == 2 ? t3 : b == 1 ? t3 + t2 : t3 + t2 + t1;
+  return (t0 + t1) + (t2 + t3);
+}
+__device__ __forceinline__ void sts_f4(float* at, float a, float b, float c, float d) {
+  *reinterpret_cast<float4*>(at) = make_float4(a, b, c, d);
 }
 
 // The three bf16 pieces of eight products w x, each piece what the ones before
@@ -222,26 +253,44 @@ __device__ __forceinline__ void issue_ds(uint32_t t_ds, uint64_t d_bt, uint64_t 
 }
 
 // Bounded waits of a CTA: on a timeout the CTA's flag and the library's status
-// word are set and every role leaves its loop.
+// word are set and every role leaves its loop.  The polling is a function of
+// its own: inlined at each of some thirty waits, it alone is larger than the
+// instruction cache.
+__device__ __noinline__ bool wait_poll(uint32_t bar, uint32_t parity, volatile uint32_t* flag,
+                                       unsigned int* fault) {
+#pragma unroll 1
+  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*flag) return false;
+  }
+  *flag = 1;
+  atomicOr(fault, kFaultScanWait);
+  return false;
+}
 struct Waits {
   volatile uint32_t* flag;
   unsigned int* fault;
-  __device__ __forceinline__ bool one(uint32_t bar, uint32_t parity) const {
-    parity &= 1u;
-    if (mbar_try_wait(bar, parity)) return true;
-    for (uint32_t i = 0; i < kWaitLimit; ++i) {
-      if (mbar_try_wait(bar, parity)) return true;
-      if (*flag) return false;
-    }
-    *flag = 1;
-    atomicOr(fault, kFaultScanWait);
-    return false;
-  }
   // for a whole warp, which stays together
   __device__ __forceinline__ bool warp(uint32_t bar, uint32_t parity) const {
-    return __all_sync(0xffffffffu, one(bar, parity)) != 0;
+    return __all_sync(0xffffffffu, wait_poll(bar, parity & 1u, flag, fault)) != 0;
   }
 };
+
+// D = A B with A [128, N] in rows of the 128-byte swizzle (K its columns), and
+// B the same way, or (TB) with its K index across the rows of 32-byte atoms.
+template <uint32_t TB>
+__device__ __forceinline__ void issue_rows(uint32_t d, uint64_t da, uint64_t db, int ksteps,
+                                           uint32_t idesc) {
+#pragma unroll 1
+  for (int k = 0; k < ksteps; k += 2) {
+    mma_bf16(d, da, db, idesc, k > 0);
+    if (k + 1 < ksteps) mma_bf16(d, da + 2, db + (TB ? 512 >> 4 : 2), idesc, true);
+    // two steps of 32 bytes in a row, then the next 64 columns
+    const uint32_t next = k & 2 ? (kRowsBytes / 2 - 64) >> 4 : 4;
+    da += next;
+    db += TB ? 2 * (512 >> 4) : next;
+  }
+}
 
 // Arrive for a whole warp (each lane's earlier work included).
 __device__ __forceinline__ void warp_arrive(uint32_t bar) {
@@ -252,7 +301,7 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar) {
 // ---------------------------------------------------------------------------
 // k_scan_tc
 // ---------------------------------------------------------------------------
-constexpr int kXWarps = 4, kMWarps = 8, kSYWarps = 16;
+constexpr int kXWarps = 4, kMWarps = 4, kSYWarps = 8;
 constexpr int kWarpM = kXWarps, kWarpSY = kWarpM + kMWarps, kWarpMma = kWarpSY + kSYWarps,
               kWarpCopy = kWarpMma + 1, kWarpDt = kWarpMma + 2;
 constexpr int kMainThreads = (kWarpMma + 3) * 32;
@@ -272,12 +321,11 @@ enum Bar {
   kWFull = 19,   // w X written
   kGDone = 20,   // G computed
   kMFull = 21,   // M written, G read
-  kDsDone = 22,  // dS computed, w X read
-  kY1Done = 23,  // C S computed, S read
-  kSFull = 24,   // S written, dS read
-  kYDone = 25,   // Y computed, M read
-  kYRead = 26,   // Y read
-  kBars = 27
+  kDsDone = 22,  // dS and C S computed, w X and S read
+  kSFull = 23,   // S written, dS read
+  kYDone = 24,   // Y computed, M read
+  kYRead = 25,   // Y read
+  kBars = 26
 };
 
 __global__ void __launch_bounds__(kMainThreads, 1)
@@ -345,58 +393,50 @@ __global__ void __launch_bounds__(kMainThreads, 1)
     const uint64_t d_s = desc_t32(sS), d_w = desc_t32(sW), d_c = desc_sw128(sC);
     const uint32_t piece = x_bytes >> 4;
     const int ksteps = (N + 15) / 16;
-    // step k of 16 along the columns of a 128-byte swizzled tile
-    auto kk = [](int k) {
-      return static_cast<uint64_t>((k >> 2) * (kRowsBytes / 2) + (k & 3) * 32) >> 4;
-    };
-    auto issue_g = [&](int c) {
-      if (!wait.warp(bar(kBFull + (c & 1)), c >> 1) || !wait.warp(bar(kCFull), c)) return false;
-      tc_fence_after();
-      if (elect_one()) {
-        const uint64_t d_b = desc_sw128(sB + (c & 1) * kRowsBytes);
-#pragma unroll 2
-        for (int k = 0; k < ksteps; ++k)
-          mma_bf16(tmem + kColG, d_c + kk(k), d_b + kk(k), id_g, k > 0);
-        mma_commit(bar(kGDone));
-      }
-      __syncwarp();
-      return true;
-    };
-    bool ok = chunks == 0 || issue_g(0);
+    bool ok = true;
+    // chunk c's C S, dS and M X, then the next one's G
 #pragma unroll 1
-    for (int c = 0; ok && c < chunks; ++c) {
-      // C S (S of the chunk before, Y and dS read)
-      if (!(ok = wait.warp(bar(kSFull), c) && (c == 0 || wait.warp(bar(kYRead), c - 1)))) break;
-      tc_fence_after();
-      if (elect_one()) {
+    for (int c = -1; c < chunks; ++c) {
+      if (c >= 0) {
+        // C S (S of the chunk before, Y and dS read)
+        if (!(ok = wait.warp(bar(kSFull), c) && (c == 0 || wait.warp(bar(kYRead), c - 1)))) break;
+        tc_fence_after();
+        if (elect_one()) {
+          issue_rows<kTransB>(t_y1, d_c, d_s, ksteps, id_y);
+          mma_commit(bar(kCFree));
+        }
+        __syncwarp();
+        // dS
+        if (!(ok = wait.warp(bar(kWFull), c))) break;
+        tc_fence_after();
+        if (elect_one()) {
+          issue_ds(t_ds, desc_t128(sB + (c & 1) * kRowsBytes, kRowsBytes / 2), d_w, piece, id_ds);
+          mma_commit(bar(kDsDone));  // (and C S is: products end in order)
+          mma_commit(bar(kBFree + (c & 1)));
+        }
+        __syncwarp();
+        // M X
+        if (!(ok = wait.warp(bar(kMFull), c))) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t d_x = desc_t32(sX + (c & 1) * x_bytes);
 #pragma unroll 2
-        for (int k = 0; k < ksteps; ++k)
-          mma_bf16(t_y1, d_c + kk(k), d_s + k * (512 >> 4), id_y, k > 0);
-        mma_commit(bar(kY1Done));
-        mma_commit(bar(kCFree));
+          for (int k = 0; k < kQ / 16; ++k)
+            mma_bf16_ts(t_y2, tmem + kColM + 8 * k, d_x + k * (512 >> 4), id_y, k > 0);
+          mma_commit(bar(kYDone));
+        }
+        __syncwarp();
       }
-      __syncwarp();
-      // dS
-      if (!(ok = wait.warp(bar(kWFull), c))) break;
-      tc_fence_after();
-      if (elect_one()) {
-        issue_ds(t_ds, desc_t128(sB + (c & 1) * kRowsBytes, kRowsBytes / 2), d_w, piece, id_ds);
-        mma_commit(bar(kDsDone));
-        mma_commit(bar(kBFree + (c & 1)));
+      if (c + 1 < chunks) {
+        const int s = (c + 1) & 1;
+        if (!(ok = wait.warp(bar(kBFull + s), (c + 1) >> 1) && wait.warp(bar(kCFull), c + 1))) break;
+        tc_fence_after();
+        if (elect_one()) {
+          issue_rows<0>(tmem + kColG, d_c, desc_sw128(sB + s * kRowsBytes), ksteps, id_g);
+          mma_commit(bar(kGDone));
+        }
+        __syncwarp();
       }
-      __syncwarp();
-      // M X
-      if (!(ok = wait.warp(bar(kMFull), c))) break;
-      tc_fence_after();
-      if (elect_one()) {
-        const uint64_t d_x = desc_t32(sX + (c & 1) * x_bytes);
-#pragma unroll 2
-        for (int k = 0; k < kQ / 16; ++k)
-          mma_bf16_ts(t_y2, tmem + kColM + 8 * k, d_x + k * (512 >> 4), id_y, k > 0);
-        mma_commit(bar(kYDone));
-      }
-      __syncwarp();
-      if (c + 1 < chunks) ok = issue_g(c + 1);
     }
     // no product may still run when the tensor memory is freed: after a
     // timeout, wait on a barrier of their own
@@ -413,41 +453,39 @@ __global__ void __launch_bounds__(kMainThreads, 1)
     const int boxes = N > 64 ? 2 : 1;
     const uint32_t bytes = boxes * (kRowsBytes / 2);
     bool ok = true;
-    auto put_y = [&](int c) {  // chunk c's Y; full chunks only
-      if (tp.otma && rows - c * kQ >= kQ) {
+#pragma unroll 1
+    for (int c = 0; c < chunks + 2; ++c) {
+      const int row = static_cast<int>(part.begin) + c * kQ, left = rows - c * kQ;
+      const int slot = c & 1;
+      const uint32_t b_at = sB + slot * kRowsBytes, x_at = sX + slot * x_bytes;
+      const uint32_t b_to = bar(left < kQ ? static_cast<int>(kTail) : kBFull + slot);
+      if (left > 0) {
+        if (c >= 2 && !(ok = wait.warp(bar(kBFree + slot), (c >> 1) - 1))) break;
         if (lane == 0) {
-          for (int i = 0; i < atoms && 16 * i < pw; ++i)
-            tma_store_3d(&tm_o, sX + (c & 1) * x_bytes + i * kAtomBytes, col0 + 16 * i, h,
-                         static_cast<int>(part.begin) + c * kQ);
+          mbar_expect_tx(b_to, bytes);
+#pragma unroll 1
+          for (int i = 0; i < boxes; ++i)
+            tma_load_3d(b_at + i * (kRowsBytes / 2), &tm_b, 64 * i, g, row, b_to);
+        }
+      }
+      if (c >= 2) {  // Y of chunk c - 2, in the place of its X
+        if (!(ok = wait.warp(bar(kYPut + slot), (c >> 1) - 1))) break;
+        if (lane == 0 && tp.otma && left + 2 * kQ >= kQ) {  // full chunks only
+#pragma unroll 1
+          for (int i = 0; 16 * i < pw; ++i)
+            tma_store_3d(&tm_o, x_at + i * kAtomBytes, col0 + 16 * i, h, row - 2 * kQ);
           bulk_commit();
           bulk_wait_read();
         }
         __syncwarp();
       }
-    };
-#pragma unroll 1
-    for (int c = 0; c < chunks; ++c) {
-      const int row = static_cast<int>(part.begin) + c * kQ, left = rows - c * kQ;
-      const int slot = c & 1;
-      const bool tail = left < kQ;
-      const uint32_t b_at = sB + slot * kRowsBytes;
-      if (c >= 2 && !(ok = wait.warp(bar(kBFree + slot), (c >> 1) - 1))) break;
-      if (lane == 0) {
-        const uint32_t to = bar(tail ? static_cast<int>(kTail) : kBFull + slot);
-        mbar_expect_tx(to, bytes);
-        for (int i = 0; i < boxes; ++i)
-          tma_load_3d(b_at + i * (kRowsBytes / 2), &tm_b, 64 * i, g, row, to);
-      }
-      if (c >= 2) {
-        if (!(ok = wait.warp(bar(kYPut + slot), (c >> 1) - 1))) break;
-        put_y(c - 2);
-      }
+      if (left <= 0) continue;
       if (lane == 0) {
         if (tp.xtma) {
           mbar_expect_tx(bar(kXLand + slot), x_bytes);
+#pragma unroll 1
           for (int i = 0; i < atoms; ++i)
-            tma_load_3d(sX + slot * x_bytes + i * kAtomBytes, &tm_x, col0 + 16 * i, h, row,
-                        bar(kXLand + slot));
+            tma_load_3d(x_at + i * kAtomBytes, &tm_x, col0 + 16 * i, h, row, bar(kXLand + slot));
         } else {
           mbar_arrive(bar(kXLand + slot));  // the place is free: the X warps load it
         }
@@ -455,13 +493,15 @@ __global__ void __launch_bounds__(kMainThreads, 1)
       if (c >= 1 && !(ok = wait.warp(bar(kCFree), c - 1))) break;
       if (lane == 0) {
         mbar_expect_tx(bar(kCFull), bytes);
+#pragma unroll 1
         for (int i = 0; i < boxes; ++i)
           tma_load_3d(sC + i * (kRowsBytes / 2), &tm_c, 64 * i, g, row, bar(kCFull));
       }
-      if (tail) {
+      if (left < kQ) {
         // rows of other sequences, or of none, count for nothing, whatever
         // they hold
         if (!(ok = wait.warp(bar(kTail), 0))) break;
+#pragma unroll 1
         for (int i = lane; i < (kQ - left) * 8; i += 32)
           for (int j = 0; j < boxes; ++j)
             sts16(b_at + j * (kRowsBytes / 2) + left * 128 + i * 16, make_uint4(0, 0, 0, 0));
@@ -469,8 +509,6 @@ __global__ void __launch_bounds__(kMainThreads, 1)
         warp_arrive(bar(kBFull + slot));
       }
     }
-    for (int c = chunks > 2 ? chunks - 2 : 0; ok && c < chunks; ++c)
-      if ((ok = wait.warp(bar(kYPut + (c & 1)), c >> 1))) put_y(c);
     if (!ok) {
       // copies may still be on their way into this CTA's shared memory: the
       // time of a bounded wait (on a barrier that nothing completes) is theirs
@@ -495,27 +533,25 @@ __global__ void __launch_bounds__(kMainThreads, 1)
     int slot = 0, use = 0;
 #pragma unroll 1
     for (int c = 0; c < chunks; ++c) {
-      float pre[4], suf[4], tot[4], dt[4];
-      make_decays(raw, rows - c * kQ, bias, a2, p, pre, suf, dt, tot);
-      if (c + 1 < chunks) fetch(c + 1);
       if (use > 0 && !wait.warp(bar(kDtFree + slot), use - 1)) break;
       float* s = s_decay + slot * kDecayFloats;
-      float before = 0.0f;
+      Decays d;
+      const float total = make_decays(raw, rows - c * kQ, bias, a2, p, s + 2 * kQ, d);
+      if (c + 1 < chunks) fetch(c + 1);
+      float* t = s + 4 * lane;
+      sts_f4(t, d.pre[0], d.pre[1], d.pre[2], d.pre[3]);
+      float f[4];
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        float after = 0.0f;
+      for (int k = 0; k < 4; ++k) f[k] = d.dt[k] * ex2_approx(d.suf[k]);
+      sts_f4(t + kQ, f[0], f[1], f[2], f[3]);
 #pragma unroll
-        for (int k = 3; k > b; --k) after += tot[k];
-        const int t = 32 * b + lane;
-        s[t] = pre[b];
-        s[kQ + t] = dt[b] * ex2_approx(suf[b]);
-        s[2 * kQ + t] = dt[b];
-        s[3 * kQ + t] = dt[b] * ex2_approx(suf[b] + after);
-        s[4 * kQ + t] = ex2_approx(before + pre[b]);
-        before += tot[b];
-        if (lane == 0) s[5 * kQ + b] = tot[b];
-      }
-      if (lane == 0) s[5 * kQ + 4] = ex2_approx(before);
+      for (int k = 0; k < 4; ++k) f[k] = d.dt[k] * ex2_approx(d.suf[k] + d.after);
+      sts_f4(t + 3 * kQ, f[0], f[1], f[2], f[3]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) f[k] = ex2_approx(d.before + d.pre[k]);
+      sts_f4(t + 4 * kQ, f[0], f[1], f[2], f[3]);
+      if ((lane & 7) == 0) s[5 * kQ + (lane >> 3)] = d.block;
+      if (lane == 0) s[5 * kQ + 4] = ex2_approx(total);
       warp_arrive(bar(kDtFull + slot));
       if (++slot == kDecays) slot = 0, ++use;
     }
@@ -546,26 +582,21 @@ __global__ void __launch_bounds__(kMainThreads, 1)
       const float* sw = s_decay + slot * kDecayFloats + 3 * kQ + r0;
       const float w0 = sw[0], w1 = sw[64];
       if (c > 0 && !wait.warp(bar(kDsDone), c - 1)) break;
-      uint32_t at = at0;
 #pragma unroll 1
-      for (int i = 0; i < atoms; ++i, at += kAtomBytes) {
-        const uint4 xa = lds16(sX + (c & 1) * x_bytes + at);
-        const uint4 xb = lds16(sX + (c & 1) * x_bytes + at + 2048);
+      for (int i = 0; i < 2 * atoms; ++i) {
+        const uint32_t at = sW + i * 2048 + at0;
         uint4 u[3];
-        pieces_of(xa, w0, u);
+        pieces_of(lds16(x_at + i * 2048), i & 1 ? w1 : w0, u);
 #pragma unroll
-        for (int k = 0; k < 3; ++k) sts16(sW + at + k * x_bytes, u[k]);
-        pieces_of(xb, w1, u);
-#pragma unroll
-        for (int k = 0; k < 3; ++k) sts16(sW + at + 2048 + k * x_bytes, u[k]);
+        for (int k = 0; k < 3; ++k) sts16(at + k * x_bytes, u[k]);
       }
       fence_async_smem();
       warp_arrive(bar(kWFull));
       if (++slot == kDecays) slot = 0, ++use;
     }
   } else if (warp < kWarpSY) {
-    // ---- M of rows 32 q + lane, column blocks hf and hf + 2 ----
-    const int q = warp & 3, hf = (warp >> 2) & 1;
+    // ---- M of rows 32 q + lane, column blocks hf, hf + kMWarps / 4, .. ----
+    const int q = warp & 3, hf = (warp - kWarpM) >> 2;
     const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
     int slot = 0, use = 0;
 #pragma unroll 1
@@ -578,12 +609,13 @@ __global__ void __launch_bounds__(kMainThreads, 1)
       if (c > 0 && !wait.warp(bar(kYDone), c - 1)) break;
       tc_fence_after();
 #pragma unroll 1
-      for (int blk = hf; blk < 4; blk += 2) {
+      for (int blk = hf; blk < 4; blk += kMWarps / 4) {
         const float* sj = sd + 32 * blk;
         const uint32_t t_g = tmem + lanes + kColG + 32 * blk, t_m = tmem + lanes + kColM + 16 * blk;
         uint32_t m[8];
         if (blk < q) {
           float between = pre;  // row prefix + the blocks between
+#pragma unroll 1
           for (int b = blk + 1; b < q; ++b) between += sd[5 * kQ + b];
           const float f = ex2_approx(between);
 #pragma unroll 1
@@ -635,7 +667,7 @@ __global__ void __launch_bounds__(kMainThreads, 1)
       if (++slot == kDecays) slot = 0, ++use;
     }
   } else {
-    // ---- S and Y: lanes 32 q.., atoms hf, hf + 4 ----
+    // ---- S and Y: lanes 32 q.., atoms hf, hf + kSYShare, .. ----
     const int q = warp & 3, hf = ((warp - kWarpSY) >> 2), n = 32 * q + lane;
     const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
     const float dskip = p.d ? __ldg(p.d + h) : 0.0f;
@@ -675,7 +707,7 @@ __global__ void __launch_bounds__(kMainThreads, 1)
       if (!wait.warp(bar(kDtFull + slot), use)) break;
       const float* sd = s_decay + slot * kDecayFloats;
       const float decay = sd[5 * kQ + 4], e = sd[4 * kQ + i];
-      if (!wait.warp(bar(kDsDone), c) || !wait.warp(bar(kY1Done), c)) break;
+      if (!wait.warp(bar(kDsDone), c)) break;
       tc_fence_after();
 #pragma unroll
       for (int k = 0; k < kSYAtoms; ++k) {
@@ -841,19 +873,16 @@ __global__ void __launch_bounds__(kStateThreads, 2)
     float log_total = 0.0f;
 #pragma unroll 1
     for (int c = 0; c < chunks; ++c) {
-      float pre[4], suf[4], tot[4], dt[4];
-      const float total = make_decays(raw, kQ, bias, a2, p, pre, suf, dt, tot);
-      if (c + 1 < chunks) fetch(c + 1);
       // this half was last read for chunk c - 2 (each phase waited for in turn)
       if (c >= 1 && !wait.warp(b_w, c - 1)) break;
       float* s = s_decay + (c & 1) * (kQ + 4);
+      Decays d;
+      const float total = make_decays(raw, kQ, bias, a2, p, s, d);
+      if (c + 1 < chunks) fetch(c + 1);
+      float f[4];
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        float after = 0.0f;
-#pragma unroll
-        for (int k = 3; k > b; --k) after += tot[k];
-        s[32 * b + lane] = dt[b] * ex2_approx(suf[b] + after);
-      }
+      for (int k = 0; k < 4; ++k) f[k] = d.dt[k] * ex2_approx(d.suf[k] + d.after);
+      sts_f4(s + 4 * lane, f[0], f[1], f[2], f[3]);
       if (lane == 0) s[kQ] = ex2_approx(total);
       log_total += total;
       warp_arrive(b_dt);
@@ -870,12 +899,14 @@ __global__ void __launch_bounds__(kStateThreads, 2)
       if (lane == 0) {
         if (tp.xtma) {
           mbar_expect_tx(b_x, x_bytes);
+#pragma unroll 1
           for (int i = 0; i < atoms; ++i)
             tma_load_3d(sW + i * kAtomBytes, &tm_x, col0 + 16 * i, h, row, b_x);
         } else {
           mbar_arrive(b_x);
         }
         mbar_expect_tx(b_b, bytes);
+#pragma unroll 1
         for (int i = 0; i < boxes; ++i)
           tma_load_3d(sB + i * (kRowsBytes / 2), &tm_b, 64 * i, g, row, b_b);
       }
