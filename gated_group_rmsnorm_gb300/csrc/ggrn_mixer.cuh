@@ -53,8 +53,11 @@ struct Part {
   int64_t index = 0, count = 1;  // this part among those of its sequence
   int64_t place = 0;           // of a sequence with more than one part
 };
+// (With cu, and wherever sequences are cut, rows fit 32 bits: the host checks.)
 __device__ __forceinline__ int64_t parts_of(int64_t n, int64_t part) {
-  return n <= part ? 1 : (n + part - 1) / part;
+  return n <= part ? 1
+                   : (static_cast<uint32_t>(n) + static_cast<uint32_t>(part) - 1) /
+                         static_cast<uint32_t>(part);
 }
 // Parts (low word) and places (high word) of a sequence of n rows.
 __device__ __forceinline__ uint64_t part_counts(int64_t n, int64_t part) {
@@ -67,7 +70,8 @@ __device__ __forceinline__ Part find_part(const Seqs& q, int64_t part, int64_t n
   Part r;
   if (!q.cu) {
     const int64_t per = parts_of(q.each, part);
-    const int64_t s = number / per;
+    const int64_t s =
+        static_cast<uint32_t>(number) / static_cast<uint32_t>(per);  // (a grid's index)
     if (s >= q.seqs) return r;
     r.seq = s;
     r.index = number - s * per;

@@ -377,6 +377,7 @@ Layout layout_of(const ggrn_scan_call& c) {
   const Shape s = shape_of(static_cast<int>(c.head_dim), static_cast<int>(c.state_size));
   l.tc = tc_covers(c);
   l.part = l.tc ? tc_part_rows(c, longest(c)) : part_rows(c.rows, c.heads * s.ptiles);
+  if (longest(c) > INT32_MAX) l.part = longest(c);  // (the kernels count parts in 32 bits)
   l.cut = longest(c) > l.part;
   if (!l.cut) l.part = std::max<int64_t>(1, longest(c));
   l.parts = c.rows / l.part + c.seqs;

@@ -72,7 +72,7 @@ struct TcParams {
   Params p;
   unsigned int* fault;
   int tile;        // columns of a head per CTA, a multiple of 16 up to 80
-  int xtma, otma;  // x / out by tensor-map copies (else 8 bytes at a time)
+  int xvec, ovec;  // bytes a copy of x (16 or 8) / a store of out (16 or 8) moves
 };
 
 // D (+)= A B with A [128, K] in tensor memory.
@@ -100,16 +100,58 @@ __device__ __forceinline__ uint64_t desc_t32(uint32_t addr) {
 }
 constexpr uint32_t kTransA = 1u << 15, kTransB = 1u << 16;  // instruction descriptor bits
 
-// Byte offset of 16-byte chunk `ck` of row r of an atom.
-__device__ __forceinline__ uint32_t atom_at(int r, int ck) {
-  return (r >> 3) * 256 + (r & 7) * 32 + ((ck ^ ((r >> 2) & 1)) << 4);
+// Byte offset of 16-byte chunk `ch` (8 columns) of row r in 32-byte swizzled
+// atoms.
+__device__ __forceinline__ uint32_t chunk_at(int r, int ch) {
+  return static_cast<uint32_t>((ch >> 1) * static_cast<int>(kAtomBytes) + r * 32 +
+                               (((ch ^ (r >> 2)) & 1) << 4));
 }
+// The 16-byte chunks of a tile of `atoms` atoms, dealt to 64 threads an atom (4
+// chunks each): eight lanes take four rows of an atom (its 128 bytes of shared
+// memory, all banks), a warp the same rows of four atoms where there are as
+// many, so that its global accesses are whole lines (16 rows of 32 bytes an
+// instruction measured 94 clocks an instruction).  Chunk i of a thread is 32
+// rows below its first one.
+constexpr int kDealt = 4, kDealtRows = 32;
+constexpr uint32_t kDealtBytes = kDealtRows * 32;
+struct Deal {
+  int row, col;
+  uint32_t at;
+  __device__ __forceinline__ Deal(int t, int atoms) {
+    const int a = (t >> 3) % atoms, rows4 = (t >> 3) / atoms;
+    row = 4 * rows4 + ((t & 7) >> 1);
+    col = 16 * a + 8 * (t & 1);
+    at = static_cast<uint32_t>(a * static_cast<int>(kAtomBytes) + row * 32 +
+                               (((t ^ rows4) & 1) << 4));
+  }
+};
 
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+// The same chunks in rounds of a number of threads that is no multiple of the
+// atoms: a round's chunk is found from the last one's.
+struct Round {
+  int rows4, a, rows_step, a_step, atoms, r, ck;
+  __device__ __forceinline__ Round(int t, int threads, int n)
+      : rows4((t >> 3) / n), a((t >> 3) % n), rows_step((threads >> 3) / n),
+        a_step((threads >> 3) % n), atoms(n), r((t & 7) >> 1), ck(t & 1) {}
+  __device__ __forceinline__ void next() {
+    rows4 += rows_step, a += a_step;
+    if (a >= atoms) a -= atoms, ++rows4;
+  }
+  __device__ __forceinline__ int row() const { return 4 * rows4 + r; }
+  __device__ __forceinline__ int col() const { return 16 * a + 8 * ck; }
+  __device__ __forceinline__ uint32_t at() const {
+    return static_cast<uint32_t>(a * static_cast<int>(kAtomBytes) + row() * 32 +
+                                 (((ck ^ rows4) & 1) << 4));
+  }
+};
+
+__device__ __forceinline__ void tmem_ld16_nowait(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7])
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
 __device__ __forceinline__ void tmem_ld_wait() {
@@ -139,6 +181,32 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
   return v;
 }
 using Bf = Elem<__nv_bfloat16>;
+
+// f32 pairs kept in one 64-bit register: the arithmetic on values that are
+// pairs from their load on needs no moves.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ F2 pair(uint32_t a, uint32_t b) {
+  return pk2(__uint_as_float(a), __uint_as_float(b));
+}
+__device__ __forceinline__ uint32_t bf16x2(F2 v) {
+  float a, b;
+  upk2(v, a, b);
+  return Bf::pack2(a, b);
+}
+// the two halves of a word of bf16
+__device__ __forceinline__ F2 wide(uint32_t u) {
+  return pk2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
 
 // The decays of one chunk, by one warp: dt of token 32 b + lane comes from
 // `raw[b]` (tokens from `left` on count for nothing), goes through `s_dt`, and
@@ -205,45 +273,56 @@ __device__ __forceinline__ void sts_f4(float* at, float a, float b, float c, flo
 // The three bf16 pieces of eight products w x, each piece what the ones before
 // leave, cut off (not rounded: 8 bits each of 24).
 __device__ __forceinline__ void pieces_of(const uint4& x, float w, uint4 (&u)[3]) {
-  float v[8];
+  const F2 ww = pk2(w, w), minus = pk2(-1.0f, -1.0f);
   uint32_t out[3][4];
-  Bf::unpack(x, v);
 #pragma unroll
-  for (int e = 0; e < 8; e += 2) {
-    float a, b;
-    mul2(a, b, v[e], v[e + 1], w, w);
+  for (int e = 0; e < 4; ++e) {
+    F2 v = mul2(wide((&x.x)[e]), ww);
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
+      float a, b;
+      upk2(v, a, b);
       const uint32_t ha = __float_as_uint(a), hb = __float_as_uint(b);
-      out[k][e / 2] = __byte_perm(ha, hb, 0x7632);
-      if (k < 2)
-        fma2(a, b, __uint_as_float(ha & 0xffff0000u), __uint_as_float(hb & 0xffff0000u), -1.0f,
-             -1.0f, a, b);
+      out[k][e] = __byte_perm(ha, hb, 0x7632);
+      if (k < 2) v = fma2(pair(ha & 0xffff0000u, hb & 0xffff0000u), minus, v);
     }
   }
 #pragma unroll
   for (int k = 0; k < 3; ++k) u[k] = make_uint4(out[k][0], out[k][1], out[k][2], out[k][3]);
 }
 
-// Columns [col, col + 8) of a row of X whose rows are only 8-byte aligned.
-__device__ __forceinline__ uint4 load_x(const __nv_bfloat16* src, int col, int pw) {
-  uint4 v = make_uint4(0, 0, 0, 0);
-  if (col < pw) {
-    const uint2 lo = __ldg(reinterpret_cast<const uint2*>(src));
-    v.x = lo.x, v.y = lo.y;
+// `bytes` (16 or 8) from global to shared memory, of which the first `valid`
+// are read and the rest zeros.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, int valid) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(valid)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// Columns [col, col + 8) of a row of X (`src` points at them), zeros behind
+// column pw and where the row is not `there` (nothing is read then; `base` is
+// an address that could be); vec: rows are 16-byte aligned (else 8).
+__device__ __forceinline__ void copy_x(uint32_t dst, const __nv_bfloat16* src,
+                                       const __nv_bfloat16* base, int col, int pw, bool there,
+                                       bool vec) {
+  if (vec) {
+    const bool v = there && col < pw;
+    cp_async16(dst, v ? src : base, v ? 16 : 0);
+  } else {
+    const bool v0 = there && col < pw, v1 = there && col + 4 < pw;
+    cp_async8(dst, v0 ? src : base, v0 ? 8 : 0);
+    cp_async8(dst + 8, v1 ? src + 4 : base, v1 ? 8 : 0);
   }
-  if (col + 4 < pw) {
-    const uint2 hi = __ldg(reinterpret_cast<const uint2*>(src + 4));
-    v.z = hi.x, v.w = hi.y;
-  }
-  return v;
 }
 
 // dS (+)= B^T [w X in pieces], smallest piece first; each step's B^T is kept
 // for its three pieces.
 __device__ __forceinline__ void issue_ds(uint32_t t_ds, uint64_t d_bt, uint64_t d_w, uint32_t piece,
                                          uint32_t idesc) {
-#pragma unroll 2
+#pragma unroll 1
   for (int k = 0; k < kQ / 16; ++k) {
     const uint64_t a = d_bt + k * (2048 >> 4), w = d_w + k * (512 >> 4);
     mma_bf16_keep<Keep::kFill>(t_ds, a, w + 2 * piece, idesc, k > 0);
@@ -252,29 +331,55 @@ __device__ __forceinline__ void issue_ds(uint32_t t_ds, uint64_t d_bt, uint64_t 
   }
 }
 
-// Bounded waits of a CTA: on a timeout the CTA's flag and the library's status
-// word are set and every role leaves its loop.  The polling is a function of
-// its own: inlined at each of some thirty waits, it alone is larger than the
-// instruction cache.
-__device__ __noinline__ bool wait_poll(uint32_t bar, uint32_t parity, volatile uint32_t* flag,
-                                       unsigned int* fault) {
-#pragma unroll 1
-  for (uint32_t i = 0; i < kWaitLimit; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
+// Bounded waits of a CTA, a whole warp at a time: a role whose wait runs out
+// (after about a second) sets the CTA's flag and leaves its loop, the others
+// follow, and the flag ends in the library's status word.  A try without a time
+// hint suspends the warp for a while of the hardware's choosing; with a hint it
+// is a sleep that ends late (450 clocks a wait that had nothing to wait for).
+// The first try is inlined, the polling a function of its own: inlined at each
+// of the waits it is larger than the instruction cache, and as one call with
+// the first try it cost a fifth of the kernel's time.
+__device__ __forceinline__ bool try_phase(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+constexpr long long kWaitClocks = 2000000000ll;
+__device__ __noinline__ bool wait_poll(uint32_t bar, uint32_t parity, volatile uint32_t* flag) {
+  const long long start = clock64();
+  do {
+    if (try_phase(bar, parity)) return true;
     if (*flag) return false;
-  }
+  } while (clock64() - start < kWaitClocks);
   *flag = 1;
-  atomicOr(fault, kFaultScanWait);
   return false;
 }
 struct Waits {
   volatile uint32_t* flag;
-  unsigned int* fault;
-  // for a whole warp, which stays together
   __device__ __forceinline__ bool warp(uint32_t bar, uint32_t parity) const {
-    return __all_sync(0xffffffffu, wait_poll(bar, parity & 1u, flag, fault)) != 0;
+    parity &= 1u;
+    if (__all_sync(0xffffffffu, try_phase(bar, parity))) return true;
+    return __all_sync(0xffffffffu, wait_poll(bar, parity, flag)) != 0;
   }
 };
+// The end of a wait by a group of warps whose first one polled: its answer for
+// all of them.  (Polled by every warp, the barriers slow each other and the
+// rest of shared memory down.)
+__device__ __forceinline__ bool group_sync(int id, int threads, bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %3, 0;\n"
+      " barrier.cta.red.and.pred q, %1, %2, p;\n selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(all)
+      : "r"(id), "r"(threads), "r"(ok ? 1u : 0u)
+      : "memory");
+  return all != 0;
+}
 
 // D = A B with A [128, N] in rows of the 128-byte swizzle (K its columns), and
 // B the same way, or (TB) with its K index across the rows of 32-byte atoms.
@@ -292,6 +397,32 @@ __device__ __forceinline__ void issue_rows(uint32_t d, uint64_t da, uint64_t db,
   }
 }
 
+// M of 16 columns of a block before the row's: G f c_j, f the row's factor and
+// c_j the columns'.
+__device__ __forceinline__ void decayed(const uint32_t (&g)[16], const float* cj, float f,
+                                        uint32_t (&m)[8]) {
+  const F2 ff = pk2(f, f);
+#pragma unroll
+  for (int e = 0; e < 16; e += 4) {
+    const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(cj + e);  // two pairs
+    m[e / 2] = bf16x2(mul2(mul2(c.x, ff), pair(g[e], g[e + 1])));
+    m[e / 2 + 1] = bf16x2(mul2(mul2(c.y, ff), pair(g[e + 2], g[e + 3])));
+  }
+}
+// The same in the row's own block (whose decays start at `s`), of the columns
+// up to `last`.
+__device__ __forceinline__ void decayed_diagonal(const uint32_t (&g)[16], const float* s, float pre,
+                                                 int last, uint32_t (&m)[8]) {
+#pragma unroll
+  for (int e = 0; e < 16; e += 2) {
+    const float2 pj = *reinterpret_cast<const float2*>(s + e);
+    const float2 dj = *reinterpret_cast<const float2*>(s + 2 * kQ + e);
+    const float v0 = __uint_as_float(g[e]) * (dj.x * ex2_approx(pre - pj.x));
+    const float v1 = __uint_as_float(g[e + 1]) * (dj.y * ex2_approx(pre - pj.y));
+    m[e / 2] = Bf::pack2(e <= last ? v0 : 0.0f, e + 1 <= last ? v1 : 0.0f);
+  }
+}
+
 // Arrive for a whole warp (each lane's earlier work included).
 __device__ __forceinline__ void warp_arrive(uint32_t bar) {
   __syncwarp();
@@ -301,36 +432,34 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar) {
 // ---------------------------------------------------------------------------
 // k_scan_tc
 // ---------------------------------------------------------------------------
-constexpr int kXWarps = 4, kMWarps = 4, kSYWarps = 8;
-constexpr int kWarpM = kXWarps, kWarpSY = kWarpM + kMWarps, kWarpMma = kWarpSY + kSYWarps,
-              kWarpCopy = kWarpMma + 1, kWarpDt = kWarpMma + 2;
-constexpr int kMainThreads = (kWarpMma + 3) * 32;
-constexpr int kSYShare = kSYWarps / 4;                    // warps on a quarter of the lanes
-constexpr int kSYAtoms = (kMaxAtoms + kSYShare - 1) / kSYShare;
+constexpr int kMWarps = 4, kSWarps = 8, kYWarps = 4, kXWarps = 2 * kMaxAtoms;
+constexpr int kWarpS = kMWarps, kWarpY = kWarpS + kSWarps, kWarpMma = kWarpY + kYWarps,
+              kWarpDt = kWarpMma + 1, kWarpX = kWarpMma + 2;
+constexpr int kMainThreads = (kWarpX + kXWarps) * 32;
+constexpr int kSShare = kSWarps / 4;                      // warps on a quarter of the lanes
+constexpr int kSAtoms = (kMaxAtoms + kSShare - 1) / kSShare;
 // barriers, 8 bytes each; [2] and [3] by buffer
 enum Bar {
   kBFull = 0,    // [2] B landed
   kBFree = 2,    // [2] B read by G and dS
   kCFull = 4,    // [2] C landed
   kCFree = 6,    // [2] C read by G and C S
-  kXLand = 8,    // [2] X landed
-  kYPut = 10,    // [2] Y in X's place (or stored)
-  kDtFull = 12,  // [3] decays made
-  kDtFree = 15,  // [3] and read
-  kTail = 18,    // B of a part's last, partial chunk landed
-  kWFull = 19,   // w X written
-  kGDone = 20,   // G computed
-  kMFull = 21,   // M written, G read
-  kDsDone = 22,  // dS and C S computed, w X and S read
-  kSFull = 23,   // S written, dS read
-  kYDone = 24,   // Y computed, M read
-  kYRead = 25,   // Y read
-  kBars = 26
+  kYPut = 8,     // [2] Y in X's place
+  kDtFull = 10,  // [3] decays made
+  kDtFree = 13,  // [3] and read
+  kTail = 16,    // B of a part's last, partial chunk landed
+  kWFull = 17,   // X and w X written
+  kGDone = 18,   // G computed
+  kMFull = 19,   // M written, G read
+  kDsDone = 20,  // dS and C S computed, w X and S read
+  kSFull = 21,   // S written, dS read
+  kYDone = 22,   // Y computed, M read
+  kYRead = 23,   // Y read
+  kBars = 24
 };
 
 __global__ void __launch_bounds__(kMainThreads, 1)
     k_scan_tc(const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ CUtensorMap tm_c,
-              const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_o,
               const TcParams tp) {
   const Params& p = tp.p;
   extern __shared__ unsigned char smem_raw[];
@@ -352,12 +481,12 @@ __global__ void __launch_bounds__(kMainThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid < kBars) {
     const int i = tid;
-    mbar_init(bar(i), i == kWFull                                  ? kXWarps
-                      : i == kMFull                                ? kMWarps
-                      : (i >= kYPut && i < kYPut + 2) || i == kSFull || i == kYRead ||
-                              (i >= kDtFree && i < kDtFree + kDecays)
-                          ? kSYWarps
-                          : 1);
+    mbar_init(bar(i), i == kWFull                             ? 2 * atoms
+                      : i == kMFull                           ? kMWarps
+                      : i == kSFull                           ? kSWarps
+                      : i == kYRead || i == kYPut || i == kYPut + 1 ? kYWarps
+                      : i >= kDtFree && i < kDtFree + kDecays ? kSWarps + kYWarps
+                                                              : 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (tid == 0) s_misc[1] = 0;
@@ -379,7 +508,17 @@ __global__ void __launch_bounds__(kMainThreads, 1)
   const bool run = part.seq >= 0 && !(part.count > 1 && part.place >= p.places);
   const int rows = run ? static_cast<int>(part.end - part.begin) : 0;
   const int chunks = (rows + kQ - 1) / kQ;
-  const Waits wait = {s_misc + 1, tp.fault};
+  const Waits wait = {s_misc + 1};
+  // the state this part starts from (zeros without one) and the one it leaves
+  const float* from = nullptr;
+  float* to = nullptr;
+  if (run) {
+    const int64_t held = static_cast<int64_t>(P) * N, at = h * held + static_cast<int64_t>(col0) * N;
+    const int64_t entry = seq_slot(p.q, part.seq);
+    if (part.count > 1) from = p.ws + part.place * p.H * held + at;
+    else if (entry >= 0 && seq_resumes(p.q, part.seq)) from = p.state + entry * p.slot_stride + at;
+    if (part.index == part.count - 1 && entry >= 0) to = p.state + entry * p.slot_stride + at;
+  }
   // Each phase of a barrier is waited for in turn: a parity tells a phase from
   // its neighbours only.  What may run ahead of a waiter by more is by buffer.
 
@@ -393,10 +532,29 @@ __global__ void __launch_bounds__(kMainThreads, 1)
     const uint64_t d_s = desc_t32(sS), d_w = desc_t32(sW), d_c = desc_sw128(sC);
     const uint32_t piece = x_bytes >> 4;
     const int ksteps = (N + 15) / 16;
+    // It copies B and C too, each as soon as the products that read the ones
+    // before are known to be done.
+    const int boxes = N > 64 ? 2 : 1;
+    auto copy = [&](const CUtensorMap* map, uint32_t to, int c, uint32_t full) {
+      if (lane == 0) {
+        mbar_expect_tx(full, boxes * (kRowsBytes / 2));
+#pragma unroll 1
+        for (int i = 0; i < boxes; ++i)
+          tma_load_3d(to + i * (kRowsBytes / 2), map, 64 * i, g,
+                      static_cast<int>(part.begin) + c * kQ, full);
+      }
+      __syncwarp();
+    };
     bool ok = true;
     // chunk c's C S, dS and M X, then the next one's G
 #pragma unroll 1
     for (int c = -1; c < chunks; ++c) {
+      const int n = c + 1, buf = n & 1;
+      if (n < chunks) {
+        if (n >= 2 && !(ok = wait.warp(bar(kBFree + buf), (n >> 1) - 1))) break;
+        copy(&tm_b, sB + buf * kRowsBytes, n,
+             bar(rows - n * kQ < kQ ? static_cast<int>(kTail) : kBFull + buf));
+      }
       if (c >= 0) {
         // C S (S of the chunk before, Y and dS read)
         if (!(ok = wait.warp(bar(kSFull), c) && (c == 0 || wait.warp(bar(kYRead), c - 1)))) break;
@@ -415,6 +573,12 @@ __global__ void __launch_bounds__(kMainThreads, 1)
           mma_commit(bar(kBFree + (c & 1)));
         }
         __syncwarp();
+      }
+      if (n < chunks) {
+        if (c >= 0 && !(ok = wait.warp(bar(kCFree), c))) break;
+        copy(&tm_c, sC, n, bar(kCFull));
+      }
+      if (c >= 0) {
         // M X
         if (!(ok = wait.warp(bar(kMFull), c))) break;
         tc_fence_after();
@@ -427,19 +591,19 @@ __global__ void __launch_bounds__(kMainThreads, 1)
         }
         __syncwarp();
       }
-      if (c + 1 < chunks) {
-        const int s = (c + 1) & 1;
-        if (!(ok = wait.warp(bar(kBFull + s), (c + 1) >> 1) && wait.warp(bar(kCFull), c + 1))) break;
+      if (n < chunks) {
+        if (!(ok = wait.warp(bar(kBFull + buf), n >> 1) && wait.warp(bar(kCFull), n))) break;
         tc_fence_after();
         if (elect_one()) {
-          issue_rows<0>(tmem + kColG, d_c, desc_sw128(sB + s * kRowsBytes), ksteps, id_g);
+          issue_rows<0>(tmem + kColG, d_c, desc_sw128(sB + buf * kRowsBytes), ksteps, id_g);
           mma_commit(bar(kGDone));
         }
         __syncwarp();
       }
     }
-    // no product may still run when the tensor memory is freed: after a
-    // timeout, wait on a barrier of their own
+    // no product may still run when the tensor memory is freed, and no copy be
+    // on its way into shared memory: after a timeout, wait on a barrier of the
+    // products' own, and as long again on one that nothing completes
     if (!ok) {
       if (elect_one()) {
         mbar_init(bar(kBars), 1);
@@ -447,97 +611,27 @@ __global__ void __launch_bounds__(kMainThreads, 1)
       }
       __syncwarp();
       mbar_wait(bar(kBars), 0);
-    }
-  } else if (warp == kWarpCopy) {
-    // ---- B, C, X in and Y out ----
-    const int boxes = N > 64 ? 2 : 1;
-    const uint32_t bytes = boxes * (kRowsBytes / 2);
-    bool ok = true;
-#pragma unroll 1
-    for (int c = 0; c < chunks + 2; ++c) {
-      const int row = static_cast<int>(part.begin) + c * kQ, left = rows - c * kQ;
-      const int slot = c & 1;
-      const uint32_t b_at = sB + slot * kRowsBytes, x_at = sX + slot * x_bytes;
-      const uint32_t b_to = bar(left < kQ ? static_cast<int>(kTail) : kBFull + slot);
-      if (left > 0) {
-        if (c >= 2 && !(ok = wait.warp(bar(kBFree + slot), (c >> 1) - 1))) break;
-        if (lane == 0) {
-          mbar_expect_tx(b_to, bytes);
-#pragma unroll 1
-          for (int i = 0; i < boxes; ++i)
-            tma_load_3d(b_at + i * (kRowsBytes / 2), &tm_b, 64 * i, g, row, b_to);
-        }
-      }
-      if (c >= 2) {  // Y of chunk c - 2, in the place of its X
-        if (!(ok = wait.warp(bar(kYPut + slot), (c >> 1) - 1))) break;
-        if (lane == 0 && tp.otma && left + 2 * kQ >= kQ) {  // full chunks only
-#pragma unroll 1
-          for (int i = 0; 16 * i < pw; ++i)
-            tma_store_3d(&tm_o, x_at + i * kAtomBytes, col0 + 16 * i, h, row - 2 * kQ);
-          bulk_commit();
-          bulk_wait_read();
-        }
-        __syncwarp();
-      }
-      if (left <= 0) continue;
-      if (lane == 0) {
-        if (tp.xtma) {
-          mbar_expect_tx(bar(kXLand + slot), x_bytes);
-#pragma unroll 1
-          for (int i = 0; i < atoms; ++i)
-            tma_load_3d(x_at + i * kAtomBytes, &tm_x, col0 + 16 * i, h, row, bar(kXLand + slot));
-        } else {
-          mbar_arrive(bar(kXLand + slot));  // the place is free: the X warps load it
-        }
-      }
-      if (c >= 1 && !(ok = wait.warp(bar(kCFree), c - 1))) break;
-      if (lane == 0) {
-        mbar_expect_tx(bar(kCFull), bytes);
-#pragma unroll 1
-        for (int i = 0; i < boxes; ++i)
-          tma_load_3d(sC + i * (kRowsBytes / 2), &tm_c, 64 * i, g, row, bar(kCFull));
-      }
-      if (left < kQ) {
-        // rows of other sequences, or of none, count for nothing, whatever
-        // they hold
-        if (!(ok = wait.warp(bar(kTail), 0))) break;
-#pragma unroll 1
-        for (int i = lane; i < (kQ - left) * 8; i += 32)
-          for (int j = 0; j < boxes; ++j)
-            sts16(b_at + j * (kRowsBytes / 2) + left * 128 + i * 16, make_uint4(0, 0, 0, 0));
-        fence_async_smem();
-        warp_arrive(bar(kBFull + slot));
-      }
-    }
-    if (!ok) {
-      // copies may still be on their way into this CTA's shared memory: the
-      // time of a bounded wait (on a barrier that nothing completes) is theirs
-      if (lane == 0) mbar_init(bar(kTail), 1);
-      __syncwarp();
-      mbar_wait(bar(kTail), 0);
+      mbar_wait(bar(kBars), 1);
     }
   } else if (warp == kWarpDt) {
-    // ---- the decays, chunks ahead ----
+    // ---- the decays, chunks ahead, and the end of a part's last B ----
     const float a2 = __ldg(p.a + h) * kLog2e;
     const float bias = p.dt_bias ? __ldg(p.dt_bias + h) : 0.0f;
     const __nv_bfloat16* dtp = static_cast<const __nv_bfloat16*>(p.dt) + part.begin * p.dts + h;
     float raw[4];
-    auto fetch = [&](int c) {
+    int slot = 0, use = 0;
+    bool ok = true;
+#pragma unroll 1
+    for (int c = 0; c < chunks; ++c) {
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
         const int t = c * kQ + 32 * b + lane;
         raw[b] = t < rows ? Bf::load1(dtp + t * p.dts, 0) : 0.0f;
       }
-    };
-    fetch(0);
-    int slot = 0, use = 0;
-#pragma unroll 1
-    for (int c = 0; c < chunks; ++c) {
-      if (use > 0 && !wait.warp(bar(kDtFree + slot), use - 1)) break;
+      if (use > 0 && !(ok = wait.warp(bar(kDtFree + slot), use - 1))) break;
       float* s = s_decay + slot * kDecayFloats;
       Decays d;
       const float total = make_decays(raw, rows - c * kQ, bias, a2, p, s + 2 * kQ, d);
-      if (c + 1 < chunks) fetch(c + 1);
       float* t = s + 4 * lane;
       sts_f4(t, d.pre[0], d.pre[1], d.pre[2], d.pre[3]);
       float f[4];
@@ -555,108 +649,135 @@ __global__ void __launch_bounds__(kMainThreads, 1)
       warp_arrive(bar(kDtFull + slot));
       if (++slot == kDecays) slot = 0, ++use;
     }
-  } else if (warp < kWarpM) {
-    // ---- the pieces of w X: row 64 (i & 1) + r0 of atom i / 2 ----
-    const int r0 = tid >> 1, col8 = (tid & 1) * 8;
-    const uint32_t at0 = atom_at(r0, tid & 1);
-    const __nv_bfloat16* xg = static_cast<const __nv_bfloat16*>(p.x) + part.begin * p.xs + hcol;
-    int slot = 0, use = 0;
+    const int left = rows - (chunks - 1) * kQ;
+    if (ok && chunks > 0 && left < kQ && wait.warp(bar(kTail), 0)) {
+      // rows of other sequences, or of none, count for nothing, whatever they
+      // hold
+      const int buf = (chunks - 1) & 1;
 #pragma unroll 1
-    for (int c = 0; c < chunks; ++c) {
-      const uint32_t x_at = sX + (c & 1) * x_bytes + at0;
-      const int left = rows - c * kQ;
-      if (!wait.warp(bar(kXLand + (c & 1)), c >> 1)) break;
-      if (!tp.xtma || left < kQ) {
-        // (re)load what the copies do not give: rows behind the sequence count
-        // for nothing, whatever they hold
+      for (int i = lane; i < (kQ - left) * 8; i += 32)
+        for (int j = 0; j < (N > 64 ? 2 : 1); ++j)
+          sts16(sB + buf * kRowsBytes + j * (kRowsBytes / 2) + left * 128 + i * 16,
+                make_uint4(0, 0, 0, 0));
+      fence_async_smem();
+      warp_arrive(bar(kBFull + buf));
+    }
+  } else if (warp >= kWarpX) {
+    // ---- X in, a chunk ahead, and Y out, and the pieces of w X; a thread
+    // reads, writes and stores its own chunks of a tile ----
+    const int t = tid - kWarpX * 32, threads = 64 * atoms;
+    if (t < threads) {
+      const Deal deal(t, atoms);
+      const int64_t first = part.begin + deal.row;
+      const __nv_bfloat16* xp = static_cast<const __nv_bfloat16*>(p.x) + hcol + deal.col;
+      __nv_bfloat16* op = static_cast<__nv_bfloat16*>(p.out) + hcol + deal.col;
+      const __nv_bfloat16* x0 = static_cast<const __nv_bfloat16*>(p.x) + part.begin * p.xs + hcol;
+      const bool cols = deal.col < pw, whole = tp.xvec == 16 && deal.col + 8 <= pw;
+      int slot = 0, use = 0;
 #pragma unroll 1
-        for (int i = 0; i < 2 * atoms; ++i) {
-          const int r = (i & 1) * 64 + r0, col = (i >> 1) * 16 + col8;
-          if (r >= left) sts16(x_at + i * 2048, make_uint4(0, 0, 0, 0));
-          else if (!tp.xtma)
-            sts16(x_at + i * 2048,
-                  load_x(xg + static_cast<int64_t>(c * kQ + r) * p.xs + col, col, pw));
+      for (int c = -1; c <= chunks; ++c) {
+        if (c >= 0 && c < chunks) {
+          bool ok = true;
+          if (warp == kWarpX)
+            ok = wait.warp(bar(kDtFull + slot), use) && (c == 0 || wait.warp(bar(kDsDone), c - 1));
+          if (!group_sync(1, threads, ok)) break;
+          const float* sw = s_decay + slot * kDecayFloats + 3 * kQ + deal.row;
+          if (++slot == kDecays) slot = 0, ++use;
+          cp_async_wait();
+          const uint32_t x_at = sX + (c & 1) * x_bytes + deal.at, w_at = sW + deal.at;
+#pragma unroll 1
+          for (int i = 0; i < kDealt; i += 2) {
+            const uint32_t o = i * kDealtBytes;
+            uint4 ua[3], ub[3];
+            const uint4 xa = lds16(x_at + o), xb = lds16(x_at + o + kDealtBytes);
+            pieces_of(xa, sw[i * kDealtRows], ua);
+            pieces_of(xb, sw[(i + 1) * kDealtRows], ub);
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+              sts16(w_at + o + k * x_bytes, ua[k]);
+              sts16(w_at + o + kDealtBytes + k * x_bytes, ub[k]);
+            }
+          }
+          fence_async_smem();
+          warp_arrive(bar(kWFull));
+        }
+        const int n = c + 1;  // the chunk to come into the place of n - 2
+        const uint32_t x_at = sX + (n & 1) * x_bytes + deal.at;
+        if (n >= 2) {
+          const bool ok = warp != kWarpX || wait.warp(bar(kYPut + (n & 1)), (n >> 1) - 1);
+          if (!group_sync(1, threads, ok)) break;
+          const int left = rows - (n - 2) * kQ - deal.row;
+          __nv_bfloat16* o = op + (first + (n - 2) * kQ) * p.os;
+#pragma unroll 2
+          for (int i = 0; i < kDealt; ++i, o += kDealtRows * p.os) {
+            const uint4 v = lds16(x_at + i * kDealtBytes);
+            if (i * kDealtRows < left && cols) {
+              if (tp.ovec == 16) {
+                *reinterpret_cast<uint4*>(o) = v;
+              } else {
+                *reinterpret_cast<uint2*>(o) = make_uint2(v.x, v.y);
+                if (deal.col + 4 < pw) *reinterpret_cast<uint2*>(o + 4) = make_uint2(v.z, v.w);
+              }
+            }
+          }
+        }
+        if (n < chunks) {
+          const __nv_bfloat16* x = xp + (first + n * kQ) * p.xs;
+          const int left = rows - n * kQ;
+          if (left >= kQ && whole) {
+#pragma unroll 2
+            for (int i = 0; i < kDealt; ++i, x += kDealtRows * p.xs)
+              cp_async16(x_at + i * kDealtBytes, x, 16);
+          } else
+#pragma unroll 1
+          for (int i = 0; i < kDealt; ++i, x += kDealtRows * p.xs)
+            copy_x(x_at + i * kDealtBytes, x, x0, deal.col, pw, deal.row + i * kDealtRows < left,
+                   tp.xvec == 16);
         }
       }
-      if (!wait.warp(bar(kDtFull + slot), use)) break;
-      const float* sw = s_decay + slot * kDecayFloats + 3 * kQ + r0;
-      const float w0 = sw[0], w1 = sw[64];
-      if (c > 0 && !wait.warp(bar(kDsDone), c - 1)) break;
-#pragma unroll 1
-      for (int i = 0; i < 2 * atoms; ++i) {
-        const uint32_t at = sW + i * 2048 + at0;
-        uint4 u[3];
-        pieces_of(lds16(x_at + i * 2048), i & 1 ? w1 : w0, u);
-#pragma unroll
-        for (int k = 0; k < 3; ++k) sts16(at + k * x_bytes, u[k]);
-      }
-      fence_async_smem();
-      warp_arrive(bar(kWFull));
-      if (++slot == kDecays) slot = 0, ++use;
+      cp_async_wait();
     }
-  } else if (warp < kWarpSY) {
-    // ---- M of rows 32 q + lane, column blocks hf, hf + kMWarps / 4, .. ----
-    const int q = warp & 3, hf = (warp - kWarpM) >> 2;
+  } else if (warp < kWarpS) {
+    // ---- M of rows 32 q + lane ----
+    const int q = warp;
     const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
     int slot = 0, use = 0;
 #pragma unroll 1
     for (int c = 0; c < chunks; ++c) {
-      if (!wait.warp(bar(kDtFull + slot), use)) break;
+      // (G done: and the M before is read, by products issued earlier)
+      bool ok = true;
+      if (warp == 0) ok = wait.warp(bar(kDtFull + slot), use) && wait.warp(bar(kGDone), c);
+      if (!group_sync(2, kMWarps * 32, ok)) break;
+      tc_fence_after();
       const float* sd = s_decay + slot * kDecayFloats;
       const float pre = sd[32 * q + lane];
-      if (!wait.warp(bar(kGDone), c)) break;
-      // the M before is read (by the same commit as Y's)
-      if (c > 0 && !wait.warp(bar(kYDone), c - 1)) break;
-      tc_fence_after();
+      float between = pre;  // row prefix + the blocks between
 #pragma unroll 1
-      for (int blk = hf; blk < 4; blk += kMWarps / 4) {
+      for (int blk = 3; blk >= 0; --blk) {
         const float* sj = sd + 32 * blk;
         const uint32_t t_g = tmem + lanes + kColG + 32 * blk, t_m = tmem + lanes + kColM + 16 * blk;
-        uint32_t m[8];
+        uint32_t ga[16], gb[16], m[8];
+        if (blk <= q) {
+          tmem_ld16_nowait(t_g, ga);
+          tmem_ld16_nowait(t_g + 16, gb);
+        }
         if (blk < q) {
-          float between = pre;  // row prefix + the blocks between
-#pragma unroll 1
-          for (int b = blk + 1; b < q; ++b) between += sd[5 * kQ + b];
           const float f = ex2_approx(between);
-#pragma unroll 1
-          for (int j = 0; j < 32; j += 16) {
-            uint32_t gr[16];
-            tmem_ld16(t_g + j, gr);
-#pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-              const float4 cf = *reinterpret_cast<const float4*>(sj + kQ + j + e);
-              float v0, v1, v2, v3;
-              mul2(v0, v1, cf.x, cf.y, f, f);
-              mul2(v2, v3, cf.z, cf.w, f, f);
-              mul2(v0, v1, v0, v1, __uint_as_float(gr[e]), __uint_as_float(gr[e + 1]));
-              mul2(v2, v3, v2, v3, __uint_as_float(gr[e + 2]), __uint_as_float(gr[e + 3]));
-              m[e / 2] = Bf::pack2(v0, v1);
-              m[e / 2 + 1] = Bf::pack2(v2, v3);
-            }
-            tmem_st8(t_m + j / 2, m);
-          }
+          between += sj[5 * kQ - 31 * blk];  // the sum over this block
+          tmem_ld_wait();
+          decayed(ga, sj + kQ, f, m);
+          tmem_st8(t_m, m);
+          decayed(gb, sj + kQ + 16, f, m);
+          tmem_st8(t_m + 8, m);
         } else if (blk == q) {
-#pragma unroll 1
-          for (int j = 0; j < 32; j += 16) {
-            uint32_t gr[16];
-            tmem_ld16(t_g + j, gr);
-#pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-              const float4 pj = *reinterpret_cast<const float4*>(sj + j + e);
-              const float4 dj = *reinterpret_cast<const float4*>(sj + 2 * kQ + j + e);
-              const int k = lane - j - e;  // columns up to the row's own
-              const float v0 = __uint_as_float(gr[e]) * (dj.x * ex2_approx(pre - pj.x));
-              const float v1 = __uint_as_float(gr[e + 1]) * (dj.y * ex2_approx(pre - pj.y));
-              const float v2 = __uint_as_float(gr[e + 2]) * (dj.z * ex2_approx(pre - pj.z));
-              const float v3 = __uint_as_float(gr[e + 3]) * (dj.w * ex2_approx(pre - pj.w));
-              m[e / 2] = Bf::pack2(k >= 0 ? v0 : 0.0f, k >= 1 ? v1 : 0.0f);
-              m[e / 2 + 1] = Bf::pack2(k >= 2 ? v2 : 0.0f, k >= 3 ? v3 : 0.0f);
-            }
-            tmem_st8(t_m + j / 2, m);
-          }
+          tmem_ld_wait();
+          decayed_diagonal(ga, sj, pre, lane, m);
+          tmem_st8(t_m, m);
+          decayed_diagonal(gb, sj + 16, pre, lane - 16, m);
+          tmem_st8(t_m + 8, m);
         } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) m[j] = 0;
+          for (int e = 0; e < 8; ++e) m[e] = 0;
           tmem_st8(t_m, m);
           tmem_st8(t_m + 8, m);
         }
@@ -666,96 +787,108 @@ __global__ void __launch_bounds__(kMainThreads, 1)
       warp_arrive(bar(kMFull));
       if (++slot == kDecays) slot = 0, ++use;
     }
-  } else {
-    // ---- S and Y: lanes 32 q.., atoms hf, hf + kSYShare, .. ----
-    const int q = warp & 3, hf = ((warp - kWarpSY) >> 2), n = 32 * q + lane;
+  } else if (warp < kWarpY) {
+    // ---- S: lanes 32 q.., atoms hf, hf + kSShare, .. ----
+    const int q = warp & 3, hf = (warp - kWarpS) >> 2, n = 32 * q + lane;
     const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
-    const float dskip = p.d ? __ldg(p.d + h) : 0.0f;
-    const int64_t slot_at = seq_slot(p.q, part.seq);
-    const int64_t PN = static_cast<int64_t>(P) * N;
-    float s[kSYAtoms][16];  // S^T: row n, columns 16 (hf + 4 k) + j
-    const float* from = nullptr;
-    if (part.count > 1) from = p.ws + (part.place * p.H + h) * PN;
-    else if (slot_at >= 0 && seq_resumes(p.q, part.seq))
-      from = p.state + slot_at * p.slot_stride + h * PN;
+    const uint32_t at0 = sS + hf * kAtomBytes + chunk_at(n, 0);
+    F2 s[kSAtoms][8];  // S^T: row n, columns 16 (hf + kSShare k) + 2 j and the next
     auto put = [&](int k) {  // atom k as the bf16 operand
-      float v[8];
 #pragma unroll
-      for (int ck = 0; ck < 2; ++ck) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = s[k][8 * ck + j];
-        sts16(sS + (hf + kSYShare * k) * kAtomBytes + atom_at(n, ck), Bf::pack(v));
-      }
+      for (int ck = 0; ck < 2; ++ck)
+        sts16((at0 + kSShare * k * kAtomBytes) ^ (ck << 4),
+              make_uint4(bf16x2(s[k][4 * ck]), bf16x2(s[k][4 * ck + 1]), bf16x2(s[k][4 * ck + 2]),
+                         bf16x2(s[k][4 * ck + 3])));
     };
+    const int first = 16 * hf;  // column of the tile
 #pragma unroll
-    for (int k = 0; k < kSYAtoms; ++k) {
-      const int a = hf + kSYShare * k;
+    for (int k = 0; k < kSAtoms; ++k)
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const int col = a * 16 + j;
-        s[k][j] = from && n < N && a < atoms && col < pw
-                      ? from[static_cast<int64_t>(col0 + col) * N + n] : 0.0f;
-      }
-      if (a < atoms) put(k);
+      for (int j = 0; j < 8; ++j) s[k][j] = 0;
+    if (from && n < N) {
+      const float* f = from + first * N + n;
+#pragma unroll
+      for (int k = 0; k < kSAtoms; ++k, f += 16 * (kSShare - 1) * N)
+#pragma unroll
+        for (int j = 0; j < 8; ++j, f += 2 * N)
+          if (first + 16 * kSShare * k + 2 * j < pw) s[k][j] = pk2(f[0], f[N]);  // (pw is even)
     }
+#pragma unroll
+    for (int k = 0; k < kSAtoms; ++k)
+      if (hf + kSShare * k < atoms) put(k);
     fence_async_smem();
     warp_arrive(bar(kSFull));
-    const int i = n;  // the row of Y
     int slot = 0, use = 0;
 #pragma unroll 1
     for (int c = 0; c < chunks; ++c) {
-      if (!wait.warp(bar(kDtFull + slot), use)) break;
-      const float* sd = s_decay + slot * kDecayFloats;
-      const float decay = sd[5 * kQ + 4], e = sd[4 * kQ + i];
-      if (!wait.warp(bar(kDsDone), c)) break;
+      bool ok = true;
+      if (warp == kWarpS) ok = wait.warp(bar(kDtFull + slot), use) && wait.warp(bar(kDsDone), c);
+      if (!group_sync(3, kSWarps * 32, ok)) break;
       tc_fence_after();
+      const float decay = s_decay[slot * kDecayFloats + 5 * kQ + 4];
+      const F2 decay2 = pk2(decay, decay);
 #pragma unroll
-      for (int k = 0; k < kSYAtoms; ++k) {
-        const int a = hf + kSYShare * k;
+      for (int k = 0; k < kSAtoms; ++k) {
+        const int a = hf + kSShare * k;
         if (a < atoms) {
           uint32_t r[16];
           tmem_ld16(t_ds + lanes + a * 16, r);
 #pragma unroll
-          for (int j = 0; j < 16; j += 2)
-            fma2(s[k][j], s[k][j + 1], s[k][j], s[k][j + 1], decay, decay, __uint_as_float(r[j]),
-                 __uint_as_float(r[j + 1]));
+          for (int j = 0; j < 8; ++j) s[k][j] = fma2(s[k][j], decay2, pair(r[2 * j], r[2 * j + 1]));
           put(k);
         }
       }
       fence_async_smem();
       tc_fence_before();
-      warp_arrive(bar(kSFull));
-      if (!wait.warp(bar(kYDone), c)) break;
-      tc_fence_after();
-      const int left = rows - c * kQ;
-      const bool stage = tp.otma && left >= kQ;  // Y into X's place, stored from there
-      __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.out) +
-                            (part.begin + c * kQ + i) * p.os + hcol;
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar(kSFull));
+        mbar_arrive(bar(kDtFree + slot));
+      }
+      if (++slot == kDecays) slot = 0, ++use;
+    }
+    // the state after the part's last row
+    if (to && n < N) {
+      float* f = to + first * N + n;
+#pragma unroll
+      for (int k = 0; k < kSAtoms; ++k, f += 16 * (kSShare - 1) * N)
+#pragma unroll
+        for (int j = 0; j < 8; ++j, f += 2 * N)
+          if (first + 16 * kSShare * k + 2 * j < pw) upk2(s[k][j], f[0], f[N]);
+    }
+  } else if (warp < kWarpMma) {
+    // ---- Y: row 32 q + lane, into X's place ----
+    const int q = warp & 3, i = 32 * q + lane;
+    const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
+    const float dskip = p.d ? __ldg(p.d + h) : 0.0f;
+    const F2 skip2 = pk2(dskip, dskip);
+    const uint32_t at0 = chunk_at(i, 0);
+    int slot = 0, use = 0;
 #pragma unroll 1
-      for (int a2 = 2 * hf; a2 < 2 * atoms; a2 += a2 & 1 ? 2 * kSYShare - 1 : 1) {
-        const uint32_t at = sX + (c & 1) * x_bytes + (a2 >> 1) * kAtomBytes + atom_at(i, a2 & 1);
-        uint32_t y1[8], y2[8];
-        tmem_ld8(t_y1 + lanes + a2 * 8, y1);
-        tmem_ld8(t_y2 + lanes + a2 * 8, y2);
-        float xv[8], y[8];
-        Bf::unpack(lds16(at), xv);
+    for (int c = 0; c < chunks; ++c) {
+      bool ok = true;
+      if (warp == kWarpY) ok = wait.warp(bar(kDtFull + slot), use) && wait.warp(bar(kYDone), c);
+      if (!group_sync(4, kYWarps * 32, ok)) break;
+      tc_fence_after();
+      const float e = s_decay[slot * kDecayFloats + 4 * kQ + i];
+      const F2 e2 = pk2(e, e);
+      uint32_t at = sX + (c & 1) * x_bytes + at0;
+#pragma unroll 1
+      for (int a = 0; a < atoms; ++a, at += kAtomBytes) {
+        uint32_t y1[16], y2[16];
+        tmem_ld16_nowait(t_y1 + lanes + a * 16, y1);
+        tmem_ld16_nowait(t_y2 + lanes + a * 16, y2);
+        uint4 xa = lds16(at), xb = lds16(at ^ 16);
         tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          fma2(y[j], y[j + 1], __uint_as_float(y1[j]), __uint_as_float(y1[j + 1]), e, e,
-               __uint_as_float(y2[j]), __uint_as_float(y2[j + 1]));
-          fma2(y[j], y[j + 1], xv[j], xv[j + 1], dskip, dskip, y[j], y[j + 1]);
+        for (int j = 0; j < 16; j += 2) {
+          uint32_t& xw = j < 8 ? (&xa.x)[j / 2] : (&xb.x)[j / 2 - 4];
+          xw = bf16x2(fma2(wide(xw), skip2,
+                           fma2(pair(y1[j], y1[j + 1]), e2, pair(y2[j], y2[j + 1]))));
         }
-        const uint4 v = Bf::pack(y);
-        const int col = a2 * 8;
-        if (stage) {
-          sts16(at, v);
-        } else if (i < left && col < pw) {
-          *reinterpret_cast<uint2*>(orow + col) = make_uint2(v.x, v.y);
-          if (col + 4 < pw) *reinterpret_cast<uint2*>(orow + col + 4) = make_uint2(v.z, v.w);
-        }
+        sts16(at, xa);
+        sts16(at ^ 16, xb);
       }
-      fence_async_smem();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -765,21 +898,10 @@ __global__ void __launch_bounds__(kMainThreads, 1)
       }
       if (++slot == kDecays) slot = 0, ++use;
     }
-    // the state after the part's last row
-    if (part.index == part.count - 1 && slot_at >= 0 && n < N) {
-      float* to = p.state + slot_at * p.slot_stride + h * PN;
-#pragma unroll
-      for (int k = 0; k < kSYAtoms; ++k)
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const int col = (hf + kSYShare * k) * 16 + j;
-          if (hf + kSYShare * k < atoms && col < pw)
-            to[static_cast<int64_t>(col0 + col) * N + n] = s[k][j];
-        }
-    }
   }
   tc_fence_before();
   __syncthreads();
+  if (tid == 0 && s_misc[1]) atomicOr(tp.fault, kFaultScanWait);
   if (warp == kWarpMma) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
@@ -789,15 +911,14 @@ __global__ void __launch_bounds__(kMainThreads, 1)
 // ---------------------------------------------------------------------------
 // k_scan_tc_state: the state a part adds from a zero start, and its decay (a
 // cut sequence's parts but the last; all their chunks are full).  Two CTAs per
-// SM, whose stages overlap: one warp copies B and X (into the place of the
-// largest piece of w X), 8 warps write the pieces, one warp issues dS, the 8
-// warps add it to S in registers.
+// SM, whose stages overlap: one warp copies B, 8 warps copy X into the place of
+// the largest piece of w X and write the pieces, one warp issues dS, the 8 warps
+// add it to S in registers.
 // ---------------------------------------------------------------------------
 constexpr int kStateThreads = 11 * 32;
 
 __global__ void __launch_bounds__(kStateThreads, 2)
-    k_scan_tc_state(const __grid_constant__ CUtensorMap tm_b,
-                    const __grid_constant__ CUtensorMap tm_x, const TcParams tp) {
+    k_scan_tc_state(const __grid_constant__ CUtensorMap tm_b, const TcParams tp) {
   constexpr int AW = (kMaxAtoms + 1) / 2;       // atoms of a warp
   const Params& p = tp.p;
   extern __shared__ unsigned char smem_raw[];
@@ -810,15 +931,13 @@ __global__ void __launch_bounds__(kStateThreads, 2)
   const uint32_t decay_off = kRowsBytes + 3 * x_bytes;
   float* s_decay = reinterpret_cast<float*>(base + decay_off);  // [2][kQ + 4]: w, decay
   const uint32_t bars_off = decay_off + 2 * (kQ + 4) * 4;
-  volatile uint32_t* s_misc = reinterpret_cast<uint32_t*>(base + bars_off + 40);
-  // per chunk: B landed; X landed; w X written; decays made; dS computed
-  const uint32_t b_b = base_u + bars_off, b_x = b_b + 8, b_w = b_b + 16, b_dt = b_b + 24,
-                 b_ds = b_b + 32;
+  volatile uint32_t* s_misc = reinterpret_cast<uint32_t*>(base + bars_off + 32);
+  // per chunk: B landed; w X written; decays made; dS computed
+  const uint32_t b_b = base_u + bars_off, b_w = b_b + 8, b_dt = b_b + 16, b_ds = b_b + 24;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     mbar_init(b_b, 1);
-    mbar_init(b_x, 1);
     mbar_init(b_w, 8);
     mbar_init(b_dt, 1);
     mbar_init(b_ds, 1);
@@ -841,7 +960,7 @@ __global__ void __launch_bounds__(kStateThreads, 2)
   const bool run = part.seq >= 0 && part.index < part.count - 1 && part.place + 1 < p.places;
   const int rows = run ? static_cast<int>(part.end - part.begin) : 0;
   const int chunks = rows / kQ;
-  const Waits wait = {s_misc + 1, tp.fault};
+  const Waits wait = {s_misc + 1};
 
   if (!run) {
     // nothing: fall through to the end
@@ -897,14 +1016,6 @@ __global__ void __launch_bounds__(kStateThreads, 2)
       const int row = static_cast<int>(part.begin) + c * kQ;
       if (c > 0 && !(ok = wait.warp(b_ds, c - 1))) break;
       if (lane == 0) {
-        if (tp.xtma) {
-          mbar_expect_tx(b_x, x_bytes);
-#pragma unroll 1
-          for (int i = 0; i < atoms; ++i)
-            tma_load_3d(sW + i * kAtomBytes, &tm_x, col0 + 16 * i, h, row, b_x);
-        } else {
-          mbar_arrive(b_x);
-        }
         mbar_expect_tx(b_b, bytes);
 #pragma unroll 1
         for (int i = 0; i < boxes; ++i)
@@ -916,37 +1027,43 @@ __global__ void __launch_bounds__(kStateThreads, 2)
   } else {
     const int q = warp & 3, hf = warp >> 2, n = 32 * q + lane;
     const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
-    const int r = tid >> 1, col8 = (tid & 1) * 8;  // row r of each atom
-    const uint32_t at0 = sW + atom_at(r, tid & 1);
-    const __nv_bfloat16* xg = static_cast<const __nv_bfloat16*>(p.x) + (part.begin + r) * p.xs +
-                              static_cast<int64_t>(h) * P + col0 + col8;
-    float s[AW][16];
+    const Round deal(tid, 256, atoms);
+    const __nv_bfloat16* x0 = static_cast<const __nv_bfloat16*>(p.x) + part.begin * p.xs +
+                              static_cast<int64_t>(h) * P + col0;
+    auto fetch = [&](int c) {
+      const __nv_bfloat16* xn = x0 + static_cast<int64_t>(c) * kQ * p.xs;
+      Round d = deal;
+#pragma unroll 1
+      for (int i = 0; i < atoms; ++i, d.next())
+        copy_x(sW + d.at(), xn + d.row() * p.xs + d.col(), x0, d.col(), pw, true, tp.xvec == 16);
+    };
+    fetch(0);
+    F2 s[AW][8];
 #pragma unroll
     for (int k = 0; k < AW; ++k)
 #pragma unroll
-      for (int j = 0; j < 16; ++j) s[k][j] = 0.0f;
+      for (int j = 0; j < 8; ++j) s[k][j] = 0;
 #pragma unroll 1
     for (int c = 0; c < chunks; ++c) {
       const float* sd = s_decay + (c & 1) * (kQ + 4);
-      if (!wait.warp(b_dt, c)) break;
-      const float w = sd[r], decay = sd[kQ];
-      if (!wait.warp(b_x, c)) break;
+      if (!group_sync(1, 256, warp != 0 || wait.warp(b_dt, c))) break;
+      const F2 decay2 = pk2(sd[kQ], sd[kQ]);
+      cp_async_wait();
+      Round d = deal;
 #pragma unroll 1
-      for (int i = 0; i < atoms; ++i) {
-        const uint32_t at = at0 + i * kAtomBytes;
+      for (int i = 0; i < atoms; ++i, d.next()) {
+        const uint32_t at = sW + d.at();
         uint4 u[3];
-        pieces_of(tp.xtma ? lds16(at)
-                          : load_x(xg + static_cast<int64_t>(c * kQ) * p.xs + 16 * i,
-                                   16 * i + col8, pw),
-                  w, u);
+        pieces_of(lds16(at), sd[d.row()], u);
 #pragma unroll
-        for (int k = 0; k < 3; ++k) sts16(at + k * x_bytes, u[k]);
+        for (int j = 0; j < 3; ++j) sts16(at + j * x_bytes, u[j]);
       }
       fence_async_smem();
       tc_fence_before();
       warp_arrive(b_w);
-      if (!wait.warp(b_ds, c)) break;
+      if (!group_sync(1, 256, warp != 0 || wait.warp(b_ds, c))) break;
       tc_fence_after();
+      if (c + 1 < chunks) fetch(c + 1);
 #pragma unroll
       for (int k = 0; k < AW; ++k) {
         const int a = hf + 2 * k;
@@ -954,26 +1071,25 @@ __global__ void __launch_bounds__(kStateThreads, 2)
           uint32_t v[16];
           tmem_ld16(tmem + lanes + a * 16, v);
 #pragma unroll
-          for (int j = 0; j < 16; j += 2)
-            fma2(s[k][j], s[k][j + 1], s[k][j], s[k][j + 1], decay, decay, __uint_as_float(v[j]),
-                 __uint_as_float(v[j + 1]));
+          for (int j = 0; j < 8; ++j) s[k][j] = fma2(s[k][j], decay2, pair(v[2 * j], v[2 * j + 1]));
         }
       }
       tc_fence_before();
     }
-    float* to = p.ws + ((part.place + 1) * p.H + h) * static_cast<int64_t>(P) * N;
+    cp_async_wait();
     if (n < N) {
+      float* to = p.ws + ((part.place + 1) * p.H + h) * static_cast<int64_t>(P) * N +
+                  static_cast<int64_t>(col0 + 16 * hf) * N + n;
 #pragma unroll
-      for (int k = 0; k < AW; ++k)
+      for (int k = 0; k < AW; ++k, to += 16 * N)
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const int col = (hf + 2 * k) * 16 + j;
-          if (hf + 2 * k < atoms && col < pw) to[static_cast<int64_t>(col0 + col) * N + n] = s[k][j];
-        }
+        for (int j = 0; j < 8; ++j, to += 2 * N)
+          if (16 * (hf + 2 * k) + 2 * j < pw) upk2(s[k][j], to[0], to[N]);
     }
   }
   tc_fence_before();
   __syncthreads();
+  if (tid == 0 && s_misc[1]) atomicOr(tp.fault, kFaultScanWait);
   if (warp == 8) {
     tc_fence_after();
     tmem_dealloc(tmem, 128);
@@ -988,7 +1104,7 @@ uint32_t main_smem(int tile) {
          8 * kBars + 16;
 }
 uint32_t state_smem(int tile) {
-  return 1024 + kRowsBytes + 3 * (tile / 16 * kAtomBytes) + 2 * (kQ + 4) * 4 + 40 + 8;
+  return 1024 + kRowsBytes + 3 * (tile / 16 * kAtomBytes) + 2 * (kQ + 4) * 4 + 32 + 8;
 }
 
 int tile_of(int64_t P) {
@@ -1009,21 +1125,22 @@ cudaError_t allow_smem() {
   return err;
 }
 
-// [rows][blocks][cols] in boxes of 128 rows and `box` columns: columns behind a
-// block's end and rows behind the buffer read as zeros and are not written.
-bool make_map(CUtensorMap* m, const void* ptr, int64_t cols, int64_t blocks, int64_t rows,
-              int64_t stride, uint32_t box, CUtensorMapSwizzle swizzle) {
+// [rows][groups][N] in boxes of 128 rows and 64 columns: columns behind N and
+// rows behind the buffer read as zeros.
+bool make_map(CUtensorMap* m, const void* ptr, int64_t N, int64_t groups, int64_t rows,
+              int64_t stride) {
   EncodeTiled enc = encode_fn();
   if (!enc) return false;
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(blocks),
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(groups),
                               static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols) * 2,
-                                 static_cast<cuuint64_t>(rows > 1 ? stride : blocks * cols) * 2};
-  const cuuint32_t boxes[3] = {box, 1, kQ};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(N) * 2,
+                                 static_cast<cuuint64_t>(rows > 1 ? stride : groups * N) * 2};
+  const cuuint32_t box[3] = {64, 1, kQ};
   const cuuint32_t estr[3] = {1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, boxes,
-             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
 }
 
 }  // namespace
@@ -1032,8 +1149,7 @@ bool make_map(CUtensorMap* m, const void* ptr, int64_t cols, int64_t blocks, int
 // columns in whole 8-byte ones, and rows aligned to those.
 bool tc_covers(const ggrn_scan_call& c) {
   if (c.rows > INT32_MAX / 2 || c.b_row_stride >= int64_t{1} << 38 ||
-      c.c_row_stride >= int64_t{1} << 38 || c.x_row_stride >= int64_t{1} << 38 ||
-      c.out_row_stride >= int64_t{1} << 38)
+      c.c_row_stride >= int64_t{1} << 38)
     return false;  // (what a tensor map holds)
   if (c.dtype != kBF16 || c.state_size % 8 != 0 || c.state_size > 128 || c.head_dim % 4 != 0)
     return false;
@@ -1082,33 +1198,29 @@ int tc_run(const ggrn_scan_call& c, const Params& p, bool cut, cudaStream_t s) {
   tp.fault = device_fault_word();
   if (!tp.fault) return GGRN_ERR_CUDA;
   tp.tile = tile_of(p.P);
-  tp.xtma = p.P % 8 == 0 && mixer::aligned_to(p.x, 16) && p.xs % 8 == 0;
-  tp.otma = p.P % 8 == 0 && mixer::aligned_to(p.out, 16) && p.os % 8 == 0;
+  tp.xvec = p.P % 8 == 0 && mixer::aligned_to(p.x, 16) && p.xs % 8 == 0 ? 16 : 8;
+  tp.ovec = p.P % 8 == 0 && mixer::aligned_to(p.out, 16) && p.os % 8 == 0 ? 16 : 8;
   const cudaError_t e = allow_smem();
   if (e != cudaSuccess) {
     record_cuda_error(e);
     return GGRN_ERR_CUDA;
   }
-  CUtensorMap tm[4];
-  std::memset(tm, 0, sizeof(tm));
-  constexpr CUtensorMapSwizzle k128 = CU_TENSOR_MAP_SWIZZLE_128B, k32 = CU_TENSOR_MAP_SWIZZLE_32B;
-  if (c.rows > 0 &&
-      (!make_map(tm, c.b, c.state_size, c.groups, c.rows, c.b_row_stride, 64, k128) ||
-       !make_map(tm + 1, c.c, c.state_size, c.groups, c.rows, c.c_row_stride, 64, k128) ||
-       (tp.xtma && !make_map(tm + 2, c.x, p.P, p.H, c.rows, c.x_row_stride, 16, k32)) ||
-       (tp.otma && !make_map(tm + 3, c.out, p.P, p.H, c.rows, c.out_row_stride, 16, k32))))
+  CUtensorMap tm_b, tm_c;
+  std::memset(&tm_b, 0, sizeof(tm_b));
+  std::memset(&tm_c, 0, sizeof(tm_c));
+  if (c.rows > 0 && (!make_map(&tm_b, c.b, c.state_size, c.groups, c.rows, c.b_row_stride) ||
+                     !make_map(&tm_c, c.c, c.state_size, c.groups, c.rows, c.c_row_stride)))
     return GGRN_ERR_UNSUPPORTED;
   const dim3 grid(static_cast<unsigned>(p.parts), static_cast<unsigned>(p.H),
                   static_cast<unsigned>((p.P + tp.tile - 1) / tp.tile));
   if (cut) {
-    int st = mixer::launch(k_scan_tc_state, grid, kStateThreads, state_smem(tp.tile), s, tm[0],
-                           tm[2], tp);
+    int st = mixer::launch(k_scan_tc_state, grid, kStateThreads, state_smem(tp.tile), s, tm_b,
+                           tp);
     if (st != GGRN_OK) return st;
     st = launch_join(p, s);
     if (st != GGRN_OK) return st;
   }
-  return mixer::launch(k_scan_tc, grid, kMainThreads, main_smem(tp.tile), s, tm[0], tm[1], tm[2],
-                       tm[3], tp);
+  return mixer::launch(k_scan_tc, grid, kMainThreads, main_smem(tp.tile), s, tm_b, tm_c, tp);
 }
 
 }  // namespace scan
