@@ -20,6 +20,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "ggrn_scan.cuh"
 
@@ -180,48 +181,76 @@ __global__ void __launch_bounds__(kMaxThreads) k_scan(const Params p, const int 
 // ---------------------------------------------------------------------------
 // k_scan_join: the states at the starts of a cut sequence's parts.  The place
 // of part i > 0 holds what part i - 1 adds to the state from a zero start; a
-// thread takes one state entry through the parts of its sequence.  grid:
-// (blocks of entries, heads, sequences).
+// thread takes four entries of a state (V = 4: 16 bytes) or one through the
+// parts of its sequence.  grid: (blocks of entries, heads, cut sequences: there
+// are at most rows / part).
 // ---------------------------------------------------------------------------
+template <int V>
 __global__ void __launch_bounds__(256) k_scan_join(const Params p) {
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t seq = blockIdx.z;
   const int h = blockIdx.y;
-  int64_t begin, end;
-  seq_range(p.q, seq, begin, end);
-  const int64_t count = parts_of(end - begin, p.part);
-  if (count == 1) return;
-  // place of the sequence's first part
-  int64_t first = 0;
+  // the blockIdx.z-th sequence of more than one part, and its first place
+  int64_t seq = -1, first = 0, count = 0;
   if (!p.q.cu) {
+    seq = blockIdx.z;
+    count = parts_of(p.q.each, p.part);
     first = seq * count;
   } else {
     const int lane = threadIdx.x & 31;
-    for (int64_t i = lane; i < seq; i += 32) {
-      int64_t b, e;
-      seq_range(p.q, i, b, e);
-      first += static_cast<int64_t>(part_counts(e - b, p.part) >> 32);
-    }
+    int before = 0;  // cut sequences
+    for (int64_t base = 0; base < p.q.seqs && seq < 0; base += 32) {
+      int64_t b = 0, e = 0;
+      if (base + lane < p.q.seqs) seq_range(p.q, base + lane, b, e);
+      const int mine = static_cast<int>(part_counts(e - b, p.part) >> 32);  // 0: not cut
+      const unsigned cut = __ballot_sync(0xffffffffu, mine > 0);
+      const int found = __popc(cut);
+      const unsigned here =
+          __ballot_sync(0xffffffffu, mine > 0 && before + __popc(cut & ((2u << lane) - 1)) ==
+                                                     static_cast<int>(blockIdx.z) + 1);
+      const int l = here ? __ffs(here) - 1 : 32;
+      int sum = lane < l ? mine : 0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) first += __shfl_xor_sync(0xffffffffu, first, o);
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      first += sum;
+      if (here) {
+        seq = base + l;
+        count = __shfl_sync(0xffffffffu, mine, l);
+      }
+      before += found;
+    }
   }
+  if (seq < 0) return;
   if (first + count > p.places) return;  // offsets that do not ascend: no places for these
   const int64_t PN = static_cast<int64_t>(p.P) * p.N;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) * V;
   if (i >= PN) return;
   const int64_t slot = seq_slot(p.q, seq);
-  float s = slot >= 0 && seq_resumes(p.q, seq)
-                ? p.state[slot * p.slot_stride + static_cast<int64_t>(h) * PN + i]
-                : 0.0f;
+  using W = typename std::conditional<V == 4, float4, float>::type;
+  W s{};
+  if (slot >= 0 && seq_resumes(p.q, seq)) {
+    const float* from = p.state + slot * p.slot_stride + static_cast<int64_t>(h) * PN + i;
+    if constexpr (V == 4) {  // (the pool need not be aligned)
+      s = make_float4(from[0], from[1], from[2], from[3]);
+    } else {
+      s = *from;
+    }
+  }
   float* w = p.ws + (first * p.H + h) * PN + i;
   const float* decay = p.ws_decay + first * p.H + h;
-  w[0] = s;
+  *reinterpret_cast<W*>(w) = s;
   const int64_t stride = static_cast<int64_t>(p.H) * PN;
   for (int64_t k = 0; k + 1 < count; ++k) {
     w += stride;
-    s = fmaf(s, decay[k * p.H], *w);
-    *w = s;
+    const float d = decay[k * p.H];
+    const W add = *reinterpret_cast<const W*>(w);
+    if constexpr (V == 4) {
+      s.x = fmaf(s.x, d, add.x), s.y = fmaf(s.y, d, add.y);
+      s.z = fmaf(s.z, d, add.z), s.w = fmaf(s.w, d, add.w);
+    } else {
+      s = fmaf(s, d, add);
+    }
+    *reinterpret_cast<W*>(w) = s;
   }
 }
 
@@ -533,9 +562,12 @@ int run(const ggrn_scan_call* call, bool step, void* stream) {
 
 int launch_join(const Params& p, cudaStream_t s) {
   const int64_t pn = static_cast<int64_t>(p.P) * p.N;
-  const dim3 grid(static_cast<unsigned>((pn + 255) / 256), static_cast<unsigned>(p.H),
-                  static_cast<unsigned>(p.q.seqs));
-  return mixer::launch(k_scan_join, grid, 256, 0, s, p);
+  const int v = pn % 4 == 0 ? 4 : 1;
+  const int64_t cut = std::min(p.q.seqs, p.q.cu ? p.q.rows / p.part : p.q.seqs);
+  const dim3 grid(static_cast<unsigned>((pn / v + 255) / 256), static_cast<unsigned>(p.H),
+                  static_cast<unsigned>(cut));
+  return v == 4 ? mixer::launch(k_scan_join<4>, grid, 256, 0, s, p)
+                : mixer::launch(k_scan_join<1>, grid, 256, 0, s, p);
 }
 
 }  // namespace scan

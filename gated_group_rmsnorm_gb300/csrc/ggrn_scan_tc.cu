@@ -126,25 +126,6 @@ struct Deal {
   }
 };
 
-// The same chunks in rounds of a number of threads that is no multiple of the
-// atoms: a round's chunk is found from the last one's.
-struct Round {
-  int rows4, a, rows_step, a_step, atoms, r, ck;
-  __device__ __forceinline__ Round(int t, int threads, int n)
-      : rows4((t >> 3) / n), a((t >> 3) % n), rows_step((threads >> 3) / n),
-        a_step((threads >> 3) % n), atoms(n), r((t & 7) >> 1), ck(t & 1) {}
-  __device__ __forceinline__ void next() {
-    rows4 += rows_step, a += a_step;
-    if (a >= atoms) a -= atoms, ++rows4;
-  }
-  __device__ __forceinline__ int row() const { return 4 * rows4 + r; }
-  __device__ __forceinline__ int col() const { return 16 * a + 8 * ck; }
-  __device__ __forceinline__ uint32_t at() const {
-    return static_cast<uint32_t>(a * static_cast<int>(kAtomBytes) + row() * 32 +
-                                 (((ck ^ rows4) & 1) << 4));
-  }
-};
-
 __device__ __forceinline__ void tmem_ld16_nowait(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
@@ -208,6 +189,30 @@ __device__ __forceinline__ F2 wide(uint32_t u) {
   return pk2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
 }
 
+// dt_of without branches or calls: softplus(v) = max(v, 0) + log1p(u), u =
+// exp(-|v|), and log1p(u) = 2 atanh(r), r = u / (2 + u) <= 1/3, by its series up
+// to r^15 (the next term is below 2^-27 of the first), so that a small dt keeps
+// its relative accuracy: 2^-22 for u's exponential, |v| 2^-24 for its argument,
+// 2^-22 for the quotient.
+__device__ __forceinline__ float dt_of_fast(float raw, float bias, const Params& p) {
+  float v = raw + bias;
+  if (p.softplus) {
+    const float u = ex2_approx(-kLog2e * fabsf(v));
+    const float r = u * rcp_approx(2.0f + u), q = r * r;
+    float t = 1.0f / 15;
+    t = fmaf(t, q, 1.0f / 13);
+    t = fmaf(t, q, 1.0f / 11);
+    t = fmaf(t, q, 1.0f / 9);
+    t = fmaf(t, q, 1.0f / 7);
+    t = fmaf(t, q, 1.0f / 5);
+    t = fmaf(t, q, 1.0f / 3);
+    t = fmaf(t * q, r, r);
+    v = fmaf(2.0f, t, v > 0.0f ? v : v != v ? v : 0.0f);
+  }
+  v = v < p.dt_min ? p.dt_min : v;
+  return v > p.dt_max ? p.dt_max : v;
+}
+
 // The decays of one chunk, by one warp: dt of token 32 b + lane comes from
 // `raw[b]` (tokens from `left` on count for nothing), goes through `s_dt`, and
 // lane k takes tokens 4 k .. 4 k + 3, so that the blocks of 32 tokens are
@@ -220,12 +225,9 @@ struct Decays {
 __device__ __forceinline__ float make_decays(const float (&raw)[4], int left, float bias, float a2,
                                              const Params& p, float* s_dt, Decays& d) {
   const int lane = threadIdx.x & 31;
-  float r = raw[0];
-#pragma unroll 1
-  for (int b = 0; b < 4; ++b) {
-    s_dt[32 * b + lane] = 32 * b + lane < left ? dt_of(r, bias, p) : 0.0f;
-    r = b == 0 ? raw[1] : b == 1 ? raw[2] : raw[3];
-  }
+#pragma unroll
+  for (int b = 0; b < 4; ++b)
+    s_dt[32 * b + lane] = 32 * b + lane < left ? dt_of_fast(raw[b], bias, p) : 0.0f;
   __syncwarp();
   const float4 v = *reinterpret_cast<const float4*>(s_dt + 4 * lane);
   d.dt[0] = v.x, d.dt[1] = v.y, d.dt[2] = v.z, d.dt[3] = v.w;
@@ -458,10 +460,21 @@ enum Bar {
   kBars = 24
 };
 
+// STATE_ONLY: the state a part adds from a zero start, and its decay (a cut
+// sequence's parts but the last): dS and S alone; the warps of M and Y but the
+// copying one have nothing to do.
+template <bool STATE_ONLY>
 __global__ void __launch_bounds__(kMainThreads, 1)
     k_scan_tc(const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ CUtensorMap tm_c,
               const TcParams tp) {
   const Params& p = tp.p;
+  pdl_wait();
+  pdl_launch_dependents();
+  const Part part = find_part(p.q, p.part, blockIdx.x);
+  // (offsets that do not ascend may count more places than there are)
+  if (part.seq < 0 || (STATE_ONLY && part.index == part.count - 1) ||
+      (part.count > 1 && part.place + (STATE_ONLY ? 1 : 0) >= p.places))
+    return;
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw_u = smem_u32(smem_raw);
   const uint32_t base_u = (raw_u + 1023u) & ~1023u;
@@ -485,7 +498,7 @@ __global__ void __launch_bounds__(kMainThreads, 1)
                       : i == kMFull                           ? kMWarps
                       : i == kSFull                           ? kSWarps
                       : i == kYRead || i == kYPut || i == kYPut + 1 ? kYWarps
-                      : i >= kDtFree && i < kDtFree + kDecays ? kSWarps + kYWarps
+                      : i >= kDtFree && i < kDtFree + kDecays ? kSWarps + (STATE_ONLY ? 0 : kYWarps)
                                                               : 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -496,35 +509,32 @@ __global__ void __launch_bounds__(kMainThreads, 1)
   tc_fence_after();
   const uint32_t tmem = s_misc[0];
   const uint32_t t_ds = tmem + kColDs, t_y1 = t_ds + tp.tile, t_y2 = t_y1 + tp.tile;
-  pdl_wait();
-  pdl_launch_dependents();
-
-  const Part part = find_part(p.q, p.part, blockIdx.x);
   const int P = p.P, N = p.N;
   const int h = blockIdx.y, g = h / p.hpg;
   const int col0 = blockIdx.z * tp.tile;         // first column of the head here
   const int pw = min(tp.tile, P - col0);         // and how many
   const int64_t hcol = static_cast<int64_t>(h) * P + col0;
-  const bool run = part.seq >= 0 && !(part.count > 1 && part.place >= p.places);
-  const int rows = run ? static_cast<int>(part.end - part.begin) : 0;
+  const int rows = static_cast<int>(part.end - part.begin);
   const int chunks = (rows + kQ - 1) / kQ;
   const Waits wait = {s_misc + 1};
   // the state this part starts from (zeros without one) and the one it leaves
   const float* from = nullptr;
   float* to = nullptr;
-  if (run) {
+  {
     const int64_t held = static_cast<int64_t>(P) * N, at = h * held + static_cast<int64_t>(col0) * N;
     const int64_t entry = seq_slot(p.q, part.seq);
-    if (part.count > 1) from = p.ws + part.place * p.H * held + at;
-    else if (entry >= 0 && seq_resumes(p.q, part.seq)) from = p.state + entry * p.slot_stride + at;
-    if (part.index == part.count - 1 && entry >= 0) to = p.state + entry * p.slot_stride + at;
+    if (STATE_ONLY) {
+      to = p.ws + (part.place + 1) * p.H * held + at;
+    } else {
+      if (part.count > 1) from = p.ws + part.place * p.H * held + at;
+      else if (entry >= 0 && seq_resumes(p.q, part.seq)) from = p.state + entry * p.slot_stride + at;
+      if (part.index == part.count - 1 && entry >= 0) to = p.state + entry * p.slot_stride + at;
+    }
   }
   // Each phase of a barrier is waited for in turn: a parity tells a phase from
   // its neighbours only.  What may run ahead of a waiter by more is by buffer.
 
-  if (!run) {
-    // nothing: fall through to the end
-  } else if (warp == kWarpMma) {
+  if (warp == kWarpMma) {
     // ---- the products (the whole warp waits, one lane issues) ----
     const uint32_t id_g = idesc_bf16(128, 128);
     const uint32_t id_ds = idesc_bf16(128, tp.tile) | kTransA | kTransB;
@@ -532,38 +542,25 @@ __global__ void __launch_bounds__(kMainThreads, 1)
     const uint64_t d_s = desc_t32(sS), d_w = desc_t32(sW), d_c = desc_sw128(sC);
     const uint32_t piece = x_bytes >> 4;
     const int ksteps = (N + 15) / 16;
-    // It copies B and C too, each as soon as the products that read the ones
-    // before are known to be done.
-    const int boxes = N > 64 ? 2 : 1;
-    auto copy = [&](const CUtensorMap* map, uint32_t to, int c, uint32_t full) {
-      if (lane == 0) {
-        mbar_expect_tx(full, boxes * (kRowsBytes / 2));
-#pragma unroll 1
-        for (int i = 0; i < boxes; ++i)
-          tma_load_3d(to + i * (kRowsBytes / 2), map, 64 * i, g,
-                      static_cast<int>(part.begin) + c * kQ, full);
-      }
-      __syncwarp();
-    };
     bool ok = true;
     // chunk c's C S, dS and M X, then the next one's G
 #pragma unroll 1
-    for (int c = -1; c < chunks; ++c) {
+    for (int c = STATE_ONLY ? 0 : -1; c < chunks; ++c) {
       const int n = c + 1, buf = n & 1;
-      if (n < chunks) {
-        if (n >= 2 && !(ok = wait.warp(bar(kBFree + buf), (n >> 1) - 1))) break;
-        copy(&tm_b, sB + buf * kRowsBytes, n,
-             bar(rows - n * kQ < kQ ? static_cast<int>(kTail) : kBFull + buf));
-      }
       if (c >= 0) {
         // C S (S of the chunk before, Y and dS read)
-        if (!(ok = wait.warp(bar(kSFull), c) && (c == 0 || wait.warp(bar(kYRead), c - 1)))) break;
-        tc_fence_after();
-        if (elect_one()) {
-          issue_rows<kTransB>(t_y1, d_c, d_s, ksteps, id_y);
-          mma_commit(bar(kCFree));
+        if (!(ok = wait.warp(bar(kSFull), c))) break;
+        if (!STATE_ONLY) {
+          if (c > 0 && !(ok = wait.warp(bar(kYRead), c - 1))) break;
+          tc_fence_after();
+          if (elect_one()) {
+            issue_rows<kTransB>(t_y1, d_c, d_s, ksteps, id_y);
+            mma_commit(bar(kCFree));
+          }
+          __syncwarp();
+        } else if (!(ok = wait.warp(bar(kBFull + (c & 1)), c >> 1))) {
+          break;
         }
-        __syncwarp();
         // dS
         if (!(ok = wait.warp(bar(kWFull), c))) break;
         tc_fence_after();
@@ -573,12 +570,7 @@ __global__ void __launch_bounds__(kMainThreads, 1)
           mma_commit(bar(kBFree + (c & 1)));
         }
         __syncwarp();
-      }
-      if (n < chunks) {
-        if (c >= 0 && !(ok = wait.warp(bar(kCFree), c))) break;
-        copy(&tm_c, sC, n, bar(kCFull));
-      }
-      if (c >= 0) {
+        if (STATE_ONLY) continue;
         // M X
         if (!(ok = wait.warp(bar(kMFull), c))) break;
         tc_fence_after();
@@ -601,6 +593,8 @@ __global__ void __launch_bounds__(kMainThreads, 1)
         __syncwarp();
       }
     }
+    // the last products are done before the tensor memory is freed
+    if (STATE_ONLY && ok) ok = wait.warp(bar(kDsDone), chunks - 1);
     // no product may still run when the tensor memory is freed, and no copy be
     // on its way into shared memory: after a timeout, wait on a barrier of the
     // products' own, and as long again on one that nothing completes
@@ -614,24 +608,48 @@ __global__ void __launch_bounds__(kMainThreads, 1)
       mbar_wait(bar(kBars), 1);
     }
   } else if (warp == kWarpDt) {
-    // ---- the decays, chunks ahead, and the end of a part's last B ----
+    // ---- B and C, as soon as what read the ones before is done, and the
+    // decays of the chunk behind ----
+    const int boxes = N > 64 ? 2 : 1;
+    auto copy = [&](const CUtensorMap* map, uint32_t to_smem, int c, uint32_t full) {
+      if (lane == 0) {
+        mbar_expect_tx(full, boxes * (kRowsBytes / 2));
+        for (int i = 0; i < boxes; ++i)
+          tma_load_3d(to_smem + i * (kRowsBytes / 2), map, 64 * i, g,
+                      static_cast<int>(part.begin) + c * kQ, full);
+      }
+      __syncwarp();
+    };
     const float a2 = __ldg(p.a + h) * kLog2e;
     const float bias = p.dt_bias ? __ldg(p.dt_bias + h) : 0.0f;
     const __nv_bfloat16* dtp = static_cast<const __nv_bfloat16*>(p.dt) + part.begin * p.dts + h;
-    float raw[4];
+    float log_total = 0.0f;
     int slot = 0, use = 0;
-    bool ok = true;
 #pragma unroll 1
-    for (int c = 0; c < chunks; ++c) {
+    for (int c = -1; c < chunks; ++c) {
+      float raw[4];  // of the next chunk
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        const int t = c * kQ + 32 * b + lane;
+        const int t = (c + 1) * kQ + 32 * b + lane;
         raw[b] = t < rows ? Bf::load1(dtp + t * p.dts, 0) : 0.0f;
       }
-      if (use > 0 && !(ok = wait.warp(bar(kDtFree + slot), use - 1))) break;
+      // (the first chunk's copies before its decays, the others' behind them)
+      const int n = c < 0 ? 0 : c;
+      if (n < chunks && c != 0) {
+        const int left = rows - n * kQ, buf = n & 1;
+        const uint32_t b_at = sB + buf * kRowsBytes;
+        if (n >= 2 && !wait.warp(bar(kBFree + buf), (n >> 1) - 1)) break;
+        copy(&tm_b, b_at, n, bar(left < kQ ? static_cast<int>(kTail) : kBFull + buf));
+        if (!STATE_ONLY) {
+          if (n >= 1 && !wait.warp(bar(kCFree), n - 1)) break;
+          copy(&tm_c, sC, n, bar(kCFull));
+        }
+      }
+      if (c + 1 == chunks) break;
+      if (use > 0 && !wait.warp(bar(kDtFree + slot), use - 1)) break;
       float* s = s_decay + slot * kDecayFloats;
       Decays d;
-      const float total = make_decays(raw, rows - c * kQ, bias, a2, p, s + 2 * kQ, d);
+      const float total = make_decays(raw, rows - (c + 1) * kQ, bias, a2, p, s + 2 * kQ, d);
       float* t = s + 4 * lane;
       sts_f4(t, d.pre[0], d.pre[1], d.pre[2], d.pre[3]);
       float f[4];
@@ -646,17 +664,20 @@ __global__ void __launch_bounds__(kMainThreads, 1)
       sts_f4(t + 4 * kQ, f[0], f[1], f[2], f[3]);
       if ((lane & 7) == 0) s[5 * kQ + (lane >> 3)] = d.block;
       if (lane == 0) s[5 * kQ + 4] = ex2_approx(total);
+      log_total += total;
       warp_arrive(bar(kDtFull + slot));
       if (++slot == kDecays) slot = 0, ++use;
     }
+    if (STATE_ONLY && lane == 0 && blockIdx.z == 0)
+      p.ws_decay[part.place * p.H + h] = ex2_approx(log_total);
     const int left = rows - (chunks - 1) * kQ;
-    if (ok && chunks > 0 && left < kQ && wait.warp(bar(kTail), 0)) {
+    if (chunks > 0 && left < kQ && wait.warp(bar(kTail), 0)) {
       // rows of other sequences, or of none, count for nothing, whatever they
       // hold
       const int buf = (chunks - 1) & 1;
 #pragma unroll 1
       for (int i = lane; i < (kQ - left) * 8; i += 32)
-        for (int j = 0; j < (N > 64 ? 2 : 1); ++j)
+        for (int j = 0; j < boxes; ++j)
           sts16(sB + buf * kRowsBytes + j * (kRowsBytes / 2) + left * 128 + i * 16,
                 make_uint4(0, 0, 0, 0));
       fence_async_smem();
@@ -703,7 +724,7 @@ __global__ void __launch_bounds__(kMainThreads, 1)
         }
         const int n = c + 1;  // the chunk to come into the place of n - 2
         const uint32_t x_at = sX + (n & 1) * x_bytes + deal.at;
-        if (n >= 2) {
+        if (!STATE_ONLY && n >= 2) {
           const bool ok = warp != kWarpX || wait.warp(bar(kYPut + (n & 1)), (n >> 1) - 1);
           if (!group_sync(1, threads, ok)) break;
           const int left = rows - (n - 2) * kQ - deal.row;
@@ -743,10 +764,10 @@ __global__ void __launch_bounds__(kMainThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
     int slot = 0, use = 0;
 #pragma unroll 1
-    for (int c = 0; c < chunks; ++c) {
+    for (int c = 0; c < (STATE_ONLY ? 0 : chunks); ++c) {
       // (G done: and the M before is read, by products issued earlier)
       bool ok = true;
-      if (warp == 0) ok = wait.warp(bar(kDtFull + slot), use) && wait.warp(bar(kGDone), c);
+      if (q == 0) ok = wait.warp(bar(kDtFull + slot), use) && wait.warp(bar(kGDone), c);
       if (!group_sync(2, kMWarps * 32, ok)) break;
       tc_fence_after();
       const float* sd = s_decay + slot * kDecayFloats;
@@ -813,10 +834,12 @@ __global__ void __launch_bounds__(kMainThreads, 1)
         for (int j = 0; j < 8; ++j, f += 2 * N)
           if (first + 16 * kSShare * k + 2 * j < pw) s[k][j] = pk2(f[0], f[N]);  // (pw is even)
     }
+    if (!STATE_ONLY) {
 #pragma unroll
-    for (int k = 0; k < kSAtoms; ++k)
-      if (hf + kSShare * k < atoms) put(k);
-    fence_async_smem();
+      for (int k = 0; k < kSAtoms; ++k)
+        if (hf + kSShare * k < atoms) put(k);
+      fence_async_smem();
+    }
     warp_arrive(bar(kSFull));
     int slot = 0, use = 0;
 #pragma unroll 1
@@ -835,10 +858,10 @@ __global__ void __launch_bounds__(kMainThreads, 1)
           tmem_ld16(t_ds + lanes + a * 16, r);
 #pragma unroll
           for (int j = 0; j < 8; ++j) s[k][j] = fma2(s[k][j], decay2, pair(r[2 * j], r[2 * j + 1]));
-          put(k);
+          if (!STATE_ONLY) put(k);
         }
       }
-      fence_async_smem();
+      if (!STATE_ONLY) fence_async_smem();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -865,7 +888,7 @@ __global__ void __launch_bounds__(kMainThreads, 1)
     const uint32_t at0 = chunk_at(i, 0);
     int slot = 0, use = 0;
 #pragma unroll 1
-    for (int c = 0; c < chunks; ++c) {
+    for (int c = 0; c < (STATE_ONLY ? 0 : chunks); ++c) {
       bool ok = true;
       if (warp == kWarpY) ok = wait.warp(bar(kDtFull + slot), use) && wait.warp(bar(kYDone), c);
       if (!group_sync(4, kYWarps * 32, ok)) break;
@@ -909,204 +932,14 @@ __global__ void __launch_bounds__(kMainThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
-// k_scan_tc_state: the state a part adds from a zero start, and its decay (a
-// cut sequence's parts but the last; all their chunks are full).  Two CTAs per
-// SM, whose stages overlap: one warp copies B, 8 warps copy X into the place of
-// the largest piece of w X and write the pieces, one warp issues dS, the 8 warps
-// add it to S in registers.
-// ---------------------------------------------------------------------------
-constexpr int kStateThreads = 11 * 32;
-
-__global__ void __launch_bounds__(kStateThreads, 2)
-    k_scan_tc_state(const __grid_constant__ CUtensorMap tm_b, const TcParams tp) {
-  constexpr int AW = (kMaxAtoms + 1) / 2;       // atoms of a warp
-  const Params& p = tp.p;
-  extern __shared__ unsigned char smem_raw[];
-  const uint32_t raw_u = smem_u32(smem_raw);
-  const uint32_t base_u = (raw_u + 1023u) & ~1023u;
-  unsigned char* base = smem_raw + (base_u - raw_u);
-  const int atoms = tp.tile / 16;
-  const uint32_t x_bytes = atoms * kAtomBytes;
-  const uint32_t sB = base_u, sW = sB + kRowsBytes;
-  const uint32_t decay_off = kRowsBytes + 3 * x_bytes;
-  float* s_decay = reinterpret_cast<float*>(base + decay_off);  // [2][kQ + 4]: w, decay
-  const uint32_t bars_off = decay_off + 2 * (kQ + 4) * 4;
-  volatile uint32_t* s_misc = reinterpret_cast<uint32_t*>(base + bars_off + 32);
-  // per chunk: B landed; w X written; decays made; dS computed
-  const uint32_t b_b = base_u + bars_off, b_w = b_b + 8, b_dt = b_b + 16, b_ds = b_b + 24;
-
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) {
-    mbar_init(b_b, 1);
-    mbar_init(b_w, 8);
-    mbar_init(b_dt, 1);
-    mbar_init(b_ds, 1);
-    s_misc[1] = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
-  if (warp == 8) tmem_alloc(smem_u32(const_cast<uint32_t*>(s_misc)), 128);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = s_misc[0];
-  pdl_wait();
-  pdl_launch_dependents();
-
-  const Part part = find_part(p.q, p.part, blockIdx.x);
-  const int P = p.P, N = p.N;
-  const int h = blockIdx.y;
-  const int col0 = blockIdx.z * tp.tile, pw = min(tp.tile, P - col0);
-  // (offsets that do not ascend may count more places than there are)
-  const bool run = part.seq >= 0 && part.index < part.count - 1 && part.place + 1 < p.places;
-  const int rows = run ? static_cast<int>(part.end - part.begin) : 0;
-  const int chunks = rows / kQ;
-  const Waits wait = {s_misc + 1};
-
-  if (!run) {
-    // nothing: fall through to the end
-  } else if (warp == 8) {
-    const uint32_t id_ds = idesc_bf16(128, tp.tile) | kTransA | kTransB;
-#pragma unroll 1
-    for (int c = 0; c < chunks; ++c) {
-      if (!wait.warp(b_b, c) || !wait.warp(b_w, c)) break;
-      tc_fence_after();
-      if (elect_one()) {
-        issue_ds(tmem, desc_t128(sB, kRowsBytes / 2), desc_t32(sW), x_bytes >> 4, id_ds);
-        mma_commit(b_ds);
-      }
-      __syncwarp();
-      // (waited for here too, so that none runs when the memory is freed)
-      if (!wait.warp(b_ds, c)) break;
-    }
-  } else if (warp == 9) {
-    const float a2 = __ldg(p.a + h) * kLog2e;
-    const float bias = p.dt_bias ? __ldg(p.dt_bias + h) : 0.0f;
-    const __nv_bfloat16* dtp = static_cast<const __nv_bfloat16*>(p.dt) + part.begin * p.dts + h;
-    float raw[4];
-    auto fetch = [&](int c) {
-#pragma unroll
-      for (int b = 0; b < 4; ++b)
-        raw[b] = Bf::load1(dtp + static_cast<int64_t>(c * kQ + 32 * b + lane) * p.dts, 0);
-    };
-    fetch(0);
-    float log_total = 0.0f;
-#pragma unroll 1
-    for (int c = 0; c < chunks; ++c) {
-      // this half was last read for chunk c - 2 (each phase waited for in turn)
-      if (c >= 1 && !wait.warp(b_w, c - 1)) break;
-      float* s = s_decay + (c & 1) * (kQ + 4);
-      Decays d;
-      const float total = make_decays(raw, kQ, bias, a2, p, s, d);
-      if (c + 1 < chunks) fetch(c + 1);
-      float f[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) f[k] = d.dt[k] * ex2_approx(d.suf[k] + d.after);
-      sts_f4(s + 4 * lane, f[0], f[1], f[2], f[3]);
-      if (lane == 0) s[kQ] = ex2_approx(total);
-      log_total += total;
-      warp_arrive(b_dt);
-    }
-    if (lane == 0 && blockIdx.z == 0) p.ws_decay[part.place * p.H + h] = ex2_approx(log_total);
-  } else if (warp == 10) {
-    const int boxes = N > 64 ? 2 : 1, g = h / p.hpg;
-    const uint32_t bytes = boxes * (kRowsBytes / 2);
-    bool ok = true;
-#pragma unroll 1
-    for (int c = 0; c < chunks; ++c) {
-      const int row = static_cast<int>(part.begin) + c * kQ;
-      if (c > 0 && !(ok = wait.warp(b_ds, c - 1))) break;
-      if (lane == 0) {
-        mbar_expect_tx(b_b, bytes);
-#pragma unroll 1
-        for (int i = 0; i < boxes; ++i)
-          tma_load_3d(sB + i * (kRowsBytes / 2), &tm_b, 64 * i, g, row, b_b);
-      }
-    }
-    // every copy has landed before the CTA leaves
-    if (ok) wait.warp(b_b, chunks - 1);
-  } else {
-    const int q = warp & 3, hf = warp >> 2, n = 32 * q + lane;
-    const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
-    const Round deal(tid, 256, atoms);
-    const __nv_bfloat16* x0 = static_cast<const __nv_bfloat16*>(p.x) + part.begin * p.xs +
-                              static_cast<int64_t>(h) * P + col0;
-    auto fetch = [&](int c) {
-      const __nv_bfloat16* xn = x0 + static_cast<int64_t>(c) * kQ * p.xs;
-      Round d = deal;
-#pragma unroll 1
-      for (int i = 0; i < atoms; ++i, d.next())
-        copy_x(sW + d.at(), xn + d.row() * p.xs + d.col(), x0, d.col(), pw, true, tp.xvec == 16);
-    };
-    fetch(0);
-    F2 s[AW][8];
-#pragma unroll
-    for (int k = 0; k < AW; ++k)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s[k][j] = 0;
-#pragma unroll 1
-    for (int c = 0; c < chunks; ++c) {
-      const float* sd = s_decay + (c & 1) * (kQ + 4);
-      if (!group_sync(1, 256, warp != 0 || wait.warp(b_dt, c))) break;
-      const F2 decay2 = pk2(sd[kQ], sd[kQ]);
-      cp_async_wait();
-      Round d = deal;
-#pragma unroll 1
-      for (int i = 0; i < atoms; ++i, d.next()) {
-        const uint32_t at = sW + d.at();
-        uint4 u[3];
-        pieces_of(lds16(at), sd[d.row()], u);
-#pragma unroll
-        for (int j = 0; j < 3; ++j) sts16(at + j * x_bytes, u[j]);
-      }
-      fence_async_smem();
-      tc_fence_before();
-      warp_arrive(b_w);
-      if (!group_sync(1, 256, warp != 0 || wait.warp(b_ds, c))) break;
-      tc_fence_after();
-      if (c + 1 < chunks) fetch(c + 1);
-#pragma unroll
-      for (int k = 0; k < AW; ++k) {
-        const int a = hf + 2 * k;
-        if (a < atoms) {
-          uint32_t v[16];
-          tmem_ld16(tmem + lanes + a * 16, v);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) s[k][j] = fma2(s[k][j], decay2, pair(v[2 * j], v[2 * j + 1]));
-        }
-      }
-      tc_fence_before();
-    }
-    cp_async_wait();
-    if (n < N) {
-      float* to = p.ws + ((part.place + 1) * p.H + h) * static_cast<int64_t>(P) * N +
-                  static_cast<int64_t>(col0 + 16 * hf) * N + n;
-#pragma unroll
-      for (int k = 0; k < AW; ++k, to += 16 * N)
-#pragma unroll
-        for (int j = 0; j < 8; ++j, to += 2 * N)
-          if (16 * (hf + 2 * k) + 2 * j < pw) upk2(s[k][j], to[0], to[N]);
-    }
-  }
-  tc_fence_before();
-  __syncthreads();
-  if (tid == 0 && s_misc[1]) atomicOr(tp.fault, kFaultScanWait);
-  if (warp == 8) {
-    tc_fence_after();
-    tmem_dealloc(tmem, 128);
-  }
-}
-
-// ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
+// Times in chunks (see tc_part_rows).
+constexpr double kStartChunks = 4.0, kStateShare = 0.6, kJoinChunks = 3.0;
 uint32_t main_smem(int tile) {
   return 1024 + 3 * kRowsBytes + 6 * (tile / 16 * kAtomBytes) + kDecays * kDecayFloats * 4 +
          8 * kBars + 16;
 }
-uint32_t state_smem(int tile) {
-  return 1024 + kRowsBytes + 3 * (tile / 16 * kAtomBytes) + 2 * (kQ + 4) * 4 + 32 + 8;
-}
-
 int tile_of(int64_t P) {
   const int64_t tiles = (P + 16 * kMaxAtoms - 1) / (16 * kMaxAtoms);
   return static_cast<int>(((P + tiles - 1) / tiles + 15) / 16 * 16);
@@ -1116,11 +949,10 @@ cudaError_t allow_smem() {
   static std::once_flag once;
   static cudaError_t err = cudaSuccess;
   std::call_once(once, [] {
-    err = cudaFuncSetAttribute(k_scan_tc, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               static_cast<int>(main_smem(16 * kMaxAtoms)));
+    const int bytes = static_cast<int>(main_smem(16 * kMaxAtoms));
+    err = cudaFuncSetAttribute(k_scan_tc<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (err == cudaSuccess)
-      err = cudaFuncSetAttribute(k_scan_tc_state, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(state_smem(16 * kMaxAtoms)));
+      err = cudaFuncSetAttribute(k_scan_tc<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   });
   return err;
 }
@@ -1163,11 +995,11 @@ bool tc_covers(const ggrn_scan_call& c) {
 }
 
 // Rows of a part.  The launch's time goes by its waves of one CTA per SM, each
-// as long as a part's chunks (and about one more to start and end); a cut
-// costs the state-only launch over the same chunks (about half of a chunk's
-// time, two CTAs per SM) and the join.  The lengths behind cu_seqlens are not
-// known here: sequences are taken for equally long, and where those stay
-// whole a part is twice their length, so that only longer ones are cut.
+// as long as a part's chunks and about four more to start and end; a cut costs
+// the state-only launch over the same chunks (a bit over half of a chunk's
+// time) and the join.  The lengths behind cu_seqlens are not known here:
+// sequences are taken for equally long, and where those stay whole a part is
+// twice their length, so that only longer ones are cut.
 int64_t tc_part_rows(const ggrn_scan_call& c, int64_t longest) {
   const int64_t tiles = (c.head_dim + tile_of(c.head_dim) - 1) / tile_of(c.head_dim);
   const int64_t heads = c.heads * tiles, sms = device_sms();
@@ -1181,9 +1013,10 @@ int64_t tc_part_rows(const ggrn_scan_call& c, int64_t longest) {
   for (int64_t cuts = 1; cuts <= std::min<int64_t>(all, 64); ++cuts) {
     const int64_t k = (all + cuts - 1) / cuts;
     const int64_t parts = (all + k - 1) / k;
-    double cost = static_cast<double>(waves(seqs * parts * heads)) * (k + 1.0);
+    double cost = static_cast<double>(waves(seqs * parts * heads)) * (k + kStartChunks);
     if (parts > 1)
-      cost += 0.5 * static_cast<double>(waves((seqs * (parts - 1) * heads + 1) / 2)) * (k + 1.0) + 2.0;
+      cost += static_cast<double>(waves(seqs * (parts - 1) * heads)) *
+                  (kStateShare * k + kStartChunks) + kJoinChunks;
     if (cuts == 1 || cost < best_cost) {
       best = k;
       best_cost = cost;
@@ -1214,13 +1047,13 @@ int tc_run(const ggrn_scan_call& c, const Params& p, bool cut, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>(p.parts), static_cast<unsigned>(p.H),
                   static_cast<unsigned>((p.P + tp.tile - 1) / tp.tile));
   if (cut) {
-    int st = mixer::launch(k_scan_tc_state, grid, kStateThreads, state_smem(tp.tile), s, tm_b,
+    int st = mixer::launch(k_scan_tc<true>, grid, kMainThreads, main_smem(tp.tile), s, tm_b, tm_c,
                            tp);
     if (st != GGRN_OK) return st;
     st = launch_join(p, s);
     if (st != GGRN_OK) return st;
   }
-  return mixer::launch(k_scan_tc, grid, kMainThreads, main_smem(tp.tile), s, tm_b, tm_c, tp);
+  return mixer::launch(k_scan_tc<false>, grid, kMainThreads, main_smem(tp.tile), s, tm_b, tm_c, tp);
 }
 
 }  // namespace scan
