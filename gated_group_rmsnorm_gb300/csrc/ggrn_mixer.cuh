@@ -59,24 +59,30 @@ __device__ __forceinline__ int64_t parts_of(int64_t n, int64_t part) {
                    : (static_cast<uint32_t>(n) + static_cast<uint32_t>(part) - 1) /
                          static_cast<uint32_t>(part);
 }
-// Parts (low word) and places (high word) of a sequence of n rows.
+// Parts, or (INNER) parts but the last, in the low word and places in the high
+// word, of a sequence of n rows.
+template <bool INNER = false>
 __device__ __forceinline__ uint64_t part_counts(int64_t n, int64_t part) {
   const uint64_t k = static_cast<uint64_t>(parts_of(n, part));
-  return k > 1 ? k | (k << 32) : k;
+  return (INNER ? k - 1 : k) | (k > 1 ? k << 32 : 0);
 }
-// Found by a whole warp: lanes take 32 sequences at a time and scan their
-// counts (which stay below 2^32: the host limits rows to 2^31 with cu).
+// Part `number` of all, or (INNER) of those that are not the last of their
+// sequence: whole ones, at most rows / part.  Found by a whole warp: lanes take
+// 32 sequences at a time and scan their counts (which stay below 2^32: the host
+// limits rows to 2^31 with cu).
+template <bool INNER>
 __device__ __forceinline__ Part find_part(const Seqs& q, int64_t part, int64_t number) {
   Part r;
   if (!q.cu) {
-    const int64_t per = parts_of(q.each, part);
+    const int64_t per = parts_of(q.each, part), each = INNER ? per - 1 : per;
+    if (each == 0) return r;
     const int64_t s =
-        static_cast<uint32_t>(number) / static_cast<uint32_t>(per);  // (a grid's index)
+        static_cast<uint32_t>(number) / static_cast<uint32_t>(each);  // (a grid's index)
     if (s >= q.seqs) return r;
     r.seq = s;
-    r.index = number - s * per;
+    r.index = number - s * each;
     r.count = per;
-    r.place = number;
+    r.place = s * per + r.index;
     r.begin = s * q.each + r.index * part;
     const int64_t e = (s + 1) * q.each;
     r.end = r.begin + part < e ? r.begin + part : e;
@@ -89,7 +95,7 @@ __device__ __forceinline__ Part find_part(const Seqs& q, int64_t part, int64_t n
     uint64_t n = 0;
     if (base + lane < q.seqs) {
       seq_range(q, base + lane, b, e);
-      n = part_counts(e - b, part);
+      n = part_counts<INNER>(e - b, part);
     }
     uint64_t inc = n;  // inclusive scan
 #pragma unroll

@@ -53,8 +53,8 @@ __global__ void __launch_bounds__(kMaxThreads) k_scan(const Params p, const int 
   float* sDt = sY + kBlock * prows;          // [kBlock] dt, [kBlock] decay
   pdl_wait();
   pdl_launch_dependents();
-  const Part part = find_part(p.q, p.part, blockIdx.x);
-  if (part.seq < 0 || (STATE_ONLY && part.index == part.count - 1)) return;
+  const Part part = find_part<STATE_ONLY>(p.q, p.part, blockIdx.x);
+  if (part.seq < 0) return;
   // (offsets that do not ascend may count more places than there are)
   if (part.count > 1 && part.place + (STATE_ONLY ? 1 : 0) >= p.places) return;
   const int h = blockIdx.y, g = h / p.hpg;
@@ -497,8 +497,8 @@ int run_typed(const ggrn_scan_call& c, Params& p, const Layout& l, cudaStream_t 
   const dim3 grid(static_cast<unsigned>(l.parts), static_cast<unsigned>(p.H),
                   static_cast<unsigned>(sh.ptiles));
   if (l.cut) {
-    int st = mixer::launch(k_scan<T, kRowsPerThread, true>, grid, sh.threads, sh.smem, s, p, sh.tl,
-                           sh.prows);
+    int st = mixer::launch(k_scan<T, kRowsPerThread, true>, dim3(inner_parts(p), grid.y, grid.z),
+                           sh.threads, sh.smem, s, p, sh.tl, sh.prows);
     if (st != GGRN_OK) return st;
     st = launch_join(p, s);
     if (st != GGRN_OK) return st;

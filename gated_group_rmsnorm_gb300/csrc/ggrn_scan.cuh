@@ -35,6 +35,11 @@ __device__ __forceinline__ float dt_of(float raw, float bias, const Params& p) {
   return v > p.dt_max ? p.dt_max : v;
 }
 
+// The most parts there can be that are not the last of their sequence.
+inline unsigned inner_parts(const Params& p) {
+  return static_cast<unsigned>(p.q.cu ? p.q.rows / p.part : p.parts - p.q.seqs);
+}
+
 // Enqueue k_scan_join (the states at the parts' starts).
 int launch_join(const Params& p, cudaStream_t s);
 

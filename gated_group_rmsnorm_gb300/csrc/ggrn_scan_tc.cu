@@ -470,9 +470,9 @@ __global__ void __launch_bounds__(kMainThreads, 1)
   const Params& p = tp.p;
   pdl_wait();
   pdl_launch_dependents();
-  const Part part = find_part(p.q, p.part, blockIdx.x);
+  const Part part = find_part<STATE_ONLY>(p.q, p.part, blockIdx.x);
   // (offsets that do not ascend may count more places than there are)
-  if (part.seq < 0 || (STATE_ONLY && part.index == part.count - 1) ||
+  if (part.seq < 0 ||
       (part.count > 1 && part.place + (STATE_ONLY ? 1 : 0) >= p.places))
     return;
   extern __shared__ unsigned char smem_raw[];
@@ -1047,7 +1047,7 @@ int tc_run(const ggrn_scan_call& c, const Params& p, bool cut, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>(p.parts), static_cast<unsigned>(p.H),
                   static_cast<unsigned>((p.P + tp.tile - 1) / tp.tile));
   if (cut) {
-    int st = mixer::launch(k_scan_tc<true>, grid, kMainThreads, main_smem(tp.tile), s, tm_b, tm_c,
+    int st = mixer::launch(k_scan_tc<true>, dim3(inner_parts(p), grid.y, grid.z), kMainThreads, main_smem(tp.tile), s, tm_b, tm_c,
                            tp);
     if (st != GGRN_OK) return st;
     st = launch_join(p, s);
