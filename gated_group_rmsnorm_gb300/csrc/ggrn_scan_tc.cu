@@ -274,12 +274,14 @@ __device__ __forceinline__ void sts_f4(float* at, float a, float b, float c, flo
 
 // The three bf16 pieces of eight products w x, each piece what the ones before
 // leave, cut off (not rounded: 8 bits each of 24).
-__device__ __forceinline__ void pieces_of(const uint4& x, float w, uint4 (&u)[3]) {
+// `odd` becomes NaN where a product is not finite.
+__device__ __forceinline__ void pieces_of(const uint4& x, float w, uint4 (&u)[3], F2& odd) {
   const F2 ww = pk2(w, w), minus = pk2(-1.0f, -1.0f);
   uint32_t out[3][4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     F2 v = mul2(wide((&x.x)[e]), ww);
+    odd = fma2(v, 0, odd);
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
       float a, b;
@@ -291,6 +293,45 @@ __device__ __forceinline__ void pieces_of(const uint4& x, float w, uint4 (&u)[3]
   }
 #pragma unroll
   for (int k = 0; k < 3; ++k) u[k] = make_uint4(out[k][0], out[k][1], out[k][2], out[k][3]);
+}
+
+// Chunks with products that are not finite.  Such a product is its largest piece
+// alone.  An x that is not finite is taken out of X, since M's zeros before its
+// row would spread it over rows before its own; add_odd puts it back.
+__device__ __noinline__ void odd_chunk(uint32_t x_at, uint32_t w_at, uint32_t x_bytes, float w) {
+  for (int i = 0; i < 8; ++i) {
+    unsigned short h;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(x_at + 2 * i));
+    const float v = w * __uint_as_float(static_cast<uint32_t>(h) << 16);
+    if ((__float_as_uint(v) & 0x7f800000u) != 0x7f800000u) continue;
+    const unsigned short top = static_cast<unsigned short>(v != v ? 0x7fc0 : __float_as_uint(v) >> 16);
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(w_at + 2 * i), "h"(top) : "memory");
+    const unsigned short zero = 0;
+    for (int k = 1; k < 3; ++k)
+      asm volatile("st.shared.u16 [%0], %1;" ::"r"(w_at + k * x_bytes + 2 * i), "h"(zero) : "memory");
+    if ((h & 0x7f80) == 0x7f80)
+      asm volatile("st.shared.u16 [%0], %1;" ::"r"(x_at + 2 * i), "h"(zero) : "memory");
+  }
+}
+// What column `col` of Y lacks in row i of a chunk for that: the terms of the x
+// that are not finite, from the definition.  x, b, c: the chunk's first row.
+__device__ __noinline__ float add_odd(const __nv_bfloat16* x, const __nv_bfloat16* b,
+                                      const __nv_bfloat16* c, const Params& p, const float* sd, int i,
+                                      float dskip) {
+  float y = 0.0f;
+  for (int j = 0; j <= i; ++j) {
+    const float v = Bf::load1(x + j * p.xs, 0);
+    if ((__float_as_uint(v) & 0x7f800000u) != 0x7f800000u) continue;
+    float l = sd[i] - sd[j], f = sd[2 * kQ + j];  // of one block: dt_j 2^(pre_i - pre_j)
+    if (i >> 5 != j >> 5) {
+      l = sd[i], f = sd[kQ + j];
+      for (int k = (j >> 5) + 1; k < i >> 5; ++k) l += sd[5 * kQ + k];
+    }
+    const float m = f * ex2_approx(l) * v;
+    for (int n = 0; n < p.N; ++n) y += m * Bf::load1(b + j * p.bs, n) * Bf::load1(c + i * p.cs, n);
+    if (j == i) y += dskip * v;
+  }
+  return y;
 }
 
 // `bytes` (16 or 8) from global to shared memory, of which the first `valid`
@@ -502,7 +543,7 @@ __global__ void __launch_bounds__(kMainThreads, 1)
                                                               : 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (tid == 0) s_misc[1] = 0;
+  if (tid < 3) s_misc[1 + tid] = 0;  // timeout; chunk + 1 with odd x, by buffer
   if (warp == kWarpMma) tmem_alloc(smem_u32(const_cast<uint32_t*>(s_misc)), 512);
   tc_fence_before();
   __syncthreads();
@@ -706,18 +747,27 @@ __global__ void __launch_bounds__(kMainThreads, 1)
           if (++slot == kDecays) slot = 0, ++use;
           cp_async_wait();
           const uint32_t x_at = sX + (c & 1) * x_bytes + deal.at, w_at = sW + deal.at;
+          F2 odd = 0;
 #pragma unroll 1
           for (int i = 0; i < kDealt; i += 2) {
             const uint32_t o = i * kDealtBytes;
             uint4 ua[3], ub[3];
             const uint4 xa = lds16(x_at + o), xb = lds16(x_at + o + kDealtBytes);
-            pieces_of(xa, sw[i * kDealtRows], ua);
-            pieces_of(xb, sw[(i + 1) * kDealtRows], ub);
+            pieces_of(xa, sw[i * kDealtRows], ua, odd);
+            pieces_of(xb, sw[(i + 1) * kDealtRows], ub, odd);
 #pragma unroll
             for (int k = 0; k < 3; ++k) {
               sts16(w_at + o + k * x_bytes, ua[k]);
               sts16(w_at + o + kDealtBytes + k * x_bytes, ub[k]);
             }
+          }
+          float odd0, odd1;
+          upk2(odd, odd0, odd1);
+          if (odd0 != odd0 || odd1 != odd1) {
+            for (int i = 0; i < kDealt; ++i)
+              odd_chunk(x_at + i * kDealtBytes, w_at + i * kDealtBytes, x_bytes,
+                        sw[i * kDealtRows]);
+            s_misc[2 + (c & 1)] = c + 1;
           }
           fence_async_smem();
           warp_arrive(bar(kWFull));
@@ -895,6 +945,7 @@ __global__ void __launch_bounds__(kMainThreads, 1)
       tc_fence_after();
       const float e = s_decay[slot * kDecayFloats + 4 * kQ + i];
       const F2 e2 = pk2(e, e);
+      const bool odd = s_misc[2 + (c & 1)] == static_cast<uint32_t>(c + 1);
       uint32_t at = sX + (c & 1) * x_bytes + at0;
 #pragma unroll 1
       for (int a = 0; a < atoms; ++a, at += kAtomBytes) {
@@ -908,6 +959,20 @@ __global__ void __launch_bounds__(kMainThreads, 1)
           uint32_t& xw = j < 8 ? (&xa.x)[j / 2] : (&xb.x)[j / 2 - 4];
           xw = bf16x2(fma2(wide(xw), skip2,
                            fma2(pair(y1[j], y1[j + 1]), e2, pair(y2[j], y2[j + 1]))));
+        }
+        if (odd && i < rows - c * kQ) {
+          const int64_t row = part.begin + c * kQ;
+          for (int j = 0; j < 16 && 16 * a + j < pw; ++j) {
+            const float add = add_odd(
+                static_cast<const __nv_bfloat16*>(p.x) + row * p.xs + hcol + 16 * a + j,
+                static_cast<const __nv_bfloat16*>(p.b) + row * p.bs + static_cast<int64_t>(g) * N,
+                static_cast<const __nv_bfloat16*>(p.c) + row * p.cs + static_cast<int64_t>(g) * N, p,
+                s_decay + slot * kDecayFloats, i, dskip);
+            if (add == 0.0f) continue;  // (none: what is added is not finite)
+            uint32_t& w = (j < 8 ? &xa.x : &xb.x)[(j & 7) >> 1];
+            w = j & 1 ? (w & 0xffffu) | (Bf::pack2(add, add) << 16)
+                      : (w & 0xffff0000u) | (Bf::pack2(add, add) & 0xffffu);
+          }
         }
         sts16(at, xa);
         sts16(at ^ 16, xb);
@@ -938,7 +1003,7 @@ __global__ void __launch_bounds__(kMainThreads, 1)
 constexpr double kStartChunks = 4.0, kStateShare = 0.6, kJoinChunks = 3.0;
 uint32_t main_smem(int tile) {
   return 1024 + 3 * kRowsBytes + 6 * (tile / 16 * kAtomBytes) + kDecays * kDecayFloats * 4 +
-         8 * kBars + 16;
+         8 * kBars + 24;
 }
 int tile_of(int64_t P) {
   const int64_t tiles = (P + 16 * kMaxAtoms - 1) / (16 * kMaxAtoms);

@@ -90,7 +90,7 @@ def scan(x, dt, a, b, c, head_dim, state_size, d=None, dt_bias=None, softplus=Tr
     dts = torch.logaddexp(v, torch.zeros_like(v)) if softplus else v
     dts = torch.where(dts < limits[0], torch.full_like(dts, limits[0]), dts)
     dts = torch.where(dts > limits[1], torch.full_like(dts, limits[1]), dts)
-    eps_dt = (1 + v.abs() + 6) * U
+    eps_dt = torch.where(torch.isfinite(v), (1 + v.abs() + 6) * U, torch.zeros_like(v))  # 0, inf: exact
     out = torch.full((rows, H, P), math.nan, dtype=torch.float64)
     bound, size = torch.zeros_like(out), torch.zeros_like(out)
     new = None if state is None else state.double().cpu().clone()

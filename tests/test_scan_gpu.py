@@ -243,6 +243,29 @@ def test_garbage_behind_and_between_sequences(dtype):
     assert torch.isnan(st[1]).all()
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("what", ["x", "b", "c", "dt"])
+def test_bad_values_leave_the_rows_before_alone(dtype, bad, what):
+    """A value that is not finite in one row: rows before it, other columns and
+    other heads have what the definition gives, and it has the definition's
+    infinities and NaN itself."""
+    k = Case(300, 3, 64, 1, 24, dtype, slots=1, seed=4)
+    row, col = 100, {"x": 64 + 5, "b": 3, "c": 7, "dt": 1}[what]
+    k.views(k.xbc, k.z)[what][row, col] = bad
+    st = k.state.cuda()
+    got = k.run(state=st).double().cpu()
+    want, bound, size, new, nb, ns = k.want(spans=[(0, 300)])
+    fine = torch.isfinite(want)
+    # (softplus of minus infinity is 0: nothing but a row without input)
+    assert fine[:row].all() and (not fine.all() or (what, bad) == ("dt", -float("inf")))
+    assert torch.equal(fine, torch.isfinite(got))
+    tol = (bound + ref.rounding(want, dtype) + (size * torch.finfo(dtype).eps / 2
+                                                if dtype != torch.float32 else 0)) * (1 + 2.0 ** -6)
+    assert ((got - want).abs() <= tol)[fine].all()
+    assert torch.equal(torch.isfinite(new), torch.isfinite(st.double().cpu()))
+
+
 def test_offsets_that_do_not_ascend():
     """Nothing outside the buffers is touched whatever the offsets say."""
     rows = 700
