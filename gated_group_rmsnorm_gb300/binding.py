@@ -1,6 +1,7 @@
 """ctypes binding of ``libggrn.so`` (the C ABI declared in ``include/ggrn.h``).
 
-Argument marshalling only: every step of the operation runs in the CUDA
+Argument marshalling only (for the mixer's operators in compiled code,
+``csrc/ggrn_python.cpp``): every step of the operation runs in the CUDA
 kernels behind the C ABI.  PyTorch supplies device memory and the current
 stream.  There is no fallback: if the library is missing or a call fails, an
 exception says so.
@@ -8,6 +9,8 @@ exception says so.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 
@@ -508,120 +511,54 @@ def _packed_pair(y, gate, rows, width, ys, gts):
 # ---------------------------------------------------------------------------
 # The mixer around the norm: causal convolution and state space scan.
 # ---------------------------------------------------------------------------
+_native = None
+
+
+def load_binding(build_if_missing: bool = True):
+    """Load ``_binding.so``, the compiled checks and calls of the mixer's
+    operators (building it first if it is missing and allowed)."""
+    global _native
+    if _native is not None:
+        return _native
+    load(build_if_missing)
+    with _lock:
+        if _native is None:
+            path = _build.BINDING_PATH
+            if not os.path.exists(path):
+                if not build_if_missing:
+                    raise RuntimeError(f"{path} is not built; run gated_group_rmsnorm_gb300.build")
+                _build.build_binding()
+            loader = importlib.machinery.ExtensionFileLoader(__package__ + "._binding", path)
+            spec = importlib.util.spec_from_file_location(__package__ + "._binding", path,
+                                                          loader=loader)
+            module = importlib.util.module_from_spec(spec)
+            loader.exec_module(module)
+            module.on_error(_raise_status)
+            _native = module
+    return _native
+
+
+def _raise_status(status: int, what: str):
+    raise GgrnError(status, what)
+
+
 def _rows_of(t: torch.Tensor, width: int, name: str) -> tuple[int, int]:
     """(rows, row_stride) of a tensor viewed as [rows, width]; an axis of one
     element may have any stride."""
-    shape, strides = t.shape, t.stride()
-    if len(shape) == 0 or shape[-1] != width:
-        raise ValueError(f"{name} must have {width} columns")
-    if width != 1 and strides[-1] != 1:
-        raise ValueError(f"{name} needs unit stride on its last dimension")
-    if len(shape) == 2:
-        return shape[0], (strides[0] if shape[0] > 1 else width)
-    if t.numel() == 0:
-        return 0, width
-    rows, stride = 1, width
-    for size, step in zip(reversed(shape[:-1]), reversed(strides[:-1])):
-        if size == 1:
-            continue
-        if rows == 1:
-            stride = step
-        elif step != stride * rows:
-            raise ValueError(f"{name}: leading axes do not fold into one row axis")
-        rows *= size
-    return rows, stride
+    return load_binding().rows_of(t, width, name)
 
 
-def _vector(t, n: int, dtype, device, name: str):
-    """Pointer of an optional contiguous vector of n elements."""
-    if t is None:
-        return None
-    if t.dtype != dtype or t.numel() != n or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} elements on {device}")
-    return t.data_ptr()
-
-
-def _fill_seqs(k, x, device, cu_seqlens, state, slots, resume, held: tuple, dtype, step: bool):
-    """Sequences and pool of a call: the fields both operators share."""
-    if step:
-        n = k.rows
-        k.seqs = n
-    elif cu_seqlens is not None:
-        n = cu_seqlens.numel() - 1
-        if n < 0:
-            raise ValueError("cu_seqlens holds one offset more than there are sequences")
-        k.cu_seqlens = _vector(cu_seqlens, n + 1, torch.int32, device, "cu_seqlens")
-        k.seqs = n
-    else:
-        n = 1
-        for size in x.shape[:-2]:
-            n *= size
-        k.seqs = n
-    if state is None:
-        if slots is not None or resume is not None:
-            raise ValueError("slots and resume name entries of a state: pass one")
-        return
-    if state.dtype != dtype or state.device != device:
-        raise ValueError(f"state must be a {dtype} tensor on {device}")
-    if state.shape[1:] != held:
-        raise ValueError(f"state must be [slots, {', '.join(map(str, held))}]")
-    expect = 1
-    for size, stride in zip(reversed(state.shape[1:]), reversed(state.stride()[1:])):
-        if size != 1 and stride != expect:
-            raise ValueError("the entries of state must be contiguous")
-        expect *= size
-    if slots is None and state.shape[0] < n:
-        raise ValueError(f"state has {state.shape[0]} entries for {n} sequences")
-    k.state = state.data_ptr()
-    k.state_slots = state.shape[0]
-    k.state_slot_stride = state.stride(0) if state.shape[0] > 1 else expect
-    k.slots = _vector(slots, n, torch.int32, device, "slots")
-    if resume is not None:
-        if resume.dtype not in (torch.bool, torch.uint8):
-            raise ValueError("resume must be a bool or uint8 tensor")
-        k.resume = _vector(resume, n, resume.dtype, device, "resume")
-
-
-def _conv_call(x, weight, bias, activation, cu_seqlens, state, slots, resume, out, step: bool):
-    """(ConvCall, out) of a convolution's arguments."""
-    if not x.is_cuda:
-        raise ValueError("the convolution runs on CUDA tensors only (no CPU path)")
-    dtype, device = x.dtype, x.device
-    if dtype not in DTYPE_CODE:
-        raise ValueError(f"unsupported dtype {dtype}")
+def _act(activation) -> int:
     if activation not in ACT_CODE:
         raise ValueError(f"unknown activation {activation!r}")
-    if x.dim() < 2:
-        raise ValueError("x must be [rows, width] or [batch, length, width]")
-    if weight.dim() != 2:
-        raise ValueError("weight must be [width, taps]")
-    width = x.shape[-1]
-    taps = weight.shape[1]
-    k = ConvCall()
-    k.rows, k.x_row_stride = _rows_of(x, width, "x")
-    k.x = x.data_ptr()
-    k.width, k.taps, k.activation, k.dtype = width, taps, ACT_CODE[activation], DTYPE_CODE[dtype]
-    k.w = _vector(weight, width * taps, torch.float32, device, "weight")
-    k.bias = _vector(bias, width, torch.float32, device, "bias")
-    if out is None:
-        out = torch.empty(x.shape, dtype=dtype, device=device)
-    elif out.shape != x.shape or out.dtype != dtype or out.device != device:
-        raise ValueError("out must have the shape, dtype and device of x")
-    k.out = out.data_ptr()
-    k.out_row_stride = _rows_of(out, width, "out")[1]
-    _fill_seqs(k, x, device, cu_seqlens, state, slots, resume, (taps - 1, width), dtype, step)
-    return k, out
+    return ACT_CODE[activation]
 
 
-def _launch(fn, k, device, what: str) -> None:
-    """A call on its tensors' device and that device's current stream."""
-    if torch.cuda.current_device() == device.index:
-        st = fn(ctypes.byref(k), torch.cuda.current_stream().cuda_stream)
-    else:
-        with torch.cuda.device(device):
-            st = fn(ctypes.byref(k), torch.cuda.current_stream().cuda_stream)
-    if st != OK:
-        raise GgrnError(st, what)
+def _sizes(state: torch.Tensor) -> tuple[int, int]:
+    """(head_dim, state_size) of a scan's state."""
+    if state.dim() != 4:
+        raise ValueError("state must be [slots, heads, head_dim, state_size]")
+    return state.shape[2], state.shape[3]
 
 
 def causal_conv(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None, *,
@@ -642,9 +579,8 @@ def causal_conv(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None
     int32; entry i without it), whose old contents the sequences with
     ``resume`` continue.  Entries of one call are distinct.
     """
-    k, out = _conv_call(x, weight, bias, activation, cu_seqlens, state, slots, resume, out, False)
-    _launch(load().ggrn_conv, k, x.device, "ggrn_conv")
-    return out
+    return (_native or load_binding()).conv(x, weight, bias, _act(activation), cu_seqlens, state,
+                                            slots, resume, out, False)
 
 
 def causal_conv_step(x: torch.Tensor, state: torch.Tensor, weight: torch.Tensor,
@@ -656,53 +592,8 @@ def causal_conv_step(x: torch.Tensor, state: torch.Tensor, weight: torch.Tensor,
     of ``state`` and updates it in place.  A row whose slot is outside the pool
     is skipped: its output row is left as it was.
     """
-    k, out = _conv_call(x, weight, bias, activation, None, state, slots, None, out, True)
-    _launch(load().ggrn_conv_step, k, x.device, "ggrn_conv_step")
-    return out
-
-
-def _scan_call(x, dt, a, b, c, head_dim, state_size, d, dt_bias, dt_softplus, dt_limits,
-               cu_seqlens, state, slots, resume, out, step: bool):
-    """(ScanCall, out) of a scan's arguments."""
-    if not x.is_cuda:
-        raise ValueError("the scan runs on CUDA tensors only (no CPU path)")
-    dtype, device = x.dtype, x.device
-    if dtype not in DTYPE_CODE:
-        raise ValueError(f"unsupported dtype {dtype}")
-    if x.dim() < 2:
-        raise ValueError("x must be [rows, width] or [batch, length, width]")
-    width, heads, gn = x.shape[-1], a.numel(), b.shape[-1]
-    if heads == 0 or head_dim * heads != width:
-        raise ValueError(f"x has {width} columns, not {heads} heads of {head_dim}")
-    if state_size <= 0 or gn % state_size or gn == 0:
-        raise ValueError(f"b has {gn} columns, not a multiple of state_size {state_size}")
-    lead = x.shape[:-1]
-    for t, n, name in ((dt, heads, "dt"), (b, gn, "b"), (c, gn, "c")):
-        if t.dtype != dtype or t.device != device:
-            raise ValueError(f"{name} must have the dtype and device of x")
-        if t.shape[:-1] != lead or t.shape[-1] != n:
-            raise ValueError(f"{name} must have the leading shape of x and {n} columns")
-    k = ScanCall()
-    k.rows, k.x_row_stride = _rows_of(x, width, "x")
-    k.dt_row_stride = _rows_of(dt, heads, "dt")[1]
-    k.b_row_stride = _rows_of(b, gn, "b")[1]
-    k.c_row_stride = _rows_of(c, gn, "c")[1]
-    k.x, k.dt, k.b, k.c = x.data_ptr(), dt.data_ptr(), b.data_ptr(), c.data_ptr()
-    k.heads, k.head_dim, k.groups, k.state_size = heads, head_dim, gn // state_size, state_size
-    k.a = _vector(a, heads, torch.float32, device, "a")
-    k.d = _vector(d, heads, torch.float32, device, "d")
-    k.dt_bias = _vector(dt_bias, heads, torch.float32, device, "dt_bias")
-    k.dt_min, k.dt_max = dt_limits
-    k.dt_softplus, k.dtype = (1 if dt_softplus else 0), DTYPE_CODE[dtype]
-    if out is None:
-        out = torch.empty(x.shape, dtype=dtype, device=device)
-    elif out.shape != x.shape or out.dtype != dtype or out.device != device:
-        raise ValueError("out must have the shape, dtype and device of x")
-    k.out = out.data_ptr()
-    k.out_row_stride = _rows_of(out, width, "out")[1]
-    _fill_seqs(k, x, device, cu_seqlens, state, slots, resume, (heads, head_dim, state_size),
-               torch.float32, step)
-    return k, out
+    return (_native or load_binding()).conv(x, weight, bias, _act(activation), None, state, slots,
+                                            None, out, True)
 
 
 def ssm_scan(x: torch.Tensor, dt: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
@@ -728,20 +619,10 @@ def ssm_scan(x: torch.Tensor, dt: torch.Tensor, a: torch.Tensor, b: torch.Tensor
     ``resume`` as in ``causal_conv``.  ``workspace``: optional uint8 device
     tensor of ``scan_workspace_bytes`` (allocated when omitted and needed).
     """
-    k, out = _scan_call(x, dt, a, b, c, head_dim, state_size, d, dt_bias, dt_softplus, dt_limits,
-                        cu_seqlens, state, slots, resume, out, False)
-    lib = load()
-    if workspace is None:
-        n = lib.ggrn_scan_workspace_bytes(ctypes.byref(k))
-        if n > 0:
-            workspace = torch.empty(n, dtype=torch.uint8, device=x.device)
-    elif workspace.device != x.device or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the device of x")
-    if workspace is not None:
-        k.workspace = workspace.data_ptr()
-        k.workspace_bytes = workspace.numel() * workspace.element_size()
-    _launch(lib.ggrn_scan, k, x.device, "ggrn_scan")
-    return out
+    lo, hi = dt_limits
+    return (_native or load_binding()).scan(x, dt, a, b, c, head_dim, state_size, d, dt_bias,
+                                            dt_softplus, lo, hi, cu_seqlens, state, slots, resume,
+                                            out, False, workspace)
 
 
 def ssm_scan_step(x: torch.Tensor, dt: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
@@ -756,20 +637,19 @@ def ssm_scan_step(x: torch.Tensor, dt: torch.Tensor, a: torch.Tensor, b: torch.T
     whose slot is outside the pool is skipped: its output row is left as it
     was.
     """
-    if state.dim() != 4:
-        raise ValueError("state must be [slots, heads, head_dim, state_size]")
-    k, out = _scan_call(x, dt, a, b, c, state.shape[2], state.shape[3], d, dt_bias, dt_softplus,
-                        dt_limits, None, state, slots, None, out, True)
-    _launch(load().ggrn_scan_step, k, x.device, "ggrn_scan_step")
-    return out
+    head_dim, state_size = _sizes(state)
+    lo, hi = dt_limits
+    return (_native or load_binding()).scan(x, dt, a, b, c, head_dim, state_size, d, dt_bias,
+                                            dt_softplus, lo, hi, None, state, slots, None, out,
+                                            True, None)
 
 
 def scan_workspace_bytes(x, dt, a, b, c, *, head_dim: int, state_size: int,
                          cu_seqlens: torch.Tensor | None = None) -> int:
     """Workspace bytes of ``ssm_scan`` on these tensors (0: none needed)."""
-    k, _ = _scan_call(x, dt, a, b, c, head_dim, state_size, None, None, True, (0.0, 0.0),
-                      cu_seqlens, None, None, None, None, False)
-    return load().ggrn_scan_workspace_bytes(ctypes.byref(k))
+    return load_binding().scan_workspace_bytes(x, dt, a, b, c, head_dim, state_size, None, None,
+                                               True, 0.0, 0.0, cu_seqlens, None, None, None, None,
+                                               False)
 
 
 def _given(c: dict, name: str):
@@ -814,20 +694,19 @@ class DecodeGraph:
                 here = y.device
             elif op == "causal_conv_step":
                 arr[i].kind = STEP_CONV
-                arr[i].u.conv = _conv_call(c.pop("x"), c.pop("weight"), c.pop("bias", None),
-                                           c.pop("activation", "silu"), None, c.pop("state"),
-                                           c.pop("slots", None), None, _given(c, "out"), True)[0]
+                arr[i].u.conv = ConvCall.from_buffer_copy(load_binding().conv_call(
+                    c.pop("x"), c.pop("weight"), c.pop("bias", None),
+                    _act(c.pop("activation", "silu")), None, c.pop("state"), c.pop("slots", None),
+                    None, _given(c, "out"), True))
                 here = call["x"].device
             elif op == "ssm_scan_step":
                 st = c.pop("state")
-                if st.dim() != 4:
-                    raise ValueError("state must be [slots, heads, head_dim, state_size]")
+                lo, hi = c.pop("dt_limits", (0.0, float("inf")))
                 arr[i].kind = STEP_SCAN
-                arr[i].u.scan = _scan_call(c.pop("x"), c.pop("dt"), c.pop("a"), c.pop("b"),
-                                           c.pop("c"), st.shape[2], st.shape[3], c.pop("d", None),
-                                           c.pop("dt_bias", None), c.pop("dt_softplus", True),
-                                           c.pop("dt_limits", (0.0, float("inf"))), None, st,
-                                           c.pop("slots", None), None, _given(c, "out"), True)[0]
+                arr[i].u.scan = ScanCall.from_buffer_copy(load_binding().scan_call(
+                    c.pop("x"), c.pop("dt"), c.pop("a"), c.pop("b"), c.pop("c"), *_sizes(st),
+                    c.pop("d", None), c.pop("dt_bias", None), c.pop("dt_softplus", True), lo, hi,
+                    None, st, c.pop("slots", None), None, _given(c, "out"), True))
                 here = call["x"].device
             else:
                 raise ValueError(f"unknown op {op!r}")

@@ -31,6 +31,10 @@ SOURCES = ["ggrn_api.cu", "ggrn_conv.cu", "ggrn_host.cu", "ggrn_kernels_bf16.cu"
 HEADERS = ["ggrn_internal.h", "ggrn_kernels.cuh", "ggrn_mixer.cuh", "ggrn_scan.cuh",
            "ggrn_slots.h", "ggrn_stream.cuh", "ggrn_umma.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
+# the Python entry of the mixer's operators (a CPython extension on torch's
+# headers), linked to libggrn.so beside it
+BINDING_PATH = os.path.join(HERE, "_binding.so")
+BINDING_SOURCE = "ggrn_python.cpp"
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "--expt-relaxed-constexpr"]
 
@@ -94,6 +98,33 @@ def build(force: bool = False, ptxas_verbose: bool = False, quiet: bool = True,
     return lib_path
 
 
+def build_binding(force: bool = False) -> str:
+    """Compile ``_binding.so``; return its path.  No-op when up to date."""
+    src = os.path.join(CSRC, BINDING_SOURCE)
+    if not force and not _stale(BINDING_PATH, [src, os.path.join(INCLUDE, "ggrn.h"),
+                                               os.path.abspath(__file__)]):
+        return BINDING_PATH
+    import sysconfig
+
+    import torch
+    troot = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    tmp = BINDING_PATH + f".tmp{os.getpid()}"
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", os.path.join(troot, "include"),
+           "-I", os.path.join(troot, "include", "torch", "csrc", "api", "include"),
+           "-I", os.path.join(cuda, "include"), "-I", sysconfig.get_paths()["include"], src,
+           "-L", HERE, "-l:libggrn.so", "-Wl,-rpath,$ORIGIN",
+           "-L", os.path.join(troot, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+           "-ltorch_python", "-Wl,-rpath," + os.path.join(troot, "lib"), "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {BINDING_SOURCE}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING_PATH)
+    return BINDING_PATH
+
+
 if __name__ == "__main__":
     ap = argparse.ArgumentParser()
     ap.add_argument("--force", action="store_true")
@@ -103,3 +134,5 @@ if __name__ == "__main__":
     args = ap.parse_args()
     print(build(force=args.force, ptxas_verbose=args.ptxas_v, quiet=False,
                 timeline=args.timeline))
+    if not args.timeline:
+        print(build_binding(force=args.force))
