@@ -313,25 +313,35 @@ __device__ __noinline__ void odd_chunk(uint32_t x_at, uint32_t w_at, uint32_t x_
       asm volatile("st.shared.u16 [%0], %1;" ::"r"(x_at + 2 * i), "h"(zero) : "memory");
   }
 }
-// What column `col` of Y lacks in row i of a chunk for that: the terms of the x
-// that are not finite, from the definition.  x, b, c: the chunk's first row.
-__device__ __noinline__ float add_odd(const __nv_bfloat16* x, const __nv_bfloat16* b,
-                                      const __nv_bfloat16* c, const Params& p, const float* sd, int i,
-                                      float dskip) {
-  float y = 0.0f;
-  for (int j = 0; j <= i; ++j) {
-    const float v = Bf::load1(x + j * p.xs, 0);
-    if ((__float_as_uint(v) & 0x7f800000u) != 0x7f800000u) continue;
-    float l = sd[i] - sd[j], f = sd[2 * kQ + j];  // of one block: dt_j 2^(pre_i - pre_j)
-    if (i >> 5 != j >> 5) {
-      l = sd[i], f = sd[kQ + j];
-      for (int k = (j >> 5) + 1; k < i >> 5; ++k) l += sd[5 * kQ + k];
+// What row i of a chunk's Y lacks for that: the terms of the x that are not
+// finite, from the definition.  y: the chunk's place in shared memory, row: its
+// first row, sd: its decays.
+__device__ __noinline__ void add_odd(uint32_t y, const Params& p, int64_t row, int64_t hcol, int pw,
+                                     int g, const float* sd, int i, float dskip) {
+  const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.x) + row * p.xs + hcol;
+  const __nv_bfloat16* b =
+      static_cast<const __nv_bfloat16*>(p.b) + row * p.bs + static_cast<int64_t>(g) * p.N;
+  const __nv_bfloat16* c =
+      static_cast<const __nv_bfloat16*>(p.c) + (row + i) * p.cs + static_cast<int64_t>(g) * p.N;
+  for (int col = 0; col < pw; ++col) {
+    float add = 0.0f;
+    for (int j = 0; j <= i; ++j) {
+      const float v = Bf::load1(x + j * p.xs, col);
+      if ((__float_as_uint(v) & 0x7f800000u) != 0x7f800000u) continue;
+      float l = sd[i] - sd[j], f = sd[2 * kQ + j];  // of one block: dt_j 2^(pre_i - pre_j)
+      if (i >> 5 != j >> 5) {
+        l = sd[i], f = sd[kQ + j];
+        for (int k = (j >> 5) + 1; k < i >> 5; ++k) l += sd[5 * kQ + k];
+      }
+      const float m = f * ex2_approx(l) * v;
+      for (int n = 0; n < p.N; ++n) add += m * Bf::load1(b + j * p.bs, n) * Bf::load1(c, n);
+      if (j == i) add += dskip * v;
     }
-    const float m = f * ex2_approx(l) * v;
-    for (int n = 0; n < p.N; ++n) y += m * Bf::load1(b + j * p.bs, n) * Bf::load1(c + i * p.cs, n);
-    if (j == i) y += dskip * v;
+    if (add == 0.0f) continue;  // (none: what is added is not finite)
+    const unsigned short h = static_cast<unsigned short>(Bf::pack2(add, add));
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(y + chunk_at(i, col >> 3) + 2 * (col & 7)), "h"(h)
+                 : "memory");
   }
-  return y;
 }
 
 // `bytes` (16 or 8) from global to shared memory, of which the first `valid`
@@ -543,7 +553,7 @@ __global__ void __launch_bounds__(kMainThreads, 1)
                                                               : 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (tid < 3) s_misc[1 + tid] = 0;  // timeout; chunk + 1 with odd x, by buffer
+  if (tid == 0) s_misc[1] = 0, s_misc[2] = 0, s_misc[3] = 0;  // timeout; chunk + 1 with odd x, by buffer
   if (warp == kWarpMma) tmem_alloc(smem_u32(const_cast<uint32_t*>(s_misc)), 512);
   tc_fence_before();
   __syncthreads();
@@ -945,7 +955,6 @@ __global__ void __launch_bounds__(kMainThreads, 1)
       tc_fence_after();
       const float e = s_decay[slot * kDecayFloats + 4 * kQ + i];
       const F2 e2 = pk2(e, e);
-      const bool odd = s_misc[2 + (c & 1)] == static_cast<uint32_t>(c + 1);
       uint32_t at = sX + (c & 1) * x_bytes + at0;
 #pragma unroll 1
       for (int a = 0; a < atoms; ++a, at += kAtomBytes) {
@@ -960,23 +969,12 @@ __global__ void __launch_bounds__(kMainThreads, 1)
           xw = bf16x2(fma2(wide(xw), skip2,
                            fma2(pair(y1[j], y1[j + 1]), e2, pair(y2[j], y2[j + 1]))));
         }
-        if (odd && i < rows - c * kQ) {
-          const int64_t row = part.begin + c * kQ;
-          for (int j = 0; j < 16 && 16 * a + j < pw; ++j) {
-            const float add = add_odd(
-                static_cast<const __nv_bfloat16*>(p.x) + row * p.xs + hcol + 16 * a + j,
-                static_cast<const __nv_bfloat16*>(p.b) + row * p.bs + static_cast<int64_t>(g) * N,
-                static_cast<const __nv_bfloat16*>(p.c) + row * p.cs + static_cast<int64_t>(g) * N, p,
-                s_decay + slot * kDecayFloats, i, dskip);
-            if (add == 0.0f) continue;  // (none: what is added is not finite)
-            uint32_t& w = (j < 8 ? &xa.x : &xb.x)[(j & 7) >> 1];
-            w = j & 1 ? (w & 0xffffu) | (Bf::pack2(add, add) << 16)
-                      : (w & 0xffff0000u) | (Bf::pack2(add, add) & 0xffffu);
-          }
-        }
         sts16(at, xa);
         sts16(at ^ 16, xb);
       }
+      if (s_misc[2 + (c & 1)] == static_cast<uint32_t>(c + 1) && i < rows - c * kQ)
+        add_odd(sX + (c & 1) * x_bytes, p, part.begin + c * kQ, hcol, pw, g,
+                s_decay + slot * kDecayFloats, i, dskip);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
