@@ -8,9 +8,10 @@
 // group.
 //
 // k_scan is the recurrence as it stands, for every type and size: the state
-// lives in registers in f32 (4 rows of S x 16 columns per thread, a team of
-// lanes across the columns), tokens come in blocks of 16 through shared
-// memory, three f32x2 instructions per pair of state entries and token.
+// lives in registers in f32 (4 rows of S x 16 columns per thread, a team of TL
+// lanes across the columns), tokens come in blocks of 16 through shared memory
+// (asynchronous copies, a block ahead), three f32x2 instructions per pair of
+// state entries and token, which bound it.
 //
 // A sequence longer than a part (see find_part) is cut: a first launch runs
 // every part but the last of its sequence from a zero state, for its final
@@ -20,6 +21,8 @@
 
 #include <algorithm>
 #include <cmath>
+#include <initializer_list>
+#include <mutex>
 #include <type_traits>
 
 #include "ggrn_scan.cuh"
@@ -32,149 +35,263 @@ namespace scan {
 // ---------------------------------------------------------------------------
 constexpr int kBlock = 16;   // tokens staged in shared memory at a time
 constexpr int kCols = 16;    // state columns of a thread: 4 runs of 4, team-interleaved
-constexpr int kMaxThreads = 256;
+constexpr int kRows = 4;     // rows of S of a thread
+constexpr int kMaxThreads = 256, kMaxRows = 256;
+constexpr int kMaxSmem = 96 * 1024;
 constexpr int kMinPart = 64;  // rows of the shortest part worth its join
 
 template <typename T>
 __device__ __forceinline__ float ld1(const T* p) {
   return Elem<T>::load1(p, 0);
 }
+// Four consecutive values from shared memory, as two pairs.
+struct Quad {
+  F2 lo, hi;
+};
+__device__ __forceinline__ Quad lds4(const float* p) {
+  const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(p);
+  return {v.x, v.y};
+}
+template <typename T>
+__device__ __forceinline__ Quad lds4(const T* p) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  float a, b, c, d;
+  Elem<T>::unpack2(u.x, a, b);
+  Elem<T>::unpack2(u.y, c, d);
+  return {pk2(a, b), pk2(c, d)};
+}
 
-// RP: rows of S per thread.  `STATE_ONLY`: the first launch of a cut scan.
-template <typename T, int RP, bool STATE_ONLY>
-__global__ void __launch_bounds__(kMaxThreads) k_scan(const Params p, const int tl, const int prows) {
-  extern __shared__ float smem[];
-  const int P = p.P, N = p.N;
-  const int NP = tl * kCols;                 // state columns padded to the teams' span
-  float* sB = smem;                          // [kBlock][NP]
-  float* sC = sB + kBlock * NP;              // [kBlock][NP]
-  float* sX = sC + kBlock * NP;              // [kBlock][prows]
-  float* sY = sX + kBlock * prows;           // [kBlock][prows]
-  float* sDt = sY + kBlock * prows;          // [kBlock] dt, [kBlock] decay
+__device__ __forceinline__ float ld_smem(const float* p) { return *p; }
+template <typename T>
+__device__ __forceinline__ float ld_smem(const T* p) {
+  return static_cast<float>(*p);
+}
+
+// What the host found out about the layout: bytes an asynchronous copy of a row
+// of B and C, or of x, may move (16, 8, 4; 2: none, element by element).
+struct Shape {
+  int tl, threads, prows, ptiles;
+  int bc_bytes, x_bytes;
+  int np, xp;      // elements of a row of B or C, and of x, in shared memory
+  size_t smem;
+};
+
+// `cols` elements of a row into shared memory by one warp.
+template <typename T>
+__device__ __forceinline__ void copy_row(T* dst, const T* src, int cols, int bytes) {
+  const int lane = threadIdx.x & 31;
+  const int total = cols * static_cast<int>(sizeof(T));
+  if (bytes == 2) {
+    for (int i = lane; i < cols; i += 32) dst[i] = src[i];
+    return;
+  }
+  const uint32_t d = smem_u32(dst);
+  const char* s = reinterpret_cast<const char*>(src);
+  for (int i = lane * bytes; i < total; i += 32 * bytes) {
+    if (bytes == 16)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d + i), "l"(s + i) : "memory");
+    else if (bytes == 8)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(d + i), "l"(s + i) : "memory");
+    else
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d + i), "l"(s + i) : "memory");
+  }
+}
+
+// Sums of four values over a team of TL lanes: afterwards lane l of the team
+// holds the sum of value team_row<TL>(l) (TL >= 4), those of two values in v[0]
+// and v[1] (TL == 2), or all four (TL == 1).
+template <int TL>
+__device__ __forceinline__ void team_sums(float (&v)[4], int l) {
+  if constexpr (TL >= 2) {
+    const bool up = l & (TL / 2);
+    const float a = up ? v[0] : v[2], b = up ? v[1] : v[3];
+    v[0] = (up ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, a, TL / 2);
+    v[1] = (up ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, b, TL / 2);
+  }
+  if constexpr (TL >= 4) {
+    const bool up = l & (TL / 4);
+    const float a = up ? v[0] : v[1];
+    v[0] = (up ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, a, TL / 4);
+#pragma unroll
+    for (int o = TL / 8; o > 0; o >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+  }
+}
+
+// `STATE_ONLY`: the first launch of a cut scan.
+template <typename T, int TL, bool STATE_ONLY>
+__global__ void __launch_bounds__(kMaxThreads) k_scan(const Params p, const Shape sh) {
+  extern __shared__ __align__(16) unsigned char smem_raw[];
   pdl_wait();
   pdl_launch_dependents();
   const Part part = find_part<STATE_ONLY>(p.q, p.part, blockIdx.x);
   if (part.seq < 0) return;
   // (offsets that do not ascend may count more places than there are)
   if (part.count > 1 && part.place + (STATE_ONLY ? 1 : 0) >= p.places) return;
+  const int P = p.P, N = p.N, prows = sh.prows;
   const int h = blockIdx.y, g = h / p.hpg;
   const int row0 = blockIdx.z * prows;
   const int rows_here = min(prows, P - row0);
-  const int tid = threadIdx.x, nthr = blockDim.x;
-  const int l = tid & (tl - 1);
-  const int r0 = tid / tl * RP;              // this thread's first row of the tile
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
+  const int l = tid & (TL - 1);
+  const int r0 = tid / TL * kRows;           // this thread's first row of the tile
+  // shared memory: two blocks of B, C and x rows; y rows; dt and decays
+  T* sB = reinterpret_cast<T*>(smem_raw);    // [2][kBlock][np]
+  T* sC = sB + 2 * kBlock * sh.np;
+  T* sX = sC + 2 * kBlock * sh.np;           // [2][kBlock][xp]
+  float* sY = reinterpret_cast<float*>(sX + 2 * kBlock * sh.xp);  // [kBlock][prows]
+  float* sDt = sY + kBlock * prows;          // [2][kBlock] dt, decay
   const float a = __ldg(p.a + h), dbias = p.dt_bias ? __ldg(p.dt_bias + h) : 0.0f;
   const float dskip = p.d ? __ldg(p.d + h) : 0.0f;
   const int64_t slot = seq_slot(p.q, part.seq);
-
-  float s[RP][kCols];
-  // the state this part starts from: the workspace's for a cut sequence,
-  // else the pool's or zeros
-  const float* from = nullptr;
-  if (!STATE_ONLY) {
-    if (part.count > 1) {
-      from = p.ws + (part.place * p.H + h) * P * N;
-    } else if (slot >= 0 && seq_resumes(p.q, part.seq)) {
-      from = p.state + slot * p.slot_stride + static_cast<int64_t>(h) * P * N;
-    }
-  }
-#pragma unroll
-  for (int r = 0; r < RP; ++r)
-#pragma unroll
-    for (int j = 0; j < kCols; ++j) {
-      const int n = (j / 4 * tl + l) * 4 + j % 4, row = row0 + r0 + r;
-      s[r][j] = from && n < N && r0 + r < rows_here ? from[static_cast<int64_t>(row) * N + n] : 0.0f;
-    }
+  const int64_t PN = static_cast<int64_t>(P) * N;
 
   const T* x = static_cast<const T*>(p.x) + static_cast<int64_t>(h) * P + row0;
   const T* b = static_cast<const T*>(p.b) + static_cast<int64_t>(g) * N;
   const T* c = static_cast<const T*>(p.c) + static_cast<int64_t>(g) * N;
   const T* dtp = static_cast<const T*>(p.dt) + h;
   T* out = static_cast<T*>(p.out) + static_cast<int64_t>(h) * P + row0;
-  float log_decay = 0.0f;  // STATE_ONLY, thread 0
 
-  for (int64_t t0 = part.begin; t0 < part.end; t0 += kBlock) {
+  auto fetch = [&](int64_t t0, int buf) {
     const int nt = static_cast<int>(min(static_cast<int64_t>(kBlock), part.end - t0));
-    __syncthreads();
-    for (int i = tid; i < nt * NP; i += nthr) {
-      const int t = i / NP, n = i - t * NP;
-      sB[i] = n < N ? ld1(b + (t0 + t) * p.bs + n) : 0.0f;
-      if (!STATE_ONLY) sC[i] = n < N ? ld1(c + (t0 + t) * p.cs + n) : 0.0f;
+    for (int t = warp; t < nt; t += warps) {
+      copy_row(sB + (buf * kBlock + t) * sh.np, b + (t0 + t) * p.bs, N, sh.bc_bytes);
+      if (!STATE_ONLY) copy_row(sC + (buf * kBlock + t) * sh.np, c + (t0 + t) * p.cs, N, sh.bc_bytes);
+      copy_row(sX + (buf * kBlock + t) * sh.xp, x + (t0 + t) * p.xs, rows_here, sh.x_bytes);
     }
-    for (int i = tid; i < nt * prows; i += nthr) {
-      const int t = i / prows, r = i - t * prows;
-      sX[i] = r < rows_here ? ld1(x + (t0 + t) * p.xs + r) : 0.0f;
-    }
-    if (tid < nt) {
-      const float dt = dt_of(ld1(dtp + (t0 + tid) * p.dts), dbias, p);
-      sDt[tid] = dt;
-      sDt[kBlock + tid] = expf(dt * a);
-    }
-    __syncthreads();
-    if (STATE_ONLY && tid == 0)
-      for (int t = 0; t < nt; ++t) log_decay = fmaf(sDt[t], a, log_decay);
-    for (int t = 0; t < nt; ++t) {
-      const float dt = sDt[t], e = sDt[kBlock + t];
-      float xv[RP], y0[RP], y1[RP];
+  };
+  // columns behind N and rows behind the tile's are zeros throughout
+  for (int i = tid; i < 2 * kBlock * sh.np; i += blockDim.x)
+    if (i % sh.np >= N) Elem<T>::store1(sB, i, 0.0f), Elem<T>::store1(sC, i, 0.0f);
+  for (int i = tid; i < 2 * kBlock * sh.xp; i += blockDim.x)
+    if (i % sh.xp >= rows_here) Elem<T>::store1(sX, i, 0.0f);
+  float raw = 0.0f;
+  if (part.begin < part.end) {
+    fetch(part.begin, 0);
+    if (part.begin + tid < part.end && tid < kBlock) raw = ld1(dtp + (part.begin + tid) * p.dts);
+  }
+
+  F2 s[kRows][kCols / 2];  // columns 4 (TL k + l) .. in two pairs
+  // the state this part starts from: the workspace's for a cut sequence,
+  // else the pool's or zeros
+  const float* from = nullptr;
+  if (!STATE_ONLY) {
+    if (part.count > 1) from = p.ws + (part.place * p.H + h) * PN;
+    else if (slot >= 0 && seq_resumes(p.q, part.seq)) from = p.state + slot * p.slot_stride + h * PN;
+  }
 #pragma unroll
-      for (int r = 0; r < RP; ++r) {
-        xv[r] = dt * sX[t * prows + r0 + r];
-        y0[r] = y1[r] = 0.0f;
+  for (int r = 0; r < kRows; ++r)
+#pragma unroll
+    for (int j = 0; j < kCols; j += 2) {
+      const int n = (j / 4 * TL + l) * 4 + j % 4, row = row0 + r0 + r;
+      const bool here = from && r0 + r < rows_here;
+      s[r][j / 2] = pk2(here && n < N ? from[row * N + n] : 0.0f,
+                        here && n + 1 < N ? from[row * N + n + 1] : 0.0f);
+    }
+  float log_decay = 0.0f;  // STATE_ONLY, threads of the first block of tokens
+
+  int buf = 0;
+  for (int64_t t0 = part.begin; t0 < part.end; t0 += kBlock, buf ^= 1) {
+    const int nt = static_cast<int>(min(static_cast<int64_t>(kBlock), part.end - t0));
+    float* dts = sDt + buf * 2 * kBlock;
+    if (tid < nt) {
+      const float dt = dt_of(raw, dbias, p);
+      dts[tid] = dt;
+      dts[kBlock + tid] = expf(dt * a);
+      if (STATE_ONLY) log_decay = fmaf(dt, a, log_decay);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    if (t0 + kBlock < part.end) {
+      fetch(t0 + kBlock, buf ^ 1);
+      if (t0 + kBlock + tid < part.end && tid < kBlock)
+        raw = ld1(dtp + (t0 + kBlock + tid) * p.dts);
+    }
+    for (int t = 0; t < nt; ++t) {
+      const float dt = dts[t], e = dts[kBlock + t];
+      const T* bt = sB + (buf * kBlock + t) * sh.np;
+      const T* ct = sC + (buf * kBlock + t) * sh.np;
+      const Quad x4 = lds4(sX + (buf * kBlock + t) * sh.xp + r0);
+      float xv[kRows];
+      upk2(x4.lo, xv[0], xv[1]);
+      upk2(x4.hi, xv[2], xv[3]);
+      const F2 ee = pk2(e, e);
+      F2 xx[kRows], yy[kRows];
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        xv[r] *= dt;
+        xx[r] = pk2(xv[r], xv[r]);
+        yy[r] = 0;
       }
 #pragma unroll
-      for (int j = 0; j < kCols; j += 4) {
-        const float4 bv = *reinterpret_cast<const float4*>(sB + t * NP + (j / 4 * tl + l) * 4);
-        float4 cv = make_float4(0, 0, 0, 0);
-        if (!STATE_ONLY)
-          cv = *reinterpret_cast<const float4*>(sC + t * NP + (j / 4 * tl + l) * 4);
+      for (int j = 0; j < kCols / 4; ++j) {
+        const Quad bv = lds4(bt + (j * TL + l) * 4);
+        Quad cv = {0, 0};
+        if (!STATE_ONLY) cv = lds4(ct + (j * TL + l) * 4);
 #pragma unroll
-        for (int r = 0; r < RP; ++r) {
-          float u0, u1, u2, u3;
-          mul2(u0, u1, bv.x, bv.y, xv[r], xv[r]);
-          mul2(u2, u3, bv.z, bv.w, xv[r], xv[r]);
-          fma2(s[r][j], s[r][j + 1], s[r][j], s[r][j + 1], e, e, u0, u1);
-          fma2(s[r][j + 2], s[r][j + 3], s[r][j + 2], s[r][j + 3], e, e, u2, u3);
+        for (int r = 0; r < kRows; ++r) {
+          s[r][2 * j] = fma2(s[r][2 * j], ee, mul2(bv.lo, xx[r]));
+          s[r][2 * j + 1] = fma2(s[r][2 * j + 1], ee, mul2(bv.hi, xx[r]));
           if (!STATE_ONLY) {
-            fma2(y0[r], y1[r], s[r][j], s[r][j + 1], cv.x, cv.y, y0[r], y1[r]);
-            fma2(y0[r], y1[r], s[r][j + 2], s[r][j + 3], cv.z, cv.w, y0[r], y1[r]);
+            yy[r] = fma2(s[r][2 * j], cv.lo, yy[r]);
+            yy[r] = fma2(s[r][2 * j + 1], cv.hi, yy[r]);
           }
         }
       }
       if (!STATE_ONLY) {
+        float y[kRows];
 #pragma unroll
-        for (int r = 0; r < RP; ++r) {
-          float y = y0[r] + y1[r];
-          for (int o = tl >> 1; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-          if (l == 0) sY[t * prows + r0 + r] = y;
+        for (int r = 0; r < kRows; ++r) {
+          float y0, y1;
+          upk2(yy[r], y0, y1);
+          y[r] = y0 + y1;
+        }
+        team_sums<TL>(y, l);
+        float* yt = sY + t * prows + r0;
+        if constexpr (TL >= 4) {
+          // the lane whose low bits are zero writes the row of its high bits
+          if ((l & (TL / 4 - 1)) == 0)
+            yt[(l & (TL / 2) ? 2 : 0) + (l & (TL / 4) ? 1 : 0)] = y[0];
+        } else if constexpr (TL == 2) {
+          yt[2 * l] = y[0], yt[2 * l + 1] = y[1];
+        } else {
+#pragma unroll
+          for (int r = 0; r < kRows; ++r) yt[r] = y[r];
         }
       }
     }
+    __syncthreads();
     if (!STATE_ONLY) {
-      __syncthreads();
-      for (int i = tid; i < nt * prows; i += nthr) {
-        const int t = i / prows, r = i - t * prows;
-        if (r < rows_here)
-          Elem<T>::store1(out + (t0 + t) * p.os + r, 0, fmaf(dskip, sX[i], sY[i]));
-      }
+      for (int t = warp; t < nt; t += warps)
+        for (int r = lane; r < rows_here; r += 32)
+          Elem<T>::store1(out + (t0 + t) * p.os, r,
+                          fmaf(dskip, ld_smem(sX + (buf * kBlock + t) * sh.xp + r),
+                               sY[t * prows + r]));
     }
   }
 
   // where the state goes: the next part's place in the workspace, or the pool
   float* to = nullptr;
   if (STATE_ONLY) {
-    to = p.ws + ((part.place + 1) * p.H + h) * P * N;
-    if (tid == 0 && blockIdx.z == 0)
-      p.ws_decay[part.place * p.H + h] = expf(log_decay);
+    to = p.ws + ((part.place + 1) * p.H + h) * PN;
+    if (warp == 0 && blockIdx.z == 0) {
+#pragma unroll
+      for (int o = kBlock / 2; o > 0; o >>= 1)
+        log_decay += __shfl_xor_sync(0xffffffffu, log_decay, o);
+      if (lane == 0) p.ws_decay[part.place * p.H + h] = expf(log_decay);
+    }
   } else if (part.index == part.count - 1 && slot >= 0) {
-    to = p.state + slot * p.slot_stride + static_cast<int64_t>(h) * P * N;
+    to = p.state + slot * p.slot_stride + h * PN;
   }
   if (!to) return;
 #pragma unroll
-  for (int r = 0; r < RP; ++r)
+  for (int r = 0; r < kRows; ++r)
 #pragma unroll
-    for (int j = 0; j < kCols; ++j) {
-      const int n = (j / 4 * tl + l) * 4 + j % 4, row = row0 + r0 + r;
-      if (n < N && r0 + r < rows_here) to[static_cast<int64_t>(row) * N + n] = s[r][j];
+    for (int j = 0; j < kCols; j += 2) {
+      const int n = (j / 4 * TL + l) * 4 + j % 4, row = row0 + r0 + r;
+      float s0, s1;
+      upk2(s[r][j / 2], s0, s1);
+      if (n < N && r0 + r < rows_here) to[row * N + n] = s0;
+      if (n + 1 < N && r0 + r < rows_here) to[row * N + n + 1] = s1;
     }
 }
 
@@ -361,29 +478,33 @@ int pow2_at_least(int v) {
   return p;
 }
 
-// Rows of S per CTA and threads of k_scan.
-struct Shape {
-  int tl, threads, prows, ptiles;
-  size_t smem;
-};
-constexpr int kRowsPerThread = 4;
-Shape shape_of(int P, int N) {
-  Shape s;
+// k_scan's CTAs.
+Shape shape_of(int P, int N, int es) {
+  Shape s = {};
   s.tl = pow2_at_least((N + kCols - 1) / kCols);
-  const int most = kMaxThreads / s.tl * kRowsPerThread;  // rows of the largest CTA
+  const int most = std::min(kMaxThreads / s.tl * kRows, kMaxRows);  // rows of the largest CTA
   s.ptiles = (P + most - 1) / most;
-  const int teams = ((P + s.ptiles - 1) / s.ptiles + kRowsPerThread - 1) / kRowsPerThread;
+  const int teams = ((P + s.ptiles - 1) / s.ptiles + kRows - 1) / kRows;
   s.threads = (teams * s.tl + 31) / 32 * 32;
-  s.prows = s.threads / s.tl * kRowsPerThread;
+  s.prows = s.threads / s.tl * kRows;
   s.ptiles = (P + s.prows - 1) / s.prows;
-  s.smem = (2 * static_cast<size_t>(kBlock) * s.tl * kCols + 2 * kBlock * s.prows + 2 * kBlock) * 4;
+  s.np = s.tl * kCols;
+  s.xp = s.prows;
+  s.smem = static_cast<size_t>(es) * 2 * kBlock * (2 * s.np + s.xp) +
+           4 * static_cast<size_t>(kBlock) * (s.prows + 4);
   return s;
+}
+// The widest copy that every row of these layouts allows.
+int copy_bytes(std::initializer_list<int64_t> at) {
+  int64_t all = 16;
+  for (int64_t v : at) all |= v;
+  return all % 16 == 0 ? 16 : all % 8 == 0 ? 8 : all % 4 == 0 ? 4 : 2;
 }
 
 // Rows of a part of k_scan: long sequences are cut until the launch holds
-// about three CTAs for each SM.
+// about four CTAs for each SM.
 int64_t part_rows(int64_t rows, int64_t ctas_per_part) {
-  const int64_t want = 3 * static_cast<int64_t>(device_sms());
+  const int64_t want = 4 * static_cast<int64_t>(device_sms());
   const int64_t parts = std::max<int64_t>(1, want / std::max<int64_t>(1, ctas_per_part));
   const int64_t part = (rows + parts - 1) / parts;
   return std::max<int64_t>(kMinPart, (part + kBlock - 1) / kBlock * kBlock);
@@ -403,7 +524,8 @@ struct Layout {
 };
 Layout layout_of(const ggrn_scan_call& c) {
   Layout l;
-  const Shape s = shape_of(static_cast<int>(c.head_dim), static_cast<int>(c.state_size));
+  const Shape s = shape_of(static_cast<int>(c.head_dim), static_cast<int>(c.state_size),
+                           mixer::elem_bytes(c.dtype));
   l.tc = tc_covers(c);
   l.part = l.tc ? tc_part_rows(c, longest(c)) : part_rows(c.rows, c.heads * s.ptiles);
   if (longest(c) > INT32_MAX) l.part = longest(c);  // (the kernels count parts in 32 bits)
@@ -489,22 +611,52 @@ int check(const ggrn_scan_call& c, bool step, Params* p) {
   return GGRN_OK;
 }
 
-template <typename T>
-int run_typed(const ggrn_scan_call& c, Params& p, const Layout& l, cudaStream_t s) {
-  const Shape sh = shape_of(p.P, p.N);
-  if (l.parts > INT32_MAX || sh.ptiles > 65535 || (l.cut && p.q.seqs > 65535))
-    return GGRN_ERR_UNSUPPORTED;
+template <typename T, int TL>
+int run_team(const Params& p, const Shape& sh, const Layout& l, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>(l.parts), static_cast<unsigned>(p.H),
                   static_cast<unsigned>(sh.ptiles));
+  if (sh.smem > 48 * 1024) {  // wide states in f32: up to 84 KB
+    static std::once_flag once;
+    static cudaError_t err = cudaSuccess;
+    std::call_once(once, [] {
+      err = cudaFuncSetAttribute(k_scan<T, TL, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kMaxSmem);
+      if (err == cudaSuccess)
+        err = cudaFuncSetAttribute(k_scan<T, TL, false>,
+                                   cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    });
+    if (err != cudaSuccess) {
+      record_cuda_error(err);
+      return GGRN_ERR_CUDA;
+    }
+  }
   if (l.cut) {
-    int st = mixer::launch(k_scan<T, kRowsPerThread, true>, dim3(inner_parts(p), grid.y, grid.z),
-                           sh.threads, sh.smem, s, p, sh.tl, sh.prows);
+    int st = mixer::launch(k_scan<T, TL, true>, dim3(inner_parts(p), grid.y, grid.z), sh.threads,
+                           sh.smem, s, p, sh);
     if (st != GGRN_OK) return st;
     st = launch_join(p, s);
     if (st != GGRN_OK) return st;
   }
-  return mixer::launch(k_scan<T, kRowsPerThread, false>, grid, sh.threads, sh.smem, s, p, sh.tl,
-                       sh.prows);
+  return mixer::launch(k_scan<T, TL, false>, grid, sh.threads, sh.smem, s, p, sh);
+}
+
+template <typename T>
+int run_typed(const Params& p, const Layout& l, cudaStream_t s) {
+  constexpr int64_t es = sizeof(T);
+  Shape sh = shape_of(p.P, p.N, es);
+  if (l.parts > INT32_MAX || sh.ptiles > 65535 || (l.cut && p.q.seqs > 65535))
+    return GGRN_ERR_UNSUPPORTED;
+  auto at = [](const void* q) { return static_cast<int64_t>(reinterpret_cast<uintptr_t>(q)); };
+  sh.bc_bytes = copy_bytes({at(p.b), at(p.c), p.bs * es, p.cs * es, p.N * es});
+  // (a head's columns start at multiples of P, a tile's of prows)
+  sh.x_bytes = copy_bytes({at(p.x), p.xs * es, p.P * es, sh.prows * es});
+  switch (sh.tl) {
+    case 1: return run_team<T, 1>(p, sh, l, s);
+    case 2: return run_team<T, 2>(p, sh, l, s);
+    case 4: return run_team<T, 4>(p, sh, l, s);
+    case 8: return run_team<T, 8>(p, sh, l, s);
+    default: return run_team<T, 16>(p, sh, l, s);
+  }
 }
 
 template <typename T>
@@ -555,9 +707,9 @@ int run(const ggrn_scan_call* call, bool step, void* stream) {
     if (l.parts > INT32_MAX || (l.cut && p.q.seqs > 65535)) return GGRN_ERR_UNSUPPORTED;
     return tc_run(c, p, l.cut, s);
   }
-  if (c.dtype == kF32) return run_typed<float>(c, p, l, s);
-  if (c.dtype == kF16) return run_typed<__half>(c, p, l, s);
-  return run_typed<__nv_bfloat16>(c, p, l, s);
+  if (c.dtype == kF32) return run_typed<float>(p, l, s);
+  if (c.dtype == kF16) return run_typed<__half>(p, l, s);
+  return run_typed<__nv_bfloat16>(p, l, s);
 }
 
 int launch_join(const Params& p, cudaStream_t s) {

@@ -26,6 +26,20 @@ struct Params {
   int softplus;
 };
 
+// f32 pairs kept in one 64-bit register: the arithmetic on values that are
+// pairs from their load on needs no moves.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 // dt of one token and head: softplus as log1p(exp(v)), v itself from 20 on
 // (the difference is below 2^-28 of it); a NaN stays one.
 __device__ __forceinline__ float dt_of(float raw, float bias, const Params& p) {

@@ -163,19 +163,6 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
 }
 using Bf = Elem<__nv_bfloat16>;
 
-// f32 pairs kept in one 64-bit register: the arithmetic on values that are
-// pairs from their load on needs no moves.
-using F2 = unsigned long long;
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 __device__ __forceinline__ F2 pair(uint32_t a, uint32_t b) {
   return pk2(__uint_as_float(a), __uint_as_float(b));
 }

@@ -79,6 +79,7 @@ def check_state(got, want, bound, size):
 SHAPES = [  # heads, head_dim, groups, state_size
     (4, 64, 1, 128), (6, 80, 2, 128), (3, 128, 3, 64), (4, 100, 1, 16), (2, 5, 1, 3),
     (1, 1, 1, 1), (2, 130, 1, 256), (5, 36, 5, 100), (8, 64, 2, 96), (3, 88, 1, 40),
+    (1, 1030, 1, 12), (2, 256, 1, 250),
 ]
 
 
