@@ -72,6 +72,7 @@ __device__ __forceinline__ float ld_smem(const T* p) {
 struct Shape {
   int tl, threads, prows, ptiles;
   int bc_bytes, x_bytes;
+  bool vec;        // rows of the state in 16-byte vectors
   int np, xp;      // elements of a row of B or C, and of x, in shared memory
   size_t smem;
 };
@@ -82,11 +83,13 @@ __device__ __forceinline__ void copy_row(T* dst, const T* src, int cols, int byt
   const int lane = threadIdx.x & 31;
   const int total = cols * static_cast<int>(sizeof(T));
   if (bytes == 2) {
+#pragma unroll 1
     for (int i = lane; i < cols; i += 32) dst[i] = src[i];
     return;
   }
   const uint32_t d = smem_u32(dst);
   const char* s = reinterpret_cast<const char*>(src);
+#pragma unroll 1
   for (int i = lane * bytes; i < total; i += 32 * bytes) {
     if (bytes == 16)
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d + i), "l"(s + i) : "memory");
@@ -119,7 +122,7 @@ __device__ __forceinline__ void team_sums(float (&v)[4], int l) {
 
 // `STATE_ONLY`: the first launch of a cut scan.
 template <typename T, int TL, bool STATE_ONLY>
-__global__ void __launch_bounds__(kMaxThreads) k_scan(const Params p, const Shape sh) {
+__global__ void __launch_bounds__(kMaxThreads, 2) k_scan(const Params p, const Shape sh) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   pdl_wait();
   pdl_launch_dependents();
@@ -153,6 +156,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_scan(const Params p, const Shap
 
   auto fetch = [&](int64_t t0, int buf) {
     const int nt = static_cast<int>(min(static_cast<int64_t>(kBlock), part.end - t0));
+#pragma unroll 1
     for (int t = warp; t < nt; t += warps) {
       copy_row(sB + (buf * kBlock + t) * sh.np, b + (t0 + t) * p.bs, N, sh.bc_bytes);
       if (!STATE_ONLY) copy_row(sC + (buf * kBlock + t) * sh.np, c + (t0 + t) * p.cs, N, sh.bc_bytes);
@@ -160,10 +164,14 @@ __global__ void __launch_bounds__(kMaxThreads) k_scan(const Params p, const Shap
     }
   };
   // columns behind N and rows behind the tile's are zeros throughout
-  for (int i = tid; i < 2 * kBlock * sh.np; i += blockDim.x)
-    if (i % sh.np >= N) Elem<T>::store1(sB, i, 0.0f), Elem<T>::store1(sC, i, 0.0f);
-  for (int i = tid; i < 2 * kBlock * sh.xp; i += blockDim.x)
-    if (i % sh.xp >= rows_here) Elem<T>::store1(sX, i, 0.0f);
+#pragma unroll 1
+  for (int t = warp; t < 2 * kBlock; t += warps) {
+#pragma unroll 1
+    for (int i = N + lane; i < sh.np; i += 32)
+      Elem<T>::store1(sB + t * sh.np, i, 0.0f), Elem<T>::store1(sC + t * sh.np, i, 0.0f);
+#pragma unroll 1
+    for (int i = rows_here + lane; i < sh.xp; i += 32) Elem<T>::store1(sX + t * sh.xp, i, 0.0f);
+  }
   float raw = 0.0f;
   if (part.begin < part.end) {
     fetch(part.begin, 0);
@@ -179,17 +187,93 @@ __global__ void __launch_bounds__(kMaxThreads) k_scan(const Params p, const Shap
     else if (slot >= 0 && seq_resumes(p.q, part.seq)) from = p.state + slot * p.slot_stride + h * PN;
   }
 #pragma unroll
-  for (int r = 0; r < kRows; ++r)
+  for (int r = 0; r < kRows; ++r) {
+    const float* at = from + static_cast<int64_t>(row0 + r0 + r) * N + l * 4;
+    const bool here = from && r0 + r < rows_here;
 #pragma unroll
-    for (int j = 0; j < kCols; j += 2) {
-      const int n = (j / 4 * TL + l) * 4 + j % 4, row = row0 + r0 + r;
-      const bool here = from && r0 + r < rows_here;
-      s[r][j / 2] = pk2(here && n < N ? from[row * N + n] : 0.0f,
-                        here && n + 1 < N ? from[row * N + n + 1] : 0.0f);
+    for (int j = 0; j < kCols / 4; ++j) {
+      float q[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      const int left = here ? N - (j * TL + l) * 4 : 0;
+      if (sh.vec) {
+        if (left > 0) {
+          const float4 v = *reinterpret_cast<const float4*>(at + j * TL * 4);
+          q[0] = v.x, q[1] = v.y, q[2] = v.z, q[3] = v.w;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (i < left) q[i] = at[j * TL * 4 + i];
+      }
+      s[r][2 * j] = pk2(q[0], q[1]), s[r][2 * j + 1] = pk2(q[2], q[3]);
     }
+  }
   float log_decay = 0.0f;  // STATE_ONLY, threads of the first block of tokens
 
+  // K tokens from token t of the block on
+  auto tokens = [&](auto k_tokens, int t, int buf, const float* dts) __attribute__((always_inline)) {
+    constexpr int K = decltype(k_tokens)::value;
+    const T* bt = sB + (buf * kBlock + t) * sh.np + l * 4;
+    const T* ct = sC + (buf * kBlock + t) * sh.np + l * 4;
+    const T* xt = sX + (buf * kBlock + t) * sh.xp + r0;
+    F2 ee[K], xx[K][kRows], yy[K][kRows];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const float dt = dts[t + k], e = dts[kBlock + t + k];
+      const Quad x4 = lds4(xt + k * sh.xp);
+      float xv[kRows];
+      upk2(x4.lo, xv[0], xv[1]);
+      upk2(x4.hi, xv[2], xv[3]);
+      ee[k] = pk2(e, e);
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) xx[k][r] = pk2(dt * xv[r], dt * xv[r]);
+    }
+#pragma unroll
+    for (int j = 0; j < kCols / 4; ++j)
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const Quad bv = lds4(bt + k * sh.np + j * TL * 4);
+        Quad cv = {0, 0};
+        if (!STATE_ONLY) cv = lds4(ct + k * sh.np + j * TL * 4);
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+          s[r][2 * j] = fma2(s[r][2 * j], ee[k], mul2(bv.lo, xx[k][r]));
+          s[r][2 * j + 1] = fma2(s[r][2 * j + 1], ee[k], mul2(bv.hi, xx[k][r]));
+          if (!STATE_ONLY) {
+            yy[k][r] = j == 0 ? mul2(s[r][0], cv.lo) : fma2(s[r][2 * j], cv.lo, yy[k][r]);
+            yy[k][r] = fma2(s[r][2 * j + 1], cv.hi, yy[k][r]);
+          }
+        }
+      }
+    if (STATE_ONLY) return;
+    float y[K][kRows];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        float y0, y1;
+        upk2(yy[k][r], y0, y1);
+        y[k][r] = y0 + y1;
+      }
+      team_sums<TL>(y[k], l);
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float* yt = sY + (t + k) * prows + r0;
+      if constexpr (TL >= 4) {
+        // the lane whose low bits are zero writes the row of its high bits
+        if ((l & (TL / 4 - 1)) == 0)
+          yt[(l & (TL / 2) ? 2 : 0) + (l & (TL / 4) ? 1 : 0)] = y[k][0];
+      } else if constexpr (TL == 2) {
+        yt[2 * l] = y[k][0], yt[2 * l + 1] = y[k][1];
+      } else {
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) yt[r] = y[k][r];
+      }
+    }
+  };
+
   int buf = 0;
+#pragma unroll 1
   for (int64_t t0 = part.begin; t0 < part.end; t0 += kBlock, buf ^= 1) {
     const int nt = static_cast<int>(min(static_cast<int64_t>(kBlock), part.end - t0));
     float* dts = sDt + buf * 2 * kBlock;
@@ -206,62 +290,16 @@ __global__ void __launch_bounds__(kMaxThreads) k_scan(const Params p, const Shap
       if (t0 + kBlock + tid < part.end && tid < kBlock)
         raw = ld1(dtp + (t0 + kBlock + tid) * p.dts);
     }
-    for (int t = 0; t < nt; ++t) {
-      const float dt = dts[t], e = dts[kBlock + t];
-      const T* bt = sB + (buf * kBlock + t) * sh.np;
-      const T* ct = sC + (buf * kBlock + t) * sh.np;
-      const Quad x4 = lds4(sX + (buf * kBlock + t) * sh.xp + r0);
-      float xv[kRows];
-      upk2(x4.lo, xv[0], xv[1]);
-      upk2(x4.hi, xv[2], xv[3]);
-      const F2 ee = pk2(e, e);
-      F2 xx[kRows], yy[kRows];
-#pragma unroll
-      for (int r = 0; r < kRows; ++r) {
-        xv[r] *= dt;
-        xx[r] = pk2(xv[r], xv[r]);
-        yy[r] = 0;
-      }
-#pragma unroll
-      for (int j = 0; j < kCols / 4; ++j) {
-        const Quad bv = lds4(bt + (j * TL + l) * 4);
-        Quad cv = {0, 0};
-        if (!STATE_ONLY) cv = lds4(ct + (j * TL + l) * 4);
-#pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-          s[r][2 * j] = fma2(s[r][2 * j], ee, mul2(bv.lo, xx[r]));
-          s[r][2 * j + 1] = fma2(s[r][2 * j + 1], ee, mul2(bv.hi, xx[r]));
-          if (!STATE_ONLY) {
-            yy[r] = fma2(s[r][2 * j], cv.lo, yy[r]);
-            yy[r] = fma2(s[r][2 * j + 1], cv.hi, yy[r]);
-          }
-        }
-      }
-      if (!STATE_ONLY) {
-        float y[kRows];
-#pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-          float y0, y1;
-          upk2(yy[r], y0, y1);
-          y[r] = y0 + y1;
-        }
-        team_sums<TL>(y, l);
-        float* yt = sY + t * prows + r0;
-        if constexpr (TL >= 4) {
-          // the lane whose low bits are zero writes the row of its high bits
-          if ((l & (TL / 4 - 1)) == 0)
-            yt[(l & (TL / 2) ? 2 : 0) + (l & (TL / 4) ? 1 : 0)] = y[0];
-        } else if constexpr (TL == 2) {
-          yt[2 * l] = y[0], yt[2 * l + 1] = y[1];
-        } else {
-#pragma unroll
-          for (int r = 0; r < kRows; ++r) yt[r] = y[r];
-        }
-      }
-    }
+    // tokens by pairs, for more instructions that do not wait for one another
+    int t = 0;
+#pragma unroll 1
+    for (; t + 2 <= nt; t += 2) tokens(std::integral_constant<int, 2>(), t, buf, dts);
+    if (t < nt) tokens(std::integral_constant<int, 1>(), t, buf, dts);
     __syncthreads();
     if (!STATE_ONLY) {
+#pragma unroll 1
       for (int t = warp; t < nt; t += warps)
+#pragma unroll 1
         for (int r = lane; r < rows_here; r += 32)
           Elem<T>::store1(out + (t0 + t) * p.os, r,
                           fmaf(dskip, ld_smem(sX + (buf * kBlock + t) * sh.xp + r),
@@ -284,15 +322,24 @@ __global__ void __launch_bounds__(kMaxThreads) k_scan(const Params p, const Shap
   }
   if (!to) return;
 #pragma unroll
-  for (int r = 0; r < kRows; ++r)
+  for (int r = 0; r < kRows; ++r) {
+    float* at = to + static_cast<int64_t>(row0 + r0 + r) * N + l * 4;
 #pragma unroll
-    for (int j = 0; j < kCols; j += 2) {
-      const int n = (j / 4 * TL + l) * 4 + j % 4, row = row0 + r0 + r;
-      float s0, s1;
-      upk2(s[r][j / 2], s0, s1);
-      if (n < N && r0 + r < rows_here) to[row * N + n] = s0;
-      if (n + 1 < N && r0 + r < rows_here) to[row * N + n + 1] = s1;
+    for (int j = 0; j < kCols / 4; ++j) {
+      float q[4];
+      upk2(s[r][2 * j], q[0], q[1]);
+      upk2(s[r][2 * j + 1], q[2], q[3]);
+      const int left = r0 + r < rows_here ? N - (j * TL + l) * 4 : 0;
+      if (sh.vec) {
+        if (left > 0)
+          *reinterpret_cast<float4*>(at + j * TL * 4) = make_float4(q[0], q[1], q[2], q[3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (i < left) at[j * TL * 4 + i] = q[i];
+      }
     }
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -302,6 +349,8 @@ __global__ void __launch_bounds__(kMaxThreads) k_scan(const Params p, const Shap
 // parts of its sequence.  grid: (blocks of entries, heads, cut sequences: there
 // are at most rows / part).
 // ---------------------------------------------------------------------------
+constexpr int kJoinAhead = 8;  // parts whose entries are in flight
+
 template <int V>
 __global__ void __launch_bounds__(256) k_scan_join(const Params p) {
   pdl_wait();
@@ -357,17 +406,28 @@ __global__ void __launch_bounds__(256) k_scan_join(const Params p) {
   const float* decay = p.ws_decay + first * p.H + h;
   *reinterpret_cast<W*>(w) = s;
   const int64_t stride = static_cast<int64_t>(p.H) * PN;
-  for (int64_t k = 0; k + 1 < count; ++k) {
-    w += stride;
-    const float d = decay[k * p.H];
-    const W add = *reinterpret_cast<const W*>(w);
-    if constexpr (V == 4) {
-      s.x = fmaf(s.x, d, add.x), s.y = fmaf(s.y, d, add.y);
-      s.z = fmaf(s.z, d, add.z), s.w = fmaf(s.w, d, add.w);
-    } else {
-      s = fmaf(s, d, add);
-    }
-    *reinterpret_cast<W*>(w) = s;
+  for (int64_t k = 0; k + 1 < count; k += kJoinAhead) {
+    W add[kJoinAhead];
+    float d[kJoinAhead];
+    const int n = static_cast<int>(min(count - 1 - k, static_cast<int64_t>(kJoinAhead)));
+#pragma unroll
+    for (int j = 0; j < kJoinAhead; ++j)
+      if (j < n) {
+        d[j] = decay[(k + j) * p.H];
+        add[j] = *reinterpret_cast<const W*>(w + (j + 1) * stride);
+      }
+#pragma unroll
+    for (int j = 0; j < kJoinAhead; ++j)
+      if (j < n) {
+        if constexpr (V == 4) {
+          s.x = fmaf(s.x, d[j], add[j].x), s.y = fmaf(s.y, d[j], add[j].y);
+          s.z = fmaf(s.z, d[j], add[j].z), s.w = fmaf(s.w, d[j], add[j].w);
+        } else {
+          s = fmaf(s, d[j], add[j]);
+        }
+        *reinterpret_cast<W*>(w + (j + 1) * stride) = s;
+      }
+    w += kJoinAhead * stride;
   }
 }
 
@@ -650,6 +710,7 @@ int run_typed(const Params& p, const Layout& l, cudaStream_t s) {
   sh.bc_bytes = copy_bytes({at(p.b), at(p.c), p.bs * es, p.cs * es, p.N * es});
   // (a head's columns start at multiples of P, a tile's of prows)
   sh.x_bytes = copy_bytes({at(p.x), p.xs * es, p.P * es, sh.prows * es});
+  sh.vec = p.N % 4 == 0 && (!p.state || (mixer::aligned_to(p.state, 16) && p.slot_stride % 4 == 0));
   switch (sh.tl) {
     case 1: return run_team<T, 1>(p, sh, l, s);
     case 2: return run_team<T, 2>(p, sh, l, s);
