@@ -11,7 +11,9 @@
 // lives in registers in f32 (4 rows of S x 16 columns per thread, a team of TL
 // lanes across the columns), tokens come in blocks of 16 through shared memory
 // (asynchronous copies, a block ahead), three f32x2 instructions per pair of
-// state entries and token, which bound it.
+// state entries and token, which bound it: each takes the multiply-add pipe for
+// two cycles, and the pipe is busy 59 % of the time (1025 tokens of 48 heads of
+// 100 x 64 in f32: 131 us with the parts' states).
 //
 // A sequence longer than a part (see find_part) is cut: a first launch runs
 // every part but the last of its sequence from a zero state, for its final
@@ -73,30 +75,36 @@ struct Shape {
   int tl, threads, prows, ptiles;
   int bc_bytes, x_bytes;
   bool vec;        // rows of the state in 16-byte vectors
-  int np, xp;      // elements of a row of B or C, and of x, in shared memory
+  int np;          // elements of a row of B or C in shared memory
   size_t smem;
 };
 
-// `cols` elements of a row into shared memory by one warp.
-template <typename T>
-__device__ __forceinline__ void copy_row(T* dst, const T* src, int cols, int bytes) {
-  const int lane = threadIdx.x & 31;
+// `cols` elements of a row into shared memory by one warp, BYTES at a time.
+template <int BYTES, typename T>
+__device__ __forceinline__ void copy_row(T* dst, const T* src, int cols) {
   const int total = cols * static_cast<int>(sizeof(T));
-  if (bytes == 2) {
-#pragma unroll 1
-    for (int i = lane; i < cols; i += 32) dst[i] = src[i];
-    return;
-  }
   const uint32_t d = smem_u32(dst);
   const char* s = reinterpret_cast<const char*>(src);
 #pragma unroll 1
-  for (int i = lane * bytes; i < total; i += 32 * bytes) {
-    if (bytes == 16)
+  for (int i = (threadIdx.x & 31) * BYTES; i < total; i += 32 * BYTES) {
+    if constexpr (BYTES == 16)
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d + i), "l"(s + i) : "memory");
-    else if (bytes == 8)
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(d + i), "l"(s + i) : "memory");
     else
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d + i), "l"(s + i) : "memory");
+      asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d + i), "l"(s + i), "n"(BYTES)
+                   : "memory");
+  }
+}
+template <typename T>
+__device__ __forceinline__ void copy_row(T* dst, const T* src, int cols, int bytes) {
+  if (bytes == 16) {
+    copy_row<16>(dst, src, cols);
+  } else if (bytes == 8) {
+    copy_row<8>(dst, src, cols);
+  } else if (bytes == 4) {
+    copy_row<4>(dst, src, cols);
+  } else {
+#pragma unroll 1
+    for (int i = threadIdx.x & 31; i < cols; i += 32) dst[i] = src[i];
   }
 }
 
@@ -137,12 +145,17 @@ __global__ void __launch_bounds__(kMaxThreads, 2) k_scan(const Params p, const S
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
   const int l = tid & (TL - 1);
   const int r0 = tid / TL * kRows;           // this thread's first row of the tile
-  // shared memory: two blocks of B, C and x rows; y rows; dt and decays
+  // shared memory: two blocks of B, C and x rows as they come; one of (dt x)
+  // as pairs of equal halves, in whose places the y are left; one of B and C in
+  // f32 if T is not; dt and decays
+  constexpr bool kWiden = sizeof(T) == 2;
   T* sB = reinterpret_cast<T*>(smem_raw);    // [2][kBlock][np]
   T* sC = sB + 2 * kBlock * sh.np;
-  T* sX = sC + 2 * kBlock * sh.np;           // [2][kBlock][xp]
-  float* sY = reinterpret_cast<float*>(sX + 2 * kBlock * sh.xp);  // [kBlock][prows]
-  float* sDt = sY + kBlock * prows;          // [2][kBlock] dt, decay
+  T* sX = sC + 2 * kBlock * sh.np;           // [2][kBlock][prows]
+  float* sXX = reinterpret_cast<float*>(sX + 2 * kBlock * prows);  // [kBlock][prows][2]
+  float* sBf = sXX + 2 * kBlock * prows;     // [kBlock][np]
+  float* sCf = sBf + kBlock * sh.np;
+  float* sDt = kWiden ? sCf + kBlock * sh.np : sBf;  // [2][kBlock] dt, decay
   const float a = __ldg(p.a + h), dbias = p.dt_bias ? __ldg(p.dt_bias + h) : 0.0f;
   const float dskip = p.d ? __ldg(p.d + h) : 0.0f;
   const int64_t slot = seq_slot(p.q, part.seq);
@@ -156,11 +169,22 @@ __global__ void __launch_bounds__(kMaxThreads, 2) k_scan(const Params p, const S
 
   auto fetch = [&](int64_t t0, int buf) {
     const int nt = static_cast<int>(min(static_cast<int64_t>(kBlock), part.end - t0));
+    const T* bt = b + (t0 + warp) * p.bs;
+    const T* ct = c + (t0 + warp) * p.cs;
+    const T* xt = x + (t0 + warp) * p.xs;
+    int row = buf * kBlock + warp;
 #pragma unroll 1
-    for (int t = warp; t < nt; t += warps) {
-      copy_row(sB + (buf * kBlock + t) * sh.np, b + (t0 + t) * p.bs, N, sh.bc_bytes);
-      if (!STATE_ONLY) copy_row(sC + (buf * kBlock + t) * sh.np, c + (t0 + t) * p.cs, N, sh.bc_bytes);
-      copy_row(sX + (buf * kBlock + t) * sh.xp, x + (t0 + t) * p.xs, rows_here, sh.x_bytes);
+    for (int t = warp; t < nt; t += warps, row += warps) {
+      if (sh.bc_bytes == 16 && sh.x_bytes == 16) {  // as a rule
+        copy_row<16>(sB + row * sh.np, bt, N);
+        if (!STATE_ONLY) copy_row<16>(sC + row * sh.np, ct, N);
+        copy_row<16>(sX + row * prows, xt, rows_here);
+      } else {
+        copy_row(sB + row * sh.np, bt, N, sh.bc_bytes);
+        if (!STATE_ONLY) copy_row(sC + row * sh.np, ct, N, sh.bc_bytes);
+        copy_row(sX + row * prows, xt, rows_here, sh.x_bytes);
+      }
+      bt += warps * p.bs, ct += warps * p.cs, xt += warps * p.xs;
     }
   };
   // columns behind N and rows behind the tile's are zeros throughout
@@ -170,7 +194,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) k_scan(const Params p, const S
     for (int i = N + lane; i < sh.np; i += 32)
       Elem<T>::store1(sB + t * sh.np, i, 0.0f), Elem<T>::store1(sC + t * sh.np, i, 0.0f);
 #pragma unroll 1
-    for (int i = rows_here + lane; i < sh.xp; i += 32) Elem<T>::store1(sX + t * sh.xp, i, 0.0f);
+    for (int i = rows_here + lane; i < prows; i += 32) Elem<T>::store1(sX + t * prows, i, 0.0f);
   }
   float raw = 0.0f;
   if (part.begin < part.end) {
@@ -210,22 +234,19 @@ __global__ void __launch_bounds__(kMaxThreads, 2) k_scan(const Params p, const S
   float log_decay = 0.0f;  // STATE_ONLY, threads of the first block of tokens
 
   // K tokens from token t of the block on
-  auto tokens = [&](auto k_tokens, int t, int buf, const float* dts) __attribute__((always_inline)) {
+  using Staged = typename std::conditional<kWiden, float, T>::type;
+  auto tokens = [&](auto k_tokens, int t, const Staged* bt, const Staged* ct,
+                    const float* dts) __attribute__((always_inline)) {
     constexpr int K = decltype(k_tokens)::value;
-    const T* bt = sB + (buf * kBlock + t) * sh.np + l * 4;
-    const T* ct = sC + (buf * kBlock + t) * sh.np + l * 4;
-    const T* xt = sX + (buf * kBlock + t) * sh.xp + r0;
+    bt += t * sh.np + l * 4;
+    ct += t * sh.np + l * 4;
+    float* xt = sXX + (t * prows + r0) * 2;
     F2 ee[K], xx[K][kRows], yy[K][kRows];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const float dt = dts[t + k], e = dts[kBlock + t + k];
-      const Quad x4 = lds4(xt + k * sh.xp);
-      float xv[kRows];
-      upk2(x4.lo, xv[0], xv[1]);
-      upk2(x4.hi, xv[2], xv[3]);
-      ee[k] = pk2(e, e);
-#pragma unroll
-      for (int r = 0; r < kRows; ++r) xx[k][r] = pk2(dt * xv[r], dt * xv[r]);
+      ee[k] = *reinterpret_cast<const F2*>(dts + kBlock + 2 * (t + k));
+      const Quad lo = lds4(xt + k * prows * 2), hi = lds4(xt + k * prows * 2 + 4);
+      xx[k][0] = lo.lo, xx[k][1] = lo.hi, xx[k][2] = hi.lo, xx[k][3] = hi.hi;
     }
 #pragma unroll
     for (int j = 0; j < kCols / 4; ++j)
@@ -244,30 +265,32 @@ __global__ void __launch_bounds__(kMaxThreads, 2) k_scan(const Params p, const S
           }
         }
       }
-    if (STATE_ONLY) return;
-    float y[K][kRows];
+    if constexpr (!STATE_ONLY) {
+      float y[K][kRows];
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
+      for (int k = 0; k < K; ++k) {
 #pragma unroll
-      for (int r = 0; r < kRows; ++r) {
-        float y0, y1;
-        upk2(yy[k][r], y0, y1);
-        y[k][r] = y0 + y1;
+        for (int r = 0; r < kRows; ++r) {
+          float y0, y1;
+          upk2(yy[k][r], y0, y1);
+          y[k][r] = y0 + y1;
+        }
+        team_sums<TL>(y[k], l);
       }
-      team_sums<TL>(y[k], l);
-    }
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      float* yt = sY + (t + k) * prows + r0;
-      if constexpr (TL >= 4) {
-        // the lane whose low bits are zero writes the row of its high bits
-        if ((l & (TL / 4 - 1)) == 0)
-          yt[(l & (TL / 2) ? 2 : 0) + (l & (TL / 4) ? 1 : 0)] = y[k][0];
-      } else if constexpr (TL == 2) {
-        yt[2 * l] = y[k][0], yt[2 * l + 1] = y[k][1];
-      } else {
+      for (int k = 0; k < K; ++k) {
+        // (only this team reads these places)
+        float* yt = xt + k * prows * 2;
+        if constexpr (TL >= 4) {
+          // the lane whose low bits are zero writes the row of its high bits
+          if ((l & (TL / 4 - 1)) == 0)
+            yt[(l & (TL / 2) ? 4 : 0) + (l & (TL / 4) ? 2 : 0)] = y[k][0];
+        } else if constexpr (TL == 2) {
+          yt[4 * l] = y[k][0], yt[4 * l + 2] = y[k][1];
+        } else {
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) yt[r] = y[k][r];
+          for (int r = 0; r < kRows; ++r) yt[2 * r] = y[k][r];
+        }
       }
     }
   };
@@ -276,11 +299,11 @@ __global__ void __launch_bounds__(kMaxThreads, 2) k_scan(const Params p, const S
 #pragma unroll 1
   for (int64_t t0 = part.begin; t0 < part.end; t0 += kBlock, buf ^= 1) {
     const int nt = static_cast<int>(min(static_cast<int64_t>(kBlock), part.end - t0));
-    float* dts = sDt + buf * 2 * kBlock;
+    float* dts = sDt + buf * 3 * kBlock;  // dt; decays, twice each
     if (tid < nt) {
-      const float dt = dt_of(raw, dbias, p);
+      const float dt = dt_of(raw, dbias, p), e = expf(dt * a);
       dts[tid] = dt;
-      dts[kBlock + tid] = expf(dt * a);
+      *reinterpret_cast<float2*>(dts + kBlock + 2 * tid) = make_float2(e, e);
       if (STATE_ONLY) log_decay = fmaf(dt, a, log_decay);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -290,20 +313,56 @@ __global__ void __launch_bounds__(kMaxThreads, 2) k_scan(const Params p, const S
       if (t0 + kBlock + tid < part.end && tid < kBlock)
         raw = ld1(dtp + (t0 + kBlock + tid) * p.dts);
     }
+    const T* bb = sB + buf * kBlock * sh.np;
+    const T* cb = sC + buf * kBlock * sh.np;
+    const T* xb = sX + buf * kBlock * prows;
+#pragma unroll 1
+    for (int t = warp; t < nt; t += warps) {
+      const F2 dd = pk2(dts[t], dts[t]);
+#pragma unroll 1
+      for (int i = lane * 4; i < prows; i += 128) {
+        const Quad q = lds4(xb + t * prows + i);
+        float v[4];
+        upk2(mul2(q.lo, dd), v[0], v[1]);
+        upk2(mul2(q.hi, dd), v[2], v[3]);
+        float4* to = reinterpret_cast<float4*>(sXX + (t * prows + i) * 2);
+        to[0] = make_float4(v[0], v[0], v[1], v[1]);
+        to[1] = make_float4(v[2], v[2], v[3], v[3]);
+      }
+      if constexpr (kWiden) {
+#pragma unroll 1
+        for (int i = lane * 4; i < sh.np; i += 128) {
+          const int at = t * sh.np + i;
+          const Quad q = lds4(bb + at);
+          *reinterpret_cast<ulonglong2*>(sBf + at) = make_ulonglong2(q.lo, q.hi);
+          if (!STATE_ONLY) {
+            const Quad r = lds4(cb + at);
+            *reinterpret_cast<ulonglong2*>(sCf + at) = make_ulonglong2(r.lo, r.hi);
+          }
+        }
+      }
+    }
+    __syncthreads();
     // tokens by pairs, for more instructions that do not wait for one another
+    const Staged* bt;
+    const Staged* ct;
+    if constexpr (kWiden) {
+      bt = sBf, ct = sCf;
+    } else {
+      bt = bb, ct = cb;
+    }
     int t = 0;
 #pragma unroll 1
-    for (; t + 2 <= nt; t += 2) tokens(std::integral_constant<int, 2>(), t, buf, dts);
-    if (t < nt) tokens(std::integral_constant<int, 1>(), t, buf, dts);
+    for (; t + 2 <= nt; t += 2) tokens(std::integral_constant<int, 2>(), t, bt, ct, dts);
+    if (t < nt) tokens(std::integral_constant<int, 1>(), t, bt, ct, dts);
     __syncthreads();
     if (!STATE_ONLY) {
+      T* ot = out + (t0 + warp) * p.os;
 #pragma unroll 1
-      for (int t = warp; t < nt; t += warps)
+      for (int t = warp; t < nt; t += warps, ot += warps * p.os)
 #pragma unroll 1
         for (int r = lane; r < rows_here; r += 32)
-          Elem<T>::store1(out + (t0 + t) * p.os, r,
-                          fmaf(dskip, ld_smem(sX + (buf * kBlock + t) * sh.xp + r),
-                               sY[t * prows + r]));
+          Elem<T>::store1(ot, r, fmaf(dskip, ld_smem(xb + t * prows + r), sXX[(t * prows + r) * 2]));
     }
   }
 
@@ -349,7 +408,9 @@ __global__ void __launch_bounds__(kMaxThreads, 2) k_scan(const Params p, const S
 // parts of its sequence.  grid: (blocks of entries, heads, cut sequences: there
 // are at most rows / part).
 // ---------------------------------------------------------------------------
-constexpr int kJoinAhead = 8;  // parts whose entries are in flight
+// Parts whose entries are in flight (eight cost registers, and with them warps:
+// 5 % of a ragged scan's time).
+constexpr int kJoinAhead = 2;
 
 template <int V>
 __global__ void __launch_bounds__(256) k_scan_join(const Params p) {
@@ -549,9 +610,8 @@ Shape shape_of(int P, int N, int es) {
   s.prows = s.threads / s.tl * kRows;
   s.ptiles = (P + s.prows - 1) / s.prows;
   s.np = s.tl * kCols;
-  s.xp = s.prows;
-  s.smem = static_cast<size_t>(es) * 2 * kBlock * (2 * s.np + s.xp) +
-           4 * static_cast<size_t>(kBlock) * (s.prows + 4);
+  s.smem = static_cast<size_t>(es) * 2 * kBlock * (2 * s.np + s.prows) +
+           4 * static_cast<size_t>(kBlock) * (2 * s.prows + (es == 2 ? 2 * s.np : 0) + 6);
   return s;
 }
 // The widest copy that every row of these layouts allows.
@@ -562,9 +622,11 @@ int copy_bytes(std::initializer_list<int64_t> at) {
 }
 
 // Rows of a part of k_scan: long sequences are cut until the launch holds
-// about four CTAs for each SM.
+// about eight CTAs for each SM.  4096 tokens of 96 heads of 80 x 128 in f16:
+// 2237 us with two, 1676 with three, 1496 with four, 1399 with eight; more
+// parts cost more states to join.
 int64_t part_rows(int64_t rows, int64_t ctas_per_part) {
-  const int64_t want = 4 * static_cast<int64_t>(device_sms());
+  const int64_t want = 8 * static_cast<int64_t>(device_sms());
   const int64_t parts = std::max<int64_t>(1, want / std::max<int64_t>(1, ctas_per_part));
   const int64_t part = (rows + parts - 1) / parts;
   return std::max<int64_t>(kMinPart, (part + kBlock - 1) / kBlock * kBlock);
