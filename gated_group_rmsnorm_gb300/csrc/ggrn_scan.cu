@@ -622,11 +622,11 @@ int copy_bytes(std::initializer_list<int64_t> at) {
 }
 
 // Rows of a part of k_scan: long sequences are cut until the launch holds
-// about eight CTAs for each SM.  4096 tokens of 96 heads of 80 x 128 in f16:
-// 2237 us with two, 1676 with three, 1496 with four, 1399 with eight; more
-// parts cost more states to join.
+// about six CTAs for each SM.  4096 tokens of 96 heads of 80 x 128 in f16:
+// 1365 us with four, 1283 with six, 1254 with eight, whose states take a third
+// more workspace; 1025 of 48 heads of 100 x 64 in f32: 132.5, 131.5, 132.
 int64_t part_rows(int64_t rows, int64_t ctas_per_part) {
-  const int64_t want = 8 * static_cast<int64_t>(device_sms());
+  const int64_t want = 6 * static_cast<int64_t>(device_sms());
   const int64_t parts = std::max<int64_t>(1, want / std::max<int64_t>(1, ctas_per_part));
   const int64_t part = (rows + parts - 1) / parts;
   return std::max<int64_t>(kMinPart, (part + kBlock - 1) / kBlock * kBlock);
