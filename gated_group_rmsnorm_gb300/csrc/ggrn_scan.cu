@@ -653,7 +653,8 @@ Layout layout_of(const ggrn_scan_call& c) {
   if (longest(c) > INT32_MAX) l.part = longest(c);  // (the kernels count parts in 32 bits)
   l.cut = longest(c) > l.part;
   if (!l.cut) l.part = std::max<int64_t>(1, longest(c));
-  l.parts = c.rows / l.part + c.seqs;
+  // (a sequence of n > 0 rows has (n - 1) / part + 1, an empty one has one)
+  l.parts = (c.rows > 0 ? (c.rows - 1) / l.part : 0) + c.seqs;
   if (!c.cu_seqlens && c.seqs > 0)
     l.parts = c.seqs * std::max<int64_t>(1, (c.rows / c.seqs + l.part - 1) / l.part);
   l.places = l.state_bytes = l.bytes = 0;
