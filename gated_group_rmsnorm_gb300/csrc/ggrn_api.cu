@@ -1112,7 +1112,7 @@ extern "C" const char* ggrn_status_string(int status) {
                                 "multiple of group_size, row stride < width, or size overflow";
     case GGRN_ERR_ALIGN: return "pointers or row strides not aligned for the requested path";
     case GGRN_ERR_DTYPE: return "unsupported dtype/mode (ONNX semantics admit float32 and float16)";
-    case GGRN_ERR_OVERLAP: return "out overlaps y, gate or w";
+    case GGRN_ERR_OVERLAP: return "an output overlaps another buffer of the call";
     case GGRN_ERR_CUDA: return "CUDA runtime error";
     case GGRN_ERR_UNSUPPORTED: return "the requested path does not cover this shape";
     case GGRN_ERR_ARG: return "invalid argument (path id, NULL out-parameter or call list)";

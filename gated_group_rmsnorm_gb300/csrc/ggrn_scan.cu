@@ -405,8 +405,9 @@ __global__ void __launch_bounds__(kMaxThreads, 2) k_scan(const Params p, const S
 // k_scan_join: the states at the starts of a cut sequence's parts.  The place
 // of part i > 0 holds what part i - 1 adds to the state from a zero start; a
 // thread takes four entries of a state (V = 4: 16 bytes) or one through the
-// parts of its sequence.  grid: (blocks of entries, heads, cut sequences: there
-// are at most rows / part).
+// parts of its sequence (1025 rows in parts of 64, 48 heads of 100 x 64: 10 us,
+// the latency of its loads).  grid: (blocks of entries, heads, cut sequences:
+// there are at most rows / part).
 // ---------------------------------------------------------------------------
 // Parts whose entries are in flight (eight cost registers, and with them warps:
 // 5 % of a ragged scan's time).
@@ -496,7 +497,8 @@ __global__ void __launch_bounds__(256) k_scan_join(const Params p) {
 // k_scan_step: one token.  Bound by the state's bytes (8 per entry, read and
 // written once).  A warp takes kStepRows rows of one head's S at a time, all
 // their loads in flight before the first is used; the lanes hold B and C of
-// their columns.  VEC: lanes take 4 columns (16 bytes), state_size a multiple
+// their columns.  128 sequences of 96 heads of 80 x 128: 152 us, 98 % of the
+// rate of a plain copy; one sequence: 3.2 us, of which 1.2 are its bytes.  VEC: lanes take 4 columns (16 bytes), state_size a multiple
 // of 4 and the pool 16-byte aligned; else one column each.
 // ---------------------------------------------------------------------------
 constexpr int kStepRows = 4;

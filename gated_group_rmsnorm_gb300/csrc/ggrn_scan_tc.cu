@@ -22,19 +22,36 @@
 // smaller one underflows in any case, and the prefix sums stay exact enough
 // beside it.
 //
-// One CTA per part of a sequence and head (or tile of a head's columns), its
+// One CTA per part of a sequence and tile of a head's columns (80 at most), its
 // warps specialised so that all stages of neighbouring chunks overlap:
-//   X    4 warps   the pieces of w X
-//   M    8 warps   G out of tensor memory, decays applied, M back into it
-//   SY   16 warps  S in registers (dS out of tensor memory, S into shared
-//                  memory as the next chunk's operand), Y out of tensor memory
-// and one warp each that issues the products, copies (B, C, X in and Y out by
-// tensor-map copies) and makes the decays.  B and C lie in the 128-byte
-// swizzled layout, which serves B as rows of state columns in G and as its
-// transpose in dS; X, its pieces, S and Y in the 32-byte swizzled one, whose
-// 16-column atoms fit any head size (the layout of an operand does not change a
-// product's time).  Products are issued in the order C S, dS, M X, G of the
-// next chunk, which leaves every other stage the time of two products.  The
+//   M    4 warps   G out of tensor memory, decays applied, M back into it as
+//                  the operand of M X
+//   S    8 warps   S in registers; dS out of tensor memory, S into shared
+//                  memory as the next chunk's operand
+//   Y    4 warps   Y out of tensor memory, into X's place
+//   1 warp         issues the products
+//   1 warp         B and C (tensor-map copies, as soon as what read the ones
+//                  before is done) and the decays
+//   X    10 warps  (two for each 16 columns) X by asynchronous copies a chunk
+//                  ahead, the pieces of w X, and Y from X's place to memory
+// B and C lie in the 128-byte swizzled layout, which serves B as rows of state
+// columns in G and as its transpose in dS; X, its pieces, S and Y in the
+// 32-byte swizzled one, whose 16-column atoms fit any head size (the layout of
+// an operand does not change a product's time).  Products are issued in the
+// order C S, dS, M X, G of the next chunk, which leaves every other stage the
+// time of two products.  A product of M = 128, K = 16 takes 44 + N/2 clocks
+// with A in shared memory and 11 + N/2 with A in tensor memory or kept from the
+// product before: hence M in tensor memory and each step of B^T kept for its
+// three pieces.
+//
+// What bounds it: the chain of a chunk's stages, 2.6 us a chunk (64 columns
+// 2.5, 80 columns 2.7; the products alone take 1.7), and about 10 us to start
+// and end a launch.  4096 tokens of 96 heads of 80 x 128: 98 us, where the bytes
+// take 22 and the products, at the rate of a large matrix product, 11; eight
+// sequences of 2048 tokens, 80 heads of 64: 259 us.  One CTA per SM for all its
+// parts, with no stop between them, starts faster (11 us against 16 for a chunk
+// of 152 heads) but was slower by a fifth a chunk, since the roles then have to
+// keep more than their registers hold: 291 us for the eight sequences.  The
 // stages' loops are kept small: unrolled, the eight of them ran out of the
 // instruction cache (10 of 24 stall cycles an instruction) at a quarter of the
 // speed.
@@ -65,7 +82,7 @@ constexpr uint32_t kRowsBytes = kQ * 128 * 2;      // B or C: 32 KB
 constexpr uint32_t kAtomBytes = kQ * 16 * 2;       // one 16-column atom of X: 4 KB
 constexpr uint32_t kDecayFloats = 5 * kQ + 8;      // pre, col, dt, w, row + block sums, decay
 constexpr int kDecays = 3;                         // chunks of decays kept
-// tensor memory columns (k_scan_tc; k_scan_tc_state has dS at 0)
+// tensor memory columns
 constexpr uint32_t kColG = 0, kColM = 128, kColDs = 192;
 
 struct TcParams {
@@ -1097,8 +1114,8 @@ int tc_run(const ggrn_scan_call& c, const Params& p, bool cut, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>(p.parts), static_cast<unsigned>(p.H),
                   static_cast<unsigned>((p.P + tp.tile - 1) / tp.tile));
   if (cut) {
-    int st = mixer::launch(k_scan_tc<true>, dim3(inner_parts(p), grid.y, grid.z), kMainThreads, main_smem(tp.tile), s, tm_b, tm_c,
-                           tp);
+    int st = mixer::launch(k_scan_tc<true>, dim3(inner_parts(p), grid.y, grid.z), kMainThreads,
+                           main_smem(tp.tile), s, tm_b, tm_c, tp);
     if (st != GGRN_OK) return st;
     st = launch_join(p, s);
     if (st != GGRN_OK) return st;

@@ -336,7 +336,8 @@ int ggrn_version(void);
  * data, 2 = the producer waited for a free stage, 4 = the producer waited for
  * its copies to land, 8 = a unit claim of the dynamic schedule gave up;
  * 32 = a WIDE_CLUSTER CTA waited for its cluster's partial sums (16: see
- * ggrn_norm_outproj).
+ * ggrn_norm_outproj); 64 = a stage of the scan's tensor-core kernel waited for
+ * another one (ggrn_scan).
  * Nonzero means the outputs of some call are incomplete.  Synchronises the device, writes the word to *flags and, when
  * `clear` is nonzero, resets it.  Returns GGRN_OK, GGRN_ERR_ARG (flags NULL)
  * or GGRN_ERR_CUDA.
