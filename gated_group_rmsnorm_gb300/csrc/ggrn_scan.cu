@@ -662,7 +662,12 @@ Layout layout_of(const ggrn_scan_call& c) {
   l.places = l.state_bytes = l.bytes = 0;
   if (l.cut) {
     l.places = c.cu_seqlens ? std::min(l.parts, 2 * (c.rows / l.part)) : l.parts;
-    l.state_bytes = (l.places * c.heads * c.head_dim * c.state_size * 4 + 15) / 16 * 16;
+    const __int128 bytes = static_cast<__int128>(l.places) * c.heads * c.head_dim * c.state_size * 4;
+    if (bytes > INT64_MAX / 2) {  // (more than there can be)
+      l.bytes = INT64_MAX;
+      return l;
+    }
+    l.state_bytes = (static_cast<int64_t>(bytes) + 15) / 16 * 16;
     l.bytes = l.state_bytes + (l.places * c.heads * 4 + 15) / 16 * 16;
   }
   return l;

@@ -509,7 +509,8 @@ int ggrn_conv_step(const ggrn_conv_call* call, void* cuda_stream);
  * positive number.  Statuses as above; GGRN_ERR_SHAPE also when heads is not
  * a multiple of groups, GGRN_ERR_UNSUPPORTED for state_size > 256,
  * GGRN_ERR_ARG for limits out of order or not numbers and for a workspace
- * too small.
+ * too small.  Calls that may run at the same time need workspaces of their
+ * own, those of captured graphs included.
  */
 int ggrn_scan(const ggrn_scan_call* call, void* cuda_stream);
 int ggrn_scan_step(const ggrn_scan_call* call, void* cuda_stream);
