@@ -34,7 +34,7 @@ constexpr int kResident = 10;
 // Rows a thread slides its window over: the multiple of kAhead up to
 // kMaxTileRows whose waves cost least, a tile costing its rows and
 // kTileCost more (loads of the taps and the rows before the tile).  One wave
-// of 48 rows against two of 24: 29.8 and 33 us in the case above.
+// of 52 rows against two of 24: 29.8 and 33 us in the case above.
 constexpr int kMaxTileRows = 64;
 constexpr int kTileCost = 6;
 static_assert(kMaxTileRows <= kThreads, "a thread places one row of the tile");
