@@ -39,16 +39,17 @@
 // 32-byte swizzled one, whose 16-column atoms fit any head size (the layout of
 // an operand does not change a product's time).  Products are issued in the
 // order C S, dS, M X, G of the next chunk, which leaves every other stage the
-// time of two products.  A product of M = 128, K = 16 takes 44 + N/2 clocks
+// time of two products; C S has two places, so that it does not wait for the Y
+// before (95.3 us against 97.6 in the first case below).  A product of M = 128, K = 16 takes 44 + N/2 clocks
 // with A in shared memory and 11 + N/2 with A in tensor memory or kept from the
 // product before: hence M in tensor memory and each step of B^T kept for its
 // three pieces.
 //
 // What bounds it: the chain of a chunk's stages, 2.6 us a chunk (64 columns
 // 2.5, 80 columns 2.7; the products alone take 1.7), and about 10 us to start
-// and end a launch.  4096 tokens of 96 heads of 80 x 128: 98 us, where the bytes
+// and end a launch.  4096 tokens of 96 heads of 80 x 128: 95 us, where the bytes
 // take 22 and the products, at the rate of a large matrix product, 11; eight
-// sequences of 2048 tokens, 80 heads of 64: 259 us.  One CTA per SM for all its
+// sequences of 2048 tokens, 80 heads of 64: 258 us.  One CTA per SM for all its
 // parts, with no stop between them, starts faster (11 us against 16 for a chunk
 // of 152 heads) but was slower by a fifth a chunk, since the roles then have to
 // keep more than their registers hold: 291 us for the eight sequences.  The
@@ -152,8 +153,17 @@ __device__ __forceinline__ void tmem_ld16_nowait(uint32_t taddr, uint32_t (&r)[1
         "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_ld_wait() {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+// The wait for two such loads: their registers pass through it, so that nothing
+// that uses them can move before it.
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&a)[16], uint32_t (&b)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]),
+                 "+r"(a[7]), "+r"(a[8]), "+r"(a[9]), "+r"(a[10]), "+r"(a[11]), "+r"(a[12]),
+                 "+r"(a[13]), "+r"(a[14]), "+r"(a[15])::"memory");
+  asm volatile(""
+               : "+r"(b[0]), "+r"(b[1]), "+r"(b[2]), "+r"(b[3]), "+r"(b[4]), "+r"(b[5]), "+r"(b[6]),
+                 "+r"(b[7]), "+r"(b[8]), "+r"(b[9]), "+r"(b[10]), "+r"(b[11]), "+r"(b[12]),
+                 "+r"(b[13]), "+r"(b[14]), "+r"(b[15])::"memory");
 }
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile(
@@ -563,7 +573,7 @@ __global__ void __launch_bounds__(kMainThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_misc[0];
-  const uint32_t t_ds = tmem + kColDs, t_y1 = t_ds + tp.tile, t_y2 = t_y1 + tp.tile;
+  const uint32_t t_ds = tmem + kColDs, t_y2 = t_ds + tp.tile, t_y1 = t_y2 + tp.tile;  // y1: [2]
   const int P = p.P, N = p.N;
   const int h = blockIdx.y, g = h / p.hpg;
   const int col0 = blockIdx.z * tp.tile;         // first column of the head here
@@ -603,13 +613,12 @@ __global__ void __launch_bounds__(kMainThreads, 1)
     for (int c = STATE_ONLY ? 0 : -1; c < chunks; ++c) {
       const int n = c + 1, buf = n & 1;
       if (c >= 0) {
-        // C S (S of the chunk before, Y and dS read)
+        // C S (S of the chunk before; dS read)
         if (!(ok = wait.warp(bar(kSFull), c))) break;
         if (!STATE_ONLY) {
-          if (c > 0 && !(ok = wait.warp(bar(kYRead), c - 1))) break;
           tc_fence_after();
           if (elect_one()) {
-            issue_rows<kTransB>(t_y1, d_c, d_s, ksteps, id_y);
+            issue_rows<kTransB>(t_y1 + (c & 1) * tp.tile, d_c, d_s, ksteps, id_y);
             mma_commit(bar(kCFree));
           }
           __syncwarp();
@@ -626,7 +635,8 @@ __global__ void __launch_bounds__(kMainThreads, 1)
         }
         __syncwarp();
         if (STATE_ONLY) continue;
-        // M X
+        // M X (Y of the chunk before read: C S has two places)
+        if (c > 0 && !(ok = wait.warp(bar(kYRead), c - 1))) break;
         if (!(ok = wait.warp(bar(kMFull), c))) break;
         tc_fence_after();
         if (elect_one()) {
@@ -849,13 +859,13 @@ __global__ void __launch_bounds__(kMainThreads, 1)
         if (blk < q) {
           const float f = ex2_approx(between);
           between += sj[5 * kQ - 31 * blk];  // the sum over this block
-          tmem_ld_wait();
+          tmem_ld_wait(ga, gb);
           decayed(ga, sj + kQ, f, m);
           tmem_st8(t_m, m);
           decayed(gb, sj + kQ + 16, f, m);
           tmem_st8(t_m + 8, m);
         } else if (blk == q) {
-          tmem_ld_wait();
+          tmem_ld_wait(ga, gb);
           decayed_diagonal(ga, sj, pre, lane, m);
           tmem_st8(t_m, m);
           decayed_diagonal(gb, sj + 16, pre, lane - 16, m);
@@ -963,10 +973,10 @@ __global__ void __launch_bounds__(kMainThreads, 1)
 #pragma unroll 1
       for (int a = 0; a < atoms; ++a, at += kAtomBytes) {
         uint32_t y1[16], y2[16];
-        tmem_ld16_nowait(t_y1 + lanes + a * 16, y1);
+        tmem_ld16_nowait(t_y1 + (c & 1) * tp.tile + lanes + a * 16, y1);
         tmem_ld16_nowait(t_y2 + lanes + a * 16, y2);
         uint4 xa = lds16(at), xb = lds16(at ^ 16);
-        tmem_ld_wait();
+        tmem_ld_wait(y1, y2);
 #pragma unroll
         for (int j = 0; j < 16; j += 2) {
           uint32_t& xw = j < 8 ? (&xa.x)[j / 2] : (&xb.x)[j / 2 - 4];
