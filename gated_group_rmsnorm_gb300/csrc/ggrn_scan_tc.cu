@@ -38,21 +38,21 @@
 // columns in G and as its transpose in dS; X, its pieces, S and Y in the
 // 32-byte swizzled one, whose 16-column atoms fit any head size (the layout of
 // an operand does not change a product's time).  Products are issued in the
-// order C S, dS, M X, G of the next chunk, which leaves every other stage the
-// time of two products; C S has two places, so that it does not wait for the Y
-// before (95.3 us against 97.6 in the first case below).  A product of M = 128, K = 16 takes 44 + N/2 clocks
-// with A in shared memory and 11 + N/2 with A in tensor memory or kept from the
-// product before: hence M in tensor memory and each step of B^T kept for its
-// three pieces.
+// order C S, dS, M X, G of the next chunk (TWO_M: G before M X), which leaves
+// every other stage the time of two products; C S has two places, so that it
+// does not wait for the Y before (2 % in the first case below).  A product of
+// M = 128, K = 16 takes 44 + N/2 clocks with A in shared memory and 11 + N/2
+// with A in tensor memory or kept from the product before: hence M in tensor
+// memory and each step of B^T kept for its three pieces.
 //
-// What bounds it: the chain of a chunk's stages, 2.6 us a chunk (64 columns
-// 2.5, 80 columns 2.7; the products alone take 1.7), and about 10 us to start
-// and end a launch.  4096 tokens of 96 heads of 80 x 128: 95 us, where the bytes
+// What bounds it: the chain of a chunk's stages, 2.5 us a chunk (64 columns
+// 2.4, 80 columns 2.6; the products alone take 1.7), and about 10 us to start
+// and end a launch.  4096 tokens of 96 heads of 80 x 128: 96 us, where the bytes
 // take 22 and the products, at the rate of a large matrix product, 11; eight
-// sequences of 2048 tokens, 80 heads of 64: 258 us.  One CTA per SM for all its
-// parts, with no stop between them, starts faster (11 us against 16 for a chunk
-// of 152 heads) but was slower by a fifth a chunk, since the roles then have to
-// keep more than their registers hold: 291 us for the eight sequences.  The
+// sequences of 2048 tokens, 80 heads of 64: 248 us.  One CTA per SM for all its
+// parts, with no stop between them, was slower by a fifth a chunk, since the
+// roles then have to keep more than their registers hold: 291 us for the eight
+// sequences.  The
 // stages' loops are kept small: unrolled, the eight of them ran out of the
 // instruction cache (10 of 24 stall cycles an instruction) at a quarter of the
 // speed.
@@ -528,7 +528,11 @@ enum Bar {
 // STATE_ONLY: the state a part adds from a zero start, and its decay (a cut
 // sequence's parts but the last): dS and S alone; the warps of M and Y but the
 // copying one have nothing to do.
-template <bool STATE_ONLY>
+// TWO_M: M has two places in tensor memory, and G of the next chunk goes before
+// M X, so that M's warps need not wait for M X; there is room for that with
+// tiles up to 64 columns (4096 tokens of 152 heads of 64: 89 us against 94; 80
+// columns with it and one place for C S: 105 us against 95 in the case above).
+template <bool STATE_ONLY, bool TWO_M>
 __global__ void __launch_bounds__(kMainThreads, 1)
     k_scan_tc(const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ CUtensorMap tm_c,
               const TcParams tp) {
@@ -574,6 +578,7 @@ __global__ void __launch_bounds__(kMainThreads, 1)
   tc_fence_after();
   const uint32_t tmem = s_misc[0];
   const uint32_t t_ds = tmem + kColDs, t_y2 = t_ds + tp.tile, t_y1 = t_y2 + tp.tile;  // y1: [2]
+  const uint32_t t_m1 = tmem + (TWO_M ? kColDs + 4 * tp.tile : kColM);
   const int P = p.P, N = p.N;
   const int h = blockIdx.y, g = h / p.hpg;
   const int col0 = blockIdx.z * tp.tile;         // first column of the head here
@@ -635,28 +640,36 @@ __global__ void __launch_bounds__(kMainThreads, 1)
         }
         __syncwarp();
         if (STATE_ONLY) continue;
-        // M X (Y of the chunk before read: C S has two places)
-        if (c > 0 && !(ok = wait.warp(bar(kYRead), c - 1))) break;
         if (!(ok = wait.warp(bar(kMFull), c))) break;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t d_x = desc_t32(sX + (c & 1) * x_bytes);
+      }
+      // M X, and G of the next chunk: first where M has two places
+#pragma unroll
+      for (int step = 0; step < 2; ++step) {
+        if ((step == 0) == TWO_M) {
+          if (n >= chunks) continue;
+          if (!(ok = wait.warp(bar(kBFull + buf), n >> 1) && wait.warp(bar(kCFull), n))) break;
+          tc_fence_after();
+          if (elect_one()) {
+            issue_rows<0>(tmem + kColG, d_c, desc_sw128(sB + buf * kRowsBytes), ksteps, id_g);
+            mma_commit(bar(kGDone));
+          }
+          __syncwarp();
+        } else if (c >= 0) {
+          // (Y of the chunk before read: C S has two places)
+          if (c > 0 && !(ok = wait.warp(bar(kYRead), c - 1))) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t d_x = desc_t32(sX + (c & 1) * x_bytes);
+            const uint32_t t_m = TWO_M && (c & 1) ? t_m1 : tmem + kColM;
 #pragma unroll 2
-          for (int k = 0; k < kQ / 16; ++k)
-            mma_bf16_ts(t_y2, tmem + kColM + 8 * k, d_x + k * (512 >> 4), id_y, k > 0);
-          mma_commit(bar(kYDone));
+            for (int k = 0; k < kQ / 16; ++k)
+              mma_bf16_ts(t_y2, t_m + 8 * k, d_x + k * (512 >> 4), id_y, k > 0);
+            mma_commit(bar(kYDone));
+          }
+          __syncwarp();
         }
-        __syncwarp();
       }
-      if (n < chunks) {
-        if (!(ok = wait.warp(bar(kBFull + buf), n >> 1) && wait.warp(bar(kCFull), n))) break;
-        tc_fence_after();
-        if (elect_one()) {
-          issue_rows<0>(tmem + kColG, d_c, desc_sw128(sB + buf * kRowsBytes), ksteps, id_g);
-          mma_commit(bar(kGDone));
-        }
-        __syncwarp();
-      }
+      if (!ok) break;
     }
     // the last products are done before the tensor memory is freed
     if (STATE_ONLY && ok) ok = wait.warp(bar(kDsDone), chunks - 1);
@@ -850,7 +863,8 @@ __global__ void __launch_bounds__(kMainThreads, 1)
 #pragma unroll 1
       for (int blk = 3; blk >= 0; --blk) {
         const float* sj = sd + 32 * blk;
-        const uint32_t t_g = tmem + lanes + kColG + 32 * blk, t_m = tmem + lanes + kColM + 16 * blk;
+        const uint32_t t_g = tmem + lanes + kColG + 32 * blk;
+        const uint32_t t_m = (TWO_M && (c & 1) ? t_m1 : tmem + kColM) + lanes + 16 * blk;
         uint32_t ga[16], gb[16], m[8];
         if (blk <= q) {
           tmem_ld16_nowait(t_g, ga);
@@ -1027,9 +1041,9 @@ cudaError_t allow_smem() {
   static cudaError_t err = cudaSuccess;
   std::call_once(once, [] {
     const int bytes = static_cast<int>(main_smem(16 * kMaxAtoms));
-    err = cudaFuncSetAttribute(k_scan_tc<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (err == cudaSuccess)
-      err = cudaFuncSetAttribute(k_scan_tc<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    for (auto kernel : {k_scan_tc<false, false>, k_scan_tc<false, true>, k_scan_tc<true, false>})
+      if (err == cudaSuccess)
+        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   });
   return err;
 }
@@ -1124,13 +1138,16 @@ int tc_run(const ggrn_scan_call& c, const Params& p, bool cut, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>(p.parts), static_cast<unsigned>(p.H),
                   static_cast<unsigned>((p.P + tp.tile - 1) / tp.tile));
   if (cut) {
-    int st = mixer::launch(k_scan_tc<true>, dim3(inner_parts(p), grid.y, grid.z), kMainThreads,
+    int st = mixer::launch(k_scan_tc<true, false>, dim3(inner_parts(p), grid.y, grid.z), kMainThreads,
                            main_smem(tp.tile), s, tm_b, tm_c, tp);
     if (st != GGRN_OK) return st;
     st = launch_join(p, s);
     if (st != GGRN_OK) return st;
   }
-  return mixer::launch(k_scan_tc<false>, grid, kMainThreads, main_smem(tp.tile), s, tm_b, tm_c, tp);
+  // (M's second place is behind the two of C S)
+  const bool two_m = kColDs + 4 * tp.tile + 64 <= 512;
+  return mixer::launch(two_m ? k_scan_tc<false, true> : k_scan_tc<false, false>, grid, kMainThreads,
+                       main_smem(tp.tile), s, tm_b, tm_c, tp);
 }
 
 }  // namespace scan
