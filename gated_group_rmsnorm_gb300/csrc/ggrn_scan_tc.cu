@@ -49,7 +49,7 @@
 // 2.4, 80 columns 2.6; the products alone take 1.7), and about 10 us to start
 // and end a launch.  4096 tokens of 96 heads of 80 x 128: 96 us, where the bytes
 // take 22 and the products, at the rate of a large matrix product, 11; eight
-// sequences of 2048 tokens, 80 heads of 64: 248 us.  One CTA per SM for all its
+// sequences of 2048 tokens, 80 heads of 64: 245 us.  One CTA per SM for all its
 // parts, with no stop between them, was slower by a fifth a chunk, since the
 // roles then have to keep more than their registers hold: 291 us for the eight
 // sequences.  The
@@ -1089,8 +1089,11 @@ bool tc_covers(const ggrn_scan_call& c) {
 // as long as a part's chunks and about four more to start and end; a cut costs
 // the state-only launch over the same chunks (a bit over half of a chunk's
 // time) and the join.  The lengths behind cu_seqlens are not known here:
-// sequences are taken for equally long, and where those stay whole a part is
-// twice their length, so that only longer ones are cut.
+// sequences are taken for equally long, and where those stay whole a part is as
+// long as the launch for them takes (and no less than twice their length): one
+// sequence of that length beside the others costs nothing.  3777 rows in 11
+// sequences of 0 to 918, 96 heads of 80 x 128: with parts of twice the mean, 50
+// of 190 us went into cutting two of them.
 int64_t tc_part_rows(const ggrn_scan_call& c, int64_t longest) {
   const int64_t tiles = (c.head_dim + tile_of(c.head_dim) - 1) / tile_of(c.head_dim);
   const int64_t heads = c.heads * tiles, sms = device_sms();
@@ -1113,7 +1116,9 @@ int64_t tc_part_rows(const ggrn_scan_call& c, int64_t longest) {
       best_cost = cost;
     }
   }
-  return (best == all ? std::min(most, 2 * all) : best) * kQ;
+  if (best < all) return best * kQ;
+  const int64_t hidden = static_cast<int64_t>(best_cost - kStartChunks);
+  return std::min(most, std::max(2 * all, hidden)) * kQ;
 }
 
 int tc_run(const ggrn_scan_call& c, const Params& p, bool cut, cudaStream_t s) {
