@@ -63,6 +63,13 @@ __device__ __forceinline__ Quad lds4(const T* p) {
   return {pk2(a, b), pk2(c, d)};
 }
 
+// The first n of a pair, zeros behind them.
+__device__ __forceinline__ F2 first_of(F2 v, int n) {
+  float a, b;
+  upk2(v, a, b);
+  return pk2(n > 0 ? a : 0.0f, n > 1 ? b : 0.0f);
+}
+
 __device__ __forceinline__ float ld_smem(const float* p) { return *p; }
 template <typename T>
 __device__ __forceinline__ float ld_smem(const T* p) {
@@ -128,8 +135,10 @@ __device__ __forceinline__ void team_sums(float (&v)[4], int l) {
   }
 }
 
-// `STATE_ONLY`: the first launch of a cut scan.
-template <typename T, int TL, bool STATE_ONLY>
+// STATE_ONLY: the first launch of a cut scan.  PADS: a team's columns go on
+// behind N (a form of its own: in one form for both, 1025 tokens of 48 heads of
+// 100 x 64 in f32 took 134 us against 131).
+template <typename T, int TL, bool STATE_ONLY, bool PADS>
 __global__ void __launch_bounds__(kMaxThreads, 2) k_scan(const Params p, const Shape sh) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   pdl_wait();
@@ -233,11 +242,14 @@ __global__ void __launch_bounds__(kMaxThreads, 2) k_scan(const Params p, const S
   }
   float log_decay = 0.0f;  // STATE_ONLY, threads of the first block of tokens
 
-  // K tokens from token t of the block on
+  // K tokens from token t of the block on.  HOLD keeps the columns behind N
+  // zeros where 0 times a value that is not finite would leave a NaN, which
+  // their zeros in C would carry into y.
   using Staged = typename std::conditional<kWiden, float, T>::type;
-  auto tokens = [&](auto k_tokens, int t, const Staged* bt, const Staged* ct,
+  auto tokens = [&](auto k_tokens, auto hold, int t, const Staged* bt, const Staged* ct,
                     const float* dts) __attribute__((always_inline)) {
     constexpr int K = decltype(k_tokens)::value;
+    constexpr bool HOLD = decltype(hold)::value;
     bt += t * sh.np + l * 4;
     ct += t * sh.np + l * 4;
     float* xt = sXX + (t * prows + r0) * 2;
@@ -259,6 +271,11 @@ __global__ void __launch_bounds__(kMaxThreads, 2) k_scan(const Params p, const S
         for (int r = 0; r < kRows; ++r) {
           s[r][2 * j] = fma2(s[r][2 * j], ee[k], mul2(bv.lo, xx[k][r]));
           s[r][2 * j + 1] = fma2(s[r][2 * j + 1], ee[k], mul2(bv.hi, xx[k][r]));
+          if constexpr (HOLD) {
+            const int left = N - (j * TL + l) * 4;
+            s[r][2 * j] = first_of(s[r][2 * j], left);
+            s[r][2 * j + 1] = first_of(s[r][2 * j + 1], left - 2);
+          }
           if (!STATE_ONLY) {
             yy[k][r] = j == 0 ? mul2(s[r][0], cv.lo) : fma2(s[r][2 * j], cv.lo, yy[k][r]);
             yy[k][r] = fma2(s[r][2 * j + 1], cv.hi, yy[k][r]);
@@ -300,8 +317,10 @@ __global__ void __launch_bounds__(kMaxThreads, 2) k_scan(const Params p, const S
   for (int64_t t0 = part.begin; t0 < part.end; t0 += kBlock, buf ^= 1) {
     const int nt = static_cast<int>(min(static_cast<int64_t>(kBlock), part.end - t0));
     float* dts = sDt + buf * 3 * kBlock;  // dt; decays, twice each
+    F2 odd = 0;  // NaN where a decay or a dt x of the block is not finite
     if (tid < nt) {
       const float dt = dt_of(raw, dbias, p), e = expf(dt * a);
+      if constexpr (PADS) odd = pk2(e * 0.0f, 0.0f);
       dts[tid] = dt;
       *reinterpret_cast<float2*>(dts + kBlock + 2 * tid) = make_float2(e, e);
       if (STATE_ONLY) log_decay = fmaf(dt, a, log_decay);
@@ -322,9 +341,11 @@ __global__ void __launch_bounds__(kMaxThreads, 2) k_scan(const Params p, const S
 #pragma unroll 1
       for (int i = lane * 4; i < prows; i += 128) {
         const Quad q = lds4(xb + t * prows + i);
+        const F2 lo = mul2(q.lo, dd), hi = mul2(q.hi, dd);
+        if constexpr (PADS) odd = fma2(lo, 0, fma2(hi, 0, odd));
         float v[4];
-        upk2(mul2(q.lo, dd), v[0], v[1]);
-        upk2(mul2(q.hi, dd), v[2], v[3]);
+        upk2(lo, v[0], v[1]);
+        upk2(hi, v[2], v[3]);
         float4* to = reinterpret_cast<float4*>(sXX + (t * prows + i) * 2);
         to[0] = make_float4(v[0], v[0], v[1], v[1]);
         to[1] = make_float4(v[2], v[2], v[3], v[3]);
@@ -342,7 +363,14 @@ __global__ void __launch_bounds__(kMaxThreads, 2) k_scan(const Params p, const S
         }
       }
     }
-    __syncthreads();
+    bool hold = false;
+    if constexpr (PADS) {
+      float odd0, odd1;
+      upk2(odd, odd0, odd1);
+      hold = __syncthreads_or(odd0 != odd0 || odd1 != odd1) != 0;
+    } else {
+      __syncthreads();
+    }
     // tokens by pairs, for more instructions that do not wait for one another
     const Staged* bt;
     const Staged* ct;
@@ -351,10 +379,16 @@ __global__ void __launch_bounds__(kMaxThreads, 2) k_scan(const Params p, const S
     } else {
       bt = bb, ct = cb;
     }
+    using One = std::integral_constant<int, 1>;
+    using Two = std::integral_constant<int, 2>;
     int t = 0;
+    if constexpr (PADS)
+      if (hold)
 #pragma unroll 1
-    for (; t + 2 <= nt; t += 2) tokens(std::integral_constant<int, 2>(), t, bt, ct, dts);
-    if (t < nt) tokens(std::integral_constant<int, 1>(), t, bt, ct, dts);
+        for (; t < nt; ++t) tokens(One(), std::true_type(), t, bt, ct, dts);
+#pragma unroll 1
+    for (; t + 2 <= nt; t += 2) tokens(Two(), std::false_type(), t, bt, ct, dts);
+    if (t < nt) tokens(One(), std::false_type(), t, bt, ct, dts);
     __syncthreads();
     if (!STATE_ONLY) {
       T* ot = out + (t0 + warp) * p.os;
@@ -572,7 +606,8 @@ __global__ void __launch_bounds__(kStepThreads) k_scan_step(const Params p, cons
       float y = 0.0f;
 #pragma unroll
       for (int k = 0; k < CH * E; ++k) {
-        s[r][k] = fmaf(s[r][k], e, xd * bv[k]);
+        // (columns behind N stay zeros whatever dt x and the decay are)
+        s[r][k] = (k / E * tl + l) * E < N ? fmaf(s[r][k], e, xd * bv[k]) : 0.0f;
         y = fmaf(s[r][k], cv[k], y);
       }
 #pragma unroll
@@ -749,11 +784,10 @@ int run_team(const Params& p, const Shape& sh, const Layout& l, cudaStream_t s) 
     static std::once_flag once;
     static cudaError_t err = cudaSuccess;
     std::call_once(once, [] {
-      err = cudaFuncSetAttribute(k_scan<T, TL, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kMaxSmem);
-      if (err == cudaSuccess)
-        err = cudaFuncSetAttribute(k_scan<T, TL, false>,
-                                   cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+      for (auto kernel : {k_scan<T, TL, true, false>, k_scan<T, TL, false, false>,
+                          k_scan<T, TL, false, true>})
+        if (err == cudaSuccess)
+          err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
     });
     if (err != cudaSuccess) {
       record_cuda_error(err);
@@ -761,13 +795,15 @@ int run_team(const Params& p, const Shape& sh, const Layout& l, cudaStream_t s) 
     }
   }
   if (l.cut) {
-    int st = mixer::launch(k_scan<T, TL, true>, dim3(inner_parts(p), grid.y, grid.z), sh.threads,
-                           sh.smem, s, p, sh);
+    int st = mixer::launch(k_scan<T, TL, true, false>, dim3(inner_parts(p), grid.y, grid.z),
+                           sh.threads, sh.smem, s, p, sh);
     if (st != GGRN_OK) return st;
     st = launch_join(p, s);
     if (st != GGRN_OK) return st;
   }
-  return mixer::launch(k_scan<T, TL, false>, grid, sh.threads, sh.smem, s, p, sh);
+  // (the states' columns behind N are not stored: the first launch needs no PADS)
+  return mixer::launch(p.N < sh.np ? k_scan<T, TL, false, true> : k_scan<T, TL, false, false>, grid,
+                       sh.threads, sh.smem, s, p, sh);
 }
 
 template <typename T>

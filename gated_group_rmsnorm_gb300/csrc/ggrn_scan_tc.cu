@@ -944,8 +944,11 @@ __global__ void __launch_bounds__(kMainThreads, 1)
         if (a < atoms) {
           uint32_t r[16];
           tmem_ld16(t_ds + lanes + a * 16, r);
+          if (n < N) {  // (rows behind N stay zeros: dS there is 0 times whatever w X is)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) s[k][j] = fma2(s[k][j], decay2, pair(r[2 * j], r[2 * j + 1]));
+            for (int j = 0; j < 8; ++j)
+              s[k][j] = fma2(s[k][j], decay2, pair(r[2 * j], r[2 * j + 1]));
+          }
           if (!STATE_ONLY) put(k);
         }
       }
