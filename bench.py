@@ -191,11 +191,12 @@ def kernel_source_hash() -> str:
     """Hash of the sources that define the norm kernels and how a call
     launches them (the host pipeline, ggrn_host.cu, only sequences copies
     around those launches, and the fused out_proj's and the mixer operators'
-    files hold kernels of their own: they are left out)."""
+    files hold kernels of their own or serve those: they are left out)."""
     h = hashlib.sha256()
     for fn in sorted(os.listdir(CSRC)):
         if fn.endswith((".cu", ".cuh", ".h")) and fn not in (
                 "ggrn_host.cu", "ggrn_outproj.cu", "ggrn_umma.cuh", "ggrn_mixer.cuh",
+                "ggrn_optin.h",
                 "ggrn_conv.cu", "ggrn_scan.cuh", "ggrn_scan.cu", "ggrn_scan_tc.cu"):
             with open(os.path.join(CSRC, fn), "rb") as fh:
                 h.update(fn.encode() + b"\0" + _without_timeline(fh.read()))

@@ -37,10 +37,10 @@
 
 #include <cstdint>
 #include <cstring>
-#include <mutex>
 
 #include "../../include/ggrn.h"
 #include "ggrn_internal.h"
+#include "ggrn_optin.h"
 #include "ggrn_stream.cuh"
 #include "ggrn_umma.cuh"
 
@@ -457,12 +457,7 @@ extern "C" int ggrn_norm_outproj(const void* y, const void* gate, const void* w,
   }
   // the GEMM
   {
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [] {
-      attr_err = cudaFuncSetAttribute(k_outproj, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      static_cast<int>(kSmemBytes));
-    });
+    const cudaError_t attr_err = allow_shared_memory<k_outproj>(static_cast<int>(kSmemBytes));
     if (attr_err != cudaSuccess) {
       record_cuda_error(attr_err);
       return GGRN_ERR_CUDA;

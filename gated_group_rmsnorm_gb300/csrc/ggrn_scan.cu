@@ -24,9 +24,9 @@
 #include <algorithm>
 #include <cmath>
 #include <initializer_list>
-#include <mutex>
 #include <type_traits>
 
+#include "ggrn_optin.h"
 #include "ggrn_scan.cuh"
 
 namespace ggrn {
@@ -781,16 +781,11 @@ int run_team(const Params& p, const Shape& sh, const Layout& l, cudaStream_t s) 
   const dim3 grid(static_cast<unsigned>(l.parts), static_cast<unsigned>(p.H),
                   static_cast<unsigned>(sh.ptiles));
   if (sh.smem > 48 * 1024) {  // wide states in f32: up to 84 KB
-    static std::once_flag once;
-    static cudaError_t err = cudaSuccess;
-    std::call_once(once, [] {
-      for (auto kernel : {k_scan<T, TL, true, false>, k_scan<T, TL, false, false>,
-                          k_scan<T, TL, false, true>})
-        if (err == cudaSuccess)
-          err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
-    });
-    if (err != cudaSuccess) {
-      record_cuda_error(err);
+    cudaError_t e = allow_shared_memory<k_scan<T, TL, true, false>>(kMaxSmem);
+    if (e == cudaSuccess) e = allow_shared_memory<k_scan<T, TL, false, false>>(kMaxSmem);
+    if (e == cudaSuccess) e = allow_shared_memory<k_scan<T, TL, false, true>>(kMaxSmem);
+    if (e != cudaSuccess) {
+      record_cuda_error(e);
       return GGRN_ERR_CUDA;
     }
   }

@@ -63,8 +63,8 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
-#include <mutex>
 
+#include "ggrn_optin.h"
 #include "ggrn_scan.cuh"
 #include "ggrn_umma.cuh"
 
@@ -1078,15 +1078,11 @@ int tile_of(int64_t P) {
 }
 
 cudaError_t allow_smem() {
-  static std::once_flag once;
-  static cudaError_t err = cudaSuccess;
-  std::call_once(once, [] {
-    const int bytes = static_cast<int>(main_smem(16 * kMaxAtoms));
-    for (auto kernel : {k_scan_tc<false, false>, k_scan_tc<false, true>, k_scan_tc<true, false>})
-      if (err == cudaSuccess)
-        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  });
-  return err;
+  const int bytes = static_cast<int>(main_smem(16 * kMaxAtoms));
+  cudaError_t e = allow_shared_memory<k_scan_tc<false, false>>(bytes);
+  if (e == cudaSuccess) e = allow_shared_memory<k_scan_tc<false, true>>(bytes);
+  if (e == cudaSuccess) e = allow_shared_memory<k_scan_tc<true, false>>(bytes);
+  return e;
 }
 
 // [rows][groups][N] in boxes of 128 rows and 64 columns: columns behind N and
