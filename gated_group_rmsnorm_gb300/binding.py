@@ -617,7 +617,8 @@ def ssm_scan(x: torch.Tensor, dt: torch.Tensor, a: torch.Tensor, b: torch.Tensor
     ``dt_softplus=False`` takes ``dt + dt_bias`` as it is.  ``state``: f32
     [slots, heads, head_dim, state_size]; ``cu_seqlens``, ``slots`` and
     ``resume`` as in ``causal_conv``.  ``workspace``: optional uint8 device
-    tensor of ``scan_workspace_bytes`` (allocated when omitted and needed).
+    tensor of ``scan_workspace_bytes`` of these tensors and ``out`` (allocated
+    when omitted and needed).
     """
     lo, hi = dt_limits
     return (_native or load_binding()).scan(x, dt, a, b, c, head_dim, state_size, d, dt_bias,
@@ -645,10 +646,13 @@ def ssm_scan_step(x: torch.Tensor, dt: torch.Tensor, a: torch.Tensor, b: torch.T
 
 
 def scan_workspace_bytes(x, dt, a, b, c, *, head_dim: int, state_size: int,
-                         cu_seqlens: torch.Tensor | None = None) -> int:
-    """Workspace bytes of ``ssm_scan`` on these tensors (0: none needed)."""
+                         cu_seqlens: torch.Tensor | None = None,
+                         out: torch.Tensor | None = None) -> int:
+    """Workspace bytes of ``ssm_scan`` on these tensors (0: none needed).  The
+    size depends on the alignment and row strides of all of them: pass the
+    ``out`` that the call will get (omitted: a new contiguous one)."""
     return load_binding().scan_workspace_bytes(x, dt, a, b, c, head_dim, state_size, None, None,
-                                               True, 0.0, 0.0, cu_seqlens, None, None, None, None,
+                                               True, 0.0, 0.0, cu_seqlens, None, None, None, out,
                                                False)
 
 

@@ -180,8 +180,11 @@ at::Tensor fill_conv(ggrn_conv_call* k, const at::Tensor*& x_out, PyObject* cons
 }
 
 // x, dt, a, b, c, head_dim, state_size, d, dt_bias, dt_softplus, dt_min, dt_max,
-// cu_seqlens, state, slots, resume, out, step
-at::Tensor fill_scan(ggrn_scan_call* k, const at::Tensor*& x_out, PyObject* const* a) {
+// cu_seqlens, state, slots, resume, out, step.  Without `make_out` an output that
+// is not given is not made either: its address stays NULL and its rows are taken
+// for contiguous ones, as those of a new tensor are.
+at::Tensor fill_scan(ggrn_scan_call* k, const at::Tensor*& x_out, PyObject* const* a,
+                     bool make_out = true) {
   const at::Tensor& x = needed(a[0], "x");
   x_out = &x;
   if (!x.is_cuda()) refuse("the scan runs on CUDA tensors only (no CPU path)");
@@ -230,9 +233,13 @@ at::Tensor fill_scan(ggrn_scan_call* k, const at::Tensor*& x_out, PyObject* cons
   k->dt_min = static_cast<float>(PyFloat_AsDouble(a[10]));
   k->dt_max = static_cast<float>(PyFloat_AsDouble(a[11]));
   if (PyErr_Occurred()) throw python_error();
-  at::Tensor out = output(a[16], x);
-  rows_of(out, width, "out", &rows, &k->out_row_stride);
-  k->out = out.data_ptr();
+  at::Tensor out;
+  k->out_row_stride = width;
+  if (make_out || a[16] != Py_None) {
+    out = output(a[16], x);
+    rows_of(out, width, "out", &rows, &k->out_row_stride);
+    k->out = out.data_ptr();
+  }
   const int64_t held[3] = {heads, head_dim, state_size};
   fill_seqs(k, x, a[12], a[13], a[14], a[15], held, at::kFloat, step);
   return out;
@@ -320,7 +327,7 @@ PyObject* py_scan_workspace(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     ggrn_scan_call k;
     const at::Tensor* x;
-    fill_scan(&k, x, a);
+    fill_scan(&k, x, a, /*make_out=*/false);
     c10::cuda::CUDAGuard guard(x->device());
     return PyLong_FromLongLong(ggrn_scan_workspace_bytes(&k));
   });

@@ -515,9 +515,10 @@ int ggrn_conv_step(const ggrn_conv_call* call, void* cuda_stream);
 int ggrn_scan(const ggrn_scan_call* call, void* cuda_stream);
 int ggrn_scan_step(const ggrn_scan_call* call, void* cuda_stream);
 
-/* Workspace bytes of ggrn_scan for this call (only its sizes and dtype, the
- * alignment of its pointers and whether cu_seqlens is NULL are looked at):
- * 0 where none is needed or the call is invalid. */
+/* Workspace bytes of ggrn_scan for this call (only its sizes, row strides and
+ * dtype, the alignment of x, b, c and out and whether cu_seqlens is NULL are
+ * looked at; calls that differ in these may need more): 0 where none is needed
+ * or the call is invalid. */
 int64_t ggrn_scan_workspace_bytes(const ggrn_scan_call* call);
 
 /* One call of a decode chain that is not only norms. */
