@@ -669,6 +669,10 @@ int64_t part_rows(int64_t rows, int64_t ctas_per_part) {
   return std::max<int64_t>(kMinPart, (part + kBlock - 1) / kBlock * kBlock);
 }
 
+// Sequences of more than one part that a call can have (a grid's third
+// dimension); parts of calls with more sequences are long enough for it.
+constexpr int64_t kMaxCut = 65535;
+
 // The most rows a sequence can have.
 int64_t longest(const ggrn_scan_call& c) {
   return c.cu_seqlens || c.seqs <= 0 ? c.rows : c.rows / c.seqs;
@@ -688,6 +692,11 @@ Layout layout_of(const ggrn_scan_call& c) {
   l.tc = tc_covers(c);
   l.part = l.tc ? tc_part_rows(c, longest(c)) : part_rows(c.rows, c.heads * s.ptiles);
   if (longest(c) > INT32_MAX) l.part = longest(c);  // (the kernels count parts in 32 bits)
+  // the join's grid holds kMaxCut sequences of more than one part
+  if (c.seqs > kMaxCut) {
+    if (!c.cu_seqlens) l.part = std::max(l.part, longest(c));
+    else if (c.rows / l.part > kMaxCut) l.part = (c.rows / kMaxCut / 128 + 1) * 128;
+  }
   l.cut = longest(c) > l.part;
   if (!l.cut) l.part = std::max<int64_t>(1, longest(c));
   // (a sequence of n > 0 rows has (n - 1) / part + 1, an empty one has one)
@@ -805,8 +814,7 @@ template <typename T>
 int run_typed(const Params& p, const Layout& l, cudaStream_t s) {
   constexpr int64_t es = sizeof(T);
   Shape sh = shape_of(p.P, p.N, es);
-  if (l.parts > INT32_MAX || sh.ptiles > 65535 || (l.cut && p.q.seqs > 65535))
-    return GGRN_ERR_UNSUPPORTED;
+  if (l.parts > INT32_MAX || sh.ptiles > 65535) return GGRN_ERR_UNSUPPORTED;
   auto at = [](const void* q) { return static_cast<int64_t>(reinterpret_cast<uintptr_t>(q)); };
   sh.bc_bytes = copy_bytes({at(p.b), at(p.c), p.bs * es, p.cs * es, p.N * es});
   // (a head's columns start at multiples of P, a tile's of prows)
@@ -866,7 +874,7 @@ int run(const ggrn_scan_call* call, bool step, void* stream) {
   p.parts = l.parts;
   p.places = l.places;
   if (l.tc) {
-    if (l.parts > INT32_MAX || (l.cut && p.q.seqs > 65535)) return GGRN_ERR_UNSUPPORTED;
+    if (l.parts > INT32_MAX) return GGRN_ERR_UNSUPPORTED;
     return tc_run(c, p, l.cut, s);
   }
   if (c.dtype == kF32) return run_typed<float>(p, l, s);

@@ -495,7 +495,8 @@ typedef struct {
  * one row of each sequence.  Return GGRN_ERR_SHAPE for negative or
  * inconsistent sizes (rows not a multiple of seqs without cu_seqlens, a
  * stride below its row's width, too few slots, overflow),
- * GGRN_ERR_UNSUPPORTED for taps outside 2..4, GGRN_ERR_DTYPE for an unknown
+ * GGRN_ERR_UNSUPPORTED for taps outside 2..4 and for more than 4194240 columns
+ * (or a grid of more than 2^31 - 1 blocks of rows), GGRN_ERR_DTYPE for an unknown
  * dtype, GGRN_ERR_ARG for an unknown activation, a NULL call, or slots or
  * resume without state, GGRN_ERR_NULL, GGRN_ERR_ALIGN (a pointer not aligned
  * to its element), GGRN_ERR_OVERLAP, GGRN_ERR_CUDA.
@@ -505,9 +506,10 @@ int ggrn_conv_step(const ggrn_conv_call* call, void* cuda_stream);
 
 /*
  * ggrn_scan / ggrn_scan_step -- the selective state space scan over prompts /
- * over one row of each sequence.  state_size is 1..256 and head_dim any
- * positive number.  Statuses as above; GGRN_ERR_SHAPE also when heads is not
- * a multiple of groups, GGRN_ERR_UNSUPPORTED for state_size > 256,
+ * over one row of each sequence.  state_size is 1..256, heads and head_dim
+ * 1..65535; the number of sequences has no limit of its own.  Statuses as
+ * above; GGRN_ERR_SHAPE also when heads is not a multiple of groups,
+ * GGRN_ERR_UNSUPPORTED for state_size, heads or head_dim above those,
  * GGRN_ERR_ARG for limits out of order or not numbers and for a workspace
  * too small.  Calls that may run at the same time need workspaces of their
  * own, those of captured graphs included.
