@@ -157,22 +157,24 @@ inline bool overlap(const Buffer& a, const Buffer& b) {
   return x < y + static_cast<uintptr_t>(b.bytes) && y < x + static_cast<uintptr_t>(a.bytes);
 }
 
+// Whether `rows` rows can be `seqs` sequences (of equal length without offsets).
+inline bool counts_ok(int64_t rows, int64_t seqs, bool offsets) {
+  if (rows < 0 || seqs < 0 || (seqs == 0 && rows > 0)) return false;
+  if (!offsets && seqs > 0 && rows % seqs != 0) return false;
+  return rows <= INT64_MAX / 2 && seqs <= INT32_MAX && !(offsets && rows > INT32_MAX);
+}
+
 // Checks of rows, sequences and the pool shared by every entry point.
 // `step`: one row a sequence, the state required.
 inline int check_seqs(int64_t rows, int64_t seqs, const int32_t* cu, const void* state,
                       const int32_t* slots, const uint8_t* resume, int64_t state_slots,
                       int64_t slot_width, int64_t slot_stride, bool step, Seqs* q) {
-  if (rows < 0 || (!step && seqs < 0)) return GGRN_ERR_SHAPE;
   if (step) {
     seqs = rows;
     cu = nullptr;
     resume = nullptr;
-  } else if (seqs == 0 && rows > 0) {
-    return GGRN_ERR_SHAPE;
-  } else if (!cu && seqs > 0 && rows % seqs != 0) {
-    return GGRN_ERR_SHAPE;
   }
-  if (rows > INT64_MAX / 2 || seqs > INT32_MAX || (cu && rows > INT32_MAX)) return GGRN_ERR_SHAPE;
+  if (!counts_ok(rows, seqs, cu != nullptr)) return GGRN_ERR_SHAPE;
   if (!aligned_to(cu, 4) || !aligned_to(slots, 4)) return GGRN_ERR_ALIGN;
   if (!state) {
     if (step && rows > 0) return GGRN_ERR_NULL;

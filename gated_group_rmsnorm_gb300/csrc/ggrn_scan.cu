@@ -908,6 +908,8 @@ extern "C" int ggrn_scan_step(const ggrn_scan_call* call, void* cuda_stream) {
   return ggrn::scan::run(call, true, cuda_stream);
 }
 extern "C" int64_t ggrn_scan_workspace_bytes(const ggrn_scan_call* call) {
-  if (!call || ggrn::scan::check_sizes(*call) != GGRN_OK || call->seqs < 0) return 0;
+  if (!call || ggrn::scan::check_sizes(*call) != GGRN_OK ||
+      !ggrn::mixer::counts_ok(call->rows, call->seqs, call->cu_seqlens != nullptr))
+    return 0;
   return ggrn::scan::layout_of(*call).bytes;
 }

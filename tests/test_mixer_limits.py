@@ -33,3 +33,15 @@ def test_workspace_of_many_sequences():
             k = _scan(rows=rows, seqs=70000, dtype=dtype, state=None, slots=None, resume=None)
             n = g.load().ggrn_scan_workspace_bytes(ctypes.byref(k))
             assert 0 <= n <= 2 * 65535 * entry + 32
+
+
+@pytest.mark.parametrize("kw", [dict(rows=1 << 40), dict(rows=(1 << 63) - 1), dict(rows=1 << 31),
+                                dict(rows=1 << 20, seqs=0), dict(rows=-1), dict(seqs=-1),
+                                dict(rows=1 << 20, seqs=1 << 31),
+                                dict(rows=1 << 20, seqs=3, cu_seqlens=None),
+                                dict(rows=(1 << 63) - 1, seqs=1, cu_seqlens=None)])
+def test_no_workspace_for_rows_that_are_refused(kw):
+    """Rows and sequences that the scan refuses have no size of a workspace."""
+    k = _scan(state=None, slots=None, resume=None, **kw)
+    assert g.load().ggrn_scan(ctypes.byref(k), None) == binding.ERR_SHAPE
+    assert g.load().ggrn_scan_workspace_bytes(ctypes.byref(k)) == 0
