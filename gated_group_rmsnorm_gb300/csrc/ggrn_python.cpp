@@ -95,6 +95,14 @@ at::Tensor output(PyObject* o, const at::Tensor& x) {
   return *t;
 }
 
+// The interpreter's lock given up for a scope (taken again on an exception too).
+struct WithoutLock {
+  PyThreadState* state = PyEval_SaveThread();
+  WithoutLock() = default;
+  WithoutLock(const WithoutLock&) = delete;
+  ~WithoutLock() { PyEval_RestoreThread(state); }
+};
+
 // Sequences and pool of a call: the fields both structures share.
 template <typename Call>
 void fill_seqs(Call* k, const at::Tensor& x, PyObject* cu_seqlens, PyObject* state_o,
@@ -245,17 +253,22 @@ at::Tensor fill_scan(ggrn_scan_call* k, const at::Tensor*& x_out, PyObject* cons
   return out;
 }
 
-// A call on its tensors' device and that device's current stream.
+// A call on its tensors' device and that device's current stream.  The
+// interpreter's lock is released for it: a launch waits while the stream's queue
+// is full, and other Python threads go on meanwhile.
 template <typename Call>
 PyObject* launch(int (*fn)(const Call*, void*), const Call& k, const at::Tensor& x,
                  const at::Tensor& out, const char* what) {
   int st;
-  const c10::DeviceIndex here = c10::cuda::current_device(), dev = x.device().index();
-  if (here == dev) {
-    st = fn(&k, c10::cuda::getCurrentCUDAStream(dev).stream());
-  } else {
-    c10::cuda::CUDAGuard guard(dev);
-    st = fn(&k, c10::cuda::getCurrentCUDAStream(dev).stream());
+  {
+    const WithoutLock released;
+    const c10::DeviceIndex here = c10::cuda::current_device(), dev = x.device().index();
+    if (here == dev) {
+      st = fn(&k, c10::cuda::getCurrentCUDAStream(dev).stream());
+    } else {
+      c10::cuda::CUDAGuard guard(dev);
+      st = fn(&k, c10::cuda::getCurrentCUDAStream(dev).stream());
+    }
   }
   if (st != GGRN_OK) {
     PyObject* r = PyObject_CallFunction(g_error, "is", st, what);
