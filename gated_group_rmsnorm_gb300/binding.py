@@ -619,6 +619,13 @@ def ssm_scan(x: torch.Tensor, dt: torch.Tensor, a: torch.Tensor, b: torch.Tensor
     ``resume`` as in ``causal_conv``.  ``workspace``: optional uint8 device
     tensor of ``scan_workspace_bytes`` of these tensors and ``out`` (allocated
     when omitted and needed).
+
+    Sums, decays and states are f32.  bf16 with ``state_size`` a multiple of 8
+    up to 128 and ``head_dim`` of 4 (rows aligned to 16 bytes in b and c, 8 in x
+    and out) runs on the tensor cores and rounds two operands of the output's
+    products to bf16 as well, c b^T with its decays and the state that c
+    multiplies: up to 2^-8 of the sum of an output's terms' sizes.  States are
+    not rounded so.
     """
     lo, hi = dt_limits
     return (_native or load_binding()).scan(x, dt, a, b, c, head_dim, state_size, d, dt_bias,

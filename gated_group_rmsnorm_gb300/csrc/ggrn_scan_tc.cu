@@ -10,8 +10,9 @@
 //   S'   = 2^L(Q-1, -1) S + dS                     f32, in registers
 // The products accumulate in f32 in tensor memory.  Only the operands M and S
 // are rounded to bf16 (2^-8 of each term of an output that is itself rounded
-// to bf16); w X carries 24 bits, since its sums are the f32 state that is
-// returned.
+// to bf16: of the sum of the terms' sizes, which is more than the output's own
+// rounding where they cancel); w X carries 24 bits, since its sums are the f32
+// state that is returned.
 //
 // The decays of M come from sums inside blocks of 32 tokens: a row's factor
 // for a whole column block is one exponential (row prefix + the blocks
@@ -1128,9 +1129,13 @@ bool tc_covers(const ggrn_scan_call& c) {
 // time) and the join.  The lengths behind cu_seqlens are not known here:
 // sequences are taken for equally long, and where those stay whole a part is as
 // long as the launch for them takes (and no less than twice their length): one
-// sequence of that length beside the others costs nothing.  3777 rows in 11
-// sequences of 0 to 918, 96 heads of 80 x 128: with parts of twice the mean, 50
-// of 190 us went into cutting two of them.
+// sequence of that length may run beside the others.  3777 rows in 11 sequences
+// of 0 to 918, 96 heads of 80 x 128: with parts of twice the mean, 50 of 190 us
+// went into cutting two of them.  It is not free: CTAs start by part first and
+// head second, so the long parts of the last heads start when the others are
+// nearly done.  Counted in chunks as above, 12 sequences of 100 rows and one of
+// 10000 behind them, 96 heads of 80, end after 143 (the longest first: 93; cut
+// at twice the mean: 168).
 int64_t tc_part_rows(const ggrn_scan_call& c, int64_t longest) {
   const int64_t tiles = (c.head_dim + tile_of(c.head_dim) - 1) / tile_of(c.head_dim);
   const int64_t heads = c.heads * tiles, sms = device_sms();

@@ -413,7 +413,24 @@ int ggrn_forward_noalloc(const void* y, const void* gate, const void* w, void* o
  *     dt[t]   = clamp(softplus(dt_raw[t,h] + dt_bias[h]), dt_min, dt_max)
  *     S[t]    = exp(dt[t] * a[h]) * S[t-1] + dt[t] * x[t,h,:] (x) B[t,g,:]
  *     out     = cast_T(S[t] C[t,g,:] + d[h] * x[t,h,:])
- * All arithmetic in f32 or better; T in {f32, f16, bf16}.
+ * T in {f32, f16, bf16}.
+ *
+ * Arithmetic.  Inputs are widened to f32, sums, decays and states are f32, and
+ * an output is rounded to T once.  One form rounds more: bf16 prompts of the
+ * scan with state_size a multiple of 8 up to 128, head_dim a multiple of 4, and
+ * rows of b and c on 16-byte, of x and out on 8-byte boundaries run on the
+ * tensor cores, whose operands are bf16.  There C B^T with its decays, and the
+ * state where C multiplies it, are rounded to bf16 before their products: an
+ * output may be off by 2^-8 of the sum of its terms' sizes besides its own
+ * rounding, which is more than that rounding where the terms cancel, and a
+ * prompt's last row is not the step form's bit for bit.  The states do not go
+ * through these roundings and keep f32's accuracy.
+ *
+ * Values that are not finite reach only the outputs and states that depend on
+ * them.  An infinite x or dt gives the definition's infinities and NaN, but
+ * that an infinity whose decay since has become zero in f32 may be a NaN; on the
+ * tensor cores an infinite b or c may give NaN where the definition has an
+ * infinity.
  *
  * Sequences.  The rows of a call are `seqs` sequences one behind the other:
  * with cu_seqlens (DEVICE int32 [seqs + 1], ascending, cu_seqlens[0] >= 0)
