@@ -39,7 +39,8 @@ EXPORTS = ("ggrn_forward", "ggrn_forward_path", "ggrn_plan", "ggrn_graph_create"
            "ggrn_forward_inproj", "ggrn_forward_host", "ggrn_forward_inproj_host",
            "ggrn_host_workspace_bytes", "ggrn_selftest_wait_timeout", "ggrn_norm_outproj",
            "ggrn_norm_outproj_workspace_bytes", "ggrn_conv", "ggrn_conv_step", "ggrn_scan",
-           "ggrn_scan_step", "ggrn_scan_workspace_bytes", "ggrn_graph_create_steps")
+           "ggrn_scan_step", "ggrn_scan_workspace_bytes", "ggrn_selftest_scan_timeout",
+           "ggrn_graph_create_steps")
 # ggrn_activation / ggrn_step_kind
 ACT_CODE = {None: 0, "silu": 1}
 STEP_FORWARD, STEP_CONV, STEP_SCAN = 0, 1, 2
@@ -170,7 +171,8 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         L.ggrn_last_cuda_error.argtypes = []
         L.ggrn_last_cuda_error.restype = ctypes.c_char_p
         for name, call in (("ggrn_conv", ConvCall), ("ggrn_conv_step", ConvCall),
-                           ("ggrn_scan", ScanCall), ("ggrn_scan_step", ScanCall)):
+                           ("ggrn_scan", ScanCall), ("ggrn_scan_step", ScanCall),
+                           ("ggrn_selftest_scan_timeout", ScanCall)):
             fn = getattr(L, name)
             fn.argtypes = [ctypes.POINTER(call), vp]
             fn.restype = ci

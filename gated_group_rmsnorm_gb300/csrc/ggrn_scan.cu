@@ -907,6 +907,23 @@ extern "C" int ggrn_scan(const ggrn_scan_call* call, void* cuda_stream) {
 extern "C" int ggrn_scan_step(const ggrn_scan_call* call, void* cuda_stream) {
   return ggrn::scan::run(call, true, cuda_stream);
 }
+// One launch of the tensor-core kernel whose B and C never come.  Without a pool
+// and cuts, so that nothing is written.
+extern "C" int ggrn_selftest_scan_timeout(const ggrn_scan_call* call, void* cuda_stream) {
+  using namespace ggrn;
+  using namespace ggrn::scan;
+  if (!call) return GGRN_ERR_ARG;
+  const ggrn_scan_call& c = *call;
+  Params p = {};
+  const int st = check(c, false, &p);
+  if (st != GGRN_OK) return st;
+  if (c.rows == 0) return GGRN_ERR_SHAPE;
+  const Layout l = layout_of(c);
+  if (!l.tc || l.cut || c.state) return GGRN_ERR_UNSUPPORTED;
+  p.part = l.part;
+  p.parts = l.parts;
+  return tc_run(c, p, false, static_cast<cudaStream_t>(cuda_stream), /*no_copies=*/true);
+}
 extern "C" int64_t ggrn_scan_workspace_bytes(const ggrn_scan_call* call) {
   if (!call || ggrn::scan::check_sizes(*call) != GGRN_OK ||
       !ggrn::mixer::counts_ok(call->rows, call->seqs, call->cu_seqlens != nullptr))

@@ -58,10 +58,11 @@ inline unsigned inner_parts(const Params& p) {
 int launch_join(const Params& p, cudaStream_t s);
 
 // The tensor-core kernels (ggrn_scan_tc.cu): whether they cover a call, the
-// rows of their parts, and their launches.
+// rows of their parts, and their launches (no_copies: the self-test's).
 bool tc_covers(const ggrn_scan_call& c);
 int64_t tc_part_rows(const ggrn_scan_call& c, int64_t longest);
-int tc_run(const ggrn_scan_call& c, const Params& p, bool cut, cudaStream_t s);
+int tc_run(const ggrn_scan_call& c, const Params& p, bool cut, cudaStream_t s,
+           bool no_copies = false);
 
 }  // namespace scan
 }  // namespace ggrn
