@@ -8,6 +8,7 @@ exception says so.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import importlib.machinery
 import importlib.util
@@ -730,13 +731,20 @@ class DecodeGraph:
             device = here
         self.device = device
         self._handle = ctypes.c_void_p()
-        st = load().ggrn_graph_create_steps(arr, len(calls), ctypes.byref(self._handle))
+        lib = load()
+        with torch.cuda.device(device) if device is not None else contextlib.nullcontext():
+            st = lib.ggrn_graph_create_steps(arr, len(calls), ctypes.byref(self._handle))
+        self._launch = lib.ggrn_graph_launch
         if st != OK:
             raise GgrnError(st, "ggrn_graph_create_steps")
 
     def replay(self, stream: torch.cuda.Stream | None = None) -> None:
         s = stream.cuda_stream if stream is not None else torch.cuda.current_stream(self.device).cuda_stream
-        st = load().ggrn_graph_launch(self._handle, ctypes.c_void_p(s))
+        if torch.cuda.current_device() == self.device.index:
+            st = self._launch(self._handle, ctypes.c_void_p(s))
+        else:
+            with torch.cuda.device(self.device):
+                st = self._launch(self._handle, ctypes.c_void_p(s))
         if st != OK:
             raise GgrnError(st, "ggrn_graph_launch")
 
