@@ -8,9 +8,10 @@
 // of one 16-byte vector of channels in registers and slides its window down a
 // tile of rows, four rows of loads ahead of the ones it computes; an input is
 // loaded once per thread plus W-1 rows of overlap between tiles, which come
-// from L2.  The arithmetic runs on f32 pairs.  4096 x 9728 bf16: 29.8 us, 79 %
-// of the rate of a plain copy (27.8 without the SiLU, whose exponential and
-// reciprocal take 17 us of the special function units).
+// from L2.  The arithmetic runs on f32 pairs.  4096 x 9728 bf16: 30.0 us, 78 %
+// of the rate of a plain copy (27.9 without the SiLU, whose exponential and
+// reciprocal take 17 us of the special function units); f32, with an accurate
+// SiLU: 53.7 us, 88 % (50.9 without it).
 //
 // Rows whose window reaches before their sequence (the first W-1) and the
 // pool's entries belong to other CTAs of the same launch, one per sequence
@@ -18,7 +19,7 @@
 // computes those rows and writes the new entry, so no thread reads an entry
 // that another one writes.  The step form is those CTAs alone, several
 // sequences to a thread (in 16-bit types the taps and the bias are ten times
-// a row's bytes): 256 x 9728 bf16 6.3 us, the pool's entries being in L2.
+// a row's bytes): 256 x 9728 bf16 6.7 us, the pool's entries being in L2.
 #include <cuda_runtime.h>
 
 #include "ggrn_mixer.cuh"

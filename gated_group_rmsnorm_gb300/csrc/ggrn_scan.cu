@@ -531,9 +531,10 @@ __global__ void __launch_bounds__(256) k_scan_join(const Params p) {
 // k_scan_step: one token.  Bound by the state's bytes (8 per entry, read and
 // written once).  A warp takes kStepRows rows of one head's S at a time, all
 // their loads in flight before the first is used; the lanes hold B and C of
-// their columns.  128 sequences of 96 heads of 80 x 128: 152 us, 98 % of the
-// rate of a plain copy; one sequence: 3.2 us, of which 1.2 are its bytes.  VEC: lanes take 4 columns (16 bytes), state_size a multiple
-// of 4 and the pool 16-byte aligned; else one column each.
+// their columns.  128 sequences of 96 heads of 80 x 128: 154 us, 97 % of the
+// rate of a plain copy; one sequence: 3.8 us, of which 1.2 are its bytes.  VEC:
+// lanes take 4 columns (16 bytes), state_size a multiple of 4 and the pool
+// 16-byte aligned; else one column each.
 // ---------------------------------------------------------------------------
 constexpr int kStepRows = 4;
 constexpr int kStepThreads = 128;

@@ -48,9 +48,9 @@
 //
 // What bounds it: the chain of a chunk's stages, 2.5 us a chunk (64 columns
 // 2.4, 80 columns 2.6; the products alone take 1.7), and about 10 us to start
-// and end a launch.  4096 tokens of 96 heads of 80 x 128: 96 us, where the bytes
+// and end a launch.  4096 tokens of 96 heads of 80 x 128: 97 us, where the bytes
 // take 22 and the products, at the rate of a large matrix product, 11; eight
-// sequences of 2048 tokens, 80 heads of 64: 245 us.  One CTA per SM for all its
+// sequences of 2048 tokens, 80 heads of 64: 246 us.  One CTA per SM for all its
 // parts, with no stop between them, was slower by a fifth a chunk, since the
 // roles then have to keep more than their registers hold: 291 us for the eight
 // sequences.  The
