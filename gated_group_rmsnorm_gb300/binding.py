@@ -732,7 +732,10 @@ class DecodeGraph:
         self.device = device
         self._handle = ctypes.c_void_p()
         lib = load()
-        with torch.cuda.device(device) if device is not None else contextlib.nullcontext():
+        # (buffers in pinned host memory name no device: the caller's current one)
+        self._index = device.index if device is not None and device.type == "cuda" else None
+        with (contextlib.nullcontext() if self._index is None else
+              torch.cuda.device(self._index)):
             st = lib.ggrn_graph_create_steps(arr, len(calls), ctypes.byref(self._handle))
         self._launch = lib.ggrn_graph_launch
         if st != OK:
@@ -740,10 +743,10 @@ class DecodeGraph:
 
     def replay(self, stream: torch.cuda.Stream | None = None) -> None:
         s = stream.cuda_stream if stream is not None else torch.cuda.current_stream(self.device).cuda_stream
-        if torch.cuda.current_device() == self.device.index:
+        if self._index is None or torch.cuda.current_device() == self._index:
             st = self._launch(self._handle, ctypes.c_void_p(s))
         else:
-            with torch.cuda.device(self.device):
+            with torch.cuda.device(self._index):
                 st = self._launch(self._handle, ctypes.c_void_p(s))
         if st != OK:
             raise GgrnError(st, "ggrn_graph_launch")

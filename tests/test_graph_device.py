@@ -83,3 +83,13 @@ def test_graph_runs_on_its_tensors_device(cuda, index, n):
 def test_no_calls_are_the_librarys_to_refuse(cuda):
     binding.DecodeGraph([])
     assert cuda.seen == [("create", 0)]
+
+
+def test_buffers_in_host_memory_take_the_callers_device(cuda):
+    """Pinned buffers are read and written over the host link, on the stream given."""
+    class Given:
+        cuda_stream = 77
+
+    graph = binding.DecodeGraph([_call("cpu")])
+    graph.replay(Given())
+    assert cuda.seen == [("create", 0), ("launch", 0, 77)]
