@@ -313,7 +313,10 @@ __device__ __forceinline__ void pieces_of(const uint4& x, float w, uint4 (&u)[3]
 
 // Chunks with products that are not finite.  Such a product is its largest piece
 // alone.  An x that is not finite is taken out of X, since M's zeros before its
-// row would spread it over rows before its own; add_odd puts it back.
+// row would spread it over rows before its own; add_odd puts it back.  In its
+// place stays the smallest normal number of its sign, which adds nothing to what
+// add_odd makes infinite anyway: beside an infinite M (of an infinite dt) a zero
+// there would be a NaN.
 __device__ __noinline__ void odd_chunk(uint32_t x_at, uint32_t w_at, uint32_t x_bytes, float w) {
   for (int i = 0; i < 8; ++i) {
     unsigned short h;
@@ -325,8 +328,9 @@ __device__ __noinline__ void odd_chunk(uint32_t x_at, uint32_t w_at, uint32_t x_
     const unsigned short zero = 0;
     for (int k = 1; k < 3; ++k)
       asm volatile("st.shared.u16 [%0], %1;" ::"r"(w_at + k * x_bytes + 2 * i), "h"(zero) : "memory");
+    const unsigned short least = (h & 0x8000) | 0x0080;
     if ((h & 0x7f80) == 0x7f80)
-      asm volatile("st.shared.u16 [%0], %1;" ::"r"(x_at + 2 * i), "h"(zero) : "memory");
+      asm volatile("st.shared.u16 [%0], %1;" ::"r"(x_at + 2 * i), "h"(least) : "memory");
   }
 }
 // What row i of a chunk's Y lacks for that: the terms of the x that are not

@@ -80,3 +80,20 @@ def test_a_long_prompt_of_infinities():
     got = k.run()
     assert torch.isposinf(got).all()
     assert g.fault_status() == 0
+
+
+@pytest.mark.parametrize("rows,row", [(1, 0), (40, 0), (300, 37), (300, 140)])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_x_and_dt_of_one_row(dtype, rows, row):
+    """An infinite dt beside x that are infinities of both signs, NaN and finite."""
+    k = _case(rows, (2, 80, 1, 24), dtype, slots=1, seed=12)
+    v = k.views(k.xbc, k.z)
+    v["dt"][row, 0] = math.inf
+    for col, bad in ((3, math.inf), (4, -math.inf), (9, math.nan), (85, math.inf)):
+        v["x"][row, col] = bad
+    st = k.state.cuda()
+    got = k.run(state=st, resume=torch.ones(1, dtype=torch.bool).cuda())
+    want, *_, new, _, _ = k.want(spans=[(0, rows)], resume=[True])
+    _same_kinds(got, want)
+    _same_kinds(st, new)
+    assert g.fault_status() == 0
