@@ -543,7 +543,7 @@ int64_t ggrn_scan_workspace_bytes(const ggrn_scan_call* call);
 /*
  * ggrn_selftest_scan_timeout -- exercise the failure path of the scan's
  * tensor-core kernel: launches it for this call without the copies of b and c,
- * so that its bounded waits run out (about two seconds).  The kernel ends by
+ * so that its bounded waits run out (about five seconds).  The kernel ends by
  * itself, sets bit 64 of the status word and writes nothing.  For tests.
  * GGRN_ERR_UNSUPPORTED for calls that do not run on the tensor cores, that may
  * be cut into parts or that have a state; statuses of ggrn_scan otherwise.
