@@ -76,3 +76,39 @@ def test_the_first_call_of_a_process_may_be_captured():
     r = subprocess.run([sys.executable, "-c", COLD], cwd=ROOT, capture_output=True, text=True,
                        timeout=300)
     assert r.returncode == 0, r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_calls_from_several_threads(dtype):
+    """Calls of several threads at the same time, each on a stream of its own."""
+    cases = [Case(900 + 100 * i, 4, 64, 1, 96, dtype, seed=20 + i) for i in range(4)]
+    w = torch.randn(256, 4, generator=torch.Generator().manual_seed(1)).cuda()
+    inputs = [k.on() for k in cases]
+
+    def both(v, c):
+        return (g.causal_conv(v["x"], w),
+                g.ssm_scan(v["x"], v["dt"], c["a"], v["b"], v["c"], head_dim=64, state_size=96,
+                           d=c["d"], dt_bias=c["dt_bias"]))
+
+    want = [both(*i) for i in inputs]
+    torch.cuda.synchronize()
+    wrong, started = [], threading.Barrier(len(cases))
+
+    def run(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                started.wait(timeout=30)
+                for _ in range(40):
+                    got = both(*inputs[i])
+                    torch.cuda.current_stream().synchronize()
+                    assert all(torch.equal(a, b) for a, b in zip(got, want[i]))
+        except BaseException as e:  # (an exception of a thread reaches no test by itself)
+            wrong.append(e)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(len(cases))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong
+    assert g.fault_status() == 0
