@@ -197,7 +197,9 @@ def kernel_source_hash() -> str:
         if fn.endswith((".cu", ".cuh", ".h")) and fn not in (
                 "ggrn_host.cu", "ggrn_outproj.cu", "ggrn_umma.cuh", "ggrn_mixer.cuh",
                 "ggrn_optin.h",
-                "ggrn_conv.cu", "ggrn_scan.cuh", "ggrn_scan.cu", "ggrn_scan_tc.cu"):
+                "ggrn_conv.cu", "ggrn_scan.cuh", "ggrn_scan.cu", "ggrn_scan_tc.cu",
+                "ggrn_recur.cu", "ggrn_norms.cuh", "ggrn_norms.cu", "ggrn_norms_bf16.cu",
+                "ggrn_norms_f16.cu", "ggrn_norms_f32.cu"):
             with open(os.path.join(CSRC, fn), "rb") as fh:
                 h.update(fn.encode() + b"\0" + _without_timeline(fh.read()))
     return h.hexdigest()[:16]

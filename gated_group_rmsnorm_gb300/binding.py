@@ -41,10 +41,15 @@ EXPORTS = ("ggrn_forward", "ggrn_forward_path", "ggrn_plan", "ggrn_graph_create"
            "ggrn_host_workspace_bytes", "ggrn_selftest_wait_timeout", "ggrn_norm_outproj",
            "ggrn_norm_outproj_workspace_bytes", "ggrn_conv", "ggrn_conv_step", "ggrn_scan",
            "ggrn_scan_step", "ggrn_scan_workspace_bytes", "ggrn_selftest_scan_timeout",
-           "ggrn_graph_create_steps")
+           "ggrn_graph_create_steps", "ggrn_recur", "ggrn_recur_step", "ggrn_recur_backward",
+           "ggrn_recur_backward_workspace_bytes", "ggrn_layer_norm", "ggrn_layer_norm_backward",
+           "ggrn_layer_norm_backward_workspace_bytes", "ggrn_backward",
+           "ggrn_backward_workspace_bytes")
 # ggrn_activation / ggrn_step_kind
 ACT_CODE = {None: 0, "silu": 1}
-STEP_FORWARD, STEP_CONV, STEP_SCAN = 0, 1, 2
+STEP_FORWARD, STEP_CONV, STEP_SCAN, STEP_RECUR, STEP_LAYER_NORM = range(5)
+# rows between the states that the recurrence keeps for its backward pass
+SAVED_ROWS = 64
 
 
 class GgrnError(RuntimeError):
@@ -98,8 +103,60 @@ class ScanCall(ctypes.Structure):
                  ("dt_softplus", ctypes.c_int32), ("dtype", ctypes.c_int32)])
 
 
+class RecurCall(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("x", "input_gate", "decay_gate", "a", "out",
+                                                "state", "slots", "resume", "cu_seqlens",
+                                                "saved")] +
+                [(n, ctypes.c_int64) for n in ("rows", "seqs", "width", "x_row_stride",
+                                               "input_gate_row_stride", "decay_gate_row_stride",
+                                               "out_row_stride", "state_slots",
+                                               "state_slot_stride")] +
+                [("dtype", ctypes.c_int32)])
+
+
+class RecurBackwardCall(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("dout", "x", "input_gate", "decay_gate", "a",
+                                                "dx", "dinput_gate", "ddecay_gate", "da",
+                                                "dinitial", "dstate", "state", "slots", "resume",
+                                                "cu_seqlens", "saved", "workspace")] +
+                [(n, ctypes.c_int64) for n in ("workspace_bytes", "rows", "seqs", "width",
+                                               "dout_row_stride", "x_row_stride",
+                                               "input_gate_row_stride", "decay_gate_row_stride",
+                                               "dx_row_stride", "dinput_gate_row_stride",
+                                               "ddecay_gate_row_stride", "state_slots",
+                                               "state_slot_stride")] +
+                [("dtype", ctypes.c_int32)])
+
+
+class LayerNormCall(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("x", "w", "b", "out")] +
+                [(n, ctypes.c_int64) for n in ("rows", "width", "x_row_stride",
+                                               "out_row_stride")] +
+                [("eps", ctypes.c_float), ("dtype", ctypes.c_int32)])
+
+
+class LayerNormBackwardCall(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("dout", "x", "w", "dx", "dw", "db",
+                                                "workspace")] +
+                [(n, ctypes.c_int64) for n in ("workspace_bytes", "rows", "width",
+                                               "dout_row_stride", "x_row_stride",
+                                               "dx_row_stride")] +
+                [("eps", ctypes.c_float), ("dtype", ctypes.c_int32)])
+
+
+class BackwardCall(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("dout", "y", "gate", "w", "dy", "dgate", "dw",
+                                                "workspace")] +
+                [(n, ctypes.c_int64) for n in ("workspace_bytes", "rows", "width", "group_size",
+                                               "dout_row_stride", "y_row_stride",
+                                               "gate_row_stride", "dy_row_stride",
+                                               "dgate_row_stride")] +
+                [("eps", ctypes.c_float), ("dtype", ctypes.c_int32), ("mode", ctypes.c_int32)])
+
+
 class _StepUnion(ctypes.Union):
-    _fields_ = [("forward", Call), ("conv", ConvCall), ("scan", ScanCall)]
+    _fields_ = [("forward", Call), ("conv", ConvCall), ("scan", ScanCall), ("recur", RecurCall),
+                ("layer_norm", LayerNormCall)]
 
 
 class Step(ctypes.Structure):
@@ -173,12 +230,21 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         L.ggrn_last_cuda_error.restype = ctypes.c_char_p
         for name, call in (("ggrn_conv", ConvCall), ("ggrn_conv_step", ConvCall),
                            ("ggrn_scan", ScanCall), ("ggrn_scan_step", ScanCall),
-                           ("ggrn_selftest_scan_timeout", ScanCall)):
+                           ("ggrn_selftest_scan_timeout", ScanCall), ("ggrn_recur", RecurCall),
+                           ("ggrn_recur_step", RecurCall),
+                           ("ggrn_recur_backward", RecurBackwardCall),
+                           ("ggrn_layer_norm", LayerNormCall),
+                           ("ggrn_layer_norm_backward", LayerNormBackwardCall),
+                           ("ggrn_backward", BackwardCall)):
             fn = getattr(L, name)
             fn.argtypes = [ctypes.POINTER(call), vp]
             fn.restype = ci
-        L.ggrn_scan_workspace_bytes.argtypes = [ctypes.POINTER(ScanCall)]
-        L.ggrn_scan_workspace_bytes.restype = i64
+        for name, call in (("ggrn_scan", ScanCall), ("ggrn_recur_backward", RecurBackwardCall),
+                           ("ggrn_layer_norm_backward", LayerNormBackwardCall),
+                           ("ggrn_backward", BackwardCall)):
+            fn = getattr(L, name + "_workspace_bytes")
+            fn.argtypes = [ctypes.POINTER(call)]
+            fn.restype = i64
         L.ggrn_graph_create_steps.argtypes = [ctypes.POINTER(Step), ctypes.c_int32,
                                               ctypes.POINTER(ctypes.c_void_p)]
         L.ggrn_graph_create_steps.restype = ci
@@ -666,6 +732,117 @@ def scan_workspace_bytes(x, dt, a, b, c, *, head_dim: int, state_size: int,
                                                False)
 
 
+# ---------------------------------------------------------------------------
+# The gated linear recurrence, layer norm, and the norms' backward passes.
+# ---------------------------------------------------------------------------
+def linear_recurrence(x: torch.Tensor, input_gate: torch.Tensor, decay_gate: torch.Tensor,
+                      a: torch.Tensor, *, cu_seqlens: torch.Tensor | None = None,
+                      state: torch.Tensor | None = None, slots: torch.Tensor | None = None,
+                      resume: torch.Tensor | None = None, saved: torch.Tensor | None = None,
+                      out: torch.Tensor | None = None) -> torch.Tensor:
+    """The gated linear recurrence over prompts (``ggrn_recur``), each channel by
+    itself, for mixers that take it in the place of the scan:
+
+        p_t = a * sigmoid(decay_gate_t)
+        h_t = exp(p_t) * h_{t-1} + sqrt(1 - exp(2 p_t)) * sigmoid(input_gate_t) * x_t
+
+    ``x``, ``input_gate``, ``decay_gate`` (both of them logits): [rows, width] or
+    [batch, length, width] of one dtype (f32, f16, bf16), row-strided views
+    allowed.  ``a``: f32 [width], the logarithm of each channel's decay at an open
+    gate (<= 0).  ``state``: f32 [slots, width]; ``cu_seqlens``, ``slots`` and
+    ``resume`` as in ``causal_conv``.  ``saved``: where given, receives what
+    ``linear_recurrence_backward`` can start from (``linear_recurrence_saved``).
+    All arithmetic and the states are f32; the output is rounded once.
+    """
+    return (_native or load_binding()).recur(x, input_gate, decay_gate, a, cu_seqlens, state, slots,
+                                             resume, saved, out, False)
+
+
+def linear_recurrence_step(x: torch.Tensor, input_gate: torch.Tensor, decay_gate: torch.Tensor,
+                           a: torch.Tensor, state: torch.Tensor, *,
+                           slots: torch.Tensor | None = None,
+                           out: torch.Tensor | None = None) -> torch.Tensor:
+    """``linear_recurrence`` for one new row of each sequence
+    (``ggrn_recur_step``): row i of ``x`` [batch, width] advances entry
+    ``slots[i]`` (i without slots) of ``state`` [slots, width] in place.  A row
+    whose slot is outside the pool is skipped: its output row is left as it was.
+    """
+    return (_native or load_binding()).recur(x, input_gate, decay_gate, a, None, state, slots, None,
+                                             None, out, True)
+
+
+def linear_recurrence_saved(x: torch.Tensor) -> torch.Tensor:
+    """A tensor for ``linear_recurrence``'s ``saved``: f32, one state for every 64
+    rows of ``x``."""
+    rows = x.numel() // x.shape[-1] if x.numel() else 0
+    return torch.empty(-(-rows // SAVED_ROWS), x.shape[-1], dtype=torch.float32, device=x.device)
+
+
+def linear_recurrence_backward(dout: torch.Tensor, x: torch.Tensor, input_gate: torch.Tensor,
+                               decay_gate: torch.Tensor, a: torch.Tensor, *,
+                               cu_seqlens: torch.Tensor | None = None,
+                               state: torch.Tensor | None = None,
+                               slots: torch.Tensor | None = None,
+                               resume: torch.Tensor | None = None,
+                               dstate: torch.Tensor | None = None,
+                               saved: torch.Tensor | None = None,
+                               dx: torch.Tensor | None = None,
+                               dinput_gate: torch.Tensor | None = None,
+                               ddecay_gate: torch.Tensor | None = None):
+    """The gradients of ``linear_recurrence`` (``ggrn_recur_backward``): ``(dx,
+    dinput_gate, ddecay_gate, da, dinitial)``.
+
+    ``dout``: the gradient of the output.  ``dstate``: f32 [sequences, width], the
+    gradient of the states after the sequences' last rows.  ``state``: the pool as
+    it was before the forward call (which overwrites it: keep a copy); with it
+    ``dinitial``, f32 [sequences, width], is the gradient of the states that the
+    sequences start from (zeros where one does not resume), else None.
+    ``saved``: what the forward call kept; without it the states are computed
+    again, at the price of the forward pass.  ``dx``, ``dinput_gate``,
+    ``ddecay_gate``: optional outputs (row-strided views allowed, such as columns
+    of one packed gradient); their rows of no sequence are zeros.  ``da``: f32
+    [width].
+    """
+    return (_native or load_binding()).recur_backward(dout, x, input_gate, decay_gate, a, cu_seqlens,
+                                                      state, slots, resume, dstate, saved, dx,
+                                                      dinput_gate, ddecay_gate)
+
+
+def layer_norm(x: torch.Tensor, w: torch.Tensor, b: torch.Tensor | None = None, *, eps: float,
+               out: torch.Tensor | None = None) -> torch.Tensor:
+    """Layer norm over the last dimension (``ggrn_layer_norm``):
+    ``out = (x - mean) * rsqrt(var + eps) * w + b``, the variance that of the
+    whole row.  ``x``: [..., width] of f32, f16 or bf16 whose leading axes fold
+    into rows (row-strided views allowed); ``w``, ``b``: f32 [width].
+    """
+    return (_native or load_binding()).layer_norm(x, w, b, eps, out)
+
+
+def layer_norm_backward(dout: torch.Tensor, x: torch.Tensor, w: torch.Tensor, *, eps: float,
+                        bias: bool = True, dx: torch.Tensor | None = None):
+    """The gradients of ``layer_norm`` (``ggrn_layer_norm_backward``): ``(dx, dw,
+    db)``; ``db`` is None with ``bias=False``.  ``dw`` and ``db`` are f32, summed
+    over all rows in a fixed order.  The row's statistics are computed again from
+    ``x``.
+    """
+    return (_native or load_binding()).layer_norm_backward(dout, x, w, eps, bias, dx)
+
+
+def backward(dout: torch.Tensor, y: torch.Tensor, gate: torch.Tensor, w: torch.Tensor, *,
+             group_size: int, eps: float, mode="mamba2", dy: torch.Tensor | None = None,
+             dgate: torch.Tensor | None = None):
+    """The gradients of ``forward`` (``ggrn_backward``): ``(dy, dgate, dw)``.
+
+    Arguments as in ``forward``; ``dout`` is the gradient of its output.  ``dy``,
+    ``dgate``: optional outputs (row-strided views allowed, such as columns of a
+    packed in-proj's gradient).  ``dw`` is f32 of ``w``'s shape, summed over all
+    rows (ONNX: and groups) in a fixed order.  The cast inside MAMBA2's formula is
+    differentiated as the identity.
+    """
+    return (_native or load_binding()).norm_backward(dout, y, gate, w, group_size, eps,
+                                                     MODE_CODE[mode], dy, dgate)
+
+
 def _given(c: dict, name: str):
     """An argument that a graph's call has to bring."""
     if c.get(name) is None:
@@ -678,9 +855,9 @@ class DecodeGraph:
 
     ``calls``: list of dicts with the tensors and arguments of ``forward``
     (``y``, ``gate``, ``w``, ``out``, ``group_size``, ``eps``, ``mode``), or, with
-    ``op`` set to "causal_conv_step" or "ssm_scan_step", those of that function
-    (``out`` included), in the order they run: a decode step of the mixer is
-    its convolution, scan and norm.  Each replay advances the states.  The
+    ``op`` set to "causal_conv_step", "ssm_scan_step", "linear_recurrence_step" or
+    "layer_norm", those of that function (``out`` included), in the order they
+    run: a decode step of the mixer is its convolution, scan and norm.  Each replay advances the states.  The
     tensors are baked into the graph: keep them alive and refill them in place
     between replays.  A chain of one call is launched directly on each replay
     (a graph of one small kernel costs more to launch than the kernel).
@@ -721,6 +898,18 @@ class DecodeGraph:
                     c.pop("x"), c.pop("dt"), c.pop("a"), c.pop("b"), c.pop("c"), *_sizes(st),
                     c.pop("d", None), c.pop("dt_bias", None), c.pop("dt_softplus", True), lo, hi,
                     None, st, c.pop("slots", None), None, _given(c, "out"), True))
+                here = call["x"].device
+            elif op == "linear_recurrence_step":
+                arr[i].kind = STEP_RECUR
+                arr[i].u.recur = RecurCall.from_buffer_copy(load_binding().recur_call(
+                    c.pop("x"), c.pop("input_gate"), c.pop("decay_gate"), c.pop("a"), None,
+                    c.pop("state"), c.pop("slots", None), None, None, _given(c, "out"), True))
+                here = call["x"].device
+            elif op == "layer_norm":
+                arr[i].kind = STEP_LAYER_NORM
+                arr[i].u.layer_norm = LayerNormCall.from_buffer_copy(
+                    load_binding().layer_norm_call(c.pop("x"), c.pop("w"), c.pop("b", None),
+                                                   c.pop("eps"), _given(c, "out")))
                 here = call["x"].device
             else:
                 raise ValueError(f"unknown op {op!r}")

@@ -26,10 +26,11 @@ TIMELINE_LIB_PATH = os.path.join(HERE, "libggrn_timeline.so")
 TIMELINE_BUILD_DIR = os.path.join(HERE, "_build_timeline")
 
 SOURCES = ["ggrn_api.cu", "ggrn_conv.cu", "ggrn_host.cu", "ggrn_kernels_bf16.cu",
-           "ggrn_kernels_f16.cu", "ggrn_kernels_f32.cu", "ggrn_outproj.cu", "ggrn_scan.cu",
-           "ggrn_scan_tc.cu"]
-HEADERS = ["ggrn_internal.h", "ggrn_kernels.cuh", "ggrn_mixer.cuh", "ggrn_optin.h",
-           "ggrn_scan.cuh", "ggrn_slots.h", "ggrn_stream.cuh", "ggrn_umma.cuh"]
+           "ggrn_kernels_f16.cu", "ggrn_kernels_f32.cu", "ggrn_norms.cu", "ggrn_norms_bf16.cu",
+           "ggrn_norms_f16.cu", "ggrn_norms_f32.cu", "ggrn_outproj.cu", "ggrn_recur.cu",
+           "ggrn_scan.cu", "ggrn_scan_tc.cu"]
+HEADERS = ["ggrn_internal.h", "ggrn_kernels.cuh", "ggrn_mixer.cuh", "ggrn_norms.cuh",
+           "ggrn_optin.h", "ggrn_scan.cuh", "ggrn_slots.h", "ggrn_stream.cuh", "ggrn_umma.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # the Python entry of the mixer's operators (a CPython extension on torch's
 # headers), linked to libggrn.so beside it

@@ -853,6 +853,8 @@ Args args_of(const ggrn_call& c) {
 int check_step(const ggrn_step& t) {
   if (t.kind == GGRN_STEP_CONV) return check_conv(t.u.conv, true);
   if (t.kind == GGRN_STEP_SCAN) return check_scan(t.u.scan, true);
+  if (t.kind == GGRN_STEP_RECUR) return check_recur(t.u.recur, true);
+  if (t.kind == GGRN_STEP_LAYER_NORM) return check_layer_norm(t.u.layer_norm);
   if (t.kind != GGRN_STEP_FORWARD) return GGRN_ERR_ARG;
   const Args a = args_of(t.u.forward);
   const int st = validate(a);
@@ -862,6 +864,8 @@ int check_step(const ggrn_step& t) {
 int enqueue_step(const ggrn_step& t, cudaStream_t s) {
   if (t.kind == GGRN_STEP_CONV) return ggrn_conv_step(&t.u.conv, s);
   if (t.kind == GGRN_STEP_SCAN) return ggrn_scan_step(&t.u.scan, s);
+  if (t.kind == GGRN_STEP_RECUR) return ggrn_recur_step(&t.u.recur, s);
+  if (t.kind == GGRN_STEP_LAYER_NORM) return ggrn_layer_norm(&t.u.layer_norm, s);
   return forward_impl(args_of(t.u.forward), kAuto, s);
 }
 

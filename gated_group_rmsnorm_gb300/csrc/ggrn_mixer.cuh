@@ -3,6 +3,8 @@
 // argument checks.
 #pragma once
 
+#include <initializer_list>
+
 #include "../../include/ggrn.h"
 #include "ggrn_kernels.cuh"
 
@@ -157,6 +159,35 @@ inline bool overlap(const Buffer& a, const Buffer& b) {
   return x < y + static_cast<uintptr_t>(b.bytes) && y < x + static_cast<uintptr_t>(a.bytes);
 }
 
+// The same of two matrices of more than one row with one row stride (bytes): columns
+// beside each other in the same rows do not overlap.
+struct Columns {
+  Buffer b;
+  int64_t width, stride;  // bytes; stride 0: not rows that can interleave
+};
+inline Columns columns(const Buffer& b, int64_t rows, int64_t width, int64_t stride, int es) {
+  return {b, width * es, rows > 1 ? stride * es : 0};
+}
+inline bool overlap(const Columns& a, const Columns& b) {
+  if (!overlap(a.b, b.b)) return false;
+  if (a.stride == 0 || a.stride != b.stride) return true;
+  int64_t d = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b.b.p) -
+                                   reinterpret_cast<uintptr_t>(a.b.p)) % a.stride;
+  if (d < 0) d += a.stride;
+  return !(d >= a.width && d <= a.stride - b.width);
+}
+// Whether an output overlaps another buffer: an input, or another output.
+inline bool outputs_overlap(std::initializer_list<Columns> outs,
+                            std::initializer_list<Columns> ins) {
+  for (const Columns& o : outs) {
+    for (const Columns& i : ins)
+      if (overlap(o, i)) return true;
+    for (const Columns& i : outs)
+      if (&i != &o && overlap(o, i)) return true;
+  }
+  return false;
+}
+
 // Whether `rows` rows can be `seqs` sequences (of equal length without offsets).
 inline bool counts_ok(int64_t rows, int64_t seqs, bool offsets) {
   if (rows < 0 || seqs < 0 || (seqs == 0 && rows > 0)) return false;
@@ -225,5 +256,7 @@ int device_sms();
 // The step forms for decode graphs: the argument checks alone, and the call.
 int check_conv(const ggrn_conv_call& c, bool step);
 int check_scan(const ggrn_scan_call& c, bool step);
+int check_recur(const ggrn_recur_call& c, bool step);
+int check_layer_norm(const ggrn_layer_norm_call& c);
 
 }  // namespace ggrn

@@ -1,4 +1,5 @@
-// ggrn_python.cpp -- the Python entry of the mixer's operators: checks tensors,
+// ggrn_python.cpp -- the Python entry of the mixer's operators, of layer norm and
+// of the backward passes: checks tensors,
 // fills the call structures of ggrn.h and makes the calls.
 //
 // A decode step's kernels take 2 to 4 microseconds; reading the sizes, strides
@@ -16,6 +17,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstring>
+#include <initializer_list>
 #include <string>
 
 #include "../../include/ggrn.h"
@@ -87,12 +89,36 @@ const T* vector(PyObject* o, int64_t n, at::ScalarType type, const at::Tensor& x
 }
 
 // The output: given, or made like x.
-at::Tensor output(PyObject* o, const at::Tensor& x) {
-  const at::Tensor* t = tensor(o, "out");
+at::Tensor output(PyObject* o, const at::Tensor& x, const char* name = "out",
+                  const char* like = "x") {
+  const at::Tensor* t = tensor(o, name);
   if (!t) return at::empty(x.sizes(), x.options().memory_format(c10::nullopt));
   if (t->sizes() != x.sizes() || t->scalar_type() != x.scalar_type() || t->device() != x.device())
-    refuse("out must have the shape, dtype and device of x");
+    refuse(std::string(name) + " must have the shape, dtype and device of " + like);
   return *t;
+}
+
+// A tensor that has to be like x: its address, and its row stride.
+const void* alike(PyObject* o, const at::Tensor& x, const char* name, int64_t* stride,
+                  const char* like = "x") {
+  const at::Tensor& t = needed(o, name);
+  if (t.sizes() != x.sizes() || t.scalar_type() != x.scalar_type() || t.device() != x.device())
+    refuse(std::string(name) + " must have the shape, dtype and device of " + like);
+  int64_t rows;
+  rows_of(t, x.size(-1), name, &rows, stride);
+  return t.const_data_ptr();
+}
+// An output like x: the tensor, its address and its row stride.
+at::Tensor output_rows(PyObject* o, const at::Tensor& x, const char* name, void** p,
+                       int64_t* stride, const char* like = "x") {
+  at::Tensor t = output(o, x, name, like);
+  int64_t rows;
+  rows_of(t, x.size(-1), name, &rows, stride);
+  *p = t.data_ptr();
+  return t;
+}
+at::Tensor new_floats(at::IntArrayRef sizes, const at::Tensor& x) {
+  return at::empty(sizes, x.options().dtype(at::kFloat).memory_format(c10::nullopt));
 }
 
 // The interpreter's lock given up for a scope (taken again on an exception too).
@@ -253,12 +279,54 @@ at::Tensor fill_scan(ggrn_scan_call* k, const at::Tensor*& x_out, PyObject* cons
   return out;
 }
 
+// x, input_gate, decay_gate, a, cu_seqlens, state, slots, resume, saved, out, step
+at::Tensor fill_recur(ggrn_recur_call* k, const at::Tensor*& x_out, PyObject* const* a) {
+  const at::Tensor& x = needed(a[0], "x");
+  x_out = &x;
+  if (!x.is_cuda()) refuse("the recurrence runs on CUDA tensors only (no CPU path)");
+  const bool step = PyObject_IsTrue(a[10]) == 1;
+  std::memset(k, 0, sizeof(*k));
+  k->dtype = dtype_code(x);
+  if (x.dim() < 2) refuse("x must be [rows, width] or [batch, length, width]");
+  const int64_t width = x.size(-1);
+  rows_of(x, width, "x", &k->rows, &k->x_row_stride);
+  k->x = x.const_data_ptr();
+  k->width = width;
+  k->input_gate = alike(a[1], x, "input_gate", &k->input_gate_row_stride);
+  k->decay_gate = alike(a[2], x, "decay_gate", &k->decay_gate_row_stride);
+  needed(a[3], "a");
+  k->a = vector<float>(a[3], width, at::kFloat, x, "a");
+  const int64_t kept = (k->rows + GGRN_RECUR_SAVED_ROWS - 1) / GGRN_RECUR_SAVED_ROWS;
+  k->saved = const_cast<float*>(vector<float>(a[8], kept * width, at::kFloat, x, "saved"));
+  const int64_t held[1] = {width};
+  fill_seqs(k, x, a[4], a[5], a[6], a[7], held, at::kFloat, step);
+  return output_rows(a[9], x, "out", &k->out, &k->out_row_stride);
+}
+
+// x, w, b, eps, out
+at::Tensor fill_layer_norm(ggrn_layer_norm_call* k, const at::Tensor*& x_out, PyObject* const* a) {
+  const at::Tensor& x = needed(a[0], "x");
+  x_out = &x;
+  if (!x.is_cuda()) refuse("layer_norm runs on CUDA tensors only (no CPU path)");
+  std::memset(k, 0, sizeof(*k));
+  k->dtype = dtype_code(x);
+  if (x.dim() < 1) refuse("x must have rank >= 1");
+  k->width = x.size(-1);
+  rows_of(x, k->width, "x", &k->rows, &k->x_row_stride);
+  k->x = x.const_data_ptr();
+  needed(a[1], "w");
+  k->w = vector<float>(a[1], k->width, at::kFloat, x, "w");
+  k->b = vector<float>(a[2], k->width, at::kFloat, x, "b");
+  k->eps = static_cast<float>(PyFloat_AsDouble(a[3]));
+  if (PyErr_Occurred()) throw python_error();
+  return output_rows(a[4], x, "out", &k->out, &k->out_row_stride);
+}
+
 // A call on its tensors' device and that device's current stream.  The
 // interpreter's lock is released for it: a launch waits while the stream's queue
 // is full, and other Python threads go on meanwhile.
 template <typename Call>
-PyObject* launch(int (*fn)(const Call*, void*), const Call& k, const at::Tensor& x,
-                 const at::Tensor& out, const char* what) {
+bool made(int (*fn)(const Call*, void*), const Call& k, const at::Tensor& x, const char* what) {
   int st;
   {
     const WithoutLock released;
@@ -273,9 +341,47 @@ PyObject* launch(int (*fn)(const Call*, void*), const Call& k, const at::Tensor&
   if (st != GGRN_OK) {
     PyObject* r = PyObject_CallFunction(g_error, "is", st, what);
     Py_XDECREF(r);
-    return nullptr;
+    return false;
   }
-  return THPVariable_Wrap(out);
+  return true;
+}
+template <typename Call>
+PyObject* launch(int (*fn)(const Call*, void*), const Call& k, const at::Tensor& x,
+                 const at::Tensor& out, const char* what) {
+  return made(fn, k, x, what) ? THPVariable_Wrap(out) : nullptr;
+}
+
+// A tuple of tensors; an undefined one is None.
+PyObject* tuple_of(std::initializer_list<at::Tensor> ts) {
+  PyObject* r = PyTuple_New(static_cast<Py_ssize_t>(ts.size()));
+  if (!r) return nullptr;
+  Py_ssize_t i = 0;
+  for (const at::Tensor& t : ts) {
+    PyObject* o = Py_None;
+    if (t.defined()) o = THPVariable_Wrap(t);
+    else Py_INCREF(o);
+    if (!o) {
+      Py_DECREF(r);
+      return nullptr;
+    }
+    PyTuple_SET_ITEM(r, i++, o);
+  }
+  return r;
+}
+
+// The workspace that a call asks for, from torch's allocator on x's device.
+template <typename Call>
+at::Tensor workspace_for(Call* k, int64_t (*bytes_of)(const Call*), const at::Tensor& x) {
+  c10::cuda::OptionalCUDAGuard guard;
+  if (c10::cuda::current_device() != x.device().index()) guard.set_device(x.device());
+  at::Tensor ws;
+  const int64_t bytes = bytes_of(k);
+  if (bytes > 0) {
+    ws = at::empty({bytes}, x.options().dtype(at::kByte).memory_format(c10::nullopt));
+    k->workspace = ws.data_ptr();
+    k->workspace_bytes = bytes;
+  }
+  return ws;
 }
 
 template <typename F>
@@ -366,6 +472,159 @@ PyObject* py_scan_call(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+PyObject* py_recur(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count_is(n, 11)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    ggrn_recur_call k;
+    const at::Tensor* x;
+    const at::Tensor out = fill_recur(&k, x, a);
+    const bool step = a[10] == Py_True;
+    return launch(step ? ggrn_recur_step : ggrn_recur, k, *x, out,
+                  step ? "ggrn_recur_step" : "ggrn_recur");
+  });
+}
+PyObject* py_recur_call(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count_is(n, 11)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    ggrn_recur_call k;
+    const at::Tensor* x;
+    fill_recur(&k, x, a);
+    return PyBytes_FromStringAndSize(reinterpret_cast<const char*>(&k), sizeof(k));
+  });
+}
+
+// dout, x, input_gate, decay_gate, a, cu_seqlens, state, slots, resume, dstate, saved, dx,
+// dinput_gate, ddecay_gate
+PyObject* py_recur_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count_is(n, 14)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    ggrn_recur_backward_call k;
+    std::memset(&k, 0, sizeof(k));
+    const at::Tensor& x = needed(a[1], "x");
+    if (!x.is_cuda()) refuse("the recurrence runs on CUDA tensors only (no CPU path)");
+    k.dtype = dtype_code(x);
+    if (x.dim() < 2) refuse("x must be [rows, width] or [batch, length, width]");
+    const int64_t width = x.size(-1);
+    rows_of(x, width, "x", &k.rows, &k.x_row_stride);
+    k.x = x.const_data_ptr();
+    k.width = width;
+    k.dout = alike(a[0], x, "dout", &k.dout_row_stride);
+    k.input_gate = alike(a[2], x, "input_gate", &k.input_gate_row_stride);
+    k.decay_gate = alike(a[3], x, "decay_gate", &k.decay_gate_row_stride);
+    needed(a[4], "a");
+    k.a = vector<float>(a[4], width, at::kFloat, x, "a");
+    const int64_t held[1] = {width};
+    fill_seqs(&k, x, a[5], a[6], a[7], a[8], held, at::kFloat, false);
+    k.dstate = vector<float>(a[9], k.seqs * width, at::kFloat, x, "dstate");
+    const int64_t kept = (k.rows + GGRN_RECUR_SAVED_ROWS - 1) / GGRN_RECUR_SAVED_ROWS;
+    k.saved = vector<float>(a[10], kept * width, at::kFloat, x, "saved");
+    const at::Tensor dx = output_rows(a[11], x, "dx", &k.dx, &k.dx_row_stride),
+                     di = output_rows(a[12], x, "dinput_gate", &k.dinput_gate,
+                                      &k.dinput_gate_row_stride),
+                     dr = output_rows(a[13], x, "ddecay_gate", &k.ddecay_gate,
+                                      &k.ddecay_gate_row_stride);
+    const at::Tensor da = new_floats({width}, x);
+    k.da = static_cast<float*>(da.data_ptr());
+    at::Tensor dh;
+    if (k.state) {
+      dh = new_floats({k.seqs, width}, x);
+      k.dinitial = static_cast<float*>(dh.data_ptr());
+    }
+    const at::Tensor ws = workspace_for(&k, ggrn_recur_backward_workspace_bytes, x);
+    if (!made(ggrn_recur_backward, k, x, "ggrn_recur_backward")) return nullptr;
+    return tuple_of({dx, di, dr, da, dh});
+  });
+}
+
+PyObject* py_layer_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count_is(n, 5)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    ggrn_layer_norm_call k;
+    const at::Tensor* x;
+    const at::Tensor out = fill_layer_norm(&k, x, a);
+    return launch(ggrn_layer_norm, k, *x, out, "ggrn_layer_norm");
+  });
+}
+PyObject* py_layer_norm_call(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count_is(n, 5)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    ggrn_layer_norm_call k;
+    const at::Tensor* x;
+    fill_layer_norm(&k, x, a);
+    return PyBytes_FromStringAndSize(reinterpret_cast<const char*>(&k), sizeof(k));
+  });
+}
+
+// dout, x, w, eps, bias, dx
+PyObject* py_layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count_is(n, 6)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    ggrn_layer_norm_backward_call k;
+    std::memset(&k, 0, sizeof(k));
+    const at::Tensor& x = needed(a[1], "x");
+    if (!x.is_cuda()) refuse("layer_norm_backward runs on CUDA tensors only (no CPU path)");
+    k.dtype = dtype_code(x);
+    if (x.dim() < 1) refuse("x must have rank >= 1");
+    k.width = x.size(-1);
+    rows_of(x, k.width, "x", &k.rows, &k.x_row_stride);
+    k.x = x.const_data_ptr();
+    k.dout = alike(a[0], x, "dout", &k.dout_row_stride);
+    needed(a[2], "w");
+    k.w = vector<float>(a[2], k.width, at::kFloat, x, "w");
+    k.eps = static_cast<float>(PyFloat_AsDouble(a[3]));
+    if (PyErr_Occurred()) throw python_error();
+    const at::Tensor dx = output_rows(a[5], x, "dx", &k.dx, &k.dx_row_stride);
+    const at::Tensor dw = new_floats({k.width}, x);
+    k.dw = static_cast<float*>(dw.data_ptr());
+    at::Tensor db;
+    if (PyObject_IsTrue(a[4]) == 1) {
+      db = new_floats({k.width}, x);
+      k.db = static_cast<float*>(db.data_ptr());
+    }
+    const at::Tensor ws = workspace_for(&k, ggrn_layer_norm_backward_workspace_bytes, x);
+    if (!made(ggrn_layer_norm_backward, k, x, "ggrn_layer_norm_backward")) return nullptr;
+    return tuple_of({dx, dw, db});
+  });
+}
+
+// dout, y, gate, w, group_size, eps, mode, dy, dgate
+PyObject* py_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count_is(n, 9)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    ggrn_backward_call k;
+    std::memset(&k, 0, sizeof(k));
+    const at::Tensor& y = needed(a[1], "y");
+    if (!y.is_cuda()) refuse("backward runs on CUDA tensors only (no CPU path)");
+    k.dtype = dtype_code(y);
+    if (y.dim() < 1) refuse("y must have rank >= 1");
+    k.width = y.size(-1);
+    k.group_size = PyLong_AsLongLong(a[4]);
+    k.eps = static_cast<float>(PyFloat_AsDouble(a[5]));
+    k.mode = static_cast<int32_t>(PyLong_AsLong(a[6]));
+    if (PyErr_Occurred()) throw python_error();
+    rows_of(y, k.width, "y", &k.rows, &k.y_row_stride);
+    k.y = y.const_data_ptr();
+    k.dout = alike(a[0], y, "dout", &k.dout_row_stride, "y");
+    k.gate = alike(a[2], y, "gate", &k.gate_row_stride, "y");
+    const bool onnx = k.mode == GGRN_MODE_ONNX;
+    const at::Tensor& w0 = needed(a[3], "w");
+    const int64_t columns = onnx ? k.group_size : k.width;
+    const at::ScalarType wt = onnx ? y.scalar_type() : at::kFloat;
+    if (w0.scalar_type() != wt || w0.numel() != columns || w0.device() != y.device())
+      refuse(onnx ? "ONNX scale has the dtype of X and group_size elements"
+                  : "MAMBA2 weight is float32 with `width` elements");
+    const at::Tensor w = w0.contiguous();
+    k.w = w.const_data_ptr();
+    const at::Tensor dy = output_rows(a[7], y, "dy", &k.dy, &k.dy_row_stride, "y"),
+                     dgate = output_rows(a[8], y, "dgate", &k.dgate, &k.dgate_row_stride, "y");
+    const at::Tensor dw = new_floats(w0.sizes(), y);
+    k.dw = static_cast<float*>(dw.data_ptr());
+    const at::Tensor ws = workspace_for(&k, ggrn_backward_workspace_bytes, y);
+    if (!made(ggrn_backward, k, y, "ggrn_backward")) return nullptr;
+    return tuple_of({dy, dgate, dw});
+  });
+}
+
 PyObject* py_rows_of(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!count_is(n, 3)) return nullptr;
   return guarded([&]() -> PyObject* {
@@ -388,6 +647,13 @@ PyMethodDef kMethods[] = {{"conv", FAST(py_conv), nullptr},
                           {"scan_workspace_bytes", FAST(py_scan_workspace), nullptr},
                           {"conv_call", FAST(py_conv_call), nullptr},
                           {"scan_call", FAST(py_scan_call), nullptr},
+                          {"recur", FAST(py_recur), nullptr},
+                          {"recur_call", FAST(py_recur_call), nullptr},
+                          {"recur_backward", FAST(py_recur_backward), nullptr},
+                          {"layer_norm", FAST(py_layer_norm), nullptr},
+                          {"layer_norm_call", FAST(py_layer_norm_call), nullptr},
+                          {"layer_norm_backward", FAST(py_layer_norm_backward), nullptr},
+                          {"norm_backward", FAST(py_norm_backward), nullptr},
                           {"rows_of", FAST(py_rows_of), nullptr},
                           {"on_error", py_on_error, METH_O, nullptr},
                           {nullptr, nullptr, 0, nullptr}};

@@ -550,14 +550,180 @@ int64_t ggrn_scan_workspace_bytes(const ggrn_scan_call* call);
  */
 int ggrn_selftest_scan_timeout(const ggrn_scan_call* call, void* cuda_stream);
 
+/* --------------------------------------------------------------------------
+ * The gated linear recurrence: a state of one number a channel, for mixers that
+ * take it in the place of the scan.  T in {f32, f16, bf16}; per channel c and
+ * row t of a sequence, with r = sigmoid(decay_gate[t,c]), i = sigmoid(input_gate[t,c]):
+ *     p[t] = a[c] * r                       (a <= 0)
+ *     h[t] = exp(p[t]) * h[t-1] + sqrt(1 - exp(2 p[t])) * i * x[t,c]
+ *     out  = cast_T(h[t])
+ * Sequences, states (f32 [width] entries of the pool), the step form, memory,
+ * streams and errors are those of the convolution and the scan above.  All
+ * arithmetic and every state is f32; an output is rounded to T once.
+ *
+ * Backward pass.  With g[t] the gradient of h[t],
+ *     g[t] = dout[t] + exp(p[t+1]) g[t+1]   (after the last row: dstate)
+ * it gives the gradients of x, of both gates' logits (T; zeros in rows of no
+ * sequence), of a (f32, summed over all rows) and of the state that each
+ * sequence starts from (f32; zeros where it starts from none).  At p = 0 the
+ * root's slope is infinite, but not that of the gates' logits, which is 0.
+ *
+ * Values that are not finite reach only what depends on them; an infinite state
+ * whose decay over a tile of 64 rows is zero in f32 may become a NaN.  16-bit T:
+ * a gate whose sigmoid is below 2^-126 is closed.
+ * -------------------------------------------------------------------------- */
+#define GGRN_RECUR_SAVED_ROWS 64
+
+typedef struct {
+  const void* x;              /* T [rows, width] */
+  const void* input_gate;     /* T [rows, width], logits */
+  const void* decay_gate;     /* T [rows, width], logits */
+  const float* a;             /* [width], finite, <= 0 */
+  void* out;                  /* T [rows, width] */
+  float* state;               /* f32, or NULL (not in the step form) */
+  const int32_t* slots;
+  const uint8_t* resume;
+  const int32_t* cu_seqlens;
+  float* saved;               /* [ceil(rows / GGRN_RECUR_SAVED_ROWS), width], or NULL: receives
+                                 the state before rows 0, 64, 128, .. for the backward pass
+                                 (entries of rows of no sequence have no meaning) */
+  int64_t rows, seqs, width;
+  int64_t x_row_stride, input_gate_row_stride, decay_gate_row_stride, out_row_stride;
+  int64_t state_slots, state_slot_stride;
+  int32_t dtype;              /* ggrn_dtype of x, both gates and out */
+} ggrn_recur_call;
+
+typedef struct {
+  const void* dout;           /* T [rows, width]: the gradient of out */
+  const void* x;              /* these and the sequences as in the forward call */
+  const void* input_gate;
+  const void* decay_gate;
+  const float* a;
+  void* dx;                   /* T [rows, width] */
+  void* dinput_gate;          /* T [rows, width] */
+  void* ddecay_gate;          /* T [rows, width] */
+  float* da;                  /* [width] */
+  float* dinitial;            /* [seqs, width], or NULL */
+  const float* dstate;        /* [seqs, width]: the gradient of the state after each sequence's
+                                 last row (of an empty one: of its first state), or NULL (0) */
+  const float* state;         /* the pool as it was before the forward call, or NULL */
+  const int32_t* slots;
+  const uint8_t* resume;
+  const int32_t* cu_seqlens;
+  const float* saved;         /* what the forward call kept, or NULL: made again */
+  void* workspace;            /* DEVICE, 16-byte aligned */
+  int64_t workspace_bytes;
+  int64_t rows, seqs, width;
+  int64_t dout_row_stride, x_row_stride, input_gate_row_stride, decay_gate_row_stride;
+  int64_t dx_row_stride, dinput_gate_row_stride, ddecay_gate_row_stride;
+  int64_t state_slots, state_slot_stride;
+  int32_t dtype;
+} ggrn_recur_backward_call;
+
+/*
+ * ggrn_recur / ggrn_recur_step / ggrn_recur_backward -- the recurrence over
+ * prompts, over one row of each sequence, and its gradients.  Statuses of
+ * ggrn_conv; GGRN_ERR_UNSUPPORTED for more than 2097120 columns.  Outputs may
+ * overlap no other buffer.  Calls of the backward pass that may run at the same
+ * time need workspaces of their own, those of captured graphs included.
+ */
+int ggrn_recur(const ggrn_recur_call* call, void* cuda_stream);
+int ggrn_recur_step(const ggrn_recur_call* call, void* cuda_stream);
+int ggrn_recur_backward(const ggrn_recur_backward_call* call, void* cuda_stream);
+
+/* Workspace bytes of ggrn_recur_backward for this call (only its sizes and
+ * whether cu_seqlens and saved are NULL are looked at): 0 where none is needed
+ * or the call is invalid. */
+int64_t ggrn_recur_backward_workspace_bytes(const ggrn_recur_backward_call* call);
+
+/* --------------------------------------------------------------------------
+ * Layer norm, and the backward passes of the norms.  f32 arithmetic, an output
+ * rounded to T once; gradients of weights are f32 sums in a fixed order.
+ *   layer norm: xh = (x - mean(x)) * rsqrt(mean((x - mean(x))^2) + eps) over a row,
+ *               out = cast_T(xh * w + b);  T in {f32, f16, bf16}
+ *     u = dout * w, dx = rsqrt(..) * (u - mean(u) - xh * mean(u * xh)),
+ *     dw = sum over rows of dout * xh, db = sum over rows of dout
+ *   gated group-RMSNorm: the gradients of ggrn_forward in both modes, with the
+ *     groups, weights and dtypes of that call.  MAMBA2's cast of gated * nf to T
+ *     is differentiated as the identity.  dw is f32: [width] (MAMBA2),
+ *     [group_size] (ONNX: summed over rows and groups).
+ * Memory, streams and errors are those of ggrn_forward; outputs may overlap no
+ * other buffer.  rows == 0 gives dw and db of zeros.
+ * -------------------------------------------------------------------------- */
+typedef struct {
+  const void* x;              /* T [rows, width], row stride x_row_stride */
+  const float* w;             /* [width] */
+  const float* b;             /* [width], or NULL (0) */
+  void* out;                  /* T [rows, width], row stride out_row_stride */
+  int64_t rows, width;
+  int64_t x_row_stride, out_row_stride;
+  float eps;
+  int32_t dtype;
+} ggrn_layer_norm_call;
+
+typedef struct {
+  const void* dout;           /* T [rows, width] */
+  const void* x;              /* T [rows, width] */
+  const float* w;             /* [width] */
+  void* dx;                   /* T [rows, width] */
+  float* dw;                  /* [width] */
+  float* db;                  /* [width], or NULL (not wanted) */
+  void* workspace;            /* DEVICE, 16-byte aligned */
+  int64_t workspace_bytes;
+  int64_t rows, width;
+  int64_t dout_row_stride, x_row_stride, dx_row_stride;
+  float eps;
+  int32_t dtype;
+} ggrn_layer_norm_backward_call;
+
+typedef struct {
+  const void* dout;           /* T [rows, width] */
+  const void* y;              /* T [rows, width] */
+  const void* gate;           /* T [rows, width] */
+  const void* w;              /* as in ggrn_forward */
+  void* dy;                   /* T [rows, width] */
+  void* dgate;                /* T [rows, width] */
+  float* dw;                  /* MAMBA2: [width]; ONNX: [group_size] */
+  void* workspace;            /* DEVICE, 16-byte aligned */
+  int64_t workspace_bytes;
+  int64_t rows, width, group_size;
+  int64_t dout_row_stride, y_row_stride, gate_row_stride, dy_row_stride, dgate_row_stride;
+  float eps;
+  int32_t dtype, mode;
+} ggrn_backward_call;
+
+/*
+ * ggrn_layer_norm / ggrn_layer_norm_backward / ggrn_backward.  Statuses of
+ * ggrn_forward; GGRN_ERR_ARG also for a workspace too small or a NULL call.  The
+ * workspace holds the partial sums of the weights' gradients; calls that may run
+ * at the same time need workspaces of their own, those of captured graphs
+ * included.
+ */
+int ggrn_layer_norm(const ggrn_layer_norm_call* call, void* cuda_stream);
+int ggrn_layer_norm_backward(const ggrn_layer_norm_backward_call* call, void* cuda_stream);
+int ggrn_backward(const ggrn_backward_call* call, void* cuda_stream);
+
+/* Workspace bytes of the two (only sizes, dtype and mode are looked at): 0 where
+ * none is needed or the call is invalid. */
+int64_t ggrn_layer_norm_backward_workspace_bytes(const ggrn_layer_norm_backward_call* call);
+int64_t ggrn_backward_workspace_bytes(const ggrn_backward_call* call);
+
 /* One call of a decode chain that is not only norms. */
-typedef enum { GGRN_STEP_FORWARD = 0, GGRN_STEP_CONV = 1, GGRN_STEP_SCAN = 2 } ggrn_step_kind;
+typedef enum {
+  GGRN_STEP_FORWARD = 0,
+  GGRN_STEP_CONV = 1,
+  GGRN_STEP_SCAN = 2,
+  GGRN_STEP_RECUR = 3,
+  GGRN_STEP_LAYER_NORM = 4
+} ggrn_step_kind;
 typedef struct {
   int32_t kind;              /* ggrn_step_kind: which member of `u` */
   union {
     ggrn_call forward;       /* ggrn_forward */
     ggrn_conv_call conv;     /* ggrn_conv_step */
     ggrn_scan_call scan;     /* ggrn_scan_step */
+    ggrn_recur_call recur;   /* ggrn_recur_step */
+    ggrn_layer_norm_call layer_norm; /* ggrn_layer_norm */
   } u;
 } ggrn_step;
 
