@@ -37,22 +37,22 @@ Plan plan(int kind, int es, int64_t rows, int64_t groups, int64_t gs, int elems)
   Plan k;
   k.elems = elems;
   const int64_t nvec = gs / elems;
-  if (nvec <= 32) {
-    // several groups to a warp, 256 threads to a CTA
-    int lanes = 1;
-    while (lanes < nvec) lanes <<= 1;
+  int lanes = 1;
+  while (lanes < 32 && lanes * 4 < nvec) lanes <<= 1;
+  if (nvec <= lanes * 4) {
+    // several groups to a CTA
+    k.vpl = nvec <= 1 ? 1 : nvec <= 2 * lanes ? 2 : 4;
     k.threads = 256;
     k.lanes = lanes;
     const int teams = k.threads / lanes;
     k.team_groups = static_cast<int>(groups < teams ? groups : teams);
     k.team_rows = teams / k.team_groups;
   } else {
-    // a CTA to a group, with the fewest vectors a thread that it can hold
+    // a CTA to a group
     k.vpl = 0;
     for (int v : {1, 2, 4}) {
-      if (v == 2 && elems * es != 16) continue;
       const int64_t threads = ((nvec + v - 1) / v + 31) / 32 * 32;
-      if (threads > kMaxThreads) continue;
+      if (threads > threads_of(v)) continue;
       k.vpl = v;
       k.threads = static_cast<int>(threads);
       break;
@@ -63,18 +63,25 @@ Plan plan(int kind, int es, int64_t rows, int64_t groups, int64_t gs, int elems)
   k.nvec = static_cast<int>(k.vpl ? nvec : 0);
   k.blocks = (groups + k.team_groups - 1) / k.team_groups;
   const int64_t sms = device_sms();
-  const int64_t resident = (k.vpl == 1 ? 1024 : k.vpl == 0 ? 2048 : 512) / k.threads;
-  const int64_t turn = static_cast<int64_t>(k.team_rows) *
-                       (k.vpl ? rows_ahead(es, elems, k.vpl) : 1);
-  const int64_t most = (rows + turn - 1) / turn;
-  k.slices = (sms * resident + k.blocks - 1) / k.blocks;
+  int64_t resident = 2048 / k.threads;
+  if (k.vpl) {
+    resident = static_cast<int64_t>(resident_of(k.vpl)) * threads_of(k.vpl) / k.threads;
+    const int row = inputs_of(kind) * k.vpl * k.threads * elems * es;
+    if (resident > 8) resident = 8;
+    // rows of copies in flight: what is left of an SM's shared memory
+    int64_t depth = (200 << 10) / resident / row;
+    k.depth = static_cast<int>(depth > kMaxDepth ? kMaxDepth : depth < 2 ? 2 : depth);
+    k.smem = k.depth * row;
+  }
+  const int64_t most = (rows + k.team_rows - 1) / k.team_rows;
+  k.slices = (sms * resident) / k.blocks;
   if (k.slices > most) k.slices = most;
   if (k.slices < 1) k.slices = 1;
   if (kind != kLayerNorm) {
     k.sums = kind == kOnnxGrad ? k.slices * k.blocks : k.slices;
     k.columns = kind == kOnnxGrad ? gs : groups * gs;
-    const int teams = kind == kOnnxGrad ? k.team_rows * k.team_groups : k.team_rows;
-    if (teams > 1) k.smem = k.threads * k.elems * k.vpl * 4;
+    const int acc = k.threads * k.elems * k.vpl * 4;  // (the ring's place, at the end)
+    if (k.smem < acc) k.smem = acc;
   }
   return k;
 }
@@ -125,6 +132,7 @@ int launch(int kind, int dtype, Params& p, const Plan& k, void* workspace, float
   p.team_groups = k.team_groups;
   p.team_rows = k.team_rows;
   p.nvec = k.nvec;
+  p.depth = k.depth;
   p.gs_f = static_cast<float>(p.gs);
   float* const sums = static_cast<float*>(workspace);
   p.dw = k.sums > 1 ? sums : dw;
