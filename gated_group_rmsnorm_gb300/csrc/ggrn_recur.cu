@@ -26,6 +26,7 @@
 #include <type_traits>
 
 #include "ggrn_mixer.cuh"
+#include "ggrn_optin.h"
 
 namespace ggrn {
 namespace recur {
@@ -48,6 +49,8 @@ struct Params {
   int64_t slot_stride, width;
   int segments;
   int keep_state;
+  int chunk;           // bytes that the inputs' rows can be copied by: 16, 4, or an element
+  int pairs;           // outputs' rows can be stored by pairs of channels
 };
 
 // V consecutive channels of T as they lie in memory.
@@ -180,28 +183,48 @@ __device__ __forceinline__ void cluster_arrive() {
 __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
-// Stores a pair at the place of *mine in the shared memory of CTA `rank`.
-__device__ __forceinline__ void put_peer(const float2* mine, uint32_t rank, float2 v) {
+__device__ __forceinline__ void put_peer_int(const int* mine, uint32_t rank, int v) {
   const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(mine));
   asm volatile(
       "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\t"
-      "st.shared::cluster.v2.f32 [a], {%2, %3};\n\t}" ::"r"(at),
-      "r"(rank), "f"(v.x), "f"(v.y)
+      "st.shared::cluster.u32 [a], %2;\n\t}" ::"r"(at),
+      "r"(rank), "r"(v)
+      : "memory");
+}
+// Stores v at the place of *mine in the shared memory of CTA `rank`.
+__device__ __forceinline__ void put_peer(const float4* mine, uint32_t rank, float4 v) {
+  const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(mine));
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\t"
+      "st.shared::cluster.v4.f32 [a], {%2, %3, %4, %5};\n\t}" ::"r"(at),
+      "r"(rank), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
       : "memory");
 }
 
 // ---------------------------------------------------------------------------
-// Pairs (E, B): v -> E v + B.  Where a sequence starts (or, for gradients, ends)
-// among the rows of a pair, nothing comes in from before them: E is kCut.
+// Pairs (E, B): v -> E v + B, of a lane's two channels as (E0, E1, B0, B1).  Where
+// a sequence starts (or, for gradients, ends) among the rows of a pair, nothing
+// comes in from before them: E is kCut.  (Not 0: a value that is not finite would
+// leave its sequence.)  CUTS: some pair may be cut.
 // ---------------------------------------------------------------------------
 constexpr float kCut = -1.0f;  // (decays are not negative)
-__device__ __forceinline__ float through(float2 s, float v) {
-  return s.x == kCut ? s.y : fmaf(s.x, v, s.y);
+template <bool CUTS>
+__device__ __forceinline__ void through(const float4& s, float (&v)[2]) {
+  if (CUTS && s.x == kCut) {
+    v[0] = s.z, v[1] = s.w;
+  } else {
+    fma2(v[0], v[1], s.x, s.y, v[0], v[1], s.z, s.w);
+  }
 }
-// First `s`, then `t`.
-__device__ __forceinline__ float2 compose(float2 s, float2 t) {
-  if (t.x == kCut) return t;
-  return make_float2(s.x == kCut ? kCut : s.x * t.x, fmaf(t.x, s.y, t.y));
+// s: first s, then t.
+template <bool CUTS>
+__device__ __forceinline__ void compose(float4& s, const float4& t) {
+  if (CUTS && t.x == kCut) {
+    s = t;
+    return;
+  }
+  fma2(s.z, s.w, t.x, t.y, s.z, s.w, t.z, t.w);
+  if (!CUTS || s.x != kCut) mul2(s.x, s.y, s.x, s.y, t.x, t.y);
 }
 
 // ---------------------------------------------------------------------------
@@ -209,6 +232,7 @@ __device__ __forceinline__ float2 compose(float2 s, float2 t) {
 // ---------------------------------------------------------------------------
 struct TileRows {
   uint32_t in[2], first[2], last[2];  // bits of the tile's rows
+  int64_t begin, end;                 // rows of the sequence of the tile's last row
   int seq[kTile];
 };
 
@@ -235,8 +259,8 @@ __device__ __forceinline__ void place_rows(const Seqs& q, int64_t tile, int64_t 
                                            TileRows* t) {
   const int64_t r = tile * kTile + threadIdx.x;
   bool in = false, first = false, last = false;
+  int64_t begin = 0, end = 0;
   if (r >= lo && r < hi) {
-    int64_t begin, end;
     const int64_t s = seq_of_row(q, r, begin, end);
     in = r >= begin && r < end;
     first = in && r == begin;
@@ -250,7 +274,18 @@ __device__ __forceinline__ void place_rows(const Seqs& q, int64_t tile, int64_t 
     t->first[threadIdx.x >> 5] = bf;
     t->last[threadIdx.x >> 5] = bl;
   }
+  if (threadIdx.x == kTile - 1) t->begin = begin, t->end = end;
 }
+
+// What a CTA knows of its tiles' rows: those inside the sequence that it found
+// last need no search.
+struct Rows {
+  int64_t begin = 0, end = 0;  // of that sequence
+  // Whether tile `t` is whole, lies in it, and holds neither end of it.
+  __device__ __forceinline__ bool inside(int64_t t) const {
+    return t * kTile > begin && (t + 1) * kTile < end;
+  }
+};
 
 // Rows [lo, hi) of segment z: cut where the first sequence begins that does so
 // at or behind the z-th of `segments` equal shares of the rows.
@@ -286,6 +321,15 @@ __device__ __forceinline__ bool start_state(const Params& p, int64_t s, int64_t 
   return resumes;
 }
 
+// Adds to g what comes to the last row of sequence s from the state behind it.
+__device__ __forceinline__ void end_gradient(const Params& p, int64_t s, int64_t c, int n,
+                                             float* g) {
+  if (!p.dstate) return;
+#pragma unroll
+  for (int v = 0; v < 2; ++v)
+    if (v < n) g[v] += __ldg(p.dstate + s * p.width + c + v);
+}
+
 // Empty sequences among those of this CTA (every `of`-th 32 from the `at`-th):
 // calls f(sequence) with the whole warp.
 template <typename F>
@@ -300,159 +344,258 @@ __device__ __forceinline__ void each_empty(const Seqs& q, int64_t at, int64_t of
 }
 
 // ---------------------------------------------------------------------------
-// Prompts.
+// Tiles in shared memory: 64 rows of 64 channels of each input.
 // ---------------------------------------------------------------------------
-template <typename T, int V>
-__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) k_recur(const Params p) {
-  constexpr int W = 8, R = kTile / W, N = R * V, C = 32 * V;
-  __shared__ float2 s_warp[W][C];
-  __shared__ float2 s_peer[2][kMaxCluster][C];
-  __shared__ TileRows s_rows[2];
+constexpr int kCols = 64;
+
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t to, const void* from, int bytes) {
+  if constexpr (BYTES == 16) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes)
+                 : "memory");
+  } else {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(bytes)
+                 : "memory");
+  }
+}
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// The CTA's threads start to copy tile `tile` of one input into `to`; rows
+// outside [lo, hi) and channels behind the last one become zeros.
+template <typename T, int THREADS>
+__device__ __forceinline__ void copy_tile(T* to, const void* base, int64_t stride, int64_t c0,
+                                          int64_t width, int64_t tile, int64_t lo, int64_t hi,
+                                          int chunk) {
+  constexpr int ES = sizeof(T);
+  const T* from = static_cast<const T*>(base) + c0;
+  const int64_t r0 = tile * kTile;
+  const int cols = static_cast<int>(width - c0 < kCols ? width - c0 : kCols);
+  const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(to));
+  if (chunk == 16) {
+    constexpr int E = 16 / ES, ROW = kCols / E;  // chunks of a row
+    const int c = static_cast<int>(threadIdx.x) % ROW * E;
+    const int row0 = static_cast<int>(threadIdx.x) / ROW;
+    const T* p = from + (r0 + row0) * stride + c;
+#pragma unroll
+    for (int k = 0; k < kTile * ROW / THREADS; ++k) {
+      const int row = row0 + k * (THREADS / ROW);
+      const bool ok = r0 + row >= lo && r0 + row < hi && c < cols;
+      copy_async<16>(at + (row * kCols + c) * ES, ok ? p : from, ok ? 16 : 0);
+      p += (THREADS / ROW) * stride;
+    }
+  } else if (chunk == 4) {
+    constexpr int E = 4 / ES, ROW = kCols / E;
+#pragma unroll 4
+    for (int k = threadIdx.x; k < kTile * ROW; k += THREADS) {
+      const int row = k / ROW, c = k % ROW * E;
+      const bool ok = r0 + row >= lo && r0 + row < hi && c < cols;
+      copy_async<4>(at + (row * kCols + c) * ES, ok ? from + (r0 + row) * stride + c : from,
+                    !ok ? 0 : cols - c < E ? ES : 4);
+    }
+  } else {
+#pragma unroll 4
+    for (int k = threadIdx.x; k < kTile * kCols; k += THREADS) {
+      const int row = k / kCols, c = k % kCols;
+      T v;
+      Elem<T>::store1(&v, 0, 0.0f);
+      if (r0 + row >= lo && r0 + row < hi && c < cols) v = from[(r0 + row) * stride + c];
+      to[k] = v;
+    }
+  }
+}
+
+// A lane's two channels of a row in shared memory.
+template <typename T>
+__device__ __forceinline__ void get2(const T* p, float* f) {
+  if constexpr (sizeof(T) == 4) {
+    const float2 v = *reinterpret_cast<const float2*>(p);
+    f[0] = v.x, f[1] = v.y;
+  } else {
+    Elem<T>::unpack2(*reinterpret_cast<const uint32_t*>(p), f[0], f[1]);
+  }
+}
+// Stores the first `cols` of two channels.
+template <typename T>
+__device__ __forceinline__ void put2(void* base, int64_t at, const float* f, int cols, bool pairs) {
+  T* p = static_cast<T*>(base) + at;
+  if (pairs && cols == 2) {
+    Raw<T, 2>::put(p, f);
+  } else {
+    if (cols > 0) Elem<T>::store1(p, 0, f[0]);
+    if (cols > 1) Elem<T>::store1(p, 1, f[1]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Prompts.  Eight warps of eight rows each.
+// ---------------------------------------------------------------------------
+constexpr int kThreads = 256, W = kThreads / 32, R = kTile / W;
+static_assert(W >= kMaxCluster, "a warp to each CTA that the tile's pair goes to");
+
+struct ForwardShared {
+  float4 pair[W][32];
+  float4 peer[2][kMaxCluster][32];
+  int cut[2][kMaxCluster];
+  TileRows rows;
+};
+
+// e and b of the warp's rows, and the pair of all of them.  INSIDE: all rows are
+// those of one sequence, neither its first nor its last.
+template <typename T, bool INSIDE, bool FAST>
+__device__ __forceinline__ void forward_rows(const Params& p, const T* tile, const float (&ac)[2],
+                                             const TileRows& t, int64_t c, int cols,
+                                             float (&e)[R][2], float (&b)[R][2], float4& s) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const T* mine = tile + warp * R * kCols + lane * 2;
+  s = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
+#pragma unroll
+  for (int j = 0; j < R; ++j) {
+    float x[2], gi[2], gr[2], m[2];
+    get2(mine + j * kCols, x);
+    get2(mine + (kTile + j) * kCols, gi);
+    get2(mine + (2 * kTile + j) * kCols, gr);
+    sigmoid2<T>(gi, gi);
+    sigmoid2<T>(gr, gr);
+    decay2<T, FAST>(gr, ac[0], ac[1], e[j], m);
+    mul2(m[0], m[1], m[0], m[1], gi[0], gi[1]);
+    mul2(b[j][0], b[j][1], m[0], m[1], x[0], x[1]);
+    if constexpr (!INSIDE) {
+      const int row = warp * R + j;
+      if (!(t.in[row >> 5] >> (row & 31) & 1)) {
+        e[j][0] = e[j][1] = 1.0f;
+        b[j][0] = b[j][1] = 0.0f;
+      }
+      if (t.first[row >> 5] >> (row & 31) & 1) {
+        float h[2];
+        if (start_state<2>(p, t.seq[row], c, cols, h))
+          fma2(b[j][0], b[j][1], e[j][0], e[j][1], h[0], h[1], b[j][0], b[j][1]);
+        e[j][0] = e[j][1] = kCut;
+      }
+    }
+    compose<!INSIDE>(s, make_float4(e[j][0], e[j][1], b[j][0], b[j][1]));
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) k_recur(const Params p) {
+  extern __shared__ uint4 s_tile[];
+  __shared__ ForwardShared sh;
+  T* const tile_of = reinterpret_cast<T*>(s_tile);  // x, input gate, decay gate
   pdl_wait();
   pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_rank(), size = cluster_size();
-  const int64_t c = (static_cast<int64_t>(blockIdx.y) * 32 + lane) * V;
-  const int cols = c >= p.width ? 0 : static_cast<int>(p.width - c < V ? p.width - c : V);
-  float ac[V];
-  bool fast = true;
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    ac[v] = v < cols ? __ldg(p.a + c + v) : 0.0f;
-    fast = fast && ac[v] > kSeries;
-  }
-  fast = __all_sync(0xffffffffu, fast);
+  const int rank = static_cast<int>(cluster_rank()), size = static_cast<int>(cluster_size());
+  const int64_t c0 = static_cast<int64_t>(blockIdx.y) * kCols, c = c0 + lane * 2;
+  const int cols = c >= p.width ? 0 : p.width - c < 2 ? 1 : 2;
+  if (size > 1) cluster_arrive();  // (every CTA has begun before another one writes to it)
   const int64_t lo = segment_begin(p, blockIdx.z), hi = segment_begin(p, blockIdx.z + 1);
   const int64_t tile0 = lo / kTile, tiles = hi > lo ? (hi + kTile - 1) / kTile - tile0 : 0;
   const int64_t turns = (tiles + size - 1) / size;
-
-  const T* x = static_cast<const T*>(p.x) + c;
-  const T* ig = static_cast<const T*>(p.ig) + c;
-  const T* rg = static_cast<const T*>(p.rg) + c;
-  T* out = static_cast<T*>(p.out) + c;
-  Raw<T, V> xr[R], ir[R], rr[R];
-  auto fetch = [&](int64_t tile) {
-#pragma unroll
-    for (int j = 0; j < R; ++j) {
-      const int64_t r = tile * kTile + warp * R + j;
-      if (cols == V && r >= lo && r < hi) {
-        xr[j].load(x + r * p.xs);
-        ir[j].load(ig + r * p.is);
-        rr[j].load(rg + r * p.rs);
-      } else {
-        xr[j].clear(), ir[j].clear(), rr[j].clear();
-      }
-    }
-    if (threadIdx.x < kTile) place_rows(p.q, tile, lo, hi, &s_rows[(tile - tile0) / size & 1]);
+  const auto fetch = [&](int64_t tile) {
+    copy_tile<T, kThreads>(tile_of, p.x, p.xs, c0, p.width, tile, lo, hi, p.chunk);
+    copy_tile<T, kThreads>(tile_of + kTile * kCols, p.ig, p.is, c0, p.width, tile, lo, hi, p.chunk);
+    copy_tile<T, kThreads>(tile_of + 2 * kTile * kCols, p.rg, p.rs, c0, p.width, tile, lo, hi,
+                           p.chunk);
   };
-
-  float carry[V] = {};  // the state before the cluster's tiles
-  cluster_arrive();     // (every CTA has begun before another one writes to it)
   if (turns > 0) fetch(tile0 + rank);
-  cluster_wait();
+  float ac[2];
+#pragma unroll
+  for (int v = 0; v < 2; ++v) ac[v] = v < cols ? __ldg(p.a + c + v) : 0.0f;
+  const bool fast = __all_sync(0xffffffffu, ac[0] > kSeries && ac[1] > kSeries);
+  if (size > 1) cluster_wait();
+
+  float carry[2] = {0.0f, 0.0f};  // the state before the cluster's tiles
+  Rows known;
   for (int64_t turn = 0; turn < turns; ++turn) {
     const int64_t tile = tile0 + turn * size + rank;
     const int buf = turn & 1;
-    __syncthreads();
-    const int shift = warp * R & 31;
-    const uint32_t in = s_rows[buf].in[warp * R >> 5] >> shift,
-                   first = s_rows[buf].first[warp * R >> 5] >> shift,
-                   last = s_rows[buf].last[warp * R >> 5] >> shift;
-
-    // e and b of each row, and the pair of all of them
-    float e[N], b[N];
-    {
-      float xf[N], m[N], gi[N], gr[N];
-#pragma unroll
-      for (int j = 0; j < R; ++j) {
-        xr[j].get(xf + j * V), ir[j].get(gi + j * V), rr[j].get(gr + j * V);
-      }
-#pragma unroll
-      for (int k = 0; k < N; k += 2) {
-        sigmoid2<T>(gi + k, gi + k);
-        sigmoid2<T>(gr + k, gr + k);
-        if (fast) decay2<T, true>(gr + k, ac[0], ac[V - 1], e + k, m + k);
-        else decay2<T, false>(gr + k, ac[0], ac[V - 1], e + k, m + k);
-        mul2(b[k], b[k + 1], m[k], m[k + 1], gi[k], gi[k + 1]);
-        mul2(b[k], b[k + 1], b[k], b[k + 1], xf[k], xf[k + 1]);
-      }
-    }
-    float2 s[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) s[v] = make_float2(1.0f, 0.0f);
-#pragma unroll
-    for (int j = 0; j < R; ++j) {
-      if (!(in >> j & 1)) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) e[j * V + v] = 1.0f, b[j * V + v] = 0.0f;
-      }
-      if (first >> j & 1) {
-        float h0[V];
-        if (start_state<V>(p, s_rows[buf].seq[warp * R + j], c, cols, h0)) {
-#pragma unroll
-          for (int v = 0; v < V; ++v) b[j * V + v] = fmaf(e[j * V + v], h0[v], b[j * V + v]);
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v) s[v] = make_float2(kCut, b[j * V + v]);
-      } else {
-#pragma unroll
-        for (int v = 0; v < V; ++v) s[v] = compose(s[v], make_float2(e[j * V + v], b[j * V + v]));
-      }
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) s_warp[warp][lane * V + v] = s[v];
+    const bool inside = known.inside(tile) && (tile + 1) * kTile <= hi;
+    if (!inside && threadIdx.x < kTile) place_rows(p.q, tile, lo, hi, &sh.rows);
+    copies_wait();
     __syncthreads();
 
-    // the tile's pair, to every CTA of the cluster
-    {
-      const int ch = threadIdx.x % C;
-      float2 t = s_warp[0][ch];
-#pragma unroll
-      for (int w = 1; w < W; ++w) t = compose(t, s_warp[w][ch]);
-      for (uint32_t k = threadIdx.x / C; k < size; k += blockDim.x / C)
-        put_peer(&s_peer[buf][rank][ch], k, t);
+    float e[R][2], b[R][2];
+    float4 s;
+    if (inside) {
+      if (fast) forward_rows<T, true, true>(p, tile_of, ac, sh.rows, c, cols, e, b, s);
+      else forward_rows<T, true, false>(p, tile_of, ac, sh.rows, c, cols, e, b, s);
+    } else {
+      forward_rows<T, false, false>(p, tile_of, ac, sh.rows, c, cols, e, b, s);
     }
-    cluster_arrive();
+    sh.pair[warp][lane] = s;
+    const bool cut = !inside && (sh.rows.first[0] | sh.rows.first[1]) != 0;
+    const uint32_t in = inside ? ~0u : sh.rows.in[warp * R >> 5] >> (warp * R & 31),
+                   last = inside ? 0u : sh.rows.last[warp * R >> 5] >> (warp * R & 31);
+    if (!inside) known.begin = sh.rows.begin, known.end = sh.rows.end;
+    __syncthreads();
     if (turn + 1 < turns) fetch(tile + size);
-    cluster_wait();
 
-    // the state before this warp's rows
-    float h[V];
-    for (uint32_t k = 0; k < size; ++k) {
-      if (k == rank) {
+    // the pair of the rows before this warp's in the tile, and of the whole tile
+    float4 before, whole = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
+    const auto fold = [&](auto cuts) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) h[v] = carry[v];
+      for (int w = 0; w < W; ++w) {
+        if (w == warp) before = whole;
+        compose<decltype(cuts)::value>(whole, sh.pair[w][lane]);
       }
-#pragma unroll
-      for (int v = 0; v < V; ++v) carry[v] = through(s_peer[buf][k][lane * V + v], carry[v]);
+    };
+    if (cut) fold(std::true_type());
+    else fold(std::false_type());
+    float h[2];
+    bool cuts = cut;
+    if (size > 1) {
+      if (warp < size) {
+        put_peer(&sh.peer[buf][rank][lane], warp, whole);
+        if (lane == 0) put_peer_int(&sh.cut[buf][rank], warp, cut);
+      }
+      cluster_arrive();
+      cluster_wait();
+      for (int k = 0; k < size; ++k) cuts = cuts || sh.cut[buf][k] != 0;
+      const auto pass = [&](auto some) {
+        for (int k = 0; k < size; ++k) {
+          if (k == rank) h[0] = carry[0], h[1] = carry[1];
+          through<decltype(some)::value>(sh.peer[buf][k][lane], carry);
+        }
+      };
+      if (cuts) pass(std::true_type());
+      else pass(std::false_type());
+    } else {
+      h[0] = carry[0], h[1] = carry[1];
+      through<true>(whole, carry);
     }
     if (p.saved && warp == 0 && tile * kTile >= lo && tile * kTile < hi) {
 #pragma unroll
-      for (int v = 0; v < V; ++v)
+      for (int v = 0; v < 2; ++v)
         if (v < cols) p.saved[tile * p.width + c + v] = h[v];
     }
+    through<true>(before, h);
+    if (inside) {
+      if (!p.out) continue;
+      int64_t at = (tile * kTile + warp * R) * p.os + c;
 #pragma unroll
-    for (int w = 0; w < W - 1; ++w) {
-      if (w < warp) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) h[v] = through(s_warp[w][lane * V + v], h[v]);
+      for (int j = 0; j < R; ++j) {
+        fma2(h[0], h[1], e[j][0], e[j][1], h[0], h[1], b[j][0], b[j][1]);
+        put2<T>(p.out, at, h, cols, p.pairs);
+        at += p.os;
       }
-    }
+    } else {
 #pragma unroll
-    for (int j = 0; j < R; ++j) {
-      const bool cut = first >> j & 1;
+      for (int j = 0; j < R; ++j) {
+        through<true>(make_float4(e[j][0], e[j][1], b[j][0], b[j][1]), h);
+        const int row = warp * R + j;
+        if (p.out && (in >> j & 1))
+          put2<T>(p.out, (tile * kTile + row) * p.os + c, h, cols, p.pairs);
+        if (p.keep_state && (last >> j & 1)) {
+          const int64_t slot = seq_slot(p.q, sh.rows.seq[row]);
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        h[v] = cut ? b[j * V + v] : fmaf(e[j * V + v], h[v], b[j * V + v]);
-      const int64_t r = tile * kTile + warp * R + j;
-      if (p.out && (in >> j & 1) && cols == V) Raw<T, V>::put(out + r * p.os, h);
-      if (p.keep_state && (last >> j & 1)) {
-        const int64_t slot = seq_slot(p.q, s_rows[buf].seq[warp * R + j]);
-        if (slot >= 0 && cols == V) {
-#pragma unroll
-          for (int v = 0; v < V; ++v) p.state[slot * p.slot_stride + c + v] = h[v];
+          for (int v = 0; v < 2; ++v)
+            if (slot >= 0 && v < cols) p.state[slot * p.slot_stride + c + v] = h[v];
         }
       }
+      // (the next turn's search writes rows)
+      __syncthreads();
     }
   }
   if (p.keep_state && warp == 0) {
@@ -469,210 +612,253 @@ __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) k_recur(const Par
 // Gradients.  The cluster's tiles go from the last rows to the first; rank 0 has
 // the last of them.
 // ---------------------------------------------------------------------------
-template <typename T, int V>
-__global__ void __launch_bounds__(512, 1) k_recur_backward(const Params p) {
-  constexpr int W = 16, R = kTile / W, N = R * V, C = 32 * V;
-  __shared__ float2 s_down[W][C];  // pairs of states
-  __shared__ float2 s_up[W][C];    // pairs of gradients
-  __shared__ float2 s_peer[2][kMaxCluster][C];
-  __shared__ TileRows s_rows[2];
+struct BackwardShared {
+  float4 down[W][32];  // pairs of states
+  float4 up[W][32];    // pairs of gradients
+  float4 peer[2][kMaxCluster][32];
+  int cut[2][kMaxCluster];
+  TileRows rows;
+};
+
+// What the warp's rows need again, and their pairs.
+struct BackwardRows {
+  float e[R][2], m[R][2], si[R][2], sr[R][2];
+};
+template <typename T, bool INSIDE, bool FAST>
+__device__ __forceinline__ void backward_rows(const Params& p, const T* tile, const float (&ac)[2],
+                                              const TileRows& t, int64_t c, int cols,
+                                              BackwardRows& k, float4& down, float4& up) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const T* mine = tile + warp * R * kCols + lane * 2;
+  down = up = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
+#pragma unroll
+  for (int j = 0; j < R; ++j) {
+    float x[2], b[2];
+    get2(mine + j * kCols, x);
+    get2(mine + (kTile + j) * kCols, k.si[j]);
+    get2(mine + (2 * kTile + j) * kCols, k.sr[j]);
+    sigmoid2<T>(k.si[j], k.si[j]);
+    sigmoid2<T>(k.sr[j], k.sr[j]);
+    decay2<T, FAST>(k.sr[j], ac[0], ac[1], k.e[j], k.m[j]);
+    mul2(b[0], b[1], k.m[j][0], k.m[j][1], k.si[j][0], k.si[j][1]);
+    mul2(b[0], b[1], b[0], b[1], x[0], x[1]);
+    if constexpr (!INSIDE) {
+      const int row = warp * R + j;
+      if (!(t.in[row >> 5] >> (row & 31) & 1)) {
+        k.e[j][0] = k.e[j][1] = 1.0f;
+        b[0] = b[1] = 0.0f;
+      }
+      if (t.first[row >> 5] >> (row & 31) & 1) {
+        float h[2];
+        start_state<2>(p, t.seq[row], c, cols, h);
+        fma2(b[0], b[1], k.e[j][0], k.e[j][1], h[0], h[1], b[0], b[1]);
+        down = make_float4(kCut, kCut, b[0], b[1]);
+        continue;
+      }
+    }
+    compose<!INSIDE>(down, make_float4(k.e[j][0], k.e[j][1], b[0], b[1]));
+  }
+#pragma unroll
+  for (int j = R - 1; j >= 0; --j) {
+    float g[2];
+    get2(mine + (3 * kTile + j) * kCols, g);
+    if constexpr (!INSIDE) {
+      const int row = warp * R + j;
+      if (!(t.in[row >> 5] >> (row & 31) & 1)) continue;
+      if (t.last[row >> 5] >> (row & 31) & 1) {
+        end_gradient(p, t.seq[row], c, cols, g);
+        mul2(g[0], g[1], g[0], g[1], k.e[j][0], k.e[j][1]);
+        up = make_float4(kCut, kCut, g[0], g[1]);
+        continue;
+      }
+    }
+    mul2(g[0], g[1], g[0], g[1], k.e[j][0], k.e[j][1]);
+    compose<!INSIDE>(up, make_float4(k.e[j][0], k.e[j][1], g[0], g[1]));
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 2) k_recur_backward(const Params p, int stages) {
+  extern __shared__ uint4 s_tile[];
+  __shared__ BackwardShared sh;
+  constexpr int kInput = kTile * kCols;  // elements of an input's tile
   pdl_wait();
   pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_rank(), size = cluster_size();
-  const int64_t c = (static_cast<int64_t>(blockIdx.y) * 32 + lane) * V;
-  const int cols = c >= p.width ? 0 : static_cast<int>(p.width - c < V ? p.width - c : V);
-  float ac[V];
-  bool fast = true;
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    ac[v] = v < cols ? __ldg(p.a + c + v) : 0.0f;
-    fast = fast && ac[v] > kSeries;
-  }
-  fast = __all_sync(0xffffffffu, fast);
+  const int rank = static_cast<int>(cluster_rank()), size = static_cast<int>(cluster_size());
+  const int64_t c0 = static_cast<int64_t>(blockIdx.y) * kCols, c = c0 + lane * 2;
+  const int cols = c >= p.width ? 0 : p.width - c < 2 ? 1 : 2;
+  cluster_arrive();  // (every CTA has begun before another one writes to it)
   const int64_t lo = segment_begin(p, blockIdx.z), hi = segment_begin(p, blockIdx.z + 1);
   const int64_t tile0 = lo / kTile, tiles = hi > lo ? (hi + kTile - 1) / kTile - tile0 : 0;
   const int64_t turns = (tiles + size - 1) / size;
   const int64_t top = tile0 + tiles - 1;  // the last tile
-
-  const T* x = static_cast<const T*>(p.x) + c;
-  const T* ig = static_cast<const T*>(p.ig) + c;
-  const T* rg = static_cast<const T*>(p.rg) + c;
-  const T* dout = static_cast<const T*>(p.dout) + c;
-  Raw<T, V> xr[R], ir[R], rr[R], gr[R];
-  float hs[V] = {};  // the state before the tile, as it was kept
-  auto fetch = [&](int64_t tile) {
-#pragma unroll
-    for (int j = 0; j < R; ++j) {
-      const int64_t r = tile * kTile + warp * R + j;
-      if (cols == V && r >= lo && r < hi) {
-        xr[j].load(x + r * p.xs);
-        ir[j].load(ig + r * p.is);
-        rr[j].load(rg + r * p.rs);
-        gr[j].load(dout + r * p.gs);
-      } else {
-        xr[j].clear(), ir[j].clear(), rr[j].clear(), gr[j].clear();
-      }
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      hs[v] = tile * kTile >= lo && v < cols ? __ldg(p.saved + tile * p.width + c + v) : 0.0f;
-    if (threadIdx.x < kTile) place_rows(p.q, tile, lo, hi, &s_rows[(top - tile) / size & 1]);
+  const auto fetch = [&](int64_t tile, T* to) {
+    copy_tile<T, kThreads>(to, p.x, p.xs, c0, p.width, tile, lo, hi, p.chunk);
+    copy_tile<T, kThreads>(to + kInput, p.ig, p.is, c0, p.width, tile, lo, hi, p.chunk);
+    copy_tile<T, kThreads>(to + 2 * kInput, p.rg, p.rs, c0, p.width, tile, lo, hi, p.chunk);
+    copy_tile<T, kThreads>(to + 3 * kInput, p.dout, p.gs, c0, p.width, tile, lo, hi, p.chunk);
   };
-
-  float carry[V] = {}, da[V] = {};
-  cluster_arrive();  // (every CTA has begun before another one writes to it)
-  if (turns > 0) fetch(top - rank);
+  T* const ring = reinterpret_cast<T*>(s_tile);
+  if (turns > 0) fetch(top - rank, ring);
+  float ac[2];
+#pragma unroll
+  for (int v = 0; v < 2; ++v) ac[v] = v < cols ? __ldg(p.a + c + v) : 0.0f;
+  const bool fast = __all_sync(0xffffffffu, ac[0] > kSeries && ac[1] > kSeries);
   cluster_wait();
+
+  float carry[2] = {0.0f, 0.0f}, da[2] = {0.0f, 0.0f};
+  Rows known;
   for (int64_t turn = 0; turn < turns; ++turn) {
     const int64_t tile = top - (turn * size + rank);
     const int buf = turn & 1;
+    const T* const mine = ring + (stages == 2 ? buf : 0) * 4 * kInput;
+    const bool inside = tile * kTile >= lo && known.inside(tile);
+    if (!inside && threadIdx.x < kTile) place_rows(p.q, tile, lo, hi, &sh.rows);
+    float h[2];  // the state before the tile, as it was kept
+#pragma unroll
+    for (int v = 0; v < 2; ++v)
+      h[v] = tile * kTile >= lo && v < cols ? __ldg(p.saved + tile * p.width + c + v) : 0.0f;
+    copies_wait();
     __syncthreads();
-    const int shift = warp * R & 31;
-    const uint32_t in = s_rows[buf].in[warp * R >> 5] >> shift,
-                   first = s_rows[buf].first[warp * R >> 5] >> shift,
-                   last = s_rows[buf].last[warp * R >> 5] >> shift;
+    if (stages == 2 && turn + 1 < turns) fetch(tile - size, ring + (buf ^ 1) * 4 * kInput);
 
-    float e[N], m[N], si[N], sr[N], xf[N], g[N];
-#pragma unroll
-    for (int j = 0; j < R; ++j) {
-      xr[j].get(xf + j * V), ir[j].get(si + j * V), rr[j].get(sr + j * V);
-      gr[j].get(g + j * V);
-    }
-#pragma unroll
-    for (int k = 0; k < N; k += 2) {
-      sigmoid2<T>(si + k, si + k);
-      sigmoid2<T>(sr + k, sr + k);
-      if (fast) decay2<T, true>(sr + k, ac[0], ac[V - 1], e + k, m + k);
-      else decay2<T, false>(sr + k, ac[0], ac[V - 1], e + k, m + k);
-    }
-    float2 down[V], up[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) down[v] = up[v] = make_float2(1.0f, 0.0f);
-#pragma unroll
-    for (int j = 0; j < R; ++j) {
-      if (!(in >> j & 1)) {
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-          e[j * V + v] = 1.0f, m[j * V + v] = xf[j * V + v] = g[j * V + v] = 0.0f;
-      }
-      float b[V];
-#pragma unroll
-      for (int v = 0; v < V; ++v) b[v] = m[j * V + v] * si[j * V + v] * xf[j * V + v];
-      if (first >> j & 1) {
-        float h0[V];
-        start_state<V>(p, s_rows[buf].seq[warp * R + j], c, cols, h0);
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-          down[v] = make_float2(kCut, fmaf(e[j * V + v], h0[v], b[v]));
+    BackwardRows k;
+    {
+      float4 down, up;
+      if (inside) {
+        if (fast) backward_rows<T, true, true>(p, mine, ac, sh.rows, c, cols, k, down, up);
+        else backward_rows<T, true, false>(p, mine, ac, sh.rows, c, cols, k, down, up);
       } else {
-#pragma unroll
-        for (int v = 0; v < V; ++v) down[v] = compose(down[v], make_float2(e[j * V + v], b[v]));
+        backward_rows<T, false, false>(p, mine, ac, sh.rows, c, cols, k, down, up);
       }
+      sh.down[warp][lane] = down;
+      sh.up[warp][lane] = up;
     }
-#pragma unroll
-    for (int j = R - 1; j >= 0; --j) {
-      if (last >> j & 1) {
-        if (p.dstate) {
-          const float* d = p.dstate + s_rows[buf].seq[warp * R + j] * p.width + c;
-#pragma unroll
-          for (int v = 0; v < V; ++v)
-            if (v < cols) g[j * V + v] += __ldg(d + v);
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v) up[v] = make_float2(kCut, e[j * V + v] * g[j * V + v]);
-      } else {
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-          up[v] = compose(up[v], make_float2(e[j * V + v], e[j * V + v] * g[j * V + v]));
+    const uint32_t in = inside ? ~0u : sh.rows.in[warp * R >> 5] >> (warp * R & 31),
+                   first = inside ? 0u : sh.rows.first[warp * R >> 5] >> (warp * R & 31),
+                   last = inside ? 0u : sh.rows.last[warp * R >> 5] >> (warp * R & 31);
+    const bool cut = !inside && (sh.rows.last[0] | sh.rows.last[1]) != 0;
+    if (!inside) {  // (of the tile's first row: its tiles come next)
+      int64_t b, e;
+      known.begin = known.end = 0;
+      if (tile * kTile >= lo && tile * kTile < hi) {
+        seq_range(p.q, sh.rows.seq[0], b, e);
+        known.begin = b, known.end = e;
       }
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      s_down[warp][lane * V + v] = down[v];
-      s_up[warp][lane * V + v] = up[v];
     }
     __syncthreads();
-    {
-      const int ch = threadIdx.x % C;
-      float2 t = s_up[W - 1][ch];
+    // the pair of the rows behind this warp's in the tile, and of the whole tile
+    float4 behind, whole = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
+    const auto fold = [&](auto cuts) {
 #pragma unroll
-      for (int w = W - 2; w >= 0; --w) t = compose(t, s_up[w][ch]);
-      for (uint32_t k = threadIdx.x / C; k < size; k += blockDim.x / C)
-        put_peer(&s_peer[buf][rank][ch], k, t);
+      for (int w = W - 1; w >= 0; --w) {
+        if (w == warp) behind = whole;
+        compose<decltype(cuts)::value>(whole, sh.up[w][lane]);
+      }
+    };
+    if (cut) fold(std::true_type());
+    else fold(std::false_type());
+    if (size > 1) {
+      if (warp < size) {
+        put_peer(&sh.peer[buf][rank][lane], warp, whole);
+        if (lane == 0) put_peer_int(&sh.cut[buf][rank], warp, cut);
+      }
+      cluster_arrive();
     }
-    cluster_arrive();
     // the states before each row, meanwhile
-    float h[V], hp[N];
+    float hp[R][2];
 #pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = hs[v];
-    for (int w = 0; w < warp; ++w) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) h[v] = through(s_down[w][lane * V + v], h[v]);
+    for (int w = 0; w < W - 1; ++w) {
+      if (w < warp) {
+        if (inside) through<false>(sh.down[w][lane], h);
+        else through<true>(sh.down[w][lane], h);
+      }
     }
 #pragma unroll
     for (int j = 0; j < R; ++j) {
-      if (first >> j & 1) start_state<V>(p, s_rows[buf].seq[warp * R + j], c, cols, h);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int k = j * V + v;
-        hp[k] = h[v];
-        h[v] = fmaf(e[k], h[v], m[k] * si[k] * xf[k]);
-      }
+      if (first >> j & 1) start_state<2>(p, sh.rows.seq[warp * R + j], c, cols, h);
+      float x[2], b[2];
+      get2(mine + (warp * R + j) * kCols + lane * 2, x);
+      mul2(b[0], b[1], k.m[j][0], k.m[j][1], k.si[j][0], k.si[j][1]);
+      mul2(b[0], b[1], b[0], b[1], x[0], x[1]);
+      hp[j][0] = h[0], hp[j][1] = h[1];
+      if (in >> j & 1) fma2(h[0], h[1], k.e[j][0], k.e[j][1], h[0], h[1], b[0], b[1]);
     }
-    if (turn + 1 < turns) fetch(tile - size);
-    cluster_wait();
 
     // the gradient that comes to this warp's last row from the rows behind it
-    float gc[V];
-    for (uint32_t k = 0; k < size; ++k) {
-      if (k == rank) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) gc[v] = carry[v];
-      }
-#pragma unroll
-      for (int v = 0; v < V; ++v) carry[v] = through(s_peer[buf][k][lane * V + v], carry[v]);
+    float gc[2];
+    if (size > 1) {
+      cluster_wait();
+      bool cuts = false;
+      for (int q = 0; q < size; ++q) cuts = cuts || sh.cut[buf][q] != 0;
+      const auto pass = [&](auto some) {
+        for (int q = 0; q < size; ++q) {
+          if (q == rank) gc[0] = carry[0], gc[1] = carry[1];
+          through<decltype(some)::value>(sh.peer[buf][q][lane], carry);
+        }
+      };
+      if (cuts) pass(std::true_type());
+      else pass(std::false_type());
+    } else {
+      gc[0] = carry[0], gc[1] = carry[1];
+      through<true>(whole, carry);
     }
-    for (int w = W - 1; w > warp; --w) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) gc[v] = through(s_up[w][lane * V + v], gc[v]);
-    }
+    through<true>(behind, gc);
 #pragma unroll
     for (int j = R - 1; j >= 0; --j) {
-      const bool cut = last >> j & 1;
-      float dx[V], di[V], dr[V];
+      const int row = warp * R + j;
+      const int64_t r = tile * kTile + row;
+      float g[2], x[2], dx[2], di[2], dr[2], t1[2], t2[2];
+      get2(mine + row * kCols + lane * 2, x);
+      get2(mine + 3 * kInput + row * kCols + lane * 2, g);
+      const float(&e)[2] = k.e[j], (&m)[2] = k.m[j], (&si)[2] = k.si[j], (&sr)[2] = k.sr[j];
+      if (last >> j & 1) end_gradient(p, sh.rows.seq[row], c, cols, g);
+      else fma2(g[0], g[1], g[0], g[1], 1.0f, 1.0f, gc[0], gc[1]);
+      // dx = g m i,  di = dx x (1 - i)
+      mul2(dx[0], dx[1], m[0], m[1], si[0], si[1]);
+      mul2(dx[0], dx[1], dx[0], dx[1], g[0], g[1]);
+      fma2(di[0], di[1], si[0], si[1], -1.0f, -1.0f, 1.0f, 1.0f);
+      mul2(di[0], di[1], di[0], di[1], x[0], x[1]);
+      mul2(di[0], di[1], di[0], di[1], dx[0], dx[1]);
+      // g (h e r - i x e^2 r / m)
+      float over[2];
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int k = j * V + v;
-        const float gk = cut ? g[k] : g[k] + gc[v];
-        const float over = m[k] > 0.0f ? (Elem<T>::kExactSilu ? sr[k] / m[k]
-                                                              : sr[k] * rcp_approx(m[k]))
-                                       : 0.0f;
-        dx[v] = gk * m[k] * si[k];
-        di[v] = dx[v] * xf[k] * (1.0f - si[k]);
-        const float dpr = gk * (hp[k] * e[k] * sr[k] - si[k] * xf[k] * e[k] * e[k] * over);
-        dr[v] = dpr * ac[v] * (1.0f - sr[k]);
-        if (in >> j & 1) da[v] += dpr;
-        gc[v] = e[k] * gk;
+      for (int v = 0; v < 2; ++v)
+        over[v] = m[v] > 0.0f ? (Elem<T>::kExactSilu ? 1.0f / m[v] : rcp_approx(m[v])) : 0.0f;
+      mul2(t2[0], t2[1], si[0], si[1], x[0], x[1]);
+      mul2(t2[0], t2[1], t2[0], t2[1], e[0], e[1]);
+      mul2(t2[0], t2[1], t2[0], t2[1], over[0], over[1]);
+      fma2(t1[0], t1[1], t2[0], t2[1], -1.0f, -1.0f, hp[j][0], hp[j][1]);
+      mul2(t2[0], t2[1], e[0], e[1], sr[0], sr[1]);
+      mul2(t1[0], t1[1], t1[0], t1[1], t2[0], t2[1]);
+      mul2(t1[0], t1[1], t1[0], t1[1], g[0], g[1]);
+      fma2(dr[0], dr[1], sr[0], sr[1], -1.0f, -1.0f, 1.0f, 1.0f);
+      mul2(dr[0], dr[1], dr[0], dr[1], ac[0], ac[1]);
+      mul2(dr[0], dr[1], dr[0], dr[1], t1[0], t1[1]);
+      if (in >> j & 1) {
+        fma2(da[0], da[1], t1[0], t1[1], 1.0f, 1.0f, da[0], da[1]);
+        mul2(gc[0], gc[1], e[0], e[1], g[0], g[1]);
+      } else {  // a row of no sequence
+#pragma unroll
+        for (int v = 0; v < 2; ++v) dx[v] = di[v] = dr[v] = 0.0f;
       }
-      const int64_t r = tile * kTile + warp * R + j;
-      if (r >= lo && r < hi && cols == V) {
-        if (!(in >> j & 1)) {  // a row of no sequence
-#pragma unroll
-          for (int v = 0; v < V; ++v) dx[v] = di[v] = dr[v] = 0.0f;
-        }
-        Raw<T, V>::put(static_cast<T*>(p.dx) + r * p.dxs + c, dx);
-        Raw<T, V>::put(static_cast<T*>(p.dig) + r * p.dis + c, di);
-        Raw<T, V>::put(static_cast<T*>(p.drg) + r * p.drs + c, dr);
+      if (inside || (r >= lo && r < hi)) {
+        put2<T>(p.dx, r * p.dxs + c, dx, cols, p.pairs);
+        put2<T>(p.dig, r * p.dis + c, di, cols, p.pairs);
+        put2<T>(p.drg, r * p.drs + c, dr, cols, p.pairs);
       }
       if (p.dinitial && (first >> j & 1)) {
-        const int64_t s = s_rows[buf].seq[warp * R + j];
+        const int64_t s = sh.rows.seq[row];
         const bool resumes = seq_slot(p.q, s) >= 0 && seq_resumes(p.q, s);
 #pragma unroll
-        for (int v = 0; v < V; ++v)
+        for (int v = 0; v < 2; ++v)
           if (v < cols) p.dinitial[s * p.width + c + v] = resumes ? gc[v] : 0.0f;
       }
     }
+    // (the next turn's search writes rows, its copies the tile)
+    if (!inside || stages == 1) __syncthreads();
+    if (stages == 1 && turn + 1 < turns) fetch(tile - size, ring);
   }
   if (p.dinitial && warp == 0) {
     each_empty(p.q, static_cast<int64_t>(blockIdx.z) * size + rank,
@@ -686,21 +872,24 @@ __global__ void __launch_bounds__(512, 1) k_recur_backward(const Params p) {
   }
   // da: the warps' sums, then the CTAs' in rank 0
   __syncthreads();
-#pragma unroll
-  for (int v = 0; v < V; ++v) s_up[warp][lane * V + v].x = da[v];
+  sh.up[warp][lane] = make_float4(da[0], da[1], 0.0f, 0.0f);
   __syncthreads();
-  if (threadIdx.x < C) {
-    float t = 0.0f;
-    for (int w = 0; w < W; ++w) t += s_up[w][threadIdx.x].x;
-    put_peer(&s_peer[turns & 1][rank][threadIdx.x], 0, make_float2(t, 0.0f));
+  if (warp == 0) {
+    float4 t = sh.up[0][lane];
+    for (int w = 1; w < W; ++w) t.x += sh.up[w][lane].x, t.y += sh.up[w][lane].y;
+    put_peer(&sh.peer[turns & 1][rank][lane], 0, t);
   }
   cluster_arrive();
   cluster_wait();
-  const int64_t ch = static_cast<int64_t>(blockIdx.y) * C + threadIdx.x;
-  if (rank == 0 && threadIdx.x < C && ch < p.width) {
-    float t = 0.0f;
-    for (uint32_t k = 0; k < size; ++k) t += s_peer[turns & 1][k][threadIdx.x].x;
-    p.da[blockIdx.z * p.width + ch] = t;
+  if (rank == 0 && warp == 0) {
+    float t[2] = {0.0f, 0.0f};
+    for (int q = 0; q < size; ++q) {
+      t[0] += sh.peer[turns & 1][q][lane].x;
+      t[1] += sh.peer[turns & 1][q][lane].y;
+    }
+#pragma unroll
+    for (int v = 0; v < 2; ++v)
+      if (v < cols) p.da[blockIdx.z * p.width + c + v] = t[v];
   }
 }
 
@@ -783,13 +972,14 @@ Split split_rows(int64_t rows, int64_t seqs, int64_t blocks, int resident) {
   return s;
 }
 
-template <typename K>
-int launch_cluster(K kernel, const Params& p, int64_t blocks, Split s, unsigned threads,
-                   cudaStream_t stream) {
+template <typename... P, typename... A>
+int launch_cluster(void (*kernel)(P...), int64_t blocks, Split s, int smem, cudaStream_t stream,
+                   A... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(s.cluster), static_cast<unsigned>(blocks),
                      static_cast<unsigned>(s.segments));
-  cfg.blockDim = dim3(threads);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = stream;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -800,7 +990,7 @@ int launch_cluster(K kernel, const Params& p, int64_t blocks, Split s, unsigned 
   at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 2;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
   if (e != cudaSuccess) {
     record_cuda_error(e);
     return GGRN_ERR_CUDA;
@@ -808,23 +998,37 @@ int launch_cluster(K kernel, const Params& p, int64_t blocks, Split s, unsigned 
   return GGRN_OK;
 }
 
-int64_t blocks_of(int64_t width, int v) { return (width + 32 * v - 1) / (32 * v); }
+int64_t blocks_of(int64_t width) { return (width + kCols - 1) / kCols; }
 
-template <typename T, int V>
+template <typename T>
 int launch_forward(Params& p, cudaStream_t s) {
-  const int64_t blocks = blocks_of(p.width, V);
-  const Split k = split_rows(p.q.rows, p.q.seqs, blocks, sizeof(T) == 2 ? 3 : 2);
+  const int64_t blocks = blocks_of(p.width);
+  const Split k = split_rows(p.q.rows, p.q.seqs, blocks, sizeof(T) == 2 ? 4 : 3);
   p.segments = k.segments;
-  return launch_cluster(k_recur<T, V>, p, blocks, k, 256, s);
+  constexpr int kSmem = 3 * kTile * kCols * sizeof(T);
+  const cudaError_t e = allow_shared_memory<k_recur<T>>(kSmem);
+  if (e != cudaSuccess) {
+    record_cuda_error(e);
+    return GGRN_ERR_CUDA;
+  }
+  return launch_cluster(k_recur<T>, blocks, k, kSmem, s, p);
 }
-template <typename T, int V>
+template <typename T>
 int launch_backward(Params& p, float* sums, cudaStream_t s) {
-  const int64_t blocks = blocks_of(p.width, V);
-  const Split k = split_rows(p.q.rows, p.q.seqs, blocks, 1);
+  const int64_t blocks = blocks_of(p.width);
+  const Split k = split_rows(p.q.rows, p.q.seqs, blocks, 2);
   p.segments = k.segments;
   float* const da = p.da;
   if (k.segments > 1) p.da = sums;
-  const int st = launch_cluster(k_recur_backward<T, V>, p, blocks, k, 512, s);
+  // two tiles of 16-bit types in shared memory, one of f32
+  constexpr int kStages = sizeof(T) == 2 ? 2 : 1;
+  constexpr int kSmem = kStages * 4 * kTile * kCols * sizeof(T);
+  const cudaError_t e = allow_shared_memory<k_recur_backward<T>>(kSmem);
+  if (e != cudaSuccess) {
+    record_cuda_error(e);
+    return GGRN_ERR_CUDA;
+  }
+  const int st = launch_cluster(k_recur_backward<T>, blocks, k, kSmem, s, p, kStages);
   if (st != GGRN_OK || k.segments == 1) return st;
   return mixer::launch(k_recur_sum, dim3(static_cast<unsigned>((p.width + 255) / 256)), 256, 0, s,
                        static_cast<const float*>(sums), da, p.width, k.segments);
@@ -838,7 +1042,8 @@ int launch_step(const Params& p, cudaStream_t s) {
                        p);
 }
 
-// Widths that a grid's second axis holds with one channel a lane.
+// Widths that a grid's second axis holds (a block of channels each, or 128 in the
+// step form).
 constexpr int64_t kMostColumns = int64_t{65535} * 32;
 
 struct Matrix {
@@ -846,11 +1051,21 @@ struct Matrix {
   int64_t stride;
 };
 // Pairs of channels: every row of every matrix starts on one.
-bool pairs(int64_t rows, int64_t width, int es, std::initializer_list<Matrix> ms) {
-  if (width % 2) return false;
+bool pairs(int64_t rows, int es, std::initializer_list<Matrix> ms) {
   for (const Matrix& m : ms)
     if (!mixer::aligned_to(m.p, 2 * es) || (rows > 1 && m.stride % 2)) return false;
   return true;
+}
+
+// Bytes that every row of every matrix can be copied by.
+int chunk_of(int64_t rows, int64_t width, int es, std::initializer_list<Matrix> ms) {
+  for (int bytes : {16, 4}) {
+    bool fits = bytes == 4 || width * es % 16 == 0;
+    for (const Matrix& m : ms)
+      fits = fits && mixer::aligned_to(m.p, bytes) && (rows <= 1 || m.stride * es % bytes == 0);
+    if (fits) return bytes;
+  }
+  return es;
 }
 
 int check_sizes(int dtype, int64_t rows, int64_t width) {
@@ -920,18 +1135,19 @@ int run(const ggrn_recur_call* call, bool step, void* stream) {
   const int st = check(c, step, &p);
   if (st != GGRN_OK || (c.rows == 0 && (step || !c.state || p.q.seqs == 0))) return st;
   const int es = mixer::elem_bytes(c.dtype);
-  const bool two = pairs(c.rows, c.width, es, {{c.x, p.xs}, {c.input_gate, p.is},
-                                               {c.decay_gate, p.rs}, {c.out, p.os}});
+  const bool two = c.width % 2 == 0 && pairs(c.rows, es, {{c.x, p.xs}, {c.input_gate, p.is},
+                                                          {c.decay_gate, p.rs}, {c.out, p.os}});
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  p.chunk = chunk_of(c.rows, c.width, es, {{c.x, p.xs}, {c.input_gate, p.is}, {c.decay_gate, p.rs}});
+  p.pairs = pairs(c.rows, es, {{c.out, p.os}});
   if (step) {
     if (c.dtype == kF32) return two ? launch_step<float, 2>(p, s) : launch_step<float, 1>(p, s);
     if (c.dtype == kF16) return two ? launch_step<__half, 2>(p, s) : launch_step<__half, 1>(p, s);
     return two ? launch_step<__nv_bfloat16, 2>(p, s) : launch_step<__nv_bfloat16, 1>(p, s);
   }
-  if (c.dtype == kF32) return two ? launch_forward<float, 2>(p, s) : launch_forward<float, 1>(p, s);
-  if (c.dtype == kF16)
-    return two ? launch_forward<__half, 2>(p, s) : launch_forward<__half, 1>(p, s);
-  return two ? launch_forward<__nv_bfloat16, 2>(p, s) : launch_forward<__nv_bfloat16, 1>(p, s);
+  if (c.dtype == kF32) return launch_forward<float>(p, s);
+  if (c.dtype == kF16) return launch_forward<__half>(p, s);
+  return launch_forward<__nv_bfloat16>(p, s);
 }
 
 // Workspace of the backward pass: the states that were not kept, then the
@@ -943,12 +1159,7 @@ Space space_of(const ggrn_recur_backward_call& c) {
   const int64_t tiles = (c.rows + kTile - 1) / kTile;
   Space s = {c.saved ? 0 : tiles * c.width * 4, 0};
   s.saved = (s.saved + 15) / 16 * 16;
-  // the most segments that split_rows makes, by pairs of channels or one by one
-  int64_t most = 1;
-  for (int v = 1; v <= 2; ++v) {
-    const int64_t n = split_rows(c.rows, c.seqs, blocks_of(c.width, v), 1).segments;
-    if (n > most) most = n;
-  }
+  const int64_t most = split_rows(c.rows, c.seqs, blocks_of(c.width), 2).segments;
   if (most > 1) s.sums = most * c.width * 4;
   return s;
 }
@@ -1026,16 +1237,16 @@ int check_backward(const ggrn_recur_backward_call& c, Params* p) {
   return GGRN_OK;
 }
 
-template <typename T, int V>
+template <typename T>
 int backward(Params& p, const Space& need, void* workspace, cudaStream_t s) {
   if (!p.saved && p.q.rows > 0) {
     Params f = p;
     p.saved = f.saved = static_cast<float*>(workspace);
-    const int st = launch_forward<T, V>(f, s);
+    const int st = launch_forward<T>(f, s);
     if (st != GGRN_OK) return st;
   }
   float* sums = reinterpret_cast<float*>(static_cast<char*>(workspace) + need.saved);
-  return launch_backward<T, V>(p, sums, s);
+  return launch_backward<T>(p, sums, s);
 }
 
 int run_backward(const ggrn_recur_backward_call* call, void* stream) {
@@ -1045,18 +1256,15 @@ int run_backward(const ggrn_recur_backward_call* call, void* stream) {
   const int st = check_backward(c, &p);
   if (st != GGRN_OK) return st;
   const int es = mixer::elem_bytes(c.dtype);
-  const bool two = pairs(c.rows, c.width, es,
-                         {{c.dout, p.gs}, {c.x, p.xs}, {c.input_gate, p.is}, {c.decay_gate, p.rs},
-                          {c.dx, p.dxs}, {c.dinput_gate, p.dis}, {c.ddecay_gate, p.drs}});
+  p.chunk = chunk_of(c.rows, c.width, es, {{c.dout, p.gs}, {c.x, p.xs}, {c.input_gate, p.is},
+                                           {c.decay_gate, p.rs}});
+  p.pairs = pairs(c.rows, es, {{c.dx, p.dxs}, {c.dinput_gate, p.dis}, {c.ddecay_gate, p.drs}});
   const Space need = space_of(c);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   void* const w = c.workspace;
-  if (c.dtype == kF32)
-    return two ? backward<float, 2>(p, need, w, s) : backward<float, 1>(p, need, w, s);
-  if (c.dtype == kF16)
-    return two ? backward<__half, 2>(p, need, w, s) : backward<__half, 1>(p, need, w, s);
-  return two ? backward<__nv_bfloat16, 2>(p, need, w, s)
-             : backward<__nv_bfloat16, 1>(p, need, w, s);
+  if (c.dtype == kF32) return backward<float>(p, need, w, s);
+  if (c.dtype == kF16) return backward<__half>(p, need, w, s);
+  return backward<__nv_bfloat16>(p, need, w, s);
 }
 
 }  // namespace recur
