@@ -49,6 +49,8 @@ struct Params {
   int64_t slot_stride, width;
   int segments;
   int keep_state;
+  int mute;            // self-test: nothing is sent, so that the waits run out
+  unsigned int* fault; // device status word
   int chunk;           // bytes that the inputs' rows can be copied by: 16, 4, or an element
   int pairs;           // outputs' rows can be stored by pairs of channels
 };
@@ -96,11 +98,14 @@ struct Raw<T, 1> {
 // approximate exponential and reciprocal (both good to about 2^-22; below
 // 2^-126 they give 0).  f32: the accurate functions.
 //
-// exp(p) - 1 comes from its series where p > -1/4 (six terms: 2^-24 of it), and
-// e = 1 + that, m^2 = 1 - e^2 = -(e - 1)(2 + (e - 1)): neither loses digits to
-// cancellation where decays are slow (an exponential that is off by an ulp to one
-// side next to 1 is off by a thousand after a thousand rows), and slow channels
-// take no second exponential.  FAST: no decay of the warp's channels is below exp(-1/4).
+// exp(p) - 1 = p + p^2 (..) where p > -1/4, with a polynomial through the
+// Chebyshev points of that range (within 2^-26 of it), and e = 1 + that, m^2 =
+// 1 - e^2 = -(e - 1)(2 + (e - 1)): neither loses digits to cancellation where
+// decays are slow (an exponential that is off by an ulp to one side next to 1 is
+// off by a thousand after a thousand rows), and slow channels take no second
+// exponential.  FAST: no decay of the warp's channels is below exp(-1/4).
+// (Constants stand in scalar instructions, which hold them; pairs would need
+// them in registers.)
 // ---------------------------------------------------------------------------
 constexpr float kSeries = -0.25f;
 
@@ -116,12 +121,8 @@ __device__ __forceinline__ void sigmoid2(const float* z, float* s) {
     s[0] = 1.0f / (1.0f + expf(-z[0]));
     s[1] = 1.0f / (1.0f + expf(-z[1]));
   } else {
-    constexpr float k = -1.4426950408889634f;
-    float t0, t1;
-    mul2(t0, t1, z[0], z[1], k, k);
-    t0 = ex2_approx(t0), t1 = ex2_approx(t1);
-    fma2(t0, t1, t0, t1, 1.0f, 1.0f, 1.0f, 1.0f);
-    s[0] = rcp_approx(t0), s[1] = rcp_approx(t1);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) s[k] = rcp_approx(1.0f + ex2_approx(z[k] * -1.4426950408889634f));
   }
 }
 
@@ -142,63 +143,117 @@ template <typename T, bool FAST>
 __device__ __forceinline__ void decay2(const float* r, float a0, float a1, float* e, float* m) {
   float p[2];
   mul2(p[0], p[1], a0, a1, r[0], r[1]);
-  float s0 = 1.0f / 720, s1 = 1.0f / 720, q0, q1;
-  if constexpr (Elem<T>::kExactSilu) fma2(s0, s1, p[0], p[1], 1.0f / 5040, 1.0f / 5040, s0, s1);
-  fma2(s0, s1, s0, s1, p[0], p[1], 1.0f / 120, 1.0f / 120);
-  fma2(s0, s1, s0, s1, p[0], p[1], 1.0f / 24, 1.0f / 24);
-  fma2(s0, s1, s0, s1, p[0], p[1], 1.0f / 6, 1.0f / 6);
-  fma2(s0, s1, s0, s1, p[0], p[1], 0.5f, 0.5f);
-  fma2(s0, s1, s0, s1, p[0], p[1], 1.0f, 1.0f);
-  mul2(s0, s1, s0, s1, p[0], p[1]);  // e - 1
-  fma2(e[0], e[1], s0, s1, 1.0f, 1.0f, 1.0f, 1.0f);
-  if constexpr (!FAST) {
-    if (!(p[0] > kSeries)) beyond_series<T>(p[0], e[0], s0);
-    if (!(p[1] > kSeries)) beyond_series<T>(p[1], e[1], s1);
+  float s[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    float c = fmaf(7.67176877707243e-3f, p[k], 4.1564859449863434e-2f);
+    c = fmaf(c, p[k], 1.666616052389145e-1f);
+    c = fmaf(c, p[k], 4.999999701976776e-1f);
+    c = fmaf(c, p[k], 1.0f);
+    s[k] = c * p[k];  // e - 1
+    e[k] = 1.0f + s[k];
   }
-  fma2(q0, q1, s0, s1, -1.0f, -1.0f, -2.0f, -2.0f);
-  mul2(q0, q1, q0, q1, s0, s1);
-  if constexpr (Elem<T>::kExactSilu) {
-    m[0] = sqrtf(q0), m[1] = sqrtf(q1);
-  } else {
-    m[0] = sqrt_approx(q0), m[1] = sqrt_approx(q1);
+  if constexpr (!FAST) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (!(p[k] > kSeries)) beyond_series<T>(p[k], e[k], s[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const float q = -s[k] * (2.0f + s[k]);
+    m[k] = Elem<T>::kExactSilu ? sqrtf(q) : sqrt_approx(q);
   }
 }
 
 // ---------------------------------------------------------------------------
 // Clusters.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
 __device__ __forceinline__ uint32_t cluster_size() {
   uint32_t r;
   asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_arrive() {
+__device__ __forceinline__ void all_arrive() {
   asm volatile("barrier.cluster.arrive.release;" ::: "memory");
 }
-__device__ __forceinline__ void cluster_wait() {
+__device__ __forceinline__ void all_wait() {
   asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-}
-__device__ __forceinline__ void put_peer_int(const int* mine, uint32_t rank, int v) {
-  const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(mine));
-  asm volatile(
-      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\t"
-      "st.shared::cluster.u32 [a], %2;\n\t}" ::"r"(at),
-      "r"(rank), "r"(v)
-      : "memory");
 }
 // Stores v at the place of *mine in the shared memory of CTA `rank`.
 __device__ __forceinline__ void put_peer(const float4* mine, uint32_t rank, float4 v) {
-  const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(mine));
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
+                   map_to_rank(smem_u32(mine), rank)),
+               "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+               : "memory");
+}
+
+// What the CTAs of a cluster send each other every turn: a pair for each lane and
+// whether it is cut, by asynchronous remote stores that count their bytes on a
+// barrier of the CTA they go to, so that no turn waits for a CTA's other memory
+// operations.  Two turns' places: a CTA sends those of turn t + 2 when it has those
+// of turn t + 1, which the others send when they are through with turn t.
+//
+// Waits are bounded: one that runs out (about a second) sets `failed`, after which
+// the CTA's waits return at once and its outputs have no meaning; the status word
+// says so.  The CTAs of a cluster end together, so that nothing is sent to one that
+// has ended.
+constexpr uint32_t kFaultRecurWait = 128u;
+constexpr long long kWaitClocks = 2000000000ll;
+struct Mail {
+  float4 pair[2][kMaxCluster][32];
+  int cut[2][kMaxCluster];
+  unsigned long long landed[2];
+  volatile uint32_t failed;
+};
+__device__ __forceinline__ bool try_phase(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
   asm volatile(
-      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\t"
-      "st.shared::cluster.v4.f32 [a], {%2, %3, %4, %5};\n\t}" ::"r"(at),
-      "r"(rank), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
       : "memory");
+  return ok != 0;
+}
+__device__ __noinline__ void wait_poll(uint32_t bar, uint32_t parity, volatile uint32_t* failed) {
+  const long long start = clock64();
+  do {
+    if (*failed || try_phase(bar, parity)) return;
+  } while (clock64() - start < kWaitClocks);
+  *failed = 1;
+}
+// Before the arrival of every CTA of the cluster that comes before its first mail.
+__device__ __forceinline__ void mail_init(Mail& m) {
+  if (threadIdx.x == 0) {
+    mbar_init(smem_u32(&m.landed[0]), 1);
+    mbar_init(smem_u32(&m.landed[1]), 1);
+    m.failed = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+}
+// A whole warp sends to CTA `to`.
+__device__ __forceinline__ void mail_send(Mail& m, int buf, int rank, int to, const float4& v,
+                                          bool cut) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t bar = map_to_rank(smem_u32(&m.landed[buf]), to);
+  asm volatile(
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];"
+      ::"r"(map_to_rank(smem_u32(&m.pair[buf][rank][lane]), to)),
+      "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(bar)
+      : "memory");
+  if (lane == 0)
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(
+                     map_to_rank(smem_u32(&m.cut[buf][rank]), to)),
+                 "r"(cut ? 1u : 0u), "r"(bar)
+                 : "memory");
+}
+// One thread, before the wait: how much will land.
+__device__ __forceinline__ void mail_expect(Mail& m, int buf, int size) {
+  mbar_expect_tx(smem_u32(&m.landed[buf]), static_cast<uint32_t>(size) * (32 * 16 + 4));
+}
+__device__ __forceinline__ void mail_wait(Mail& m, int buf, uint32_t parity) {
+  const uint32_t bar = smem_u32(&m.landed[buf]);
+  if (!try_phase(bar, parity)) wait_poll(bar, parity, &m.failed);
 }
 
 // ---------------------------------------------------------------------------
@@ -363,36 +418,41 @@ __device__ __forceinline__ void copies_wait() {
 }
 
 // The CTA's threads start to copy tile `tile` of one input into `to`; rows
-// outside [lo, hi) and channels behind the last one become zeros.
+// outside [lo, hi) and channels behind the last one become zeros.  `whole`: there
+// are none of either.
 template <typename T, int THREADS>
 __device__ __forceinline__ void copy_tile(T* to, const void* base, int64_t stride, int64_t c0,
                                           int64_t width, int64_t tile, int64_t lo, int64_t hi,
-                                          int chunk) {
+                                          int chunk, bool whole) {
   constexpr int ES = sizeof(T);
   const T* from = static_cast<const T*>(base) + c0;
   const int64_t r0 = tile * kTile;
-  const int cols = static_cast<int>(width - c0 < kCols ? width - c0 : kCols);
   const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(to));
-  if (chunk == 16) {
-    constexpr int E = 16 / ES, ROW = kCols / E;  // chunks of a row
-    const int c = static_cast<int>(threadIdx.x) % ROW * E;
-    const int row0 = static_cast<int>(threadIdx.x) / ROW;
-    const T* p = from + (r0 + row0) * stride + c;
+  constexpr int E = 16 / ES, ROW = kCols / E, ROWS = THREADS / ROW;  // 16-byte chunks
+  if (chunk == 16 && whole) {
+    const T* p = from + (r0 + threadIdx.x / ROW) * stride + threadIdx.x % ROW * E;
+    const int64_t step = ROWS * stride;
 #pragma unroll
-    for (int k = 0; k < kTile * ROW / THREADS; ++k) {
-      const int row = row0 + k * (THREADS / ROW);
-      const bool ok = r0 + row >= lo && r0 + row < hi && c < cols;
-      copy_async<16>(at + (row * kCols + c) * ES, ok ? p : from, ok ? 16 : 0);
-      p += (THREADS / ROW) * stride;
-    }
-  } else if (chunk == 4) {
-    constexpr int E = 4 / ES, ROW = kCols / E;
-#pragma unroll 4
+    for (int k = 0; k < kTile / ROWS; ++k, p += step)
+      copy_async<16>(at + (threadIdx.x + k * THREADS) * 16, p, 16);
+    return;
+  }
+  const int cols = static_cast<int>(width - c0 < kCols ? width - c0 : kCols);
+  if (chunk == 16) {
+#pragma unroll 1
     for (int k = threadIdx.x; k < kTile * ROW; k += THREADS) {
       const int row = k / ROW, c = k % ROW * E;
       const bool ok = r0 + row >= lo && r0 + row < hi && c < cols;
-      copy_async<4>(at + (row * kCols + c) * ES, ok ? from + (r0 + row) * stride + c : from,
-                    !ok ? 0 : cols - c < E ? ES : 4);
+      copy_async<16>(at + k * 16, ok ? from + (r0 + row) * stride + c : from, ok ? 16 : 0);
+    }
+  } else if (chunk == 4) {
+    constexpr int E4 = 4 / ES, ROW4 = kCols / E4;
+#pragma unroll 2
+    for (int k = threadIdx.x; k < kTile * ROW4; k += THREADS) {
+      const int row = k / ROW4, c = k % ROW4 * E4;
+      const bool ok = r0 + row >= lo && r0 + row < hi && c < cols;
+      copy_async<4>(at + k * 4, ok ? from + (r0 + row) * stride + c : from,
+                    !ok ? 0 : cols - c < E4 ? ES : 4);
     }
   } else {
 #pragma unroll 4
@@ -428,28 +488,71 @@ __device__ __forceinline__ void put2(void* base, int64_t at, const float* f, int
   }
 }
 
-// ---------------------------------------------------------------------------
-// Prompts.  Eight warps of eight rows each.
-// ---------------------------------------------------------------------------
-constexpr int kThreads = 256, W = kThreads / 32, R = kTile / W;
-static_assert(W >= kMaxCluster, "a warp to each CTA that the tile's pair goes to");
+// What a CTA knows for all of its tiles.
+struct Place {
+  int64_t lo, hi;   // rows of its segment
+  int64_t c0, c;    // first channel of the CTA and of the lane
+  int cols;         // the lane's channels (0 to 2)
+  int rank, size;   // in its cluster
+  float ac[2];
+};
+__device__ __forceinline__ Place find_place(const Params& p) {
+  Place w;
+  const int lane = threadIdx.x & 31;
+  w.rank = static_cast<int>(cluster_ctarank());
+  w.size = static_cast<int>(cluster_size());
+  w.c0 = static_cast<int64_t>(blockIdx.y) * kCols;
+  w.c = w.c0 + lane * 2;
+  w.cols = w.c >= p.width ? 0 : p.width - w.c < 2 ? 1 : 2;
+  w.lo = segment_begin(p, blockIdx.z);
+  w.hi = segment_begin(p, blockIdx.z + 1);
+#pragma unroll
+  for (int v = 0; v < 2; ++v) w.ac[v] = v < w.cols ? __ldg(p.a + w.c + v) : 0.0f;
+  return w;
+}
+__device__ __forceinline__ bool whole_tile(const Params& p, const Place& w, int64_t tile) {
+  return tile * kTile >= w.lo && (tile + 1) * kTile <= w.hi && w.c0 + kCols <= p.width;
+}
 
-struct ForwardShared {
+// ---------------------------------------------------------------------------
+// Prompts.  Four warps of sixteen rows each: an element costs about 25
+// instructions of its own, what a tile costs besides is shared by 32 elements of
+// a thread.
+// ---------------------------------------------------------------------------
+namespace forward {
+
+constexpr int W = 4, R = kTile / W, kThreads = 32 * W;
+
+struct Shared {
   float4 pair[W][32];
-  float4 peer[2][kMaxCluster][32];
-  int cut[2][kMaxCluster];
+  Mail mail;
   TileRows rows;
 };
 
-// e and b of the warp's rows, and the pair of all of them.  INSIDE: all rows are
-// those of one sequence, neither its first nor its last.
+template <typename T>
+__device__ __forceinline__ void fetch(const Params& p, const Place& w, T* to, int64_t tile) {
+  const bool whole = whole_tile(p, w, tile);
+  const auto copy = [&](int k, const void* base, int64_t stride) {
+    copy_tile<T, kThreads>(to + k * kTile * kCols, base, stride, w.c0, p.width, tile, w.lo, w.hi,
+                           p.chunk, whole);
+  };
+  copy(0, p.x, p.xs), copy(1, p.ig, p.is), copy(2, p.rg, p.rs);
+}
+
+// One tile.  INSIDE: all of its rows are those of one sequence, neither its first
+// nor its last.  FAST: see decay2.  Takes the state before the cluster's tiles and
+// gives the one behind them.
 template <typename T, bool INSIDE, bool FAST>
-__device__ __forceinline__ void forward_rows(const Params& p, const T* tile, const float (&ac)[2],
-                                             const TileRows& t, int64_t c, int cols,
-                                             float (&e)[R][2], float (&b)[R][2], float4& s) {
+__device__ __forceinline__ float2 turn_of(const Params& p, const Place& w, Shared& sh, T* tiles,
+                                          int64_t tile, int64_t next, int64_t turn, float2 state) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const T* mine = tile + warp * R * kCols + lane * 2;
-  s = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
+  const int buf = turn & 1;
+  const uint32_t parity = turn >> 1 & 1;
+  const T* mine = tiles + warp * R * kCols + lane * 2;
+  const TileRows& t = sh.rows;
+  // e and b of the warp's rows, and the pair of all of them
+  float e[R][2], b[R][2];
+  float4 s = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
 #pragma unroll
   for (int j = 0; j < R; ++j) {
     float x[2], gi[2], gr[2], m[2];
@@ -458,7 +561,7 @@ __device__ __forceinline__ void forward_rows(const Params& p, const T* tile, con
     get2(mine + (2 * kTile + j) * kCols, gr);
     sigmoid2<T>(gi, gi);
     sigmoid2<T>(gr, gr);
-    decay2<T, FAST>(gr, ac[0], ac[1], e[j], m);
+    decay2<T, FAST>(gr, w.ac[0], w.ac[1], e[j], m);
     mul2(m[0], m[1], m[0], m[1], gi[0], gi[1]);
     mul2(b[j][0], b[j][1], m[0], m[1], x[0], x[1]);
     if constexpr (!INSIDE) {
@@ -469,429 +572,436 @@ __device__ __forceinline__ void forward_rows(const Params& p, const T* tile, con
       }
       if (t.first[row >> 5] >> (row & 31) & 1) {
         float h[2];
-        if (start_state<2>(p, t.seq[row], c, cols, h))
+        if (start_state<2>(p, t.seq[row], w.c, w.cols, h))
           fma2(b[j][0], b[j][1], e[j][0], e[j][1], h[0], h[1], b[j][0], b[j][1]);
         e[j][0] = e[j][1] = kCut;
       }
     }
     compose<!INSIDE>(s, make_float4(e[j][0], e[j][1], b[j][0], b[j][1]));
   }
+  sh.pair[warp][lane] = s;
+  const bool cut = !INSIDE && (t.first[0] | t.first[1]) != 0;
+  __syncthreads();
+  if (next >= 0) fetch(p, w, tiles, next);
+
+  // the pair of the rows before this warp's in the tile, and of the whole tile
+  float4 before = make_float4(1.0f, 1.0f, 0.0f, 0.0f), whole = sh.pair[0][lane];
+#pragma unroll
+  for (int k = 1; k < W; ++k) {
+    if (k == warp) before = whole;
+    compose<!INSIDE>(whole, sh.pair[k][lane]);
+  }
+  float carry[2] = {state.x, state.y}, h[2] = {state.x, state.y};
+  if (w.size > 1) {
+    if (threadIdx.x == 0) mail_expect(sh.mail, buf, w.size);
+    if (!p.mute)
+      for (int k = warp; k < w.size; k += W) mail_send(sh.mail, buf, w.rank, k, whole, cut);
+    mail_wait(sh.mail, buf, parity);
+    bool cuts = false;
+    for (int k = 0; k < w.size; ++k) cuts = cuts || sh.mail.cut[buf][k] != 0;
+    if (cuts) {
+      for (int k = 0; k < w.size; ++k) {
+        if (k == w.rank) h[0] = carry[0], h[1] = carry[1];
+        through<true>(sh.mail.pair[buf][k][lane], carry);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < kMaxCluster; ++k) {
+        if (k >= w.size) break;
+        if (k == w.rank) h[0] = carry[0], h[1] = carry[1];
+        through<false>(sh.mail.pair[buf][k][lane], carry);
+      }
+    }
+  } else {
+    through<!INSIDE>(whole, carry);
+  }
+  if (p.saved && warp == 0 && tile * kTile >= w.lo && tile * kTile < w.hi) {
+#pragma unroll
+    for (int v = 0; v < 2; ++v)
+      if (v < w.cols) p.saved[tile * p.width + w.c + v] = h[v];
+  }
+  through<!INSIDE>(before, h);
+  if constexpr (INSIDE) {
+    if (p.out) {
+      T* at = static_cast<T*>(p.out) + (tile * kTile + warp * R) * p.os + w.c;
+      if (p.pairs && w.cols == 2) {
+#pragma unroll
+        for (int j = 0; j < R; ++j, at += p.os) {
+          fma2(h[0], h[1], e[j][0], e[j][1], h[0], h[1], b[j][0], b[j][1]);
+          Raw<T, 2>::put(at, h);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < R; ++j, at += p.os) {
+          fma2(h[0], h[1], e[j][0], e[j][1], h[0], h[1], b[j][0], b[j][1]);
+          put2<T>(at, 0, h, w.cols, false);
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      through<true>(make_float4(e[j][0], e[j][1], b[j][0], b[j][1]), h);
+      const int row = warp * R + j;
+      if (p.out && (t.in[row >> 5] >> (row & 31) & 1))
+        put2<T>(p.out, (tile * kTile + row) * p.os + w.c, h, w.cols, p.pairs);
+      if (p.keep_state && (t.last[row >> 5] >> (row & 31) & 1)) {
+        const int64_t slot = seq_slot(p.q, t.seq[row]);
+#pragma unroll
+        for (int v = 0; v < 2; ++v)
+          if (slot >= 0 && v < w.cols) p.state[slot * p.slot_stride + w.c + v] = h[v];
+      }
+    }
+    __syncthreads();  // (the next turn's search writes rows)
+  }
+  return make_float2(carry[0], carry[1]);
+}
+// The forms that few tiles take, out of the way of the loop's instructions and
+// registers.
+template <typename T, bool INSIDE, bool FAST>
+__device__ __noinline__ float2 turn_apart(const Params& p, Place w, Shared& sh, T* tiles,
+                                          int64_t tile, int64_t next, int64_t turn, float2 state) {
+  return turn_of<T, INSIDE, FAST>(p, w, sh, tiles, tile, next, turn, state);
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3) k_recur(const Params p) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
+    k_recur(const __grid_constant__ Params p) {
   extern __shared__ uint4 s_tile[];
-  __shared__ ForwardShared sh;
-  T* const tile_of = reinterpret_cast<T*>(s_tile);  // x, input gate, decay gate
+  __shared__ Shared sh;
+  T* const tiles = reinterpret_cast<T*>(s_tile);  // x, input gate, decay gate
   pdl_wait();
   pdl_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = static_cast<int>(cluster_rank()), size = static_cast<int>(cluster_size());
-  const int64_t c0 = static_cast<int64_t>(blockIdx.y) * kCols, c = c0 + lane * 2;
-  const int cols = c >= p.width ? 0 : p.width - c < 2 ? 1 : 2;
-  if (size > 1) cluster_arrive();  // (every CTA has begun before another one writes to it)
-  const int64_t lo = segment_begin(p, blockIdx.z), hi = segment_begin(p, blockIdx.z + 1);
-  const int64_t tile0 = lo / kTile, tiles = hi > lo ? (hi + kTile - 1) / kTile - tile0 : 0;
-  const int64_t turns = (tiles + size - 1) / size;
-  const auto fetch = [&](int64_t tile) {
-    copy_tile<T, kThreads>(tile_of, p.x, p.xs, c0, p.width, tile, lo, hi, p.chunk);
-    copy_tile<T, kThreads>(tile_of + kTile * kCols, p.ig, p.is, c0, p.width, tile, lo, hi, p.chunk);
-    copy_tile<T, kThreads>(tile_of + 2 * kTile * kCols, p.rg, p.rs, c0, p.width, tile, lo, hi,
-                           p.chunk);
-  };
-  if (turns > 0) fetch(tile0 + rank);
-  float ac[2];
-#pragma unroll
-  for (int v = 0; v < 2; ++v) ac[v] = v < cols ? __ldg(p.a + c + v) : 0.0f;
-  const bool fast = __all_sync(0xffffffffu, ac[0] > kSeries && ac[1] > kSeries);
-  if (size > 1) cluster_wait();
+  mail_init(sh.mail);
+  all_arrive();  // (every CTA has begun before another one writes to it)
+  const Place w = find_place(p);
+  const int64_t tile0 = w.lo / kTile, count = w.hi > w.lo ? (w.hi + kTile - 1) / kTile - tile0 : 0;
+  const int64_t turns = (count + w.size - 1) / w.size;
+  int64_t tile = tile0 + w.rank;
+  if (turns > 0) fetch(p, w, tiles, tile);
+  const bool fast = __all_sync(0xffffffffu, w.ac[0] > kSeries && w.ac[1] > kSeries);
+  all_wait();
 
-  float carry[2] = {0.0f, 0.0f};  // the state before the cluster's tiles
+  float2 state = make_float2(0.0f, 0.0f);  // before the cluster's tiles
   Rows known;
-  for (int64_t turn = 0; turn < turns; ++turn) {
-    const int64_t tile = tile0 + turn * size + rank;
-    const int buf = turn & 1;
-    const bool inside = known.inside(tile) && (tile + 1) * kTile <= hi;
-    if (!inside && threadIdx.x < kTile) place_rows(p.q, tile, lo, hi, &sh.rows);
+  for (int64_t turn = 0; turn < turns; ++turn, tile += w.size) {
+    const int64_t next = turn + 1 < turns ? tile + w.size : -1;
+    const bool inside = known.inside(tile) && (tile + 1) * kTile <= w.hi;
+    if (!inside && threadIdx.x < kTile) place_rows(p.q, tile, w.lo, w.hi, &sh.rows);
     copies_wait();
     __syncthreads();
-
-    float e[R][2], b[R][2];
-    float4 s;
-    if (inside) {
-      if (fast) forward_rows<T, true, true>(p, tile_of, ac, sh.rows, c, cols, e, b, s);
-      else forward_rows<T, true, false>(p, tile_of, ac, sh.rows, c, cols, e, b, s);
+    if (inside && fast) {
+      state = turn_of<T, true, true>(p, w, sh, tiles, tile, next, turn, state);
+    } else if (inside) {
+      state = turn_apart<T, true, false>(p, w, sh, tiles, tile, next, turn, state);
     } else {
-      forward_rows<T, false, false>(p, tile_of, ac, sh.rows, c, cols, e, b, s);
-    }
-    sh.pair[warp][lane] = s;
-    const bool cut = !inside && (sh.rows.first[0] | sh.rows.first[1]) != 0;
-    const uint32_t in = inside ? ~0u : sh.rows.in[warp * R >> 5] >> (warp * R & 31),
-                   last = inside ? 0u : sh.rows.last[warp * R >> 5] >> (warp * R & 31);
-    if (!inside) known.begin = sh.rows.begin, known.end = sh.rows.end;
-    __syncthreads();
-    if (turn + 1 < turns) fetch(tile + size);
-
-    // the pair of the rows before this warp's in the tile, and of the whole tile
-    float4 before, whole = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
-    const auto fold = [&](auto cuts) {
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
-        if (w == warp) before = whole;
-        compose<decltype(cuts)::value>(whole, sh.pair[w][lane]);
-      }
-    };
-    if (cut) fold(std::true_type());
-    else fold(std::false_type());
-    float h[2];
-    bool cuts = cut;
-    if (size > 1) {
-      if (warp < size) {
-        put_peer(&sh.peer[buf][rank][lane], warp, whole);
-        if (lane == 0) put_peer_int(&sh.cut[buf][rank], warp, cut);
-      }
-      cluster_arrive();
-      cluster_wait();
-      for (int k = 0; k < size; ++k) cuts = cuts || sh.cut[buf][k] != 0;
-      const auto pass = [&](auto some) {
-        for (int k = 0; k < size; ++k) {
-          if (k == rank) h[0] = carry[0], h[1] = carry[1];
-          through<decltype(some)::value>(sh.peer[buf][k][lane], carry);
-        }
-      };
-      if (cuts) pass(std::true_type());
-      else pass(std::false_type());
-    } else {
-      h[0] = carry[0], h[1] = carry[1];
-      through<true>(whole, carry);
-    }
-    if (p.saved && warp == 0 && tile * kTile >= lo && tile * kTile < hi) {
-#pragma unroll
-      for (int v = 0; v < 2; ++v)
-        if (v < cols) p.saved[tile * p.width + c + v] = h[v];
-    }
-    through<true>(before, h);
-    if (inside) {
-      if (!p.out) continue;
-      int64_t at = (tile * kTile + warp * R) * p.os + c;
-#pragma unroll
-      for (int j = 0; j < R; ++j) {
-        fma2(h[0], h[1], e[j][0], e[j][1], h[0], h[1], b[j][0], b[j][1]);
-        put2<T>(p.out, at, h, cols, p.pairs);
-        at += p.os;
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < R; ++j) {
-        through<true>(make_float4(e[j][0], e[j][1], b[j][0], b[j][1]), h);
-        const int row = warp * R + j;
-        if (p.out && (in >> j & 1))
-          put2<T>(p.out, (tile * kTile + row) * p.os + c, h, cols, p.pairs);
-        if (p.keep_state && (last >> j & 1)) {
-          const int64_t slot = seq_slot(p.q, sh.rows.seq[row]);
-#pragma unroll
-          for (int v = 0; v < 2; ++v)
-            if (slot >= 0 && v < cols) p.state[slot * p.slot_stride + c + v] = h[v];
-        }
-      }
-      // (the next turn's search writes rows)
-      __syncthreads();
+      known.begin = sh.rows.begin, known.end = sh.rows.end;
+      state = turn_apart<T, false, false>(p, w, sh, tiles, tile, next, turn, state);
     }
   }
-  if (p.keep_state && warp == 0) {
-    each_empty(p.q, static_cast<int64_t>(blockIdx.z) * size + rank,
-               static_cast<int64_t>(size) * p.segments, [&](int64_t s) {
+  if (p.keep_state && threadIdx.x < 32) {
+    each_empty(p.q, static_cast<int64_t>(blockIdx.z) * w.size + w.rank,
+               static_cast<int64_t>(w.size) * p.segments, [&](int64_t s) {
                  const int64_t slot = seq_slot(p.q, s);
                  if (slot < 0 || seq_resumes(p.q, s)) return;
-                 for (int v = 0; v < cols; ++v) p.state[slot * p.slot_stride + c + v] = 0.0f;
+                 for (int v = 0; v < w.cols; ++v) p.state[slot * p.slot_stride + w.c + v] = 0.0f;
                });
+  }
+  if (w.size > 1) {
+    if (threadIdx.x == 0 && sh.mail.failed) atomicOr(p.fault, kFaultRecurWait);
+    all_arrive();
+    all_wait();
   }
 }
 
+}  // namespace forward
+
 // ---------------------------------------------------------------------------
-// Gradients.  The cluster's tiles go from the last rows to the first; rank 0 has
-// the last of them.
+// Gradients.  Eight warps of eight rows each; the cluster's tiles go from the
+// last rows to the first, rank 0 has the last of them.
 // ---------------------------------------------------------------------------
-struct BackwardShared {
+namespace backward {
+
+constexpr int W = 8, R = kTile / W, kThreads = 32 * W;
+static_assert(W >= kMaxCluster, "a warp to each CTA that the tile's pair goes to");
+constexpr int kInput = kTile * kCols;  // elements of an input's tile
+
+struct Shared {
   float4 down[W][32];  // pairs of states
   float4 up[W][32];    // pairs of gradients
-  float4 peer[2][kMaxCluster][32];
-  int cut[2][kMaxCluster];
+  Mail mail;
   TileRows rows;
 };
 
-// What the warp's rows need again, and their pairs.
-struct BackwardRows {
-  float e[R][2], m[R][2], si[R][2], sr[R][2];
+// Tiles of the inputs in shared memory: two of 16-bit types, one of f32.
+template <typename T>
+constexpr int stages() {
+  return sizeof(T) == 2 ? 2 : 1;
+}
+
+template <typename T>
+__device__ __forceinline__ void fetch(const Params& p, const Place& w, T* to, int64_t tile) {
+  const bool whole = whole_tile(p, w, tile);
+  const auto copy = [&](int k, const void* base, int64_t stride) {
+    copy_tile<T, kThreads>(to + k * kInput, base, stride, w.c0, p.width, tile, w.lo, w.hi, p.chunk,
+                           whole);
+  };
+  copy(0, p.x, p.xs), copy(1, p.ig, p.is), copy(2, p.rg, p.rs), copy(3, p.dout, p.gs);
+}
+
+struct Carry {
+  float g[2];   // the gradient of the state behind the cluster's tiles
+  float da[2];
 };
+
 template <typename T, bool INSIDE, bool FAST>
-__device__ __forceinline__ void backward_rows(const Params& p, const T* tile, const float (&ac)[2],
-                                              const TileRows& t, int64_t c, int cols,
-                                              BackwardRows& k, float4& down, float4& up) {
+__device__ __forceinline__ Carry turn_of(const Params& p, const Place& w, Shared& sh, T* ring,
+                                         int64_t tile, int64_t next, int64_t turn, Carry carry) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const T* mine = tile + warp * R * kCols + lane * 2;
-  down = up = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
+  const int buf = turn & 1;
+  const uint32_t parity = turn >> 1 & 1;
+  T* const tiles = ring + (stages<T>() == 2 ? buf : 0) * 4 * kInput;
+  const T* mine = tiles + warp * R * kCols + lane * 2;
+  const TileRows& t = sh.rows;
+  float h[2];  // the state before the tile, as it was kept
+#pragma unroll
+  for (int v = 0; v < 2; ++v)
+    h[v] = tile * kTile >= w.lo && v < w.cols ? __ldg(p.saved + tile * p.width + w.c + v) : 0.0f;
+  if (stages<T>() == 2 && next != INT64_MIN) fetch(p, w, ring + (buf ^ 1) * 4 * kInput, next);
+  const uint32_t in = INSIDE ? ~0u : t.in[warp * R >> 5] >> (warp * R & 31),
+                 first = INSIDE ? 0u : t.first[warp * R >> 5] >> (warp * R & 31),
+                 last = INSIDE ? 0u : t.last[warp * R >> 5] >> (warp * R & 31);
+
+  float e[R][2], m[R][2], si[R][2], sr[R][2], b[R][2];
+  float4 down = make_float4(1.0f, 1.0f, 0.0f, 0.0f), up = down;
 #pragma unroll
   for (int j = 0; j < R; ++j) {
-    float x[2], b[2];
+    float x[2];
     get2(mine + j * kCols, x);
-    get2(mine + (kTile + j) * kCols, k.si[j]);
-    get2(mine + (2 * kTile + j) * kCols, k.sr[j]);
-    sigmoid2<T>(k.si[j], k.si[j]);
-    sigmoid2<T>(k.sr[j], k.sr[j]);
-    decay2<T, FAST>(k.sr[j], ac[0], ac[1], k.e[j], k.m[j]);
-    mul2(b[0], b[1], k.m[j][0], k.m[j][1], k.si[j][0], k.si[j][1]);
-    mul2(b[0], b[1], b[0], b[1], x[0], x[1]);
-    if constexpr (!INSIDE) {
-      const int row = warp * R + j;
-      if (!(t.in[row >> 5] >> (row & 31) & 1)) {
-        k.e[j][0] = k.e[j][1] = 1.0f;
-        b[0] = b[1] = 0.0f;
-      }
-      if (t.first[row >> 5] >> (row & 31) & 1) {
-        float h[2];
-        start_state<2>(p, t.seq[row], c, cols, h);
-        fma2(b[0], b[1], k.e[j][0], k.e[j][1], h[0], h[1], b[0], b[1]);
-        down = make_float4(kCut, kCut, b[0], b[1]);
-        continue;
-      }
+    get2(mine + kInput + j * kCols, si[j]);
+    get2(mine + 2 * kInput + j * kCols, sr[j]);
+    sigmoid2<T>(si[j], si[j]);
+    sigmoid2<T>(sr[j], sr[j]);
+    decay2<T, FAST>(sr[j], w.ac[0], w.ac[1], e[j], m[j]);
+    mul2(b[j][0], b[j][1], m[j][0], m[j][1], si[j][0], si[j][1]);
+    mul2(b[j][0], b[j][1], b[j][0], b[j][1], x[0], x[1]);
+    if (!INSIDE && !(in >> j & 1)) {
+      e[j][0] = e[j][1] = 1.0f;
+      b[j][0] = b[j][1] = 0.0f;
     }
-    compose<!INSIDE>(down, make_float4(k.e[j][0], k.e[j][1], b[0], b[1]));
+    if (!INSIDE && (first >> j & 1)) {
+      float h0[2];
+      start_state<2>(p, t.seq[warp * R + j], w.c, w.cols, h0);
+      fma2(h0[0], h0[1], e[j][0], e[j][1], h0[0], h0[1], b[j][0], b[j][1]);
+      down = make_float4(kCut, kCut, h0[0], h0[1]);
+    } else {
+      compose<!INSIDE>(down, make_float4(e[j][0], e[j][1], b[j][0], b[j][1]));
+    }
   }
 #pragma unroll
   for (int j = R - 1; j >= 0; --j) {
     float g[2];
-    get2(mine + (3 * kTile + j) * kCols, g);
-    if constexpr (!INSIDE) {
-      const int row = warp * R + j;
-      if (!(t.in[row >> 5] >> (row & 31) & 1)) continue;
-      if (t.last[row >> 5] >> (row & 31) & 1) {
-        end_gradient(p, t.seq[row], c, cols, g);
-        mul2(g[0], g[1], g[0], g[1], k.e[j][0], k.e[j][1]);
-        up = make_float4(kCut, kCut, g[0], g[1]);
-        continue;
+    get2(mine + 3 * kInput + j * kCols, g);
+    if (!INSIDE && !(in >> j & 1)) continue;
+    const bool end = !INSIDE && (last >> j & 1);
+    if (end) end_gradient(p, t.seq[warp * R + j], w.c, w.cols, g);
+    mul2(g[0], g[1], g[0], g[1], e[j][0], e[j][1]);
+    if (end) up = make_float4(kCut, kCut, g[0], g[1]);
+    else compose<!INSIDE>(up, make_float4(e[j][0], e[j][1], g[0], g[1]));
+  }
+  sh.down[warp][lane] = down;
+  sh.up[warp][lane] = up;
+  const bool cut = !INSIDE && (t.last[0] | t.last[1]) != 0;
+  __syncthreads();
+  // the pair of the rows behind this warp's in the tile, and of the whole tile
+  float4 behind = make_float4(1.0f, 1.0f, 0.0f, 0.0f), whole = sh.up[W - 1][lane];
+#pragma unroll
+  for (int k = W - 2; k >= 0; --k) {
+    if (k == warp) behind = whole;
+    compose<!INSIDE>(whole, sh.up[k][lane]);
+  }
+  if (w.size > 1) {
+    if (threadIdx.x == 0) mail_expect(sh.mail, buf, w.size);
+    if (warp < w.size) mail_send(sh.mail, buf, w.rank, warp, whole, cut);
+  }
+  // the states before each row, meanwhile
+#pragma unroll
+  for (int k = 0; k < W - 1; ++k)
+    if (k < warp) through<!INSIDE>(sh.down[k][lane], h);
+#pragma unroll
+  for (int j = 0; j < R; ++j) {
+    if (!INSIDE && (first >> j & 1)) start_state<2>(p, t.seq[warp * R + j], w.c, w.cols, h);
+    const float b0 = b[j][0], b1 = b[j][1];
+    b[j][0] = h[0], b[j][1] = h[1];  // (from here on the state before the row)
+    if (INSIDE || (in >> j & 1)) fma2(h[0], h[1], e[j][0], e[j][1], h[0], h[1], b0, b1);
+  }
+  // the gradient that comes to this warp's last row from the rows behind it
+  float gc[2] = {carry.g[0], carry.g[1]};
+  if (w.size > 1) {
+    mail_wait(sh.mail, buf, parity);
+    bool cuts = false;
+    for (int k = 0; k < w.size; ++k) cuts = cuts || sh.mail.cut[buf][k] != 0;
+    if (cuts) {
+      for (int k = 0; k < w.size; ++k) {
+        if (k == w.rank) gc[0] = carry.g[0], gc[1] = carry.g[1];
+        through<true>(sh.mail.pair[buf][k][lane], carry.g);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < kMaxCluster; ++k) {
+        if (k >= w.size) break;
+        if (k == w.rank) gc[0] = carry.g[0], gc[1] = carry.g[1];
+        through<false>(sh.mail.pair[buf][k][lane], carry.g);
       }
     }
-    mul2(g[0], g[1], g[0], g[1], k.e[j][0], k.e[j][1]);
-    compose<!INSIDE>(up, make_float4(k.e[j][0], k.e[j][1], g[0], g[1]));
+  } else {
+    through<!INSIDE>(whole, carry.g);
   }
+  through<!INSIDE>(behind, gc);
+
+  const int64_t row0 = tile * kTile + warp * R;
+  T* dx_at = static_cast<T*>(p.dx) + row0 * p.dxs + w.c;
+  T* di_at = static_cast<T*>(p.dig) + row0 * p.dis + w.c;
+  T* dr_at = static_cast<T*>(p.drg) + row0 * p.drs + w.c;
+  const bool pairs = p.pairs && w.cols == 2;
+#pragma unroll
+  for (int j = R - 1; j >= 0; --j) {
+    float g[2], x[2], dx[2], di[2], dr[2], t1[2], t2[2];
+    get2(mine + j * kCols, x);
+    get2(mine + 3 * kInput + j * kCols, g);
+    if (!INSIDE && (last >> j & 1)) end_gradient(p, t.seq[warp * R + j], w.c, w.cols, g);
+    else g[0] += gc[0], g[1] += gc[1];
+    // dx = g m i,  di = dx x (1 - i)
+    mul2(dx[0], dx[1], m[j][0], m[j][1], si[j][0], si[j][1]);
+    mul2(dx[0], dx[1], dx[0], dx[1], g[0], g[1]);
+    mul2(di[0], di[1], dx[0], dx[1], x[0], x[1]);
+    mul2(di[0], di[1], di[0], di[1], 1.0f - si[j][0], 1.0f - si[j][1]);
+    // g e r (h - i x e / m)
+    float over[2];
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      over[v] = Elem<T>::kExactSilu ? 1.0f / m[j][v] : rcp_approx(m[j][v]);
+      if (!(m[j][v] > 0.0f)) over[v] = 0.0f;
+    }
+    mul2(t2[0], t2[1], si[j][0], si[j][1], x[0], x[1]);
+    mul2(t2[0], t2[1], t2[0], t2[1], -e[j][0], -e[j][1]);
+    fma2(t1[0], t1[1], t2[0], t2[1], over[0], over[1], b[j][0], b[j][1]);
+    mul2(t2[0], t2[1], e[j][0], e[j][1], sr[j][0], sr[j][1]);
+    mul2(t1[0], t1[1], t1[0], t1[1], t2[0], t2[1]);
+    mul2(t1[0], t1[1], t1[0], t1[1], g[0], g[1]);
+    mul2(dr[0], dr[1], t1[0], t1[1], w.ac[0], w.ac[1]);
+    mul2(dr[0], dr[1], dr[0], dr[1], 1.0f - sr[j][0], 1.0f - sr[j][1]);
+    if (INSIDE || (in >> j & 1)) {
+      carry.da[0] += t1[0], carry.da[1] += t1[1];
+      mul2(gc[0], gc[1], e[j][0], e[j][1], g[0], g[1]);
+    } else {  // a row of no sequence
+#pragma unroll
+      for (int v = 0; v < 2; ++v) dx[v] = di[v] = dr[v] = 0.0f;
+    }
+    if (INSIDE || (row0 + j >= w.lo && row0 + j < w.hi)) {
+      if (pairs) {
+        Raw<T, 2>::put(dx_at + j * p.dxs, dx);
+        Raw<T, 2>::put(di_at + j * p.dis, di);
+        Raw<T, 2>::put(dr_at + j * p.drs, dr);
+      } else {
+        put2<T>(dx_at, j * p.dxs, dx, w.cols, false);
+        put2<T>(di_at, j * p.dis, di, w.cols, false);
+        put2<T>(dr_at, j * p.drs, dr, w.cols, false);
+      }
+    }
+    if (!INSIDE && p.dinitial && (first >> j & 1)) {
+      const int64_t s = t.seq[warp * R + j];
+      const bool resumes = seq_slot(p.q, s) >= 0 && seq_resumes(p.q, s);
+#pragma unroll
+      for (int v = 0; v < 2; ++v)
+        if (v < w.cols) p.dinitial[s * p.width + w.c + v] = resumes ? gc[v] : 0.0f;
+    }
+  }
+  // (the next turn's search writes rows, its copies the tile)
+  if (!INSIDE || stages<T>() == 1) __syncthreads();
+  if (stages<T>() == 1 && next != INT64_MIN) fetch(p, w, ring, next);
+  return carry;
+}
+template <typename T, bool INSIDE, bool FAST>
+__device__ __noinline__ Carry turn_apart(const Params& p, Place w, Shared& sh, T* ring,
+                                         int64_t tile, int64_t next, int64_t turn, Carry carry) {
+  return turn_of<T, INSIDE, FAST>(p, w, sh, ring, tile, next, turn, carry);
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) k_recur_backward(const Params p, int stages) {
+__global__ void __launch_bounds__(kThreads, 2)
+    k_recur_backward(const __grid_constant__ Params p) {
   extern __shared__ uint4 s_tile[];
-  __shared__ BackwardShared sh;
-  constexpr int kInput = kTile * kCols;  // elements of an input's tile
+  __shared__ Shared sh;
+  T* const ring = reinterpret_cast<T*>(s_tile);  // x, input gate, decay gate, dout
   pdl_wait();
   pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = static_cast<int>(cluster_rank()), size = static_cast<int>(cluster_size());
-  const int64_t c0 = static_cast<int64_t>(blockIdx.y) * kCols, c = c0 + lane * 2;
-  const int cols = c >= p.width ? 0 : p.width - c < 2 ? 1 : 2;
-  cluster_arrive();  // (every CTA has begun before another one writes to it)
-  const int64_t lo = segment_begin(p, blockIdx.z), hi = segment_begin(p, blockIdx.z + 1);
-  const int64_t tile0 = lo / kTile, tiles = hi > lo ? (hi + kTile - 1) / kTile - tile0 : 0;
-  const int64_t turns = (tiles + size - 1) / size;
-  const int64_t top = tile0 + tiles - 1;  // the last tile
-  const auto fetch = [&](int64_t tile, T* to) {
-    copy_tile<T, kThreads>(to, p.x, p.xs, c0, p.width, tile, lo, hi, p.chunk);
-    copy_tile<T, kThreads>(to + kInput, p.ig, p.is, c0, p.width, tile, lo, hi, p.chunk);
-    copy_tile<T, kThreads>(to + 2 * kInput, p.rg, p.rs, c0, p.width, tile, lo, hi, p.chunk);
-    copy_tile<T, kThreads>(to + 3 * kInput, p.dout, p.gs, c0, p.width, tile, lo, hi, p.chunk);
-  };
-  T* const ring = reinterpret_cast<T*>(s_tile);
-  if (turns > 0) fetch(top - rank, ring);
-  float ac[2];
-#pragma unroll
-  for (int v = 0; v < 2; ++v) ac[v] = v < cols ? __ldg(p.a + c + v) : 0.0f;
-  const bool fast = __all_sync(0xffffffffu, ac[0] > kSeries && ac[1] > kSeries);
-  cluster_wait();
+  mail_init(sh.mail);
+  all_arrive();  // (every CTA has begun before another one writes to it)
+  const Place w = find_place(p);
+  const int64_t tile0 = w.lo / kTile, count = w.hi > w.lo ? (w.hi + kTile - 1) / kTile - tile0 : 0;
+  const int64_t turns = (count + w.size - 1) / w.size;
+  int64_t tile = tile0 + count - 1 - w.rank;
+  if (turns > 0) fetch(p, w, ring, tile);
+  const bool fast = __all_sync(0xffffffffu, w.ac[0] > kSeries && w.ac[1] > kSeries);
+  all_wait();
 
-  float carry[2] = {0.0f, 0.0f}, da[2] = {0.0f, 0.0f};
+  Carry carry = {};
   Rows known;
-  for (int64_t turn = 0; turn < turns; ++turn) {
-    const int64_t tile = top - (turn * size + rank);
-    const int buf = turn & 1;
-    const T* const mine = ring + (stages == 2 ? buf : 0) * 4 * kInput;
-    const bool inside = tile * kTile >= lo && known.inside(tile);
-    if (!inside && threadIdx.x < kTile) place_rows(p.q, tile, lo, hi, &sh.rows);
-    float h[2];  // the state before the tile, as it was kept
-#pragma unroll
-    for (int v = 0; v < 2; ++v)
-      h[v] = tile * kTile >= lo && v < cols ? __ldg(p.saved + tile * p.width + c + v) : 0.0f;
+  for (int64_t turn = 0; turn < turns; ++turn, tile -= w.size) {
+    const int64_t next = turn + 1 < turns ? tile - w.size : INT64_MIN;
+    const bool inside = tile * kTile >= w.lo && known.inside(tile);
+    if (!inside && threadIdx.x < kTile) place_rows(p.q, tile, w.lo, w.hi, &sh.rows);
     copies_wait();
     __syncthreads();
-    if (stages == 2 && turn + 1 < turns) fetch(tile - size, ring + (buf ^ 1) * 4 * kInput);
-
-    BackwardRows k;
-    {
-      float4 down, up;
-      if (inside) {
-        if (fast) backward_rows<T, true, true>(p, mine, ac, sh.rows, c, cols, k, down, up);
-        else backward_rows<T, true, false>(p, mine, ac, sh.rows, c, cols, k, down, up);
-      } else {
-        backward_rows<T, false, false>(p, mine, ac, sh.rows, c, cols, k, down, up);
-      }
-      sh.down[warp][lane] = down;
-      sh.up[warp][lane] = up;
-    }
-    const uint32_t in = inside ? ~0u : sh.rows.in[warp * R >> 5] >> (warp * R & 31),
-                   first = inside ? 0u : sh.rows.first[warp * R >> 5] >> (warp * R & 31),
-                   last = inside ? 0u : sh.rows.last[warp * R >> 5] >> (warp * R & 31);
-    const bool cut = !inside && (sh.rows.last[0] | sh.rows.last[1]) != 0;
-    if (!inside) {  // (of the tile's first row: its tiles come next)
-      int64_t b, e;
-      known.begin = known.end = 0;
-      if (tile * kTile >= lo && tile * kTile < hi) {
-        seq_range(p.q, sh.rows.seq[0], b, e);
-        known.begin = b, known.end = e;
-      }
-    }
-    __syncthreads();
-    // the pair of the rows behind this warp's in the tile, and of the whole tile
-    float4 behind, whole = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
-    const auto fold = [&](auto cuts) {
-#pragma unroll
-      for (int w = W - 1; w >= 0; --w) {
-        if (w == warp) behind = whole;
-        compose<decltype(cuts)::value>(whole, sh.up[w][lane]);
-      }
-    };
-    if (cut) fold(std::true_type());
-    else fold(std::false_type());
-    if (size > 1) {
-      if (warp < size) {
-        put_peer(&sh.peer[buf][rank][lane], warp, whole);
-        if (lane == 0) put_peer_int(&sh.cut[buf][rank], warp, cut);
-      }
-      cluster_arrive();
-    }
-    // the states before each row, meanwhile
-    float hp[R][2];
-#pragma unroll
-    for (int w = 0; w < W - 1; ++w) {
-      if (w < warp) {
-        if (inside) through<false>(sh.down[w][lane], h);
-        else through<true>(sh.down[w][lane], h);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < R; ++j) {
-      if (first >> j & 1) start_state<2>(p, sh.rows.seq[warp * R + j], c, cols, h);
-      float x[2], b[2];
-      get2(mine + (warp * R + j) * kCols + lane * 2, x);
-      mul2(b[0], b[1], k.m[j][0], k.m[j][1], k.si[j][0], k.si[j][1]);
-      mul2(b[0], b[1], b[0], b[1], x[0], x[1]);
-      hp[j][0] = h[0], hp[j][1] = h[1];
-      if (in >> j & 1) fma2(h[0], h[1], k.e[j][0], k.e[j][1], h[0], h[1], b[0], b[1]);
-    }
-
-    // the gradient that comes to this warp's last row from the rows behind it
-    float gc[2];
-    if (size > 1) {
-      cluster_wait();
-      bool cuts = false;
-      for (int q = 0; q < size; ++q) cuts = cuts || sh.cut[buf][q] != 0;
-      const auto pass = [&](auto some) {
-        for (int q = 0; q < size; ++q) {
-          if (q == rank) gc[0] = carry[0], gc[1] = carry[1];
-          through<decltype(some)::value>(sh.peer[buf][q][lane], carry);
-        }
-      };
-      if (cuts) pass(std::true_type());
-      else pass(std::false_type());
+    if (inside && fast) {
+      carry = turn_of<T, true, true>(p, w, sh, ring, tile, next, turn, carry);
+    } else if (inside) {
+      carry = turn_apart<T, true, false>(p, w, sh, ring, tile, next, turn, carry);
     } else {
-      gc[0] = carry[0], gc[1] = carry[1];
-      through<true>(whole, carry);
+      // (of the tile's first row: the tiles before it come next)
+      known.begin = known.end = 0;
+      if (tile * kTile >= w.lo && tile * kTile < w.hi)
+        seq_range(p.q, sh.rows.seq[0], known.begin, known.end);
+      carry = turn_apart<T, false, false>(p, w, sh, ring, tile, next, turn, carry);
     }
-    through<true>(behind, gc);
-#pragma unroll
-    for (int j = R - 1; j >= 0; --j) {
-      const int row = warp * R + j;
-      const int64_t r = tile * kTile + row;
-      float g[2], x[2], dx[2], di[2], dr[2], t1[2], t2[2];
-      get2(mine + row * kCols + lane * 2, x);
-      get2(mine + 3 * kInput + row * kCols + lane * 2, g);
-      const float(&e)[2] = k.e[j], (&m)[2] = k.m[j], (&si)[2] = k.si[j], (&sr)[2] = k.sr[j];
-      if (last >> j & 1) end_gradient(p, sh.rows.seq[row], c, cols, g);
-      else fma2(g[0], g[1], g[0], g[1], 1.0f, 1.0f, gc[0], gc[1]);
-      // dx = g m i,  di = dx x (1 - i)
-      mul2(dx[0], dx[1], m[0], m[1], si[0], si[1]);
-      mul2(dx[0], dx[1], dx[0], dx[1], g[0], g[1]);
-      fma2(di[0], di[1], si[0], si[1], -1.0f, -1.0f, 1.0f, 1.0f);
-      mul2(di[0], di[1], di[0], di[1], x[0], x[1]);
-      mul2(di[0], di[1], di[0], di[1], dx[0], dx[1]);
-      // g (h e r - i x e^2 r / m)
-      float over[2];
-#pragma unroll
-      for (int v = 0; v < 2; ++v)
-        over[v] = m[v] > 0.0f ? (Elem<T>::kExactSilu ? 1.0f / m[v] : rcp_approx(m[v])) : 0.0f;
-      mul2(t2[0], t2[1], si[0], si[1], x[0], x[1]);
-      mul2(t2[0], t2[1], t2[0], t2[1], e[0], e[1]);
-      mul2(t2[0], t2[1], t2[0], t2[1], over[0], over[1]);
-      fma2(t1[0], t1[1], t2[0], t2[1], -1.0f, -1.0f, hp[j][0], hp[j][1]);
-      mul2(t2[0], t2[1], e[0], e[1], sr[0], sr[1]);
-      mul2(t1[0], t1[1], t1[0], t1[1], t2[0], t2[1]);
-      mul2(t1[0], t1[1], t1[0], t1[1], g[0], g[1]);
-      fma2(dr[0], dr[1], sr[0], sr[1], -1.0f, -1.0f, 1.0f, 1.0f);
-      mul2(dr[0], dr[1], dr[0], dr[1], ac[0], ac[1]);
-      mul2(dr[0], dr[1], dr[0], dr[1], t1[0], t1[1]);
-      if (in >> j & 1) {
-        fma2(da[0], da[1], t1[0], t1[1], 1.0f, 1.0f, da[0], da[1]);
-        mul2(gc[0], gc[1], e[0], e[1], g[0], g[1]);
-      } else {  // a row of no sequence
-#pragma unroll
-        for (int v = 0; v < 2; ++v) dx[v] = di[v] = dr[v] = 0.0f;
-      }
-      if (inside || (r >= lo && r < hi)) {
-        put2<T>(p.dx, r * p.dxs + c, dx, cols, p.pairs);
-        put2<T>(p.dig, r * p.dis + c, di, cols, p.pairs);
-        put2<T>(p.drg, r * p.drs + c, dr, cols, p.pairs);
-      }
-      if (p.dinitial && (first >> j & 1)) {
-        const int64_t s = sh.rows.seq[row];
-        const bool resumes = seq_slot(p.q, s) >= 0 && seq_resumes(p.q, s);
-#pragma unroll
-        for (int v = 0; v < 2; ++v)
-          if (v < cols) p.dinitial[s * p.width + c + v] = resumes ? gc[v] : 0.0f;
-      }
-    }
-    // (the next turn's search writes rows, its copies the tile)
-    if (!inside || stages == 1) __syncthreads();
-    if (stages == 1 && turn + 1 < turns) fetch(tile - size, ring);
   }
   if (p.dinitial && warp == 0) {
-    each_empty(p.q, static_cast<int64_t>(blockIdx.z) * size + rank,
-               static_cast<int64_t>(size) * p.segments, [&](int64_t s) {
+    each_empty(p.q, static_cast<int64_t>(blockIdx.z) * w.size + w.rank,
+               static_cast<int64_t>(w.size) * p.segments, [&](int64_t s) {
                  const bool keep = p.dstate && seq_slot(p.q, s) >= 0 && seq_resumes(p.q, s);
-                 for (int v = 0; v < cols; ++v) {
-                   const int64_t k = s * p.width + c + v;
+                 for (int v = 0; v < w.cols; ++v) {
+                   const int64_t k = s * p.width + w.c + v;
                    p.dinitial[k] = keep ? __ldg(p.dstate + k) : 0.0f;
                  }
                });
   }
   // da: the warps' sums, then the CTAs' in rank 0
   __syncthreads();
-  sh.up[warp][lane] = make_float4(da[0], da[1], 0.0f, 0.0f);
+  sh.up[warp][lane] = make_float4(carry.da[0], carry.da[1], 0.0f, 0.0f);
   __syncthreads();
   if (warp == 0) {
     float4 t = sh.up[0][lane];
-    for (int w = 1; w < W; ++w) t.x += sh.up[w][lane].x, t.y += sh.up[w][lane].y;
-    put_peer(&sh.peer[turns & 1][rank][lane], 0, t);
+    for (int k = 1; k < W; ++k) t.x += sh.up[k][lane].x, t.y += sh.up[k][lane].y;
+    put_peer(&sh.mail.pair[turns & 1][w.rank][lane], 0, t);
+    if (lane == 0 && sh.mail.failed) atomicOr(p.fault, kFaultRecurWait);
   }
-  cluster_arrive();
-  cluster_wait();
-  if (rank == 0 && warp == 0) {
+  all_arrive();
+  all_wait();
+  if (w.rank == 0 && warp == 0) {
     float t[2] = {0.0f, 0.0f};
-    for (int q = 0; q < size; ++q) {
-      t[0] += sh.peer[turns & 1][q][lane].x;
-      t[1] += sh.peer[turns & 1][q][lane].y;
+    for (int k = 0; k < w.size; ++k) {
+      t[0] += sh.mail.pair[turns & 1][k][lane].x;
+      t[1] += sh.mail.pair[turns & 1][k][lane].y;
     }
 #pragma unroll
     for (int v = 0; v < 2; ++v)
-      if (v < cols) p.da[blockIdx.z * p.width + c + v] = t[v];
+      if (v < w.cols) p.da[blockIdx.z * p.width + w.c + v] = t[v];
   }
 }
+
+}  // namespace backward
 
 // out[c] = the sum of in[k, c] over the segments.
 __global__ void __launch_bounds__(256) k_recur_sum(const float* in, float* out, int64_t width,
@@ -973,12 +1083,12 @@ Split split_rows(int64_t rows, int64_t seqs, int64_t blocks, int resident) {
 }
 
 template <typename... P, typename... A>
-int launch_cluster(void (*kernel)(P...), int64_t blocks, Split s, int smem, cudaStream_t stream,
-                   A... args) {
+int launch_cluster(void (*kernel)(P...), int64_t blocks, Split s, int threads, int smem,
+                   cudaStream_t stream, A... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(s.cluster), static_cast<unsigned>(blocks),
                      static_cast<unsigned>(s.segments));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = stream;
   cudaLaunchAttribute at[2];
@@ -1005,30 +1115,34 @@ int launch_forward(Params& p, cudaStream_t s) {
   const int64_t blocks = blocks_of(p.width);
   const Split k = split_rows(p.q.rows, p.q.seqs, blocks, sizeof(T) == 2 ? 4 : 3);
   p.segments = k.segments;
+  p.fault = device_fault_word();
+  if (!p.fault) return GGRN_ERR_CUDA;
+  if (p.mute && k.cluster == 1) return GGRN_ERR_UNSUPPORTED;
   constexpr int kSmem = 3 * kTile * kCols * sizeof(T);
-  const cudaError_t e = allow_shared_memory<k_recur<T>>(kSmem);
+  const cudaError_t e = allow_shared_memory<forward::k_recur<T>>(kSmem);
   if (e != cudaSuccess) {
     record_cuda_error(e);
     return GGRN_ERR_CUDA;
   }
-  return launch_cluster(k_recur<T>, blocks, k, kSmem, s, p);
+  return launch_cluster(forward::k_recur<T>, blocks, k, forward::kThreads, kSmem, s, p);
 }
 template <typename T>
 int launch_backward(Params& p, float* sums, cudaStream_t s) {
   const int64_t blocks = blocks_of(p.width);
   const Split k = split_rows(p.q.rows, p.q.seqs, blocks, 2);
   p.segments = k.segments;
+  p.fault = device_fault_word();
+  if (!p.fault) return GGRN_ERR_CUDA;
   float* const da = p.da;
   if (k.segments > 1) p.da = sums;
-  // two tiles of 16-bit types in shared memory, one of f32
-  constexpr int kStages = sizeof(T) == 2 ? 2 : 1;
-  constexpr int kSmem = kStages * 4 * kTile * kCols * sizeof(T);
-  const cudaError_t e = allow_shared_memory<k_recur_backward<T>>(kSmem);
+  constexpr int kSmem = backward::stages<T>() * 4 * kTile * kCols * sizeof(T);
+  const cudaError_t e = allow_shared_memory<backward::k_recur_backward<T>>(kSmem);
   if (e != cudaSuccess) {
     record_cuda_error(e);
     return GGRN_ERR_CUDA;
   }
-  const int st = launch_cluster(k_recur_backward<T>, blocks, k, kSmem, s, p, kStages);
+  const int st = launch_cluster(backward::k_recur_backward<T>, blocks, k, backward::kThreads, kSmem,
+                                s, p);
   if (st != GGRN_OK || k.segments == 1) return st;
   return mixer::launch(k_recur_sum, dim3(static_cast<unsigned>((p.width + 255) / 256)), 256, 0, s,
                        static_cast<const float*>(sums), da, p.width, k.segments);
@@ -1238,7 +1352,7 @@ int check_backward(const ggrn_recur_backward_call& c, Params* p) {
 }
 
 template <typename T>
-int backward(Params& p, const Space& need, void* workspace, cudaStream_t s) {
+int run_kernels(Params& p, const Space& need, void* workspace, cudaStream_t s) {
   if (!p.saved && p.q.rows > 0) {
     Params f = p;
     p.saved = f.saved = static_cast<float*>(workspace);
@@ -1262,9 +1376,9 @@ int run_backward(const ggrn_recur_backward_call* call, void* stream) {
   const Space need = space_of(c);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   void* const w = c.workspace;
-  if (c.dtype == kF32) return backward<float>(p, need, w, s);
-  if (c.dtype == kF16) return backward<__half>(p, need, w, s);
-  return backward<__nv_bfloat16>(p, need, w, s);
+  if (c.dtype == kF32) return run_kernels<float>(p, need, w, s);
+  if (c.dtype == kF16) return run_kernels<__half>(p, need, w, s);
+  return run_kernels<__nv_bfloat16>(p, need, w, s);
 }
 
 }  // namespace recur
