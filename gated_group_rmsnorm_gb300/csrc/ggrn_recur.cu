@@ -22,6 +22,7 @@
 // tile finds its own; without them a first launch makes them.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <initializer_list>
 #include <type_traits>
 
@@ -104,8 +105,10 @@ struct Raw<T, 1> {
 // decays are slow (an exponential that is off by an ulp to one side next to 1 is
 // off by a thousand after a thousand rows), and slow channels take no second
 // exponential.  FAST: no decay of the warp's channels is below exp(-1/4).
-// (Constants stand in scalar instructions, which hold them; pairs would need
-// them in registers.)
+//
+// The arithmetic is on pairs, and so are its constants: a loop over rows keeps them
+// in registers (Constants, made by instructions that the compiler does not repeat),
+// since a pair of constants costs two moves wherever it is used otherwise.
 // ---------------------------------------------------------------------------
 constexpr float kSeries = -0.25f;
 
@@ -115,14 +118,45 @@ __device__ __forceinline__ float sqrt_approx(float x) {
   return y;
 }
 
+using Two = unsigned long long;  // two f32
+__device__ __forceinline__ Two fma(Two a, Two b, Two c) {
+  Two r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ Two mul(Two a, Two b) {
+  Two r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Two add(Two a, Two b) {
+  Two r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+template <typename F>
+__device__ __forceinline__ Two each(Two a, F f) {
+  float x, y;
+  upk2(a, x, y);
+  return pk2(f(x), f(y));
+}
+__device__ __forceinline__ Two held(float v) {
+  Two r;
+  asm volatile("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(v));
+  return r;
+}
+struct Constants {
+  Two c4 = held(7.67176877707243e-3f), c3 = held(4.1564859449863434e-2f),
+      c2 = held(1.666616052389145e-1f), c1 = held(4.999999701976776e-1f), one = held(1.0f),
+      two = held(2.0f), minus = held(-1.0f), log2e = held(-1.4426950408889634f);
+};
+
 template <typename T>
-__device__ __forceinline__ void sigmoid2(const float* z, float* s) {
+__device__ __forceinline__ Two sigmoid2(Two z, const Constants& k) {
   if constexpr (Elem<T>::kExactSilu) {
-    s[0] = 1.0f / (1.0f + expf(-z[0]));
-    s[1] = 1.0f / (1.0f + expf(-z[1]));
+    return each(z, [](float v) { return 1.0f / (1.0f + expf(-v)); });
   } else {
-#pragma unroll
-    for (int k = 0; k < 2; ++k) s[k] = rcp_approx(1.0f + ex2_approx(z[k] * -1.4426950408889634f));
+    return each(add(each(mul(z, k.log2e), ex2_approx), k.one), rcp_approx);
   }
 }
 
@@ -140,29 +174,56 @@ __device__ __forceinline__ void beyond_series(float p, float& e, float& less) {
 
 // From r and the channels' a: e = exp(a r), m = sqrt(1 - e^2).
 template <typename T, bool FAST>
-__device__ __forceinline__ void decay2(const float* r, float a0, float a1, float* e, float* m) {
-  float p[2];
-  mul2(p[0], p[1], a0, a1, r[0], r[1]);
-  float s[2];
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    float c = fmaf(7.67176877707243e-3f, p[k], 4.1564859449863434e-2f);
-    c = fmaf(c, p[k], 1.666616052389145e-1f);
-    c = fmaf(c, p[k], 4.999999701976776e-1f);
-    c = fmaf(c, p[k], 1.0f);
-    s[k] = c * p[k];  // e - 1
-    e[k] = 1.0f + s[k];
-  }
+__device__ __forceinline__ void decay2(Two r, Two a, const Constants& k, Two& e, Two& m) {
+  const Two p = mul(a, r);
+  Two s = fma(fma(fma(fma(p, k.c4, k.c3), p, k.c2), p, k.c1), p, k.one);
+  s = mul(s, p);  // e - 1
+  e = add(s, k.one);
   if constexpr (!FAST) {
+    float pv[2], ev[2], sv[2];
+    upk2(p, pv[0], pv[1]), upk2(e, ev[0], ev[1]), upk2(s, sv[0], sv[1]);
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-      if (!(p[k] > kSeries)) beyond_series<T>(p[k], e[k], s[k]);
+    for (int i = 0; i < 2; ++i)
+      if (!(pv[i] > kSeries)) beyond_series<T>(pv[i], ev[i], sv[i]);
+    e = pk2(ev[0], ev[1]), s = pk2(sv[0], sv[1]);
   }
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const float q = -s[k] * (2.0f + s[k]);
-    m[k] = Elem<T>::kExactSilu ? sqrtf(q) : sqrt_approx(q);
-  }
+  m = each(mul(s, add(s, k.two)), [](float q) {
+    return Elem<T>::kExactSilu ? sqrtf(-q) : sqrt_approx(-q);
+  });
+}
+
+// ---------------------------------------------------------------------------
+// Pairs (E, B): v -> E v + B, of a lane's two channels.  Where a sequence starts
+// (or, for gradients, ends) among the rows of a pair, nothing comes in from before
+// them: E is kCut.  (Not 0: a value that is not finite would leave its sequence.)
+// CUTS: some pair may be cut.
+// ---------------------------------------------------------------------------
+struct Pair {
+  Two e, b;
+};
+constexpr uint32_t kCutWord = 0xbf800000u;  // -1: decays are not negative
+constexpr Two kCut = (static_cast<Two>(kCutWord) << 32) | kCutWord;
+constexpr Two kOnes = 0x3f8000003f800000ull;
+__device__ __forceinline__ bool is_cut(const Pair& s) {
+  return static_cast<uint32_t>(s.e) == kCutWord;
+}
+template <bool CUTS>
+__device__ __forceinline__ Two through(const Pair& s, Two v) {
+  return CUTS && is_cut(s) ? s.b : fma(s.e, v, s.b);
+}
+// First s, then t.
+template <bool CUTS>
+__device__ __forceinline__ Pair compose(const Pair& s, const Pair& t) {
+  if (CUTS && is_cut(t)) return t;
+  return {CUTS && is_cut(s) ? kCut : mul(s.e, t.e), fma(t.e, s.b, t.b)};
+}
+// In shared memory: 16 bytes.
+__device__ __forceinline__ Pair get_pair(const ulonglong2* p) {
+  const ulonglong2 v = *p;
+  return {v.x, v.y};
+}
+__device__ __forceinline__ void put_pair(ulonglong2* p, const Pair& s) {
+  *p = make_ulonglong2(s.e, s.b);
 }
 
 // ---------------------------------------------------------------------------
@@ -180,10 +241,8 @@ __device__ __forceinline__ void all_wait() {
   asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 // Stores v at the place of *mine in the shared memory of CTA `rank`.
-__device__ __forceinline__ void put_peer(const float4* mine, uint32_t rank, float4 v) {
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
-                   map_to_rank(smem_u32(mine), rank)),
-               "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+__device__ __forceinline__ void put_peer(const ulonglong2* mine, uint32_t rank, Two v) {
+  asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(map_to_rank(smem_u32(mine), rank)), "l"(v)
                : "memory");
 }
 
@@ -199,9 +258,9 @@ __device__ __forceinline__ void put_peer(const float4* mine, uint32_t rank, floa
 // has ended.
 constexpr uint32_t kFaultRecurWait = 128u;
 constexpr long long kWaitClocks = 2000000000ll;
-struct Mail {
-  float4 pair[2][kMaxCluster][32];
-  int cut[2][kMaxCluster];
+struct alignas(16) Mail {
+  ulonglong2 pair[2][kMaxCluster][32];
+  int cut[2][kMaxCluster];  // (of CTAs that the cluster has not: 0)
   unsigned long long landed[2];
   volatile uint32_t failed;
 };
@@ -224,6 +283,7 @@ __device__ __noinline__ void wait_poll(uint32_t bar, uint32_t parity, volatile u
 }
 // Before the arrival of every CTA of the cluster that comes before its first mail.
 __device__ __forceinline__ void mail_init(Mail& m) {
+  if (threadIdx.x < 2 * kMaxCluster) (&m.cut[0][0])[threadIdx.x] = 0;
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&m.landed[0]), 1);
     mbar_init(smem_u32(&m.landed[1]), 1);
@@ -232,14 +292,14 @@ __device__ __forceinline__ void mail_init(Mail& m) {
   }
 }
 // A whole warp sends to CTA `to`.
-__device__ __forceinline__ void mail_send(Mail& m, int buf, int rank, int to, const float4& v,
+__device__ __forceinline__ void mail_send(Mail& m, int buf, int rank, int to, const Pair& v,
                                           bool cut) {
   const int lane = threadIdx.x & 31;
   const uint32_t bar = map_to_rank(smem_u32(&m.landed[buf]), to);
   asm volatile(
-      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];"
-      ::"r"(map_to_rank(smem_u32(&m.pair[buf][rank][lane]), to)),
-      "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(bar)
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b64 [%0], {%1, %2}, [%3];" ::"r"(
+          map_to_rank(smem_u32(&m.pair[buf][rank][lane]), to)),
+      "l"(v.e), "l"(v.b), "r"(bar)
       : "memory");
   if (lane == 0)
     asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(
@@ -255,31 +315,27 @@ __device__ __forceinline__ void mail_wait(Mail& m, int buf, uint32_t parity) {
   const uint32_t bar = smem_u32(&m.landed[buf]);
   if (!try_phase(bar, parity)) wait_poll(bar, parity, &m.failed);
 }
-
-// ---------------------------------------------------------------------------
-// Pairs (E, B): v -> E v + B, of a lane's two channels as (E0, E1, B0, B1).  Where
-// a sequence starts (or, for gradients, ends) among the rows of a pair, nothing
-// comes in from before them: E is kCut.  (Not 0: a value that is not finite would
-// leave its sequence.)  CUTS: some pair may be cut.
-// ---------------------------------------------------------------------------
-constexpr float kCut = -1.0f;  // (decays are not negative)
-template <bool CUTS>
-__device__ __forceinline__ void through(const float4& s, float (&v)[2]) {
-  if (CUTS && s.x == kCut) {
-    v[0] = s.z, v[1] = s.w;
+// The value that comes to the tiles of CTA `rank`, and (in `v`) the one behind all
+// tiles of the cluster, from the one before them.
+__device__ __forceinline__ Two mail_through(const Mail& m, int buf, int rank, int size, Two& v) {
+  const int lane = threadIdx.x & 31;
+  const int4 c0 = *reinterpret_cast<const int4*>(&m.cut[buf][0]);
+  const int4 c1 = *reinterpret_cast<const int4*>(&m.cut[buf][4]);
+  Two mine = v;
+  if (((c0.x | c0.y) | (c0.z | c0.w)) | ((c1.x | c1.y) | (c1.z | c1.w))) {
+    for (int k = 0; k < size; ++k) {
+      if (k == rank) mine = v;
+      v = through<true>(get_pair(&m.pair[buf][k][lane]), v);
+    }
   } else {
-    fma2(v[0], v[1], s.x, s.y, v[0], v[1], s.z, s.w);
+#pragma unroll
+    for (int k = 0; k < kMaxCluster; ++k) {
+      if (k >= size) break;
+      if (k == rank) mine = v;
+      v = through<false>(get_pair(&m.pair[buf][k][lane]), v);
+    }
   }
-}
-// s: first s, then t.
-template <bool CUTS>
-__device__ __forceinline__ void compose(float4& s, const float4& t) {
-  if (CUTS && t.x == kCut) {
-    s = t;
-    return;
-  }
-  fma2(s.z, s.w, t.x, t.y, s.z, s.w, t.z, t.w);
-  if (!CUTS || s.x != kCut) mul2(s.x, s.y, s.x, s.y, t.x, t.y);
+  return mine;
 }
 
 // ---------------------------------------------------------------------------
@@ -287,7 +343,6 @@ __device__ __forceinline__ void compose(float4& s, const float4& t) {
 // ---------------------------------------------------------------------------
 struct TileRows {
   uint32_t in[2], first[2], last[2];  // bits of the tile's rows
-  int64_t begin, end;                 // rows of the sequence of the tile's last row
   int seq[kTile];
 };
 
@@ -295,7 +350,8 @@ struct TileRows {
 __device__ __forceinline__ int64_t seq_of_row(const Seqs& q, int64_t r, int64_t& begin,
                                               int64_t& end) {
   int64_t s = 0;
-  if (q.cu) {
+  if (q.seqs == 1) {
+  } else if (q.cu) {
     int64_t hi = q.seqs;
     while (hi - s > 1) {
       const int64_t mid = (s + hi) >> 1;
@@ -314,8 +370,8 @@ __device__ __forceinline__ void place_rows(const Seqs& q, int64_t tile, int64_t 
                                            TileRows* t) {
   const int64_t r = tile * kTile + threadIdx.x;
   bool in = false, first = false, last = false;
-  int64_t begin = 0, end = 0;
   if (r >= lo && r < hi) {
+    int64_t begin, end;
     const int64_t s = seq_of_row(q, r, begin, end);
     in = r >= begin && r < end;
     first = in && r == begin;
@@ -329,16 +385,19 @@ __device__ __forceinline__ void place_rows(const Seqs& q, int64_t tile, int64_t 
     t->first[threadIdx.x >> 5] = bf;
     t->last[threadIdx.x >> 5] = bl;
   }
-  if (threadIdx.x == kTile - 1) t->begin = begin, t->end = end;
 }
 
-// What a CTA knows of its tiles' rows: those inside the sequence that it found
-// last need no search.
+// What a CTA knows of its tiles' rows: the rows of a sequence.
 struct Rows {
-  int64_t begin = 0, end = 0;  // of that sequence
-  // Whether tile `t` is whole, lies in it, and holds neither end of it.
-  __device__ __forceinline__ bool inside(int64_t t) const {
-    return t * kTile > begin && (t + 1) * kTile < end;
+  int64_t begin = 0, end = 0;
+  // Whether tile `t` of the segment's rows [lo, hi) is whole, lies in one sequence,
+  // and holds neither end of it.
+  __device__ __forceinline__ bool inside(const Seqs& q, int64_t t, int64_t lo, int64_t hi) {
+    const int64_t r0 = t * kTile, r1 = r0 + kTile;
+    if (r0 > begin && r1 < end) return true;
+    if (r0 < lo || r1 > hi) return false;
+    seq_of_row(q, r0, begin, end);
+    return r0 > begin && r1 < end;
   }
 };
 
@@ -361,28 +420,20 @@ __device__ __forceinline__ int64_t segment_begin(const Params& p, int z) {
   return b < 0 ? 0 : (b > q.rows ? q.rows : b);
 }
 
-// The state that sequence s starts from, in channels c, c + 1, .. (0 where it
+// The state that sequence s starts from, in the lane's channels c .. (0 where it
 // starts from none).
-template <int V>
-__device__ __forceinline__ bool start_state(const Params& p, int64_t s, int64_t c, int n,
-                                            float* h) {
+__device__ __forceinline__ Two start_state(const Params& p, int64_t s, int64_t c, int n) {
   const int64_t slot = seq_slot(p.q, s);
-  const bool resumes = slot >= 0 && seq_resumes(p.q, s);
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    h[v] = 0.0f;
-    if (resumes && v < n) h[v] = p.state[slot * p.slot_stride + c + v];
-  }
-  return resumes;
+  if (slot < 0 || !seq_resumes(p.q, s)) return 0;
+  const float* h = p.state + slot * p.slot_stride + c;
+  return pk2(n > 0 ? h[0] : 0.0f, n > 1 ? h[1] : 0.0f);
 }
 
-// Adds to g what comes to the last row of sequence s from the state behind it.
-__device__ __forceinline__ void end_gradient(const Params& p, int64_t s, int64_t c, int n,
-                                             float* g) {
-  if (!p.dstate) return;
-#pragma unroll
-  for (int v = 0; v < 2; ++v)
-    if (v < n) g[v] += __ldg(p.dstate + s * p.width + c + v);
+// What comes to the last row of sequence s from the state behind it.
+__device__ __forceinline__ Two end_gradient(const Params& p, int64_t s, int64_t c, int n) {
+  if (!p.dstate) return 0;
+  const float* g = p.dstate + s * p.width + c;
+  return pk2(n > 0 ? __ldg(g) : 0.0f, n > 1 ? __ldg(g + 1) : 0.0f);
 }
 
 // Empty sequences among those of this CTA (every `of`-th 32 from the `at`-th):
@@ -420,7 +471,7 @@ __device__ __forceinline__ void copies_wait() {
 // The CTA's threads start to copy tile `tile` of one input into `to`; rows
 // outside [lo, hi) and channels behind the last one become zeros.  `whole`: there
 // are none of either.
-template <typename T, int THREADS>
+template <typename T, int THREADS, int PITCH>
 __device__ __forceinline__ void copy_tile(T* to, const void* base, int64_t stride, int64_t c0,
                                           int64_t width, int64_t tile, int64_t lo, int64_t hi,
                                           int chunk, bool whole) {
@@ -434,7 +485,8 @@ __device__ __forceinline__ void copy_tile(T* to, const void* base, int64_t strid
     const int64_t step = ROWS * stride;
 #pragma unroll
     for (int k = 0; k < kTile / ROWS; ++k, p += step)
-      copy_async<16>(at + (threadIdx.x + k * THREADS) * 16, p, 16);
+      copy_async<16>(at + (threadIdx.x / ROW + k * ROWS) * PITCH * ES + threadIdx.x % ROW * 16, p,
+                     16);
     return;
   }
   const int cols = static_cast<int>(width - c0 < kCols ? width - c0 : kCols);
@@ -443,7 +495,7 @@ __device__ __forceinline__ void copy_tile(T* to, const void* base, int64_t strid
     for (int k = threadIdx.x; k < kTile * ROW; k += THREADS) {
       const int row = k / ROW, c = k % ROW * E;
       const bool ok = r0 + row >= lo && r0 + row < hi && c < cols;
-      copy_async<16>(at + k * 16, ok ? from + (r0 + row) * stride + c : from, ok ? 16 : 0);
+      copy_async<16>(at + (row * PITCH + c) * ES, ok ? from + (r0 + row) * stride + c : from, ok ? 16 : 0);
     }
   } else if (chunk == 4) {
     constexpr int E4 = 4 / ES, ROW4 = kCols / E4;
@@ -451,7 +503,7 @@ __device__ __forceinline__ void copy_tile(T* to, const void* base, int64_t strid
     for (int k = threadIdx.x; k < kTile * ROW4; k += THREADS) {
       const int row = k / ROW4, c = k % ROW4 * E4;
       const bool ok = r0 + row >= lo && r0 + row < hi && c < cols;
-      copy_async<4>(at + k * 4, ok ? from + (r0 + row) * stride + c : from,
+      copy_async<4>(at + (row * PITCH + c) * ES, ok ? from + (r0 + row) * stride + c : from,
                     !ok ? 0 : cols - c < E4 ? ES : 4);
     }
   } else {
@@ -461,31 +513,35 @@ __device__ __forceinline__ void copy_tile(T* to, const void* base, int64_t strid
       T v;
       Elem<T>::store1(&v, 0, 0.0f);
       if (r0 + row >= lo && r0 + row < hi && c < cols) v = from[(r0 + row) * stride + c];
-      to[k] = v;
+      to[row * PITCH + c] = v;
     }
   }
 }
 
 // A lane's two channels of a row in shared memory.
 template <typename T>
-__device__ __forceinline__ void get2(const T* p, float* f) {
+__device__ __forceinline__ Two get2(const T* p) {
   if constexpr (sizeof(T) == 4) {
-    const float2 v = *reinterpret_cast<const float2*>(p);
-    f[0] = v.x, f[1] = v.y;
+    return *reinterpret_cast<const Two*>(p);
   } else {
-    Elem<T>::unpack2(*reinterpret_cast<const uint32_t*>(p), f[0], f[1]);
+    float x, y;
+    Elem<T>::unpack2(*reinterpret_cast<const uint32_t*>(p), x, y);
+    return pk2(x, y);
   }
 }
-// Stores the first `cols` of two channels.
+// Stores both channels, or the first `cols` of them.
 template <typename T>
-__device__ __forceinline__ void put2(void* base, int64_t at, const float* f, int cols, bool pairs) {
-  T* p = static_cast<T*>(base) + at;
-  if (pairs && cols == 2) {
-    Raw<T, 2>::put(p, f);
-  } else {
-    if (cols > 0) Elem<T>::store1(p, 0, f[0]);
-    if (cols > 1) Elem<T>::store1(p, 1, f[1]);
-  }
+__device__ __forceinline__ void put2(T* p, Two v) {
+  float f[2];
+  upk2(v, f[0], f[1]);
+  Raw<T, 2>::put(p, f);
+}
+template <typename T>
+__device__ __forceinline__ void put_some(T* p, Two v, int cols) {
+  float x, y;
+  upk2(v, x, y);
+  if (cols > 0) Elem<T>::store1(p, 0, x);
+  if (cols > 1) Elem<T>::store1(p, 1, y);
 }
 
 // What a CTA knows for all of its tiles.
@@ -494,7 +550,8 @@ struct Place {
   int64_t c0, c;    // first channel of the CTA and of the lane
   int cols;         // the lane's channels (0 to 2)
   int rank, size;   // in its cluster
-  float ac[2];
+  Two a;
+  bool fast;        // see decay2
 };
 __device__ __forceinline__ Place find_place(const Params& p) {
   Place w;
@@ -506,8 +563,9 @@ __device__ __forceinline__ Place find_place(const Params& p) {
   w.cols = w.c >= p.width ? 0 : p.width - w.c < 2 ? 1 : 2;
   w.lo = segment_begin(p, blockIdx.z);
   w.hi = segment_begin(p, blockIdx.z + 1);
-#pragma unroll
-  for (int v = 0; v < 2; ++v) w.ac[v] = v < w.cols ? __ldg(p.a + w.c + v) : 0.0f;
+  const float a0 = w.cols > 0 ? __ldg(p.a + w.c) : 0.0f, a1 = w.cols > 1 ? __ldg(p.a + w.c + 1) : 0.0f;
+  w.a = pk2(a0, a1);
+  w.fast = __all_sync(0xffffffffu, a0 > kSeries && a1 > kSeries);
   return w;
 }
 __device__ __forceinline__ bool whole_tile(const Params& p, const Place& w, int64_t tile) {
@@ -515,16 +573,25 @@ __device__ __forceinline__ bool whole_tile(const Params& p, const Place& w, int6
 }
 
 // ---------------------------------------------------------------------------
-// Prompts.  Four warps of sixteen rows each: an element costs about 25
-// instructions of its own, what a tile costs besides is shared by 32 elements of
-// a thread.
+// Prompts.  Four warps of sixteen rows each.  A row of the tile in shared memory
+// holds x, the input gate and the decay gate of 64 channels; e and b take their
+// place (512 bytes a row, which f32's inputs need anyway), so that the loops over
+// rows stay rolled: unrolled, with e and b in registers, they were larger than the
+// instruction cache, which a third of all stalls waited for.
 // ---------------------------------------------------------------------------
 namespace forward {
 
 constexpr int W = 4, R = kTile / W, kThreads = 32 * W;
+constexpr int kAtOnce = 4;  // rows of a loop's turn
+
+// Elements between rows of the tile.
+template <typename T>
+constexpr int pitch() {
+  return (sizeof(T) == 2 ? 4 : 3) * kCols;
+}
 
 struct Shared {
-  float4 pair[W][32];
+  ulonglong2 pair[W][32];
   Mail mail;
   TileRows rows;
 };
@@ -533,8 +600,8 @@ template <typename T>
 __device__ __forceinline__ void fetch(const Params& p, const Place& w, T* to, int64_t tile) {
   const bool whole = whole_tile(p, w, tile);
   const auto copy = [&](int k, const void* base, int64_t stride) {
-    copy_tile<T, kThreads>(to + k * kTile * kCols, base, stride, w.c0, p.width, tile, w.lo, w.hi,
-                           p.chunk, whole);
+    copy_tile<T, kThreads, pitch<T>()>(to + k * kCols, base, stride, w.c0, p.width, tile, w.lo,
+                                       w.hi, p.chunk, whole);
   };
   copy(0, p.x, p.xs), copy(1, p.ig, p.is), copy(2, p.rg, p.rs);
 }
@@ -543,129 +610,105 @@ __device__ __forceinline__ void fetch(const Params& p, const Place& w, T* to, in
 // nor its last.  FAST: see decay2.  Takes the state before the cluster's tiles and
 // gives the one behind them.
 template <typename T, bool INSIDE, bool FAST>
-__device__ __forceinline__ float2 turn_of(const Params& p, const Place& w, Shared& sh, T* tiles,
-                                          int64_t tile, int64_t next, int64_t turn, float2 state) {
+__device__ __forceinline__ Two turn_of(const Params& p, const Place& w, Shared& sh, T* tiles,
+                                       int64_t tile, int64_t turn, Two state, const Constants& con) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int buf = turn & 1;
   const uint32_t parity = turn >> 1 & 1;
-  const T* mine = tiles + warp * R * kCols + lane * 2;
+  T* const mine = tiles + warp * R * pitch<T>();
   const TileRows& t = sh.rows;
+  const auto pair_of = [&](int j) {
+    return reinterpret_cast<ulonglong2*>(mine + j * pitch<T>()) + lane;
+  };
   // e and b of the warp's rows, and the pair of all of them
-  float e[R][2], b[R][2];
-  float4 s = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
+  Pair all = {kOnes, 0};
+#pragma unroll 1
+  for (int j0 = 0; j0 < R; j0 += kAtOnce) {
+    Two x[kAtOnce], gi[kAtOnce], gr[kAtOnce];
 #pragma unroll
-  for (int j = 0; j < R; ++j) {
-    float x[2], gi[2], gr[2], m[2];
-    get2(mine + j * kCols, x);
-    get2(mine + (kTile + j) * kCols, gi);
-    get2(mine + (2 * kTile + j) * kCols, gr);
-    sigmoid2<T>(gi, gi);
-    sigmoid2<T>(gr, gr);
-    decay2<T, FAST>(gr, w.ac[0], w.ac[1], e[j], m);
-    mul2(m[0], m[1], m[0], m[1], gi[0], gi[1]);
-    mul2(b[j][0], b[j][1], m[0], m[1], x[0], x[1]);
-    if constexpr (!INSIDE) {
-      const int row = warp * R + j;
-      if (!(t.in[row >> 5] >> (row & 31) & 1)) {
-        e[j][0] = e[j][1] = 1.0f;
-        b[j][0] = b[j][1] = 0.0f;
-      }
-      if (t.first[row >> 5] >> (row & 31) & 1) {
-        float h[2];
-        if (start_state<2>(p, t.seq[row], w.c, w.cols, h))
-          fma2(b[j][0], b[j][1], e[j][0], e[j][1], h[0], h[1], b[j][0], b[j][1]);
-        e[j][0] = e[j][1] = kCut;
-      }
+    for (int k = 0; k < kAtOnce; ++k) {
+      const T* row = mine + (j0 + k) * pitch<T>() + lane * 2;
+      x[k] = get2(row), gi[k] = get2(row + kCols), gr[k] = get2(row + 2 * kCols);
     }
-    compose<!INSIDE>(s, make_float4(e[j][0], e[j][1], b[j][0], b[j][1]));
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      Pair s;
+      Two m;
+      decay2<T, FAST>(sigmoid2<T>(gr[k], con), w.a, con, s.e, m);
+      s.b = mul(mul(m, sigmoid2<T>(gi[k], con)), x[k]);
+      if constexpr (!INSIDE) {
+        const int row = warp * R + j0 + k;
+        if (!(t.in[row >> 5] >> (row & 31) & 1)) s = {kOnes, 0};
+        if (t.first[row >> 5] >> (row & 31) & 1)
+          s = {kCut, fma(s.e, start_state(p, t.seq[row], w.c, w.cols), s.b)};
+      }
+      all = compose<!INSIDE>(all, s);
+      put_pair(pair_of(j0 + k), s);
+    }
   }
-  sh.pair[warp][lane] = s;
+  put_pair(&sh.pair[warp][lane], all);
   const bool cut = !INSIDE && (t.first[0] | t.first[1]) != 0;
   __syncthreads();
-  if (next >= 0) fetch(p, w, tiles, next);
 
   // the pair of the rows before this warp's in the tile, and of the whole tile
-  float4 before = make_float4(1.0f, 1.0f, 0.0f, 0.0f), whole = sh.pair[0][lane];
+  Pair before = {kOnes, 0}, whole = get_pair(&sh.pair[0][lane]);
 #pragma unroll
   for (int k = 1; k < W; ++k) {
     if (k == warp) before = whole;
-    compose<!INSIDE>(whole, sh.pair[k][lane]);
+    whole = compose<!INSIDE>(whole, get_pair(&sh.pair[k][lane]));
   }
-  float carry[2] = {state.x, state.y}, h[2] = {state.x, state.y};
+  Two h = state;
   if (w.size > 1) {
     if (threadIdx.x == 0) mail_expect(sh.mail, buf, w.size);
     if (!p.mute)
       for (int k = warp; k < w.size; k += W) mail_send(sh.mail, buf, w.rank, k, whole, cut);
     mail_wait(sh.mail, buf, parity);
-    bool cuts = false;
-    for (int k = 0; k < w.size; ++k) cuts = cuts || sh.mail.cut[buf][k] != 0;
-    if (cuts) {
-      for (int k = 0; k < w.size; ++k) {
-        if (k == w.rank) h[0] = carry[0], h[1] = carry[1];
-        through<true>(sh.mail.pair[buf][k][lane], carry);
-      }
-    } else {
+    h = mail_through(sh.mail, buf, w.rank, w.size, state);
+  } else {
+    state = through<!INSIDE>(whole, state);
+  }
+  if (p.saved && warp == 0 && tile * kTile >= w.lo && tile * kTile < w.hi)
+    put_some(p.saved + tile * p.width + w.c, h, w.cols);
+  h = through<!INSIDE>(before, h);
+  T* at = static_cast<T*>(p.out) + (tile * kTile + warp * R) * p.os + w.c;
+  if (INSIDE && !p.out) {
+    // (only the states to be kept are wanted)
+  } else if (INSIDE && p.pairs && w.c0 + kCols <= p.width) {
+    // (the loop that nearly all tiles of a call take)
+#pragma unroll 1
+    for (int j0 = 0; j0 < R; j0 += kAtOnce) {
 #pragma unroll
-      for (int k = 0; k < kMaxCluster; ++k) {
-        if (k >= w.size) break;
-        if (k == w.rank) h[0] = carry[0], h[1] = carry[1];
-        through<false>(sh.mail.pair[buf][k][lane], carry);
+      for (int k = 0; k < kAtOnce; ++k, at += p.os) {
+        h = through<false>(get_pair(pair_of(j0 + k)), h);
+        put2(at, h);
       }
     }
   } else {
-    through<!INSIDE>(whole, carry);
-  }
-  if (p.saved && warp == 0 && tile * kTile >= w.lo && tile * kTile < w.hi) {
-#pragma unroll
-    for (int v = 0; v < 2; ++v)
-      if (v < w.cols) p.saved[tile * p.width + w.c + v] = h[v];
-  }
-  through<!INSIDE>(before, h);
-  if constexpr (INSIDE) {
-    if (p.out) {
-      T* at = static_cast<T*>(p.out) + (tile * kTile + warp * R) * p.os + w.c;
-      if (p.pairs && w.cols == 2) {
-#pragma unroll
-        for (int j = 0; j < R; ++j, at += p.os) {
-          fma2(h[0], h[1], e[j][0], e[j][1], h[0], h[1], b[j][0], b[j][1]);
-          Raw<T, 2>::put(at, h);
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < R; ++j, at += p.os) {
-          fma2(h[0], h[1], e[j][0], e[j][1], h[0], h[1], b[j][0], b[j][1]);
-          put2<T>(at, 0, h, w.cols, false);
-        }
-      }
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < R; ++j) {
-      through<true>(make_float4(e[j][0], e[j][1], b[j][0], b[j][1]), h);
+#pragma unroll 1
+    for (int j = 0; j < R; ++j, at += p.os) {
+      h = through<!INSIDE>(get_pair(pair_of(j)), h);
       const int row = warp * R + j;
-      if (p.out && (t.in[row >> 5] >> (row & 31) & 1))
-        put2<T>(p.out, (tile * kTile + row) * p.os + w.c, h, w.cols, p.pairs);
-      if (p.keep_state && (t.last[row >> 5] >> (row & 31) & 1)) {
+      if (p.out && (INSIDE || (t.in[row >> 5] >> (row & 31) & 1))) put_some(at, h, w.cols);
+      if (!INSIDE && p.keep_state && (t.last[row >> 5] >> (row & 31) & 1)) {
         const int64_t slot = seq_slot(p.q, t.seq[row]);
-#pragma unroll
-        for (int v = 0; v < 2; ++v)
-          if (slot >= 0 && v < w.cols) p.state[slot * p.slot_stride + w.c + v] = h[v];
+        if (slot >= 0) put_some(p.state + slot * p.slot_stride + w.c, h, w.cols);
       }
     }
-    __syncthreads();  // (the next turn's search writes rows)
   }
-  return make_float2(carry[0], carry[1]);
+  __syncthreads();  // (the next tile's copies and search write what was read here)
+  return state;
 }
 // The forms that few tiles take, out of the way of the loop's instructions and
 // registers.
 template <typename T, bool INSIDE, bool FAST>
-__device__ __noinline__ float2 turn_apart(const Params& p, Place w, Shared& sh, T* tiles,
-                                          int64_t tile, int64_t next, int64_t turn, float2 state) {
-  return turn_of<T, INSIDE, FAST>(p, w, sh, tiles, tile, next, turn, state);
+__device__ __noinline__ Two turn_apart(const Params& p, Place w, Shared& sh, T* tiles,
+                                       int64_t tile, int64_t turn, Two state) {
+  return turn_of<T, INSIDE, FAST>(p, w, sh, tiles, tile, turn, state, Constants());
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4)
     k_recur(const __grid_constant__ Params p) {
   extern __shared__ uint4 s_tile[];
   __shared__ Shared sh;
@@ -678,26 +721,20 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 3)
   const int64_t tile0 = w.lo / kTile, count = w.hi > w.lo ? (w.hi + kTile - 1) / kTile - tile0 : 0;
   const int64_t turns = (count + w.size - 1) / w.size;
   int64_t tile = tile0 + w.rank;
-  if (turns > 0) fetch(p, w, tiles, tile);
-  const bool fast = __all_sync(0xffffffffu, w.ac[0] > kSeries && w.ac[1] > kSeries);
   all_wait();
 
-  float2 state = make_float2(0.0f, 0.0f);  // before the cluster's tiles
+  const Constants con;
+  Two state = 0;  // before the cluster's tiles
   Rows known;
   for (int64_t turn = 0; turn < turns; ++turn, tile += w.size) {
-    const int64_t next = turn + 1 < turns ? tile + w.size : -1;
-    const bool inside = known.inside(tile) && (tile + 1) * kTile <= w.hi;
+    fetch(p, w, tiles, tile);
+    const bool inside = known.inside(p.q, tile, w.lo, w.hi);
     if (!inside && threadIdx.x < kTile) place_rows(p.q, tile, w.lo, w.hi, &sh.rows);
     copies_wait();
     __syncthreads();
-    if (inside && fast) {
-      state = turn_of<T, true, true>(p, w, sh, tiles, tile, next, turn, state);
-    } else if (inside) {
-      state = turn_apart<T, true, false>(p, w, sh, tiles, tile, next, turn, state);
-    } else {
-      known.begin = sh.rows.begin, known.end = sh.rows.end;
-      state = turn_apart<T, false, false>(p, w, sh, tiles, tile, next, turn, state);
-    }
+    if (inside && w.fast) state = turn_of<T, true, true>(p, w, sh, tiles, tile, turn, state, con);
+    else if (inside) state = turn_apart<T, true, false>(p, w, sh, tiles, tile, turn, state);
+    else state = turn_apart<T, false, false>(p, w, sh, tiles, tile, turn, state);
   }
   if (p.keep_state && threadIdx.x < 32) {
     each_empty(p.q, static_cast<int64_t>(blockIdx.z) * w.size + w.rank,
@@ -727,8 +764,8 @@ static_assert(W >= kMaxCluster, "a warp to each CTA that the tile's pair goes to
 constexpr int kInput = kTile * kCols;  // elements of an input's tile
 
 struct Shared {
-  float4 down[W][32];  // pairs of states
-  float4 up[W][32];    // pairs of gradients
+  ulonglong2 down[W][32];  // pairs of states
+  ulonglong2 up[W][32];    // pairs of gradients
   Mail mail;
   TileRows rows;
 };
@@ -743,82 +780,71 @@ template <typename T>
 __device__ __forceinline__ void fetch(const Params& p, const Place& w, T* to, int64_t tile) {
   const bool whole = whole_tile(p, w, tile);
   const auto copy = [&](int k, const void* base, int64_t stride) {
-    copy_tile<T, kThreads>(to + k * kInput, base, stride, w.c0, p.width, tile, w.lo, w.hi, p.chunk,
+    copy_tile<T, kThreads, kCols>(to + k * kInput, base, stride, w.c0, p.width, tile, w.lo, w.hi, p.chunk,
                            whole);
   };
   copy(0, p.x, p.xs), copy(1, p.ig, p.is), copy(2, p.rg, p.rs), copy(3, p.dout, p.gs);
 }
 
 struct Carry {
-  float g[2];   // the gradient of the state behind the cluster's tiles
-  float da[2];
+  Two g;   // the gradient of the state behind the cluster's tiles
+  Two da;
 };
 
 template <typename T, bool INSIDE, bool FAST>
 __device__ __forceinline__ Carry turn_of(const Params& p, const Place& w, Shared& sh, T* ring,
-                                         int64_t tile, int64_t next, int64_t turn, Carry carry) {
+                                         int64_t tile, int64_t next, int64_t turn, Carry carry,
+                                         const Constants& con) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int buf = turn & 1;
   const uint32_t parity = turn >> 1 & 1;
   T* const tiles = ring + (stages<T>() == 2 ? buf : 0) * 4 * kInput;
   const T* mine = tiles + warp * R * kCols + lane * 2;
   const TileRows& t = sh.rows;
-  float h[2];  // the state before the tile, as it was kept
-#pragma unroll
-  for (int v = 0; v < 2; ++v)
-    h[v] = tile * kTile >= w.lo && v < w.cols ? __ldg(p.saved + tile * p.width + w.c + v) : 0.0f;
+  Two h = 0;  // the state before the tile, as it was kept
+  if (tile * kTile >= w.lo) {
+    const float* kept = p.saved + tile * p.width + w.c;
+    h = pk2(w.cols > 0 ? __ldg(kept) : 0.0f, w.cols > 1 ? __ldg(kept + 1) : 0.0f);
+  }
   if (stages<T>() == 2 && next != INT64_MIN) fetch(p, w, ring + (buf ^ 1) * 4 * kInput, next);
   const uint32_t in = INSIDE ? ~0u : t.in[warp * R >> 5] >> (warp * R & 31),
                  first = INSIDE ? 0u : t.first[warp * R >> 5] >> (warp * R & 31),
                  last = INSIDE ? 0u : t.last[warp * R >> 5] >> (warp * R & 31);
 
-  float e[R][2], m[R][2], si[R][2], sr[R][2], b[R][2];
-  float4 down = make_float4(1.0f, 1.0f, 0.0f, 0.0f), up = down;
+  Two e[R], m[R], si[R], sr[R], b[R];
+  Pair down = {kOnes, 0}, up = {kOnes, 0};
 #pragma unroll
   for (int j = 0; j < R; ++j) {
-    float x[2];
-    get2(mine + j * kCols, x);
-    get2(mine + kInput + j * kCols, si[j]);
-    get2(mine + 2 * kInput + j * kCols, sr[j]);
-    sigmoid2<T>(si[j], si[j]);
-    sigmoid2<T>(sr[j], sr[j]);
-    decay2<T, FAST>(sr[j], w.ac[0], w.ac[1], e[j], m[j]);
-    mul2(b[j][0], b[j][1], m[j][0], m[j][1], si[j][0], si[j][1]);
-    mul2(b[j][0], b[j][1], b[j][0], b[j][1], x[0], x[1]);
-    if (!INSIDE && !(in >> j & 1)) {
-      e[j][0] = e[j][1] = 1.0f;
-      b[j][0] = b[j][1] = 0.0f;
-    }
-    if (!INSIDE && (first >> j & 1)) {
-      float h0[2];
-      start_state<2>(p, t.seq[warp * R + j], w.c, w.cols, h0);
-      fma2(h0[0], h0[1], e[j][0], e[j][1], h0[0], h0[1], b[j][0], b[j][1]);
-      down = make_float4(kCut, kCut, h0[0], h0[1]);
-    } else {
-      compose<!INSIDE>(down, make_float4(e[j][0], e[j][1], b[j][0], b[j][1]));
-    }
+    si[j] = sigmoid2<T>(get2(mine + kInput + j * kCols), con);
+    sr[j] = sigmoid2<T>(get2(mine + 2 * kInput + j * kCols), con);
+    decay2<T, FAST>(sr[j], w.a, con, e[j], m[j]);
+    b[j] = mul(mul(m[j], si[j]), get2(mine + j * kCols));
+    if (!INSIDE && !(in >> j & 1)) e[j] = kOnes, b[j] = 0;
+    if (!INSIDE && (first >> j & 1))
+      down = {kCut, fma(e[j], start_state(p, t.seq[warp * R + j], w.c, w.cols), b[j])};
+    else
+      down = compose<!INSIDE>(down, {e[j], b[j]});
   }
 #pragma unroll
   for (int j = R - 1; j >= 0; --j) {
-    float g[2];
-    get2(mine + 3 * kInput + j * kCols, g);
     if (!INSIDE && !(in >> j & 1)) continue;
+    Two g = get2(mine + 3 * kInput + j * kCols);
     const bool end = !INSIDE && (last >> j & 1);
-    if (end) end_gradient(p, t.seq[warp * R + j], w.c, w.cols, g);
-    mul2(g[0], g[1], g[0], g[1], e[j][0], e[j][1]);
-    if (end) up = make_float4(kCut, kCut, g[0], g[1]);
-    else compose<!INSIDE>(up, make_float4(e[j][0], e[j][1], g[0], g[1]));
+    if (end) g = add(g, end_gradient(p, t.seq[warp * R + j], w.c, w.cols));
+    g = mul(g, e[j]);
+    if (end) up = {kCut, g};
+    else up = compose<!INSIDE>(up, {e[j], g});
   }
-  sh.down[warp][lane] = down;
-  sh.up[warp][lane] = up;
+  put_pair(&sh.down[warp][lane], down);
+  put_pair(&sh.up[warp][lane], up);
   const bool cut = !INSIDE && (t.last[0] | t.last[1]) != 0;
   __syncthreads();
   // the pair of the rows behind this warp's in the tile, and of the whole tile
-  float4 behind = make_float4(1.0f, 1.0f, 0.0f, 0.0f), whole = sh.up[W - 1][lane];
+  Pair behind = {kOnes, 0}, whole = get_pair(&sh.up[W - 1][lane]);
 #pragma unroll
   for (int k = W - 2; k >= 0; --k) {
     if (k == warp) behind = whole;
-    compose<!INSIDE>(whole, sh.up[k][lane]);
+    whole = compose<!INSIDE>(whole, get_pair(&sh.up[k][lane]));
   }
   if (w.size > 1) {
     if (threadIdx.x == 0) mail_expect(sh.mail, buf, w.size);
@@ -827,94 +853,63 @@ __device__ __forceinline__ Carry turn_of(const Params& p, const Place& w, Shared
   // the states before each row, meanwhile
 #pragma unroll
   for (int k = 0; k < W - 1; ++k)
-    if (k < warp) through<!INSIDE>(sh.down[k][lane], h);
+    if (k < warp) h = through<!INSIDE>(get_pair(&sh.down[k][lane]), h);
 #pragma unroll
   for (int j = 0; j < R; ++j) {
-    if (!INSIDE && (first >> j & 1)) start_state<2>(p, t.seq[warp * R + j], w.c, w.cols, h);
-    const float b0 = b[j][0], b1 = b[j][1];
-    b[j][0] = h[0], b[j][1] = h[1];  // (from here on the state before the row)
-    if (INSIDE || (in >> j & 1)) fma2(h[0], h[1], e[j][0], e[j][1], h[0], h[1], b0, b1);
+    if (!INSIDE && (first >> j & 1)) h = start_state(p, t.seq[warp * R + j], w.c, w.cols);
+    const Two before = h;
+    if (INSIDE || (in >> j & 1)) h = fma(e[j], h, b[j]);
+    b[j] = before;  // (from here on the state before the row)
   }
   // the gradient that comes to this warp's last row from the rows behind it
-  float gc[2] = {carry.g[0], carry.g[1]};
+  Two gc = carry.g;
   if (w.size > 1) {
     mail_wait(sh.mail, buf, parity);
-    bool cuts = false;
-    for (int k = 0; k < w.size; ++k) cuts = cuts || sh.mail.cut[buf][k] != 0;
-    if (cuts) {
-      for (int k = 0; k < w.size; ++k) {
-        if (k == w.rank) gc[0] = carry.g[0], gc[1] = carry.g[1];
-        through<true>(sh.mail.pair[buf][k][lane], carry.g);
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < kMaxCluster; ++k) {
-        if (k >= w.size) break;
-        if (k == w.rank) gc[0] = carry.g[0], gc[1] = carry.g[1];
-        through<false>(sh.mail.pair[buf][k][lane], carry.g);
-      }
-    }
+    gc = mail_through(sh.mail, buf, w.rank, w.size, carry.g);
   } else {
-    through<!INSIDE>(whole, carry.g);
+    carry.g = through<!INSIDE>(whole, carry.g);
   }
-  through<!INSIDE>(behind, gc);
+  gc = through<!INSIDE>(behind, gc);
 
   const int64_t row0 = tile * kTile + warp * R;
-  T* dx_at = static_cast<T*>(p.dx) + row0 * p.dxs + w.c;
-  T* di_at = static_cast<T*>(p.dig) + row0 * p.dis + w.c;
-  T* dr_at = static_cast<T*>(p.drg) + row0 * p.drs + w.c;
-  const bool pairs = p.pairs && w.cols == 2;
+  T* dx_at = static_cast<T*>(p.dx) + (row0 + R - 1) * p.dxs + w.c;
+  T* di_at = static_cast<T*>(p.dig) + (row0 + R - 1) * p.dis + w.c;
+  T* dr_at = static_cast<T*>(p.drg) + (row0 + R - 1) * p.drs + w.c;
+  const bool pairs = p.pairs && w.c0 + kCols <= p.width;
 #pragma unroll
   for (int j = R - 1; j >= 0; --j) {
-    float g[2], x[2], dx[2], di[2], dr[2], t1[2], t2[2];
-    get2(mine + j * kCols, x);
-    get2(mine + 3 * kInput + j * kCols, g);
-    if (!INSIDE && (last >> j & 1)) end_gradient(p, t.seq[warp * R + j], w.c, w.cols, g);
-    else g[0] += gc[0], g[1] += gc[1];
+    const Two x = get2(mine + j * kCols);
+    Two g = get2(mine + 3 * kInput + j * kCols);
+    if (!INSIDE && (last >> j & 1)) g = add(g, end_gradient(p, t.seq[warp * R + j], w.c, w.cols));
+    else g = add(g, gc);
     // dx = g m i,  di = dx x (1 - i)
-    mul2(dx[0], dx[1], m[j][0], m[j][1], si[j][0], si[j][1]);
-    mul2(dx[0], dx[1], dx[0], dx[1], g[0], g[1]);
-    mul2(di[0], di[1], dx[0], dx[1], x[0], x[1]);
-    mul2(di[0], di[1], di[0], di[1], 1.0f - si[j][0], 1.0f - si[j][1]);
+    Two dx = mul(mul(m[j], si[j]), g);
+    Two di = mul(mul(dx, x), fma(si[j], con.minus, con.one));
     // g e r (h - i x e / m)
-    float over[2];
-#pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      over[v] = Elem<T>::kExactSilu ? 1.0f / m[j][v] : rcp_approx(m[j][v]);
-      if (!(m[j][v] > 0.0f)) over[v] = 0.0f;
-    }
-    mul2(t2[0], t2[1], si[j][0], si[j][1], x[0], x[1]);
-    mul2(t2[0], t2[1], t2[0], t2[1], -e[j][0], -e[j][1]);
-    fma2(t1[0], t1[1], t2[0], t2[1], over[0], over[1], b[j][0], b[j][1]);
-    mul2(t2[0], t2[1], e[j][0], e[j][1], sr[j][0], sr[j][1]);
-    mul2(t1[0], t1[1], t1[0], t1[1], t2[0], t2[1]);
-    mul2(t1[0], t1[1], t1[0], t1[1], g[0], g[1]);
-    mul2(dr[0], dr[1], t1[0], t1[1], w.ac[0], w.ac[1]);
-    mul2(dr[0], dr[1], dr[0], dr[1], 1.0f - sr[j][0], 1.0f - sr[j][1]);
+    const Two over = each(m[j], [](float v) {
+      const float o = Elem<T>::kExactSilu ? 1.0f / v : rcp_approx(v);
+      return v > 0.0f ? -o : 0.0f;
+    });
+    Two d = fma(mul(mul(si[j], x), e[j]), over, b[j]);
+    const Two eg = mul(e[j], g);
+    d = mul(mul(d, sr[j]), eg);
+    Two dr = mul(mul(d, w.a), fma(sr[j], con.minus, con.one));
     if (INSIDE || (in >> j & 1)) {
-      carry.da[0] += t1[0], carry.da[1] += t1[1];
-      mul2(gc[0], gc[1], e[j][0], e[j][1], g[0], g[1]);
+      carry.da = add(carry.da, d);
+      gc = eg;
     } else {  // a row of no sequence
-#pragma unroll
-      for (int v = 0; v < 2; ++v) dx[v] = di[v] = dr[v] = 0.0f;
+      dx = di = dr = 0;
     }
-    if (INSIDE || (row0 + j >= w.lo && row0 + j < w.hi)) {
-      if (pairs) {
-        Raw<T, 2>::put(dx_at + j * p.dxs, dx);
-        Raw<T, 2>::put(di_at + j * p.dis, di);
-        Raw<T, 2>::put(dr_at + j * p.drs, dr);
-      } else {
-        put2<T>(dx_at, j * p.dxs, dx, w.cols, false);
-        put2<T>(di_at, j * p.dis, di, w.cols, false);
-        put2<T>(dr_at, j * p.drs, dr, w.cols, false);
-      }
+    if (INSIDE && pairs) {
+      put2(dx_at, dx), put2(di_at, di), put2(dr_at, dr);
+    } else if (INSIDE || (row0 + j >= w.lo && row0 + j < w.hi)) {
+      put_some(dx_at, dx, w.cols), put_some(di_at, di, w.cols), put_some(dr_at, dr, w.cols);
     }
+    dx_at -= p.dxs, di_at -= p.dis, dr_at -= p.drs;
     if (!INSIDE && p.dinitial && (first >> j & 1)) {
       const int64_t s = t.seq[warp * R + j];
       const bool resumes = seq_slot(p.q, s) >= 0 && seq_resumes(p.q, s);
-#pragma unroll
-      for (int v = 0; v < 2; ++v)
-        if (v < w.cols) p.dinitial[s * p.width + w.c + v] = resumes ? gc[v] : 0.0f;
+      put_some(p.dinitial + s * p.width + w.c, resumes ? gc : 0, w.cols);
     }
   }
   // (the next turn's search writes rows, its copies the tile)
@@ -925,7 +920,7 @@ __device__ __forceinline__ Carry turn_of(const Params& p, const Place& w, Shared
 template <typename T, bool INSIDE, bool FAST>
 __device__ __noinline__ Carry turn_apart(const Params& p, Place w, Shared& sh, T* ring,
                                          int64_t tile, int64_t next, int64_t turn, Carry carry) {
-  return turn_of<T, INSIDE, FAST>(p, w, sh, ring, tile, next, turn, carry);
+  return turn_of<T, INSIDE, FAST>(p, w, sh, ring, tile, next, turn, carry, Constants());
 }
 
 template <typename T>
@@ -944,28 +939,23 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int64_t turns = (count + w.size - 1) / w.size;
   int64_t tile = tile0 + count - 1 - w.rank;
   if (turns > 0) fetch(p, w, ring, tile);
-  const bool fast = __all_sync(0xffffffffu, w.ac[0] > kSeries && w.ac[1] > kSeries);
   all_wait();
 
-  Carry carry = {};
+  const Constants con;
+  Carry carry = {0, 0};
   Rows known;
   for (int64_t turn = 0; turn < turns; ++turn, tile -= w.size) {
     const int64_t next = turn + 1 < turns ? tile - w.size : INT64_MIN;
-    const bool inside = tile * kTile >= w.lo && known.inside(tile);
+    const bool inside = known.inside(p.q, tile, w.lo, w.hi);
     if (!inside && threadIdx.x < kTile) place_rows(p.q, tile, w.lo, w.hi, &sh.rows);
     copies_wait();
     __syncthreads();
-    if (inside && fast) {
-      carry = turn_of<T, true, true>(p, w, sh, ring, tile, next, turn, carry);
-    } else if (inside) {
+    if (inside && w.fast)
+      carry = turn_of<T, true, true>(p, w, sh, ring, tile, next, turn, carry, con);
+    else if (inside)
       carry = turn_apart<T, true, false>(p, w, sh, ring, tile, next, turn, carry);
-    } else {
-      // (of the tile's first row: the tiles before it come next)
-      known.begin = known.end = 0;
-      if (tile * kTile >= w.lo && tile * kTile < w.hi)
-        seq_range(p.q, sh.rows.seq[0], known.begin, known.end);
+    else
       carry = turn_apart<T, false, false>(p, w, sh, ring, tile, next, turn, carry);
-    }
   }
   if (p.dinitial && warp == 0) {
     each_empty(p.q, static_cast<int64_t>(blockIdx.z) * w.size + w.rank,
@@ -979,25 +969,20 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   // da: the warps' sums, then the CTAs' in rank 0
   __syncthreads();
-  sh.up[warp][lane] = make_float4(carry.da[0], carry.da[1], 0.0f, 0.0f);
+  sh.up[warp][lane].x = carry.da;
   __syncthreads();
   if (warp == 0) {
-    float4 t = sh.up[0][lane];
-    for (int k = 1; k < W; ++k) t.x += sh.up[k][lane].x, t.y += sh.up[k][lane].y;
+    Two t = sh.up[0][lane].x;
+    for (int k = 1; k < W; ++k) t = add(t, sh.up[k][lane].x);
     put_peer(&sh.mail.pair[turns & 1][w.rank][lane], 0, t);
     if (lane == 0 && sh.mail.failed) atomicOr(p.fault, kFaultRecurWait);
   }
   all_arrive();
   all_wait();
   if (w.rank == 0 && warp == 0) {
-    float t[2] = {0.0f, 0.0f};
-    for (int k = 0; k < w.size; ++k) {
-      t[0] += sh.mail.pair[turns & 1][k][lane].x;
-      t[1] += sh.mail.pair[turns & 1][k][lane].y;
-    }
-#pragma unroll
-    for (int v = 0; v < 2; ++v)
-      if (v < w.cols) p.da[blockIdx.z * p.width + w.c + v] = t[v];
+    Two t = 0;
+    for (int k = 0; k < w.size; ++k) t = add(t, sh.mail.pair[turns & 1][k][lane].x);
+    put_some(p.da + blockIdx.z * p.width + w.c, t, w.cols);
   }
 }
 
@@ -1026,32 +1011,26 @@ __global__ void __launch_bounds__(128) k_recur_step(const Params p) {
   const int64_t row = blockIdx.x;
   const int64_t slot = seq_slot(p.q, row);
   if (c >= p.width || slot < 0) return;
-  // (two elements at a time; the second is the first again where there is one)
-  constexpr int N = V == 1 ? 2 : V;
-  float x[N], gi[N], gr[N], ac[N], h[N], e[N], m[N];
+  const Constants con;
   float* state = p.state + slot * p.slot_stride + c;
   Raw<T, V> xr, ir, rr;
   xr.load(static_cast<const T*>(p.x) + row * p.xs + c);
   ir.load(static_cast<const T*>(p.ig) + row * p.is + c);
   rr.load(static_cast<const T*>(p.rg) + row * p.rs + c);
+  float x[2] = {0.0f, 0.0f}, gi[2] = {0.0f, 0.0f}, gr[2] = {0.0f, 0.0f}, a[2] = {0.0f, 0.0f},
+        h[2] = {0.0f, 0.0f};
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    ac[v] = __ldg(p.a + c + v);
+    a[v] = __ldg(p.a + c + v);
     h[v] = state[v];
   }
   xr.get(x), ir.get(gi), rr.get(gr);
-  if constexpr (V == 1) x[1] = x[0], gi[1] = gi[0], gr[1] = gr[0], ac[1] = ac[0], h[1] = h[0];
+  Two e, m;
+  decay2<T, false>(sigmoid2<T>(pk2(gr[0], gr[1]), con), pk2(a[0], a[1]), con, e, m);
+  const Two b = mul(mul(m, sigmoid2<T>(pk2(gi[0], gi[1]), con)), pk2(x[0], x[1]));
+  upk2(fma(e, pk2(h[0], h[1]), b), h[0], h[1]);
 #pragma unroll
-  for (int k = 0; k < N; k += 2) {
-    sigmoid2<T>(gi + k, gi + k);
-    sigmoid2<T>(gr + k, gr + k);
-    decay2<T, false>(gr + k, ac[k], ac[k + 1], e + k, m + k);
-  }
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    h[v] = fmaf(e[v], h[v], m[v] * gi[v] * x[v]);
-    state[v] = h[v];
-  }
+  for (int v = 0; v < V; ++v) state[v] = h[v];
   Raw<T, V>::put(static_cast<T*>(p.out) + row * p.os + c, h);
 }
 
@@ -1063,19 +1042,55 @@ struct Split {
   int cluster = 1, segments = 1;
 };
 
-Split split_rows(int64_t rows, int64_t seqs, int64_t blocks, int resident) {
-  Split s;
-  const int64_t tiles = (rows + kTile - 1) / kTile, sms = device_sms();
-  const int64_t most = tiles < kMaxCluster ? (tiles < 1 ? 1 : tiles) : kMaxCluster;
-  // the cluster whose fullest SM has least to do; the smaller one of two alike
-  double best = 1e30;
-  for (int64_t k = 1; k <= most; ++k) {
-    const int64_t ctas = blocks * k;
-    const int64_t per_sm = (ctas + sms - 1) / sms;
-    const double cost = static_cast<double>(per_sm) / static_cast<double>(k);
-    if (cost < best * 0.98) best = cost, s.cluster = static_cast<int>(k);
+// Clusters of k CTAs that run at the same time, a kernel's CTAs `resident` to an SM:
+// as the device says (a cluster lies within a group of SMs, which leaves places
+// over), once for each kernel, k and device; without a device its places' number.
+template <auto kernel>
+int64_t clusters_at_once(int threads, int smem, int resident, int k) {
+  static std::atomic<int> known[64][kMaxCluster + 1];
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    cudaGetLastError();
+    return device_sms() * static_cast<int64_t>(resident) / k;
   }
-  const int64_t want = sms * resident / (blocks * s.cluster);
+  int n = known[dev][k].load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(k), 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = static_cast<unsigned>(k);
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) {
+      cudaGetLastError();
+      n = device_sms() * resident / k;
+    }
+    known[dev][k].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+// The largest cluster of which those of all blocks of channels run at the same
+// time: one more CTA in each makes a second round of clusters (4096 x 7680 bf16: 106
+// us with four CTAs, 92 with five, 84 with six, of which 120 fit, and 124 with
+// seven).  Where eight leave room, packed sequences are cut into segments.
+template <auto kernel>
+Split split_rows(int threads, int smem, int resident, int64_t rows, int64_t seqs,
+                 int64_t blocks) {
+  Split s;
+  const int64_t tiles = (rows + kTile - 1) / kTile;
+  const int64_t most = tiles < kMaxCluster ? (tiles < 1 ? 1 : tiles) : kMaxCluster;
+  int64_t room = clusters_at_once<kernel>(threads, smem, resident, 1);
+  for (int k = 2; k <= most; ++k) {
+    const int64_t n = clusters_at_once<kernel>(threads, smem, resident, k);
+    if (blocks <= n) s.cluster = k, room = n;
+  }
+  const int64_t want = room / blocks;
   int64_t parts = want < seqs ? want : seqs;
   if (parts > tiles / s.cluster) parts = tiles / s.cluster;
   if (parts > 1) s.segments = static_cast<int>(parts < 65535 ? parts : 65535);
@@ -1113,34 +1128,46 @@ int64_t blocks_of(int64_t width) { return (width + kCols - 1) / kCols; }
 template <typename T>
 int launch_forward(Params& p, cudaStream_t s) {
   const int64_t blocks = blocks_of(p.width);
-  const Split k = split_rows(p.q.rows, p.q.seqs, blocks, sizeof(T) == 2 ? 4 : 3);
-  p.segments = k.segments;
-  p.fault = device_fault_word();
-  if (!p.fault) return GGRN_ERR_CUDA;
-  if (p.mute && k.cluster == 1) return GGRN_ERR_UNSUPPORTED;
-  constexpr int kSmem = 3 * kTile * kCols * sizeof(T);
+  constexpr int kSmem = kTile * forward::pitch<T>() * sizeof(T);
   const cudaError_t e = allow_shared_memory<forward::k_recur<T>>(kSmem);
   if (e != cudaSuccess) {
     record_cuda_error(e);
     return GGRN_ERR_CUDA;
   }
+  const Split k = split_rows<forward::k_recur<T>>(forward::kThreads, kSmem, sizeof(T) == 2 ? 5 : 4,
+                                                  p.q.rows, p.q.seqs, blocks);
+  p.segments = k.segments;
+  p.fault = device_fault_word();
+  if (!p.fault) return GGRN_ERR_CUDA;
+  if (p.mute && k.cluster == 1) return GGRN_ERR_UNSUPPORTED;
   return launch_cluster(forward::k_recur<T>, blocks, k, forward::kThreads, kSmem, s, p);
+}
+template <typename T>
+constexpr int backward_smem() {
+  return backward::stages<T>() * 4 * kTile * kCols * static_cast<int>(sizeof(T));
+}
+template <typename T>
+Split split_backward(int64_t rows, int64_t seqs, int64_t width) {
+  constexpr int kSmem = backward_smem<T>();
+  if (allow_shared_memory<backward::k_recur_backward<T>>(kSmem) != cudaSuccess) cudaGetLastError();
+  return split_rows<backward::k_recur_backward<T>>(backward::kThreads, kSmem, 2, rows, seqs,
+                                                   blocks_of(width));
 }
 template <typename T>
 int launch_backward(Params& p, float* sums, cudaStream_t s) {
   const int64_t blocks = blocks_of(p.width);
-  const Split k = split_rows(p.q.rows, p.q.seqs, blocks, 2);
-  p.segments = k.segments;
-  p.fault = device_fault_word();
-  if (!p.fault) return GGRN_ERR_CUDA;
-  float* const da = p.da;
-  if (k.segments > 1) p.da = sums;
-  constexpr int kSmem = backward::stages<T>() * 4 * kTile * kCols * sizeof(T);
+  constexpr int kSmem = backward_smem<T>();
   const cudaError_t e = allow_shared_memory<backward::k_recur_backward<T>>(kSmem);
   if (e != cudaSuccess) {
     record_cuda_error(e);
     return GGRN_ERR_CUDA;
   }
+  const Split k = split_backward<T>(p.q.rows, p.q.seqs, p.width);
+  p.segments = k.segments;
+  p.fault = device_fault_word();
+  if (!p.fault) return GGRN_ERR_CUDA;
+  float* const da = p.da;
+  if (k.segments > 1) p.da = sums;
   const int st = launch_cluster(backward::k_recur_backward<T>, blocks, k, backward::kThreads, kSmem,
                                 s, p);
   if (st != GGRN_OK || k.segments == 1) return st;
@@ -1273,7 +1300,10 @@ Space space_of(const ggrn_recur_backward_call& c) {
   const int64_t tiles = (c.rows + kTile - 1) / kTile;
   Space s = {c.saved ? 0 : tiles * c.width * 4, 0};
   s.saved = (s.saved + 15) / 16 * 16;
-  const int64_t most = split_rows(c.rows, c.seqs, blocks_of(c.width), 2).segments;
+  const Split k = c.dtype == kF32   ? split_backward<float>(c.rows, c.seqs, c.width)
+                  : c.dtype == kF16 ? split_backward<__half>(c.rows, c.seqs, c.width)
+                                    : split_backward<__nv_bfloat16>(c.rows, c.seqs, c.width);
+  const int64_t most = k.segments;
   if (most > 1) s.sums = most * c.width * 4;
   return s;
 }
