@@ -10,6 +10,40 @@
 
 namespace ggrn {
 
+// ---------------------------------------------------------------------------
+// Two f32 in a register pair (see fma2 in ggrn_kernels.cuh): values that stay
+// pairs from their load to their store need no moves between registers.
+// ---------------------------------------------------------------------------
+using Two = unsigned long long;  // two f32
+__device__ __forceinline__ Two fma(Two a, Two b, Two c) {
+  Two r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ Two mul(Two a, Two b) {
+  Two r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Two add(Two a, Two b) {
+  Two r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// f of each half.
+template <typename F>
+__device__ __forceinline__ Two each(Two a, F f) {
+  float x, y;
+  upk2(a, x, y);
+  return pk2(f(x), f(y));
+}
+// A constant that stays in registers: made once, where it is written, and not
+// again at each use (which takes two moves).
+__device__ __forceinline__ Two held(float v) {
+  Two r;
+  asm volatile("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(v));
+  return r;
+}
 // The sequences of a call (see ggrn.h): cu == NULL means seqs equal ones.
 struct Seqs {
   const int32_t* cu;

@@ -8,9 +8,9 @@
 namespace ggrn {
 namespace norms {
 
-// out[c] = the sum of in[k, c] over k < n, in a fixed order: sixteen threads to
-// a column, each every sixteenth row.
-constexpr int kSumRows = 16;
+// out[c] = the sum of in[k, c] over k < n, in a fixed order: 32 threads to a
+// column, each every 32nd row.
+constexpr int kSumRows = 32;
 __global__ void __launch_bounds__(32 * kSumRows) k_column_sum(const float* in0, const float* in1,
                                                               float* out0, float* out1, int64_t n,
                                                               int64_t columns) {
@@ -23,7 +23,7 @@ __global__ void __launch_bounds__(32 * kSumRows) k_column_sum(const float* in0, 
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   float t = 0.0f;
   if (c < columns) {
-#pragma unroll 8
+#pragma unroll 16
     for (int64_t k = row; k < n; k += kSumRows) t += in[k * columns + c];
   }
   s[row][lane] = t;
@@ -37,22 +37,27 @@ Plan plan(int kind, int es, int64_t rows, int64_t groups, int64_t gs, int elems)
   Plan k;
   k.elems = elems;
   const int64_t nvec = gs / elems;
+  int vpl = most_elems(kind) / elems;
+  vpl = vpl > 4 ? 4 : vpl;
   int lanes = 1;
-  while (lanes < 32 && lanes * 4 < nvec) lanes <<= 1;
-  if (nvec <= lanes * 4) {
+  while (lanes < 32 && lanes * vpl < nvec) lanes <<= 1;
+  if (nvec <= lanes * vpl) {
     // several groups to a CTA
-    k.vpl = nvec <= 1 ? 1 : nvec <= 2 * lanes ? 2 : 4;
+    k.vpl = nvec <= lanes ? 1 : nvec <= 2 * lanes ? 2 : 4;
     k.threads = 256;
     k.lanes = lanes;
     const int teams = k.threads / lanes;
     k.team_groups = static_cast<int>(groups < teams ? groups : teams);
     k.team_rows = teams / k.team_groups;
   } else {
-    // a CTA to a group
+    // a CTA to a group: as many vectors a thread as it holds well, fewer threads to
+    // sum over, or else as many as it takes
     k.vpl = 0;
-    for (int v : {1, 2, 4}) {
+    for (int v : {vpl, 4}) {
       const int64_t threads = ((nvec + v - 1) / v + 31) / 32 * 32;
-      if (threads > threads_of(v)) continue;
+      if (threads > threads_of(kind, v * elems) ||
+          threads * v * elems * es * inputs_of(kind) * kDepth > kRingMost)
+        continue;
       k.vpl = v;
       k.threads = static_cast<int>(threads);
       break;
@@ -65,13 +70,12 @@ Plan plan(int kind, int es, int64_t rows, int64_t groups, int64_t gs, int elems)
   const int64_t sms = device_sms();
   int64_t resident = 2048 / k.threads;
   if (k.vpl) {
-    resident = static_cast<int64_t>(resident_of(k.vpl)) * threads_of(k.vpl) / k.threads;
+    resident = room_of(kind, k.vpl * elems) / k.threads;
     const int row = inputs_of(kind) * k.vpl * k.threads * elems * es;
-    if (resident > 8) resident = 8;
-    // rows of copies in flight: what is left of an SM's shared memory
-    int64_t depth = (200 << 10) / resident / row;
-    k.depth = static_cast<int>(depth > kMaxDepth ? kMaxDepth : depth < 2 ? 2 : depth);
-    k.smem = k.depth * row;
+    if (resident > (216 << 10) / (kDepth * row + 2048)) resident = (216 << 10) / (kDepth * row + 2048);
+    if (resident > 16) resident = 16;
+    if (resident < 1) resident = 1;
+    k.smem = kDepth * row;
   }
   const int64_t most = (rows + k.team_rows - 1) / k.team_rows;
   k.slices = (sms * resident) / k.blocks;
@@ -132,7 +136,6 @@ int launch(int kind, int dtype, Params& p, const Plan& k, void* workspace, float
   p.team_groups = k.team_groups;
   p.team_rows = k.team_rows;
   p.nvec = k.nvec;
-  p.depth = k.depth;
   p.gs_f = static_cast<float>(p.gs);
   float* const sums = static_cast<float*>(workspace);
   p.dw = k.sums > 1 ? sums : dw;

@@ -46,7 +46,6 @@ struct Params {
   int team_groups;  // groups that the CTA's teams hold at a time
   int team_rows;    // rows that they hold at a time
   int nvec;         // vectors of a group
-  int depth;        // rows of copies in flight
   float eps, gs_f;
 };
 
@@ -56,7 +55,7 @@ struct Plan {
   int vpl = 1;       // vectors of a thread (0: the form that reads a group again)
   int threads = 0, lanes = 0, team_groups = 1, team_rows = 1, nvec = 0;
   int64_t slices = 0, blocks = 1;  // grid: rows, groups
-  int depth = 1, smem = 0;
+  int smem = 0;
   int64_t sums = 0, columns = 0;   // partial sums
 };
 
@@ -81,23 +80,32 @@ struct Block {
       *to = *from;
     }
   }
-  __device__ __forceinline__ void get(float (&f)[E]) const {
-    if constexpr (E == Elem<T>::E) {
-      Elem<T>::unpack(w, f);
-    } else if constexpr (E == 1) {
-      f[0] = static_cast<float>(w);
+  // As pairs (one element: the first half of one, the other 0).
+  static constexpr int N = E > 1 ? E / 2 : 1;
+  __device__ __forceinline__ void get(Two (&v)[N]) const {
+    if constexpr (E == 1) {
+      v[0] = pk2(static_cast<float>(w), 0.0f);
     } else if constexpr (sizeof(T) == 4) {
-      f[0] = __uint_as_float(w.x), f[1] = __uint_as_float(w.y);
+      v[0] = pk2(__uint_as_float(w.x), __uint_as_float(w.y));
+      if constexpr (E == 4) v[1] = pk2(__uint_as_float(w.z), __uint_as_float(w.w));
     } else {
-      Elem<T>::unpack2(w.x, f[0], f[1]);
-      Elem<T>::unpack2(w.y, f[2], f[3]);
+      v[0] = two(w.x), v[1] = two(w.y);
+      if constexpr (E == 8) v[2] = two(w.z), v[3] = two(w.w);
     }
   }
-  __device__ __forceinline__ static void put(T* p, const float (&f)[E]) {
-    if constexpr (E == Elem<T>::E) {
-      st_stream(p, Elem<T>::pack(f));
-    } else if constexpr (E == 1) {
+  __device__ __forceinline__ static Two two(uint32_t u) {
+    float x, y;
+    Elem<T>::unpack2(u, x, y);
+    return pk2(x, y);
+  }
+  __device__ __forceinline__ static void put(T* p, const Two (&v)[N]) {
+    float f[2 * N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) upk2(v[k], f[2 * k], f[2 * k + 1]);
+    if constexpr (E == 1) {
       Elem<T>::store1(p, 0, f[0]);
+    } else if constexpr (E == Elem<T>::E) {
+      st_stream(p, Elem<T>::pack(f));
     } else if constexpr (sizeof(T) == 4) {
       __stcs(reinterpret_cast<float2*>(p), make_float2(f[0], f[1]));
     } else {
@@ -109,70 +117,26 @@ struct Block {
 __device__ __forceinline__ void copies_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
-// Waits until at most n of the thread's groups of copies are in flight.
-__device__ __forceinline__ void copies_wait(int n) {
-  switch (n) {
-    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
-    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
-    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
-    default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
-  }
+constexpr int kRingMost = 200 << 10;  // bytes of a CTA's ring
+// Rows of a ring: two ahead of the one that is read.
+constexpr int kDepth = 3;
+// Waits until the copies of the row that is read have landed.
+__device__ __forceinline__ void copies_wait() {
+  static_assert(kDepth == 3, "the groups that may be in flight");
+  asm volatile("cp.async.wait_group 2;" ::: "memory");
 }
-constexpr int kMaxDepth = 4;
+__device__ __forceinline__ void copies_wait_all() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
 
-// Pairs of f32 (see mul2 and fma2), for an even E; one by one for E = 1.
-// d[k] = a[k] b[k] + c[k] with b or c the same for all where it is a number.
-template <int E, typename B, typename C>
-__device__ __forceinline__ void fma_n(float (&d)[E], const float (&a)[E], const B& b, const C& c) {
-  const auto at = [](const auto& v, int k) {
-    if constexpr (std::is_same<std::decay_t<decltype(v)>, float>::value) return v;
-    else return v[k];
-  };
-  if constexpr (E == 1) {
-    d[0] = fmaf(a[0], at(b, 0), at(c, 0));
-  } else {
-#pragma unroll
-    for (int k = 0; k < E; k += 2)
-      fma2(d[k], d[k + 1], a[k], a[k + 1], at(b, k), at(b, k + 1), at(c, k), at(c, k + 1));
-  }
+__device__ __forceinline__ Two both(float v) { return pk2(v, v); }
+// A sum kept in two halves (of single elements: in the first).
+template <int E>
+__device__ __forceinline__ float value(Two s) {
+  float x, y;
+  upk2(s, x, y);
+  return E == 1 ? x : x + y;
 }
-template <int E, typename B>
-__device__ __forceinline__ void mul_n(float (&d)[E], const float (&a)[E], const B& b) {
-  const auto at = [](const auto& v, int k) {
-    if constexpr (std::is_same<std::decay_t<decltype(v)>, float>::value) return v;
-    else return v[k];
-  };
-  if constexpr (E == 1) {
-    d[0] = a[0] * at(b, 0);
-  } else {
-#pragma unroll
-    for (int k = 0; k < E; k += 2)
-      mul2(d[k], d[k + 1], a[k], a[k + 1], at(b, k), at(b, k + 1));
-  }
-}
-// A sum kept in two halves.
-struct Sum {
-  float lo = 0.0f, hi = 0.0f;
-  template <int E>
-  __device__ __forceinline__ void add(const float (&a)[E]) {
-    if constexpr (E == 1) {
-      lo += a[0];
-    } else {
-#pragma unroll
-      for (int k = 0; k < E; k += 2) fma2(lo, hi, a[k], a[k + 1], 1.0f, 1.0f, lo, hi);
-    }
-  }
-  template <int E>
-  __device__ __forceinline__ void add(const float (&a)[E], const float (&b)[E]) {
-    if constexpr (E == 1) {
-      lo = fmaf(a[0], b[0], lo);
-    } else {
-#pragma unroll
-      for (int k = 0; k < E; k += 2) fma2(lo, hi, a[k], a[k + 1], b[k], b[k + 1], lo, hi);
-    }
-  }
-  __device__ __forceinline__ float value() const { return lo + hi; }
-};
 
 // sigmoid(z), as silu<T> has it.
 template <typename T>
@@ -181,17 +145,30 @@ __device__ __forceinline__ float sigmoid(float z) {
   return rcp_approx(1.0f + ex2_approx(z * -1.4426950408889634f));
 }
 
+template <typename T>
+__device__ __forceinline__ Two sigmoid2(Two z, Two log2e, Two one) {
+  if constexpr (Elem<T>::kExactSilu) return each(z, sigmoid<T>);
+  return each(add(each(mul(z, log2e), ex2_approx), one), rcp_approx);
+}
+
 // The sums of N values over a team, in every one of its threads.  A team that is
 // the CTA goes through shared memory, in one of two places in turn (`place`): a
 // barrier lies between two uses of a place.
 template <int N>
 __device__ __forceinline__ void team_sum(float (&v)[N], int lanes, float4* s_sum, int place) {
-  const int most = lanes < 32 ? lanes : 32;
-  for (int o = most >> 1; o; o >>= 1) {
+  if (lanes < 32) {
+    for (int o = lanes >> 1; o; o >>= 1) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+    }
+    return;
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
 #pragma unroll
     for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
   }
-  if (lanes <= 32) return;
+  if (lanes == 32) return;
   // [sum][warp]: read four warps at a time, the places behind the last one zeros
   float* s = reinterpret_cast<float*>(s_sum + place * 3 * (kMaxWarps / 4));
   const int warp = threadIdx.x >> 5, fours = (lanes + 127) >> 7;
@@ -223,15 +200,26 @@ __device__ __forceinline__ float weight_at(const void* w, int64_t c, int64_t j) 
 // Matrices that a kind reads.
 constexpr int inputs_of(int kind) { return kind == kLayerNorm ? 1 : kind == kLayerNormGrad ? 2 : 3; }
 
-// Most threads of a CTA, and CTAs that the registers have to leave room for.
-constexpr int threads_of(int vpl) { return vpl == 4 ? kMaxThreads : 256; }
-constexpr int resident_of(int vpl) { return vpl == 1 ? 4 : vpl == 2 ? 3 : 1; }
+// Threads of an SM that a kernel's registers leave room for, by the elements that a
+// thread holds of each matrix, and the most of a CTA.
+__host__ __device__ constexpr int room_of(int kind, int elems) {
+  return kind == kLayerNorm ? (elems <= 8 ? 1024 : elems <= 16 ? 768 : 512)
+                            : (elems <= 4 ? 1024 : elems <= 8 ? 768 : 512);
+}
+__host__ __device__ constexpr int threads_of(int kind, int elems) {
+  return room_of(kind, elems) == 768 ? 256 : kMaxThreads;
+}
+// Most elements of a thread: more need more registers than there are (a team of 32
+// times as many, or a CTA of 512, may hold a larger group all the same).
+__host__ __device__ constexpr int most_elems(int kind) { return kind == kLayerNorm ? 32 : 16; }
 
 // A team goes down its rows; each thread copies its own vectors of the rows
 // ahead into its own places of a ring in shared memory (so that no thread waits
 // for another's copies), and reads them from there for each pass.
 template <int KIND, typename T, int E, int VPL>
-__global__ void __launch_bounds__(threads_of(VPL), resident_of(VPL)) k_norm(const Params p) {
+__global__ void __launch_bounds__(threads_of(KIND, VPL * E),
+                                  room_of(KIND, VPL * E) / threads_of(KIND, VPL * E))
+    k_norm(const Params p) {
   constexpr bool kGrad = KIND != kLayerNorm, kGated = KIND == kMamba2Grad || KIND == kOnnxGrad;
   constexpr bool kLayer = !kGated;
   constexpr int M = inputs_of(KIND);
@@ -250,185 +238,204 @@ __global__ void __launch_bounds__(threads_of(VPL), resident_of(VPL)) k_norm(cons
   const T* x = static_cast<const T*>(p.x) + c0;
   const T* dout = static_cast<const T*>(p.dout) + c0;
   const T* gate = static_cast<const T*>(p.gate) + c0;
-  // the thread's places: [depth][M][VPL], a CTA's threads beside each other
+  // the thread's places: [row of the ring][M][VPL], a CTA's threads beside each other
   using Word = typename Vec::Word;
   Word* const ring = reinterpret_cast<Word*>(s_ring) + threadIdx.x;
+  const int place = M * VPL * blockDim.x;  // of a row
   const int64_t step = static_cast<int64_t>(gridDim.x) * p.team_rows;
-  const auto has = [&](int i) { return lane + i * p.lanes < p.nvec; };
-  const auto fetch = [&](int64_t row, int place) {
-    if (mine && row < p.rows) {
+  // the thread's vectors: the first `count` of VPL
+  int count = 0;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) count += mine && lane + i * p.lanes < p.nvec;
+  const auto has = [&](int i) { return i < count; };
+  int64_t row = static_cast<int64_t>(blockIdx.x) * p.team_rows + row_of_team, ahead = row;
+  x += row * p.xs, dout += row * p.ds, gate += row * p.gts;
+  Word* to = ring;
+  const auto fetch = [&]() {
+    if (ahead < p.rows) {
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
         if (!has(i)) continue;
-        Word* to = ring + (place * M * VPL + i) * blockDim.x;
-        Vec::copy(to, x + row * p.xs + i * apart);
-        if constexpr (kGrad) Vec::copy(to + VPL * blockDim.x, dout + row * p.ds + i * apart);
-        if constexpr (kGated) Vec::copy(to + 2 * VPL * blockDim.x, gate + row * p.gts + i * apart);
+        Vec::copy(to + i * blockDim.x, x + i * apart);
+        if constexpr (kGrad) Vec::copy(to + (VPL + i) * blockDim.x, dout + i * apart);
+        if constexpr (kGated) Vec::copy(to + (2 * VPL + i) * blockDim.x, gate + i * apart);
       }
     }
     copies_commit();
+    ahead += step;
+    x += step * p.xs;
+    if constexpr (kGrad) dout += step * p.ds;
+    if constexpr (kGated) gate += step * p.gts;
+    to = to == ring + (kDepth - 1) * place ? ring : to + place;
   };
-  int64_t row = static_cast<int64_t>(blockIdx.x) * p.team_rows + row_of_team;
-  for (int k = 0; k < p.depth - 1; ++k) fetch(row + k * step, k);
+  for (int k = 0; k < kDepth - 1; ++k) fetch();
 
-  float w[VPL][E], b[kLayer && !kGrad ? VPL : 1][E];
+  constexpr int N = Vec::N;
+  Two w[VPL][N], b[kLayer && !kGrad ? VPL : 1][N];
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
+    float wf[2 * N], bf[2 * N];
 #pragma unroll
-    for (int k = 0; k < E; ++k) {
+    for (int k = 0; k < 2 * N; ++k) {
       const int64_t at = i * apart + k;
-      w[i][k] = mine && has(i) ? weight_at<KIND, T>(p.w, c0 + at, lane * E + at) : 0.0f;
-      if constexpr (kLayer && !kGrad) b[i][k] = mine && has(i) && p.b ? __ldg(p.b + c0 + at) : 0.0f;
+      const bool in = has(i) && k < E;
+      wf[k] = in ? weight_at<KIND, T>(p.w, c0 + at, lane * E + at) : 0.0f;
+      if constexpr (kLayer && !kGrad) bf[k] = in && p.b ? __ldg(p.b + c0 + at) : 0.0f;
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      w[i][k] = pk2(wf[2 * k], wf[2 * k + 1]);
+      if constexpr (kLayer && !kGrad) b[i][k] = pk2(bf[2 * k], bf[2 * k + 1]);
+      // (kept, not loaded again for every row)
+      asm volatile("" : "+l"(w[i][k]));
+      if constexpr (kLayer && !kGrad) asm volatile("" : "+l"(b[i][k]));
     }
   }
-  float dw[kGrad ? VPL : 1][E], db[KIND == kLayerNormGrad ? VPL : 1][E];
+  Two dw[kGrad ? VPL : 1][N], db[KIND == kLayerNormGrad ? VPL : 1][N];
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
 #pragma unroll
-    for (int k = 0; k < E; ++k) {
-      if constexpr (kGrad) dw[i][k] = 0.0f;
-      if constexpr (KIND == kLayerNormGrad) db[i][k] = 0.0f;
+    for (int k = 0; k < N; ++k) {
+      if constexpr (kGrad) dw[i][k] = 0;
+      if constexpr (KIND == kLayerNormGrad) db[i][k] = 0;
     }
   }
+  const Two one = held(1.0f), minus = held(-1.0f), log2e = held(-1.4426950408889634f);
   if (p.lanes > 32) clear_sums(s_sum);
 
-  int place = 0, turn = 0;
+  int turn = 0;
+  const Word* from = ring;
+  T* out = static_cast<T*>(p.out) + row * p.os + c0;
+  T* dgate = static_cast<T*>(p.dgate) + row * p.dgs + c0;
   // (the rows of the CTA's teams follow each other: all take as many turns)
   for (int64_t first = static_cast<int64_t>(blockIdx.x) * p.team_rows; first < p.rows;
-       first += step, row += step) {
-    {
-      const int ahead = place == 0 ? p.depth - 1 : place - 1;
-      fetch(row + (p.depth - 1) * step, ahead);
-    }
-    copies_wait(p.depth - 1);
-    const bool live = mine && row < p.rows;
-    const Word* from = ring + place * M * VPL * blockDim.x;
-    place = place + 1 == p.depth ? 0 : place + 1;
-    const auto load = [&](int m, int i, float (&f)[E]) {
+       first += step) {
+    fetch();
+    copies_wait();
+    const bool live = row < p.rows;
+    const auto load = [&](int m, int i, Two (&f)[N]) {
       Vec v;
       v.w = from[(m * VPL + i) * blockDim.x];
       v.get(f);
     };
-
     if constexpr (kLayer) {
-      float mean[1];
-      {
-        Sum s;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-          if (!live || !has(i)) continue;
-          float f[E];
-          load(0, i, f);
-          s.add(f);
-        }
-        mean[0] = s.value();
-      }
-      team_sum<1>(mean, p.lanes, s_sum, 0);
-      const float less = -__fdiv_rn(mean[0], p.gs_f);
-      constexpr int S = kGrad ? 3 : 1;
-      Sum q[3];
+      Two x[VPL][N], g[kGrad ? VPL : 1][N];
+      Two sum = 0;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
         if (!live || !has(i)) continue;
-        float d[E];
-        load(0, i, d);
-        fma_n(d, d, 1.0f, less);
-        q[0].add(d, d);
-        if constexpr (kGrad) {
-          float u[E];
-          load(1, i, u);
-          mul_n(u, u, w[i]);
-          q[1].add(u);
-          q[2].add(u, d);
+        load(0, i, x[i]);
+        if constexpr (kGrad) load(1, i, g[i]);
+#pragma unroll
+        for (int k = 0; k < N; ++k) sum = add(sum, x[i][k]);
+      }
+      float mean[1] = {value<E>(sum)};
+      team_sum<1>(mean, p.lanes, s_sum, 0);
+      const Two less = both(-__fdiv_rn(mean[0], p.gs_f));
+      constexpr int S = kGrad ? 3 : 1;
+      Two q[3] = {0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        if (!live || !has(i)) continue;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          x[i][k] = add(x[i][k], less);
+          q[0] = fma(x[i][k], x[i][k], q[0]);
+          if constexpr (kGrad) {
+            const Two u = mul(g[i][k], w[i][k]);
+            q[1] = add(q[1], u);
+            q[2] = fma(u, x[i][k], q[2]);
+          }
         }
       }
       float s[S];
 #pragma unroll
-      for (int k = 0; k < S; ++k) s[k] = q[k].value();
+      for (int k = 0; k < S; ++k) s[k] = value<E>(q[k]);
       team_sum<S>(s, p.lanes, s_sum, 1);
-      const float n = rsqrtf(__fdiv_rn(s[0], p.gs_f) + p.eps);
-      float mu = 0.0f, mud = 0.0f;
+      const float nf = rsqrtf(__fdiv_rn(s[0], p.gs_f) + p.eps);
+      const Two n = both(nf);
+      Two mu = 0, mud = 0;
       if constexpr (kGrad) {
-        mu = -__fdiv_rn(s[1], p.gs_f);
-        mud = -__fdiv_rn(s[2], p.gs_f) * n * n;
+        mu = both(-__fdiv_rn(s[1], p.gs_f));
+        mud = both(-__fdiv_rn(s[2], p.gs_f) * nf * nf);
       }
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
         if (!live || !has(i)) continue;
-        float d[E], o[E];
-        load(0, i, d);
-        fma_n(d, d, 1.0f, less);
-        if constexpr (kGrad) {
-          float gv[E];
-          load(1, i, gv);
-          fma_n(o, gv, w[i], mu);
-          float t[E];
-          fma_n(t, d, mud, o);
-          mul_n(o, t, n);
-          mul_n(d, d, n);
-          fma_n(dw[i], gv, d, dw[i]);
-          fma_n(db[i], gv, 1.0f, db[i]);
-        } else {
-          mul_n(d, d, n);
-          fma_n(o, d, w[i], b[i]);
+        Two o[N];
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          const Two xh = mul(x[i][k], n);
+          if constexpr (kGrad) {
+            o[k] = mul(fma(x[i][k], mud, fma(g[i][k], w[i][k], mu)), n);
+            dw[i][k] = fma(g[i][k], xh, dw[i][k]);
+            db[i][k] = add(g[i][k], db[i][k]);
+          } else {
+            o[k] = fma(xh, w[i][k], b[i][k]);
+          }
         }
-        Vec::put(static_cast<T*>(p.out) + row * p.os + c0 + i * apart, o);
+        Vec::put(out + i * apart, o);
       }
     } else {
-      Sum q[2];
-      float sig[VPL][E];
+      // MAMBA2 keeps silu, y s', y silu and dout; ONNX u, dout w s', y and dout silu
+      Two ka[VPL][N], kb[VPL][N], kv[VPL][N], kg[VPL][N];
+      Two q[2] = {0, 0};
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
         if (!live || !has(i)) continue;
-        float y[E], u[E], z[E];
-        load(0, i, y), load(1, i, u), load(2, i, z);
+        Two y[N], g[N], z[N];
+        load(0, i, y), load(1, i, g), load(2, i, z);
 #pragma unroll
-        for (int k = 0; k < E; ++k) sig[i][k] = sigmoid<T>(z[k]);
-        mul_n(z, z, sig[i]);  // silu
-        mul_n(u, u, w[i]);
-        if constexpr (KIND == kMamba2Grad) mul_n(y, y, z);
-        else mul_n(u, u, z);
-        q[0].add(y, y);
-        q[1].add(u, y);
-      }
-      float s[2] = {q[0].value(), q[1].value()};
-      team_sum<2>(s, p.lanes, s_sum, turn++ & 1);
-      const float n = rsqrtf(__fdiv_rn(s[0], p.gs_f) + p.eps);
-      const float muv = -__fdiv_rn(s[1], p.gs_f) * n * n;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        if (!live || !has(i)) continue;
-        float y[E], gv[E], z[E], act[E], slope[E], u[E], t[E];
-        load(0, i, y), load(1, i, gv), load(2, i, z);
-        mul_n(act, z, sig[i]);
-        fma_n(t, sig[i], -1.0f, 1.0f);
-        fma_n(t, z, t, 1.0f);
-        mul_n(slope, t, sig[i]);
-        mul_n(u, gv, w[i]);
-        if constexpr (KIND == kMamba2Grad) {
-          float v[E];
-          mul_n(v, y, act);
-          fma_n(t, v, muv, u);
-          mul_n(t, t, n);  // dv
-          mul_n(v, v, n);
-          fma_n(dw[i], gv, v, dw[i]);
-          mul_n(act, t, act);    // dy
-          mul_n(t, t, y);
-          mul_n(slope, t, slope);  // dz
-        } else {
-          mul_n(t, u, act);
-          fma_n(t, y, muv, t);
-          mul_n(y, y, n);
-          mul_n(gv, gv, act);
-          fma_n(dw[i], gv, y, dw[i]);
-          mul_n(act, t, n);      // dy
-          mul_n(u, u, y);
-          mul_n(slope, u, slope);  // dz
+        for (int k = 0; k < N; ++k) {
+          const Two sig = sigmoid2<T>(z[k], log2e, one);
+          const Two act = mul(z[k], sig);
+          const Two slope = mul(fma(z[k], fma(sig, minus, one), one), sig);
+          const Two u = mul(g[k], w[i][k]);
+          if constexpr (KIND == kMamba2Grad) {
+            ka[i][k] = act;
+            kb[i][k] = mul(y[k], slope);
+            kv[i][k] = mul(y[k], act);
+            kg[i][k] = g[k];
+            q[1] = fma(u, kv[i][k], q[1]);
+          } else {
+            ka[i][k] = mul(u, act);
+            kb[i][k] = mul(u, slope);
+            kv[i][k] = y[k];
+            kg[i][k] = mul(g[k], act);
+            q[1] = fma(ka[i][k], y[k], q[1]);
+          }
+          q[0] = fma(kv[i][k], kv[i][k], q[0]);
         }
-        Vec::put(static_cast<T*>(p.out) + row * p.os + c0 + i * apart, act);
-        Vec::put(static_cast<T*>(p.dgate) + row * p.dgs + c0 + i * apart, slope);
       }
+      float s[2] = {value<E>(q[0]), value<E>(q[1])};
+      team_sum<2>(s, p.lanes, s_sum, turn++ & 1);
+      const float nf = rsqrtf(__fdiv_rn(s[0], p.gs_f) + p.eps);
+      const Two n = both(nf), muv = both(-__fdiv_rn(s[1], p.gs_f) * nf * nf);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        if (!live || !has(i)) continue;
+        Two dy[N], dz[N];
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          const Two vn = mul(kv[i][k], n);
+          dw[i][k] = fma(kg[i][k], vn, dw[i][k]);
+          if constexpr (KIND == kMamba2Grad) {
+            const Two dv = mul(fma(kv[i][k], muv, mul(kg[i][k], w[i][k])), n);
+            dy[k] = mul(dv, ka[i][k]);
+            dz[k] = mul(dv, kb[i][k]);
+          } else {
+            dy[k] = mul(fma(kv[i][k], muv, ka[i][k]), n);
+            dz[k] = mul(kb[i][k], vn);
+          }
+        }
+        Vec::put(out + i * apart, dy);
+        Vec::put(dgate + i * apart, dz);
+      }
+      dgate += step * p.dgs;
     }
+    out += step * p.os;
+    row += step;
+    from = from == ring + (kDepth - 1) * place ? ring : from + place;
   }
 
   if constexpr (kGrad) {
@@ -440,8 +447,14 @@ __global__ void __launch_bounds__(threads_of(VPL), resident_of(VPL)) k_norm(cons
     const int64_t sum = KIND == kOnnxGrad ? blockIdx.y * gridDim.x + blockIdx.x : blockIdx.x;
     const int64_t col0 = KIND == kOnnxGrad ? lane * E : c0;
     float* s_acc = reinterpret_cast<float*>(s_ring);  // (the ring is at its end)
-    copies_wait(0);
-    const auto finish = [&](float (&a)[VPL][E], float* out) {
+    copies_wait_all();
+    const auto finish = [&](const Two (&sums)[VPL][N], float* out) {
+      float a[VPL][2 * N];
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) upk2(sums[i][k], a[i][2 * k], a[i][2 * k + 1]);
+      }
       if (teams > 1) {
         __syncthreads();
 #pragma unroll
@@ -561,21 +574,22 @@ __global__ void __launch_bounds__(kMaxThreads) k_norm_any(const Params p) {
 // ---------------------------------------------------------------------------
 // Launch of a plan.
 // ---------------------------------------------------------------------------
-template <int KIND, typename T, int E, typename Go>
-int go_vpl(const Params& p, const Plan& k, Go go) {
-  constexpr int kMost = 200 << 10;
+template <int KIND, typename T, int E, int VPL, typename Go>
+int go_with(const Plan& k, Go go) {
   if (k.smem > 40 << 10) {  // (48 KB with what a kernel has by itself)
-    cudaError_t e = k.vpl == 1   ? allow_shared_memory<k_norm<KIND, T, E, 1>>(kMost)
-                    : k.vpl == 2 ? allow_shared_memory<k_norm<KIND, T, E, 2>>(kMost)
-                                 : allow_shared_memory<k_norm<KIND, T, E, 4>>(kMost);
+    const cudaError_t e = allow_shared_memory<k_norm<KIND, T, E, VPL>>(kRingMost);
     if (e != cudaSuccess) {
       record_cuda_error(e);
       return GGRN_ERR_CUDA;
     }
   }
-  if (k.vpl == 1) return go(k_norm<KIND, T, E, 1>);
-  if (k.vpl == 2) return go(k_norm<KIND, T, E, 2>);
-  return go(k_norm<KIND, T, E, 4>);
+  return go(k_norm<KIND, T, E, VPL>);
+}
+template <int KIND, typename T, int E, typename Go>
+int go_vpl(const Plan& k, Go go) {
+  if (k.vpl == 1) return go_with<KIND, T, E, 1>(k, go);
+  if (k.vpl == 2) return go_with<KIND, T, E, 2>(k, go);
+  return go_with<KIND, T, E, 4>(k, go);
 }
 template <int KIND, typename T>
 int launch_kind(const Params& p, const Plan& k, cudaStream_t s) {
@@ -585,9 +599,9 @@ int launch_kind(const Params& p, const Plan& k, cudaStream_t s) {
   };
   if (k.vpl == 0) return go(k_norm_any<KIND, T>);
   constexpr int V = 16 / sizeof(T);
-  if (k.elems == V) return go_vpl<KIND, T, V>(p, k, go);
-  if (k.elems == V / 2) return go_vpl<KIND, T, V / 2>(p, k, go);
-  return go_vpl<KIND, T, 1>(p, k, go);
+  if (k.elems == V) return go_vpl<KIND, T, V>(k, go);
+  if (k.elems == V / 2) return go_vpl<KIND, T, V / 2>(k, go);
+  return go_vpl<KIND, T, 1>(k, go);
 }
 
 int launch_f32(int kind, const Params& p, const Plan& k, cudaStream_t s);

@@ -118,33 +118,6 @@ __device__ __forceinline__ float sqrt_approx(float x) {
   return y;
 }
 
-using Two = unsigned long long;  // two f32
-__device__ __forceinline__ Two fma(Two a, Two b, Two c) {
-  Two r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ Two mul(Two a, Two b) {
-  Two r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ Two add(Two a, Two b) {
-  Two r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-template <typename F>
-__device__ __forceinline__ Two each(Two a, F f) {
-  float x, y;
-  upk2(a, x, y);
-  return pk2(f(x), f(y));
-}
-__device__ __forceinline__ Two held(float v) {
-  Two r;
-  asm volatile("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(v));
-  return r;
-}
 struct Constants {
   Two c4 = held(7.67176877707243e-3f), c3 = held(4.1564859449863434e-2f),
       c2 = held(1.666616052389145e-1f), c1 = held(4.999999701976776e-1f), one = held(1.0f),
