@@ -15,27 +15,29 @@ namespace ggrn {
 // pairs from their load to their store need no moves between registers.
 // ---------------------------------------------------------------------------
 using Two = unsigned long long;  // two f32
+__device__ __forceinline__ Two join(float a, float b) {
+  return __builtin_bit_cast(Two, make_float2(a, b));
+}
+__device__ __forceinline__ void split(Two v, float& a, float& b) {
+  const float2 f = __builtin_bit_cast(float2, v);
+  a = f.x, b = f.y;
+}
+__device__ __forceinline__ float2 halves(Two v) { return __builtin_bit_cast(float2, v); }
 __device__ __forceinline__ Two fma(Two a, Two b, Two c) {
-  Two r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
+  return __builtin_bit_cast(Two, __ffma2_rn(halves(a), halves(b), halves(c)));
 }
 __device__ __forceinline__ Two mul(Two a, Two b) {
-  Two r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
+  return __builtin_bit_cast(Two, __fmul2_rn(halves(a), halves(b)));
 }
 __device__ __forceinline__ Two add(Two a, Two b) {
-  Two r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
+  return __builtin_bit_cast(Two, __fadd2_rn(halves(a), halves(b)));
 }
 // f of each half.
 template <typename F>
 __device__ __forceinline__ Two each(Two a, F f) {
   float x, y;
-  upk2(a, x, y);
-  return pk2(f(x), f(y));
+  split(a, x, y);
+  return join(f(x), f(y));
 }
 // A constant that stays in registers: made once, where it is written, and not
 // again at each use (which takes two moves).

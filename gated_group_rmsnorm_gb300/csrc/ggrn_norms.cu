@@ -44,25 +44,31 @@ Plan plan(int kind, int es, int64_t rows, int64_t groups, int64_t gs, int elems)
   if (nvec <= lanes * vpl) {
     // several groups to a CTA
     k.vpl = nvec <= lanes ? 1 : nvec <= 2 * lanes ? 2 : 4;
-    k.threads = 256;
     k.lanes = lanes;
-    const int teams = k.threads / lanes;
-    k.team_groups = static_cast<int>(groups < teams ? groups : teams);
+    const int teams = 256 / lanes;
+    const int64_t blocks = (groups + teams - 1) / teams;  // as full as each other
+    k.team_groups = static_cast<int>((groups + blocks - 1) / blocks);
     k.team_rows = teams / k.team_groups;
+    k.threads = (k.team_groups * k.team_rows * lanes + 31) / 32 * 32;
   } else {
-    // a CTA to a group: as many vectors a thread as it holds well, fewer threads to
-    // sum over, or else as many as it takes
+    // a CTA to a group: as many vectors a thread as it holds well (fewer threads to
+    // sum over: 16384 rows of 3840, gradients, 91 us with two and 140 with one), if
+    // that leaves an SM at least three quarters of the threads it may have
     k.vpl = 0;
-    for (int v : {vpl, 4}) {
+    for (int v : {vpl, vpl / 2, 4}) {
+      if (v < 1 || v > 4) continue;
       const int64_t threads = ((nvec + v - 1) / v + 31) / 32 * 32;
       if (threads > threads_of(kind, v * elems) ||
-          threads * v * elems * es * inputs_of(kind) * kDepth > kRingMost)
+          threads * v * elems * es * inputs_of(kind) * depth_of(kind) > kRingMost)
         continue;
+      const int64_t room = room_of(kind, v * elems), held = room / threads * threads;
+      if (k.vpl && v == vpl / 2 && k.threads * (room_of(kind, vpl * elems) / k.threads) >= held * 3 / 4)
+        continue;
+      if (k.vpl && v == 4) continue;
       k.vpl = v;
       k.threads = static_cast<int>(threads);
-      break;
     }
-    if (k.vpl == 0) k.threads = kMaxThreads;
+    if (k.vpl == 0) k.threads = kAnyThreads;
     k.lanes = k.threads;
   }
   k.nvec = static_cast<int>(k.vpl ? nvec : 0);
@@ -72,10 +78,11 @@ Plan plan(int kind, int es, int64_t rows, int64_t groups, int64_t gs, int elems)
   if (k.vpl) {
     resident = room_of(kind, k.vpl * elems) / k.threads;
     const int row = inputs_of(kind) * k.vpl * k.threads * elems * es;
-    if (resident > (216 << 10) / (kDepth * row + 2048)) resident = (216 << 10) / (kDepth * row + 2048);
+    const int most = (220 << 10) / (depth_of(kind) * row + 2048);
+    if (resident > most) resident = most;
     if (resident > 16) resident = 16;
     if (resident < 1) resident = 1;
-    k.smem = kDepth * row;
+    k.smem = depth_of(kind) * row;
   }
   const int64_t most = (rows + k.team_rows - 1) / k.team_rows;
   k.slices = (sms * resident) / k.blocks;

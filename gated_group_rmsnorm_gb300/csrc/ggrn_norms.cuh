@@ -32,7 +32,8 @@ namespace norms {
 
 enum Kind : int { kLayerNorm = 0, kLayerNormGrad = 1, kMamba2Grad = 2, kOnnxGrad = 3 };
 
-constexpr int kMaxThreads = 512;
+constexpr int kMaxThreads = 768;
+constexpr int kAnyThreads = 512;
 constexpr int kMaxWarps = kMaxThreads / 32;
 
 struct Params {
@@ -84,10 +85,10 @@ struct Block {
   static constexpr int N = E > 1 ? E / 2 : 1;
   __device__ __forceinline__ void get(Two (&v)[N]) const {
     if constexpr (E == 1) {
-      v[0] = pk2(static_cast<float>(w), 0.0f);
+      v[0] = join(static_cast<float>(w), 0.0f);
     } else if constexpr (sizeof(T) == 4) {
-      v[0] = pk2(__uint_as_float(w.x), __uint_as_float(w.y));
-      if constexpr (E == 4) v[1] = pk2(__uint_as_float(w.z), __uint_as_float(w.w));
+      v[0] = join(__uint_as_float(w.x), __uint_as_float(w.y));
+      if constexpr (E == 4) v[1] = join(__uint_as_float(w.z), __uint_as_float(w.w));
     } else {
       v[0] = two(w.x), v[1] = two(w.y);
       if constexpr (E == 8) v[2] = two(w.z), v[3] = two(w.w);
@@ -96,12 +97,12 @@ struct Block {
   __device__ __forceinline__ static Two two(uint32_t u) {
     float x, y;
     Elem<T>::unpack2(u, x, y);
-    return pk2(x, y);
+    return join(x, y);
   }
   __device__ __forceinline__ static void put(T* p, const Two (&v)[N]) {
     float f[2 * N];
 #pragma unroll
-    for (int k = 0; k < N; ++k) upk2(v[k], f[2 * k], f[2 * k + 1]);
+    for (int k = 0; k < N; ++k) split(v[k], f[2 * k], f[2 * k + 1]);
     if constexpr (E == 1) {
       Elem<T>::store1(p, 0, f[0]);
     } else if constexpr (E == Elem<T>::E) {
@@ -118,23 +119,25 @@ __device__ __forceinline__ void copies_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
 constexpr int kRingMost = 200 << 10;  // bytes of a CTA's ring
-// Rows of a ring: two ahead of the one that is read.
-constexpr int kDepth = 3;
-// Waits until the copies of the row that is read have landed.
+// Rows of a ring: those ahead of the one that is read are in flight.
+__host__ __device__ constexpr int depth_of(int kind) {
+  return kind == kLayerNorm || kind == kLayerNormGrad ? 5 : 4;
+}
+// Waits until all but the newest `depth` - 1 rows' copies have landed.
+template <int DEPTH>
 __device__ __forceinline__ void copies_wait() {
-  static_assert(kDepth == 3, "the groups that may be in flight");
-  asm volatile("cp.async.wait_group 2;" ::: "memory");
+  asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
 }
 __device__ __forceinline__ void copies_wait_all() {
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-__device__ __forceinline__ Two both(float v) { return pk2(v, v); }
+__device__ __forceinline__ Two both(float v) { return join(v, v); }
 // A sum kept in two halves (of single elements: in the first).
 template <int E>
 __device__ __forceinline__ float value(Two s) {
   float x, y;
-  upk2(s, x, y);
+  split(s, x, y);
   return E == 1 ? x : x + y;
 }
 
@@ -163,25 +166,48 @@ __device__ __forceinline__ void team_sum(float (&v)[N], int lanes, float4* s_sum
     }
     return;
   }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-#pragma unroll
-    for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-  }
-  if (lanes == 32) return;
   // [sum][warp]: read four warps at a time, the places behind the last one zeros
   float* s = reinterpret_cast<float*>(s_sum + place * 3 * (kMaxWarps / 4));
-  const int warp = threadIdx.x >> 5, fours = (lanes + 127) >> 7;
-  if ((threadIdx.x & 31) == 0) {
+  if (N == 3 && lanes > 32) {
+    // three sums in six shuffles: a quarter of the lanes ends with each (and one with
+    // nothing)
+    const int lane = threadIdx.x & 31;
+    const bool up = lane & 16, right = lane & 8;
+    float a = up ? v[N - 1] : v[0], b = up ? 0.0f : v[1 % N];
+    a += __shfl_xor_sync(0xffffffffu, up ? v[0] : v[N - 1], 16);
+    b += __shfl_xor_sync(0xffffffffu, up ? v[1 % N] : 0.0f, 16);
+    float c = right ? b : a;
+    c += __shfl_xor_sync(0xffffffffu, right ? a : b, 8);
 #pragma unroll
-    for (int k = 0; k < N; ++k) s[k * kMaxWarps + warp] = v[k];
+    for (int o = 4; o; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+    // lanes 0, 8, 16: sums 0, 1, 2
+    if ((lane & 7) == 0 && lane < 24) s[(lane >> 3) * kMaxWarps + (threadIdx.x >> 5)] = c;
+  } else {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+    }
+    if (lanes == 32) return;
+    if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) s[k * kMaxWarps + (threadIdx.x >> 5)] = v[k];
+    }
   }
   __syncthreads();
+  const ulonglong2* q = reinterpret_cast<const ulonglong2*>(s);
+  constexpr int F = kMaxWarps / 4;  // reads of a sum
+  static_assert(F == 6, "those below");
 #pragma unroll
   for (int k = 0; k < N; ++k) {
-    const float4* q = reinterpret_cast<const float4*>(s + k * kMaxWarps);
-    v[k] = 0.0f;
-    for (int w = 0; w < fours; ++w) v[k] += (q[w].x + q[w].y) + (q[w].z + q[w].w);
+    const auto four = [&](int i) { return add(q[k * F + i].x, q[k * F + i].y); };
+    Two t = four(0);
+    if (lanes > 128) t = add(t, four(1));
+    if (lanes > 256) t = add(t, add(four(2), four(3)));
+    if (lanes > 512) t = add(t, add(four(4), four(5)));
+    float x, y;
+    split(t, x, y);
+    v[k] = x + y;
   }
 }
 __device__ __forceinline__ void clear_sums(float4* s_sum) {
@@ -203,15 +229,18 @@ constexpr int inputs_of(int kind) { return kind == kLayerNorm ? 1 : kind == kLay
 // Threads of an SM that a kernel's registers leave room for, by the elements that a
 // thread holds of each matrix, and the most of a CTA.
 __host__ __device__ constexpr int room_of(int kind, int elems) {
-  return kind == kLayerNorm ? (elems <= 8 ? 1024 : elems <= 16 ? 768 : 512)
-                            : (elems <= 4 ? 1024 : elems <= 8 ? 768 : 512);
+  return kind == kLayerNorm       ? (elems <= 8 ? 1024 : elems <= 16 ? 768 : 512)
+         : kind == kLayerNormGrad ? (elems <= 4 ? 1024 : elems <= 8 ? 768 : 512)
+                                  : (elems <= 4 ? 1024 : elems <= 8 ? 768 : 512);
 }
 __host__ __device__ constexpr int threads_of(int kind, int elems) {
-  return room_of(kind, elems) == 768 ? 256 : kMaxThreads;
+  return room_of(kind, elems) == 768 ? 768 : 512;
 }
 // Most elements of a thread: more need more registers than there are (a team of 32
-// times as many, or a CTA of 512, may hold a larger group all the same).
-__host__ __device__ constexpr int most_elems(int kind) { return kind == kLayerNorm ? 32 : 16; }
+// times as many, or a CTA, may hold a larger group all the same).
+__host__ __device__ constexpr int most_elems(int kind) {
+  return kind == kLayerNorm ? 32 : kind == kLayerNormGrad ? 16 : 8;
+}
 
 // A team goes down its rows; each thread copies its own vectors of the rows
 // ahead into its own places of a ring in shared memory (so that no thread waits
@@ -222,7 +251,7 @@ __global__ void __launch_bounds__(threads_of(KIND, VPL * E),
     k_norm(const Params p) {
   constexpr bool kGrad = KIND != kLayerNorm, kGated = KIND == kMamba2Grad || KIND == kOnnxGrad;
   constexpr bool kLayer = !kGated;
-  constexpr int M = inputs_of(KIND);
+  constexpr int M = inputs_of(KIND), kDepth = depth_of(KIND);
   using Vec = Block<T, E>;
   extern __shared__ uint4 s_ring[];
   __shared__ float4 s_sum[2 * 3 * (kMaxWarps / 4)];
@@ -268,6 +297,12 @@ __global__ void __launch_bounds__(threads_of(KIND, VPL * E),
     if constexpr (kGated) gate += step * p.gts;
     to = to == ring + (kDepth - 1) * place ? ring : to + place;
   };
+  // (vectors behind the group's last one read zeros)
+  for (int k = 0; k < kDepth * M; ++k) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (!has(i)) ring[(k * VPL + i) * blockDim.x] = Word{};
+  }
   for (int k = 0; k < kDepth - 1; ++k) fetch();
 
   constexpr int N = Vec::N;
@@ -284,8 +319,8 @@ __global__ void __launch_bounds__(threads_of(KIND, VPL * E),
     }
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-      w[i][k] = pk2(wf[2 * k], wf[2 * k + 1]);
-      if constexpr (kLayer && !kGrad) b[i][k] = pk2(bf[2 * k], bf[2 * k + 1]);
+      w[i][k] = join(wf[2 * k], wf[2 * k + 1]);
+      if constexpr (kLayer && !kGrad) b[i][k] = join(bf[2 * k], bf[2 * k + 1]);
       // (kept, not loaded again for every row)
       asm volatile("" : "+l"(w[i][k]));
       if constexpr (kLayer && !kGrad) asm volatile("" : "+l"(b[i][k]));
@@ -311,7 +346,7 @@ __global__ void __launch_bounds__(threads_of(KIND, VPL * E),
   for (int64_t first = static_cast<int64_t>(blockIdx.x) * p.team_rows; first < p.rows;
        first += step) {
     fetch();
-    copies_wait();
+    copies_wait<kDepth>();
     const bool live = row < p.rows;
     const auto load = [&](int m, int i, Two (&f)[N]) {
       Vec v;
@@ -323,7 +358,6 @@ __global__ void __launch_bounds__(threads_of(KIND, VPL * E),
       Two sum = 0;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
-        if (!live || !has(i)) continue;
         load(0, i, x[i]);
         if constexpr (kGrad) load(1, i, g[i]);
 #pragma unroll
@@ -336,10 +370,10 @@ __global__ void __launch_bounds__(threads_of(KIND, VPL * E),
       Two q[3] = {0, 0, 0};
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
-        if (!live || !has(i)) continue;
+        const Two by = has(i) ? less : 0;
 #pragma unroll
         for (int k = 0; k < N; ++k) {
-          x[i][k] = add(x[i][k], less);
+          x[i][k] = add(x[i][k], by);
           q[0] = fma(x[i][k], x[i][k], q[0]);
           if constexpr (kGrad) {
             const Two u = mul(g[i][k], w[i][k]);
@@ -354,27 +388,28 @@ __global__ void __launch_bounds__(threads_of(KIND, VPL * E),
       team_sum<S>(s, p.lanes, s_sum, 1);
       const float nf = rsqrtf(__fdiv_rn(s[0], p.gs_f) + p.eps);
       const Two n = both(nf);
-      Two mu = 0, mud = 0;
-      if constexpr (kGrad) {
-        mu = both(-__fdiv_rn(s[1], p.gs_f));
-        mud = both(-__fdiv_rn(s[2], p.gs_f) * nf * nf);
-      }
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        if (!live || !has(i)) continue;
-        Two o[N];
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-          const Two xh = mul(x[i][k], n);
-          if constexpr (kGrad) {
-            o[k] = mul(fma(x[i][k], mud, fma(g[i][k], w[i][k], mu)), n);
-            dw[i][k] = fma(g[i][k], xh, dw[i][k]);
-            db[i][k] = add(g[i][k], db[i][k]);
-          } else {
-            o[k] = fma(xh, w[i][k], b[i][k]);
-          }
+      if (live) {
+        Two mu = 0, mud = 0;
+        if constexpr (kGrad) {
+          mu = both(-__fdiv_rn(s[1], p.gs_f));
+          mud = both(-__fdiv_rn(s[2], p.gs_f) * nf * nf);
         }
-        Vec::put(out + i * apart, o);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+          Two o[N];
+#pragma unroll
+          for (int k = 0; k < N; ++k) {
+            const Two xh = mul(x[i][k], n);
+            if constexpr (kGrad) {
+              o[k] = mul(fma(x[i][k], mud, fma(g[i][k], w[i][k], mu)), n);
+              dw[i][k] = fma(g[i][k], xh, dw[i][k]);
+              db[i][k] = add(g[i][k], db[i][k]);
+            } else {
+              o[k] = fma(xh, w[i][k], b[i][k]);
+            }
+          }
+          if (has(i)) Vec::put(out + i * apart, o);
+        }
       }
     } else {
       // MAMBA2 keeps silu, y s', y silu and dout; ONNX u, dout w s', y and dout silu
@@ -382,7 +417,6 @@ __global__ void __launch_bounds__(threads_of(KIND, VPL * E),
       Two q[2] = {0, 0};
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
-        if (!live || !has(i)) continue;
         Two y[N], g[N], z[N];
         load(0, i, y), load(1, i, g), load(2, i, z);
 #pragma unroll
@@ -411,25 +445,28 @@ __global__ void __launch_bounds__(threads_of(KIND, VPL * E),
       team_sum<2>(s, p.lanes, s_sum, turn++ & 1);
       const float nf = rsqrtf(__fdiv_rn(s[0], p.gs_f) + p.eps);
       const Two n = both(nf), muv = both(-__fdiv_rn(s[1], p.gs_f) * nf * nf);
+      if (live) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        if (!live || !has(i)) continue;
-        Two dy[N], dz[N];
+        for (int i = 0; i < VPL; ++i) {
+          Two dy[N], dz[N];
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-          const Two vn = mul(kv[i][k], n);
-          dw[i][k] = fma(kg[i][k], vn, dw[i][k]);
-          if constexpr (KIND == kMamba2Grad) {
-            const Two dv = mul(fma(kv[i][k], muv, mul(kg[i][k], w[i][k])), n);
-            dy[k] = mul(dv, ka[i][k]);
-            dz[k] = mul(dv, kb[i][k]);
-          } else {
-            dy[k] = mul(fma(kv[i][k], muv, ka[i][k]), n);
-            dz[k] = mul(kb[i][k], vn);
+          for (int k = 0; k < N; ++k) {
+            const Two vn = mul(kv[i][k], n);
+            dw[i][k] = fma(kg[i][k], vn, dw[i][k]);
+            if constexpr (KIND == kMamba2Grad) {
+              const Two dv = mul(fma(kv[i][k], muv, mul(kg[i][k], w[i][k])), n);
+              dy[k] = mul(dv, ka[i][k]);
+              dz[k] = mul(dv, kb[i][k]);
+            } else {
+              dy[k] = mul(fma(kv[i][k], muv, ka[i][k]), n);
+              dz[k] = mul(kb[i][k], vn);
+            }
+          }
+          if (has(i)) {
+            Vec::put(out + i * apart, dy);
+            Vec::put(dgate + i * apart, dz);
           }
         }
-        Vec::put(out + i * apart, dy);
-        Vec::put(dgate + i * apart, dz);
       }
       dgate += step * p.dgs;
     }
@@ -453,7 +490,7 @@ __global__ void __launch_bounds__(threads_of(KIND, VPL * E),
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
 #pragma unroll
-        for (int k = 0; k < N; ++k) upk2(sums[i][k], a[i][2 * k], a[i][2 * k + 1]);
+        for (int k = 0; k < N; ++k) split(sums[i][k], a[i][2 * k], a[i][2 * k + 1]);
       }
       if (teams > 1) {
         __syncthreads();
@@ -493,7 +530,7 @@ __global__ void __launch_bounds__(threads_of(KIND, VPL * E),
 // again for every pass (from L1 and L2).  Each thread owns the same columns in
 // every row; their sums lie in its CTA's row of the partial sums.
 template <int KIND, typename T>
-__global__ void __launch_bounds__(kMaxThreads) k_norm_any(const Params p) {
+__global__ void __launch_bounds__(kAnyThreads) k_norm_any(const Params p) {
   constexpr bool kGrad = KIND != kLayerNorm, kGated = KIND == kMamba2Grad || KIND == kOnnxGrad;
   __shared__ float4 s_sum[2 * 3 * (kMaxWarps / 4)];
   pdl_wait();

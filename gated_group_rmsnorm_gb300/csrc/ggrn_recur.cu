@@ -154,11 +154,11 @@ __device__ __forceinline__ void decay2(Two r, Two a, const Constants& k, Two& e,
   e = add(s, k.one);
   if constexpr (!FAST) {
     float pv[2], ev[2], sv[2];
-    upk2(p, pv[0], pv[1]), upk2(e, ev[0], ev[1]), upk2(s, sv[0], sv[1]);
+    split(p, pv[0], pv[1]), split(e, ev[0], ev[1]), split(s, sv[0], sv[1]);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
       if (!(pv[i] > kSeries)) beyond_series<T>(pv[i], ev[i], sv[i]);
-    e = pk2(ev[0], ev[1]), s = pk2(sv[0], sv[1]);
+    e = join(ev[0], ev[1]), s = join(sv[0], sv[1]);
   }
   m = each(mul(s, add(s, k.two)), [](float q) {
     return Elem<T>::kExactSilu ? sqrtf(-q) : sqrt_approx(-q);
@@ -314,9 +314,10 @@ __device__ __forceinline__ Two mail_through(const Mail& m, int buf, int rank, in
 // ---------------------------------------------------------------------------
 // Rows and their sequences.
 // ---------------------------------------------------------------------------
+template <int ROWS>
 struct TileRows {
-  uint32_t in[2], first[2], last[2];  // bits of the tile's rows
-  int seq[kTile];
+  uint32_t in[ROWS / 32], first[ROWS / 32], last[ROWS / 32];  // bits of the tile's rows
+  int seq[ROWS];
 };
 
 // The sequence of row r: the last one that begins at or before it.
@@ -338,10 +339,11 @@ __device__ __forceinline__ int64_t seq_of_row(const Seqs& q, int64_t r, int64_t&
   return s;
 }
 
-// Threads 0 .. 63 of the CTA: row `tile` x 64 + thread, if it is one of [lo, hi).
+// Threads 0 .. ROWS - 1 of the CTA: row `tile` x ROWS + thread, if it is one of [lo, hi).
+template <int ROWS>
 __device__ __forceinline__ void place_rows(const Seqs& q, int64_t tile, int64_t lo, int64_t hi,
-                                           TileRows* t) {
-  const int64_t r = tile * kTile + threadIdx.x;
+                                           TileRows<ROWS>* t) {
+  const int64_t r = tile * ROWS + threadIdx.x;
   bool in = false, first = false, last = false;
   if (r >= lo && r < hi) {
     int64_t begin, end;
@@ -365,8 +367,9 @@ struct Rows {
   int64_t begin = 0, end = 0;
   // Whether tile `t` of the segment's rows [lo, hi) is whole, lies in one sequence,
   // and holds neither end of it.
+  template <int ROWS>
   __device__ __forceinline__ bool inside(const Seqs& q, int64_t t, int64_t lo, int64_t hi) {
-    const int64_t r0 = t * kTile, r1 = r0 + kTile;
+    const int64_t r0 = t * ROWS, r1 = r0 + ROWS;
     if (r0 > begin && r1 < end) return true;
     if (r0 < lo || r1 > hi) return false;
     seq_of_row(q, r0, begin, end);
@@ -399,14 +402,14 @@ __device__ __forceinline__ Two start_state(const Params& p, int64_t s, int64_t c
   const int64_t slot = seq_slot(p.q, s);
   if (slot < 0 || !seq_resumes(p.q, s)) return 0;
   const float* h = p.state + slot * p.slot_stride + c;
-  return pk2(n > 0 ? h[0] : 0.0f, n > 1 ? h[1] : 0.0f);
+  return join(n > 0 ? h[0] : 0.0f, n > 1 ? h[1] : 0.0f);
 }
 
 // What comes to the last row of sequence s from the state behind it.
 __device__ __forceinline__ Two end_gradient(const Params& p, int64_t s, int64_t c, int n) {
   if (!p.dstate) return 0;
   const float* g = p.dstate + s * p.width + c;
-  return pk2(n > 0 ? __ldg(g) : 0.0f, n > 1 ? __ldg(g + 1) : 0.0f);
+  return join(n > 0 ? __ldg(g) : 0.0f, n > 1 ? __ldg(g + 1) : 0.0f);
 }
 
 // Empty sequences among those of this CTA (every `of`-th 32 from the `at`-th):
@@ -423,7 +426,7 @@ __device__ __forceinline__ void each_empty(const Seqs& q, int64_t at, int64_t of
 }
 
 // ---------------------------------------------------------------------------
-// Tiles in shared memory: 64 rows of 64 channels of each input.
+// Tiles in shared memory: rows of 64 channels of each input.
 // ---------------------------------------------------------------------------
 constexpr int kCols = 64;
 
@@ -441,52 +444,62 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// The CTA's threads start to copy tile `tile` of one input into `to`; rows
-// outside [lo, hi) and channels behind the last one become zeros.  `whole`: there
-// are none of either.
-template <typename T, int THREADS, int PITCH>
-__device__ __forceinline__ void copy_tile(T* to, const void* base, int64_t stride, int64_t c0,
-                                          int64_t width, int64_t tile, int64_t lo, int64_t hi,
-                                          int chunk, bool whole) {
-  constexpr int ES = sizeof(T);
-  const T* from = static_cast<const T*>(base) + c0;
-  const int64_t r0 = tile * kTile;
-  const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(to));
-  constexpr int E = 16 / ES, ROW = kCols / E, ROWS = THREADS / ROW;  // 16-byte chunks
-  if (chunk == 16 && whole) {
-    const T* p = from + (r0 + threadIdx.x / ROW) * stride + threadIdx.x % ROW * E;
-    const int64_t step = ROWS * stride;
+// The CTA's threads start to copy the ROWS rows of tile `tile` of one input into
+// `to`, PITCH elements apart; rows outside [lo, hi) and channels behind the last one
+// become zeros.  `whole`: there are none of either.
+template <typename T, int THREADS, int ROWS, int PITCH, int BYTES>
+__device__ __forceinline__ void copy_by(uint32_t to, const T* from, int64_t stride, int cols,
+                                        int64_t r0, int64_t lo, int64_t hi, bool whole) {
+  constexpr int ES = sizeof(T), E = BYTES / ES, ROW = kCols / E;  // chunks of a row
+  constexpr int STEP = THREADS / ROW;                             // rows of a round
+  static_assert(THREADS % ROW == 0 && ROWS % STEP == 0, "whole rounds");
+  // (a thread's chunks lie below each other)
+  const int row0 = static_cast<int>(threadIdx.x) / ROW, c = static_cast<int>(threadIdx.x) % ROW * E;
+  const T* p = from + (r0 + row0) * stride + c;
+  const int64_t step = STEP * stride;
+  uint32_t at = to + (row0 * PITCH + c) * ES;
+  if (whole) {
 #pragma unroll
-    for (int k = 0; k < kTile / ROWS; ++k, p += step)
-      copy_async<16>(at + (threadIdx.x / ROW + k * ROWS) * PITCH * ES + threadIdx.x % ROW * 16, p,
-                     16);
+    for (int k = 0; k < ROWS / STEP; ++k, p += step, at += STEP * PITCH * ES)
+      copy_async<BYTES>(at, p, BYTES);
     return;
   }
-  const int cols = static_cast<int>(width - c0 < kCols ? width - c0 : kCols);
-  if (chunk == 16) {
-#pragma unroll 1
-    for (int k = threadIdx.x; k < kTile * ROW; k += THREADS) {
-      const int row = k / ROW, c = k % ROW * E;
-      const bool ok = r0 + row >= lo && r0 + row < hi && c < cols;
-      copy_async<16>(at + (row * PITCH + c) * ES, ok ? from + (r0 + row) * stride + c : from, ok ? 16 : 0);
-    }
-  } else if (chunk == 4) {
-    constexpr int E4 = 4 / ES, ROW4 = kCols / E4;
+  const int left = cols - c, bytes = left <= 0 ? 0 : left < E ? left * ES : BYTES;
 #pragma unroll 2
-    for (int k = threadIdx.x; k < kTile * ROW4; k += THREADS) {
-      const int row = k / ROW4, c = k % ROW4 * E4;
-      const bool ok = r0 + row >= lo && r0 + row < hi && c < cols;
-      copy_async<4>(at + (row * PITCH + c) * ES, ok ? from + (r0 + row) * stride + c : from,
-                    !ok ? 0 : cols - c < E4 ? ES : 4);
-    }
+  for (int k = 0; k < ROWS / STEP; ++k, p += step, at += STEP * PITCH * ES) {
+    const int64_t r = r0 + row0 + k * STEP;
+    const int n = r >= lo && r < hi ? bytes : 0;
+    copy_async<BYTES>(at, n ? p : from, n);
+  }
+}
+template <typename T, int THREADS, int ROWS, int PITCH>
+__device__ __forceinline__ void copy_tile(T* to, const void* base, int64_t stride, int64_t c0,
+                                          int64_t width, int64_t tile, int64_t lo, int64_t hi,
+                                          int chunk) {
+  const T* from = static_cast<const T*>(base) + c0;
+  const int64_t r0 = tile * ROWS;
+  const int cols = static_cast<int>(width - c0 < kCols ? width - c0 : kCols);
+  const bool whole = r0 >= lo && r0 + ROWS <= hi && cols == kCols;
+  if (chunk == 16) {
+    copy_by<T, THREADS, ROWS, PITCH, 16>(smem_u32(to), from, stride, cols, r0, lo, hi, whole);
+  } else if (chunk == 4) {
+    copy_by<T, THREADS, ROWS, PITCH, 4>(smem_u32(to), from, stride, cols, r0, lo, hi, whole);
   } else {
-#pragma unroll 4
-    for (int k = threadIdx.x; k < kTile * kCols; k += THREADS) {
-      const int row = k / kCols, c = k % kCols;
-      T v;
-      Elem<T>::store1(&v, 0, 0.0f);
-      if (r0 + row >= lo && r0 + row < hi && c < cols) v = from[(r0 + row) * stride + c];
-      to[row * PITCH + c] = v;
+    // single 16-bit elements: through registers, eight in flight
+    const int c = static_cast<int>(threadIdx.x) % kCols, row0 = static_cast<int>(threadIdx.x) / kCols;
+    constexpr int STEP = THREADS / kCols, AT_ONCE = 8;
+    static_assert(ROWS % (STEP * AT_ONCE) == 0, "whole rounds");
+#pragma unroll 1
+    for (int k = row0; k < ROWS; k += STEP * AT_ONCE) {
+      T v[AT_ONCE];
+#pragma unroll
+      for (int i = 0; i < AT_ONCE; ++i) {
+        const int64_t r = r0 + k + i * STEP;
+        Elem<T>::store1(&v[i], 0, 0.0f);
+        if (r >= lo && r < hi && c < cols) v[i] = from[r * stride + c];
+      }
+#pragma unroll
+      for (int i = 0; i < AT_ONCE; ++i) to[(k + i * STEP) * PITCH + c] = v[i];
     }
   }
 }
@@ -499,20 +512,20 @@ __device__ __forceinline__ Two get2(const T* p) {
   } else {
     float x, y;
     Elem<T>::unpack2(*reinterpret_cast<const uint32_t*>(p), x, y);
-    return pk2(x, y);
+    return join(x, y);
   }
 }
 // Stores both channels, or the first `cols` of them.
 template <typename T>
 __device__ __forceinline__ void put2(T* p, Two v) {
   float f[2];
-  upk2(v, f[0], f[1]);
+  split(v, f[0], f[1]);
   Raw<T, 2>::put(p, f);
 }
 template <typename T>
 __device__ __forceinline__ void put_some(T* p, Two v, int cols) {
   float x, y;
-  upk2(v, x, y);
+  split(v, x, y);
   if (cols > 0) Elem<T>::store1(p, 0, x);
   if (cols > 1) Elem<T>::store1(p, 1, y);
 }
@@ -537,47 +550,84 @@ __device__ __forceinline__ Place find_place(const Params& p) {
   w.lo = segment_begin(p, blockIdx.z);
   w.hi = segment_begin(p, blockIdx.z + 1);
   const float a0 = w.cols > 0 ? __ldg(p.a + w.c) : 0.0f, a1 = w.cols > 1 ? __ldg(p.a + w.c + 1) : 0.0f;
-  w.a = pk2(a0, a1);
+  w.a = join(a0, a1);
   w.fast = __all_sync(0xffffffffu, a0 > kSeries && a1 > kSeries);
   return w;
 }
-__device__ __forceinline__ bool whole_tile(const Params& p, const Place& w, int64_t tile) {
-  return tile * kTile >= w.lo && (tile + 1) * kTile <= w.hi && w.c0 + kCols <= p.width;
-}
-
 // ---------------------------------------------------------------------------
-// Prompts.  Four warps of sixteen rows each.  A row of the tile in shared memory
-// holds x, the input gate and the decay gate of 64 channels; e and b take their
-// place (512 bytes a row, which f32's inputs need anyway), so that the loops over
-// rows stay rolled: unrolled, with e and b in registers, they were larger than the
-// instruction cache, which a third of all stalls waited for.
+// Prompts.  Four warps of sixteen rows each, five CTAs to an SM (f32: four).  A row of
+// the tile in shared memory holds x, the input gate and the decay gate of 64
+// channels; e and b take their place (512 bytes a row, which f32's inputs need
+// anyway), so that the loops over rows stay rolled: unrolled, with e and b in
+// registers, they were larger than the instruction cache, which a third of all
+// stalls waited for.  One CTA of twelve warps to an SM, its next tile's copies under
+// way meanwhile, took 100 us for 4096 x 7680 in bf16 where this takes 77: a CTA's
+// stages wait for each other, and other CTAs fill the gaps better.
 // ---------------------------------------------------------------------------
 namespace forward {
 
-constexpr int W = 4, R = kTile / W, kThreads = 32 * W;
+constexpr int R = 16;
 constexpr int kAtOnce = 4;  // rows of a loop's turn
-
-// Elements between rows of the tile.
+constexpr int W = 4, kThreads = 32 * W;
+static_assert(R * W == kTile, "a tile's rows");
 template <typename T>
-constexpr int pitch() {
+constexpr int pitch() {  // elements between rows of the tile
   return (sizeof(T) == 2 ? 4 : 3) * kCols;
+}
+template <typename T>
+constexpr int smem() {
+  return kTile * pitch<T>() * static_cast<int>(sizeof(T));
 }
 
 struct Shared {
   ulonglong2 pair[W][32];
   Mail mail;
-  TileRows rows;
+  TileRows<kTile> rows;
 };
 
 template <typename T>
 __device__ __forceinline__ void fetch(const Params& p, const Place& w, T* to, int64_t tile) {
-  const bool whole = whole_tile(p, w, tile);
   const auto copy = [&](int k, const void* base, int64_t stride) {
-    copy_tile<T, kThreads, pitch<T>()>(to + k * kCols, base, stride, w.c0, p.width, tile, w.lo,
-                                       w.hi, p.chunk, whole);
+    copy_tile<T, kThreads, kTile, pitch<T>()>(to + k * kCols, base, stride, w.c0, p.width, tile,
+                                              w.lo, w.hi, p.chunk);
   };
   copy(0, p.x, p.xs), copy(1, p.ig, p.is), copy(2, p.rg, p.rs);
 }
+
+// The same for whole tiles in 16-byte chunks, with a thread's addresses kept from one
+// tile to the next.
+template <typename T>
+struct Feed {
+  static constexpr int E = 16 / sizeof(T), ROW = kCols / E, STEP = kThreads / ROW;
+  const T* from[3];
+  int64_t step[3], turn[3];  // between a thread's rows; between the CTA's tiles
+  uint32_t to;
+  __device__ __forceinline__ Feed(const Params& p, const Place& w, T* tiles, int64_t tile) {
+    const int row = static_cast<int>(threadIdx.x) / ROW, c = static_cast<int>(threadIdx.x) % ROW * E;
+    const void* base[3] = {p.x, p.ig, p.rg};
+    const int64_t stride[3] = {p.xs, p.is, p.rs};
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      from[k] = static_cast<const T*>(base[k]) + w.c0 + (tile * kTile + row) * stride[k] + c;
+      step[k] = STEP * stride[k];
+      turn[k] = w.size * kTile * stride[k];
+    }
+    to = smem_u32(tiles + row * pitch<T>() + c);
+  }
+  __device__ __forceinline__ void copy() const {
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const T* f = from[k];
+#pragma unroll
+      for (int i = 0; i < kTile / STEP; ++i, f += step[k])
+        copy_async<16>(to + (k * kCols + i * STEP * pitch<T>()) * static_cast<int>(sizeof(T)), f, 16);
+    }
+  }
+  __device__ __forceinline__ void advance() {
+#pragma unroll
+    for (int k = 0; k < 3; ++k) from[k] += turn[k];
+  }
+};
 
 // One tile.  INSIDE: all of its rows are those of one sequence, neither its first
 // nor its last.  FAST: see decay2.  Takes the state before the cluster's tiles and
@@ -589,7 +639,11 @@ __device__ __forceinline__ Two turn_of(const Params& p, const Place& w, Shared& 
   const int buf = turn & 1;
   const uint32_t parity = turn >> 1 & 1;
   T* const mine = tiles + warp * R * pitch<T>();
-  const TileRows& t = sh.rows;
+  const auto& t = sh.rows;
+  const auto bits = [&](const uint32_t* of) {
+    return INSIDE ? 0u : of[warp >> 1] >> (warp & 1) * 16 & 0xffffu;
+  };
+  const uint32_t in = bits(t.in), first = bits(t.first), last = bits(t.last);
   const auto pair_of = [&](int j) {
     return reinterpret_cast<ulonglong2*>(mine + j * pitch<T>()) + lane;
   };
@@ -611,43 +665,47 @@ __device__ __forceinline__ Two turn_of(const Params& p, const Place& w, Shared& 
       decay2<T, FAST>(sigmoid2<T>(gr[k], con), w.a, con, s.e, m);
       s.b = mul(mul(m, sigmoid2<T>(gi[k], con)), x[k]);
       if constexpr (!INSIDE) {
-        const int row = warp * R + j0 + k;
-        if (!(t.in[row >> 5] >> (row & 31) & 1)) s = {kOnes, 0};
-        if (t.first[row >> 5] >> (row & 31) & 1)
-          s = {kCut, fma(s.e, start_state(p, t.seq[row], w.c, w.cols), s.b)};
+        if (!(in >> (j0 + k) & 1)) s = {kOnes, 0};
+        if (first >> (j0 + k) & 1)
+          s = {kCut, fma(s.e, start_state(p, t.seq[warp * R + j0 + k], w.c, w.cols), s.b)};
       }
       all = compose<!INSIDE>(all, s);
       put_pair(pair_of(j0 + k), s);
     }
   }
   put_pair(&sh.pair[warp][lane], all);
-  const bool cut = !INSIDE && (t.first[0] | t.first[1]) != 0;
   __syncthreads();
 
-  // the pair of the rows before this warp's in the tile, and of the whole tile
-  Pair before = {kOnes, 0}, whole = get_pair(&sh.pair[0][lane]);
-#pragma unroll
-  for (int k = 1; k < W; ++k) {
-    if (k == warp) before = whole;
-    whole = compose<!INSIDE>(whole, get_pair(&sh.pair[k][lane]));
-  }
+  // the state before this warp's rows
   Two h = state;
-  if (w.size > 1) {
+  if (w.size == 1) {
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      if (k == warp) h = state;
+      state = through<!INSIDE>(get_pair(&sh.pair[k][lane]), state);
+    }
+  } else {
+    Pair whole = get_pair(&sh.pair[0][lane]);
+#pragma unroll
+    for (int k = 1; k < W; ++k) whole = compose<!INSIDE>(whole, get_pair(&sh.pair[k][lane]));
     if (threadIdx.x == 0) mail_expect(sh.mail, buf, w.size);
+    const bool cut = !INSIDE && (t.first[0] | t.first[1]) != 0;
     if (!p.mute)
       for (int k = warp; k < w.size; k += W) mail_send(sh.mail, buf, w.rank, k, whole, cut);
     mail_wait(sh.mail, buf, parity);
     h = mail_through(sh.mail, buf, w.rank, w.size, state);
-  } else {
-    state = through<!INSIDE>(whole, state);
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k)
+      if (k < warp) h = through<!INSIDE>(get_pair(&sh.pair[k][lane]), h);
   }
-  if (p.saved && warp == 0 && tile * kTile >= w.lo && tile * kTile < w.hi)
+  const int64_t row0 = tile * kTile + warp * R;
+  if (p.saved && warp == 0 && row0 >= w.lo && row0 < w.hi)
     put_some(p.saved + tile * p.width + w.c, h, w.cols);
-  h = through<!INSIDE>(before, h);
-  T* at = static_cast<T*>(p.out) + (tile * kTile + warp * R) * p.os + w.c;
+  T* at = static_cast<T*>(p.out) + row0 * p.os + w.c;
+  const bool pairs = p.pairs && w.c0 + kCols <= p.width;
   if (INSIDE && !p.out) {
     // (only the states to be kept are wanted)
-  } else if (INSIDE && p.pairs && w.c0 + kCols <= p.width) {
+  } else if (INSIDE && pairs) {
     // (the loop that nearly all tiles of a call take)
 #pragma unroll 1
     for (int j0 = 0; j0 < R; j0 += kAtOnce) {
@@ -658,13 +716,15 @@ __device__ __forceinline__ Two turn_of(const Params& p, const Place& w, Shared& 
       }
     }
   } else {
-#pragma unroll 1
+#pragma unroll 2
     for (int j = 0; j < R; ++j, at += p.os) {
       h = through<!INSIDE>(get_pair(pair_of(j)), h);
-      const int row = warp * R + j;
-      if (p.out && (INSIDE || (t.in[row >> 5] >> (row & 31) & 1))) put_some(at, h, w.cols);
-      if (!INSIDE && p.keep_state && (t.last[row >> 5] >> (row & 31) & 1)) {
-        const int64_t slot = seq_slot(p.q, t.seq[row]);
+      if (p.out && (INSIDE || (in >> j & 1))) {
+        if (pairs) put2(at, h);
+        else put_some(at, h, w.cols);
+      }
+      if (!INSIDE && p.keep_state && (last >> j & 1)) {
+        const int64_t slot = seq_slot(p.q, t.seq[warp * R + j]);
         if (slot >= 0) put_some(p.state + slot * p.slot_stride + w.c, h, w.cols);
       }
     }
@@ -685,7 +745,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4)
     k_recur(const __grid_constant__ Params p) {
   extern __shared__ uint4 s_tile[];
   __shared__ Shared sh;
-  T* const tiles = reinterpret_cast<T*>(s_tile);  // x, input gate, decay gate
+  T* const tiles = reinterpret_cast<T*>(s_tile);
   pdl_wait();
   pdl_launch_dependents();
   mail_init(sh.mail);
@@ -694,19 +754,24 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4)
   const int64_t tile0 = w.lo / kTile, count = w.hi > w.lo ? (w.hi + kTile - 1) / kTile - tile0 : 0;
   const int64_t turns = (count + w.size - 1) / w.size;
   int64_t tile = tile0 + w.rank;
+  Feed<T> feed(p, w, tiles, tile);
+  const bool wide = p.chunk == 16 && w.c0 + kCols <= p.width;
   all_wait();
 
   const Constants con;
   Two state = 0;  // before the cluster's tiles
   Rows known;
   for (int64_t turn = 0; turn < turns; ++turn, tile += w.size) {
-    fetch(p, w, tiles, tile);
-    const bool inside = known.inside(p.q, tile, w.lo, w.hi);
-    if (!inside && threadIdx.x < kTile) place_rows(p.q, tile, w.lo, w.hi, &sh.rows);
+    if (wide && tile * kTile >= w.lo && (tile + 1) * kTile <= w.hi) feed.copy();
+    else fetch(p, w, tiles, tile);
+    feed.advance();
+    const bool inside = known.inside<kTile>(p.q, tile, w.lo, w.hi);
+    if (!inside && threadIdx.x < kTile) place_rows<kTile>(p.q, tile, w.lo, w.hi, &sh.rows);
     copies_wait();
     __syncthreads();
     if (inside && w.fast) state = turn_of<T, true, true>(p, w, sh, tiles, tile, turn, state, con);
     else if (inside) state = turn_apart<T, true, false>(p, w, sh, tiles, tile, turn, state);
+    else if (w.fast) state = turn_apart<T, false, true>(p, w, sh, tiles, tile, turn, state);
     else state = turn_apart<T, false, false>(p, w, sh, tiles, tile, turn, state);
   }
   if (p.keep_state && threadIdx.x < 32) {
@@ -740,7 +805,7 @@ struct Shared {
   ulonglong2 down[W][32];  // pairs of states
   ulonglong2 up[W][32];    // pairs of gradients
   Mail mail;
-  TileRows rows;
+  TileRows<kTile> rows;
 };
 
 // Tiles of the inputs in shared memory: two of 16-bit types, one of f32.
@@ -751,10 +816,9 @@ constexpr int stages() {
 
 template <typename T>
 __device__ __forceinline__ void fetch(const Params& p, const Place& w, T* to, int64_t tile) {
-  const bool whole = whole_tile(p, w, tile);
   const auto copy = [&](int k, const void* base, int64_t stride) {
-    copy_tile<T, kThreads, kCols>(to + k * kInput, base, stride, w.c0, p.width, tile, w.lo, w.hi, p.chunk,
-                           whole);
+    copy_tile<T, kThreads, kTile, kCols>(to + k * kInput, base, stride, w.c0, p.width, tile, w.lo,
+                                         w.hi, p.chunk);
   };
   copy(0, p.x, p.xs), copy(1, p.ig, p.is), copy(2, p.rg, p.rs), copy(3, p.dout, p.gs);
 }
@@ -773,11 +837,11 @@ __device__ __forceinline__ Carry turn_of(const Params& p, const Place& w, Shared
   const uint32_t parity = turn >> 1 & 1;
   T* const tiles = ring + (stages<T>() == 2 ? buf : 0) * 4 * kInput;
   const T* mine = tiles + warp * R * kCols + lane * 2;
-  const TileRows& t = sh.rows;
+  const TileRows<kTile>& t = sh.rows;
   Two h = 0;  // the state before the tile, as it was kept
   if (tile * kTile >= w.lo) {
     const float* kept = p.saved + tile * p.width + w.c;
-    h = pk2(w.cols > 0 ? __ldg(kept) : 0.0f, w.cols > 1 ? __ldg(kept + 1) : 0.0f);
+    h = join(w.cols > 0 ? __ldg(kept) : 0.0f, w.cols > 1 ? __ldg(kept + 1) : 0.0f);
   }
   if (stages<T>() == 2 && next != INT64_MIN) fetch(p, w, ring + (buf ^ 1) * 4 * kInput, next);
   const uint32_t in = INSIDE ? ~0u : t.in[warp * R >> 5] >> (warp * R & 31),
@@ -919,8 +983,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   Rows known;
   for (int64_t turn = 0; turn < turns; ++turn, tile -= w.size) {
     const int64_t next = turn + 1 < turns ? tile - w.size : INT64_MIN;
-    const bool inside = known.inside(p.q, tile, w.lo, w.hi);
-    if (!inside && threadIdx.x < kTile) place_rows(p.q, tile, w.lo, w.hi, &sh.rows);
+    const bool inside = known.inside<kTile>(p.q, tile, w.lo, w.hi);
+    if (!inside && threadIdx.x < kTile) place_rows<kTile>(p.q, tile, w.lo, w.hi, &sh.rows);
     copies_wait();
     __syncthreads();
     if (inside && w.fast)
@@ -999,9 +1063,9 @@ __global__ void __launch_bounds__(128) k_recur_step(const Params p) {
   }
   xr.get(x), ir.get(gi), rr.get(gr);
   Two e, m;
-  decay2<T, false>(sigmoid2<T>(pk2(gr[0], gr[1]), con), pk2(a[0], a[1]), con, e, m);
-  const Two b = mul(mul(m, sigmoid2<T>(pk2(gi[0], gi[1]), con)), pk2(x[0], x[1]));
-  upk2(fma(e, pk2(h[0], h[1]), b), h[0], h[1]);
+  decay2<T, false>(sigmoid2<T>(join(gr[0], gr[1]), con), join(a[0], a[1]), con, e, m);
+  const Two b = mul(mul(m, sigmoid2<T>(join(gi[0], gi[1]), con)), join(x[0], x[1]));
+  split(fma(e, join(h[0], h[1]), b), h[0], h[1]);
 #pragma unroll
   for (int v = 0; v < V; ++v) state[v] = h[v];
   Raw<T, V>::put(static_cast<T*>(p.out) + row * p.os + c, h);
@@ -1101,7 +1165,7 @@ int64_t blocks_of(int64_t width) { return (width + kCols - 1) / kCols; }
 template <typename T>
 int launch_forward(Params& p, cudaStream_t s) {
   const int64_t blocks = blocks_of(p.width);
-  constexpr int kSmem = kTile * forward::pitch<T>() * sizeof(T);
+  constexpr int kSmem = forward::smem<T>();
   const cudaError_t e = allow_shared_memory<forward::k_recur<T>>(kSmem);
   if (e != cudaSuccess) {
     record_cuda_error(e);
