@@ -44,7 +44,7 @@ EXPORTS = ("ggrn_forward", "ggrn_forward_path", "ggrn_plan", "ggrn_graph_create"
            "ggrn_graph_create_steps", "ggrn_recur", "ggrn_recur_step", "ggrn_recur_backward",
            "ggrn_recur_backward_workspace_bytes", "ggrn_layer_norm", "ggrn_layer_norm_backward",
            "ggrn_layer_norm_backward_workspace_bytes", "ggrn_backward",
-           "ggrn_backward_workspace_bytes")
+           "ggrn_backward_workspace_bytes", "ggrn_selftest_recur_timeout")
 # ggrn_activation / ggrn_step_kind
 ACT_CODE = {None: 0, "silu": 1}
 STEP_FORWARD, STEP_CONV, STEP_SCAN, STEP_RECUR, STEP_LAYER_NORM = range(5)
@@ -232,6 +232,7 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
                            ("ggrn_scan", ScanCall), ("ggrn_scan_step", ScanCall),
                            ("ggrn_selftest_scan_timeout", ScanCall), ("ggrn_recur", RecurCall),
                            ("ggrn_recur_step", RecurCall),
+                           ("ggrn_selftest_recur_timeout", RecurCall),
                            ("ggrn_recur_backward", RecurBackwardCall),
                            ("ggrn_layer_norm", LayerNormCall),
                            ("ggrn_layer_norm_backward", LayerNormBackwardCall),

@@ -280,9 +280,10 @@ __device__ __forceinline__ void mail_send(Mail& m, int buf, int rank, int to, co
                  "r"(cut ? 1u : 0u), "r"(bar)
                  : "memory");
 }
-// One thread, before the wait: how much will land.
+// One thread, before the wait: how much will land.  (Not behind a wait that ran out,
+// whose phase is not over.)
 __device__ __forceinline__ void mail_expect(Mail& m, int buf, int size) {
-  mbar_expect_tx(smem_u32(&m.landed[buf]), static_cast<uint32_t>(size) * (32 * 16 + 4));
+  if (!m.failed) mbar_expect_tx(smem_u32(&m.landed[buf]), static_cast<uint32_t>(size) * (32 * 16 + 4));
 }
 __device__ __forceinline__ void mail_wait(Mail& m, int buf, uint32_t parity) {
   const uint32_t bar = smem_u32(&m.landed[buf]);
@@ -1280,13 +1281,17 @@ int check(const ggrn_recur_call& c, bool step, Params* p) {
   if (!mixer::aligned_to(c.a, 4) || !mixer::aligned_to(c.state, 4) ||
       !mixer::aligned_to(saved_p, 4))
     return GGRN_ERR_ALIGN;
-  const mixer::Buffer a = {c.a, c.width * 4}, cu = {p->q.cu, (p->q.seqs + 1) * 4},
-                      slots = {p->q.slots, p->q.seqs * 4}, res = {p->q.resume, p->q.seqs},
-                      saved = {saved_p, (c.rows + kTile - 1) / kTile * c.width * 4};
-  for (const mixer::Buffer& o : {out, state, saved})
-    for (const mixer::Buffer& i : {x, ig, rg, a, cu, slots, res})
-      if (mixer::overlap(o, i)) return GGRN_ERR_OVERLAP;
-  if (mixer::overlap(out, state) || mixer::overlap(out, saved) || mixer::overlap(state, saved))
+  const auto matrix = [&](const mixer::Buffer& b, int64_t stride) {
+    return mixer::columns(b, c.rows, c.width, stride, es);
+  };
+  const auto vector = [](const void* q, int64_t n) { return mixer::Columns{{q, n}, 0, 0}; };
+  const int64_t kept = (c.rows + kTile - 1) / kTile * c.width * 4;
+  if (mixer::outputs_overlap(
+          {matrix(out, c.out_row_stride), mixer::Columns{state, 0, 0}, vector(saved_p, kept)},
+          {matrix(x, c.x_row_stride), matrix(ig, c.input_gate_row_stride),
+           matrix(rg, c.decay_gate_row_stride), vector(c.a, c.width * 4),
+           vector(p->q.cu, (p->q.seqs + 1) * 4), vector(p->q.slots, p->q.seqs * 4),
+           vector(p->q.resume, p->q.seqs)}))
     return GGRN_ERR_OVERLAP;
   p->x = c.x;
   p->ig = c.input_gate;
@@ -1306,11 +1311,18 @@ int check(const ggrn_recur_call& c, bool step, Params* p) {
   return GGRN_OK;
 }
 
-int run(const ggrn_recur_call* call, bool step, void* stream) {
+int run(const ggrn_recur_call* call, bool step, void* stream, bool mute = false) {
   if (!call) return GGRN_ERR_ARG;
   const ggrn_recur_call& c = *call;
   Params p = {};
   const int st = check(c, step, &p);
+  if (mute) {
+    if (st != GGRN_OK) return st;
+    if (c.state || c.rows == 0) return GGRN_ERR_UNSUPPORTED;
+    p.mute = 1;
+    p.out = nullptr;
+    p.saved = nullptr;
+  }
   if (st != GGRN_OK || (c.rows == 0 && (step || !c.state || p.q.seqs == 0))) return st;
   const int es = mixer::elem_bytes(c.dtype);
   const bool two = c.width % 2 == 0 && pairs(c.rows, es, {{c.x, p.xs}, {c.input_gate, p.is},
@@ -1462,6 +1474,9 @@ extern "C" int ggrn_recur(const ggrn_recur_call* call, void* cuda_stream) {
 }
 extern "C" int ggrn_recur_step(const ggrn_recur_call* call, void* cuda_stream) {
   return ggrn::recur::run(call, true, cuda_stream);
+}
+extern "C" int ggrn_selftest_recur_timeout(const ggrn_recur_call* call, void* cuda_stream) {
+  return ggrn::recur::run(call, false, cuda_stream, /*mute=*/true);
 }
 extern "C" int ggrn_recur_backward(const ggrn_recur_backward_call* call, void* cuda_stream) {
   return ggrn::recur::run_backward(call, cuda_stream);

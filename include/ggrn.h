@@ -337,7 +337,8 @@ int ggrn_version(void);
  * its copies to land, 8 = a unit claim of the dynamic schedule gave up;
  * 32 = a WIDE_CLUSTER CTA waited for its cluster's partial sums (16: see
  * ggrn_norm_outproj); 64 = a stage of the scan's tensor-core kernel waited for
- * another one (ggrn_scan).
+ * another one (ggrn_scan); 128 = a CTA of the recurrence waited for its cluster
+ * (ggrn_recur, ggrn_recur_backward).
  * Nonzero means the outputs of some call are incomplete.  Synchronises the device, writes the word to *flags and, when
  * `clear` is nonzero, resets it.  Returns GGRN_OK, GGRN_ERR_ARG (flags NULL)
  * or GGRN_ERR_CUDA.
@@ -630,6 +631,16 @@ typedef struct {
 int ggrn_recur(const ggrn_recur_call* call, void* cuda_stream);
 int ggrn_recur_step(const ggrn_recur_call* call, void* cuda_stream);
 int ggrn_recur_backward(const ggrn_recur_backward_call* call, void* cuda_stream);
+
+/*
+ * ggrn_selftest_recur_timeout -- exercise the failure path of the recurrence's
+ * kernels, whose CTAs wait for each other within a cluster: launches ggrn_recur
+ * with nothing sent, so that the bounded waits run out (about a second).  The
+ * kernel ends by itself, sets bit 128 of the status word and writes nothing.  For
+ * tests.  GGRN_ERR_UNSUPPORTED for calls that take no cluster or have a state;
+ * statuses of ggrn_recur otherwise.
+ */
+int ggrn_selftest_recur_timeout(const ggrn_recur_call* call, void* cuda_stream);
 
 /* Workspace bytes of ggrn_recur_backward for this call (only its sizes and
  * whether cu_seqlens and saved are NULL are looked at): 0 where none is needed
