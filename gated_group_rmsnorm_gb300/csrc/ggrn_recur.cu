@@ -505,6 +505,40 @@ __device__ __forceinline__ void copy_tile(T* to, const void* base, int64_t strid
   }
 }
 
+// copy_tile of N inputs for whole tiles in 16-byte chunks, with a thread's addresses
+// kept from one tile to the next.
+template <typename T, int THREADS, int PITCH, int N>
+struct Feed {
+  static constexpr int ES = sizeof(T), E = 16 / ES, ROW = kCols / E, STEP = THREADS / ROW;
+  const T* from[N];
+  int64_t step[N], turn[N];  // between a thread's rows; between the CTA's tiles
+  uint32_t to;
+  __device__ __forceinline__ Feed(const void* const (&base)[N], const int64_t (&stride)[N],
+                                  int64_t c0, T* tiles, int64_t tile, int tiles_apart) {
+    const int row = static_cast<int>(threadIdx.x) / ROW, c = static_cast<int>(threadIdx.x) % ROW * E;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      from[k] = static_cast<const T*>(base[k]) + c0 + (tile * kTile + row) * stride[k] + c;
+      step[k] = STEP * stride[k];
+      turn[k] = tiles_apart * kTile * stride[k];
+    }
+    to = smem_u32(tiles + row * PITCH + c);
+  }
+  __device__ __forceinline__ void copy() const {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const T* f = from[k];
+#pragma unroll
+      for (int i = 0; i < kTile / STEP; ++i, f += step[k])
+        copy_async<16>(to + (k * kCols + i * STEP * PITCH) * ES, f, 16);
+    }
+  }
+  __device__ __forceinline__ void advance() {
+#pragma unroll
+    for (int k = 0; k < N; ++k) from[k] += turn[k];
+  }
+};
+
 // A lane's two channels of a row in shared memory.
 template <typename T>
 __device__ __forceinline__ Two get2(const T* p) {
@@ -516,6 +550,21 @@ __device__ __forceinline__ Two get2(const T* p) {
     return join(x, y);
   }
 }
+// An address that goes down (or up) rows.  The step is kept in bytes: the compiler
+// would scale the elements' number again at every row.
+template <typename T>
+struct Down {
+  char* at;
+  int64_t step;
+  __device__ __forceinline__ Down(void* base, int64_t row, int64_t stride, int64_t c, int way) {
+    step = stride * static_cast<int64_t>(sizeof(T));
+    at = static_cast<char*>(base) + row * step + c * static_cast<int64_t>(sizeof(T));
+    step *= way;
+    asm volatile("" : "+l"(step));
+  }
+  __device__ __forceinline__ T* operator*() const { return reinterpret_cast<T*>(at); }
+  __device__ __forceinline__ void next() { at += step; }
+};
 // Stores both channels, or the first `cols` of them.
 template <typename T>
 __device__ __forceinline__ void put2(T* p, Two v) {
@@ -595,41 +644,6 @@ __device__ __forceinline__ void fetch(const Params& p, const Place& w, T* to, in
   copy(0, p.x, p.xs), copy(1, p.ig, p.is), copy(2, p.rg, p.rs);
 }
 
-// The same for whole tiles in 16-byte chunks, with a thread's addresses kept from one
-// tile to the next.
-template <typename T>
-struct Feed {
-  static constexpr int E = 16 / sizeof(T), ROW = kCols / E, STEP = kThreads / ROW;
-  const T* from[3];
-  int64_t step[3], turn[3];  // between a thread's rows; between the CTA's tiles
-  uint32_t to;
-  __device__ __forceinline__ Feed(const Params& p, const Place& w, T* tiles, int64_t tile) {
-    const int row = static_cast<int>(threadIdx.x) / ROW, c = static_cast<int>(threadIdx.x) % ROW * E;
-    const void* base[3] = {p.x, p.ig, p.rg};
-    const int64_t stride[3] = {p.xs, p.is, p.rs};
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      from[k] = static_cast<const T*>(base[k]) + w.c0 + (tile * kTile + row) * stride[k] + c;
-      step[k] = STEP * stride[k];
-      turn[k] = w.size * kTile * stride[k];
-    }
-    to = smem_u32(tiles + row * pitch<T>() + c);
-  }
-  __device__ __forceinline__ void copy() const {
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      const T* f = from[k];
-#pragma unroll
-      for (int i = 0; i < kTile / STEP; ++i, f += step[k])
-        copy_async<16>(to + (k * kCols + i * STEP * pitch<T>()) * static_cast<int>(sizeof(T)), f, 16);
-    }
-  }
-  __device__ __forceinline__ void advance() {
-#pragma unroll
-    for (int k = 0; k < 3; ++k) from[k] += turn[k];
-  }
-};
-
 // One tile.  INSIDE: all of its rows are those of one sequence, neither its first
 // nor its last.  FAST: see decay2.  Takes the state before the cluster's tiles and
 // gives the one behind them.
@@ -702,7 +716,7 @@ __device__ __forceinline__ Two turn_of(const Params& p, const Place& w, Shared& 
   const int64_t row0 = tile * kTile + warp * R;
   if (p.saved && warp == 0 && row0 >= w.lo && row0 < w.hi)
     put_some(p.saved + tile * p.width + w.c, h, w.cols);
-  T* at = static_cast<T*>(p.out) + row0 * p.os + w.c;
+  Down<T> at(p.out, row0, p.os, w.c, 1);
   const bool pairs = p.pairs && w.c0 + kCols <= p.width;
   if (INSIDE && !p.out) {
     // (only the states to be kept are wanted)
@@ -711,18 +725,18 @@ __device__ __forceinline__ Two turn_of(const Params& p, const Place& w, Shared& 
 #pragma unroll 1
     for (int j0 = 0; j0 < R; j0 += kAtOnce) {
 #pragma unroll
-      for (int k = 0; k < kAtOnce; ++k, at += p.os) {
+      for (int k = 0; k < kAtOnce; ++k, at.next()) {
         h = through<false>(get_pair(pair_of(j0 + k)), h);
-        put2(at, h);
+        put2(*at, h);
       }
     }
   } else {
 #pragma unroll 2
-    for (int j = 0; j < R; ++j, at += p.os) {
+    for (int j = 0; j < R; ++j, at.next()) {
       h = through<!INSIDE>(get_pair(pair_of(j)), h);
       if (p.out && (INSIDE || (in >> j & 1))) {
-        if (pairs) put2(at, h);
-        else put_some(at, h, w.cols);
+        if (pairs) put2(*at, h);
+        else put_some(*at, h, w.cols);
       }
       if (!INSIDE && p.keep_state && (last >> j & 1)) {
         const int64_t slot = seq_slot(p.q, t.seq[warp * R + j]);
@@ -755,7 +769,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4)
   const int64_t tile0 = w.lo / kTile, count = w.hi > w.lo ? (w.hi + kTile - 1) / kTile - tile0 : 0;
   const int64_t turns = (count + w.size - 1) / w.size;
   int64_t tile = tile0 + w.rank;
-  Feed<T> feed(p, w, tiles, tile);
+  Feed<T, kThreads, pitch<T>(), 3> feed({p.x, p.ig, p.rg}, {p.xs, p.is, p.rs}, w.c0, tiles, tile,
+                                        w.size);
   const bool wide = p.chunk == 16 && w.c0 + kCols <= p.width;
   all_wait();
 
@@ -793,14 +808,31 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4)
 }  // namespace forward
 
 // ---------------------------------------------------------------------------
-// Gradients.  Eight warps of eight rows each; the cluster's tiles go from the
-// last rows to the first, rank 0 has the last of them.
+// Gradients.  Eight warps of eight rows each; the cluster's tiles go from the last
+// rows to the first, rank 0 has the last of them.  What a row needs again on the way
+// back (e, m, both gates, the state before it) lies in shared memory behind its
+// inputs, so that the loops over rows stay rolled, as in the forward pass.
 // ---------------------------------------------------------------------------
 namespace backward {
 
 constexpr int W = 8, R = kTile / W, kThreads = 32 * W;
+constexpr int kAtOnce = 4;  // rows of a loop's turn
 static_assert(W >= kMaxCluster, "a warp to each CTA that the tile's pair goes to");
-constexpr int kInput = kTile * kCols;  // elements of an input's tile
+
+// A row of the tile, in bytes: x, dout, the input gate, the decay gate; (e, m) of each
+// lane; (i, r) of each lane; b, later the state before the row.  i and r of f32, b of
+// 16-bit types take the place of the gates' logits.
+template <typename T>
+struct Row {
+  static constexpr int ES = sizeof(T), kRaw = 4 * kCols * ES;
+  static constexpr int kDecay = kRaw, kGates = ES == 4 ? 2 * kCols * ES : kRaw + 512,
+                       kState = ES == 4 ? kRaw + 512 : 2 * kCols * ES;
+  static constexpr int kPitch = ES == 4 ? kRaw + 768 : kRaw + 1024;
+};
+template <typename T>
+constexpr int smem() {
+  return kTile * Row<T>::kPitch;
+}
 
 struct Shared {
   ulonglong2 down[W][32];  // pairs of states
@@ -809,19 +841,13 @@ struct Shared {
   TileRows<kTile> rows;
 };
 
-// Tiles of the inputs in shared memory: two of 16-bit types, one of f32.
-template <typename T>
-constexpr int stages() {
-  return sizeof(T) == 2 ? 2 : 1;
-}
-
 template <typename T>
 __device__ __forceinline__ void fetch(const Params& p, const Place& w, T* to, int64_t tile) {
   const auto copy = [&](int k, const void* base, int64_t stride) {
-    copy_tile<T, kThreads, kTile, kCols>(to + k * kInput, base, stride, w.c0, p.width, tile, w.lo,
-                                         w.hi, p.chunk);
+    copy_tile<T, kThreads, kTile, Row<T>::kPitch / static_cast<int>(sizeof(T))>(
+        to + k * kCols, base, stride, w.c0, p.width, tile, w.lo, w.hi, p.chunk);
   };
-  copy(0, p.x, p.xs), copy(1, p.ig, p.is), copy(2, p.rg, p.rs), copy(3, p.dout, p.gs);
+  copy(0, p.x, p.xs), copy(1, p.dout, p.gs), copy(2, p.ig, p.is), copy(3, p.rg, p.rs);
 }
 
 struct Carry {
@@ -830,52 +856,73 @@ struct Carry {
 };
 
 template <typename T, bool INSIDE, bool FAST>
-__device__ __forceinline__ Carry turn_of(const Params& p, const Place& w, Shared& sh, T* ring,
-                                         int64_t tile, int64_t next, int64_t turn, Carry carry,
+__device__ __forceinline__ Carry turn_of(const Params& p, const Place& w, Shared& sh, T* tiles,
+                                         int64_t tile, int64_t turn, Carry carry,
                                          const Constants& con) {
+  using L = Row<T>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int buf = turn & 1;
   const uint32_t parity = turn >> 1 & 1;
-  T* const tiles = ring + (stages<T>() == 2 ? buf : 0) * 4 * kInput;
-  const T* mine = tiles + warp * R * kCols + lane * 2;
+  char* const mine = reinterpret_cast<char*>(tiles) + warp * R * L::kPitch;
   const TileRows<kTile>& t = sh.rows;
+  const auto raw = [&](int j, int k) {
+    return get2(reinterpret_cast<const T*>(mine + j * L::kPitch) + k * kCols + lane * 2);
+  };
+  const auto decay_at = [&](int j) {
+    return reinterpret_cast<ulonglong2*>(mine + j * L::kPitch + L::kDecay) + lane;
+  };
+  const auto gates_at = [&](int j) {
+    return reinterpret_cast<ulonglong2*>(mine + j * L::kPitch + L::kGates) + lane;
+  };
+  const auto state_at = [&](int j) {
+    return reinterpret_cast<Two*>(mine + j * L::kPitch + L::kState) + lane;
+  };
   Two h = 0;  // the state before the tile, as it was kept
   if (tile * kTile >= w.lo) {
     const float* kept = p.saved + tile * p.width + w.c;
     h = join(w.cols > 0 ? __ldg(kept) : 0.0f, w.cols > 1 ? __ldg(kept + 1) : 0.0f);
   }
-  if (stages<T>() == 2 && next != INT64_MIN) fetch(p, w, ring + (buf ^ 1) * 4 * kInput, next);
-  const uint32_t in = INSIDE ? ~0u : t.in[warp * R >> 5] >> (warp * R & 31),
-                 first = INSIDE ? 0u : t.first[warp * R >> 5] >> (warp * R & 31),
-                 last = INSIDE ? 0u : t.last[warp * R >> 5] >> (warp * R & 31);
+  const auto bits = [&](const uint32_t* of) {
+    return INSIDE ? 0u : of[warp >> 2] >> (warp & 3) * R & 0xffu;
+  };
+  const uint32_t in = bits(t.in), first = bits(t.first), last = bits(t.last);
 
-  Two e[R], m[R], si[R], sr[R], b[R];
-  Pair down = {kOnes, 0}, up = {kOnes, 0};
+  Pair down = {kOnes, 0};
+  Two through_e = kOnes, up = 0;  // the rows' gradients as they come out before the first one
+  bool ended = false;             // (behind a last row nothing comes through)
+#pragma unroll 1
+  for (int j0 = 0; j0 < R; j0 += kAtOnce) {
+    Two x[kAtOnce], g[kAtOnce], zi[kAtOnce], zr[kAtOnce];
 #pragma unroll
-  for (int j = 0; j < R; ++j) {
-    si[j] = sigmoid2<T>(get2(mine + kInput + j * kCols), con);
-    sr[j] = sigmoid2<T>(get2(mine + 2 * kInput + j * kCols), con);
-    decay2<T, FAST>(sr[j], w.a, con, e[j], m[j]);
-    b[j] = mul(mul(m[j], si[j]), get2(mine + j * kCols));
-    if (!INSIDE && !(in >> j & 1)) e[j] = kOnes, b[j] = 0;
-    if (!INSIDE && (first >> j & 1))
-      down = {kCut, fma(e[j], start_state(p, t.seq[warp * R + j], w.c, w.cols), b[j])};
-    else
-      down = compose<!INSIDE>(down, {e[j], b[j]});
-  }
+    for (int k = 0; k < kAtOnce; ++k)
+      x[k] = raw(j0 + k, 0), g[k] = raw(j0 + k, 1), zi[k] = raw(j0 + k, 2), zr[k] = raw(j0 + k, 3);
+    __syncwarp();
 #pragma unroll
-  for (int j = R - 1; j >= 0; --j) {
-    if (!INSIDE && !(in >> j & 1)) continue;
-    Two g = get2(mine + 3 * kInput + j * kCols);
-    const bool end = !INSIDE && (last >> j & 1);
-    if (end) g = add(g, end_gradient(p, t.seq[warp * R + j], w.c, w.cols));
-    g = mul(g, e[j]);
-    if (end) up = {kCut, g};
-    else up = compose<!INSIDE>(up, {e[j], g});
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int j = j0 + k;
+      const Two si = sigmoid2<T>(zi[k], con), sr = sigmoid2<T>(zr[k], con);
+      Two e, m;
+      decay2<T, FAST>(sr, w.a, con, e, m);
+      Two b = mul(mul(m, si), x[k]);
+      if (!INSIDE && !(in >> j & 1)) e = kOnes, b = 0, g[k] = 0;
+      if (!INSIDE && (last >> j & 1))
+        g[k] = add(g[k], end_gradient(p, t.seq[warp * R + j], w.c, w.cols));
+      *decay_at(j) = make_ulonglong2(e, m);
+      *gates_at(j) = make_ulonglong2(si, sr);
+      *state_at(j) = b;
+      if (!INSIDE && (first >> j & 1))
+        down = {kCut, fma(e, start_state(p, t.seq[warp * R + j], w.c, w.cols), b)};
+      else
+        down = compose<!INSIDE>(down, {e, b});
+      if (INSIDE || !ended) {
+        through_e = mul(through_e, e);
+        up = fma(through_e, g[k], up);
+      }
+      if (!INSIDE && (last >> j & 1)) ended = true;
+    }
   }
   put_pair(&sh.down[warp][lane], down);
-  put_pair(&sh.up[warp][lane], up);
-  const bool cut = !INSIDE && (t.last[0] | t.last[1]) != 0;
+  put_pair(&sh.up[warp][lane], {ended ? kCut : through_e, up});
   __syncthreads();
   // the pair of the rows behind this warp's in the tile, and of the whole tile
   Pair behind = {kOnes, 0}, whole = get_pair(&sh.up[W - 1][lane]);
@@ -886,18 +933,19 @@ __device__ __forceinline__ Carry turn_of(const Params& p, const Place& w, Shared
   }
   if (w.size > 1) {
     if (threadIdx.x == 0) mail_expect(sh.mail, buf, w.size);
+    const bool cut = !INSIDE && (t.last[0] | t.last[1]) != 0;
     if (warp < w.size) mail_send(sh.mail, buf, w.rank, warp, whole, cut);
   }
   // the states before each row, meanwhile
 #pragma unroll
   for (int k = 0; k < W - 1; ++k)
     if (k < warp) h = through<!INSIDE>(get_pair(&sh.down[k][lane]), h);
-#pragma unroll
+#pragma unroll 4
   for (int j = 0; j < R; ++j) {
     if (!INSIDE && (first >> j & 1)) h = start_state(p, t.seq[warp * R + j], w.c, w.cols);
-    const Two before = h;
-    if (INSIDE || (in >> j & 1)) h = fma(e[j], h, b[j]);
-    b[j] = before;  // (from here on the state before the row)
+    const Two b = *state_at(j), e = decay_at(j)->x;
+    *state_at(j) = h;
+    if (INSIDE || (in >> j & 1)) h = fma(e, h, b);
   }
   // the gradient that comes to this warp's last row from the rows behind it
   Two gc = carry.g;
@@ -910,55 +958,61 @@ __device__ __forceinline__ Carry turn_of(const Params& p, const Place& w, Shared
   gc = through<!INSIDE>(behind, gc);
 
   const int64_t row0 = tile * kTile + warp * R;
-  T* dx_at = static_cast<T*>(p.dx) + (row0 + R - 1) * p.dxs + w.c;
-  T* di_at = static_cast<T*>(p.dig) + (row0 + R - 1) * p.dis + w.c;
-  T* dr_at = static_cast<T*>(p.drg) + (row0 + R - 1) * p.drs + w.c;
+  Down<T> dx_at(p.dx, row0 + R - 1, p.dxs, w.c, -1), di_at(p.dig, row0 + R - 1, p.dis, w.c, -1),
+      dr_at(p.drg, row0 + R - 1, p.drs, w.c, -1);
   const bool pairs = p.pairs && w.c0 + kCols <= p.width;
+#pragma unroll 1
+  for (int j0 = R - kAtOnce; j0 >= 0; j0 -= kAtOnce) {
 #pragma unroll
-  for (int j = R - 1; j >= 0; --j) {
-    const Two x = get2(mine + j * kCols);
-    Two g = get2(mine + 3 * kInput + j * kCols);
-    if (!INSIDE && (last >> j & 1)) g = add(g, end_gradient(p, t.seq[warp * R + j], w.c, w.cols));
-    else g = add(g, gc);
-    // dx = g m i,  di = dx x (1 - i)
-    Two dx = mul(mul(m[j], si[j]), g);
-    Two di = mul(mul(dx, x), fma(si[j], con.minus, con.one));
-    // g e r (h - i x e / m)
-    const Two over = each(m[j], [](float v) {
-      const float o = Elem<T>::kExactSilu ? 1.0f / v : rcp_approx(v);
-      return v > 0.0f ? -o : 0.0f;
-    });
-    Two d = fma(mul(mul(si[j], x), e[j]), over, b[j]);
-    const Two eg = mul(e[j], g);
-    d = mul(mul(d, sr[j]), eg);
-    Two dr = mul(mul(d, w.a), fma(sr[j], con.minus, con.one));
-    if (INSIDE || (in >> j & 1)) {
-      carry.da = add(carry.da, d);
-      gc = eg;
-    } else {  // a row of no sequence
-      dx = di = dr = 0;
-    }
-    if (INSIDE && pairs) {
-      put2(dx_at, dx), put2(di_at, di), put2(dr_at, dr);
-    } else if (INSIDE || (row0 + j >= w.lo && row0 + j < w.hi)) {
-      put_some(dx_at, dx, w.cols), put_some(di_at, di, w.cols), put_some(dr_at, dr, w.cols);
-    }
-    dx_at -= p.dxs, di_at -= p.dis, dr_at -= p.drs;
-    if (!INSIDE && p.dinitial && (first >> j & 1)) {
-      const int64_t s = t.seq[warp * R + j];
-      const bool resumes = seq_slot(p.q, s) >= 0 && seq_resumes(p.q, s);
-      put_some(p.dinitial + s * p.width + w.c, resumes ? gc : 0, w.cols);
+    for (int k = kAtOnce - 1; k >= 0; --k) {
+      const int j = j0 + k;
+      const ulonglong2 em = *decay_at(j), ir = *gates_at(j);
+      const Two e = em.x, m = em.y, si = ir.x, sr = ir.y, x = raw(j, 0);
+      Two g = raw(j, 1);
+      if (!INSIDE && (last >> j & 1))
+        g = add(g, end_gradient(p, t.seq[warp * R + j], w.c, w.cols));
+      else
+        g = add(g, gc);
+      // dx = g m i,  di = dx x (1 - i)
+      Two dx = mul(mul(m, si), g);
+      Two di = mul(mul(dx, x), fma(si, con.minus, con.one));
+      // g e r (h - i x e / m)
+      const Two over = each(m, [](float v) {
+        const float o = Elem<T>::kExactSilu ? 1.0f / v : rcp_approx(v);
+        return v > 0.0f ? -o : 0.0f;
+      });
+      Two d = fma(mul(mul(si, x), e), over, *state_at(j));
+      const Two eg = mul(e, g);
+      d = mul(mul(d, sr), eg);
+      Two dr = mul(mul(d, w.a), fma(sr, con.minus, con.one));
+      if (INSIDE || (in >> j & 1)) {
+        carry.da = add(carry.da, d);
+        gc = eg;
+      } else {  // a row of no sequence
+        dx = di = dr = 0;
+      }
+      if (INSIDE || (row0 + j >= w.lo && row0 + j < w.hi)) {
+        if (pairs) {
+          put2(*dx_at, dx), put2(*di_at, di), put2(*dr_at, dr);
+        } else {
+          put_some(*dx_at, dx, w.cols), put_some(*di_at, di, w.cols), put_some(*dr_at, dr, w.cols);
+        }
+      }
+      dx_at.next(), di_at.next(), dr_at.next();
+      if (!INSIDE && p.dinitial && (first >> j & 1)) {
+        const int64_t s = t.seq[warp * R + j];
+        const bool resumes = seq_slot(p.q, s) >= 0 && seq_resumes(p.q, s);
+        put_some(p.dinitial + s * p.width + w.c, resumes ? gc : 0, w.cols);
+      }
     }
   }
-  // (the next turn's search writes rows, its copies the tile)
-  if (!INSIDE || stages<T>() == 1) __syncthreads();
-  if (stages<T>() == 1 && next != INT64_MIN) fetch(p, w, ring, next);
+  __syncthreads();  // (the next tile's copies and search write what was read here)
   return carry;
 }
 template <typename T, bool INSIDE, bool FAST>
-__device__ __noinline__ Carry turn_apart(const Params& p, Place w, Shared& sh, T* ring,
-                                         int64_t tile, int64_t next, int64_t turn, Carry carry) {
-  return turn_of<T, INSIDE, FAST>(p, w, sh, ring, tile, next, turn, carry, Constants());
+__device__ __noinline__ Carry turn_apart(const Params& p, Place w, Shared& sh, T* tiles,
+                                         int64_t tile, int64_t turn, Carry carry) {
+  return turn_of<T, INSIDE, FAST>(p, w, sh, tiles, tile, turn, carry, Constants());
 }
 
 template <typename T>
@@ -966,7 +1020,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     k_recur_backward(const __grid_constant__ Params p) {
   extern __shared__ uint4 s_tile[];
   __shared__ Shared sh;
-  T* const ring = reinterpret_cast<T*>(s_tile);  // x, input gate, decay gate, dout
+  T* const tiles = reinterpret_cast<T*>(s_tile);
   pdl_wait();
   pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -976,24 +1030,26 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int64_t tile0 = w.lo / kTile, count = w.hi > w.lo ? (w.hi + kTile - 1) / kTile - tile0 : 0;
   const int64_t turns = (count + w.size - 1) / w.size;
   int64_t tile = tile0 + count - 1 - w.rank;
-  if (turns > 0) fetch(p, w, ring, tile);
+  Feed<T, kThreads, Row<T>::kPitch / static_cast<int>(sizeof(T)), 4> feed(
+      {p.x, p.dout, p.ig, p.rg}, {p.xs, p.gs, p.is, p.rs}, w.c0, tiles, tile, -w.size);
+  const bool wide = p.chunk == 16 && w.c0 + kCols <= p.width;
   all_wait();
 
   const Constants con;
   Carry carry = {0, 0};
   Rows known;
   for (int64_t turn = 0; turn < turns; ++turn, tile -= w.size) {
-    const int64_t next = turn + 1 < turns ? tile - w.size : INT64_MIN;
+    if (wide && tile * kTile >= w.lo && (tile + 1) * kTile <= w.hi) feed.copy();
+    else fetch(p, w, tiles, tile);
+    feed.advance();
     const bool inside = known.inside<kTile>(p.q, tile, w.lo, w.hi);
     if (!inside && threadIdx.x < kTile) place_rows<kTile>(p.q, tile, w.lo, w.hi, &sh.rows);
     copies_wait();
     __syncthreads();
-    if (inside && w.fast)
-      carry = turn_of<T, true, true>(p, w, sh, ring, tile, next, turn, carry, con);
-    else if (inside)
-      carry = turn_apart<T, true, false>(p, w, sh, ring, tile, next, turn, carry);
-    else
-      carry = turn_apart<T, false, false>(p, w, sh, ring, tile, next, turn, carry);
+    if (inside && w.fast) carry = turn_of<T, true, true>(p, w, sh, tiles, tile, turn, carry, con);
+    else if (inside) carry = turn_apart<T, true, false>(p, w, sh, tiles, tile, turn, carry);
+    else if (w.fast) carry = turn_apart<T, false, true>(p, w, sh, tiles, tile, turn, carry);
+    else carry = turn_apart<T, false, false>(p, w, sh, tiles, tile, turn, carry);
   }
   if (p.dinitial && warp == 0) {
     each_empty(p.q, static_cast<int64_t>(blockIdx.z) * w.size + w.rank,
@@ -1181,20 +1237,16 @@ int launch_forward(Params& p, cudaStream_t s) {
   return launch_cluster(forward::k_recur<T>, blocks, k, forward::kThreads, kSmem, s, p);
 }
 template <typename T>
-constexpr int backward_smem() {
-  return backward::stages<T>() * 4 * kTile * kCols * static_cast<int>(sizeof(T));
-}
-template <typename T>
 Split split_backward(int64_t rows, int64_t seqs, int64_t width) {
-  constexpr int kSmem = backward_smem<T>();
+  constexpr int kSmem = backward::smem<T>();
   if (allow_shared_memory<backward::k_recur_backward<T>>(kSmem) != cudaSuccess) cudaGetLastError();
-  return split_rows<backward::k_recur_backward<T>>(backward::kThreads, kSmem, 2, rows, seqs,
-                                                   blocks_of(width));
+  return split_rows<backward::k_recur_backward<T>>(
+      backward::kThreads, kSmem, sizeof(T) == 2 ? 2 : 1, rows, seqs, blocks_of(width));
 }
 template <typename T>
 int launch_backward(Params& p, float* sums, cudaStream_t s) {
   const int64_t blocks = blocks_of(p.width);
-  constexpr int kSmem = backward_smem<T>();
+  constexpr int kSmem = backward::smem<T>();
   const cudaError_t e = allow_shared_memory<backward::k_recur_backward<T>>(kSmem);
   if (e != cudaSuccess) {
     record_cuda_error(e);
