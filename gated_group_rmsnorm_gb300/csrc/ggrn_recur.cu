@@ -95,9 +95,10 @@ struct Raw<T, 1> {
 // ---------------------------------------------------------------------------
 // Gates of a pair of elements.
 //
-// 16-bit T: sigmoid(z) = 1 / (1 + 2^(-z log2 e)) with the hardware's
-// approximate exponential and reciprocal (both good to about 2^-22; below
-// 2^-126 they give 0).  f32: the accurate functions.
+// sigmoid(z) = 1 / (1 + 2^(-z log2 e)) with the hardware's approximate exponential
+// and reciprocal, both good to about 2^-22 (below 2^-126 they give 0), for f32 too:
+// the accurate functions made its kernels three times as much code, which a call of
+// few tiles spends its time fetching, for outputs 3e-7 instead of 6e-7 off.
 //
 // exp(p) - 1 = p + p^2 (..) where p > -1/4, with a polynomial through the
 // Chebyshev points of that range (within 2^-26 of it), and e = 1 + that, m^2 =
@@ -112,9 +113,12 @@ struct Raw<T, 1> {
 // ---------------------------------------------------------------------------
 constexpr float kSeries = -0.25f;
 
+// (16-bit T: 0 below 2^-126)
+template <typename T>
 __device__ __forceinline__ float sqrt_approx(float x) {
   float y;
-  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  if constexpr (sizeof(T) == 4) asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  else asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
@@ -124,25 +128,8 @@ struct Constants {
       two = held(2.0f), minus = held(-1.0f), log2e = held(-1.4426950408889634f);
 };
 
-template <typename T>
 __device__ __forceinline__ Two sigmoid2(Two z, const Constants& k) {
-  if constexpr (Elem<T>::kExactSilu) {
-    return each(z, [](float v) { return 1.0f / (1.0f + expf(-v)); });
-  } else {
-    return each(add(each(mul(z, k.log2e), ex2_approx), k.one), rcp_approx);
-  }
-}
-
-// exp(p) and exp(p) - 1 for p <= kSeries.
-template <typename T>
-__device__ __forceinline__ void beyond_series(float p, float& e, float& less) {
-  if constexpr (Elem<T>::kExactSilu) {
-    e = expf(p);
-    less = expm1f(p);
-  } else {
-    e = ex2_approx(p * 1.4426950408889634f);
-    less = e - 1.0f;
-  }
+  return each(add(each(mul(z, k.log2e), ex2_approx), k.one), rcp_approx);
 }
 
 // From r and the channels' a: e = exp(a r), m = sqrt(1 - e^2).
@@ -156,13 +143,13 @@ __device__ __forceinline__ void decay2(Two r, Two a, const Constants& k, Two& e,
     float pv[2], ev[2], sv[2];
     split(p, pv[0], pv[1]), split(e, ev[0], ev[1]), split(s, sv[0], sv[1]);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (!(pv[i] > kSeries)) beyond_series<T>(pv[i], ev[i], sv[i]);
+    for (int i = 0; i < 2; ++i) {
+      const float far = ex2_approx(pv[i] * 1.4426950408889634f);
+      if (!(pv[i] > kSeries)) ev[i] = far, sv[i] = far - 1.0f;
+    }
     e = join(ev[0], ev[1]), s = join(sv[0], sv[1]);
   }
-  m = each(mul(s, add(s, k.two)), [](float q) {
-    return Elem<T>::kExactSilu ? sqrtf(-q) : sqrt_approx(-q);
-  });
+  m = each(mul(s, add(s, k.two)), [](float q) { return sqrt_approx<T>(-q); });
 }
 
 // ---------------------------------------------------------------------------
@@ -460,13 +447,13 @@ __device__ __forceinline__ void copy_by(uint32_t to, const T* from, int64_t stri
   const int64_t step = STEP * stride;
   uint32_t at = to + (row0 * PITCH + c) * ES;
   if (whole) {
-#pragma unroll
+#pragma unroll 4
     for (int k = 0; k < ROWS / STEP; ++k, p += step, at += STEP * PITCH * ES)
       copy_async<BYTES>(at, p, BYTES);
     return;
   }
   const int left = cols - c, bytes = left <= 0 ? 0 : left < E ? left * ES : BYTES;
-#pragma unroll 2
+#pragma unroll 1
   for (int k = 0; k < ROWS / STEP; ++k, p += step, at += STEP * PITCH * ES) {
     const int64_t r = r0 + row0 + k * STEP;
     const int n = r >= lo && r < hi ? bytes : 0;
@@ -485,10 +472,10 @@ __device__ __forceinline__ void copy_tile(T* to, const void* base, int64_t strid
     copy_by<T, THREADS, ROWS, PITCH, 16>(smem_u32(to), from, stride, cols, r0, lo, hi, whole);
   } else if (chunk == 4) {
     copy_by<T, THREADS, ROWS, PITCH, 4>(smem_u32(to), from, stride, cols, r0, lo, hi, whole);
-  } else {
-    // single 16-bit elements: through registers, eight in flight
+  } else if constexpr (sizeof(T) == 2) {
+    // single elements: through registers, sixteen in flight
     const int c = static_cast<int>(threadIdx.x) % kCols, row0 = static_cast<int>(threadIdx.x) / kCols;
-    constexpr int STEP = THREADS / kCols, AT_ONCE = 8;
+    constexpr int STEP = THREADS / kCols, AT_ONCE = 16;
     static_assert(ROWS % (STEP * AT_ONCE) == 0, "whole rounds");
 #pragma unroll 1
     for (int k = row0; k < ROWS; k += STEP * AT_ONCE) {
@@ -636,12 +623,13 @@ struct Shared {
 };
 
 template <typename T>
-__device__ __forceinline__ void fetch(const Params& p, const Place& w, T* to, int64_t tile) {
-  const auto copy = [&](int k, const void* base, int64_t stride) {
-    copy_tile<T, kThreads, kTile, pitch<T>()>(to + k * kCols, base, stride, w.c0, p.width, tile,
-                                              w.lo, w.hi, p.chunk);
-  };
-  copy(0, p.x, p.xs), copy(1, p.ig, p.is), copy(2, p.rg, p.rs);
+__device__ __noinline__ void fetch(const Params& p, int64_t lo, int64_t hi, int64_t c0, T* to,
+                                   int64_t tile) {
+#pragma unroll 1
+  for (int k = 0; k < 3; ++k)
+    copy_tile<T, kThreads, kTile, pitch<T>()>(to + k * kCols, k == 0 ? p.x : k == 1 ? p.ig : p.rg,
+                                              k == 0 ? p.xs : k == 1 ? p.is : p.rs, c0, p.width,
+                                              tile, lo, hi, p.chunk);
 }
 
 // One tile.  INSIDE: all of its rows are those of one sequence, neither its first
@@ -663,6 +651,8 @@ __device__ __forceinline__ Two turn_of(const Params& p, const Place& w, Shared& 
     return reinterpret_cast<ulonglong2*>(mine + j * pitch<T>()) + lane;
   };
   // e and b of the warp's rows, and the pair of all of them
+  // (off the loop that nearly all tiles take, short code counts for more)
+  constexpr int kAtOnce = INSIDE && FAST ? forward::kAtOnce : 2;
   Pair all = {kOnes, 0};
 #pragma unroll 1
   for (int j0 = 0; j0 < R; j0 += kAtOnce) {
@@ -677,8 +667,8 @@ __device__ __forceinline__ Two turn_of(const Params& p, const Place& w, Shared& 
     for (int k = 0; k < kAtOnce; ++k) {
       Pair s;
       Two m;
-      decay2<T, FAST>(sigmoid2<T>(gr[k], con), w.a, con, s.e, m);
-      s.b = mul(mul(m, sigmoid2<T>(gi[k], con)), x[k]);
+      decay2<T, FAST>(sigmoid2(gr[k], con), w.a, con, s.e, m);
+      s.b = mul(mul(m, sigmoid2(gi[k], con)), x[k]);
       if constexpr (!INSIDE) {
         if (!(in >> (j0 + k) & 1)) s = {kOnes, 0};
         if (first >> (j0 + k) & 1)
@@ -731,7 +721,7 @@ __device__ __forceinline__ Two turn_of(const Params& p, const Place& w, Shared& 
       }
     }
   } else {
-#pragma unroll 2
+#pragma unroll 1
     for (int j = 0; j < R; ++j, at.next()) {
       h = through<!INSIDE>(get_pair(pair_of(j)), h);
       if (p.out && (INSIDE || (in >> j & 1))) {
@@ -779,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4)
   Rows known;
   for (int64_t turn = 0; turn < turns; ++turn, tile += w.size) {
     if (wide && tile * kTile >= w.lo && (tile + 1) * kTile <= w.hi) feed.copy();
-    else fetch(p, w, tiles, tile);
+    else fetch(p, w.lo, w.hi, w.c0, tiles, tile);
     feed.advance();
     const bool inside = known.inside<kTile>(p.q, tile, w.lo, w.hi);
     if (!inside && threadIdx.x < kTile) place_rows<kTile>(p.q, tile, w.lo, w.hi, &sh.rows);
@@ -842,12 +832,13 @@ struct Shared {
 };
 
 template <typename T>
-__device__ __forceinline__ void fetch(const Params& p, const Place& w, T* to, int64_t tile) {
-  const auto copy = [&](int k, const void* base, int64_t stride) {
+__device__ __noinline__ void fetch(const Params& p, int64_t lo, int64_t hi, int64_t c0, T* to,
+                                   int64_t tile) {
+#pragma unroll 1
+  for (int k = 0; k < 4; ++k)
     copy_tile<T, kThreads, kTile, Row<T>::kPitch / static_cast<int>(sizeof(T))>(
-        to + k * kCols, base, stride, w.c0, p.width, tile, w.lo, w.hi, p.chunk);
-  };
-  copy(0, p.x, p.xs), copy(1, p.dout, p.gs), copy(2, p.ig, p.is), copy(3, p.rg, p.rs);
+        to + k * kCols, k == 0 ? p.x : k == 1 ? p.dout : k == 2 ? p.ig : p.rg,
+        k == 0 ? p.xs : k == 1 ? p.gs : k == 2 ? p.is : p.rs, c0, p.width, tile, lo, hi, p.chunk);
 }
 
 struct Carry {
@@ -887,6 +878,7 @@ __device__ __forceinline__ Carry turn_of(const Params& p, const Place& w, Shared
   };
   const uint32_t in = bits(t.in), first = bits(t.first), last = bits(t.last);
 
+  constexpr int kAtOnce = INSIDE && FAST ? backward::kAtOnce : 2;
   Pair down = {kOnes, 0};
   Two through_e = kOnes, up = 0;  // the rows' gradients as they come out before the first one
   bool ended = false;             // (behind a last row nothing comes through)
@@ -900,7 +892,7 @@ __device__ __forceinline__ Carry turn_of(const Params& p, const Place& w, Shared
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k) {
       const int j = j0 + k;
-      const Two si = sigmoid2<T>(zi[k], con), sr = sigmoid2<T>(zr[k], con);
+      const Two si = sigmoid2(zi[k], con), sr = sigmoid2(zr[k], con);
       Two e, m;
       decay2<T, FAST>(sr, w.a, con, e, m);
       Two b = mul(mul(m, si), x[k]);
@@ -940,7 +932,7 @@ __device__ __forceinline__ Carry turn_of(const Params& p, const Place& w, Shared
 #pragma unroll
   for (int k = 0; k < W - 1; ++k)
     if (k < warp) h = through<!INSIDE>(get_pair(&sh.down[k][lane]), h);
-#pragma unroll 4
+#pragma unroll (INSIDE && FAST ? 4 : 1)
   for (int j = 0; j < R; ++j) {
     if (!INSIDE && (first >> j & 1)) h = start_state(p, t.seq[warp * R + j], w.c, w.cols);
     const Two b = *state_at(j), e = decay_at(j)->x;
@@ -978,8 +970,7 @@ __device__ __forceinline__ Carry turn_of(const Params& p, const Place& w, Shared
       Two di = mul(mul(dx, x), fma(si, con.minus, con.one));
       // g e r (h - i x e / m)
       const Two over = each(m, [](float v) {
-        const float o = Elem<T>::kExactSilu ? 1.0f / v : rcp_approx(v);
-        return v > 0.0f ? -o : 0.0f;
+        return v > 0.0f ? -rcp_approx(v) : 0.0f;
       });
       Two d = fma(mul(mul(si, x), e), over, *state_at(j));
       const Two eg = mul(e, g);
@@ -1040,7 +1031,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   Rows known;
   for (int64_t turn = 0; turn < turns; ++turn, tile -= w.size) {
     if (wide && tile * kTile >= w.lo && (tile + 1) * kTile <= w.hi) feed.copy();
-    else fetch(p, w, tiles, tile);
+    else fetch(p, w.lo, w.hi, w.c0, tiles, tile);
     feed.advance();
     const bool inside = known.inside<kTile>(p.q, tile, w.lo, w.hi);
     if (!inside && threadIdx.x < kTile) place_rows<kTile>(p.q, tile, w.lo, w.hi, &sh.rows);
@@ -1120,8 +1111,8 @@ __global__ void __launch_bounds__(128) k_recur_step(const Params p) {
   }
   xr.get(x), ir.get(gi), rr.get(gr);
   Two e, m;
-  decay2<T, false>(sigmoid2<T>(join(gr[0], gr[1]), con), join(a[0], a[1]), con, e, m);
-  const Two b = mul(mul(m, sigmoid2<T>(join(gi[0], gi[1]), con)), join(x[0], x[1]));
+  decay2<T, false>(sigmoid2(join(gr[0], gr[1]), con), join(a[0], a[1]), con, e, m);
+  const Two b = mul(mul(m, sigmoid2(join(gi[0], gi[1]), con)), join(x[0], x[1]));
   split(fma(e, join(h[0], h[1]), b), h[0], h[1]);
 #pragma unroll
   for (int v = 0; v < V; ++v) state[v] = h[v];
