@@ -156,6 +156,7 @@ int launch(int kind, int dtype, Params& p, const Plan& k, void* workspace, float
   p.team_rows = k.team_rows;
   p.nvec = k.nvec;
   p.gs_f = static_cast<float>(p.gs);
+  p.inv_gs = 1.0f / static_cast<float>(p.gs);
   float* const sums = static_cast<float*>(workspace);
   p.dw = k.sums > 1 ? sums : dw;
   p.db = !db ? nullptr : k.sums > 1 ? sums + k.sums * k.columns : db;

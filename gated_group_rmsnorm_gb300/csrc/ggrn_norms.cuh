@@ -54,7 +54,7 @@ struct Params {
   int team_groups;  // groups that the CTA's teams hold at a time
   int team_rows;    // rows that they hold at a time
   int nvec;         // vectors of a group
-  float eps, gs_f;
+  float eps, gs_f, inv_gs;  // inv_gs: 1 / gs, for sums that need no division
 };
 
 // How a call is laid out (norms::plan).
@@ -372,6 +372,7 @@ __global__ void __launch_bounds__(threads_of(KIND, VPL * E),
       }
       float mean[1] = {value<E>(sum)};
       team_sum<1>(mean, p.lanes, s_sum, 0);
+      // (divided: of a row of one value nothing is left)
       const Two less = both(-__fdiv_rn(mean[0], p.gs_f));
       constexpr int S = kGrad ? 3 : 1;
       Two q[3] = {0, 0, 0};
@@ -393,13 +394,13 @@ __global__ void __launch_bounds__(threads_of(KIND, VPL * E),
 #pragma unroll
       for (int k = 0; k < S; ++k) s[k] = value<E>(q[k]);
       team_sum<S>(s, p.lanes, s_sum, 1);
-      const float nf = rsqrtf(__fdiv_rn(s[0], p.gs_f) + p.eps);
+      const float nf = rsqrtf(s[0] * p.inv_gs + p.eps);
       const Two n = both(nf);
       if (live) {
         Two mu = 0, mud = 0;
         if constexpr (kGrad) {
-          mu = both(-__fdiv_rn(s[1], p.gs_f));
-          mud = both(-__fdiv_rn(s[2], p.gs_f) * nf * nf);
+          mu = both(-s[1] * p.inv_gs);
+          mud = both(-s[2] * p.inv_gs * nf * nf);
         }
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
@@ -450,8 +451,8 @@ __global__ void __launch_bounds__(threads_of(KIND, VPL * E),
       }
       float s[2] = {value<E>(q[0]), value<E>(q[1])};
       team_sum<2>(s, p.lanes, s_sum, turn++ & 1);
-      const float nf = rsqrtf(__fdiv_rn(s[0], p.gs_f) + p.eps);
-      const Two n = both(nf), muv = both(-__fdiv_rn(s[1], p.gs_f) * nf * nf);
+      const float nf = rsqrtf(s[0] * p.inv_gs + p.eps);
+      const Two n = both(nf), muv = both(-s[1] * p.inv_gs * nf * nf);
       if (live) {
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
@@ -579,9 +580,9 @@ __global__ void __launch_bounds__(kAnyThreads) k_norm_any(const Params p) {
     }
     team_sum<3>(s, blockDim.x, s_sum, place);
     place ^= 1;
-    const float n = rsqrtf(__fdiv_rn(s[0], p.gs_f) + p.eps);
-    const float mu = kGated ? 0.0f : __fdiv_rn(s[1], p.gs_f);
-    const float muv = __fdiv_rn(s[2], p.gs_f) * n * n;
+    const float n = rsqrtf(s[0] * p.inv_gs + p.eps);
+    const float mu = kGated ? 0.0f : s[1] * p.inv_gs;
+    const float muv = s[2] * p.inv_gs * n * n;
     for (int64_t j = threadIdx.x; j < p.gs; j += blockDim.x) {
       const float wj = weight_at<KIND, T>(p.w, c0 + j, j);
       const float d = static_cast<float>(x[j]) - mean;

@@ -407,7 +407,7 @@ __device__ __forceinline__ Two end_gradient(const Params& p, int64_t s, int64_t 
   return join(n > 0 ? __ldg(g) : 0.0f, n > 1 ? __ldg(g + 1) : 0.0f);
 }
 
-// Empty sequences among those of this CTA (every `of`-th 32 from the `at`-th):
+// Empty sequences among those of this warp (every `of`-th 32 from the `at`-th):
 // calls f(sequence) with the whole warp.
 template <typename F>
 __device__ __forceinline__ void each_empty(const Seqs& q, int64_t at, int64_t of, F f) {
@@ -787,9 +787,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4)
     else if (w.fast) state = turn_apart<T, false, true>(p, w, sh, tiles, tile, turn, state);
     else state = turn_apart<T, false, false>(p, w, sh, tiles, tile, turn, state);
   }
-  if (p.keep_state && threadIdx.x < 32) {
-    each_empty(p.q, static_cast<int64_t>(blockIdx.z) * w.size + w.rank,
-               static_cast<int64_t>(w.size) * p.segments, [&](int64_t s) {
+  if (p.keep_state) {
+    each_empty(p.q, (static_cast<int64_t>(blockIdx.z) * w.size + w.rank) * W + (threadIdx.x >> 5),
+               static_cast<int64_t>(w.size) * p.segments * W, [&](int64_t s) {
                  const int64_t slot = seq_slot(p.q, s);
                  if (slot < 0 || seq_resumes(p.q, s)) return;
                  for (int v = 0; v < w.cols; ++v) p.state[slot * p.slot_stride + w.c + v] = 0.0f;
@@ -1051,9 +1051,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     else if (w.fast) carry = turn_apart<T, false, true>(p, w, sh, tiles, tile, turn, carry);
     else carry = turn_apart<T, false, false>(p, w, sh, tiles, tile, turn, carry);
   }
-  if (p.dinitial && warp == 0) {
-    each_empty(p.q, static_cast<int64_t>(blockIdx.z) * w.size + w.rank,
-               static_cast<int64_t>(w.size) * p.segments, [&](int64_t s) {
+  if (p.dinitial) {
+    each_empty(p.q, (static_cast<int64_t>(blockIdx.z) * w.size + w.rank) * W + warp,
+               static_cast<int64_t>(w.size) * p.segments * W, [&](int64_t s) {
                  const bool keep = p.dstate && seq_slot(p.q, s) >= 0 && seq_resumes(p.q, s);
                  for (int v = 0; v < w.cols; ++v) {
                    const int64_t k = s * p.width + w.c + v;

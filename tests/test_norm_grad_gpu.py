@@ -78,6 +78,15 @@ def test_layer_norm_far_from_zero():
         ref.assert_close(v, *want[n], torch.float32, n)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("width", [100, 1001, 3840])
+def test_layer_norm_of_rows_of_one_value(width, dtype):
+    """Sums of up to 2^12 times an 8-bit value are exact: nothing is left of the row."""
+    x = torch.tensor([1.0, -3.0, 96.0, 0.0]).to(dtype)[:, None].expand(4, width).contiguous().cuda()
+    w, b = torch.full((width,), 2.0, device="cuda"), torch.full((width,), 0.5, device="cuda")
+    assert (g.layer_norm(x, w, b, eps=1e-6) == 0.5).all()
+
+
 NORM = [(3, 7680, 960), (2, 5120, 5120), (700, 960, 8), (9, 4800, 100), (40, 4096, 128),
         (13, 1001, 77), (5, 1001, 1001), (6, 30, 3), (1, 64, 64), (2, 12288, 6144), (2, 4100, 2050),
         (1, 36000, 18000), (300, 96, 96)]

@@ -273,3 +273,38 @@ def test_the_same_bits_every_time():
         got = (g.linear_recurrence(x, i, r, a),) + g.linear_recurrence_backward(dout, x, i, r, a)[:4]
         first = first or got
         assert all(torch.equal(u, v) for u, v in zip(first, got))
+
+
+def test_many_sequences_most_of_them_empty():
+    """66000 sequences of 300 rows: their states, and the gradients of those."""
+    n, rows, width = 66000, 300, 40
+    gen = torch.Generator().manual_seed(0)
+    cu = torch.sort(torch.randint(0, rows + 1, (n + 1,), generator=gen)).values.to(torch.int32)
+    cu[0], cu[-1] = 0, rows
+    case = Case(rows, width, torch.float32, 1)
+    state = torch.randn(n, width, generator=gen)
+    resume = torch.arange(n) % 2 == 0
+    spans = [(int(cu[k]), int(cu[k + 1])) for k in range(n)]
+    some = [k for k in range(n) if spans[k][1] > spans[k][0]]
+    x, i, r = case.cuda()
+    st = state.cuda()
+    out = g.linear_recurrence(x, i, r, case.a.cuda(), cu_seqlens=cu.cuda(), state=st,
+                              resume=resume.cuda())
+    # (the same without the empty ones)
+    want, bound, new, new_bound, *_ = ref.recur(*case.host(), case.a, [spans[k] for k in some],
+                                                state[some], None, resume[some].tolist())
+    ref.assert_close(out, want, bound, torch.float32)
+    ref.assert_close(st[some], new, new_bound, torch.float32)
+    empty = torch.ones(n, dtype=torch.bool)
+    empty[some] = False
+    assert torch.equal(st.cpu()[empty], state[empty] * resume[empty, None])
+    dstate = torch.randn(n, width, generator=gen)
+    got = g.linear_recurrence_backward(case.dout.cuda(), x, i, r, case.a.cuda(),
+                                       cu_seqlens=cu.cuda(), state=state.cuda(),
+                                       resume=resume.cuda(), dstate=dstate.cuda())
+    grads = ref.recur_backward(case.dout, *case.host(), case.a, [spans[k] for k in some],
+                               state[some], None, resume[some].tolist(), dstate[some])
+    for name, v in zip(("dx", "di", "dr", "da"), got):
+        ref.assert_close(v, *grads[name], torch.float32, name)
+    ref.assert_close(got[4][some], *grads["dh"], torch.float32, "dh")
+    assert torch.equal(got[4].cpu()[empty], dstate[empty] * resume[empty, None])

@@ -1,6 +1,9 @@
 """Layer norm, recurrence and gated norm as a layer uses them together: a training
 step forward and backward, decoding in a graph, calls of several threads, tensors
 past 2^31 elements, and what the binding refuses."""
+import os
+import subprocess
+import sys
 import threading
 
 import pytest
@@ -10,6 +13,7 @@ import gated_group_rmsnorm_gb300 as g
 from tests import train_ref as ref
 
 pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 T = torch.bfloat16
 MODEL, WIDTH, GROUP, EPS = 192, 320, 80, 1e-5
 CU = [0, 1, 130, 130, 400]
@@ -120,6 +124,35 @@ def test_a_captured_training_step():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(u, v) for u, v in zip(got, m.step(cu)))
+
+
+COLD = """
+import torch, gated_group_rmsnorm_gb300 as g
+gen = torch.Generator().manual_seed(0)
+x, i, r, z, d = (torch.randn(900, 512, generator=gen).bfloat16().cuda() for _ in range(5))
+w, a = torch.randn(512, generator=gen).cuda(), -torch.rand(512, generator=gen).cuda()
+torch.cuda.synchronize()
+
+def step():
+    y = g.linear_recurrence(x, i, r, a)
+    out = (g.layer_norm(x, w, eps=1e-5), y) + g.linear_recurrence_backward(d, x, i, r, a)[:4]
+    out += g.layer_norm_backward(d, x, w, eps=1e-5)
+    return out + g.backward(d, y, z, w, group_size=64, eps=1e-5)
+
+graph, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+with torch.cuda.graph(graph, stream=s):
+    got = step()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(u, v) for u, v in zip(got, step()))
+assert g.fault_status() == 0
+"""
+
+
+def test_the_first_calls_of_a_process_may_be_captured():
+    r = subprocess.run([sys.executable, "-c", COLD], cwd=ROOT, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
 
 
 def test_two_captured_steps_at_once():
