@@ -238,10 +238,10 @@ constexpr int inputs_of(int kind) { return kind == kLayerNorm ? 1 : kind == kLay
 __host__ __device__ constexpr int room_of(int kind, int elems) {
   return kind == kLayerNorm       ? (elems <= 8 ? 1024 : elems <= 16 ? 768 : 512)
          : kind == kLayerNormGrad ? (elems <= 4 ? 1024 : elems <= 8 ? 768 : 512)
-                                  : (elems <= 4 ? 1024 : elems <= 8 ? 768 : 512);
+                                  : (elems <= 4 ? 1024 : elems <= 8 ? 640 : 512);
 }
 __host__ __device__ constexpr int threads_of(int kind, int elems) {
-  return room_of(kind, elems) == 768 ? 768 : 512;
+  return room_of(kind, elems) == 1024 ? 512 : room_of(kind, elems);
 }
 // Most elements of a thread: more need more registers than there are (a team of 32
 // times as many, or a CTA, may hold a larger group all the same).
