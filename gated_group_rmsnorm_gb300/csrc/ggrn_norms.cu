@@ -46,7 +46,7 @@ Plan plan(int kind, int es, int64_t rows, int64_t groups, int64_t gs, int elems)
   Plan k;
   k.elems = elems;
   const int64_t nvec = gs / elems;
-  int vpl = most_elems(kind) / elems;
+  int vpl = team_elems(kind) / elems;
   vpl = vpl > 4 ? 4 : vpl;
   int lanes = 1;
   while (lanes < 32 && lanes * vpl < nvec) lanes <<= 1;
@@ -60,20 +60,19 @@ Plan plan(int kind, int es, int64_t rows, int64_t groups, int64_t gs, int elems)
     k.team_rows = teams / k.team_groups;
     k.threads = (k.team_groups * k.team_rows * lanes + 31) / 32 * 32;
   } else {
-    // a CTA to a group: as many vectors a thread as it holds well (fewer threads to
-    // sum over: 16384 rows of 3840, gradients, 91 us with two and 140 with one), if
-    // that leaves an SM at least three quarters of the threads it may have
+    // a CTA to a group.  Layer norm: as many vectors a thread as it holds well (16384
+    // rows of 3840: 46 us with four, 64 with one, whose sums take more threads).  The
+    // gradients: those that give an SM the most threads, the more of two alike.
     k.vpl = 0;
-    for (int v : {vpl, vpl / 2, 4}) {
-      if (v < 1 || v > 4) continue;
+    int64_t most = 0;
+    for (int v = 1; v <= 4; v *= 2) {
       const int64_t threads = ((nvec + v - 1) / v + 31) / 32 * 32;
       if (threads > threads_of(kind, v * elems) ||
           threads * v * elems * es * inputs_of(kind) * depth_of(kind) > kRingMost)
         continue;
-      const int64_t room = room_of(kind, v * elems), held = room / threads * threads;
-      if (k.vpl && v == vpl / 2 && k.threads * (room_of(kind, vpl * elems) / k.threads) >= held * 3 / 4)
-        continue;
-      if (k.vpl && v == 4) continue;
+      const int64_t held = room_of(kind, v * elems) / threads * threads;
+      if (k.vpl && (v * elems > cta_elems(kind) || (kind != kLayerNorm && held < most))) continue;
+      most = held;
       k.vpl = v;
       k.threads = static_cast<int>(threads);
     }
