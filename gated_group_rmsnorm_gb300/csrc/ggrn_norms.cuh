@@ -21,10 +21,10 @@
 // The mean is taken off before squares are summed (two reductions), so a row
 // whose mean is far from zero loses nothing.
 //
-// Of the measured copy rate: layer norm 79-86 % (16384 x 3840 bf16 46 us), its
-// gradients 51-68 % (95 us), the gated norm's 59-80 % (16384 x 4800 bf16 in groups of
-// 100 180 us, 16384 x 4096 f16 in groups of 128 124 us).  The gradients are bound by
-// their instructions (26 to 45 an element, the sums over a group among them) at the
+// Of the measured copy rate: layer norm 80-93 % (16384 x 3840 bf16 46 us), its
+// gradients 46-71 % from rows of 1024 (89 us), the gated norm's 73-82 % (16384 x 4800 bf16 in groups of
+// 100 155 us, 16384 x 4096 f16 in groups of 128 121 us).  The gradients are bound by
+// their instructions (24 to 53 an element, the sums over a group among them) at the
 // 16 to 24 warps that their registers leave an SM: a thread keeps its columns' sums
 // and weights besides a row's values.
 #pragma once
