@@ -354,7 +354,8 @@ __global__ void __launch_bounds__(threads_of(KIND, VPL * E),
        first += step) {
     fetch();
     copies_wait<kDepth>();
-    const bool live = row < p.rows;
+    // (a team without a group has n = inf of its zeros where eps is 0)
+    const bool live = mine && row < p.rows;
     const auto load = [&](int m, int i, Two (&f)[N]) {
       Vec v;
       v.w = from[(m * VPL + i) * blockDim.x];
