@@ -102,10 +102,9 @@ struct Raw<T, 1> {
 // ---------------------------------------------------------------------------
 // Gates of a pair of elements.
 //
-// sigmoid(z) = 1 / (1 + 2^(-z log2 e)) with the hardware's approximate exponential
-// and reciprocal, both good to about 2^-22 (below 2^-126 they give 0), for f32 too:
-// the accurate functions made its kernels three times as much code, which a call of
-// few tiles spends its time fetching, for outputs 3e-7 instead of 6e-7 off.
+// 16-bit T: sigmoid(z) = 1 / (1 + 2^(-z log2 e)) with the hardware's approximate
+// exponential and reciprocal, both good to about 2^-22 (below 2^-126 they give 0).
+// f32: see Accurate below.
 //
 // exp(p) - 1 = p + p^2 (..) where p > -1/4, with a polynomial through the
 // Chebyshev points of that range (within 2^-26 of it), and e = 1 + that, m^2 =
@@ -119,19 +118,17 @@ struct Raw<T, 1> {
 // since a pair of constants costs two moves wherever it is used otherwise.
 // ---------------------------------------------------------------------------
 constexpr float kSeries = -0.25f;
+constexpr float kC4 = 7.67176877707243e-3f, kC3 = 4.1564859449863434e-2f,
+                kC2 = 1.666616052389145e-1f, kC1 = 4.999999701976776e-1f;
 
-// (16-bit T: 0 below 2^-126)
-template <typename T>
 __device__ __forceinline__ float sqrt_approx(float x) {
   float y;
-  if constexpr (sizeof(T) == 4) asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-  else asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
 struct Constants {
-  Two c4 = held(7.67176877707243e-3f), c3 = held(4.1564859449863434e-2f),
-      c2 = held(1.666616052389145e-1f), c1 = held(4.999999701976776e-1f), one = held(1.0f),
+  Two c4 = held(kC4), c3 = held(kC3), c2 = held(kC2), c1 = held(kC1), one = held(1.0f),
       two = held(2.0f), minus = held(-1.0f), log2e = held(-1.4426950408889634f);
 };
 
@@ -140,7 +137,7 @@ __device__ __forceinline__ Two sigmoid2(Two z, const Constants& k) {
 }
 
 // From r and the channels' a: e = exp(a r), m = sqrt(1 - e^2).
-template <typename T, bool FAST>
+template <bool FAST>
 __device__ __forceinline__ void decay2(Two r, Two a, const Constants& k, Two& e, Two& m) {
   const Two p = mul(a, r);
   Two s = fma(fma(fma(fma(p, k.c4, k.c3), p, k.c2), p, k.c1), p, k.one);
@@ -156,7 +153,78 @@ __device__ __forceinline__ void decay2(Two r, Two a, const Constants& k, Two& e,
     }
     e = join(ev[0], ev[1]), s = join(sv[0], sv[1]);
   }
-  m = each(mul(s, add(s, k.two)), [](float q) { return sqrt_approx<T>(-q); });
+  m = each(mul(s, add(s, k.two)), [](float q) { return sqrt_approx(-q); });
+}
+
+// ---------------------------------------------------------------------------
+// The same for f32, each result within a few roundings (u = 2^-24) of its argument's:
+//   exp(-|z|)    t = -|z| log2 e rounded, m = -|z| - t ln 2 by two fma (Cody and Waite's
+//                reduction, without an integer part), 2^t (1 + m): 5 u, 4 of them the
+//                hardware's exponential (below 2^-126 it gives 0).
+//   1 / (1 + E)  Newton's iteration once, from the hardware's reciprocal.  It is the larger
+//                of sigmoid(z) and sigmoid(-z), E times it the smaller: 8 u, at both ends.
+//   sqrt(q)      Newton's iteration once, from the hardware's reciprocal root.
+// (CUDA's expf, division and sqrtf are as good, one element at a time and with branches:
+// 2048 x 5120 took 84 us with them, 56 with these and 48 with the approximate functions
+// of 16-bit T.)  Decays beyond the series take expf and expm1f.
+// ---------------------------------------------------------------------------
+struct Accurate {
+  Two c4 = held(kC4), c3 = held(kC3), c2 = held(kC2), c1 = held(kC1), one = held(1.0f),
+      two = held(2.0f), minus = held(-1.0f), half = held(0.5f), log2e = held(1.4426950408889634f),
+      ln2 = held(-0.693147180559945309f), ln2_rest = held(1.904654299958e-9f);
+};
+template <typename T>
+using ConstantsOf = typename std::conditional<Elem<T>::kExactSilu, Accurate, Constants>::type;
+
+// sigmoid(z)
+__device__ __forceinline__ Two sigmoid_accurate(Two z, const Accurate& k) {
+  const Two a = each(z, [](float v) {  // -|z| (a NaN stays one), where E is 0 at the latest
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(-fabsf(v)), "f"(-128.0f));
+    return r;
+  });
+  const Two t = mul(a, k.log2e);
+  const Two m = fma(t, k.ln2_rest, fma(t, k.ln2, a));
+  const Two e0 = each(t, ex2_approx), e = fma(e0, m, e0);
+  const Two less = fma(e, k.minus, k.minus);  // -(1 + E)
+  const Two r = each(less, [](float v) { return rcp_approx(-v); });
+  const Two big = fma(r, fma(less, r, k.one), r), small = mul(e, big);
+  float zv[2], bv[2], sv[2];
+  split(z, zv[0], zv[1]), split(big, bv[0], bv[1]), split(small, sv[0], sv[1]);
+  return join(zv[0] < 0.0f ? sv[0] : bv[0], zv[1] < 0.0f ? sv[1] : bv[1]);
+}
+// exp(p) and exp(p) - 1 of the halves that the series does not reach.
+__device__ __noinline__ ulonglong2 decay_beyond(Two p, Two e, Two s) {
+  float pv[2], ev[2], sv[2];
+  split(p, pv[0], pv[1]), split(e, ev[0], ev[1]), split(s, sv[0], sv[1]);
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i) {
+    const float v = i ? pv[1] : pv[0];
+    if (v > kSeries) continue;
+    const float x = expf(v), y = expm1f(v);
+    if (i) ev[1] = x, sv[1] = y;
+    else ev[0] = x, sv[0] = y;
+  }
+  return make_ulonglong2(join(ev[0], ev[1]), join(sv[0], sv[1]));
+}
+// e = exp(a r), m = sqrt(1 - e^2)
+__device__ __forceinline__ void decay_accurate(Two r, Two a, const Accurate& k, Two& e, Two& m) {
+  const Two p = mul(a, r);
+  Two s = fma(fma(fma(fma(p, k.c4, k.c3), p, k.c2), p, k.c1), p, k.one);
+  s = mul(s, p);  // e - 1
+  e = add(s, k.one);
+  float p0, p1;
+  split(p, p0, p1);
+  if (!(p0 > kSeries && p1 > kSeries)) {
+    const ulonglong2 f = decay_beyond(p, e, s);
+    e = f.x, s = f.y;
+  }
+  const Two q = mul(s, add(s, k.two));  // -m^2
+  const Two y = each(q, [](float v) { return rsqrtf(-v); });
+  const Two root = mul(q, y), half = mul(y, k.half);  // -m, nearly; 1 / 2m
+  float qv[2], mv[2];
+  split(q, qv[0], qv[1]), split(mul(fma(fma(root, root, q), half, root), k.minus), mv[0], mv[1]);
+  m = join(qv[0] == 0.0f ? 0.0f : mv[0], qv[1] == 0.0f ? 0.0f : mv[1]);
 }
 
 // ---------------------------------------------------------------------------
@@ -640,14 +708,16 @@ __device__ __noinline__ void fetch(const Params& p, int64_t lo, int64_t hi, int6
 }
 
 // One tile.  INSIDE: all of its rows are those of one sequence, neither its first
-// nor its last.  FAST: see decay2.  Takes the state before the cluster's tiles and
-// gives the one behind them.
+// nor its last.  FAST: see decay2 (f32: true).  Takes the state before the cluster's
+// tiles and gives the one behind them.
 template <typename T, bool INSIDE, bool FAST>
 __device__ __forceinline__ Two turn_of(const Params& p, const Place& w, Shared& sh, T* tiles,
-                                       int64_t tile, int64_t turn, Two state, const Constants& con) {
+                                       int64_t tile, int64_t turn, Two state,
+                                       const ConstantsOf<T>& con) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int buf = turn & 1;
   const uint32_t parity = turn >> 1 & 1;
+  constexpr bool kAccurate = Elem<T>::kExactSilu;
   T* const mine = tiles + warp * R * pitch<T>();
   const auto& t = sh.rows;
   const auto bits = [&](const uint32_t* of) {
@@ -674,8 +744,13 @@ __device__ __forceinline__ Two turn_of(const Params& p, const Place& w, Shared& 
     for (int k = 0; k < kAtOnce; ++k) {
       Pair s;
       Two m;
-      decay2<T, FAST>(sigmoid2(gr[k], con), w.a, con, s.e, m);
-      s.b = mul(mul(m, sigmoid2(gi[k], con)), x[k]);
+      if constexpr (kAccurate) {
+        decay_accurate(sigmoid_accurate(gr[k], con), w.a, con, s.e, m);
+        s.b = mul(mul(m, sigmoid_accurate(gi[k], con)), x[k]);
+      } else {
+        decay2<FAST>(sigmoid2(gr[k], con), w.a, con, s.e, m);
+        s.b = mul(mul(m, sigmoid2(gi[k], con)), x[k]);
+      }
       if constexpr (!INSIDE) {
         if (!(in >> (j0 + k) & 1)) s = {kOnes, 0};
         if (first >> (j0 + k) & 1)
@@ -749,7 +824,7 @@ __device__ __forceinline__ Two turn_of(const Params& p, const Place& w, Shared& 
 template <typename T, bool INSIDE, bool FAST>
 __device__ __noinline__ Two turn_apart(const Params& p, Place w, Shared& sh, T* tiles,
                                        int64_t tile, int64_t turn, Two state) {
-  return turn_of<T, INSIDE, FAST>(p, w, sh, tiles, tile, turn, state, Constants());
+  return turn_of<T, INSIDE, FAST>(p, w, sh, tiles, tile, turn, state, ConstantsOf<T>());
 }
 
 template <typename T>
@@ -771,7 +846,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4)
   const bool wide = p.chunk == 16 && w.c0 + kCols <= p.width;
   all_wait();
 
-  const Constants con;
+  const ConstantsOf<T> con;
   Two state = 0;  // before the cluster's tiles
   Rows known;
   for (int64_t turn = 0; turn < turns; ++turn, tile += w.size) {
@@ -782,10 +857,15 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4)
     if (!inside && threadIdx.x < kTile) place_rows<kTile>(p.q, tile, w.lo, w.hi, &sh.rows);
     copies_wait();
     __syncthreads();
-    if (inside && w.fast) state = turn_of<T, true, true>(p, w, sh, tiles, tile, turn, state, con);
-    else if (inside) state = turn_apart<T, true, false>(p, w, sh, tiles, tile, turn, state);
-    else if (w.fast) state = turn_apart<T, false, true>(p, w, sh, tiles, tile, turn, state);
-    else state = turn_apart<T, false, false>(p, w, sh, tiles, tile, turn, state);
+    if constexpr (Elem<T>::kExactSilu) {
+      if (inside) state = turn_of<T, true, true>(p, w, sh, tiles, tile, turn, state, con);
+      else state = turn_apart<T, false, true>(p, w, sh, tiles, tile, turn, state);
+    } else {
+      if (inside && w.fast) state = turn_of<T, true, true>(p, w, sh, tiles, tile, turn, state, con);
+      else if (inside) state = turn_apart<T, true, false>(p, w, sh, tiles, tile, turn, state);
+      else if (w.fast) state = turn_apart<T, false, true>(p, w, sh, tiles, tile, turn, state);
+      else state = turn_apart<T, false, false>(p, w, sh, tiles, tile, turn, state);
+    }
   }
   if (p.keep_state) {
     each_empty(p.q, (static_cast<int64_t>(blockIdx.z) * w.size + w.rank) * W + (threadIdx.x >> 5),
@@ -858,7 +938,7 @@ struct Carry {
 template <typename T, bool INSIDE, bool FAST>
 __device__ __forceinline__ Carry turn_of(const Params& p, const Place& w, Shared& sh, T* tiles,
                                          int64_t tile, int64_t turn, Carry carry,
-                                         const Constants& con) {
+                                         const ConstantsOf<T>& con) {
   using L = Row<T>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int buf = turn & 1;
@@ -891,6 +971,7 @@ __device__ __forceinline__ Carry turn_of(const Params& p, const Place& w, Shared
   Pair down = {kOnes, 0};
   Two through_e = kOnes, up = 0;  // the rows' gradients as they come out before the first one
   bool ended = false;             // (behind a last row nothing comes through)
+  constexpr bool kAccurate = Elem<T>::kExactSilu;
 #pragma unroll 1
   for (int j0 = 0; j0 < R; j0 += kAtOnce) {
     Two x[kAtOnce], g[kAtOnce], zi[kAtOnce], zr[kAtOnce];
@@ -901,16 +982,22 @@ __device__ __forceinline__ Carry turn_of(const Params& p, const Place& w, Shared
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k) {
       const int j = j0 + k;
-      const Two si = sigmoid2(zi[k], con), sr = sigmoid2(zr[k], con);
-      Two e, m;
-      decay2<T, FAST>(sr, w.a, con, e, m);
+      Two si, sr, e, m;
+      if constexpr (kAccurate) {
+        si = sigmoid_accurate(zi[k], con), sr = sigmoid_accurate(zr[k], con);
+        decay_accurate(sr, w.a, con, e, m);
+      } else {
+        si = sigmoid2(zi[k], con), sr = sigmoid2(zr[k], con);
+        decay2<FAST>(sr, w.a, con, e, m);
+      }
       Two b = mul(mul(m, si), x[k]);
-      if (!INSIDE && !(in >> j & 1)) e = kOnes, b = 0, g[k] = 0;
-      if (!INSIDE && (last >> j & 1))
-        g[k] = add(g[k], end_gradient(p, t.seq[warp * R + j], w.c, w.cols));
       *decay_at(j) = make_ulonglong2(e, m);
       *gates_at(j) = make_ulonglong2(si, sr);
       *state_at(j) = b;
+      // (what is kept of a row of no sequence is not used)
+      if (!INSIDE && !(in >> j & 1)) e = kOnes, b = 0, g[k] = 0;
+      if (!INSIDE && (last >> j & 1))
+        g[k] = add(g[k], end_gradient(p, t.seq[warp * R + j], w.c, w.cols));
       if (!INSIDE && (first >> j & 1))
         down = {kCut, fma(e, start_state(p, t.seq[warp * R + j], w.c, w.cols), b)};
       else
@@ -979,7 +1066,8 @@ __device__ __forceinline__ Carry turn_of(const Params& p, const Place& w, Shared
       Two di = mul(mul(dx, x), fma(si, con.minus, con.one));
       // g e r (h - i x e / m)
       const Two over = each(m, [](float v) {
-        return v > 0.0f ? -rcp_approx(v) : 0.0f;
+        const float o = kAccurate ? 1.0f / v : rcp_approx(v);
+        return v > 0.0f ? -o : 0.0f;
       });
       Two d = fma(mul(mul(si, x), e), over, *state_at(j));
       const Two eg = mul(e, g);
@@ -1012,7 +1100,7 @@ __device__ __forceinline__ Carry turn_of(const Params& p, const Place& w, Shared
 template <typename T, bool INSIDE, bool FAST>
 __device__ __noinline__ Carry turn_apart(const Params& p, Place w, Shared& sh, T* tiles,
                                          int64_t tile, int64_t turn, Carry carry) {
-  return turn_of<T, INSIDE, FAST>(p, w, sh, tiles, tile, turn, carry, Constants());
+  return turn_of<T, INSIDE, FAST>(p, w, sh, tiles, tile, turn, carry, ConstantsOf<T>());
 }
 
 template <typename T>
@@ -1035,7 +1123,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const bool wide = p.chunk == 16 && w.c0 + kCols <= p.width;
   all_wait();
 
-  const Constants con;
+  const ConstantsOf<T> con;
   Carry carry = {0, 0};
   Rows known;
   for (int64_t turn = 0; turn < turns; ++turn, tile -= w.size) {
@@ -1046,10 +1134,15 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (!inside && threadIdx.x < kTile) place_rows<kTile>(p.q, tile, w.lo, w.hi, &sh.rows);
     copies_wait();
     __syncthreads();
-    if (inside && w.fast) carry = turn_of<T, true, true>(p, w, sh, tiles, tile, turn, carry, con);
-    else if (inside) carry = turn_apart<T, true, false>(p, w, sh, tiles, tile, turn, carry);
-    else if (w.fast) carry = turn_apart<T, false, true>(p, w, sh, tiles, tile, turn, carry);
-    else carry = turn_apart<T, false, false>(p, w, sh, tiles, tile, turn, carry);
+    if constexpr (Elem<T>::kExactSilu) {
+      if (inside) carry = turn_of<T, true, true>(p, w, sh, tiles, tile, turn, carry, con);
+      else carry = turn_apart<T, false, true>(p, w, sh, tiles, tile, turn, carry);
+    } else {
+      if (inside && w.fast) carry = turn_of<T, true, true>(p, w, sh, tiles, tile, turn, carry, con);
+      else if (inside) carry = turn_apart<T, true, false>(p, w, sh, tiles, tile, turn, carry);
+      else if (w.fast) carry = turn_apart<T, false, true>(p, w, sh, tiles, tile, turn, carry);
+      else carry = turn_apart<T, false, false>(p, w, sh, tiles, tile, turn, carry);
+    }
   }
   if (p.dinitial) {
     each_empty(p.q, (static_cast<int64_t>(blockIdx.z) * w.size + w.rank) * W + warp,
@@ -1105,7 +1198,6 @@ __global__ void __launch_bounds__(128) k_recur_step(const Params p) {
   const int64_t row = blockIdx.x;
   const int64_t slot = seq_slot(p.q, row);
   if (c >= p.width || slot < 0) return;
-  const Constants con;
   float* state = p.state + slot * p.slot_stride + c;
   Raw<T, V> xr, ir, rr;
   xr.load(static_cast<const T*>(p.x) + row * p.xs + c);
@@ -1119,10 +1211,17 @@ __global__ void __launch_bounds__(128) k_recur_step(const Params p) {
     h[v] = state[v];
   }
   xr.get(x), ir.get(gi), rr.get(gr);
-  Two e, m;
-  decay2<T, false>(sigmoid2(join(gr[0], gr[1]), con), join(a[0], a[1]), con, e, m);
-  const Two b = mul(mul(m, sigmoid2(join(gi[0], gi[1]), con)), join(x[0], x[1]));
-  split(fma(e, join(h[0], h[1]), b), h[0], h[1]);
+  const Two zi = join(gi[0], gi[1]), zr = join(gr[0], gr[1]), av = join(a[0], a[1]);
+  const ConstantsOf<T> con;
+  Two e, m, si;
+  if constexpr (Elem<T>::kExactSilu) {
+    si = sigmoid_accurate(zi, con);
+    decay_accurate(sigmoid_accurate(zr, con), av, con, e, m);
+  } else {
+    si = sigmoid2(zi, con);
+    decay2<false>(sigmoid2(zr, con), av, con, e, m);
+  }
+  split(fma(e, join(h[0], h[1]), mul(mul(m, si), join(x[0], x[1]))), h[0], h[1]);
 #pragma unroll
   for (int v = 0; v < V; ++v) state[v] = h[v];
   Raw<T, V>::put(static_cast<T*>(p.out) + row * p.os + c, h);

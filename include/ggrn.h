@@ -572,7 +572,8 @@ int ggrn_selftest_scan_timeout(const ggrn_scan_call* call, void* cuda_stream);
  * Values that are not finite reach only what depends on them; an infinite state
  * whose decay over a tile of 64 rows is zero in f32 may become a NaN.  A gate whose
  * sigmoid is below 2^-126 is closed (16-bit T: one that leaves 1 - exp(2 p) below
- * 2^-126, too); exponentials, reciprocals and roots are good to about 2^-22.
+ * 2^-126, too).  f32: sigmoids, decays and roots are good to a few times 2^-24;
+ * 16-bit T: exponentials, reciprocals and roots to about 2^-22.
  * -------------------------------------------------------------------------- */
 #define GGRN_RECUR_SAVED_ROWS 64
 
