@@ -132,8 +132,22 @@ struct Constants {
       two = held(2.0f), minus = held(-1.0f), log2e = held(-1.4426950408889634f);
 };
 
+// exp(-z), and sigmoid(z) of that
+__device__ __forceinline__ Two odds2(Two z, const Constants& k) {
+  return each(mul(z, k.log2e), ex2_approx);
+}
+__device__ __forceinline__ Two gate_of(Two odds, const Constants& k) {
+  return each(add(odds, k.one), rcp_approx);
+}
 __device__ __forceinline__ Two sigmoid2(Two z, const Constants& k) {
-  return each(add(each(mul(z, k.log2e), ex2_approx), k.one), rcp_approx);
+  return gate_of(odds2(z, k), k);
+}
+// 1 - sigmoid(z), without cancellation (where infinite odds meet a gate of 0, a 0: the
+// gate is a factor of all that this is one of)
+__device__ __forceinline__ Two rest_of(Two odds, Two gate) {
+  float o[2], g[2];
+  split(odds, o[0], o[1]), split(gate, g[0], g[1]);
+  return join(__saturatef(o[0] * g[0]), __saturatef(o[1] * g[1]));
 }
 
 // From r and the channels' a: e = exp(a r), m = sqrt(1 - e^2).
@@ -176,8 +190,8 @@ struct Accurate {
 template <typename T>
 using ConstantsOf = typename std::conditional<Elem<T>::kExactSilu, Accurate, Constants>::type;
 
-// sigmoid(z)
-__device__ __forceinline__ Two sigmoid_accurate(Two z, const Accurate& k) {
+// sigmoid(z), and (in `rest`) 1 - sigmoid(z)
+__device__ __forceinline__ Two sigmoid_accurate(Two z, const Accurate& k, Two& rest) {
   const Two a = each(z, [](float v) {  // -|z| (a NaN stays one), where E is 0 at the latest
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(-fabsf(v)), "f"(-128.0f));
@@ -191,7 +205,12 @@ __device__ __forceinline__ Two sigmoid_accurate(Two z, const Accurate& k) {
   const Two big = fma(r, fma(less, r, k.one), r), small = mul(e, big);
   float zv[2], bv[2], sv[2];
   split(z, zv[0], zv[1]), split(big, bv[0], bv[1]), split(small, sv[0], sv[1]);
+  rest = join(zv[0] < 0.0f ? bv[0] : sv[0], zv[1] < 0.0f ? bv[1] : sv[1]);
   return join(zv[0] < 0.0f ? sv[0] : bv[0], zv[1] < 0.0f ? sv[1] : bv[1]);
+}
+__device__ __forceinline__ Two sigmoid_accurate(Two z, const Accurate& k) {
+  Two rest;
+  return sigmoid_accurate(z, k, rest);
 }
 // exp(p) and exp(p) - 1 of the halves that the series does not reach.
 __device__ __noinline__ ulonglong2 decay_beyond(Two p, Two e, Two s) {
@@ -207,8 +226,9 @@ __device__ __noinline__ ulonglong2 decay_beyond(Two p, Two e, Two s) {
   }
   return make_ulonglong2(join(ev[0], ev[1]), join(sv[0], sv[1]));
 }
-// e = exp(a r), m = sqrt(1 - e^2)
-__device__ __forceinline__ void decay_accurate(Two r, Two a, const Accurate& k, Two& e, Two& m) {
+// e = exp(a r), m = sqrt(1 - e^2), and 1 / m (0 where m is)
+__device__ __forceinline__ void decay_accurate(Two r, Two a, const Accurate& k, Two& e, Two& m,
+                                               Two& over) {
   const Two p = mul(a, r);
   Two s = fma(fma(fma(fma(p, k.c4, k.c3), p, k.c2), p, k.c1), p, k.one);
   s = mul(s, p);  // e - 1
@@ -222,9 +242,15 @@ __device__ __forceinline__ void decay_accurate(Two r, Two a, const Accurate& k, 
   const Two q = mul(s, add(s, k.two));  // -m^2
   const Two y = each(q, [](float v) { return rsqrtf(-v); });
   const Two root = mul(q, y), half = mul(y, k.half);  // -m, nearly; 1 / 2m
-  float qv[2], mv[2];
+  float qv[2], mv[2], ov[2];
   split(q, qv[0], qv[1]), split(mul(fma(fma(root, root, q), half, root), k.minus), mv[0], mv[1]);
+  split(fma(fma(root, y, k.one), half, y), ov[0], ov[1]);
   m = join(qv[0] == 0.0f ? 0.0f : mv[0], qv[1] == 0.0f ? 0.0f : mv[1]);
+  over = join(qv[0] == 0.0f ? 0.0f : ov[0], qv[1] == 0.0f ? 0.0f : ov[1]);
+}
+__device__ __forceinline__ void decay_accurate(Two r, Two a, const Accurate& k, Two& e, Two& m) {
+  Two over;
+  decay_accurate(r, a, k, e, m, over);
 }
 
 // ---------------------------------------------------------------------------
@@ -898,15 +924,18 @@ constexpr int W = 8, R = kTile / W, kThreads = 32 * W;
 constexpr int kAtOnce = 4;  // rows of a loop's turn
 static_assert(W >= kMaxCluster, "a warp to each CTA that the tile's pair goes to");
 
-// A row of the tile, in bytes: x, dout, the input gate, the decay gate; (e, m) of each
-// lane; (i, r) of each lane; b, later the state before the row.  i and r of f32, b of
-// 16-bit types take the place of the gates' logits.
+// A row of the tile, in bytes: x, dout, the input gate, the decay gate; then, of each lane,
+//   16-bit T  (e, m); the gates' odds exp(-z), from which i, r, 1 - i and 1 - r come again
+//             (1 - i of the rounded i has no digit left at logits of 16); b, later the
+//             state before the row, in the place of the gates' logits
+//   f32       (e, m i), in the place of the gates' logits; (r, 1 - r);
+//             (m i x (1 - i), -i x e / m); b, later the state, in the place of x
 template <typename T>
 struct Row {
-  static constexpr int ES = sizeof(T), kRaw = 4 * kCols * ES;
-  static constexpr int kDecay = kRaw, kGates = ES == 4 ? 2 * kCols * ES : kRaw + 512,
-                       kState = ES == 4 ? kRaw + 512 : 2 * kCols * ES;
-  static constexpr int kPitch = ES == 4 ? kRaw + 768 : kRaw + 1024;
+  static constexpr int ES = sizeof(T), kRaw = 4 * kCols * ES, kLogits = 2 * kCols * ES;
+  static constexpr int kDecay = ES == 4 ? kLogits : kRaw, kGates = ES == 4 ? kRaw : kRaw + 512,
+                       kTerms = kRaw + 512, kState = ES == 4 ? 0 : kLogits;
+  static constexpr int kPitch = kRaw + 1024;
 };
 template <typename T>
 constexpr int smem() {
@@ -954,6 +983,9 @@ __device__ __forceinline__ Carry turn_of(const Params& p, const Place& w, Shared
   const auto gates_at = [&](int j) {
     return reinterpret_cast<ulonglong2*>(mine + j * L::kPitch + L::kGates) + lane;
   };
+  const auto terms_at = [&](int j) {
+    return reinterpret_cast<ulonglong2*>(mine + j * L::kPitch + L::kTerms) + lane;
+  };
   const auto state_at = [&](int j) {
     return reinterpret_cast<Two*>(mine + j * L::kPitch + L::kState) + lane;
   };
@@ -982,17 +1014,24 @@ __device__ __forceinline__ Carry turn_of(const Params& p, const Place& w, Shared
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k) {
       const int j = j0 + k;
-      Two si, sr, e, m;
+      Two e, m, b;
       if constexpr (kAccurate) {
-        si = sigmoid_accurate(zi[k], con), sr = sigmoid_accurate(zr[k], con);
-        decay_accurate(sr, w.a, con, e, m);
+        Two ci, cr, over;
+        const Two si = sigmoid_accurate(zi[k], con, ci), sr = sigmoid_accurate(zr[k], con, cr);
+        decay_accurate(sr, w.a, con, e, m, over);
+        const Two mi = mul(m, si);
+        b = mul(mi, x[k]);
+        *decay_at(j) = make_ulonglong2(e, mi);
+        *gates_at(j) = make_ulonglong2(sr, cr);
+        *terms_at(j) = make_ulonglong2(
+            mul(b, ci), mul(mul(mul(si, x[k]), e), mul(over, con.minus)));
       } else {
-        si = sigmoid2(zi[k], con), sr = sigmoid2(zr[k], con);
-        decay2<FAST>(sr, w.a, con, e, m);
+        const Two oi = odds2(zi[k], con), od = odds2(zr[k], con);
+        decay2<FAST>(gate_of(od, con), w.a, con, e, m);
+        b = mul(mul(m, gate_of(oi, con)), x[k]);
+        *decay_at(j) = make_ulonglong2(e, m);
+        *gates_at(j) = make_ulonglong2(oi, od);
       }
-      Two b = mul(mul(m, si), x[k]);
-      *decay_at(j) = make_ulonglong2(e, m);
-      *gates_at(j) = make_ulonglong2(si, sr);
       *state_at(j) = b;
       // (what is kept of a row of no sequence is not used)
       if (!INSIDE && !(in >> j & 1)) e = kOnes, b = 0, g[k] = 0;
@@ -1028,7 +1067,7 @@ __device__ __forceinline__ Carry turn_of(const Params& p, const Place& w, Shared
 #pragma unroll
   for (int k = 0; k < W - 1; ++k)
     if (k < warp) h = through<!INSIDE>(get_pair(&sh.down[k][lane]), h);
-#pragma unroll (INSIDE && FAST ? 4 : 1)
+#pragma unroll (INSIDE ? 8 : 1)
   for (int j = 0; j < R; ++j) {
     if (!INSIDE && (first >> j & 1)) h = start_state(p, t.seq[warp * R + j], w.c, w.cols);
     const Two b = *state_at(j), e = decay_at(j)->x;
@@ -1049,30 +1088,37 @@ __device__ __forceinline__ Carry turn_of(const Params& p, const Place& w, Shared
   Down<T> dx_at(p.dx, row0 + R - 1, p.dxs, w.c, -1), di_at(p.dig, row0 + R - 1, p.dis, w.c, -1),
       dr_at(p.drg, row0 + R - 1, p.drs, w.c, -1);
   const bool pairs = p.pairs && w.c0 + kCols <= p.width;
+  constexpr int kLast = INSIDE ? 8 : 2;
 #pragma unroll 1
-  for (int j0 = R - kAtOnce; j0 >= 0; j0 -= kAtOnce) {
+  for (int j0 = R - kLast; j0 >= 0; j0 -= kLast) {
 #pragma unroll
-    for (int k = kAtOnce - 1; k >= 0; --k) {
+    for (int k = kLast - 1; k >= 0; --k) {
       const int j = j0 + k;
-      const ulonglong2 em = *decay_at(j), ir = *gates_at(j);
-      const Two e = em.x, m = em.y, si = ir.x, sr = ir.y, x = raw(j, 0);
       Two g = raw(j, 1);
       if (!INSIDE && (last >> j & 1))
         g = add(g, end_gradient(p, t.seq[warp * R + j], w.c, w.cols));
       else
         g = add(g, gc);
-      // dx = g m i,  di = dx x (1 - i)
-      Two dx = mul(mul(m, si), g);
-      Two di = mul(mul(dx, x), fma(si, con.minus, con.one));
-      // g e r (h - i x e / m)
-      const Two over = each(m, [](float v) {
-        const float o = kAccurate ? 1.0f / v : rcp_approx(v);
-        return v > 0.0f ? -o : 0.0f;
-      });
-      Two d = fma(mul(mul(si, x), e), over, *state_at(j));
-      const Two eg = mul(e, g);
-      d = mul(mul(d, sr), eg);
-      Two dr = mul(mul(d, w.a), fma(sr, con.minus, con.one));
+      // dx = g m i,  di = dx x (1 - i),  d = g e r (h - i x e / m),  dr = d a (1 - r)
+      const ulonglong2 em = *decay_at(j), gates = *gates_at(j);
+      const Two eg = mul(em.x, g);
+      Two dx, di, d, rest;
+      if constexpr (kAccurate) {
+        const ulonglong2 terms = *terms_at(j);
+        rest = gates.y;
+        dx = mul(em.y, g), di = mul(terms.x, g);
+        d = mul(mul(add(*state_at(j), terms.y), gates.x), eg);
+      } else {
+        const Two e = em.x, m = em.y, x = raw(j, 0);
+        const Two si = gate_of(gates.x, con), sr = gate_of(gates.y, con);
+        rest = rest_of(gates.y, sr);
+        dx = mul(mul(m, si), g), di = mul(mul(dx, x), rest_of(gates.x, si));
+        const Two over = each(m, [](float v) {
+          return v > 0.0f ? -rcp_approx(v) : 0.0f;
+        });
+        d = mul(mul(fma(mul(mul(si, x), e), over, *state_at(j)), sr), eg);
+      }
+      Two dr = mul(mul(d, w.a), rest);
       if (INSIDE || (in >> j & 1)) {
         carry.da = add(carry.da, d);
         gc = eg;

@@ -17,6 +17,7 @@ import gated_group_rmsnorm_gb300 as g
 from tests.mixer_ref import U, rounding
 
 pytestmark = pytest.mark.gpu
+DTYPES = [torch.bfloat16, torch.float16, torch.float32]
 WIDTH = 256
 
 
@@ -76,3 +77,42 @@ def test_root_of_f32():
     x, i, r = _rows(torch.ones_like(z), torch.full_like(z, 40.0), z)
     for out in _forward(x, i, r, a.cuda()):
         _within(out, torch.sqrt(-torch.expm1(2 * p)), 8 * U, torch.float32)
+
+
+def _open(dtype):
+    """Logits of open gates, from where 1 - sigmoid is 3e-4 to where it is 1e-7."""
+    gen = torch.Generator().manual_seed(3)
+    return (torch.rand(64, WIDTH, generator=gen) * 8 + 8).to(dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_gradient_of_an_open_input_gate(dtype):
+    """m = 1, x = 1, dout = 1: di = i (1 - i).  f32: i (of an E below 3e-4) 2.1 u, 1 - i 8.2 u,
+    m 1.1 u and four products.  16 bit: 1 - i has 1.7 |z| u of its argument's roundings
+    (|z| <= 16), 4 u of the exponential, 2 u of the reciprocal and two roundings, i 3 u, and
+    four products."""
+    z = _open(dtype)
+    one = torch.ones_like(z)
+    x, i, r, dout = _rows(one, z, one * 20, one)
+    a = torch.full((WIDTH,), -40.0, device="cuda")
+    _, di, _, _, _ = g.linear_recurrence_backward(dout, x, i, r, a)
+    zd = z.double()
+    want = torch.sigmoid(zd) * torch.sigmoid(-zd)
+    _within(di, want, (20 if dtype == torch.float32 else 64) * U, dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_gradient_of_an_open_decay_gate(dtype):
+    """x = 1, i = 1, dout = 1, no state: dr = -a e^2 / m r (1 - r), p near a = -1/2.  f32: e (twice)
+    5.6 u, 1 / m 5.2 u, r 2.1 u, 1 - r 8.2 u and six products: below 64 u.  16 bit: e 8 u, 1 - e
+    12 u of it, 1 / m 12 u, r 3 u, 1 - r 35 u and six products: below 128 u."""
+    z = _open(dtype)
+    one = torch.ones_like(z)
+    x, i, r, dout = _rows(one, one * 40, z, one)
+    a = torch.full((WIDTH,), -0.5)
+    _, _, dr, _, _ = g.linear_recurrence_backward(dout, x, i, r, a.cuda())
+    zd = z.double()
+    p = a.double() * torch.sigmoid(zd)
+    want = (-a.double() * torch.exp(2 * p) / torch.sqrt(-torch.expm1(2 * p)) * torch.sigmoid(zd) *
+            torch.sigmoid(-zd))
+    _within(dr, want, (64 if dtype == torch.float32 else 128) * U, dtype)
