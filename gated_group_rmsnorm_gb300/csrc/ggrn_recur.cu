@@ -929,7 +929,7 @@ static_assert(W >= kMaxCluster, "a warp to each CTA that the tile's pair goes to
 //             (1 - i of the rounded i has no digit left at logits of 16); b, later the
 //             state before the row, in the place of the gates' logits
 //   f32       (e, m i), in the place of the gates' logits; (r, 1 - r);
-//             (m i x (1 - i), -i x e / m); b, later the state, in the place of x
+//             (m i x (1 - i), -i x e r / m); b, later the state, in the place of x
 template <typename T>
 struct Row {
   static constexpr int ES = sizeof(T), kRaw = 4 * kCols * ES, kLogits = 2 * kCols * ES;
@@ -1024,7 +1024,7 @@ __device__ __forceinline__ Carry turn_of(const Params& p, const Place& w, Shared
         *decay_at(j) = make_ulonglong2(e, mi);
         *gates_at(j) = make_ulonglong2(sr, cr);
         *terms_at(j) = make_ulonglong2(
-            mul(b, ci), mul(mul(mul(si, x[k]), e), mul(over, con.minus)));
+            mul(b, ci), mul(mul(mul(si, x[k]), e), mul(mul(over, sr), con.minus)));
       } else {
         const Two oi = odds2(zi[k], con), od = odds2(zr[k], con);
         decay2<FAST>(gate_of(od, con), w.a, con, e, m);
@@ -1099,7 +1099,7 @@ __device__ __forceinline__ Carry turn_of(const Params& p, const Place& w, Shared
         g = add(g, end_gradient(p, t.seq[warp * R + j], w.c, w.cols));
       else
         g = add(g, gc);
-      // dx = g m i,  di = dx x (1 - i),  d = g e r (h - i x e / m),  dr = d a (1 - r)
+      // dx = g m i,  di = dx x (1 - i),  d = g e (h r - i x e r / m),  dr = d a (1 - r)
       const ulonglong2 em = *decay_at(j), gates = *gates_at(j);
       const Two eg = mul(em.x, g);
       Two dx, di, d, rest;
@@ -1107,7 +1107,7 @@ __device__ __forceinline__ Carry turn_of(const Params& p, const Place& w, Shared
         const ulonglong2 terms = *terms_at(j);
         rest = gates.y;
         dx = mul(em.y, g), di = mul(terms.x, g);
-        d = mul(mul(add(*state_at(j), terms.y), gates.x), eg);
+        d = mul(fma(*state_at(j), gates.x, terms.y), eg);
       } else {
         const Two e = em.x, m = em.y, x = raw(j, 0);
         const Two si = gate_of(gates.x, con), sr = gate_of(gates.y, con);
@@ -1116,7 +1116,7 @@ __device__ __forceinline__ Carry turn_of(const Params& p, const Place& w, Shared
         const Two over = each(m, [](float v) {
           return v > 0.0f ? -rcp_approx(v) : 0.0f;
         });
-        d = mul(mul(fma(mul(mul(si, x), e), over, *state_at(j)), sr), eg);
+        d = mul(fma(mul(mul(si, x), e), mul(over, sr), mul(*state_at(j), sr)), eg);
       }
       Two dr = mul(mul(d, w.a), rest);
       if (INSIDE || (in >> j & 1)) {

@@ -14,6 +14,7 @@ import pytest
 import torch
 
 import gated_group_rmsnorm_gb300 as g
+from tests import train_ref as ref
 from tests.mixer_ref import U, rounding
 
 pytestmark = pytest.mark.gpu
@@ -116,3 +117,19 @@ def test_gradient_of_an_open_decay_gate(dtype):
     want = (-a.double() * torch.exp(2 * p) / torch.sqrt(-torch.expm1(2 * p)) * torch.sigmoid(zd) *
             torch.sigmoid(-zd))
     _within(dr, want, (64 if dtype == torch.float32 else 128) * U, dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_a_closed_decay_gate_and_a_large_input(dtype):
+    """x / m passes what f32 holds, r x / m does not: finite gradients."""
+    rows, width = 70, 96
+    gen = torch.Generator().manual_seed(4)
+    x = (torch.randn(rows, width, generator=gen) * 2.0 ** 90).to(dtype)
+    i, dout = (torch.randn(rows, width, generator=gen).to(dtype) for _ in range(2))
+    r = (torch.rand(rows, width, generator=gen) * 20 - 65).to(dtype)
+    a = -0.1 * torch.rand(width, generator=gen) - 0.01
+    want = ref.recur_backward(dout, x, i, r, a, [(0, rows)])
+    got = g.linear_recurrence_backward(dout.cuda(), x.cuda(), i.cuda(), r.cuda(), a.cuda())
+    for n, v in zip(("dx", "di", "dr", "da"), got):
+        assert torch.isfinite(v).all(), n
+        ref.assert_close(v, *want[n], torch.float32 if n == "da" else dtype, n)
