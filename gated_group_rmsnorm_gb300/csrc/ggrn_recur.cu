@@ -71,7 +71,6 @@ struct Raw<T, 2> {
   using Word = typename std::conditional<sizeof(T) == 4, uint2, uint32_t>::type;
   Word w;
   __device__ __forceinline__ void load(const T* p) { w = __ldg(reinterpret_cast<const Word*>(p)); }
-  __device__ __forceinline__ void clear() { w = Word{}; }
   __device__ __forceinline__ void get(float* f) const {
     if constexpr (sizeof(T) == 4) {
       f[0] = __uint_as_float(w.x), f[1] = __uint_as_float(w.y);
@@ -91,10 +90,6 @@ template <typename T>
 struct Raw<T, 1> {
   T w;
   __device__ __forceinline__ void load(const T* p) { w = *p; }
-  __device__ __forceinline__ void clear() {
-    const float z = 0.0f;
-    Elem<T>::store1(&w, 0, z);
-  }
   __device__ __forceinline__ void get(float* f) const { f[0] = static_cast<float>(w); }
   __device__ __forceinline__ static void put(T* p, const float* f) { Elem<T>::store1(p, 0, f[0]); }
 };
