@@ -16,6 +16,10 @@ layer norm (``layer_norm``), and for training the backward passes of the
 recurrence, of layer norm and of the gated norm (``linear_recurrence_backward``,
 ``layer_norm_backward``, ``backward``).  All computed by hand-written CUDA kernels behind a C ABI
 (``include/ggrn.h``, ``libggrn.so``).  This package is the thin Python binding.
+
+No function records anything for autograd: an output carries no graph, even where
+an input requires gradients.  A training program calls the backward passes itself,
+or from a ``torch.autograd.Function`` of its own.
 """
 from .binding import (BF16, DTYPE_CODE, F16, F32, MAMBA2, ONNX, PATH_AUTO, PATH_NAMES,
                       PATH_SCALAR, PATH_STRADDLE, PATH_STREAM, PATH_TEAM, PATH_WIDE,

@@ -380,6 +380,8 @@ def forward(y: torch.Tensor, gate: torch.Tensor, w: torch.Tensor, *, group_size:
     ``w``: MAMBA2 -> f32 [width]; ONNX -> T scale with ``group_size`` elements
     (any of the shapes (C), (1, C), (C, 1)).
     ``out``: optional output (same shape as y; allocated like y when omitted).
+    Nothing is recorded for autograd: the output carries no graph, even where an
+    input requires gradients (``backward`` gives them).
     """
     if not y.is_cuda:
         raise ValueError("forward runs on CUDA tensors only (no CPU path)")
@@ -753,7 +755,9 @@ def linear_recurrence(x: torch.Tensor, input_gate: torch.Tensor, decay_gate: tor
     gate (<= 0).  ``state``: f32 [slots, width]; ``cu_seqlens``, ``slots`` and
     ``resume`` as in ``causal_conv``.  ``saved``: where given, receives what
     ``linear_recurrence_backward`` can start from (``linear_recurrence_saved``).
-    All arithmetic and the states are f32; the output is rounded once.
+    All arithmetic and the states are f32; the output is rounded once.  Nothing is
+    recorded for autograd: the output carries no graph, even where an input
+    requires gradients.
     """
     return (_native or load_binding()).recur(x, input_gate, decay_gate, a, cu_seqlens, state, slots,
                                              resume, saved, out, False)
@@ -767,6 +771,7 @@ def linear_recurrence_step(x: torch.Tensor, input_gate: torch.Tensor, decay_gate
     (``ggrn_recur_step``): row i of ``x`` [batch, width] advances entry
     ``slots[i]`` (i without slots) of ``state`` [slots, width] in place.  A row
     whose slot is outside the pool is skipped: its output row is left as it was.
+    Nothing is recorded for autograd.
     """
     return (_native or load_binding()).recur(x, input_gate, decay_gate, a, None, state, slots, None,
                                              None, out, True)
@@ -802,7 +807,8 @@ def linear_recurrence_backward(dout: torch.Tensor, x: torch.Tensor, input_gate: 
     again, at the price of the forward pass.  ``dx``, ``dinput_gate``,
     ``ddecay_gate``: optional outputs (row-strided views allowed, such as columns
     of one packed gradient); their rows of no sequence are zeros.  ``da``: f32
-    [width].
+    [width].  For the backward of a ``torch.autograd.Function``, or called as it
+    is; nothing is recorded for autograd (no second derivatives).
     """
     return (_native or load_binding()).recur_backward(dout, x, input_gate, decay_gate, a, cu_seqlens,
                                                       state, slots, resume, dstate, saved, dx,
@@ -814,7 +820,9 @@ def layer_norm(x: torch.Tensor, w: torch.Tensor, b: torch.Tensor | None = None, 
     """Layer norm over the last dimension (``ggrn_layer_norm``):
     ``out = (x - mean) * rsqrt(var + eps) * w + b``, the variance that of the
     whole row.  ``x``: [..., width] of f32, f16 or bf16 whose leading axes fold
-    into rows (row-strided views allowed); ``w``, ``b``: f32 [width].
+    into rows (row-strided views allowed); ``w``, ``b``: f32 [width].  Nothing is
+    recorded for autograd: the output carries no graph, even where an input
+    requires gradients.
     """
     return (_native or load_binding()).layer_norm(x, w, b, eps, out)
 
@@ -824,7 +832,8 @@ def layer_norm_backward(dout: torch.Tensor, x: torch.Tensor, w: torch.Tensor, *,
     """The gradients of ``layer_norm`` (``ggrn_layer_norm_backward``): ``(dx, dw,
     db)``; ``db`` is None with ``bias=False``.  ``dw`` and ``db`` are f32, summed
     over all rows in a fixed order.  The row's statistics are computed again from
-    ``x``.
+    ``x``.  For the backward of a ``torch.autograd.Function``, or called as it is;
+    nothing is recorded for autograd (no second derivatives).
     """
     return (_native or load_binding()).layer_norm_backward(dout, x, w, eps, bias, dx)
 
@@ -838,7 +847,9 @@ def backward(dout: torch.Tensor, y: torch.Tensor, gate: torch.Tensor, w: torch.T
     ``dgate``: optional outputs (row-strided views allowed, such as columns of a
     packed in-proj's gradient).  ``dw`` is f32 of ``w``'s shape, summed over all
     rows (ONNX: and groups) in a fixed order.  The cast inside MAMBA2's formula is
-    differentiated as the identity.
+    differentiated as the identity.  For the backward of a
+    ``torch.autograd.Function``, or called as it is; nothing is recorded for
+    autograd (no second derivatives).
     """
     return (_native or load_binding()).norm_backward(dout, y, gate, w, group_size, eps,
                                                      MODE_CODE[mode], dy, dgate)
