@@ -21,12 +21,12 @@
 // The mean is taken off before squares are summed (two reductions), so a row
 // whose mean is far from zero loses nothing.
 //
-// Of the measured copy rate: layer norm 80-93 % (16384 x 3840 bf16 46 us), its
-// gradients 46-71 % from rows of 1024 (89 us), the gated norm's 73-82 % (16384 x 4800 bf16 in groups of
-// 100 155 us, 16384 x 4096 f16 in groups of 128 121 us).  The gradients are bound by
-// their instructions (24 to 53 an element, the sums over a group among them) at the
-// 16 to 24 warps that their registers leave an SM: a thread keeps its columns' sums
-// and weights besides a row's values.
+// Of the measured copy rate: layer norm 66 % (rows of 1024) to 93 % (16384 x 3840 bf16 46
+// us, 81 %), its gradients 48 to 75 % (89 us, 62 %), the gated norm's 72 to 82 % (16384 x
+// 4800 bf16 in groups of 100 155 us, 16384 x 4096 f16 in groups of 128 121 us).  The
+// gradients are bound by their instructions (24 to 53 an element, the sums over a group
+// among them) at 15 or 16 warps an SM: a thread keeps its columns' sums and weights
+// besides a row's values, so that no more CTAs fit.
 #pragma once
 
 #include <type_traits>
@@ -228,11 +228,11 @@ __device__ __forceinline__ void clear_sums(float4* s_sum) {
 // of Markstein's correction (IBM J. Res. Dev. 34, 1990): q = s (1 / gs) is within 1.5 ulp,
 // s - q gs is exact, and q + (s - q gs) (1 / gs) misses the quotient by 2^-23 ulp before
 // it is rounded, where a quotient by gs < 2^20 keeps 2^-21 from every midpoint.  (An
-// infinite sum has no remainder.)  The division's own instructions cost 2 to 3 % of the
+// infinite quotient has no remainder.)  The division's own instructions cost 2 to 3 % of the
 // gradients' time.
 __device__ __forceinline__ float mean_of(float s, const Params& p) {
-  const float q = s * p.inv_gs, r = fmaf(-q, p.gs_f, s);
-  return fmaf(r == r ? r : 0.0f, p.inv_gs, q);
+  const float q = s * p.inv_gs, t = fmaf(fmaf(-q, p.gs_f, s), p.inv_gs, q);
+  return fabsf(q) < INFINITY ? t : q;
 }
 
 // The weight of element j of a group (column c of the row), widened.
@@ -247,8 +247,10 @@ constexpr int inputs_of(int kind) { return kind == kLayerNorm ? 1 : kind == kLay
 
 // Threads of an SM that a kernel's registers leave room for, by the elements that a
 // thread holds of each matrix, and the most of a CTA.
-// (Spilled registers cost more than threads: the gated norm's gradients of 16384 x 4800
-// in groups of 100 take 156 us with 96 registers and 182 with 80.)
+// (Eight elements: the gated norm's gradients of 16384 x 4800 in groups of 100 take 155 us
+// with 96 registers, 16 warps an SM and nothing spilled, and 182 with 80, 24 warps and
+// spills.  Elsewhere kernels of the gradients do spill: single elements by four a thread
+// 40 to 132 bytes, 16 elements up to 116, 32 elements 640 to 750; not measured apart.)
 __host__ __device__ constexpr int room_of(int kind, int elems) {
   return kind == kLayerNorm ? (elems <= 8 ? 1024 : elems <= 16 ? 768 : 512)
                             : (elems <= 4 ? 1024 : elems <= 8 ? 640 : 512);
@@ -548,8 +550,13 @@ __global__ void __launch_bounds__(threads_of(KIND, VPL * E),
 }
 
 // Any layout and any group: a CTA for each group of its rows, which it reads
-// again for every pass (from L1 and L2).  Each thread owns the same columns in
-// every row; their sums lie in its CTA's row of the partial sums.
+// again for every pass (from L1 and L2).  For what the threads of a CTA, or its ring of
+// rows in shared memory, do not hold: more than 2048 single elements, layer norm beyond
+// 16384 columns (f32: 10240), its gradients beyond 10240 (5120), groups of the gated
+// norm beyond 8192 (4096).  Each thread owns the same columns in every row; their sums
+// lie in its CTA's row of the partial sums.  Three passes, and sums read and written for
+// each row: the gated norm's gradients of 4096 x 12288 bf16 in one group take 413 us
+// (floor 74), of 4096 x 5120 f32 167 (62), layer norm's of 4096 x 7680 f32 209 (56).
 template <int KIND, typename T>
 __global__ void __launch_bounds__(kAnyThreads) k_norm_any(const Params p) {
   constexpr bool kGrad = KIND != kLayerNorm, kGated = KIND == kMamba2Grad || KIND == kOnnxGrad;

@@ -21,9 +21,10 @@
 // before every 64th row (f32, 1/32 of a 16-bit tensor's bytes), from which each
 // tile finds its own; without them a first launch makes them.
 //
-// An element takes 8 bytes of HBM forward and 14 back (16-bit T), five and six
+// An element takes 8 bytes of HBM forward and 14 back (16-bit T), five and eight
 // operations of the special function units, and about 40 and 80 instructions.
-// 4096 x 7680 bf16: 73 us forward, 175 back, against 37 and 65 for the bytes alone.
+// 4096 x 7680 bf16: 73 us forward, 177 back, against 37 and 65 for the bytes alone.
+// f32: 2048 x 5120 56 us forward, 167 back (25 and 43).
 // What is left is latency: an SM's schedulers issue half of the time, since a turn
 // of a cluster is a chain (copies, gates, exchange, outputs) that the five (back: two)
 // CTAs of the SM overlap only in part.
@@ -909,9 +910,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 4)
 // Gradients.  Eight warps of eight rows each; the cluster's tiles go from the last
 // rows to the first, rank 0 has the last of them.  What a row needs again on the way
 // back (e, m, both gates, the state before it) lies in shared memory behind its
-// inputs, so that the loops over rows stay rolled, as in the forward pass.  (With
-// these in registers and the loops unrolled: 171 us for 4096 x 7680 in bf16, against
-// 175, and 61 for 1025 x 1001 in f32, against 30.)
+// inputs, so that the first loop over rows stays rolled, as in the forward pass.  (With
+// these in registers and all loops unrolled 4096 x 7680 in bf16 took 171 us, against 175
+// then, and 1025 x 1001 in f32 61, against 30.  Of what lies in shared memory, the loops
+// behind the exchange gain by it: 177 us, 181 by four rows.)
 // ---------------------------------------------------------------------------
 namespace backward {
 
@@ -1413,8 +1415,8 @@ int launch_step(const Params& p, cudaStream_t s) {
                        p);
 }
 
-// Widths that a grid's second axis holds (a block of channels each, or 128 in the
-// step form).
+// The most columns of a call, as ggrn.h gives it: half of what the blocks of 64 channels on
+// a grid's second axis could hold (the step form's have 128 at least).
 constexpr int64_t kMostColumns = int64_t{65535} * 32;
 
 struct Matrix {
